@@ -380,6 +380,110 @@ QZ_API qz_status qz_host_plan_status(const qz_host_plan* plan, uint32_t* flags_h
 /* Wait for the plan's streams and free everything it allocated.  NULL is ignored. */
 QZ_API void qz_host_plan_destroy(qz_host_plan* plan);
 
+/* ---- Products with quantized weights -------------------------------------------------------
+ * The feed-forward half of a transformer layer on 4-bit weights, as qz_quantize leaves them:
+ * the product with one weight (a projection, an output head), the gated block on two, and the
+ * layer norm in front of them, each with its gradient.  The blog post has no counterpart.
+ *
+ * A weight W is a [rows, cols] tensor of MXFP4, NVFP4 or INT4 codes, rows = output channels,
+ * blocks along cols = input channels.  Its values are those of qz_dequantize,
+ * W[r][c] = decode(code) * s, with one difference: the tensor scale of NVFP4 multiplies the
+ * finished sum instead of the block scale (one fp32 rounding less per value).
+ *   format, block_size   QZ_MXFP4 / 32, QZ_NVFP4 / 16, QZ_INT4 / 16, 32, 64 or 128
+ *   codes, scales        device, dense, as qz_quantize writes them (granularity BLOCK or UNIT)
+ *   tensor_scale_dev     device fp32, the tensor scale of NVFP4 (NULL: 1); ignored otherwise
+ * The struct is read during the call; the buffers must live until the work on `stream` is done. */
+typedef struct {
+  int32_t format;
+  int32_t block_size;
+  int64_t rows;
+  int64_t cols;
+  const void* codes;
+  const void* scales;
+  const float* tensor_scale_dev;
+} qz_weight;
+
+/* The activation of the gated block. */
+typedef enum {
+  QZ_ACT_SILU = 1,      /* a / (1 + exp(-a))                                              */
+  QZ_ACT_GELU_TANH = 2  /* a / 2 * (1 + tanh(sqrt(2 / pi) * (a + 0.044715 a^3)))          */
+} qz_activation;
+
+/* Common to the four product calls below.
+ *   Activations and gradients are bf16, [tokens, ld] row-major with unit inner stride; each
+ *   matrix has its own leading dimension, at least its width.  Outputs must not overlap inputs
+ *   or each other.
+ *   Arithmetic: products of bf16 activations with the exact weight values, summed in fp32 in an
+ *   unspecified but fixed order (equal inputs give equal results); outputs are rounded once,
+ *   to nearest even.  A non-finite activation makes the outputs of its own token non-finite
+ *   and no others, as IEEE arithmetic has it (INT4: an Inf may become NaN, because a weight may
+ *   be held as the sum of two bf16 values).
+ *   Errors: QZ_ERR_NULL, QZ_ERR_ENUM (format, out_dtype, act), QZ_ERR_UNSUPPORTED (block_size;
+ *   2^31 and more tokens, rows or cols), QZ_ERR_SHAPE (negative sizes, cols not a multiple of
+ *   block_size, a leading dimension too small, gate and up of different shapes), QZ_ERR_ALIGN.
+ *   tokens == 0 or an empty output enqueues nothing; an empty sum is 0.
+ *   Alignment: any pointer and leading dimension of the element type's own alignment is right;
+ *   16-byte aligned codes and activations, leading dimensions that are multiples of 8 and cols a
+ *   multiple of 32 get the fast kernels.
+ *   Asynchronous on `stream`; no workspace. */
+
+/* y = x W^T: y[t][r] = sum_c x[t][c] W[r][c]; x [tokens, cols], y [tokens, rows] of out_dtype. */
+QZ_API qz_status qz_linear(const qz_weight* w, const void* x, int64_t ld_x, int64_t tokens, void* y,
+                           int64_t ld_y, int32_t out_dtype, qz_stream_t stream);
+
+/* The input gradient of qz_linear, dx = dy W: dx[t][c] = sum_r dy[t][r] W[r][c]; dy [tokens,
+ * rows], dx [tokens, cols] of out_dtype.  The codes take no gradient. */
+QZ_API qz_status qz_linear_backward(const qz_weight* w, const void* dy, int64_t ld_dy, int64_t tokens,
+                                    void* dx, int64_t ld_dx, int32_t out_dtype, qz_stream_t stream);
+
+/* The gated feed-forward block, both projections, the activation and the product in one kernel:
+ *   g = x gate^T, u = x up^T, h = act(g) * u;  x [tokens, cols], h [tokens, rows].
+ *   g_out, u_out  bf16 [tokens, ld_gu], the rounded pre-activations for the backward pass; both
+ *                 NULL: not written.  h is formed from the unrounded fp32 sums.
+ * gate and up have the same format, block_size, rows and cols. */
+QZ_API qz_status qz_gated_ffn(const qz_weight* gate, const qz_weight* up, int32_t act, const void* x,
+                              int64_t ld_x, int64_t tokens, void* h, int64_t ld_h, void* g_out,
+                              void* u_out, int64_t ld_gu, qz_stream_t stream);
+
+/* Its backward pass from the kept pre-activations:
+ *   dg = dh * u * act'(g), du = dh * act(g), dx = dg gate + du up.
+ *   dh, g, u, dg, du  [tokens, rows] (g and u share ld_gu, dg and du ld_dgu);  dx [tokens, cols].
+ * dg and du are rounded to bf16 once, as outputs and as the tensor cores' operands of dx. */
+QZ_API qz_status qz_gated_ffn_backward(const qz_weight* gate, const qz_weight* up, int32_t act,
+                                       const void* dh, int64_t ld_dh, const void* g, const void* u,
+                                       int64_t ld_gu, int64_t tokens, void* dg, void* du, int64_t ld_dgu,
+                                       void* dx, int64_t ld_dx, qz_stream_t stream);
+
+/* Layer norm over the rows of x [rows, cols] (dtype QZ_BF16 or QZ_F32, leading dimension ld_x):
+ *   mean = sum x / cols, rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps),
+ *   y = (x - mean) * rstd * weight + bias.
+ *   weight, bias  device fp32 [cols]; NULL: 1 and 0
+ *   y             [rows, ld_y] of the same dtype
+ *   mean, rstd    device fp32 [rows], kept for the backward pass; NULL: not written
+ * The sums run in fp32 over the row held on the chip, the squares about the mean.  eps >= 0.
+ * Errors as above; cols == 0 is QZ_ERR_SHAPE unless rows == 0. */
+QZ_API qz_status qz_layer_norm(int32_t dtype, const void* x, int64_t ld_x, int64_t rows, int64_t cols,
+                               const float* weight, const float* bias, float eps, void* y, int64_t ld_y,
+                               float* mean, float* rstd, qz_stream_t stream);
+
+/* Bytes of device workspace qz_layer_norm_backward needs for this shape (uninitialised memory
+ * will do). */
+QZ_API size_t qz_layer_norm_backward_workspace(int64_t rows, int64_t cols);
+
+/* The gradients of qz_layer_norm: with n = (x - mean) * rstd and t = dy * weight,
+ *   dx = rstd * (t - sum t / cols - n * sum (t n) / cols),
+ *   dweight = sum over rows of dy n, dbias = sum over rows of dy.
+ *   dy, x, dx        [rows, ld] of dtype;  mean, rstd as qz_layer_norm wrote them
+ *   dweight, dbias   device fp32 [cols], both or neither (NULL: not computed); overwritten, and
+ *                    zero for rows == 0.  The row sums run in a fixed order: equal inputs give
+ *                    equal results.
+ *   ws, ws_bytes     the workspace (16-byte aligned); may be NULL when dweight is NULL */
+QZ_API qz_status qz_layer_norm_backward(int32_t dtype, const void* dy, int64_t ld_dy, const void* x,
+                                        int64_t ld_x, int64_t rows, int64_t cols, const float* mean,
+                                        const float* rstd, const float* weight, void* dx, int64_t ld_dx,
+                                        float* dweight, float* dbias, void* ws, size_t ws_bytes,
+                                        qz_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,5 +1,7 @@
 """Python binding of libqz: quantize tensors on a GB300 to INT8 / FP8 E4M3 / FP8 E5M2 /
-MXFP4 / NVFP4, dequantize them, and measure the quantization error.
+MXFP4 / NVFP4, dequantize them, measure the quantization error, and run the feed-forward half
+of a transformer layer on the 4-bit weights (``Weight``, ``linear``, ``gated_ffn``,
+``layer_norm`` and their gradients).
 
 The functions ``qz_*`` mirror the C ABI of ``include/qz.h`` one to one (same names, same
 arguments, device pointers as integers).  ``quantize`` / ``dequantize`` / ``error_stats`` /
@@ -28,12 +30,14 @@ QZ_BF16, QZ_F32 = 1, 2
 QZ_GRAN_TENSOR, QZ_GRAN_ROW, QZ_GRAN_BLOCK, QZ_GRAN_UNIT = 1, 2, 3, 4
 QZ_ROUND_RNE = 0
 QZ_SCALE_UP, QZ_SCALE_NEAREST = 0, 1
+QZ_ACT_SILU, QZ_ACT_GELU_TANH = 1, 2
 QZ_FLAG_NONFINITE_INPUT, QZ_FLAG_BAD_AMAX, QZ_FLAG_PIPELINE_TIMEOUT = 0x1, 0x2, 0x4
 
 FORMATS = {"int8": QZ_INT8, "e4m3": QZ_FP8_E4M3, "e5m2": QZ_FP8_E5M2,
            "mxfp4": QZ_MXFP4, "nvfp4": QZ_NVFP4, "int4": QZ_INT4}
 GRANULARITIES = {"tensor": QZ_GRAN_TENSOR, "row": QZ_GRAN_ROW, "block": QZ_GRAN_BLOCK,
                  "unit": QZ_GRAN_UNIT}
+ACTIVATIONS = {"silu": QZ_ACT_SILU, "gelu_tanh": QZ_ACT_GELU_TANH}
 BLOCK_SIZE = {QZ_MXFP4: 32, QZ_NVFP4: 16, QZ_INT4: 32}  # INT4: the default group
 
 # Names of the exported C symbols (the whole ABI of include/qz.h).
@@ -41,7 +45,9 @@ ABI_SYMBOLS = ("qz_status_string", "qz_workspace_size", "qz_workspace_init", "qz
                "qz_quantize", "qz_quantize_delayed", "qz_dequantize", "qz_error_stats",
                "qz_error_stats_noalloc", "qz_error_stats_noalloc_status", "qz_stats_merge", "qz_dequantize_asym4", "qz_quant_dot",
                "qz_selftest_pipeline_timeout", "qz_get_device_status", "qz_host_plan_create",
-               "qz_host_run", "qz_host_plan_status", "qz_host_plan_destroy")
+               "qz_host_run", "qz_host_plan_status", "qz_host_plan_destroy", "qz_linear",
+               "qz_linear_backward", "qz_gated_ffn", "qz_gated_ffn_backward", "qz_layer_norm",
+               "qz_layer_norm_backward_workspace", "qz_layer_norm_backward")
 QZ_HOST_MAX_RUNS = 16
 
 
@@ -68,6 +74,13 @@ class QzHostIo(C.Structure):
                 ("stats_host", C.c_void_p)]
 
 
+class QzWeight(C.Structure):
+    """qz_weight: a 4-bit weight as qz_quantize leaves it."""
+    _fields_ = [("format", C.c_int32), ("block_size", C.c_int32), ("rows", C.c_int64),
+                ("cols", C.c_int64), ("codes", C.c_void_p), ("scales", C.c_void_p),
+                ("tensor_scale_dev", C.c_void_p)]
+
+
 class QzError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {qz_status_string(status)} (status {status})")
@@ -84,7 +97,8 @@ def lib():
         if not os.path.exists(LIB_PATH):
             raise ImportError(f"{LIB_PATH} is missing: build it with __graft_entry__.build()")
         L = C.CDLL(LIB_PATH)
-        vp, dp, i32 = C.c_void_p, C.POINTER(QzDesc), C.c_int32
+        vp, dp, i32, i64 = C.c_void_p, C.POINTER(QzDesc), C.c_int32, C.c_int64
+        wp = C.POINTER(QzWeight)
         sig = {
             "qz_status_string": (C.c_char_p, [i32]),
             "qz_workspace_size": (C.c_size_t, [dp]),
@@ -107,6 +121,16 @@ def lib():
             "qz_host_run": (i32, [vp, vp, C.POINTER(QzHostIo)]),
             "qz_host_plan_status": (i32, [vp, C.POINTER(C.c_uint32)]),
             "qz_host_plan_destroy": (None, [vp]),
+            "qz_linear": (i32, [wp, vp, i64, i64, vp, i64, i32, vp]),
+            "qz_linear_backward": (i32, [wp, vp, i64, i64, vp, i64, i32, vp]),
+            "qz_gated_ffn": (i32, [wp, wp, i32, vp, i64, i64, vp, i64, vp, vp, i64, vp]),
+            "qz_gated_ffn_backward": (i32, [wp, wp, i32, vp, i64, vp, vp, i64, i64, vp, vp, i64,
+                                            vp, i64, vp]),
+            "qz_layer_norm": (i32, [i32, vp, i64, i64, i64, vp, vp, C.c_float, vp, i64, vp, vp,
+                                    vp]),
+            "qz_layer_norm_backward_workspace": (C.c_size_t, [i64, i64]),
+            "qz_layer_norm_backward": (i32, [i32, vp, i64, vp, i64, i64, i64, vp, vp, vp, vp, i64,
+                                             vp, vp, vp, C.c_size_t, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -240,6 +264,48 @@ def qz_get_device_status(ws: int, stream: int = 0) -> tuple[int, int]:
     flags = C.c_uint32(0)
     st = lib().qz_get_device_status(ws, C.byref(flags), stream)
     return st, flags.value
+
+
+def qz_linear(w: QzWeight, x: int, ld_x: int, tokens: int, y: int, ld_y: int, out_dtype: int,
+              stream: int = 0) -> int:
+    return lib().qz_linear(w, x, ld_x, tokens, y, ld_y, out_dtype, stream)
+
+
+def qz_linear_backward(w: QzWeight, dy: int, ld_dy: int, tokens: int, dx: int, ld_dx: int,
+                       out_dtype: int, stream: int = 0) -> int:
+    return lib().qz_linear_backward(w, dy, ld_dy, tokens, dx, ld_dx, out_dtype, stream)
+
+
+def qz_gated_ffn(gate: QzWeight, up: QzWeight, act: int, x: int, ld_x: int, tokens: int, h: int,
+                 ld_h: int, g_out: int | None, u_out: int | None, ld_gu: int,
+                 stream: int = 0) -> int:
+    return lib().qz_gated_ffn(gate, up, act, x, ld_x, tokens, h, ld_h, g_out, u_out, ld_gu, stream)
+
+
+def qz_gated_ffn_backward(gate: QzWeight, up: QzWeight, act: int, dh: int, ld_dh: int, g: int,
+                          u: int, ld_gu: int, tokens: int, dg: int, du: int, ld_dgu: int, dx: int,
+                          ld_dx: int, stream: int = 0) -> int:
+    return lib().qz_gated_ffn_backward(gate, up, act, dh, ld_dh, g, u, ld_gu, tokens, dg, du,
+                                       ld_dgu, dx, ld_dx, stream)
+
+
+def qz_layer_norm(dtype: int, x: int, ld_x: int, rows: int, cols: int, weight: int | None,
+                  bias: int | None, eps: float, y: int, ld_y: int, mean: int | None,
+                  rstd: int | None, stream: int = 0) -> int:
+    return lib().qz_layer_norm(dtype, x, ld_x, rows, cols, weight, bias, eps, y, ld_y, mean, rstd,
+                               stream)
+
+
+def qz_layer_norm_backward_workspace(rows: int, cols: int) -> int:
+    return lib().qz_layer_norm_backward_workspace(rows, cols)
+
+
+def qz_layer_norm_backward(dtype: int, dy: int, ld_dy: int, x: int, ld_x: int, rows: int, cols: int,
+                           mean: int, rstd: int, weight: int | None, dx: int, ld_dx: int,
+                           dweight: int | None, dbias: int | None, ws: int | None, ws_bytes: int,
+                           stream: int = 0) -> int:
+    return lib().qz_layer_norm_backward(dtype, dy, ld_dy, x, ld_x, rows, cols, mean, rstd, weight,
+                                        dx, ld_dx, dweight, dbias, ws, ws_bytes, stream)
 
 
 # ---------------------------------------------------------------- torch marshalling
@@ -478,3 +544,208 @@ def amax(x, workspace: Workspace | None = None, stream=None):
     workspace = workspace or Workspace(x.device)
     _check(qz_amax(desc, x.data_ptr(), out.data_ptr(), workspace.ptr, _stream(stream)), "qz_amax")
     return out
+
+
+# ---------------------------------------------------------------- products with 4-bit weights
+class Weight:
+    """A 4-bit weight for ``linear`` and ``gated_ffn``: the handle of a ``Quantized`` [rows, cols]
+    tensor of MXFP4, NVFP4 or INT4 codes (rows = output channels).  It refers to the codes and
+    scales where they are; they must stay there, and may change in place."""
+
+    def __init__(self, q: Quantized):
+        if q.fmt not in (QZ_MXFP4, QZ_NVFP4, QZ_INT4):
+            raise ValueError("products take MXFP4, NVFP4 and INT4 weights")
+        if q.fmt == QZ_NVFP4 and q.tensor_scale is None:
+            raise ValueError("an NVFP4 weight needs its tensor scale")
+        if not (q.codes.is_contiguous() and q.scales.is_contiguous()):
+            raise ValueError("codes and scales must be contiguous")
+        self.q, self.rows, self.cols = q, q.rows, q.cols
+        bs = q.block_size or BLOCK_SIZE[q.fmt]
+        torch = _torch()
+        sdt = torch.float32 if q.fmt == QZ_INT4 else torch.uint8
+        if (q.codes.dtype != torch.uint8 or q.codes.numel() * 2 != q.rows * q.cols
+                or q.scales.dtype != sdt or q.scales.numel() * bs != q.rows * q.cols):
+            raise ValueError("codes / scales do not match the weight's shape and format")
+        self.desc = QzWeight(q.fmt, bs, q.rows, q.cols, q.codes.data_ptr(), q.scales.data_ptr(),
+                             _ptr(q.tensor_scale) if q.fmt == QZ_NVFP4 else None)
+
+
+def _matrix(t, width: int, dtype, what: str):
+    """Leading dimension of a [tokens, width] CUDA matrix with unit inner stride."""
+    if t.dim() != 2 or t.shape[1] != width or t.dtype != dtype:
+        raise ValueError(f"{what} must be a [tokens, {width}] {dtype} matrix, not "
+                         f"{tuple(t.shape)} {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on the GPU")
+    s0, s1 = t.stride()
+    if s1 != 1 and t.shape[1] > 1 and t.shape[0]:
+        raise ValueError(f"{what}: the inner dimension must be contiguous")
+    if t.shape[0] <= 1:
+        return max(s0, width)
+    if s0 < width:
+        raise ValueError(f"{what}: rows overlap")
+    return s0
+
+
+def _same_tokens(tokens: int, **matrices):
+    for what, t in matrices.items():
+        if t.shape[0] != tokens:
+            raise ValueError(f"{what} must have {tokens} rows, not {t.shape[0]}")
+
+
+def _raw_stream(stream, device) -> int:
+    torch = _torch()
+    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+
+def linear(x, weight: Weight, out_dtype=None, out=None, stream=None):
+    """y = x W^T (qz_linear): x bf16 [tokens, cols] -> [tokens, rows] in out_dtype (bf16 by
+    default, or fp32)."""
+    torch = _torch()
+    ld_x = _matrix(x, weight.cols, torch.bfloat16, "x")
+    tokens = x.shape[0]
+    if out is None:
+        out = torch.empty((tokens, weight.rows), dtype=out_dtype or torch.bfloat16, device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out has another dtype than out_dtype")
+    ld_y = _matrix(out, weight.rows, out.dtype, "out")
+    _same_tokens(tokens, out=out)
+    _check(lib().qz_linear(weight.desc, x.data_ptr(), ld_x, tokens, out.data_ptr(), ld_y,
+                           _dtype_code(out.dtype), _raw_stream(stream, x.device)), "qz_linear")
+    return out
+
+
+def linear_backward(dy, weight: Weight, out_dtype=None, out=None, stream=None):
+    """dx = dy W (qz_linear_backward): dy bf16 [tokens, rows] -> [tokens, cols]."""
+    torch = _torch()
+    ld_dy = _matrix(dy, weight.rows, torch.bfloat16, "dy")
+    tokens = dy.shape[0]
+    if out is None:
+        out = torch.empty((tokens, weight.cols), dtype=out_dtype or torch.bfloat16, device=dy.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out has another dtype than out_dtype")
+    ld_dx = _matrix(out, weight.cols, out.dtype, "out")
+    _same_tokens(tokens, out=out)
+    _check(lib().qz_linear_backward(weight.desc, dy.data_ptr(), ld_dy, tokens, out.data_ptr(),
+                                    ld_dx, _dtype_code(out.dtype), _raw_stream(stream, dy.device)),
+           "qz_linear_backward")
+    return out
+
+
+def _activation(a) -> int:
+    return ACTIVATIONS[a] if isinstance(a, str) else int(a)
+
+
+def gated_ffn(x, gate: Weight, up: Weight, activation="silu", save: bool = False, out=None,
+              stream=None):
+    """h = act(x gate^T) * (x up^T) (qz_gated_ffn): x bf16 [tokens, cols] -> h bf16 [tokens,
+    rows]; with ``save`` also the bf16 pre-activations, (h, g, u).  out: h, or (h, g, u) with
+    ``save``."""
+    torch = _torch()
+    ld_x = _matrix(x, gate.cols, torch.bfloat16, "x")
+    tokens, rows = x.shape[0], gate.rows
+    if out is None:
+        out = [torch.empty((tokens, rows), dtype=torch.bfloat16, device=x.device)
+               for _ in range(3 if save else 1)]
+    else:
+        out = list(out) if save else [out]
+    lds = [_matrix(t, rows, torch.bfloat16, "out") for t in out]
+    for t in out:
+        _same_tokens(tokens, out=t)
+    if save and lds[1] != lds[2]:
+        raise ValueError("g and u must have the same leading dimension")
+    g, u = (out[1].data_ptr(), out[2].data_ptr()) if save else (None, None)
+    _check(lib().qz_gated_ffn(gate.desc, up.desc, _activation(activation), x.data_ptr(), ld_x,
+                              tokens, out[0].data_ptr(), lds[0], g, u, lds[-1],
+                              _raw_stream(stream, x.device)), "qz_gated_ffn")
+    return tuple(out) if save else out[0]
+
+
+def gated_ffn_backward(dh, g, u, gate: Weight, up: Weight, activation="silu", out=None,
+                       stream=None):
+    """The gradients of gated_ffn from its kept pre-activations (qz_gated_ffn_backward):
+    (dx [tokens, cols], dg, du [tokens, rows]), all bf16.  out: the three, in that order."""
+    torch = _torch()
+    bf = torch.bfloat16
+    rows, cols, tokens = gate.rows, gate.cols, dh.shape[0]
+    ld_dh, ld_g, ld_u = (_matrix(t, rows, bf, w) for t, w in ((dh, "dh"), (g, "g"), (u, "u")))
+    if out is None:
+        out = (torch.empty((tokens, cols), dtype=bf, device=dh.device),
+               torch.empty((tokens, rows), dtype=bf, device=dh.device),
+               torch.empty((tokens, rows), dtype=bf, device=dh.device))
+    dx, dg, du = out
+    ld_dx, ld_dg, ld_du = _matrix(dx, cols, bf, "dx"), _matrix(dg, rows, bf, "dg"), _matrix(du, rows, bf, "du")
+    _same_tokens(tokens, g=g, u=u, dx=dx, dg=dg, du=du)
+    if ld_g != ld_u or ld_dg != ld_du:
+        raise ValueError("g and u, and dg and du, must have the same leading dimension")
+    _check(lib().qz_gated_ffn_backward(gate.desc, up.desc, _activation(activation), dh.data_ptr(),
+                                       ld_dh, g.data_ptr(), u.data_ptr(), ld_g, tokens,
+                                       dg.data_ptr(), du.data_ptr(), ld_dg, dx.data_ptr(), ld_dx,
+                                       _raw_stream(stream, dh.device)), "qz_gated_ffn_backward")
+    return dx, dg, du
+
+
+def _vector(t, n: int, what: str):
+    if t is None:
+        return None
+    torch = _torch()
+    if t.dtype != torch.float32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{what} must be a contiguous fp32 CUDA vector of {n} values")
+    return t.data_ptr()
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=None):
+    """Layer norm over the rows of a 2-D bf16 / fp32 CUDA tensor (qz_layer_norm).  weight, bias:
+    fp32 [cols] or None.  Returns (y, mean, rstd); mean and rstd, fp32 [rows], are what
+    layer_norm_backward takes.  out: the three, in that order."""
+    torch = _torch()
+    dt = _dtype_code(x.dtype)
+    if x.dim() != 2:
+        raise ValueError("2-D tensors only")
+    rows, cols = x.shape
+    ld_x = _matrix(x, cols, x.dtype, "x")
+    if out is None:
+        stats = torch.empty((2, rows), dtype=torch.float32, device=x.device)
+        out = (torch.empty((rows, cols), dtype=x.dtype, device=x.device), stats[0], stats[1])
+    y, mean, rstd = out
+    ld_y = _matrix(y, cols, x.dtype, "y")
+    _same_tokens(rows, y=y)
+    _check(lib().qz_layer_norm(dt, x.data_ptr(), ld_x, rows, cols, _vector(weight, cols, "weight"),
+                               _vector(bias, cols, "bias"), eps, y.data_ptr(), ld_y,
+                               _vector(mean, rows, "mean"), _vector(rstd, rows, "rstd"),
+                               _raw_stream(stream, x.device)), "qz_layer_norm")
+    return y, mean, rstd
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, params: bool = True, out=None,
+                        workspace=None, stream=None):
+    """The gradients of layer_norm (qz_layer_norm_backward): (dx, dweight, dbias), the last two
+    fp32 [cols], or None without ``params``.  out: the three, in that order.  workspace: a uint8
+    CUDA tensor of qz_layer_norm_backward_workspace(rows, cols) bytes."""
+    torch = _torch()
+    dt = _dtype_code(x.dtype)
+    if x.dim() != 2:
+        raise ValueError("2-D tensors only")
+    rows, cols = x.shape
+    ld_x, ld_dy = _matrix(x, cols, x.dtype, "x"), _matrix(dy, cols, x.dtype, "dy")
+    if out is None:
+        dx = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+        dw, db = torch.empty((2, cols), dtype=torch.float32, device=x.device) if params else (None, None)
+    else:
+        dx, dw, db = out
+    ld_dx = _matrix(dx, cols, x.dtype, "dx")
+    _same_tokens(rows, dy=dy, dx=dx)
+    need = 0
+    if params:
+        need = lib().qz_layer_norm_backward_workspace(rows, cols)
+        if workspace is None:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
+        need = workspace.numel() * workspace.element_size()
+    _check(lib().qz_layer_norm_backward(
+        dt, dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, rows, cols, _vector(mean, rows, "mean"),
+        _vector(rstd, rows, "rstd"), _vector(weight, cols, "weight"), dx.data_ptr(), ld_dx,
+        _vector(dw, cols, "dweight") if params else None,
+        _vector(db, cols, "dbias") if params else None,
+        workspace.data_ptr() if params else None, need, _raw_stream(stream, x.device)),
+        "qz_layer_norm_backward")
+    return dx, dw, db

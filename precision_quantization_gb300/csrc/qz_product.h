@@ -1,0 +1,29 @@
+// qz_product.h -- the arguments that the product kernels share.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "qz.h"
+#include "qz_weight.cuh"
+
+namespace qz {
+
+constexpr int kModeLinear = 0;    // y = x W^T
+constexpr int kModeGated = 1;     // h = act(x W0^T) * (x W1^T)
+constexpr int kModeBackward = 2;  // dx = x0 W0 (+ x1 W1)
+
+struct ProductArgs {
+  int mode, format, log2_block, n_weights, act;
+  bool out_f32;
+  WeightView w0, w1;
+  int64_t rows, cols, tokens;
+  const uint16_t *x0, *x1;  // bf16 [tokens, ld_x]: the activations, or the gradients dy / (dg, du)
+  int64_t ld_x;
+  void* y;                  // bf16 or fp32 [tokens, ld_y]
+  int64_t ld_y;
+  uint16_t *g_out, *u_out;  // bf16 [tokens, ld_gu] or null
+  int64_t ld_gu;
+};
+
+}  // namespace qz
