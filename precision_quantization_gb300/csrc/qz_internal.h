@@ -77,6 +77,9 @@ qz_status launch_quant_dot(const uint32_t* w, const float* scales, const uint32_
                            int64_t n0, int64_t mid, int64_t group, const void* y, int64_t ld_y,
                            int64_t n1, float* z, int64_t ld_z, cudaStream_t s);
 
+// cuTensorMapEncodeTiled, looked up once (null where the driver lacks it)
+void* tensor_map_encoder();
+
 inline qz_status launch_status() {
   return cudaGetLastError() == cudaSuccess ? QZ_OK : QZ_ERR_CUDA;
 }

@@ -119,6 +119,11 @@ qz_status run_tile(const ProductArgs& p, cudaStream_t s) {
 }
 
 qz_status launch_product(const ProductArgs& p, cudaStream_t s) {
+  if (product_tc_applicable(p)) {
+    if (p.format == QZ_MXFP4) return launch_product_tc_mxfp4(p, s);
+    if (p.format == QZ_NVFP4) return launch_product_tc_nvfp4(p, s);
+    return launch_product_tc_int4(p, s);
+  }
   if (p.format == QZ_MXFP4) return run_tile<QZ_MXFP4>(p, s);
   if (p.format == QZ_NVFP4) return run_tile<QZ_NVFP4>(p, s);
   return run_tile<QZ_INT4>(p, s);
@@ -190,6 +195,18 @@ qz_status launch_gate_grad(const GateGradArgs& a, int act, cudaStream_t s) {
   void* args[] = {const_cast<GateGradArgs*>(&a)};
   return cudaLaunchKernel(k, dim3(grid), dim3(256), args, 0, s) == cudaSuccess ? launch_status() : QZ_ERR_CUDA;
 }
+
+}  // namespace
+
+bool product_tc_applicable(const ProductArgs& p) {
+  const auto a16 = [](const void* q) { return aligned(q, 16); };
+  const int64_t big = int64_t{1} << 30;
+  return p.cols % 32 == 0 && p.cols > 0 && p.rows > 0 && p.cols < big && p.rows < big && p.tokens < big && p.ld_x % 8 == 0 &&
+         a16(p.x0) && a16(p.w0.codes) && (p.n_weights == 1 || a16(p.w1.codes)) &&
+         (p.mode != kModeBackward || p.n_weights == 1 || a16(p.x1));
+}
+
+namespace {
 
 // ---- checks -------------------------------------------------------------------------------------
 constexpr int64_t kMaxDim = int64_t{1} << 31;

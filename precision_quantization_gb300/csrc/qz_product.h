@@ -26,4 +26,11 @@ struct ProductArgs {
   int64_t ld_gu;
 };
 
+// The tcgen05 kernels (qz_product_tc.cuh): applicable when cols % 32 == 0 and codes, activations
+// and their rows are 16-byte aligned.
+bool product_tc_applicable(const ProductArgs& p);
+qz_status launch_product_tc_mxfp4(const ProductArgs& p, cudaStream_t s);
+qz_status launch_product_tc_nvfp4(const ProductArgs& p, cudaStream_t s);
+qz_status launch_product_tc_int4(const ProductArgs& p, cudaStream_t s);
+
 }  // namespace qz

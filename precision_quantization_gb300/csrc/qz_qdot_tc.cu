@@ -725,6 +725,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 
 }  // namespace
 
+void* tensor_map_encoder() { return reinterpret_cast<void*>(encoder()); }
+
 bool quant_dot_tc_applicable(const uint32_t* w, int64_t n0, int64_t mid, int64_t group, const void* y,
                              int64_t ld_y, int64_t n1) {
   return n1 > 8 && group % 16 == 0 && mid % kBK == 0 && mid < (int64_t{1} << 30) && n0 < (int64_t{1} << 30) &&
