@@ -41,25 +41,27 @@ namespace {
 
 constexpr int kBM = 128;            // outputs per CTA (MMA rows, tensor-memory lanes)
 constexpr int kBK = 64;             // summands per step: 128 bytes of bf16, one swizzle row
-constexpr int kThreadsTc = 512;
-constexpr int kDecWarp0 = 4, kDecWarps = 8, kEpiWarp0 = 12, kEpiWarps = 4;
+constexpr int kDecWarp0 = 4, kEpiWarps = 4;
 constexpr uint32_t kABytes = kBM * kBK * 2;        // 16 KiB of decoded weights
-constexpr uint32_t kCodeBytes = kBM * kBK / 2;     // 4 KiB of codes per step
+constexpr uint32_t kBoxBytes = kBM * kBK;          // 8 KiB of codes: a box of two steps
 constexpr uint32_t kTmemCols = 512;                // two accumulators of 256 columns
 constexpr uint64_t kTcWaitNs = 1000000000ull;      // 1 s: far beyond any step's latency
-constexpr int kMaxBStages = 8, kCodeSlots = 10;    // code ring: ten steps
-constexpr int kMaxAStages = 4;
+constexpr int kMaxBStages = 8, kMaxAStages = 6, kMaxBoxes = 6;
 
 template <int FMT>
 struct TcFormat {
-  static constexpr int kTerms = FMT == QZ_INT4 ? 2 : 1;  // bf16 terms per weight
-  static constexpr int kAStages = FMT == QZ_INT4 ? 3 : 4;
+  static constexpr int kTerms = FMT == QZ_INT4 ? 2 : 1;      // bf16 terms per weight
+  static constexpr int kGroups = FMT == QZ_INT4 ? 2 : 3;     // decoder groups of four warps
+  // Stages of decoded weights: a box of two steps per group.  Both this ring and the code ring hold
+  // a whole number of rounds of the groups, so a slot belongs to one group, which is never a lap
+  // ahead of another on it (a parity wait could not tell the laps apart).
+  static constexpr int kAStages = 2 * kGroups;
+  static constexpr int kEpiWarp0 = kDecWarp0 + 4 * kGroups;
+  static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 };
-template <int FMT>
-constexpr uint32_t kARing = TcFormat<FMT>::kAStages * TcFormat<FMT>::kTerms * kABytes;
 constexpr uint32_t kSmemMax = 227 * 1024 - 2048;   // dynamic; the barriers are static
 template <int FMT>
-constexpr uint32_t kBRoom = kSmemMax - 1024 - kARing<FMT> - kCodeSlots * kCodeBytes;
+constexpr uint32_t kRingRoom = kSmemMax - 1024 - TcFormat<FMT>::kAStages * TcFormat<FMT>::kTerms * kABytes;  // codes and tokens
 
 struct TcArgs {
   CUtensorMap map_x0, map_x1;  // bf16 [tokens][sum], box 64 x (tokens of a CTA's load)
@@ -69,9 +71,11 @@ struct TcArgs {
   ProductArgs p;
   int nout, nsum;         // outputs and summands (per weight)
   int blocks_row;         // scales per weight row
-  int steps_w, steps;     // steps per weight, in all (backward: both weights one after the other)
+  int steps_w, steps;     // steps per weight (even; the last may lie past the sum, where copies
+                          // give zeros), in all (backward: both weights one after the other)
   int n;                  // tokens per tile (a multiple of 32)
-  int b_stages;
+  int boxes, b_stages;    // slots of the code ring (a multiple of the decoder groups), of the tokens' ring
+  bool scales_vec;        // the scales of 64 columns are one aligned load
   int tiles_n, tiles;
   int slices, slice_steps;  // Alone: slices of the sum (the cluster), steps per slice
 };
@@ -90,19 +94,12 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// arrive on a barrier of this CTA or (shared::cluster address) of another in the cluster
+__device__ __forceinline__ void arrive_local(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// arrive on a barrier of another CTA of the cluster (a shared::cluster address)
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
 }
 template <int CG>
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -177,10 +174,11 @@ __device__ __forceinline__ uint32_t idesc_of(int m, int n, bool a_mn) {
          (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// Bounded wait on phase `parity`.
 __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (try_wait_cluster(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
-  while (!try_wait_cluster(bar, parity)) {
+  while (!mbar_try_wait(bar, parity)) {
     if (*abort) return false;
     if (globaltimer_ns() - t0 > kTcWaitNs) {
       *abort = 1;
@@ -188,6 +186,13 @@ __device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile 
     }
   }
   return true;
+}
+// One lane of a converged warp.  The compiler knows that at most one thread passes, and so feeds
+// the uniform operands of tcgen05 and TMA instructions without a loop over the lanes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // After a wait has given up: let the copies already issued land before their memory is released.
@@ -199,7 +204,7 @@ __device__ __forceinline__ void let_land(uint64_t* full, int s, uint32_t ph, int
       s = stages - 1;
       ph ^= 1u;
     }
-    while (!try_wait_cluster(smem_addr(&full[s]), ph) && globaltimer_ns() - t0 < kTcWaitNs) {
+    while (!mbar_try_wait(smem_addr(&full[s]), ph) && globaltimer_ns() - t0 < kTcWaitNs) {
     }
   }
 }
@@ -222,48 +227,57 @@ __device__ __forceinline__ uint32_t nibble_pair(uint32_t t0, uint32_t t1) {
 // bits 6-8, and bf16's own exponent (biased 127 against 1) and subnormals do the rest.
 __device__ __forceinline__ uint32_t e2m1_pair(uint32_t d) { return (d * 0x1040u) & 0x81C081C0u; }
 
-// The scale(s) of one thread's 32 weights.  raw: an E8M0 byte, two E4M3 bytes, or fp32 (two for
-// groups of 16).
+// The scales of 64 columns of a weight row: two E8M0 bytes, four E4M3 bytes, or fp32.
 template <int FMT>
 struct Scales {
-  uint32_t a, b;
+  uint32_t v[FMT == QZ_INT4 ? 4 : 1];  // INT4: of each 16 columns
 };
 template <int FMT>
-__device__ __forceinline__ Scales<FMT> load_scales(const void* base, int64_t row_blocks, int col, int log2_block, bool in) {
-  Scales<FMT> s{0u, 0u};  // outside the weight: finite (its codes are 0)
-  if (!in) return s;
-  const int64_t i = row_blocks + (col >> log2_block);
-  if constexpr (FMT == QZ_MXFP4) {
-    s.a = __ldg(static_cast<const uint8_t*>(base) + i);
-  } else if constexpr (FMT == QZ_NVFP4) {
-    s.a = __ldg(static_cast<const uint8_t*>(base) + i);
-    s.b = __ldg(static_cast<const uint8_t*>(base) + i + 1);
+__device__ __forceinline__ Scales<FMT> load_scales(const void* base, int64_t row_first, int col, int cols, bool row_in, int log2_block, bool vec) {
+  Scales<FMT> s{};  // outside the weight: finite (its codes are 0)
+  if (!row_in || col >= cols) return s;
+  const int64_t i = row_first + (col >> log2_block);
+  if constexpr (FMT == QZ_INT4) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (col + 16 * q >= cols) break;
+      s.v[q] = __ldg(static_cast<const uint32_t*>(base) + i + ((16 * q) >> log2_block));
+    }
   } else {
-    s.a = __ldg(static_cast<const uint32_t*>(base) + i);
-    s.b = log2_block == 4 ? __ldg(static_cast<const uint32_t*>(base) + i + 1) : s.a;
+    constexpr int kN = FMT == QZ_MXFP4 ? 2 : 4;  // bytes
+    const uint8_t* p = static_cast<const uint8_t*>(base) + i;
+    if (vec) {
+      if constexpr (FMT == QZ_MXFP4) s.v[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
+      else s.v[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    } else {
+#pragma unroll
+      for (int q = 0; q < kN; ++q)
+        if (col + (64 / kN) * q < cols) s.v[0] |= static_cast<uint32_t>(__ldg(p + q)) << (8 * q);
+    }
   }
   return s;
 }
 
-// 32 weights (16 bytes of codes) to bf16, stored as four 16-byte chunks of line `line`:
-// chunk 4 half + j at its swizzled place.
+// 32 weights (16 bytes of codes; half h of a line's 64) to bf16, stored as chunks 4 h .. 4 h + 3
+// of the line at `dst`, each at its swizzled place (x: line % 8).
 template <int FMT>
-__device__ __forceinline__ void decode32(const uint4 codes, const Scales<FMT> s, uint32_t dst, uint32_t line_addr, int line, int half) {
+__device__ __forceinline__ void decode32(const uint4 codes, const Scales<FMT>& s, uint32_t dst, int x, int h) {
   const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
   uint32_t f0, f1;  // bf16 pairs: the factor of the first and the second 16 weights
-  bool big = false;
   uint32_t extra = 0x3F803F80u;
+  bool big = false;
   if constexpr (FMT == QZ_MXFP4) {
-    // 2^(E - 127) 2^126 as bf16 has exponent field E + 126; fields above 254 take a second factor
-    const uint32_t e = min(s.a + 126u, 254u);
-    f0 = s.a == 255u ? 0x7FC07FC0u : (e << 7) * 0x00010001u;
+    // 2^(E - 127) 2^126 as bf16 has exponent field E + 126; what exceeds 254 is a second factor
+    const uint32_t E = (s.v[0] >> (8 * h)) & 255u;
+    f0 = E == 255u ? 0x7FC07FC0u : (min(E + 126u, 254u) << 7) * 0x00010001u;
     f1 = f0;
-    big = s.a > 128u && s.a != 255u;
-    if (big) extra = ((s.a - 128u + 127u) << 7) * 0x00010001u;
+    big = E > 128u;
+    if (big) extra = ((E - 1u) << 7) * 0x00010001u;  // 2^(E - 128); NaN stays NaN
   } else if constexpr (FMT == QZ_NVFP4) {
     // an E4M3 byte at bits 4-10 is its value times 2^-120 as bf16; 2^127 and 2^111 bring it to
     // 2^118 times its value (below 2^127), so a weight comes out as 2^-8 of its own
-    uint32_t c = (s.a << 4) | (s.b << 20);
+    const uint32_t b = s.v[0] >> (16 * h);
+    uint32_t c = ((b & 255u) << 4) | ((b & 0xff00u) << 12);
     c = mul_bf16x2(mul_bf16x2(c, 0x7F007F00u), 0x77007700u);
     f0 = (c & 0xffffu) * 0x00010001u;
     f1 = (c >> 16) * 0x00010001u;
@@ -272,9 +286,9 @@ __device__ __forceinline__ void decode32(const uint4 codes, const Scales<FMT> s,
   for (int j = 0; j < 4; ++j) {
     const uint32_t t0 = cw[j] & 0x0F0F0F0Fu, t1 = (cw[j] >> 4) & 0x0F0F0F0Fu;
     uint32_t d[4] = {nibble_pair<0>(t0, t1), nibble_pair<1>(t0, t1), nibble_pair<2>(t0, t1), nibble_pair<3>(t0, t1)};
-    const uint32_t at = dst + line_addr + static_cast<uint32_t>(((4 * half + j) ^ (line & 7)) << 4);
+    const uint32_t at = dst + static_cast<uint32_t>(((4 * h + j) ^ x) << 4);
     if constexpr (FMT == QZ_INT4) {
-      const float sc = __uint_as_float(j < 2 ? s.a : s.b);
+      const float sc = __uint_as_float(s.v[2 * h + (j >> 1)]);
       uint32_t lo[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -378,15 +392,13 @@ __device__ __forceinline__ void store8(const TcArgs& a, StoreFlags f, const floa
 // ---- the kernel ---------------------------------------------------------------------------------
 // PAIR = true: CG = 2, persistent; false: CG = 1, one tile per cluster of a.slices CTAs.
 template <int FMT, int MODE, bool PAIR>
-__global__ void __launch_bounds__(kThreadsTc, 1) product_tc_kernel(const __grid_constant__ TcArgs a) {
+__global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(const __grid_constant__ TcArgs a) {
   constexpr int CG = PAIR ? 2 : 1;
-  constexpr int kTerms = TcFormat<FMT>::kTerms, kAStages = TcFormat<FMT>::kAStages;
-  constexpr int kStepsPerCode = MODE == kModeBackward ? 1 : 2;      // steps of one code box
-  constexpr int kSlots = kCodeSlots / kStepsPerCode;
+  constexpr int kTerms = TcFormat<FMT>::kTerms, kGroups = TcFormat<FMT>::kGroups, kEpiWarp0 = TcFormat<FMT>::kEpiWarp0;
   constexpr int kOut = MODE == kModeGated ? kBM / 2 : kBM;          // outputs per CTA
   extern __shared__ uint8_t tc_raw[];
   __shared__ __align__(8) uint64_t b_full[kMaxBStages], b_empty[kMaxBStages], a_full[kMaxAStages], a_empty[kMaxAStages];
-  __shared__ __align__(8) uint64_t c_full[kCodeSlots], c_empty[kCodeSlots], d_full[2], d_empty[2], drain;
+  __shared__ __align__(8) uint64_t c_full[kMaxBoxes], c_empty[kMaxBoxes], d_full[2], d_empty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int s_abort;
 
@@ -394,10 +406,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1) product_tc_kernel(const __grid_
   const uint32_t rank = cluster_rank();
   const bool leader = !PAIR || rank == 0;
   const uint32_t base = (smem_addr(tc_raw) + 1023u) & ~1023u;
-  const uint32_t a_base = base, c_base = base + kARing<FMT>, b_base = c_base + kCodeSlots * kCodeBytes;
+  constexpr int a_stages = TcFormat<FMT>::kAStages;
+  const int boxes = a.boxes, b_stages = a.b_stages;
+  const uint32_t a_base = base, c_base = base + a_stages * (kTerms * kABytes), b_base = c_base + boxes * kBoxBytes;
   const int b_rows = a.n / CG;                       // tokens that this CTA loads
   const uint32_t b_bytes = static_cast<uint32_t>(b_rows) * kBK * 2;
-  const int b_stages = a.b_stages;
 
   if (tid == 0) {
     for (int s = 0; s < kMaxBStages; ++s) {
@@ -405,12 +418,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1) product_tc_kernel(const __grid_
       mbar_init(smem_addr(&b_empty[s]), 1);
     }
     for (int s = 0; s < kMaxAStages; ++s) {
-      mbar_init(smem_addr(&a_full[s]), kDecWarps * CG);
+      mbar_init(smem_addr(&a_full[s]), PAIR && rank == 0 ? 5 : 4);  // a group's warps, and the peer's word
       mbar_init(smem_addr(&a_empty[s]), 1);
     }
-    for (int s = 0; s < kCodeSlots; ++s) {
+    for (int s = 0; s < kMaxBoxes; ++s) {
       mbar_init(smem_addr(&c_full[s]), 1);
-      mbar_init(smem_addr(&c_empty[s]), kDecWarps);
+      mbar_init(smem_addr(&c_empty[s]), 4);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_addr(&d_full[s]), 1);
@@ -445,7 +458,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) product_tc_kernel(const __grid_
   const auto tile_n0 = [&](int t) { return (t % a.tiles_n) * a.n; };
 
   if (warp == 0) {
-    if (lane == 0) {
+    if (elect_one()) {
       int s = 0;
       uint32_t ph = 0, issued = 0;
       bool ok = true;
@@ -468,18 +481,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1) product_tc_kernel(const __grid_
     }
     __syncwarp();
   } else if (warp == 2) {
-    if (lane == 0) {
+    if (elect_one()) {
       int s = 0;
       uint32_t ph = 0, issued = 0;
       bool ok = true;
       for (int t = first; t < tile_end && ok; t += tile_step) {
         const int m0 = tile_m0(t);
-        for (int st = st_begin; st < st_end; st += kStepsPerCode) {
+        for (int st = st_begin; st < st_end; st += 2) {
           if (!(ok = tc_wait(smem_addr(&c_empty[s]), ph ^ 1u, &s_abort))) break;
-          const uint32_t fb = smem_addr(&c_full[s]), dst = c_base + s * (kStepsPerCode * kCodeBytes);
-          mbar_expect_tx(fb, kStepsPerCode * kCodeBytes);
+          const uint32_t fb = smem_addr(&c_full[s]), dst = c_base + s * kBoxBytes;
+          mbar_expect_tx(fb, kBoxBytes);
           if constexpr (MODE == kModeBackward) {
-            // 64 weight rows x 128 columns (64 bytes)
+            // 128 weight rows x 128 columns (64 bytes)
             const bool second = st >= a.steps_w;
             tma_load<1>(dst, second ? &a.map_w1 : &a.map_w0, m0 / 2, (second ? st - a.steps_w : st) * kBK, fb);
           } else if constexpr (MODE == kModeGated) {
@@ -493,17 +506,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1) product_tc_kernel(const __grid_
             tma_load<1>(dst, &a.map_w0, st * (kBK / 2), m0, fb);
           }
           ++issued;
-          if (++s == kSlots) {
+          if (++s == boxes) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
-      if (s_abort) let_land(c_full, s, ph, kSlots, issued);
+      if (s_abort) let_land(c_full, s, ph, boxes, issued);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
+    if (leader) {
       const uint32_t idesc = idesc_of(kBM * CG, a.n, MODE == kModeBackward);
       int bs = 0, as = 0, buf = 0;
       uint32_t bph = 0, aph = 0, dph = 3u;  // dph: parity bit per accumulator of the next "empty" wait
@@ -514,30 +527,33 @@ __global__ void __launch_bounds__(kThreadsTc, 1) product_tc_kernel(const __grid_
           const bool start = st == st_begin || (MODE == kModeBackward && st == a.steps_w);
           if (start) {
             if (st != st_begin) {
-              tc_commit<CG>(smem_addr(&d_full[buf]));
+              if (elect_one()) tc_commit<CG>(smem_addr(&d_full[buf]));
               buf ^= 1;
             }
-            if (!(ok = tc_wait(smem_addr(&d_empty[buf]), (dph >> buf) & 1u, &s_abort))) break;
+            if (!(ok = __all_sync(kFull, tc_wait(smem_addr(&d_empty[buf]), (dph >> buf) & 1u, &s_abort)))) break;
             dph ^= 1u << buf;
           }
-          if (!(ok = tc_wait(smem_addr(&b_full[bs]), bph, &s_abort) && tc_wait(smem_addr(&a_full[as]), aph, &s_abort))) break;
+          if (!(ok = __all_sync(kFull, tc_wait(smem_addr(&b_full[bs]), bph, &s_abort) && tc_wait(smem_addr(&a_full[as]), aph, &s_abort)))) break;
           tc_fence_after();
           const uint32_t at = a_base + as * (kTerms * kABytes);
           const uint64_t bd = desc_sw128(b_base + bs * b_bytes, 16u, 1024u);
+          if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < kBK / 16; ++j) {
+            for (int j = 0; j < kBK / 16; ++j) {
 #pragma unroll
-            for (int k = 0; k < kTerms; ++k) {
-              // K-major A: lines of 128 bytes, 32 bytes a 16-wide step; MN-major A: two slabs of
-              // 64 outputs, 8 KiB apart, 16 lines (2 KiB) a step
-              const uint64_t ad = MODE == kModeBackward ? desc_sw128(at + k * kABytes, 8192u, 1024u) + 128u * j
-                                                        : desc_sw128(at + k * kABytes, 16u, 1024u) + 2u * j;
-              tc_mma<CG>(tmem + static_cast<uint32_t>(buf) * 256u, ad, bd + 2u * j, idesc, !(start && j == 0 && k == 0));
+              for (int k = 0; k < kTerms; ++k) {
+                // K-major A: lines of 128 bytes, 32 bytes a 16-wide step; MN-major A: two slabs of
+                // 64 outputs, 8 KiB apart, 16 lines (2 KiB) a step
+                const uint64_t ad = MODE == kModeBackward ? desc_sw128(at + k * kABytes, 8192u, 1024u) + 128u * j
+                                                          : desc_sw128(at + k * kABytes, 16u, 1024u) + 2u * j;
+                tc_mma<CG>(tmem + static_cast<uint32_t>(buf) * 256u, ad, bd + 2u * j, idesc, !(start && j == 0 && k == 0));
+              }
             }
+            tc_commit<CG>(smem_addr(&a_empty[as]));
+            tc_commit<CG>(smem_addr(&b_empty[bs]));
           }
-          tc_commit<CG>(smem_addr(&a_empty[as]));
-          tc_commit<CG>(smem_addr(&b_empty[bs]));
-          if (++as == kAStages) {
+          __syncwarp();
+          if (++as == a_stages) {
             as = 0;
             aph ^= 1u;
           }
@@ -548,88 +564,105 @@ __global__ void __launch_bounds__(kThreadsTc, 1) product_tc_kernel(const __grid_
         }
         if (!ok) break;
         if (st_begin < st_end) {
-          tc_commit<CG>(smem_addr(&d_full[buf]));
+          if (elect_one()) tc_commit<CG>(smem_addr(&d_full[buf]));
           buf ^= 1;
         }
       }
       // every MMA issued has completed before tensor memory and shared memory are released
-      tc_commit<CG>(smem_addr(&drain));
-    }
-    __syncwarp();
-  } else if (warp >= kDecWarp0 && warp < kDecWarp0 + kDecWarps) {
-    // thread i: line i % 128 (an output; backward: a slab's weight row), half i / 128 of its 64
-    const int i = tid - kDecWarp0 * 32, line = i & 127, half = i >> 7;
-    const uint32_t line_addr = 128u * line;
-    const uint32_t full0 = PAIR ? map_to_rank(smem_addr(&a_full[0]), 0) : smem_addr(&a_full[0]);
-    int as = 0, cs = 0;
-    uint32_t aph = 0, cph = 0;
-    bool ok = true;
-    for (int t = first; t < tile_end && ok; t += tile_step) {
-      const int m0 = tile_m0(t);
-      // the scales of step st, (row, first column) of this thread's 32 weights
-      const auto scales_of = [&](int st) {
-        int row, col;
-        const void* base;
-        if constexpr (MODE == kModeBackward) {
-          const bool second = st >= a.steps_w;
-          row = (second ? st - a.steps_w : st) * kBK + (line & 63);
-          col = m0 + 64 * (line >> 6) + 32 * half;
-          base = second ? a.scales1 : a.scales0;
-        } else {
-          col = st * kBK + 32 * half;
-          if constexpr (MODE == kModeGated) {
-            row = m0 + 16 * (line >> 5) + (line & 15);
-            base = (line & 16) ? a.scales1 : a.scales0;
-          } else {
-            row = m0 + line;
-            base = a.scales0;
-          }
-        }
-        const bool in = st < st_end && row < (MODE == kModeBackward ? a.nsum : a.nout) && col < a.p.cols;
-        return load_scales<FMT>(base, static_cast<int64_t>(row) * a.blocks_row, col, a.p.log2_block, in);
-      };
-      constexpr int kAhead = 4;  // steps that the scales are loaded ahead
-      Scales<FMT> sc[kAhead];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) sc[k] = scales_of(st_begin + k);
-      for (int st0 = st_begin; st0 < st_end && ok; st0 += kAhead) {
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const int st = st0 + k;
-          if (st >= st_end) break;
-          const int sub = kStepsPerCode == 2 ? k & 1 : 0;  // slices start at even steps
-          if (sub == 0 && !__all_sync(kFull, tc_wait(smem_addr(&c_full[cs]), cph, &s_abort))) {
-            ok = false;
-            break;
-          }
-          // the code box has 64-byte lines, 64-byte swizzle: 16-byte chunk c of line l is at
-          // c ^ (l / 2 % 4)
-          const int cl = MODE == kModeBackward ? line & 63 : line;
-          const int c = MODE == kModeBackward ? 2 * (line >> 6) + half : 2 * sub + half;
-          const uint4 codes = lds16(c_base + cs * (kStepsPerCode * kCodeBytes) + 64u * cl + static_cast<uint32_t>((c ^ ((cl >> 1) & 3)) << 4));
-          const Scales<FMT> now = sc[k];
-          sc[k] = scales_of(st + kAhead);
-          if (sub == kStepsPerCode - 1 || st + 1 == st_end) {
-            __syncwarp();
-            if (lane == 0) arrive_cluster(smem_addr(&c_empty[cs]));
-            if (++cs == kSlots) {
-              cs = 0;
-              cph ^= 1u;
-            }
-          }
-          if (!__all_sync(kFull, tc_wait(smem_addr(&a_empty[as]), aph ^ 1u, &s_abort))) {
-            ok = false;
-            break;
-          }
-          decode32<FMT>(codes, now, a_base + as * (kTerms * kABytes), line_addr, line, half);
-          fence_proxy_async();  // the stores, before the tensor cores read them
-          __syncwarp();
-          if (lane == 0) arrive_cluster(full0 + 8u * as);
-          if (++as == kAStages) {
+      if (elect_one()) tc_commit<CG>(smem_addr(&drain));
+    } else {
+      // The second CTA of a pair: passes its decoders' arrivals on to the first, one for a stage.  A
+      // release at cluster scope waits for the thread's loads in flight, which the decoders
+      // always have (1100 cycles a step when they signalled the first CTA themselves).
+      int as = 0;
+      uint32_t aph = 0;
+      const uint32_t to = map_to_rank(smem_addr(&a_full[0]), 0);
+      bool ok = true;
+      for (int t = first; t < tile_end && ok; t += tile_step)
+        for (int st = st_begin; st < st_end; ++st) {
+          if (!(ok = __all_sync(kFull, tc_wait(smem_addr(&a_full[as]), aph, &s_abort)))) break;
+          if (elect_one()) arrive_cluster(to + 8u * as);
+          if (++as == a_stages) {
             as = 0;
             aph ^= 1u;
           }
         }
+    }
+    __syncwarp();
+  } else if (warp >= kDecWarp0 && warp < kEpiWarp0) {
+    // Group g of four warps takes every kGroups-th box (two steps); thread i of it line i of each:
+    // an output (backward: weight row i % 64 of the step, outputs 64 (i / 64) .. + 63).
+    const int group = (warp - kDecWarp0) >> 2, line = (tid - kDecWarp0 * 32) & 127, x = line & 7;
+    const uint32_t line_addr = 128u * line;
+    // the code box has 64-byte lines with a 64-byte swizzle: 16-byte chunk c of line l is at
+    // c ^ (l / 2 % 4); a thread's chunks are 2 k and 2 k + 1 of step k (backward: of its slab)
+    const int cl = MODE == kModeBackward ? line & 63 : line, cx = (cl >> 1) & 3;
+    const int per_tile = (st_end - st_begin + 1) / 2;  // boxes
+    int t = first, st = st_begin + 2 * group;          // this group's box
+    const int as0 = 2 * group;                         // its two stages
+    int cs = group;
+    uint32_t aph = 0, cph = 0;
+    const auto settle = [&]() {  // st past the tile's end: the next tiles'
+      while (t < tile_end && st >= st_end) {
+        st -= 2 * per_tile;
+        t += tile_step;
+      }
+    };
+    const auto scales_of = [&](int k) {
+      const int m0 = tile_m0(t);
+      int row, col;
+      const void* base;
+      if constexpr (MODE == kModeBackward) {
+        const bool second = st >= a.steps_w;
+        row = (second ? st - a.steps_w : st) * kBK + 64 * k + (line & 63);
+        col = m0 + 64 * (line >> 6);
+        base = second ? a.scales1 : a.scales0;
+      } else {
+        col = st * kBK + 64 * k;
+        if constexpr (MODE == kModeGated) {
+          row = m0 + 16 * (line >> 5) + (line & 15);
+          base = (line & 16) ? a.scales1 : a.scales0;
+        } else {
+          row = m0 + line;
+          base = a.scales0;
+        }
+      }
+      return load_scales<FMT>(base, static_cast<int64_t>(row) * a.blocks_row, col, static_cast<int>(a.p.cols),
+                              t < tile_end && row < (MODE == kModeBackward ? a.nsum : a.nout), a.p.log2_block, a.scales_vec);
+    };
+    settle();
+    Scales<FMT> next[2] = {scales_of(0), scales_of(1)};
+    bool ok = true;
+    while (t < tile_end && ok) {
+      const Scales<FMT> now[2] = {next[0], next[1]};
+      st += 2 * kGroups;
+      settle();
+      next[0] = scales_of(0);  // of this group's next box, in flight during this one
+      next[1] = scales_of(1);
+      if (!__all_sync(kFull, tc_wait(smem_addr(&c_full[cs]), cph, &s_abort))) break;
+      const uint32_t box = c_base + cs * kBoxBytes;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t from = box + 64u * cl + (MODE == kModeBackward ? 4096u * k : 0u);
+        const int c = 2 * (MODE == kModeBackward ? line >> 6 : k);
+        const uint4 c0 = lds16(from + static_cast<uint32_t>((c ^ cx) << 4)), c1 = lds16(from + static_cast<uint32_t>(((c + 1) ^ cx) << 4));
+        if (k == 1) {
+          __syncwarp();
+          if (lane == 0) arrive_local(smem_addr(&c_empty[cs]));
+        }
+        if (!(ok = __all_sync(kFull, tc_wait(smem_addr(&a_empty[as0 + k]), aph ^ 1u, &s_abort)))) break;
+        const uint32_t dst = a_base + (as0 + k) * (kTerms * kABytes) + line_addr;
+        decode32<FMT>(c0, now[k], dst, x, 0);
+        decode32<FMT>(c1, now[k], dst, x, 1);
+        fence_proxy_async();  // the stores, before the tensor cores read them
+        __syncwarp();
+        if (lane == 0) arrive_local(smem_addr(&a_full[as0 + k]));
+      }
+      aph ^= 1u;
+      cs += kGroups;
+      if (cs >= boxes) {
+        cs -= boxes;
+        cph ^= 1u;
       }
     }
   } else if (PAIR && warp >= kEpiWarp0) {
@@ -689,7 +722,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) product_tc_kernel(const __grid_
   if constexpr (!PAIR) {
     // ---- the slices of the tile: partial sums to the CTA that finishes their columns ----------
     const int slices = a.slices, cols = a.n / slices;  // columns this CTA finishes
-    const int quarter = warp & 3, part = warp >> 2;    // 16 warps: four column parts a quarter
+    const int quarter = warp & 3, part = warp >> 2;    // the warps of a quarter share the columns
+    constexpr int kStride = 8 * (TcFormat<FMT>::kThreads / 128);
     const uint32_t ta = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     constexpr float kUnit = FMT == QZ_NVFP4 ? 256.0f : 1.0f;
     const float f0 = sum_factor<FMT>(a.tscale0) * kUnit, f1 = a.p.n_weights == 2 ? sum_factor<FMT>(a.tscale1) * kUnit : 0.0f;
@@ -719,7 +753,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) product_tc_kernel(const __grid_
     };
     if (slices > 1) {
       cluster_sync();  // every slice's rings are idle: their memory takes the partial sums
-      for (int c = 8 * part; c < a.n; c += 32) {
+      for (int c = 8 * part; c < a.n; c += kStride) {
         const int dst = c / cols;
         if (dst == static_cast<int>(rank) || n0 + c >= a.p.tokens) continue;
         float v[8];
@@ -733,7 +767,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) product_tc_kernel(const __grid_
     const StoreFlags fl{(reinterpret_cast<uintptr_t>(a.p.y) & 3u) == 0 && (a.p.ld_y & 1) == 0,
                         (reinterpret_cast<uintptr_t>(a.p.g_out) & 3u) == 0 && (reinterpret_cast<uintptr_t>(a.p.u_out) & 3u) == 0 && (a.p.ld_gu & 1) == 0};
     const int c_begin = static_cast<int>(rank) * cols;
-    for (int c = 8 * part; c < cols && n0 + c_begin + c < a.p.tokens; c += 32) {
+    for (int c = 8 * part; c < cols && n0 + c_begin + c < a.p.tokens; c += kStride) {
       float mine[8], v[8];
       own(c_begin + c, mine);
 #pragma unroll
@@ -786,7 +820,7 @@ qz_status run_tc(const TcArgs& a, int grid, cudaStream_t s) {
   at[0].val.clusterDim.x = PAIR ? 2u : static_cast<unsigned>(a.slices);
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreadsTc);
+  cfg.blockDim = dim3(TcFormat<FMT>::kThreads);
   cfg.dynamicSmemBytes = kSmemMax;
   cfg.stream = s;
   cfg.attrs = at;
@@ -807,7 +841,7 @@ struct Plan {
   bool pair;
   int n, tiles_n, tiles, slices, slice_steps, grid;
 };
-inline Plan plan_of(int64_t nout, int out_per_cta, int64_t tokens, int steps, int even, int terms) {
+inline Plan plan_of(int64_t nout, int out_per_cta, int64_t tokens, int steps, int terms) {
   const int sms = sm_count();
   Plan best{};
   double best_cost = 1e30;
@@ -827,7 +861,7 @@ inline Plan plan_of(int64_t nout, int out_per_cta, int64_t tokens, int steps, in
     const int ns = n % (8 * s) ? (n + 8 * s - 1) / (8 * s) * (8 * s) : n;  // columns divide into eights per slice
     const int64_t tiles = (nout + out_per_cta - 1) / out_per_cta * tiles_n;
     int per = (steps + s - 1) / s;
-    per += per % even;
+    per += per & 1;  // whole boxes
     const int64_t clusters = std::max(1, s == 1 ? sms : (s == 2 ? sms * 9 / 10 : sms * 5 / 6) / s);
     const double cost = static_cast<double>((tiles + clusters - 1) / clusters) * (per * std::max(2.8 * ns, 300.0) * terms + 5000 + (s > 1 ? 2000 + 16.0 * ns : 0));
     if (ns <= 256 && tiles * s < (int64_t{1} << 30) && cost < best_cost) {
@@ -850,9 +884,9 @@ qz_status launch_tc(const ProductArgs& p, cudaStream_t s) {
   a.nout = static_cast<int>(back ? p.cols : p.rows);
   a.nsum = static_cast<int>(back ? p.rows : p.cols);
   a.blocks_row = static_cast<int>(p.cols >> p.log2_block);
-  a.steps_w = (a.nsum + kBK - 1) / kBK;
+  a.steps_w = (a.nsum + 2 * kBK - 1) / (2 * kBK) * 2;
   a.steps = back ? a.steps_w * p.n_weights : a.steps_w;
-  const Plan plan = plan_of(a.nout, p.mode == kModeGated ? kBM / 2 : kBM, p.tokens, a.steps, back ? 1 : 2, TcFormat<FMT>::kTerms);
+  const Plan plan = plan_of(a.nout, p.mode == kModeGated ? kBM / 2 : kBM, p.tokens, a.steps, TcFormat<FMT>::kTerms);
   if (plan.grid == 0) return QZ_ERR_UNSUPPORTED;
   a.n = plan.n;
   a.tiles_n = plan.tiles_n;
@@ -860,8 +894,14 @@ qz_status launch_tc(const ProductArgs& p, cudaStream_t s) {
   a.slices = plan.slices;
   a.slice_steps = plan.slice_steps;
   const int b_rows = plan.pair ? plan.n / 2 : plan.n;
-  a.b_stages = static_cast<int>(std::min<uint32_t>(kMaxBStages, kBRoom<FMT> / (static_cast<uint32_t>(b_rows) * kBK * 2)));
-  const int code_rows = back ? 64 : (p.mode == kModeGated ? 16 : 128);
+  // two rounds of code boxes, or one where the tokens' steps are too large to leave them three
+  const uint32_t stage_b = static_cast<uint32_t>(b_rows) * kBK * 2;
+  constexpr int kGroups = TcFormat<FMT>::kGroups;
+  a.boxes = kRingRoom<FMT> < 2 * kGroups * kBoxBytes + 3 * stage_b ? kGroups : 2 * kGroups;
+  a.b_stages = static_cast<int>(std::min<uint32_t>(kMaxBStages, (kRingRoom<FMT> - a.boxes * kBoxBytes) / stage_b));
+  const int align = p.format == QZ_MXFP4 ? 2 : 4;
+  a.scales_vec = p.cols % 64 == 0 && reinterpret_cast<uintptr_t>(a.scales0) % align == 0 && reinterpret_cast<uintptr_t>(a.scales1) % align == 0;
+  const int code_rows = p.mode == kModeGated ? 16 : 128;
   bool ok = encode(&a.map_x0, false, p.x0, a.nsum, p.tokens, p.ld_x * 2, kBK, b_rows) &&
             encode(&a.map_w0, true, p.w0.codes, p.cols / 2, p.rows, p.cols / 2, 64, code_rows);
   if (p.n_weights == 2) ok = ok && encode(&a.map_w1, true, p.w1.codes, p.cols / 2, p.rows, p.cols / 2, 64, code_rows);
