@@ -97,9 +97,11 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void arrive_local(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// arrive on a barrier of another CTA of the cluster (a shared::cluster address)
-__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Arrive on a barrier of another CTA of the cluster (a shared::cluster address).  What it announces
+// is read by the tensor core of this SM, behind a proxy fence, and by no thread of the other CTA,
+// so the default scope does; release.cluster waits for every load in flight (1100 cycles a step).
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 template <int CG>
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
       mbar_init(smem_addr(&b_empty[s]), 1);
     }
     for (int s = 0; s < kMaxAStages; ++s) {
-      mbar_init(smem_addr(&a_full[s]), PAIR && rank == 0 ? 5 : 4);  // a group's warps, and the peer's word
+      mbar_init(smem_addr(&a_full[s]), 4 * CG);  // a group's warps, in both CTAs
       mbar_init(smem_addr(&a_empty[s]), 1);
     }
     for (int s = 0; s < kMaxBoxes; ++s) {
@@ -570,23 +572,6 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
       }
       // every MMA issued has completed before tensor memory and shared memory are released
       if (elect_one()) tc_commit<CG>(smem_addr(&drain));
-    } else {
-      // The second CTA of a pair: passes its decoders' arrivals on to the first, one for a stage.  A
-      // release at cluster scope waits for the thread's loads in flight, which the decoders
-      // always have (1100 cycles a step when they signalled the first CTA themselves).
-      int as = 0;
-      uint32_t aph = 0;
-      const uint32_t to = map_to_rank(smem_addr(&a_full[0]), 0);
-      bool ok = true;
-      for (int t = first; t < tile_end && ok; t += tile_step)
-        for (int st = st_begin; st < st_end; ++st) {
-          if (!(ok = __all_sync(kFull, tc_wait(smem_addr(&a_full[as]), aph, &s_abort)))) break;
-          if (elect_one()) arrive_cluster(to + 8u * as);
-          if (++as == a_stages) {
-            as = 0;
-            aph ^= 1u;
-          }
-        }
     }
     __syncwarp();
   } else if (warp >= kDecWarp0 && warp < kEpiWarp0) {
@@ -600,6 +585,7 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
     const int per_tile = (st_end - st_begin + 1) / 2;  // boxes
     int t = first, st = st_begin + 2 * group;          // this group's box
     const int as0 = 2 * group;                         // its two stages
+    const uint32_t full0 = PAIR ? map_to_rank(smem_addr(&a_full[as0]), 0) : smem_addr(&a_full[as0]);
     int cs = group;
     uint32_t aph = 0, cph = 0;
     const auto settle = [&]() {  // st past the tile's end: the next tiles'
@@ -656,7 +642,10 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
         decode32<FMT>(c1, now[k], dst, x, 1);
         fence_proxy_async();  // the stores, before the tensor cores read them
         __syncwarp();
-        if (lane == 0) arrive_local(smem_addr(&a_full[as0 + k]));
+        if (lane == 0) {
+          if constexpr (PAIR) arrive_remote(full0 + 8u * k);
+          else arrive_local(full0 + 8u * k);
+        }
       }
       aph ^= 1u;
       cs += kGroups;
@@ -708,7 +697,7 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
       if (lane == 0) {
         for (int k = 0; k < (two ? 2 : 1); ++k) {
           const uint32_t bar = smem_addr(&d_empty[buf ^ k]);
-          arrive_cluster(map_to_rank(bar, 0));
+          arrive_remote(map_to_rank(bar, 0));
         }
       }
       if (!two) buf ^= 1;
