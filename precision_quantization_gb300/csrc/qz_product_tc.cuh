@@ -9,13 +9,15 @@
 // q s is held as the sum of two bf16 values (16 bits of it) and takes two MMAs.  So kind::f16
 // with fp32 accumulation gives the sums of include/qz.h without a rounding of the weights.
 //
-// Roles of a CTA of 16 warps (every wait is bounded):
-//   warp 0       streams the tokens' 64-wide steps into a shared-memory ring by TMA
-//   warp 2       streams the 4-bit codes into a ring of their own by TMA
-//   warps 4-11   decode: 256 threads take 32 weights of every step each (16 bytes of codes),
-//                turn them into bf16 and store them in the layout the MMA reads
-//   warp 1       issues the MMAs, four 16-wide ones a step (one thread)
-//   warps 12-15  read finished accumulators from tensor memory, apply the activation and store
+// Roles of a CTA's warps (every wait is bounded):
+//   warp 0       streams the tokens' 128-wide boxes (two 64-wide steps) into a ring by TMA
+//   warp 2       streams the 4-bit codes' boxes into a ring of their own by TMA
+//   decoders     two or three groups of four warps that take the boxes in turn: a thread turns a
+//                line's codes into bf16 and stores them in the layout the MMA reads
+//   warp 1       issues the MMAs, eight 16-wide ones a box (one thread)
+//   last four    read finished accumulators from tensor memory, apply the activation and store
+// A box is the unit of every hand-over: a wait or a commit of the issuing thread takes some 60 to
+// 140 cycles even when nothing is to be waited for, which 64-wide steps paid twice as often.
 // Two forms.  PAIR: two CTAs on neighbouring SMs share one 256 x 256 tile (cta_group::2: each
 // decodes its own 128 outputs and loads half of the tokens, so the shared-memory traffic per MMA
 // halves), persistent over the tiles, the epilogue of a tile beside the next tile's MMAs (two
@@ -44,24 +46,25 @@ constexpr int kBK = 64;             // summands per step: 128 bytes of bf16, one
 constexpr int kDecWarp0 = 4, kEpiWarps = 4;
 constexpr uint32_t kABytes = kBM * kBK * 2;        // 16 KiB of decoded weights
 constexpr uint32_t kBoxBytes = kBM * kBK;          // 8 KiB of codes: a box of two steps
+constexpr int kBoxK = 2 * kBK;
 constexpr uint32_t kTmemCols = 512;                // two accumulators of 256 columns
 constexpr uint64_t kTcWaitNs = 1000000000ull;      // 1 s: far beyond any step's latency
-constexpr int kMaxBStages = 8, kMaxAStages = 6, kMaxBoxes = 6;
+constexpr int kMaxBStages = 8, kMaxGroups = 3, kMaxBoxes = 6;
 
 template <int FMT>
 struct TcFormat {
   static constexpr int kTerms = FMT == QZ_INT4 ? 2 : 1;      // bf16 terms per weight
   static constexpr int kGroups = FMT == QZ_INT4 ? 2 : 3;     // decoder groups of four warps
-  // Stages of decoded weights: a box of two steps per group.  Both this ring and the code ring hold
-  // a whole number of rounds of the groups, so a slot belongs to one group, which is never a lap
-  // ahead of another on it (a parity wait could not tell the laps apart).
-  static constexpr int kAStages = 2 * kGroups;
+  // Stages of decoded weights: one box per group.  Both this ring and the code ring hold a whole
+  // number of rounds of the groups, so a slot belongs to one group, which is never a lap ahead of
+  // another on it (a parity wait could not tell the laps apart).
+  static constexpr uint32_t kStageBytes = 2 * kTerms * kABytes;
   static constexpr int kEpiWarp0 = kDecWarp0 + 4 * kGroups;
   static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 };
 constexpr uint32_t kSmemMax = 227 * 1024 - 2048;   // dynamic; the barriers are static
 template <int FMT>
-constexpr uint32_t kRingRoom = kSmemMax - 1024 - TcFormat<FMT>::kAStages * TcFormat<FMT>::kTerms * kABytes;  // codes and tokens
+constexpr uint32_t kRingRoom = kSmemMax - 1024 - TcFormat<FMT>::kGroups * TcFormat<FMT>::kStageBytes;  // codes and tokens
 
 struct TcArgs {
   CUtensorMap map_x0, map_x1;  // bf16 [tokens][sum], box 64 x (tokens of a CTA's load)
@@ -71,13 +74,13 @@ struct TcArgs {
   ProductArgs p;
   int nout, nsum;         // outputs and summands (per weight)
   int blocks_row;         // scales per weight row
-  int steps_w, steps;     // steps per weight (even; the last may lie past the sum, where copies
-                          // give zeros), in all (backward: both weights one after the other)
+  int boxes_w, boxes;     // 128-wide boxes per weight (past the sum's end copies give zeros), in all
+                          // (backward: both weights' one after the other)
   int n;                  // tokens per tile (a multiple of 32)
-  int boxes, b_stages;    // slots of the code ring (a multiple of the decoder groups), of the tokens' ring
+  int code_slots, b_stages;  // slots of the code ring (a multiple of the groups), of the tokens' ring
   bool scales_vec;        // the scales of 64 columns are one aligned load
   int tiles_n, tiles;
-  int slices, slice_steps;  // Alone: slices of the sum (the cluster), steps per slice
+  int slices, slice_boxes;  // Alone: slices of the sum (the cluster), boxes per slice
 };
 
 // ---- PTX ------------------------------------------------------------------------------------
@@ -399,7 +402,7 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
   constexpr int kTerms = TcFormat<FMT>::kTerms, kGroups = TcFormat<FMT>::kGroups, kEpiWarp0 = TcFormat<FMT>::kEpiWarp0;
   constexpr int kOut = MODE == kModeGated ? kBM / 2 : kBM;          // outputs per CTA
   extern __shared__ uint8_t tc_raw[];
-  __shared__ __align__(8) uint64_t b_full[kMaxBStages], b_empty[kMaxBStages], a_full[kMaxAStages], a_empty[kMaxAStages];
+  __shared__ __align__(8) uint64_t b_full[kMaxBStages], b_empty[kMaxBStages], a_full[kMaxGroups], a_empty[kMaxGroups];
   __shared__ __align__(8) uint64_t c_full[kMaxBoxes], c_empty[kMaxBoxes], d_full[2], d_empty[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int s_abort;
@@ -408,18 +411,18 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
   const uint32_t rank = cluster_rank();
   const bool leader = !PAIR || rank == 0;
   const uint32_t base = (smem_addr(tc_raw) + 1023u) & ~1023u;
-  constexpr int a_stages = TcFormat<FMT>::kAStages;
-  const int boxes = a.boxes, b_stages = a.b_stages;
-  const uint32_t a_base = base, c_base = base + a_stages * (kTerms * kABytes), b_base = c_base + boxes * kBoxBytes;
+  constexpr uint32_t kStageBytes = TcFormat<FMT>::kStageBytes;
+  const int code_slots = a.code_slots, b_stages = a.b_stages;
+  const uint32_t a_base = base, c_base = base + kGroups * kStageBytes, b_base = c_base + code_slots * kBoxBytes;
   const int b_rows = a.n / CG;                       // tokens that this CTA loads
-  const uint32_t b_bytes = static_cast<uint32_t>(b_rows) * kBK * 2;
+  const uint32_t b_bytes = static_cast<uint32_t>(b_rows) * kBK * 2;  // of a step; a box is two
 
   if (tid == 0) {
     for (int s = 0; s < kMaxBStages; ++s) {
       mbar_init(smem_addr(&b_full[s]), 1);
       mbar_init(smem_addr(&b_empty[s]), 1);
     }
-    for (int s = 0; s < kMaxAStages; ++s) {
+    for (int s = 0; s < kMaxGroups; ++s) {
       mbar_init(smem_addr(&a_full[s]), 4 * CG);  // a group's warps, in both CTAs
       mbar_init(smem_addr(&a_empty[s]), 1);
     }
@@ -454,8 +457,8 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
   const int first = PAIR ? static_cast<int>(blockIdx.x) / 2 : static_cast<int>(blockIdx.x) / a.slices;
   const int tile_end = PAIR ? a.tiles : first + 1;
   const int tile_step = PAIR ? static_cast<int>(gridDim.x) / 2 : 1;
-  const int st_begin = PAIR ? 0 : static_cast<int>(rank) * a.slice_steps;
-  const int st_end = PAIR ? a.steps : min(a.steps, st_begin + a.slice_steps);
+  const int bx_begin = PAIR ? 0 : static_cast<int>(rank) * a.slice_boxes;
+  const int bx_end = PAIR ? a.boxes : min(a.boxes, bx_begin + a.slice_boxes);
   const auto tile_m0 = [&](int t) { return (t / a.tiles_n) * (kOut * CG) + (PAIR ? static_cast<int>(rank) * kOut : 0); };
   const auto tile_n0 = [&](int t) { return (t % a.tiles_n) * a.n; };
 
@@ -466,12 +469,16 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
       bool ok = true;
       for (int t = first; t < tile_end && ok; t += tile_step) {
         const int n0 = tile_n0(t) + (PAIR ? static_cast<int>(rank) * b_rows : 0);
-        for (int st = st_begin; st < st_end; ++st) {
+        for (int bx = bx_begin; bx < bx_end; ++bx) {
           if (!(ok = tc_wait(smem_addr(&b_empty[s]), ph ^ 1u, &s_abort))) break;
           const uint32_t fb = PAIR ? map_to_rank(smem_addr(&b_full[s]), 0) : smem_addr(&b_full[s]);
-          if (leader) mbar_expect_tx(smem_addr(&b_full[s]), b_bytes * CG);
-          const bool second = MODE == kModeBackward && st >= a.steps_w;
-          tma_load<CG>(b_base + s * b_bytes, second ? &a.map_x1 : &a.map_x0, (second ? st - a.steps_w : st) * kBK, n0, fb);
+          if (leader) mbar_expect_tx(smem_addr(&b_full[s]), 2 * b_bytes * CG);
+          const bool second = MODE == kModeBackward && bx >= a.boxes_w;
+          const CUtensorMap* map = second ? &a.map_x1 : &a.map_x0;
+          const int k0 = (second ? bx - a.boxes_w : bx) * kBoxK;
+          const uint32_t dst = b_base + s * 2 * b_bytes;
+          tma_load<CG>(dst, map, k0, n0, fb);
+          tma_load<CG>(dst + b_bytes, map, k0 + kBK, n0, fb);
           ++issued;
           if (++s == b_stages) {
             s = 0;
@@ -489,74 +496,72 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
       bool ok = true;
       for (int t = first; t < tile_end && ok; t += tile_step) {
         const int m0 = tile_m0(t);
-        for (int st = st_begin; st < st_end; st += 2) {
+        for (int bx = bx_begin; bx < bx_end; ++bx) {
           if (!(ok = tc_wait(smem_addr(&c_empty[s]), ph ^ 1u, &s_abort))) break;
           const uint32_t fb = smem_addr(&c_full[s]), dst = c_base + s * kBoxBytes;
           mbar_expect_tx(fb, kBoxBytes);
           if constexpr (MODE == kModeBackward) {
             // 128 weight rows x 128 columns (64 bytes)
-            const bool second = st >= a.steps_w;
-            tma_load<1>(dst, second ? &a.map_w1 : &a.map_w0, m0 / 2, (second ? st - a.steps_w : st) * kBK, fb);
+            const bool second = bx >= a.boxes_w;
+            tma_load<1>(dst, second ? &a.map_w1 : &a.map_w0, m0 / 2, (second ? bx - a.boxes_w : bx) * kBoxK, fb);
           } else if constexpr (MODE == kModeGated) {
             // 16 gate rows, the same 16 up rows, ...: 128 columns (64 bytes) each
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              tma_load<1>(dst + q * 2048u, &a.map_w0, st * (kBK / 2), m0 + 16 * q, fb);
-              tma_load<1>(dst + q * 2048u + 1024u, &a.map_w1, st * (kBK / 2), m0 + 16 * q, fb);
+              tma_load<1>(dst + q * 2048u, &a.map_w0, bx * (kBoxK / 2), m0 + 16 * q, fb);
+              tma_load<1>(dst + q * 2048u + 1024u, &a.map_w1, bx * (kBoxK / 2), m0 + 16 * q, fb);
             }
           } else {
-            tma_load<1>(dst, &a.map_w0, st * (kBK / 2), m0, fb);
+            tma_load<1>(dst, &a.map_w0, bx * (kBoxK / 2), m0, fb);
           }
           ++issued;
-          if (++s == boxes) {
+          if (++s == code_slots) {
             s = 0;
             ph ^= 1u;
           }
         }
       }
-      if (s_abort) let_land(c_full, s, ph, boxes, issued);
+      if (s_abort) let_land(c_full, s, ph, code_slots, issued);
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (leader) {
+    if (leader && elect_one()) {
       const uint32_t idesc = idesc_of(kBM * CG, a.n, MODE == kModeBackward);
-      int bs = 0, as = 0, buf = 0;
+      // K-major A: lines of 128 bytes, 32 bytes a 16-wide MMA; MN-major A: two slabs of 64 outputs,
+      // 8 KiB apart, 16 lines (2 KiB) an MMA
+      const uint64_t a_desc = MODE == kModeBackward ? desc_sw128(a_base, 8192u, 1024u) : desc_sw128(a_base, 16u, 1024u);
+      constexpr uint32_t kAStep = MODE == kModeBackward ? 128u : 2u;
+      const uint64_t b_desc = desc_sw128(b_base, 16u, 1024u);
+      int bs = 0, g = 0, buf = 0;
       uint32_t bph = 0, aph = 0, dph = 3u;  // dph: parity bit per accumulator of the next "empty" wait
       bool ok = true;
       for (int t = first; t < tile_end && ok; t += tile_step) {
-        for (int st = st_begin; st < st_end; ++st) {
-          // a sum starts: the tile's first step, or (backward) the second weight's
-          const bool start = st == st_begin || (MODE == kModeBackward && st == a.steps_w);
+        for (int bx = bx_begin; bx < bx_end; ++bx) {
+          // a sum starts: the tile's first box, or (backward) the second weight's
+          const bool start = bx == bx_begin || (MODE == kModeBackward && bx == a.boxes_w);
           if (start) {
-            if (st != st_begin) {
-              if (elect_one()) tc_commit<CG>(smem_addr(&d_full[buf]));
+            if (bx != bx_begin) {
+              tc_commit<CG>(smem_addr(&d_full[buf]));
               buf ^= 1;
             }
-            if (!(ok = __all_sync(kFull, tc_wait(smem_addr(&d_empty[buf]), (dph >> buf) & 1u, &s_abort)))) break;
+            if (!(ok = tc_wait(smem_addr(&d_empty[buf]), (dph >> buf) & 1u, &s_abort))) break;
             dph ^= 1u << buf;
           }
-          if (!(ok = __all_sync(kFull, tc_wait(smem_addr(&b_full[bs]), bph, &s_abort) && tc_wait(smem_addr(&a_full[as]), aph, &s_abort)))) break;
+          if (!(ok = tc_wait(smem_addr(&b_full[bs]), bph, &s_abort) && tc_wait(smem_addr(&a_full[g]), aph, &s_abort))) break;
           tc_fence_after();
-          const uint32_t at = a_base + as * (kTerms * kABytes);
-          const uint64_t bd = desc_sw128(b_base + bs * b_bytes, 16u, 1024u);
-          if (elect_one()) {
+          const uint64_t ad = a_desc + g * (kStageBytes >> 4), bd = b_desc + bs * (b_bytes >> 3);
+          const uint32_t d = tmem + static_cast<uint32_t>(buf) * 256u;
 #pragma unroll
-            for (int j = 0; j < kBK / 16; ++j) {
+          for (int j = 0; j < kBoxK / 16; ++j) {
+            const uint64_t bj = bd + (j >> 2) * (b_bytes >> 4) + 2u * (j & 3);
 #pragma unroll
-              for (int k = 0; k < kTerms; ++k) {
-                // K-major A: lines of 128 bytes, 32 bytes a 16-wide step; MN-major A: two slabs of
-                // 64 outputs, 8 KiB apart, 16 lines (2 KiB) a step
-                const uint64_t ad = MODE == kModeBackward ? desc_sw128(at + k * kABytes, 8192u, 1024u) + 128u * j
-                                                          : desc_sw128(at + k * kABytes, 16u, 1024u) + 2u * j;
-                tc_mma<CG>(tmem + static_cast<uint32_t>(buf) * 256u, ad, bd + 2u * j, idesc, !(start && j == 0 && k == 0));
-              }
-            }
-            tc_commit<CG>(smem_addr(&a_empty[as]));
-            tc_commit<CG>(smem_addr(&b_empty[bs]));
+            for (int k = 0; k < kTerms; ++k)
+              tc_mma<CG>(d, ad + ((j >> 2) * kTerms + k) * (kABytes >> 4) + kAStep * (j & 3), bj, idesc, !(start && j == 0 && k == 0));
           }
-          __syncwarp();
-          if (++as == a_stages) {
-            as = 0;
+          tc_commit<CG>(smem_addr(&a_empty[g]));
+          tc_commit<CG>(smem_addr(&b_empty[bs]));
+          if (++g == kGroups) {
+            g = 0;
             aph ^= 1u;
           }
           if (++bs == b_stages) {
@@ -565,13 +570,13 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
           }
         }
         if (!ok) break;
-        if (st_begin < st_end) {
-          if (elect_one()) tc_commit<CG>(smem_addr(&d_full[buf]));
+        if (bx_begin < bx_end) {
+          tc_commit<CG>(smem_addr(&d_full[buf]));
           buf ^= 1;
         }
       }
       // every MMA issued has completed before tensor memory and shared memory are released
-      if (elect_one()) tc_commit<CG>(smem_addr(&drain));
+      tc_commit<CG>(smem_addr(&drain));
     }
     __syncwarp();
   } else if (warp >= kDecWarp0 && warp < kEpiWarp0) {
@@ -582,15 +587,15 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
     // the code box has 64-byte lines with a 64-byte swizzle: 16-byte chunk c of line l is at
     // c ^ (l / 2 % 4); a thread's chunks are 2 k and 2 k + 1 of step k (backward: of its slab)
     const int cl = MODE == kModeBackward ? line & 63 : line, cx = (cl >> 1) & 3;
-    const int per_tile = (st_end - st_begin + 1) / 2;  // boxes
-    int t = first, st = st_begin + 2 * group;          // this group's box
-    const int as0 = 2 * group;                         // its two stages
-    const uint32_t full0 = PAIR ? map_to_rank(smem_addr(&a_full[as0]), 0) : smem_addr(&a_full[as0]);
+    const int per_tile = bx_end - bx_begin;
+    int t = first, bx = bx_begin + group;              // this group's box
+    const uint32_t empty = smem_addr(&a_empty[group]);
+    const uint32_t full = PAIR ? map_to_rank(smem_addr(&a_full[group]), 0) : smem_addr(&a_full[group]);
     int cs = group;
     uint32_t aph = 0, cph = 0;
-    const auto settle = [&]() {  // st past the tile's end: the next tiles'
-      while (t < tile_end && st >= st_end) {
-        st -= 2 * per_tile;
+    const auto settle = [&]() {  // a box past the tile's end: the next tiles'
+      while (t < tile_end && bx >= bx_end) {
+        bx -= per_tile;
         t += tile_step;
       }
     };
@@ -599,12 +604,12 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
       int row, col;
       const void* base;
       if constexpr (MODE == kModeBackward) {
-        const bool second = st >= a.steps_w;
-        row = (second ? st - a.steps_w : st) * kBK + 64 * k + (line & 63);
+        const bool second = bx >= a.boxes_w;
+        row = (second ? bx - a.boxes_w : bx) * kBoxK + 64 * k + (line & 63);
         col = m0 + 64 * (line >> 6);
         base = second ? a.scales1 : a.scales0;
       } else {
-        col = st * kBK + 64 * k;
+        col = bx * kBoxK + 64 * k;
         if constexpr (MODE == kModeGated) {
           row = m0 + 16 * (line >> 5) + (line & 15);
           base = (line & 16) ? a.scales1 : a.scales0;
@@ -618,39 +623,34 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
     };
     settle();
     Scales<FMT> next[2] = {scales_of(0), scales_of(1)};
-    bool ok = true;
-    while (t < tile_end && ok) {
+    while (t < tile_end) {
       const Scales<FMT> now[2] = {next[0], next[1]};
-      st += 2 * kGroups;
+      bx += kGroups;
       settle();
       next[0] = scales_of(0);  // of this group's next box, in flight during this one
       next[1] = scales_of(1);
-      if (!__all_sync(kFull, tc_wait(smem_addr(&c_full[cs]), cph, &s_abort))) break;
+      if (!__all_sync(kFull, tc_wait(smem_addr(&c_full[cs]), cph, &s_abort) && tc_wait(empty, aph ^ 1u, &s_abort))) break;
       const uint32_t box = c_base + cs * kBoxBytes;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint32_t from = box + 64u * cl + (MODE == kModeBackward ? 4096u * k : 0u);
         const int c = 2 * (MODE == kModeBackward ? line >> 6 : k);
         const uint4 c0 = lds16(from + static_cast<uint32_t>((c ^ cx) << 4)), c1 = lds16(from + static_cast<uint32_t>(((c + 1) ^ cx) << 4));
-        if (k == 1) {
-          __syncwarp();
-          if (lane == 0) arrive_local(smem_addr(&c_empty[cs]));
-        }
-        if (!(ok = __all_sync(kFull, tc_wait(smem_addr(&a_empty[as0 + k]), aph ^ 1u, &s_abort)))) break;
-        const uint32_t dst = a_base + (as0 + k) * (kTerms * kABytes) + line_addr;
+        const uint32_t dst = a_base + group * kStageBytes + k * (kTerms * kABytes) + line_addr;
         decode32<FMT>(c0, now[k], dst, x, 0);
         decode32<FMT>(c1, now[k], dst, x, 1);
-        fence_proxy_async();  // the stores, before the tensor cores read them
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (PAIR) arrive_remote(full0 + 8u * k);
-          else arrive_local(full0 + 8u * k);
-        }
+      }
+      fence_proxy_async();  // the stores, before the tensor cores read them
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) arrive_remote(full);
+        else arrive_local(full);
+        arrive_local(smem_addr(&c_empty[cs]));
       }
       aph ^= 1u;
       cs += kGroups;
-      if (cs >= boxes) {
-        cs -= boxes;
+      if (cs >= code_slots) {
+        cs -= code_slots;
         cph ^= 1u;
       }
     }
@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
 
   // every MMA has completed (or its wait has given up) before shared and tensor memory go
   __syncthreads();
-  const bool done = __all_sync(kFull, st_begin >= st_end || tc_wait(smem_addr(&drain), 0u, &s_abort)) && !s_abort;
+  const bool done = __all_sync(kFull, bx_begin >= bx_end || tc_wait(smem_addr(&drain), 0u, &s_abort)) && !s_abort;
   tc_fence_after();
   if constexpr (!PAIR) {
     // ---- the slices of the tile: partial sums to the CTA that finishes their columns ----------
@@ -716,8 +716,8 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
     const uint32_t ta = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     constexpr float kUnit = FMT == QZ_NVFP4 ? 256.0f : 1.0f;
     const float f0 = sum_factor<FMT>(a.tscale0) * kUnit, f1 = a.p.n_weights == 2 ? sum_factor<FMT>(a.tscale1) * kUnit : 0.0f;
-    const bool has0 = MODE == kModeBackward ? st_begin < min(st_end, a.steps_w) : st_begin < st_end;
-    const bool has1 = MODE == kModeBackward && max(st_begin, a.steps_w) < st_end;
+    const bool has0 = MODE == kModeBackward ? bx_begin < min(bx_end, a.boxes_w) : bx_begin < bx_end;
+    const bool has1 = MODE == kModeBackward && max(bx_begin, a.boxes_w) < bx_end;
     const int m0 = tile_m0(first), n0 = tile_n0(first);
     // 8 columns of this CTA's own partial sums; the backward pass joins its weights' here
     const auto own = [&](int c, float (&v)[8]) {
@@ -822,39 +822,42 @@ qz_status run_tc(const TcArgs& a, int grid, cudaStream_t s) {
   return launch_status();
 }
 
-// The form and its tiles.  Estimated in SM cycles: a step's MMAs take 2 cycles a token column
-// (128 x n x 64 at 8192 FLOP a cycle; about 2.8 where one CTA loads all the tokens, the
-// shared-memory bandwidth), its decoding about 300; a tile of the second form starts with an empty
+// The form and its tiles.  Estimated in SM cycles: a box's MMAs take 4 cycles a token column
+// (128 x n x 128 at 8192 FLOP a cycle), its hand-over at least 700 cycles; a tile of the second form starts with an empty
 // pipeline and ends with the exchange.
 struct Plan {
   bool pair;
-  int n, tiles_n, tiles, slices, slice_steps, grid;
+  int n, tiles_n, tiles, slices, slice_boxes, grid;
 };
-inline Plan plan_of(int64_t nout, int out_per_cta, int64_t tokens, int steps, int terms) {
+inline void tokens_per_tile(int64_t tokens, int most, int unit, int* n, int64_t* tiles_n) {
+  const int64_t t = (tokens + most - 1) / most;
+  *n = static_cast<int>(((tokens + t - 1) / t + unit - 1) / unit * unit);
+  *tiles_n = (tokens + *n - 1) / *n;
+}
+inline Plan plan_of(int64_t nout, int out_per_cta, int64_t tokens, int boxes, int terms) {
   const int sms = sm_count();
   Plan best{};
   double best_cost = 1e30;
-  const int64_t tn256 = (tokens + 255) / 256;
-  const int n = static_cast<int>(((tokens + tn256 - 1) / tn256 + 31) / 32 * 32);
-  const int64_t tiles_n = (tokens + n - 1) / n;
+  int n;
+  int64_t tiles_n;
   {
+    tokens_per_tile(tokens, 256, 32, &n, &tiles_n);
     const int64_t tiles = (nout + 2 * out_per_cta - 1) / (2 * out_per_cta) * tiles_n;
     const int64_t pairs = std::max(1, sms / 2);
-    const double cost = static_cast<double>((tiles + pairs - 1) / pairs) * steps * std::max(2.0 * n, 300.0) * terms + 6000;
+    const double cost = static_cast<double>((tiles + pairs - 1) / pairs) * boxes * std::max(4.0 * n * terms, 700.0) + 6000;
     if (tiles < (int64_t{1} << 30)) {
-      best = Plan{true, n, static_cast<int>(tiles_n), static_cast<int>(tiles), 1, steps, static_cast<int>(2 * std::min(tiles, pairs))};
+      best = Plan{true, n, static_cast<int>(tiles_n), static_cast<int>(tiles), 1, boxes, static_cast<int>(2 * std::min(tiles, pairs))};
       best_cost = cost;
     }
   }
   for (int s = 1; s <= 8; s *= 2) {
-    const int ns = n % (8 * s) ? (n + 8 * s - 1) / (8 * s) * (8 * s) : n;  // columns divide into eights per slice
+    tokens_per_tile(tokens, 128, std::max(32, 8 * s), &n, &tiles_n);  // the columns divide into eights per slice
     const int64_t tiles = (nout + out_per_cta - 1) / out_per_cta * tiles_n;
-    int per = (steps + s - 1) / s;
-    per += per & 1;  // whole boxes
+    const int per = (boxes + s - 1) / s;
     const int64_t clusters = std::max(1, s == 1 ? sms : (s == 2 ? sms * 9 / 10 : sms * 5 / 6) / s);
-    const double cost = static_cast<double>((tiles + clusters - 1) / clusters) * (per * std::max(2.8 * ns, 300.0) * terms + 5000 + (s > 1 ? 2000 + 16.0 * ns : 0));
-    if (ns <= 256 && tiles * s < (int64_t{1} << 30) && cost < best_cost) {
-      best = Plan{false, ns, static_cast<int>(tiles_n), static_cast<int>(tiles), s, per, static_cast<int>(tiles * s)};
+    const double cost = static_cast<double>((tiles + clusters - 1) / clusters) * (per * std::max(4.0 * n * terms, 700.0) + 5000 + (s > 1 ? 2000 + 16.0 * n : 0));
+    if (tiles * s < (int64_t{1} << 30) && cost < best_cost) {
+      best = Plan{false, n, static_cast<int>(tiles_n), static_cast<int>(tiles), s, per, static_cast<int>(tiles * s)};
       best_cost = cost;
     }
   }
@@ -873,21 +876,21 @@ qz_status launch_tc(const ProductArgs& p, cudaStream_t s) {
   a.nout = static_cast<int>(back ? p.cols : p.rows);
   a.nsum = static_cast<int>(back ? p.rows : p.cols);
   a.blocks_row = static_cast<int>(p.cols >> p.log2_block);
-  a.steps_w = (a.nsum + 2 * kBK - 1) / (2 * kBK) * 2;
-  a.steps = back ? a.steps_w * p.n_weights : a.steps_w;
-  const Plan plan = plan_of(a.nout, p.mode == kModeGated ? kBM / 2 : kBM, p.tokens, a.steps, TcFormat<FMT>::kTerms);
+  a.boxes_w = (a.nsum + kBoxK - 1) / kBoxK;
+  a.boxes = back ? a.boxes_w * p.n_weights : a.boxes_w;
+  const Plan plan = plan_of(a.nout, p.mode == kModeGated ? kBM / 2 : kBM, p.tokens, a.boxes, TcFormat<FMT>::kTerms);
   if (plan.grid == 0) return QZ_ERR_UNSUPPORTED;
   a.n = plan.n;
   a.tiles_n = plan.tiles_n;
   a.tiles = plan.tiles;
   a.slices = plan.slices;
-  a.slice_steps = plan.slice_steps;
+  a.slice_boxes = plan.slice_boxes;
   const int b_rows = plan.pair ? plan.n / 2 : plan.n;
-  // two rounds of code boxes, or one where the tokens' steps are too large to leave them three
-  const uint32_t stage_b = static_cast<uint32_t>(b_rows) * kBK * 2;
+  // two rounds of code boxes, or one where that leaves the tokens fewer than three stages
+  const uint32_t stage_b = static_cast<uint32_t>(b_rows) * kBoxK * 2;
   constexpr int kGroups = TcFormat<FMT>::kGroups;
-  a.boxes = kRingRoom<FMT> < 2 * kGroups * kBoxBytes + 3 * stage_b ? kGroups : 2 * kGroups;
-  a.b_stages = static_cast<int>(std::min<uint32_t>(kMaxBStages, (kRingRoom<FMT> - a.boxes * kBoxBytes) / stage_b));
+  a.code_slots = kRingRoom<FMT> < 2 * kGroups * kBoxBytes + 3 * stage_b ? kGroups : 2 * kGroups;
+  a.b_stages = static_cast<int>(std::min<uint32_t>(kMaxBStages, (kRingRoom<FMT> - a.code_slots * kBoxBytes) / stage_b));
   const int align = p.format == QZ_MXFP4 ? 2 : 4;
   a.scales_vec = p.cols % 64 == 0 && reinterpret_cast<uintptr_t>(a.scales0) % align == 0 && reinterpret_cast<uintptr_t>(a.scales1) % align == 0;
   const int code_rows = p.mode == kModeGated ? 16 : 128;
