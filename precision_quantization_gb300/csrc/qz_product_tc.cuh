@@ -10,10 +10,10 @@
 // with fp32 accumulation gives the sums of include/qz.h without a rounding of the weights.
 //
 // Roles of a CTA's warps (every wait is bounded):
-//   warp 0       streams the tokens' 128-wide boxes (two 64-wide steps) into a ring by TMA
+//   warp 0       streams the tokens' boxes (128 summands, INT4 64) into a ring by TMA
 //   warp 2       streams the 4-bit codes' boxes into a ring of their own by TMA
-//   decoders     two or three groups of four warps that take the boxes in turn: a thread turns a
-//                line's codes into bf16 and stores them in the layout the MMA reads
+//   decoders     three groups of four warps that take the boxes in turn: a thread turns a line's
+//                codes into bf16 and stores them in the layout the MMA reads
 //   warp 1       issues the MMAs, eight 16-wide ones a box (one thread)
 //   last four    read finished accumulators from tensor memory, apply the activation and store
 // A box is the unit of every hand-over: a wait or a commit of the issuing thread takes some 60 to
@@ -45,8 +45,6 @@ constexpr int kBM = 128;            // outputs per CTA (MMA rows, tensor-memory 
 constexpr int kBK = 64;             // summands per step: 128 bytes of bf16, one swizzle row
 constexpr int kDecWarp0 = 4, kEpiWarps = 4;
 constexpr uint32_t kABytes = kBM * kBK * 2;        // 16 KiB of decoded weights
-constexpr uint32_t kBoxBytes = kBM * kBK;          // 8 KiB of codes: a box of two steps
-constexpr int kBoxK = 2 * kBK;
 constexpr uint32_t kTmemCols = 512;                // two accumulators of 256 columns
 constexpr uint64_t kTcWaitNs = 1000000000ull;      // 1 s: far beyond any step's latency
 constexpr int kMaxBStages = 8, kMaxGroups = 3, kMaxBoxes = 6;
@@ -54,11 +52,14 @@ constexpr int kMaxBStages = 8, kMaxGroups = 3, kMaxBoxes = 6;
 template <int FMT>
 struct TcFormat {
   static constexpr int kTerms = FMT == QZ_INT4 ? 2 : 1;      // bf16 terms per weight
-  static constexpr int kGroups = FMT == QZ_INT4 ? 2 : 3;     // decoder groups of four warps
+  static constexpr int kSteps = FMT == QZ_INT4 ? 1 : 2;      // 64-wide steps of a box: eight MMAs
+  static constexpr int kBoxK = kSteps * kBK;
+  static constexpr uint32_t kBoxBytes = kBM * kBoxK / 2;     // of codes
+  static constexpr int kGroups = 3;                          // decoder groups of four warps
   // Stages of decoded weights: one box per group.  Both this ring and the code ring hold a whole
   // number of rounds of the groups, so a slot belongs to one group, which is never a lap ahead of
   // another on it (a parity wait could not tell the laps apart).
-  static constexpr uint32_t kStageBytes = 2 * kTerms * kABytes;
+  static constexpr uint32_t kStageBytes = kSteps * kTerms * kABytes;  // 32 KiB
   static constexpr int kEpiWarp0 = kDecWarp0 + 4 * kGroups;
   static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 };
@@ -74,11 +75,11 @@ struct TcArgs {
   ProductArgs p;
   int nout, nsum;         // outputs and summands (per weight)
   int blocks_row;         // scales per weight row
-  int boxes_w, boxes;     // 128-wide boxes per weight (past the sum's end copies give zeros), in all
+  int boxes_w, boxes;     // boxes per weight (past the sum's end copies give zeros), in all
                           // (backward: both weights' one after the other)
   int n;                  // tokens per tile (a multiple of 32)
   int code_slots, b_stages;  // slots of the code ring (a multiple of the groups), of the tokens' ring
-  bool scales_vec;        // the scales of 64 columns are one aligned load
+  int scales_vec;         // 1: the scales of 64 columns are one aligned load; 2: those of 128 are
   int tiles_n, tiles;
   int slices, slice_boxes;  // Alone: slices of the sum (the cluster), boxes per slice
 };
@@ -232,25 +233,26 @@ __device__ __forceinline__ uint32_t nibble_pair(uint32_t t0, uint32_t t1) {
 // bits 6-8, and bf16's own exponent (biased 127 against 1) and subnormals do the rest.
 __device__ __forceinline__ uint32_t e2m1_pair(uint32_t d) { return (d * 0x1040u) & 0x81C081C0u; }
 
-// The scales of 64 columns of a weight row: two E8M0 bytes, four E4M3 bytes, or fp32.
+// The scales of one 64-wide step of a line: two E8M0 bytes, four E4M3 bytes, or fp32 (of each 16
+// columns).
 template <int FMT>
 struct Scales {
-  uint32_t v[FMT == QZ_INT4 ? 4 : 1];  // INT4: of each 16 columns
+  uint32_t v[FMT == QZ_INT4 ? 4 : 1];
 };
+// Those of 64 columns from `col` on; p: the scales of the row.  Outside the weight they are 0 (finite; the
+// codes there are 0).
 template <int FMT>
-__device__ __forceinline__ Scales<FMT> load_scales(const void* base, int64_t row_first, int col, int cols, bool row_in, int log2_block, bool vec) {
-  Scales<FMT> s{};  // outside the weight: finite (its codes are 0)
-  if (!row_in || col >= cols) return s;
-  const int64_t i = row_first + (col >> log2_block);
+__device__ __forceinline__ Scales<FMT> load_scales(const uint8_t* p, int col, int cols, int log2_block, bool vec) {
+  Scales<FMT> s{};
+  if (p == nullptr || col >= cols) return s;
   if constexpr (FMT == QZ_INT4) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p) + (col >> log2_block);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (col + 16 * q >= cols) break;
-      s.v[q] = __ldg(static_cast<const uint32_t*>(base) + i + ((16 * q) >> log2_block));
-    }
+    for (int i = 0; i < 4; ++i)
+      if (col + 16 * i < cols) s.v[i] = __ldg(q + ((16 * i) >> log2_block));
   } else {
     constexpr int kN = FMT == QZ_MXFP4 ? 2 : 4;  // bytes
-    const uint8_t* p = static_cast<const uint8_t*>(base) + i;
+    p += static_cast<uint32_t>(col) / (64 / kN);
     if (vec) {
       if constexpr (FMT == QZ_MXFP4) s.v[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
       else s.v[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
@@ -261,6 +263,22 @@ __device__ __forceinline__ Scales<FMT> load_scales(const void* base, int64_t row
     }
   }
   return s;
+}
+// Those of a box's two steps, 128 columns, as one aligned load (cols % 128 == 0).
+template <int FMT>
+__device__ __forceinline__ void load_scales_box(const uint8_t* p, int col, Scales<FMT> (&s)[2]) {
+  static_assert(FMT != QZ_INT4, "two-step boxes");
+  if (p == nullptr) {
+    s[0] = s[1] = Scales<FMT>{};
+  } else if constexpr (FMT == QZ_MXFP4) {
+    const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(p + static_cast<uint32_t>(col) / 32u));
+    s[0].v[0] = v;  // the second step's bytes lie above the first's
+    s[1].v[0] = v >> 16;
+  } else {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + static_cast<uint32_t>(col) / 16u));
+    s[0].v[0] = v.x;
+    s[1].v[0] = v.y;
+  }
 }
 
 // 32 weights (16 bytes of codes; half h of a line's 64) to bf16, stored as chunks 4 h .. 4 h + 3
@@ -399,6 +417,8 @@ __device__ __forceinline__ void store8(const TcArgs& a, StoreFlags f, const floa
 template <int FMT, int MODE, bool PAIR>
 __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(const __grid_constant__ TcArgs a) {
   constexpr int CG = PAIR ? 2 : 1;
+  constexpr int kSteps = TcFormat<FMT>::kSteps, kBoxK = TcFormat<FMT>::kBoxK;
+  constexpr uint32_t kBoxBytes = TcFormat<FMT>::kBoxBytes;
   constexpr int kTerms = TcFormat<FMT>::kTerms, kGroups = TcFormat<FMT>::kGroups, kEpiWarp0 = TcFormat<FMT>::kEpiWarp0;
   constexpr int kOut = MODE == kModeGated ? kBM / 2 : kBM;          // outputs per CTA
   extern __shared__ uint8_t tc_raw[];
@@ -415,7 +435,7 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
   const int code_slots = a.code_slots, b_stages = a.b_stages;
   const uint32_t a_base = base, c_base = base + kGroups * kStageBytes, b_base = c_base + code_slots * kBoxBytes;
   const int b_rows = a.n / CG;                       // tokens that this CTA loads
-  const uint32_t b_bytes = static_cast<uint32_t>(b_rows) * kBK * 2;  // of a step; a box is two
+  const uint32_t b_bytes = static_cast<uint32_t>(b_rows) * kBK * 2;  // of a step
 
   if (tid == 0) {
     for (int s = 0; s < kMaxBStages; ++s) {
@@ -472,13 +492,12 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
         for (int bx = bx_begin; bx < bx_end; ++bx) {
           if (!(ok = tc_wait(smem_addr(&b_empty[s]), ph ^ 1u, &s_abort))) break;
           const uint32_t fb = PAIR ? map_to_rank(smem_addr(&b_full[s]), 0) : smem_addr(&b_full[s]);
-          if (leader) mbar_expect_tx(smem_addr(&b_full[s]), 2 * b_bytes * CG);
+          if (leader) mbar_expect_tx(smem_addr(&b_full[s]), kSteps * b_bytes * CG);
           const bool second = MODE == kModeBackward && bx >= a.boxes_w;
           const CUtensorMap* map = second ? &a.map_x1 : &a.map_x0;
           const int k0 = (second ? bx - a.boxes_w : bx) * kBoxK;
-          const uint32_t dst = b_base + s * 2 * b_bytes;
-          tma_load<CG>(dst, map, k0, n0, fb);
-          tma_load<CG>(dst + b_bytes, map, k0 + kBK, n0, fb);
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k) tma_load<CG>(b_base + (s * kSteps + k) * b_bytes, map, k0 + k * kBK, n0, fb);
           ++issued;
           if (++s == b_stages) {
             s = 0;
@@ -501,15 +520,15 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
           const uint32_t fb = smem_addr(&c_full[s]), dst = c_base + s * kBoxBytes;
           mbar_expect_tx(fb, kBoxBytes);
           if constexpr (MODE == kModeBackward) {
-            // 128 weight rows x 128 columns (64 bytes)
+            // kBoxK weight rows x 128 columns (64 bytes)
             const bool second = bx >= a.boxes_w;
             tma_load<1>(dst, second ? &a.map_w1 : &a.map_w0, m0 / 2, (second ? bx - a.boxes_w : bx) * kBoxK, fb);
           } else if constexpr (MODE == kModeGated) {
-            // 16 gate rows, the same 16 up rows, ...: 128 columns (64 bytes) each
+            // 16 gate rows, the same 16 up rows, ...: kBoxK columns each
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              tma_load<1>(dst + q * 2048u, &a.map_w0, bx * (kBoxK / 2), m0 + 16 * q, fb);
-              tma_load<1>(dst + q * 2048u + 1024u, &a.map_w1, bx * (kBoxK / 2), m0 + 16 * q, fb);
+              tma_load<1>(dst + q * (kBoxBytes / 4), &a.map_w0, bx * (kBoxK / 2), m0 + 16 * q, fb);
+              tma_load<1>(dst + q * (kBoxBytes / 4) + kBoxBytes / 8, &a.map_w1, bx * (kBoxK / 2), m0 + 16 * q, fb);
             }
           } else {
             tma_load<1>(dst, &a.map_w0, bx * (kBoxK / 2), m0, fb);
@@ -549,14 +568,13 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
           }
           if (!(ok = tc_wait(smem_addr(&b_full[bs]), bph, &s_abort) && tc_wait(smem_addr(&a_full[g]), aph, &s_abort))) break;
           tc_fence_after();
-          const uint64_t ad = a_desc + g * (kStageBytes >> 4), bd = b_desc + bs * (b_bytes >> 3);
+          const uint64_t ad = a_desc + g * (kStageBytes >> 4), bd = b_desc + bs * (kSteps * b_bytes >> 4);
           const uint32_t d = tmem + static_cast<uint32_t>(buf) * 256u;
 #pragma unroll
-          for (int j = 0; j < kBoxK / 16; ++j) {
-            const uint64_t bj = bd + (j >> 2) * (b_bytes >> 4) + 2u * (j & 3);
-#pragma unroll
-            for (int k = 0; k < kTerms; ++k)
-              tc_mma<CG>(d, ad + ((j >> 2) * kTerms + k) * (kABytes >> 4) + kAStep * (j & 3), bj, idesc, !(start && j == 0 && k == 0));
+          for (int i = 0; i < 8; ++i) {  // kBoxK / 16 steps of kTerms MMAs
+            const int j = i / kTerms, k = i % kTerms;
+            tc_mma<CG>(d, ad + ((j >> 2) * kTerms + k) * (kABytes >> 4) + kAStep * (j & 3),
+                       bd + (j >> 2) * (b_bytes >> 4) + 2u * (j & 3), idesc, !(start && i == 0));
           }
           tc_commit<CG>(smem_addr(&a_empty[g]));
           tc_commit<CG>(smem_addr(&b_empty[bs]));
@@ -580,13 +598,15 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
     }
     __syncwarp();
   } else if (warp >= kDecWarp0 && warp < kEpiWarp0) {
-    // Group g of four warps takes every kGroups-th box (two steps); thread i of it line i of each:
+    // Group g of four warps takes every kGroups-th box; thread i of it line i of each:
     // an output (backward: weight row i % 64 of the step, outputs 64 (i / 64) .. + 63).
     const int group = (warp - kDecWarp0) >> 2, line = (tid - kDecWarp0 * 32) & 127, x = line & 7;
     const uint32_t line_addr = 128u * line;
-    // the code box has 64-byte lines with a 64-byte swizzle: 16-byte chunk c of line l is at
-    // c ^ (l / 2 % 4); a thread's chunks are 2 k and 2 k + 1 of step k (backward: of its slab)
-    const int cl = MODE == kModeBackward ? line & 63 : line, cx = (cl >> 1) & 3;
+    // the code box has 64-byte lines with a 64-byte swizzle, 16-byte chunk c of line l at
+    // c ^ (l / 2 % 4), or 32-byte ones (c ^ (l / 4 % 2)); a thread's chunks are 2 k and 2 k + 1 of
+    // step k (backward: of its slab), so eight lanes' 16-byte loads take different banks
+    constexpr uint32_t kLine = MODE == kModeBackward ? 64u : kBoxK / 2;
+    const int cl = MODE == kModeBackward ? line & 63 : line, cx = kLine == 64 ? (cl >> 1) & 3 : (cl >> 2) & 1;
     const int per_tile = bx_end - bx_begin;
     int t = first, bx = bx_begin + group;              // this group's box
     const uint32_t empty = smem_addr(&a_empty[group]);
@@ -599,44 +619,61 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
         t += tile_step;
       }
     };
-    const auto scales_of = [&](int k) {
-      const int m0 = tile_m0(t);
-      int row, col;
-      const void* base;
+    constexpr int kScaleBytes = FMT == QZ_INT4 ? 4 : 1;
+    const int64_t pitch = static_cast<int64_t>(a.blocks_row) * kScaleBytes;
+    const uint8_t* row_scales = nullptr;  // forward: of this thread's line in tile `row_tile` (null: outside)
+    int row_tile = -1;
+    const auto load_next = [&](Scales<FMT> (&s)[kSteps]) {  // of box bx in tile t
+      const int cols = static_cast<int>(a.p.cols);
+      if (t >= tile_end) return;
       if constexpr (MODE == kModeBackward) {
         const bool second = bx >= a.boxes_w;
-        row = (second ? bx - a.boxes_w : bx) * kBoxK + 64 * k + (line & 63);
-        col = m0 + 64 * (line >> 6);
-        base = second ? a.scales1 : a.scales0;
+        const int row = (second ? bx - a.boxes_w : bx) * kBoxK + (line & 63), col = tile_m0(t) + 64 * (line >> 6);
+        const uint8_t* base = static_cast<const uint8_t*>(second ? a.scales1 : a.scales0) + row * pitch;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+          s[k] = load_scales<FMT>(row + 64 * k < a.nsum ? base + 64 * k * pitch : nullptr, col, cols, a.p.log2_block, a.scales_vec >= 1);
       } else {
-        col = bx * kBoxK + 64 * k;
-        if constexpr (MODE == kModeGated) {
-          row = m0 + 16 * (line >> 5) + (line & 15);
-          base = (line & 16) ? a.scales1 : a.scales0;
-        } else {
-          row = m0 + line;
-          base = a.scales0;
+        if (row_tile != t) {
+          row_tile = t;
+          const int m0 = tile_m0(t);
+          const int row = MODE == kModeGated ? m0 + 16 * (line >> 5) + (line & 15) : m0 + line;
+          const void* base = MODE == kModeGated && (line & 16) ? a.scales1 : a.scales0;
+          row_scales = row < a.nout ? static_cast<const uint8_t*>(base) + row * pitch : nullptr;
         }
+        const int col = bx * kBoxK;
+        if constexpr (kSteps == 2) {
+          if (a.scales_vec == 2) {
+            load_scales_box<FMT>(row_scales, col, s);
+            return;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) s[k] = load_scales<FMT>(row_scales, col + 64 * k, cols, a.p.log2_block, a.scales_vec >= 1);
       }
-      return load_scales<FMT>(base, static_cast<int64_t>(row) * a.blocks_row, col, static_cast<int>(a.p.cols),
-                              t < tile_end && row < (MODE == kModeBackward ? a.nsum : a.nout), a.p.log2_block, a.scales_vec);
     };
     settle();
-    Scales<FMT> next[2] = {scales_of(0), scales_of(1)};
+    Scales<FMT> next[kSteps] = {};
+    load_next(next);
     while (t < tile_end) {
-      const Scales<FMT> now[2] = {next[0], next[1]};
+      Scales<FMT> now[kSteps];
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) now[k] = next[k];
       bx += kGroups;
       settle();
-      next[0] = scales_of(0);  // of this group's next box, in flight during this one
-      next[1] = scales_of(1);
+      load_next(next);  // of this group's next box, in flight during this one
       if (!__all_sync(kFull, tc_wait(smem_addr(&c_full[cs]), cph, &s_abort) && tc_wait(empty, aph ^ 1u, &s_abort))) break;
       const uint32_t box = c_base + cs * kBoxBytes;
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t from = box + 64u * cl + (MODE == kModeBackward ? 4096u * k : 0u);
+      for (int k = 0; k < kSteps; ++k) {
+        const uint32_t from = box + kLine * cl + (MODE == kModeBackward ? 4096u * k : 0u);
         const int c = 2 * (MODE == kModeBackward ? line >> 6 : k);
         const uint4 c0 = lds16(from + static_cast<uint32_t>((c ^ cx) << 4)), c1 = lds16(from + static_cast<uint32_t>(((c + 1) ^ cx) << 4));
         const uint32_t dst = a_base + group * kStageBytes + k * (kTerms * kABytes) + line_addr;
+        if (kSteps == 1) {  // the codes are in registers
+          __syncwarp();
+          if (lane == 0) arrive_local(smem_addr(&c_empty[cs]));
+        }
         decode32<FMT>(c0, now[k], dst, x, 0);
         decode32<FMT>(c1, now[k], dst, x, 1);
       }
@@ -645,7 +682,7 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
       if (lane == 0) {
         if constexpr (PAIR) arrive_remote(full);
         else arrive_local(full);
-        arrive_local(smem_addr(&c_empty[cs]));
+        if (kSteps == 2) arrive_local(smem_addr(&c_empty[cs]));
       }
       aph ^= 1u;
       cs += kGroups;
@@ -788,14 +825,14 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
 }
 
 // ---- host side ----------------------------------------------------------------------------------
-inline bool encode(CUtensorMap* m, bool codes, const void* base, int64_t inner, int64_t outer, int64_t pitch, int box_in, int box_out) {
+inline bool encode(CUtensorMap* m, int swizzle, const void* base, int64_t inner, int64_t outer, int64_t pitch, int box_in, int box_out) {
   const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
   if (!enc) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
   const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_in), static_cast<cuuint32_t>(box_out)}, es[2] = {1, 1};
-  return enc(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
-             box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, codes ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+  return enc(m, swizzle < 128 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
+             box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -822,9 +859,9 @@ qz_status run_tc(const TcArgs& a, int grid, cudaStream_t s) {
   return launch_status();
 }
 
-// The form and its tiles.  Estimated in SM cycles: a box's MMAs take 4 cycles a token column
-// (128 x n x 128 at 8192 FLOP a cycle), its hand-over at least 700 cycles; a tile of the second form starts with an empty
-// pipeline and ends with the exchange.
+// The form and its tiles.  Estimated in SM cycles: a box's eight MMAs take 4 cycles a token column
+// (128 x n x 16 each at 8192 FLOP a cycle), its hand-over at least 700 cycles; a tile of the second
+// form starts with an empty pipeline and ends with the exchange.
 struct Plan {
   bool pair;
   int n, tiles_n, tiles, slices, slice_boxes, grid;
@@ -834,7 +871,7 @@ inline void tokens_per_tile(int64_t tokens, int most, int unit, int* n, int64_t*
   *n = static_cast<int>(((tokens + t - 1) / t + unit - 1) / unit * unit);
   *tiles_n = (tokens + *n - 1) / *n;
 }
-inline Plan plan_of(int64_t nout, int out_per_cta, int64_t tokens, int boxes, int terms) {
+inline Plan plan_of(int64_t nout, int out_per_cta, int64_t tokens, int boxes) {
   const int sms = sm_count();
   Plan best{};
   double best_cost = 1e30;
@@ -844,7 +881,7 @@ inline Plan plan_of(int64_t nout, int out_per_cta, int64_t tokens, int boxes, in
     tokens_per_tile(tokens, 256, 32, &n, &tiles_n);
     const int64_t tiles = (nout + 2 * out_per_cta - 1) / (2 * out_per_cta) * tiles_n;
     const int64_t pairs = std::max(1, sms / 2);
-    const double cost = static_cast<double>((tiles + pairs - 1) / pairs) * boxes * std::max(4.0 * n * terms, 700.0) + 6000;
+    const double cost = static_cast<double>((tiles + pairs - 1) / pairs) * boxes * std::max(4.0 * n, 700.0) + 6000;
     if (tiles < (int64_t{1} << 30)) {
       best = Plan{true, n, static_cast<int>(tiles_n), static_cast<int>(tiles), 1, boxes, static_cast<int>(2 * std::min(tiles, pairs))};
       best_cost = cost;
@@ -855,7 +892,7 @@ inline Plan plan_of(int64_t nout, int out_per_cta, int64_t tokens, int boxes, in
     const int64_t tiles = (nout + out_per_cta - 1) / out_per_cta * tiles_n;
     const int per = (boxes + s - 1) / s;
     const int64_t clusters = std::max(1, s == 1 ? sms : (s == 2 ? sms * 9 / 10 : sms * 5 / 6) / s);
-    const double cost = static_cast<double>((tiles + clusters - 1) / clusters) * (per * std::max(4.0 * n * terms, 700.0) + 5000 + (s > 1 ? 2000 + 16.0 * n : 0));
+    const double cost = static_cast<double>((tiles + clusters - 1) / clusters) * (per * std::max(4.0 * n, 700.0) + 5000 + (s > 1 ? 2000 + 16.0 * n : 0));
     if (tiles * s < (int64_t{1} << 30) && cost < best_cost) {
       best = Plan{false, n, static_cast<int>(tiles_n), static_cast<int>(tiles), s, per, static_cast<int>(tiles * s)};
       best_cost = cost;
@@ -876,9 +913,10 @@ qz_status launch_tc(const ProductArgs& p, cudaStream_t s) {
   a.nout = static_cast<int>(back ? p.cols : p.rows);
   a.nsum = static_cast<int>(back ? p.rows : p.cols);
   a.blocks_row = static_cast<int>(p.cols >> p.log2_block);
+  constexpr int kBoxK = TcFormat<FMT>::kBoxK;
   a.boxes_w = (a.nsum + kBoxK - 1) / kBoxK;
   a.boxes = back ? a.boxes_w * p.n_weights : a.boxes_w;
-  const Plan plan = plan_of(a.nout, p.mode == kModeGated ? kBM / 2 : kBM, p.tokens, a.boxes, TcFormat<FMT>::kTerms);
+  const Plan plan = plan_of(a.nout, p.mode == kModeGated ? kBM / 2 : kBM, p.tokens, a.boxes);
   if (plan.grid == 0) return QZ_ERR_UNSUPPORTED;
   a.n = plan.n;
   a.tiles_n = plan.tiles_n;
@@ -889,15 +927,18 @@ qz_status launch_tc(const ProductArgs& p, cudaStream_t s) {
   // two rounds of code boxes, or one where that leaves the tokens fewer than three stages
   const uint32_t stage_b = static_cast<uint32_t>(b_rows) * kBoxK * 2;
   constexpr int kGroups = TcFormat<FMT>::kGroups;
+  constexpr uint32_t kBoxBytes = TcFormat<FMT>::kBoxBytes;
   a.code_slots = kRingRoom<FMT> < 2 * kGroups * kBoxBytes + 3 * stage_b ? kGroups : 2 * kGroups;
   a.b_stages = static_cast<int>(std::min<uint32_t>(kMaxBStages, (kRingRoom<FMT> - a.code_slots * kBoxBytes) / stage_b));
-  const int align = p.format == QZ_MXFP4 ? 2 : 4;
-  a.scales_vec = p.cols % 64 == 0 && reinterpret_cast<uintptr_t>(a.scales0) % align == 0 && reinterpret_cast<uintptr_t>(a.scales1) % align == 0;
-  const int code_rows = p.mode == kModeGated ? 16 : 128;
-  bool ok = encode(&a.map_x0, false, p.x0, a.nsum, p.tokens, p.ld_x * 2, kBK, b_rows) &&
-            encode(&a.map_w0, true, p.w0.codes, p.cols / 2, p.rows, p.cols / 2, 64, code_rows);
-  if (p.n_weights == 2) ok = ok && encode(&a.map_w1, true, p.w1.codes, p.cols / 2, p.rows, p.cols / 2, 64, code_rows);
-  if (p.n_weights == 2 && back) ok = ok && encode(&a.map_x1, false, p.x1, a.nsum, p.tokens, p.ld_x * 2, kBK, b_rows);
+  const auto aligned_scales = [&](uintptr_t n) { return reinterpret_cast<uintptr_t>(a.scales0) % n == 0 && reinterpret_cast<uintptr_t>(a.scales1) % n == 0; };
+  const int unit = p.format == QZ_MXFP4 ? 2 : 4;  // bytes of scales per 64 columns
+  a.scales_vec = p.cols % 128 == 0 && aligned_scales(2 * unit) ? 2 : p.cols % 64 == 0 && aligned_scales(unit) ? 1 : 0;
+  const int code_line = back ? 64 : kBoxK / 2;  // bytes, and the swizzle
+  const int code_rows = back ? kBoxK : p.mode == kModeGated ? 16 : 128;
+  bool ok = encode(&a.map_x0, 128, p.x0, a.nsum, p.tokens, p.ld_x * 2, kBK, b_rows) &&
+            encode(&a.map_w0, code_line, p.w0.codes, p.cols / 2, p.rows, p.cols / 2, code_line, code_rows);
+  if (p.n_weights == 2) ok = ok && encode(&a.map_w1, code_line, p.w1.codes, p.cols / 2, p.rows, p.cols / 2, code_line, code_rows);
+  if (p.n_weights == 2 && back) ok = ok && encode(&a.map_x1, 128, p.x1, a.nsum, p.tokens, p.ld_x * 2, kBK, b_rows);
   if (!ok) return QZ_ERR_CUDA;
   if (plan.pair) {
     if (p.mode == kModeLinear) return run_tc<FMT, kModeLinear, true>(a, plan.grid, s);
