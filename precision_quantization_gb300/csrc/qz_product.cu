@@ -119,6 +119,7 @@ qz_status run_tile(const ProductArgs& p, cudaStream_t s) {
 }
 
 qz_status launch_product(const ProductArgs& p, cudaStream_t s) {
+  if (product_few_applicable(p)) return launch_product_few(p, s);
   if (product_tc_applicable(p)) {
     if (p.format == QZ_MXFP4) return launch_product_tc_mxfp4(p, s);
     if (p.format == QZ_NVFP4) return launch_product_tc_nvfp4(p, s);

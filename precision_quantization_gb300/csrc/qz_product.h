@@ -26,6 +26,11 @@ struct ProductArgs {
   int64_t ld_gu;
 };
 
+// The streaming kernels for up to kFewTokens tokens (qz_product_few.cu).
+constexpr int kFewTokens = 32;
+bool product_few_applicable(const ProductArgs& p);
+qz_status launch_product_few(const ProductArgs& p, cudaStream_t s);
+
 // The tcgen05 kernels (qz_product_tc.cuh): applicable when cols % 32 == 0 and codes, activations
 // and their rows are 16-byte aligned.
 bool product_tc_applicable(const ProductArgs& p);
