@@ -2,16 +2,25 @@
 //   y[t][r] = sum_c W[r][c] x[t][c]        (one weight, or gate and up with the activation)
 //
 // Every weight is used once per token, so the weights' 4 bits (and scales) are the traffic and HBM
-// the bound; the work to hide is the decoding, 8 weights per lane and mma.sync m16n8k16 (weights
-// 16 rows, tokens the 8 columns: 32 tokens share one decoding in four of them).  The weights
-// are exact in bf16 times their block scale (E2M1) or as integers (INT4, whose group scale takes
-// the fp32 sum of its group), so the sums are those of include/qz.h.
+// the bound; what has to fit beside the traffic is the decoding: at HBM speed an SM has about 22
+// issue slots for 8 weights a lane, one mma.sync m16n8k16 (16 weight rows, 8 tokens).
+//   - E2M1 pairs become f16 by one conversion each, INT4 nibbles by the bits of f16 1024 + n.
+//   - f16 holds E2M1 times an E4M3 block scale exactly (6 significant bits, 2^-10 .. 2688), so
+//     NVFP4 weights are scaled before the product; E8M0 and fp32 scales take the fp32 sum of their
+//     block or group (one FMA per output).
+//   - The activations are f16 too: token t's values times a power of two 2^p that brings its
+//     largest finite magnitude into [2^14, 2^15).  bf16's 8 bits fit f16's 11 as long as a value is
+//     at least 2^-28 of that magnitude; below it keeps an absolute error of 2^-39 of it, against
+//     the 2^-24 of the largest product that an fp32 sum rounds to.  The sum is multiplied by 2^-p.
 //
-// A tile is 16 outputs (gated: 16 of gate and of up).  KS of a CTA's eight warps share a tile, each
-// with a contiguous part of the sum, and join their partial sums in shared memory in warp order;
-// CTAs are persistent over the tiles.  A warp streams 128 columns of its 16 rows a step (64 bytes
-// a row) through a ring of kDepth steps by cp.async, running on into the next tile, so the copies
-// never pause; the activations come through L1, which they alone use.
+// A tile is 16 outputs (gated: 16 of gate and of up).  ks of a CTA's warps share a tile, each with a
+// contiguous part of the sum, and join their partial sums in shared memory in warp order; CTAs
+// (one per SM) are persistent over the tiles.  A warp streams 256 columns of its 16 rows a step
+// (whole 128-byte lines) through a ring of its own by TMA and runs on into the next tile, so the
+// copies never pause; a step's scales are loaded into registers one step ahead.
+#include <cuda.h>  // CUtensorMap and its enumerators (types only; the encoder is looked up)
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <cstdint>
 
@@ -24,25 +33,42 @@
 namespace qz {
 namespace {
 
-constexpr int kFewWarps = 8;
-constexpr int kTokenStride = 20;  // floats of a token's 16 sums in the join (banks 8 t + g)
+constexpr int kFewWarps = 16;
+constexpr int kTokenStride = 20;        // floats of a token's 16 sums in the join (banks 8 t + g)
+constexpr uint32_t kFewSmem = 227 * 1024;
+constexpr float kShift = 0x1p-64f;      // the sums' unit once a scale above 2^73 has been met
 
 struct FewArgs {
+  CUtensorMap map_w0, map_w1;  // codes [rows][cols / 2] bytes, box 128 x 16
   ProductArgs p;
-  int tiles, ks, steps, scale_bytes;  // warps per tile, 128-wide steps of a row, bytes of scales a step
-  int64_t code_pitch, scale_pitch;    // bytes per weight row
+  int tiles, ks, groups, steps;  // warps per tile, tiles a CTA works on at once, 256-wide steps of a row
+  int depth;                     // ring slots
+  int x_chunks;                  // 32-wide chunks of the activations' copy (whole steps)
+  int64_t scale_pitch;           // bytes per weight row
+  bool scales_vec;               // a step's scales are aligned vector loads
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+constexpr uint64_t kFewWaitNs = 1000000000ull;  // 1 s: far beyond any copy's latency
+// Bounded wait for a copy; after one has given up nothing is waited for, and the outputs are NaN.
+__device__ __forceinline__ void few_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*abort) return;
+    if (globaltimer_ns() - t0 > kFewWaitNs) *abort = 1;
+  }
 }
-template <int N>
-__device__ __forceinline__ void cp_small(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ bool few_elect() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
 __device__ __forceinline__ uint4 lds4(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -55,271 +81,404 @@ __device__ __forceinline__ uint32_t lds1(uint32_t a) {
 }
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t mulb(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t mulh(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// byte q of a word as two 4-bit fields at bits 0 and 16
-template <int Q>
-__device__ __forceinline__ uint32_t nibbles(uint32_t t0, uint32_t t1) {
-  uint32_t d;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(t0), "r"(t1), "n"(0x8080 | Q | ((4 + Q) << 8)));
-  return d;
+// a word's 8 weights as f16 pairs (2 q, 2 q + 1): E2M1 values, or INT4 integers
+template <int FMT>
+__device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&v)[4]) {
+  if constexpr (FMT == QZ_INT4) {
+    const uint32_t t0 = w & 0x0F0F0F0Fu, t1 = (w >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t d;  // byte q's nibbles at bits 0 and 16 (selector 8: the sign of byte 0, which is 0)
+      asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(t0), "r"(t1), "r"(0x8080u | q | ((4u + q) << 8)));
+      // f16 1024 + (n ^ 8), less 1032: the two's complement value, exactly
+      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[q]) : "r"(d ^ 0x64086408u), "r"(0x64086408u));
+    }
+  } else {
+    asm("{\n\t.reg .b8 b<4>;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+        : "r"(w));
+  }
 }
-// E2M1 pairs as bf16 times 2^-126: sign to bit 15, exponent and mantissa to bits 6-8
-__device__ __forceinline__ void word_pairs(uint32_t w, uint32_t (&d)[4]) {
-  const uint32_t t0 = w & 0x0F0F0F0Fu, t1 = (w >> 4) & 0x0F0F0F0Fu;
-  d[0] = nibbles<0>(t0, t1);
-  d[1] = nibbles<1>(t0, t1);
-  d[2] = nibbles<2>(t0, t1);
-  d[3] = nibbles<3>(t0, t1);
+__device__ __forceinline__ float pow2(int e) {  // 2^e as fp32, e in [-149, 127]
+  return e >= -126 ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : __uint_as_float(1u << (e + 149));
 }
 
-// FMT; MT weights (gate and up: 2); NT groups of eight tokens; ring of D steps.
-template <int FMT, int MT, int NT>
-struct FewShape {
-  static constexpr int kDepth = MT == 2 ? (NT >= 4 ? 3 : 4) : 8;
-  static constexpr int kScale = FMT == QZ_MXFP4 ? 4 : FMT == QZ_NVFP4 ? 8 : 16;  // bytes of scales per row and step at most
-  static constexpr uint32_t kSlot = MT * (1024 + 16 * kScale);
-  static constexpr uint32_t kJoin = MT * NT * 8 * kTokenStride * 4;              // bytes per warp
-  static constexpr uint32_t kSmem = kFewWarps * (kDepth * kSlot + kJoin);
+// The scales of a weight row's 256 columns of a step, in the words they are stored in: eight E8M0
+// bytes, sixteen E4M3 bytes, or eight fp32 (one per 32 columns, groups of 64 and 128 repeated).
+template <int FMT>
+struct StepScales {
+  static constexpr int kWords = FMT == QZ_MXFP4 ? 2 : FMT == QZ_NVFP4 ? 4 : 8;
+  uint32_t v[kWords];
 };
+// p: the row's scales; outside the weight they are 0 (finite; the codes there are 0)
+template <int FMT>
+__device__ __forceinline__ void load_step_scales(StepScales<FMT>& s, const uint8_t* p, int col, int cols, int log2_block, bool vec) {
+  constexpr int kBytes = FMT == QZ_MXFP4 ? 8 : 16;
+  if constexpr (FMT == QZ_INT4) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p) + (col >> log2_block);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) s.v[c] = col + 32 * c < cols ? __ldg(q + ((32 * c) >> log2_block)) : 0u;
+  } else {
+    p += col / (256 / kBytes);
+    if (vec) {
+      if constexpr (FMT == QZ_MXFP4) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        s.v[0] = v.x;
+        s.v[1] = v.y;
+      } else {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+        s.v[0] = v.x;
+        s.v[1] = v.y;
+        s.v[2] = v.z;
+        s.v[3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < StepScales<FMT>::kWords; ++i) s.v[i] = 0u;
+#pragma unroll
+      for (int i = 0; i < kBytes; ++i)
+        if (col + (256 / kBytes) * i < cols) s.v[i / 4] |= static_cast<uint32_t>(__ldg(p + i)) << (8 * (i % 4));
+    }
+  }
+}
+
+template <int MT>
+struct FewShape {
+  static constexpr uint32_t kSlot = MT * 2048;  // 16 rows x 128 bytes of codes
+  static constexpr uint32_t kJoin = MT * 8 * kTokenStride * 4;
+  static constexpr uint32_t fixed(int depth) { return kFewWarps * (depth * kSlot + kJoin) + 1024; }
+};
+constexpr int kMaxDepth = 6;
 
 template <int FMT, int MT, int NT>
-__global__ void __launch_bounds__(32 * kFewWarps, 2) product_few_kernel(const __grid_constant__ FewArgs a) {
-  using S = FewShape<FMT, MT, NT>;
-  constexpr int kDepth = S::kDepth;
-  extern __shared__ __align__(16) uint8_t few_smem[];
+__global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __grid_constant__ FewArgs a) {
+  using S = FewShape<MT>;
+  extern __shared__ uint8_t few_raw[];
+  __shared__ __align__(8) uint64_t s_full[kFewWarps][kMaxDepth];
+  __shared__ uint32_t s_amax[8 * NT];
+  __shared__ volatile int s_abort;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const ProductArgs& p = a.p;
-  const uint32_t ring = smem_addr(few_smem) + warp * (kDepth * S::kSlot);
+  const int depth = a.depth;
+  uint8_t* few_smem = few_raw + ((1024u - (smem_addr(few_raw) & 1023u)) & 1023u);  // swizzled boxes: 1 KiB
+  const uint32_t ring = smem_addr(few_smem) + warp * (depth * S::kSlot);
+  float* join = reinterpret_cast<float*>(few_smem + kFewWarps * depth * S::kSlot);
+  constexpr int kJoin = S::kJoin / 4;
+  uint8_t* xs = few_smem + kFewWarps * (depth * S::kSlot + S::kJoin);
   const int ks = a.ks, group = warp / ks, part = warp % ks;
-  const int tile0 = blockIdx.x * (kFewWarps / ks) + group, tile_step = gridDim.x * (kFewWarps / ks);
+  const bool busy = group < a.groups;
+  const int tile0 = busy ? blockIdx.x * a.groups + group : a.tiles, tile_step = gridDim.x * a.groups;
   const int s_begin = part * a.steps / ks, s_end = (part + 1) * a.steps / ks;
-  const int rows = static_cast<int>(p.rows), tokens = static_cast<int>(p.tokens);
+  const int rows = static_cast<int>(p.rows), cols = static_cast<int>(p.cols), tokens = static_cast<int>(p.tokens);
+  const uint32_t full = smem_addr(&s_full[warp][0]);
 
-  // ---- the copies, kDepth - 1 steps ahead of the use ----
-  int ptile = tile0, ps = s_begin, pslot = 0;
-  const uint8_t* pc[MT][2];   // codes of rows g and g + 8 at this lane's 16 bytes of step 0
-  const uint8_t* psc[MT];     // scales of row g (t = 0) or g + 8 (t = 1)
-  const auto point = [&]() {
-    const int r0 = min(ptile * 16 + g, rows - 1), r1 = min(ptile * 16 + g + 8, rows - 1);
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const WeightView& w = m ? p.w1 : p.w0;
-      pc[m][0] = w.codes + r0 * a.code_pitch + 16 * t;
-      pc[m][1] = w.codes + r1 * a.code_pitch + 16 * t;
-      psc[m] = static_cast<const uint8_t*>(w.scales) + (t == 0 ? r0 : r1) * a.scale_pitch;
-    }
-  };
-  // INT4 reads word t of chunk c where FP4 reads its own chunk: chunk c of row g then sits at
-  // c ^ (g / 2), which keeps the four-byte loads of a warp on 32 banks
-  const uint32_t own = FMT == QZ_INT4 ? 64u * g + 16u * (t ^ (g >> 1)) : 16u * lane;
+  if (lane == 0) {
+    for (int i = 0; i < kMaxDepth; ++i) mbar_init(full + 8u * i, 1);
+    mbar_init_fence();
+  }
+  if (threadIdx.x == 0) s_abort = 0;
+  if (threadIdx.x < 8 * NT) s_amax[threadIdx.x] = 0u;
+  __syncthreads();
+
+  // ---- the copies, depth - 1 steps ahead of their use ----
+  int ptile = tile0, ps = s_begin, pi = 0;
   const auto issue = [&]() {
     if (ptile < a.tiles) {
-      const uint32_t slot = ring + pslot * S::kSlot;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        cp16(slot + m * 1024 + own, pc[m][0] + ps * 64);
-        cp16(slot + m * 1024 + 512 + own, pc[m][1] + ps * 64);
-        if (t < 2) {
-          const uint32_t dst = slot + MT * 1024 + (m * 16 + g + 8 * t) * S::kScale;
-          const uint8_t* src = psc[m] + static_cast<int64_t>(ps) * a.scale_bytes;
-          if constexpr (FMT == QZ_MXFP4) {
-            cp_small<4>(dst, src);
-          } else if constexpr (FMT == QZ_NVFP4) {
-            cp_small<8>(dst, src);
-          } else {
-            if (a.scale_bytes == 4) cp_small<4>(dst, src);
-            else if (a.scale_bytes == 8) cp_small<8>(dst, src);
-            else cp_small<16>(dst, src);
-          }
-        }
+      if (few_elect()) {
+        const uint32_t bar = full + 8u * pi, dst = ring + pi * S::kSlot;
+        mbar_expect_tx(bar, S::kSlot);
+        tma_box(dst, &a.map_w0, ps * 128, ptile * 16, bar);
+        if constexpr (MT == 2) tma_box(dst + 2048, &a.map_w1, ps * 128, ptile * 16, bar);
       }
+      __syncwarp();
       if (++ps == s_end) {
         ps = s_begin;
         ptile += tile_step;
-        if (ptile < a.tiles) point();
       }
+      if (++pi == depth) pi = 0;
     }
-    cp_commit();  // empty groups keep the count uniform
-    pslot = pslot == kDepth - 1 ? 0 : pslot + 1;
   };
-  if (ptile < a.tiles) point();
-#pragma unroll
-  for (int i = 0; i < kDepth - 1; ++i) issue();
+  for (int i = 0; i < depth - 1; ++i) issue();
 
-  // activations: token 8 nt + g (the last one again past the end: its columns are not stored)
-  const uint16_t* px[NT];
+  // ---- the activations, times 2^p, as f16: [32-wide chunk][token][32], zero past the columns ----
+  {
+    constexpr int kHeld = 8;
+    const int per_token = a.x_chunks * 4, n = per_token * tokens;  // 16-byte pieces
+    uint4 v[kHeld];
+    const auto load = [&](int base) {
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) px[nt] = p.x0 + static_cast<int64_t>(min(8 * nt + g, tokens - 1)) * p.ld_x + (FMT == QZ_INT4 ? 8 * t : 32 * t);
-
-  float* join = reinterpret_cast<float*>(few_smem + kFewWarps * (kDepth * S::kSlot));
-  constexpr int kJoin = S::kJoin / 4;
-  int slot_i = 0;
-  for (int tile = tile0; tile < a.tiles; tile += tile_step) {
-    float z[MT][NT][4] = {};
-#pragma unroll 1
-    for (int s = s_begin; s < s_end; ++s) {
-      cp_wait<kDepth - 2>();
-      __syncwarp();  // every lane's copies of this slot are in; the slot before is read
-      issue();
-      const uint32_t slot = ring + slot_i * S::kSlot;
-      slot_i = slot_i == kDepth - 1 ? 0 : slot_i + 1;
-      if constexpr (FMT == QZ_INT4) {
-        float acc[MT][NT][4] = {};
-        const int per = a.scale_bytes == 4 ? 4 : a.scale_bytes == 8 ? 2 : 1;  // 32-wide chunks per group
-        int gi = 0;
+      for (int i = 0; i < kHeld; ++i) {
+        const int e = base + i * (32 * kFewWarps) + static_cast<int>(threadIdx.x);
+        const int tok = e / per_token, c = e - tok * per_token;
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (e < n && 8 * c < cols) v[i] = __ldg(reinterpret_cast<const uint4*>(p.x0 + tok * p.ld_x) + c);
+      }
+    };
+    constexpr int kRound = kHeld * 32 * kFewWarps;
+    for (int base = 0; base < n; base += kRound) {
+      load(base);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {  // chunk c: 32 columns of one group, lane t its word t
-          uint4 xv[NT];
+      for (int i = 0; i < kHeld; ++i) {
+        const int e = base + i * (32 * kFewWarps) + static_cast<int>(threadIdx.x);
+        if (base + i * (32 * kFewWarps) >= n) break;
+        const int tok = min(e / per_token, tokens - 1);
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t m = 0u;  // the largest finite magnitude
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) xv[nt] = __ldg(reinterpret_cast<const uint4*>(px[nt] + s * 128 + 32 * c));
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint32_t at = slot + m * 1024 + 64u * g + 16u * (c ^ (g >> 1)) + 4u * t;
-            uint32_t v[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              word_pairs(lds1(at + 512 * h), v[h]);
-#pragma unroll
-              for (int q = 0; q < 4; ++q)  // bf16 128 + (n ^ 8), less 136: the value, exactly
-                asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(v[h][q]) : "r"((v[h][q] ^ 0x00080008u) | 0x43004300u), "r"(0xC308C308u));
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma(acc[m][nt], v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
-              mma(acc[m][nt], v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
-            }
-          }
-          if ((c + 1) % per == 0) {  // the group ends: its scale takes the sum
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              const uint32_t sa = slot + MT * 1024 + (m * 16 + g) * S::kScale + 4u * gi;
-              const float s0 = __uint_as_float(lds1(sa)), s1 = __uint_as_float(lds1(sa + 8 * S::kScale));
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  z[m][nt][i] = __fmaf_rn(i < 2 ? s0 : s1, acc[m][nt][i], z[m][nt][i]);
-                  acc[m][nt][i] = 0.0f;
-                }
-              }
-            }
-            ++gi;
-          }
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t hi = w[q] & 0x7fff0000u, lo = (w[q] << 16) & 0x7fff0000u;
+          m = max(m, max(hi < 0x7f800000u ? hi : 0u, lo < 0x7f800000u ? lo : 0u));
         }
-      } else {
-        uint32_t f[MT][2][2];   // bf16 factor pairs of rows g, g + 8; first and second 16 columns
-        uint32_t extra[MT][2];
-        bool big = false;
-        uint4 cw[MT][2];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            cw[m][h] = lds4(slot + m * 1024 + 512 * h + own);
-            const uint32_t sa = slot + MT * 1024 + (m * 16 + g + 8 * h) * S::kScale;
-            if constexpr (FMT == QZ_MXFP4) {
-              // 2^(E - 127) 2^126; exponent fields above 254 take a second factor
-              const uint32_t E = (lds1(sa) >> (8 * t)) & 255u;
-              f[m][h][0] = f[m][h][1] = E == 255u ? 0x7FC07FC0u : (min(E + 126u, 254u) << 7) * 0x00010001u;
-              extra[m][h] = E > 128u ? ((E - 1u) << 7) * 0x00010001u : 0x3F803F80u;
-              big |= E > 128u;
-            } else {
-              // E4M3 bytes at bits 4-10 are 2^-120 of their value; times 2^127 2^111: 2^118 of it
-              const uint32_t b = lds1(sa + 4u * (t >> 1)) >> (16 * (t & 1));
-              const uint32_t c = mulb(mulb(((b & 255u) << 4) | ((b & 0xff00u) << 12), 0x7F007F00u), 0x77007700u);
-              f[m][h][0] = __byte_perm(c, 0, 0x1010);
-              f[m][h][1] = __byte_perm(c, 0, 0x3232);
-            }
-          }
-        const bool any_big = FMT == QZ_MXFP4 && __any_sync(kFull, big);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // word j: columns 32 t + 8 j .. + 7 of the step
-          uint4 xv[NT];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) xv[nt] = __ldg(reinterpret_cast<const uint4*>(px[nt] + s * 128 + 8 * j));
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            uint32_t v[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t w = j == 0 ? cw[m][h].x : j == 1 ? cw[m][h].y : j == 2 ? cw[m][h].z : cw[m][h].w;
-              word_pairs(w, v[h]);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) v[h][q] = mulb((v[h][q] * 0x1040u) & 0x81C081C0u, f[m][h][j >> 1]);
-              if (any_big) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) v[h][q] = mulb(v[h][q], extra[m][h]);
-              }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma(z[m][nt], v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
-              mma(z[m][nt], v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
-            }
-          }
+        if (__match_any_sync(kFull, tok) == kFull) {  // one token
+          m = __reduce_max_sync(kFull, m);
+          if (lane == 0) atomicMax(&s_amax[tok], m);
+        } else {
+          atomicMax(&s_amax[tok], m);
         }
       }
     }
-    // ---- join the parts and store ----
-    float* mine = join + warp * kJoin;
+    __syncthreads();
+    for (int base = 0; base < n; base += kRound) {
+      if (n > kRound) load(base);  // else still in registers
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const int e = base + i * (32 * kFewWarps) + static_cast<int>(threadIdx.x);
+        if (e >= n) break;
+        const int tok = e / per_token, c = e - tok * per_token;
+        const uint32_t m = s_amax[tok];
+        // 2^p: 14 less the exponent of the largest magnitude, 120 at most
+        const float f = pow2(m == 0u ? 0 : min(120, 14 + 127 - static_cast<int>(m >> 23)));
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        uint32_t o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[q]) : "f"(__uint_as_float(w[q] & 0xffff0000u) * f), "f"(__uint_as_float(w[q] << 16) * f));
+        *reinterpret_cast<uint4*>(xs + ((c >> 2) * tokens + tok) * 64 + (c & 3) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+  __syncthreads();
+  if (!busy) return;  // (fewer tiles than warps to share them; no barrier of the whole CTA follows)
+  // this lane's B operand: token 8 nt + g (the last again past the end: its columns are not stored)
+  uint32_t xa[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) xa[nt] = smem_addr(xs) + min(8 * nt + g, tokens - 1) * 64 + 16 * t;
+  const uint32_t x_chunk = 64u * tokens;
+
+  // scales of rows g and g + 8, one step ahead
+  StepScales<FMT> next[MT][2];
+  int ntile = tile0, ns = s_begin;
+  const uint8_t* pr[MT][2];
+  const auto point = [&]() {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int h = 0; h < 2; ++h)
+        pr[m][h] = static_cast<const uint8_t*>(m ? p.w1.scales : p.w0.scales) + min(ntile * 16 + g + 8 * h, rows - 1) * a.scale_pitch;
+  };
+  const auto load_next = [&]() {
+    if (ntile >= a.tiles) return;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          mine[((m * NT + nt) * 8 + 2 * t + (i & 1)) * kTokenStride + g + (i >= 2 ? 8 : 0)] = z[m][nt][i];
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * ks) : "memory");
-    const float* from = join + group * ks * kJoin;
-    constexpr float kUnit = FMT == QZ_NVFP4 ? 256.0f : 1.0f;  // decoded NVFP4 weights are 2^-8 of their value
-    const float f0 = sum_factor<FMT>(p.w0.tscale) * kUnit, f1 = MT == 2 ? sum_factor<FMT>(p.w1.tscale) * kUnit : 0.0f;
-    for (int e = part * 32 + lane; e < 16 * tokens; e += 32 * ks) {
-      const int row = tile * 16 + (e & 15), tok = e >> 4;
-      float sum[MT];
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int at = (m * NT * 8 + tok) * kTokenStride + (e & 15);
-        sum[m] = from[at];
-        for (int w = 1; w < ks; ++w) sum[m] += from[w * kJoin + at];
+      for (int h = 0; h < 2; ++h) load_step_scales<FMT>(next[m][h], pr[m][h], ns * 256, cols, p.log2_block, a.scales_vec);
+    if (++ns == s_end) {
+      ns = s_begin;
+      ntile += tile_step;
+      if (ntile < a.tiles) point();
+    }
+  };
+  if (ntile < a.tiles) point();
+  load_next();
+
+  int ci = 0;
+  uint32_t cph = 0;
+  for (int tile = tile0; tile < a.tiles; tile += tile_step) {
+    float z[MT][NT][4] = {};
+    bool shifted = false;  // z is in units of 2^64 (see kShift)
+#pragma unroll 1
+    for (int s = s_begin; s < s_end; ++s) {
+      StepScales<FMT> now[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) now[m][h] = next[m][h];
+      load_next();
+      few_wait(full + 8u * ci, cph, &s_abort);
+      __syncwarp();  // the slot before is read by every lane
+      issue();
+      const uint32_t slot = ring + ci * S::kSlot;
+      if (++ci == depth) {
+        ci = 0;
+        cph ^= 1u;
       }
-      if (row >= rows) continue;
-      const int64_t o = static_cast<int64_t>(tok) * p.ld_y + row;
-      const float v = sum[0] * f0;
-      if constexpr (MT == 2) {
-        const float u = sum[1] * f1;
-        static_cast<uint16_t*>(p.y)[o] = bf16_bits((p.act == QZ_ACT_SILU ? act_value<QZ_ACT_SILU>(v) : act_value<QZ_ACT_GELU_TANH>(v)) * u);
-        if (p.g_out) {
-          const int64_t q = static_cast<int64_t>(tok) * p.ld_gu + row;
-          p.g_out[q] = bf16_bits(v);
-          p.u_out[q] = bf16_bits(u);
+      // Scales that fp32 does not hold as normal numbers or that could take a sum out of range:
+      // E8M0 bytes 0 and above 200, fp32 above 2^73.
+      bool odd = false, high = false;
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < StepScales<FMT>::kWords; ++i) {
+            if constexpr (FMT == QZ_MXFP4) {
+              odd |= __vcmpeq4(now[m][h].v[i], 0u) != 0u;
+              high |= __vcmpgtu4(now[m][h].v[i], 0xC8C8C8C8u) != 0u;
+            } else if constexpr (FMT == QZ_INT4) {
+              high |= fabsf(__uint_as_float(now[m][h].v[i])) > 0x1p73f;
+            }
+          }
+      if constexpr (FMT != QZ_NVFP4) {
+        if (!shifted && __any_sync(kFull, high)) {
+          shifted = true;
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) z[m][nt][i] *= kShift;
         }
-      } else if (p.out_f32) {
-        static_cast<float*>(p.y)[o] = v;
-      } else {
-        static_cast<uint16_t*>(p.y)[o] = bf16_bits(v);
+        odd = __any_sync(kFull, odd | shifted);
+      }
+      const uint32_t x0 = static_cast<uint32_t>(s) * 8u * x_chunk;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {  // chunk c: 32 columns, lane t its word t
+        uint4 xv[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) xv[nt] = lds4(xa[nt] + x0 + c * x_chunk);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const uint32_t at = slot + m * 2048 + 128u * g + 16u * (c ^ g) + 4u * t;  // 128-byte swizzle
+          uint32_t v[2][4];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            decode_word<FMT>(lds1(at + 1024 * h), v[h]);
+            if constexpr (FMT == QZ_NVFP4) {
+              // this lane's block of the chunk is 2 c + t / 2: its E4M3 byte as an f16 pair
+              const uint32_t b = now[m][h].v[c >> 1] >> (16 * (c & 1));
+              uint32_t f;
+              const uint16_t both = static_cast<uint16_t>(__byte_perm(b, 0, t < 2 ? 0x4400 : 0x4411));
+              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(both));
+#pragma unroll
+              for (int q = 0; q < 4; ++q) v[h][q] = mulh(v[h][q], f);
+            }
+          }
+          float f[2];
+          if constexpr (FMT == QZ_MXFP4) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t E = (now[m][h].v[c >> 2] >> (8 * (c & 3))) & 255u;
+              f[h] = __uint_as_float(E << 23);
+              if (odd) f[h] = E == 255u ? __uint_as_float(0x7fc00000u) : pow2(static_cast<int>(E) - 127) * (shifted ? kShift : 1.0f);
+            }
+          } else if constexpr (FMT == QZ_INT4) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) f[h] = __uint_as_float(now[m][h].v[c]) * (odd ? kShift : 1.0f);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (FMT == QZ_NVFP4) {
+              mma(z[m][nt], v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
+              mma(z[m][nt], v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
+            } else {  // the block's scale takes its sum
+              float acc[4] = {};
+              mma(acc, v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
+              mma(acc, v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) z[m][nt][i] = __fmaf_rn(f[i >> 1], acc[i], z[m][nt][i]);
+            }
+          }
+        }
       }
     }
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * ks) : "memory");
+    // ---- join the parts, eight tokens at a time, and store ----
+    const float f0 = sum_factor<FMT>(p.w0.tscale), f1 = MT == 2 ? sum_factor<FMT>(p.w1.tscale) : 0.0f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float* mine = join + warp * kJoin;
+      float down[2];  // 2^-p of the tokens 8 nt + 2 t and + 1
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t m = s_amax[min(8 * nt + 2 * t + i, tokens - 1)];
+        down[i] = pow2(m == 0u ? 0 : -min(120, 14 + 127 - static_cast<int>(m >> 23)));
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float v = z[m][nt][i] * down[i & 1];
+          mine[(m * 8 + 2 * t + (i & 1)) * kTokenStride + g + (i >= 2 ? 8 : 0)] = shifted ? v * 0x1p64f : v;
+        }
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * ks) : "memory");
+      const float* from = join + group * ks * kJoin;
+      const int count = 16 * min(8, tokens - 8 * nt);
+      for (int e = part * 32 + lane; e < count; e += 32 * ks) {
+        const int row = tile * 16 + (e & 15), tok = 8 * nt + (e >> 4);
+        float sum[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const int at = (m * 8 + (e >> 4)) * kTokenStride + (e & 15);
+          sum[m] = from[at];
+          for (int w = 1; w < ks; ++w) sum[m] += from[w * kJoin + at];
+        }
+        if (row >= rows) continue;
+        const int64_t o = static_cast<int64_t>(tok) * p.ld_y + row;
+        const float v = s_abort ? __uint_as_float(0x7fc00000u) : sum[0] * f0;
+        if constexpr (MT == 2) {
+          const float u = sum[1] * f1;
+          static_cast<uint16_t*>(p.y)[o] = bf16_bits((p.act == QZ_ACT_SILU ? act_value<QZ_ACT_SILU>(v) : act_value<QZ_ACT_GELU_TANH>(v)) * u);
+          if (p.g_out) {
+            const int64_t q = static_cast<int64_t>(tok) * p.ld_gu + row;
+            p.g_out[q] = bf16_bits(v);
+            p.u_out[q] = bf16_bits(u);
+          }
+        } else if (p.out_f32) {
+          static_cast<float*>(p.y)[o] = v;
+        } else {
+          static_cast<uint16_t*>(p.y)[o] = bf16_bits(v);
+        }
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * ks) : "memory");
+    }
   }
-  cp_wait<0>();
+  // (every copy issued has been waited for by its step; after a wait that gave up they get a second more)
+  if (s_abort)
+    for (int i = 0; i < depth; ++i) {
+      const uint64_t t0 = globaltimer_ns();
+      const uint32_t ph = i < ci ? cph : cph ^ 1u;
+      while (!mbar_try_wait(full + 8u * i, ph) && globaltimer_ns() - t0 < kFewWaitNs / 8) {
+      }
+    }
+}
+
+int64_t x_bytes(const ProductArgs& p) { return p.tokens * ((p.cols + 255) / 256) * 512; }
+// the deepest ring that leaves room for the activations, 0: none does
+int few_depth(const ProductArgs& p) {
+  for (int d = p.mode == kModeGated ? 3 : kMaxDepth; d >= 2; --d) {
+    const uint32_t fixed = p.mode == kModeGated ? FewShape<2>::fixed(d) : FewShape<1>::fixed(d);
+    if (fixed + x_bytes(p) <= kFewSmem - 1536) return d;
+  }
+  return 0;
 }
 
 template <int FMT, int MT, int NT>
 qz_status run_few(const FewArgs& a, cudaStream_t s) {
-  using S = FewShape<FMT, MT, NT>;
   const void* k = reinterpret_cast<const void*>(&product_few_kernel<FMT, MT, NT>);
-  if (!set_dyn_smem(k, static_cast<int>(S::kSmem))) return QZ_ERR_CUDA;
-  const int per_cta = kFewWarps / a.ks;
-  const int grid = std::min((a.tiles + per_cta - 1) / per_cta, 2 * sm_count());
-  product_few_kernel<FMT, MT, NT><<<grid, 32 * kFewWarps, S::kSmem, s>>>(a);
+  if (!set_dyn_smem(k, static_cast<int>(kFewSmem - 1536))) return QZ_ERR_CUDA;
+  const int grid = std::min((a.tiles + a.groups - 1) / a.groups, sm_count());
+  const size_t smem = FewShape<MT>::fixed(a.depth) + static_cast<size_t>(x_bytes(a.p));
+  product_few_kernel<FMT, MT, NT><<<grid, 32 * kFewWarps, smem, s>>>(a);
   return launch_status();
 }
 template <int FMT, int MT>
@@ -331,31 +490,45 @@ qz_status run_few_nt(const FewArgs& a, cudaStream_t s) {
     default: return run_few<FMT, MT, 4>(a, s);
   }
 }
+bool encode_codes(CUtensorMap* m, const ProductArgs& p, const WeightView& w) {
+  const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.cols / 2), static_cast<cuuint64_t>(p.rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.cols / 2)};
+  const cuuint32_t box[2] = {128, 16}, es[2] = {1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(w.codes), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 }  // namespace
 
 bool product_few_applicable(const ProductArgs& p) {
-  // whole 128-wide steps; the scales of a step are one aligned copy; groups of 16 change inside
-  // an INT4 mma
-  if (p.mode == kModeBackward || p.tokens > kFewTokens || p.cols % 128 != 0 || p.cols == 0) return false;
-  if (p.format == QZ_INT4 && p.log2_block < 5) return false;
-  const uintptr_t n = p.format == QZ_MXFP4 ? 4 : p.format == QZ_NVFP4 ? 8 : (p.log2_block == 5 ? 16 : p.log2_block == 6 ? 8 : 4);
-  const auto ok = [&](const void* q, uintptr_t a) { return reinterpret_cast<uintptr_t>(q) % a == 0; };
-  return p.ld_x % 8 == 0 && ok(p.x0, 16) && ok(p.w0.codes, 16) && ok(p.w0.scales, n) &&
-         (p.n_weights == 1 || (ok(p.w1.codes, 16) && ok(p.w1.scales, n)));
+  if (p.mode == kModeBackward || p.tokens > kFewTokens || p.cols == 0 || p.cols % 32 != 0) return false;
+  if (p.format == QZ_INT4 && p.log2_block < 5) return false;  // groups of 16 change inside a chunk's sum
+  if (p.rows >= (int64_t{1} << 30) || p.cols >= (int64_t{1} << 30) || few_depth(p) == 0) return false;
+  const auto a16 = [&](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
+  return p.ld_x % 8 == 0 && a16(p.x0) && a16(p.w0.codes) && (p.n_weights == 1 || a16(p.w1.codes));
 }
 
 qz_status launch_product_few(const ProductArgs& p, cudaStream_t s) {
   FewArgs a{};
   a.p = p;
+  if (!encode_codes(&a.map_w0, p, p.w0) || (p.n_weights == 2 && !encode_codes(&a.map_w1, p, p.w1))) return QZ_ERR_CUDA;
   a.tiles = static_cast<int>((p.rows + 15) / 16);
-  a.steps = static_cast<int>(p.cols / 128);
-  // all eight warps on a tile, while every warp has a step
-  a.ks = 8;
+  a.steps = static_cast<int>((p.cols + 255) / 256);
+  a.x_chunks = 8 * a.steps;
+  // all sixteen warps on a tile while the SMs have a tile each at most, else eight on each of two
+  // (a join of eight); every warp has a step
+  const int sms = sm_count();
+  a.ks = a.tiles <= sms ? 16 : 8;
   while (a.ks > a.steps) a.ks /= 2;
-  a.scale_bytes = static_cast<int>((128 >> p.log2_block) * (p.format == QZ_INT4 ? 4 : 1));
-  a.code_pitch = p.cols / 2;
-  a.scale_pitch = static_cast<int64_t>(a.steps) * a.scale_bytes;
+  a.groups = std::max(1, std::min(kFewWarps / a.ks, (a.tiles + sms - 1) / sms));
+  a.depth = few_depth(p);
+  a.scale_pitch = (p.cols >> p.log2_block) * (p.format == QZ_INT4 ? 4 : 1);
+  const uintptr_t n = p.format == QZ_MXFP4 ? 8 : 16;
+  const auto ok = [&](const void* q) { return reinterpret_cast<uintptr_t>(q) % n == 0; };
+  a.scales_vec = p.cols % 256 == 0 && ok(p.w0.scales) && (p.n_weights == 1 || ok(p.w1.scales));
   const bool two = p.mode == kModeGated;
   if (p.format == QZ_MXFP4) return two ? run_few_nt<QZ_MXFP4, 2>(a, s) : run_few_nt<QZ_MXFP4, 1>(a, s);
   if (p.format == QZ_NVFP4) return two ? run_few_nt<QZ_NVFP4, 2>(a, s) : run_few_nt<QZ_NVFP4, 1>(a, s);
