@@ -33,10 +33,10 @@
 namespace qz {
 namespace {
 
-constexpr int kFewWarps = 16;
+constexpr int W = 16;                   // warps per CTA
 constexpr int kTokenStride = 20;        // floats of a token's 16 sums in the join (banks 8 t + g)
 constexpr uint32_t kFewSmem = 227 * 1024;
-constexpr float kShift = 0x1p-64f;      // the sums' unit once a scale above 2^73 has been met
+constexpr float kShift = 0x1p-64f;      // the sums' unit once a scale above 2^64 (INT4 2^73) has been met
 
 struct FewArgs {
   CUtensorMap map_w0, map_w1;  // codes [rows][cols / 2] bytes, box 128 x 16
@@ -45,7 +45,6 @@ struct FewArgs {
   int depth;                     // ring slots
   int x_chunks;                  // 32-wide chunks of the activations' copy (whole steps)
   int64_t scale_pitch;           // bytes per weight row
-  bool scales_vec;               // a step's scales are aligned vector loads
 };
 
 constexpr uint64_t kFewWaitNs = 1000000000ull;  // 1 s: far beyond any copy's latency
@@ -121,62 +120,49 @@ struct StepScales {
   static constexpr int kWords = FMT == QZ_MXFP4 ? 2 : FMT == QZ_NVFP4 ? 4 : 8;
   uint32_t v[kWords];
 };
-// p: the row's scales; outside the weight they are 0 (finite; the codes there are 0)
+// p: the row's scales.  Straight loads without a branch: where two paths meet, the loaded registers
+// would be copied and so waited for at once.
 template <int FMT>
-__device__ __forceinline__ void load_step_scales(StepScales<FMT>& s, const uint8_t* p, int col, int cols, int log2_block, bool vec) {
-  constexpr int kBytes = FMT == QZ_MXFP4 ? 8 : 16;
-  if constexpr (FMT == QZ_INT4) {
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(p) + (col >> log2_block);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) s.v[c] = col + 32 * c < cols ? __ldg(q + ((32 * c) >> log2_block)) : 0u;
+__device__ __forceinline__ void load_step_scales(StepScales<FMT>& s, const uint8_t* p, int step, int log2_block) {
+  if constexpr (FMT == QZ_MXFP4) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + 8 * step));
+    s.v[0] = v.x;
+    s.v[1] = v.y;
+  } else if constexpr (FMT == QZ_NVFP4) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + 16 * step));
+    s.v[0] = v.x;
+    s.v[1] = v.y;
+    s.v[2] = v.z;
+    s.v[3] = v.w;
   } else {
-    p += col / (256 / kBytes);
-    if (vec) {
-      if constexpr (FMT == QZ_MXFP4) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-        s.v[0] = v.x;
-        s.v[1] = v.y;
-      } else {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-        s.v[0] = v.x;
-        s.v[1] = v.y;
-        s.v[2] = v.z;
-        s.v[3] = v.w;
-      }
-    } else {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p) + ((256 * step) >> log2_block);
 #pragma unroll
-      for (int i = 0; i < StepScales<FMT>::kWords; ++i) s.v[i] = 0u;
-#pragma unroll
-      for (int i = 0; i < kBytes; ++i)
-        if (col + (256 / kBytes) * i < cols) s.v[i / 4] |= static_cast<uint32_t>(__ldg(p + i)) << (8 * (i % 4));
-    }
+    for (int c = 0; c < 8; ++c) s.v[c] = __ldg(q + ((32 * c) >> log2_block));
   }
 }
 
-template <int MT>
-struct FewShape {
-  static constexpr uint32_t kSlot = MT * 2048;  // 16 rows x 128 bytes of codes
-  static constexpr uint32_t kJoin = MT * 8 * kTokenStride * 4;
-  static constexpr uint32_t fixed(int depth) { return kFewWarps * (depth * kSlot + kJoin) + 1024; }
-};
+constexpr uint32_t kSlot = 2048;                    // a step: 16 rows x 128 bytes of codes
+constexpr uint32_t kJoin = 8 * kTokenStride;        // floats of a warp's sums for 8 tokens
+constexpr uint32_t few_fixed(int depth) { return W * (depth * kSlot + kJoin * 4) + 1024; }
 constexpr int kMaxDepth = 6;
 
-template <int FMT, int MT, int NT>
-__global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __grid_constant__ FewArgs a) {
-  using S = FewShape<MT>;
+template <int FMT, int NT, bool GATED>
+__global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_constant__ FewArgs a) {
   extern __shared__ uint8_t few_raw[];
-  __shared__ __align__(8) uint64_t s_full[kFewWarps][kMaxDepth];
+  __shared__ __align__(8) uint64_t s_full[W][kMaxDepth];
   __shared__ uint32_t s_amax[8 * NT];
   __shared__ volatile int s_abort;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const ProductArgs& p = a.p;
   const int depth = a.depth;
   uint8_t* few_smem = few_raw + ((1024u - (smem_addr(few_raw) & 1023u)) & 1023u);  // swizzled boxes: 1 KiB
-  const uint32_t ring = smem_addr(few_smem) + warp * (depth * S::kSlot);
-  float* join = reinterpret_cast<float*>(few_smem + kFewWarps * depth * S::kSlot);
-  constexpr int kJoin = S::kJoin / 4;
-  uint8_t* xs = few_smem + kFewWarps * (depth * S::kSlot + S::kJoin);
-  const int ks = a.ks, group = warp / ks, part = warp % ks;
+  const uint32_t ring = smem_addr(few_smem) + warp * (depth * kSlot);
+  float* join = reinterpret_cast<float*>(few_smem + W * depth * kSlot);
+  uint8_t* xs = few_smem + W * (depth * kSlot + kJoin * 4);
+  // ks warps share a tile; gated: ks more have the same outputs of the second weight
+  constexpr int kWeights = GATED ? 2 : 1;
+  const int ks = a.ks, team = ks * kWeights, group = warp / team, member = warp % team, part = member % ks;
+  const bool second = GATED && member >= ks;
   const bool busy = group < a.groups;
   const int tile0 = busy ? blockIdx.x * a.groups + group : a.tiles, tile_step = gridDim.x * a.groups;
   const int s_begin = part * a.steps / ks, s_end = (part + 1) * a.steps / ks;
@@ -196,10 +182,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
   const auto issue = [&]() {
     if (ptile < a.tiles) {
       if (few_elect()) {
-        const uint32_t bar = full + 8u * pi, dst = ring + pi * S::kSlot;
-        mbar_expect_tx(bar, S::kSlot);
-        tma_box(dst, &a.map_w0, ps * 128, ptile * 16, bar);
-        if constexpr (MT == 2) tma_box(dst + 2048, &a.map_w1, ps * 128, ptile * 16, bar);
+        const uint32_t bar = full + 8u * pi, dst = ring + pi * kSlot;
+        mbar_expect_tx(bar, kSlot);
+        tma_box(dst, second ? &a.map_w1 : &a.map_w0, ps * 128, ptile * 16, bar);
       }
       __syncwarp();
       if (++ps == s_end) {
@@ -213,49 +198,53 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
 
   // ---- the activations, times 2^p, as f16: [32-wide chunk][token][32], zero past the columns ----
   {
-    constexpr int kHeld = 8;
-    const int per_token = a.x_chunks * 4, n = per_token * tokens;  // 16-byte pieces
+    constexpr int kHeld = 8, kAll = 32 * W;
+    // a round holds up to eight pieces of 8 values a thread, each of them kAll consecutive pieces of one token
+    const int per_token = a.x_chunks * 4, blocks = (per_token + kAll - 1) / kAll, n = blocks * tokens;
     uint4 v[kHeld];
+    const auto piece = [&](int j, int& tok, int& c) {  // block j (uniform): its token, this thread's piece
+      tok = j / blocks;
+      c = (j - tok * blocks) * kAll + static_cast<int>(threadIdx.x);
+    };
     const auto load = [&](int base) {
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) {
-        const int e = base + i * (32 * kFewWarps) + static_cast<int>(threadIdx.x);
-        const int tok = e / per_token, c = e - tok * per_token;
+        int tok, c;
+        piece(base + i, tok, c);
         v[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (e < n && 8 * c < cols) v[i] = __ldg(reinterpret_cast<const uint4*>(p.x0 + tok * p.ld_x) + c);
+        if (base + i < n && 8 * c < cols) v[i] = __ldg(reinterpret_cast<const uint4*>(p.x0 + tok * p.ld_x) + c);
       }
     };
-    constexpr int kRound = kHeld * 32 * kFewWarps;
-    for (int base = 0; base < n; base += kRound) {
+    for (int base = 0; base < n; base += kHeld) {
       load(base);
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) {
-        const int e = base + i * (32 * kFewWarps) + static_cast<int>(threadIdx.x);
-        if (base + i * (32 * kFewWarps) >= n) break;
-        const int tok = min(e / per_token, tokens - 1);
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t m = 0u;  // the largest finite magnitude
+        if (base + i >= n) break;
+        int tok, c;
+        piece(base + i, tok, c);
+        const uint32_t w[4] = {v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu, v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu};
+        const uint32_t m2 = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+        uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+        if (m >= 0x7f80u) {  // the largest finite magnitude
+          m = 0u;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t hi = w[q] & 0x7fff0000u, lo = (w[q] << 16) & 0x7fff0000u;
-          m = max(m, max(hi < 0x7f800000u ? hi : 0u, lo < 0x7f800000u ? lo : 0u));
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t lo = w[q] & 0xffffu, hi = w[q] >> 16;
+            m = max(m, max(hi < 0x7f80u ? hi : 0u, lo < 0x7f80u ? lo : 0u));
+          }
         }
-        if (__match_any_sync(kFull, tok) == kFull) {  // one token
-          m = __reduce_max_sync(kFull, m);
-          if (lane == 0) atomicMax(&s_amax[tok], m);
-        } else {
-          atomicMax(&s_amax[tok], m);
-        }
+        m = __reduce_max_sync(kFull, m);
+        if (lane == 0) atomicMax(&s_amax[tok], m << 16);
       }
     }
     __syncthreads();
-    for (int base = 0; base < n; base += kRound) {
-      if (n > kRound) load(base);  // else still in registers
+    for (int base = 0; base < n; base += kHeld) {
+      if (n > kHeld) load(base);  // else still in registers
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) {
-        const int e = base + i * (32 * kFewWarps) + static_cast<int>(threadIdx.x);
-        if (e >= n) break;
-        const int tok = e / per_token, c = e - tok * per_token;
+        if (base + i >= n) break;
+        int tok, c;
+        piece(base + i, tok, c);
         const uint32_t m = s_amax[tok];
         // 2^p: 14 less the exponent of the largest magnitude, 120 at most
         const float f = pow2(m == 0u ? 0 : min(120, 14 + 127 - static_cast<int>(m >> 23)));
@@ -264,7 +253,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[q]) : "f"(__uint_as_float(w[q] & 0xffff0000u) * f), "f"(__uint_as_float(w[q] << 16) * f));
-        *reinterpret_cast<uint4*>(xs + ((c >> 2) * tokens + tok) * 64 + (c & 3) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+        if (c < per_token)
+          *reinterpret_cast<uint4*>(xs + ((c >> 2) * tokens + tok) * 64 + (c & 3) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
@@ -277,77 +267,81 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
   const uint32_t x_chunk = 64u * tokens;
 
   // scales of rows g and g + 8, one step ahead
-  StepScales<FMT> next[MT][2];
+  StepScales<FMT> next[2];
   int ntile = tile0, ns = s_begin;
-  const uint8_t* pr[MT][2];
+  const uint8_t* pr[2];
   const auto point = [&]() {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        pr[m][h] = static_cast<const uint8_t*>(m ? p.w1.scales : p.w0.scales) + min(ntile * 16 + g + 8 * h, rows - 1) * a.scale_pitch;
+    for (int h = 0; h < 2; ++h)
+      pr[h] = static_cast<const uint8_t*>(second ? p.w1.scales : p.w0.scales) + min(ntile * 16 + g + 8 * h, rows - 1) * a.scale_pitch;
   };
-  const auto load_next = [&]() {
-    if (ntile >= a.tiles) return;
+  const auto load_next = [&]() {  // (past the last tile: its last row's again)
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) load_step_scales<FMT>(next[m][h], pr[m][h], ns * 256, cols, p.log2_block, a.scales_vec);
+    for (int h = 0; h < 2; ++h) load_step_scales<FMT>(next[h], pr[h], ns, p.log2_block);
     if (++ns == s_end) {
       ns = s_begin;
       ntile += tile_step;
-      if (ntile < a.tiles) point();
+      point();
     }
   };
-  if (ntile < a.tiles) point();
+  point();
   load_next();
 
   int ci = 0;
   uint32_t cph = 0;
+  const uint32_t word = 128u * g + 4u * t;  // word t of chunk c of row g: 16 (c ^ g) further (128-byte swizzle)
   for (int tile = tile0; tile < a.tiles; tile += tile_step) {
-    float z[MT][NT][4] = {};
+    float z[NT][4] = {};
     bool shifted = false;  // z is in units of 2^64 (see kShift)
 #pragma unroll 1
     for (int s = s_begin; s < s_end; ++s) {
-      StepScales<FMT> now[MT][2];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) now[m][h] = next[m][h];
+      StepScales<FMT> now[2] = {next[0], next[1]};
       load_next();
       few_wait(full + 8u * ci, cph, &s_abort);
       __syncwarp();  // the slot before is read by every lane
       issue();
-      const uint32_t slot = ring + ci * S::kSlot;
+      const uint32_t slot = ring + ci * kSlot + word;
       if (++ci == depth) {
         ci = 0;
         cph ^= 1u;
       }
-      // Scales that fp32 does not hold as normal numbers or that could take a sum out of range:
-      // E8M0 bytes 0 and above 200, fp32 above 2^73.
-      bool odd = false, high = false;
+      bool odd = false;
+      if constexpr (FMT == QZ_NVFP4) {
+        // this lane's block of chunk c is 2 c + t / 2: eight E4M3 bytes, then f16 (chunks 2 i, 2 i + 1)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t sel = t < 2 ? 0x6420u : 0x7531u;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t b;
+            asm("prmt.b32 %0, %1, %2, %3;" : "=r"(b) : "r"(now[h].v[2 * i]), "r"(now[h].v[2 * i + 1]), "r"(sel));
+            asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+                : "=r"(now[h].v[2 * i]), "=r"(now[h].v[2 * i + 1])
+                : "r"(b));
+          }
+        }
+      } else {
+        // Scales that fp32 does not hold as normal numbers or that could take a sum out of range:
+        // E8M0 bytes 0 and above 191, fp32 above 2^73.
+        bool high = false;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int i = 0; i < StepScales<FMT>::kWords; ++i) {
             if constexpr (FMT == QZ_MXFP4) {
-              odd |= __vcmpeq4(now[m][h].v[i], 0u) != 0u;
-              high |= __vcmpgtu4(now[m][h].v[i], 0xC8C8C8C8u) != 0u;
-            } else if constexpr (FMT == QZ_INT4) {
-              high |= fabsf(__uint_as_float(now[m][h].v[i])) > 0x1p73f;
+              const uint32_t e = now[h].v[i];
+              odd |= ((e - 0x01010101u) & ~e & 0x80808080u) != 0u;  // a byte 0 (and some bytes 1 above one)
+              high |= ((e & 0x80808080u) & ((e << 1) & 0x80808080u)) != 0u;  // a byte above 191
+            } else {
+              high |= fabsf(__uint_as_float(now[h].v[i])) > 0x1p73f;
             }
           }
-      if constexpr (FMT != QZ_NVFP4) {
         if (!shifted && __any_sync(kFull, high)) {
           shifted = true;
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) z[m][nt][i] *= kShift;
+            for (int i = 0; i < 4; ++i) z[nt][i] *= kShift;
         }
         odd = __any_sync(kFull, odd | shifted);
       }
@@ -357,86 +351,73 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
         uint4 xv[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) xv[nt] = lds4(xa[nt] + x0 + c * x_chunk);
+        uint32_t v[2][4];
+        float f[2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const uint32_t at = slot + m * 2048 + 128u * g + 16u * (c ^ g) + 4u * t;  // 128-byte swizzle
-          uint32_t v[2][4];
+        for (int h = 0; h < 2; ++h) {
+          decode_word<FMT>(lds1(slot + 1024 * h + ((c ^ g) << 4)), v[h]);
+          if constexpr (FMT == QZ_NVFP4) {
+            const uint32_t both = __byte_perm(now[h].v[c >> 1], 0, (c & 1) ? 0x3232 : 0x1010);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            decode_word<FMT>(lds1(at + 1024 * h), v[h]);
-            if constexpr (FMT == QZ_NVFP4) {
-              // this lane's block of the chunk is 2 c + t / 2: its E4M3 byte as an f16 pair
-              const uint32_t b = now[m][h].v[c >> 1] >> (16 * (c & 1));
-              uint32_t f;
-              const uint16_t both = static_cast<uint16_t>(__byte_perm(b, 0, t < 2 ? 0x4400 : 0x4411));
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(both));
-#pragma unroll
-              for (int q = 0; q < 4; ++q) v[h][q] = mulh(v[h][q], f);
+            for (int q = 0; q < 4; ++q) v[h][q] = mulh(v[h][q], both);
+          } else if constexpr (FMT == QZ_MXFP4) {
+            const uint32_t E = now[h].v[c >> 2];
+            f[h] = __uint_as_float(((c & 3) == 3 ? E >> 1 : E << (23 - 8 * (c & 3))) & 0x7f800000u);
+            if (odd) {
+              const uint32_t b = (E >> (8 * (c & 3))) & 255u;
+              f[h] = b == 255u ? __uint_as_float(0x7fc00000u) : pow2(static_cast<int>(b) - 127) * (shifted ? kShift : 1.0f);
             }
+          } else {
+            f[h] = __uint_as_float(now[h].v[c]) * (odd ? kShift : 1.0f);
           }
-          float f[2];
-          if constexpr (FMT == QZ_MXFP4) {
+        }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t E = (now[m][h].v[c >> 2] >> (8 * (c & 3))) & 255u;
-              f[h] = __uint_as_float(E << 23);
-              if (odd) f[h] = E == 255u ? __uint_as_float(0x7fc00000u) : pow2(static_cast<int>(E) - 127) * (shifted ? kShift : 1.0f);
-            }
-          } else if constexpr (FMT == QZ_INT4) {
+        for (int nt = 0; nt < NT; ++nt) {
+          if constexpr (FMT == QZ_NVFP4) {
+            mma(z[nt], v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
+            mma(z[nt], v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
+          } else {  // the block's scale takes its sum
+            float acc[4] = {};
+            mma(acc, v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
+            mma(acc, v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) f[h] = __uint_as_float(now[m][h].v[c]) * (odd ? kShift : 1.0f);
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (FMT == QZ_NVFP4) {
-              mma(z[m][nt], v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
-              mma(z[m][nt], v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
-            } else {  // the block's scale takes its sum
-              float acc[4] = {};
-              mma(acc, v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
-              mma(acc, v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) z[m][nt][i] = __fmaf_rn(f[i >> 1], acc[i], z[m][nt][i]);
-            }
+            for (int i = 0; i < 4; ++i) z[nt][i] = __fmaf_rn(f[i >> 1], acc[i], z[nt][i]);
           }
         }
       }
     }
     // ---- join the parts, eight tokens at a time, and store ----
-    const float f0 = sum_factor<FMT>(p.w0.tscale), f1 = MT == 2 ? sum_factor<FMT>(p.w1.tscale) : 0.0f;
+    const float f0 = sum_factor<FMT>(p.w0.tscale), f1 = GATED ? sum_factor<FMT>(p.w1.tscale) : 0.0f;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float* mine = join + warp * kJoin;
-      float down[2];  // 2^-p of the tokens 8 nt + 2 t and + 1
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 2; ++i) {  // tokens 8 nt + 2 t and + 1: 2^-p of each
         const uint32_t m = s_amax[min(8 * nt + 2 * t + i, tokens - 1)];
-        down[i] = pow2(m == 0u ? 0 : -min(120, 14 + 127 - static_cast<int>(m >> 23)));
-      }
+        const float down = pow2(m == 0u ? 0 : -min(120, 14 + 127 - static_cast<int>(m >> 23)));
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float v = z[m][nt][i] * down[i & 1];
-          mine[(m * 8 + 2 * t + (i & 1)) * kTokenStride + g + (i >= 2 ? 8 : 0)] = shifted ? v * 0x1p64f : v;
+        for (int h = 0; h < 2; ++h) {
+          const float v = z[nt][2 * h + i] * down;
+          mine[(2 * t + i) * kTokenStride + g + 8 * h] = shifted ? v * 0x1p64f : v;
         }
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * ks) : "memory");
-      const float* from = join + group * ks * kJoin;
+      }
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * team) : "memory");
+      const float* from = join + group * team * kJoin;
       const int count = 16 * min(8, tokens - 8 * nt);
-      for (int e = part * 32 + lane; e < count; e += 32 * ks) {
+      for (int e = member * 32 + lane; e < count; e += 32 * team) {
         const int row = tile * 16 + (e & 15), tok = 8 * nt + (e >> 4);
-        float sum[MT];
+        float sum[kWeights];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const int at = (m * 8 + (e >> 4)) * kTokenStride + (e & 15);
-          sum[m] = from[at];
-          for (int w = 1; w < ks; ++w) sum[m] += from[w * kJoin + at];
+        for (int m = 0; m < kWeights; ++m) {
+          const float* q = from + m * ks * kJoin + (e >> 4) * kTokenStride + (e & 15);
+          sum[m] = q[0];
+          for (int w = 1; w < ks; ++w) sum[m] += q[w * kJoin];
         }
         if (row >= rows) continue;
         const int64_t o = static_cast<int64_t>(tok) * p.ld_y + row;
         const float v = s_abort ? __uint_as_float(0x7fc00000u) : sum[0] * f0;
-        if constexpr (MT == 2) {
-          const float u = sum[1] * f1;
+        if constexpr (GATED) {
+          const float u = sum[kWeights - 1] * f1;
           static_cast<uint16_t*>(p.y)[o] = bf16_bits((p.act == QZ_ACT_SILU ? act_value<QZ_ACT_SILU>(v) : act_value<QZ_ACT_GELU_TANH>(v)) * u);
           if (p.g_out) {
             const int64_t q = static_cast<int64_t>(tok) * p.ld_gu + row;
@@ -449,7 +430,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
           static_cast<uint16_t*>(p.y)[o] = bf16_bits(v);
         }
       }
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * ks) : "memory");
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * team) : "memory");
     }
   }
   // (every copy issued has been waited for by its step; after a wait that gave up they get a second more)
@@ -462,32 +443,39 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
     }
 }
 
-int64_t x_bytes(const ProductArgs& p) { return p.tokens * ((p.cols + 255) / 256) * 512; }
+int64_t x_bytes(const ProductArgs& p) { return p.tokens * p.cols * 2; }
 // the deepest ring that leaves room for the activations, 0: none does
 int few_depth(const ProductArgs& p) {
-  for (int d = p.mode == kModeGated ? 3 : kMaxDepth; d >= 2; --d) {
-    const uint32_t fixed = p.mode == kModeGated ? FewShape<2>::fixed(d) : FewShape<1>::fixed(d);
-    if (fixed + x_bytes(p) <= kFewSmem - 1536) return d;
-  }
+  for (int d = kMaxDepth; d >= 2; --d)
+    if (few_fixed(d) + x_bytes(p) <= kFewSmem - 2048) return d;
   return 0;
 }
 
-template <int FMT, int MT, int NT>
+template <int FMT, int NT, bool GATED>
 qz_status run_few(const FewArgs& a, cudaStream_t s) {
-  const void* k = reinterpret_cast<const void*>(&product_few_kernel<FMT, MT, NT>);
-  if (!set_dyn_smem(k, static_cast<int>(kFewSmem - 1536))) return QZ_ERR_CUDA;
+  const void* k = reinterpret_cast<const void*>(&product_few_kernel<FMT, NT, GATED>);
+  if (!set_dyn_smem(k, static_cast<int>(kFewSmem - 2048))) return QZ_ERR_CUDA;
   const int grid = std::min((a.tiles + a.groups - 1) / a.groups, sm_count());
-  const size_t smem = FewShape<MT>::fixed(a.depth) + static_cast<size_t>(x_bytes(a.p));
-  product_few_kernel<FMT, MT, NT><<<grid, 32 * kFewWarps, smem, s>>>(a);
+  const size_t smem = few_fixed(a.depth) + static_cast<size_t>(x_bytes(a.p));
+  product_few_kernel<FMT, NT, GATED><<<grid, 32 * W, smem, s>>>(a);
   return launch_status();
 }
-template <int FMT, int MT>
-qz_status run_few_nt(const FewArgs& a, cudaStream_t s) {
-  switch ((a.p.tokens + 7) / 8) {
-    case 1: return run_few<FMT, MT, 1>(a, s);
-    case 2: return run_few<FMT, MT, 2>(a, s);
-    case 3: return run_few<FMT, MT, 3>(a, s);
-    default: return run_few<FMT, MT, 4>(a, s);
+template <int FMT, bool GATED>
+qz_status run_few_nt(FewArgs& a, cudaStream_t s) {
+  const ProductArgs& p = a.p;
+  const int nt = static_cast<int>((p.tokens + 7) / 8), sms = sm_count();
+  constexpr int kWeights = GATED ? 2 : 1;
+  // a tile takes all of a CTA's warps while the SMs have a tile each at most, else half of them at
+  // most (a shorter join); every warp has a step
+  a.ks = (a.tiles <= sms ? W : W / 2) / kWeights;
+  while (a.ks > a.steps) a.ks /= 2;
+  a.groups = std::max(1, std::min({W / (a.ks * kWeights), (a.tiles + sms - 1) / sms, 15}));  // 15 named barriers
+  a.depth = few_depth(p);
+  switch (nt) {
+    case 1: return run_few<FMT, 1, GATED>(a, s);
+    case 2: return run_few<FMT, 2, GATED>(a, s);
+    case 3: return run_few<FMT, 3, GATED>(a, s);
+    default: return run_few<FMT, 4, GATED>(a, s);
   }
 }
 bool encode_codes(CUtensorMap* m, const ProductArgs& p, const WeightView& w) {
@@ -504,11 +492,14 @@ bool encode_codes(CUtensorMap* m, const ProductArgs& p, const WeightView& w) {
 }  // namespace
 
 bool product_few_applicable(const ProductArgs& p) {
-  if (p.mode == kModeBackward || p.tokens > kFewTokens || p.cols == 0 || p.cols % 32 != 0) return false;
+  if (p.mode == kModeBackward || p.tokens > kFewTokens || p.cols == 0 || p.cols % 256 != 0) return false;
   if (p.format == QZ_INT4 && p.log2_block < 5) return false;  // groups of 16 change inside a chunk's sum
   if (p.rows >= (int64_t{1} << 30) || p.cols >= (int64_t{1} << 30) || few_depth(p) == 0) return false;
-  const auto a16 = [&](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
-  return p.ld_x % 8 == 0 && a16(p.x0) && a16(p.w0.codes) && (p.n_weights == 1 || a16(p.w1.codes));
+  // whole steps; a step's scales are one aligned load
+  const uintptr_t n = p.format == QZ_MXFP4 ? 8 : p.format == QZ_NVFP4 ? 16 : 4;
+  const auto ok = [&](const void* q, uintptr_t a) { return reinterpret_cast<uintptr_t>(q) % a == 0; };
+  return p.ld_x % 8 == 0 && ok(p.x0, 16) && ok(p.w0.codes, 16) && ok(p.w0.scales, n) &&
+         (p.n_weights == 1 || (ok(p.w1.codes, 16) && ok(p.w1.scales, n)));
 }
 
 qz_status launch_product_few(const ProductArgs& p, cudaStream_t s) {
@@ -516,23 +507,13 @@ qz_status launch_product_few(const ProductArgs& p, cudaStream_t s) {
   a.p = p;
   if (!encode_codes(&a.map_w0, p, p.w0) || (p.n_weights == 2 && !encode_codes(&a.map_w1, p, p.w1))) return QZ_ERR_CUDA;
   a.tiles = static_cast<int>((p.rows + 15) / 16);
-  a.steps = static_cast<int>((p.cols + 255) / 256);
+  a.steps = static_cast<int>(p.cols / 256);
   a.x_chunks = 8 * a.steps;
-  // all sixteen warps on a tile while the SMs have a tile each at most, else eight on each of two
-  // (a join of eight); every warp has a step
-  const int sms = sm_count();
-  a.ks = a.tiles <= sms ? 16 : 8;
-  while (a.ks > a.steps) a.ks /= 2;
-  a.groups = std::max(1, std::min(kFewWarps / a.ks, (a.tiles + sms - 1) / sms));
-  a.depth = few_depth(p);
   a.scale_pitch = (p.cols >> p.log2_block) * (p.format == QZ_INT4 ? 4 : 1);
-  const uintptr_t n = p.format == QZ_MXFP4 ? 8 : 16;
-  const auto ok = [&](const void* q) { return reinterpret_cast<uintptr_t>(q) % n == 0; };
-  a.scales_vec = p.cols % 256 == 0 && ok(p.w0.scales) && (p.n_weights == 1 || ok(p.w1.scales));
   const bool two = p.mode == kModeGated;
-  if (p.format == QZ_MXFP4) return two ? run_few_nt<QZ_MXFP4, 2>(a, s) : run_few_nt<QZ_MXFP4, 1>(a, s);
-  if (p.format == QZ_NVFP4) return two ? run_few_nt<QZ_NVFP4, 2>(a, s) : run_few_nt<QZ_NVFP4, 1>(a, s);
-  return two ? run_few_nt<QZ_INT4, 2>(a, s) : run_few_nt<QZ_INT4, 1>(a, s);
+  if (p.format == QZ_MXFP4) return two ? run_few_nt<QZ_MXFP4, true>(a, s) : run_few_nt<QZ_MXFP4, false>(a, s);
+  if (p.format == QZ_NVFP4) return two ? run_few_nt<QZ_NVFP4, true>(a, s) : run_few_nt<QZ_NVFP4, false>(a, s);
+  return two ? run_few_nt<QZ_INT4, true>(a, s) : run_few_nt<QZ_INT4, false>(a, s);
 }
 
 }  // namespace qz
