@@ -570,21 +570,22 @@ class Weight:
                              _ptr(q.tensor_scale) if q.fmt == QZ_NVFP4 else None)
 
 
-def _matrix(t, width: int, dtype, what: str):
-    """Leading dimension of a [tokens, width] CUDA matrix with unit inner stride."""
-    if t.dim() != 2 or t.shape[1] != width or t.dtype != dtype:
-        raise ValueError(f"{what} must be a [tokens, {width}] {dtype} matrix, not "
-                         f"{tuple(t.shape)} {t.dtype}")
+def _matrix(t, width: int, dtype, what: str) -> int:
+    """Leading dimension of a [tokens, width] CUDA matrix with unit inner stride.  (A product of one
+    token takes a few microseconds on the GPU, so the common case is one test of each property.)"""
+    if t.dim() == 2 and t.dtype is dtype and t.is_cuda:
+        (n, w), (s0, s1) = t.shape, t.stride()
+        if w == width and (s1 == 1 or w <= 1 or n == 0):
+            if n <= 1:
+                return s0 if s0 > width else width
+            if s0 >= width:
+                return s0
+            raise ValueError(f"{what}: rows overlap")
+        if w == width:
+            raise ValueError(f"{what}: the inner dimension must be contiguous")
     if not t.is_cuda:
         raise ValueError(f"{what} must be on the GPU")
-    s0, s1 = t.stride()
-    if s1 != 1 and t.shape[1] > 1 and t.shape[0]:
-        raise ValueError(f"{what}: the inner dimension must be contiguous")
-    if t.shape[0] <= 1:
-        return max(s0, width)
-    if s0 < width:
-        raise ValueError(f"{what}: rows overlap")
-    return s0
+    raise ValueError(f"{what} must be a [tokens, {width}] {dtype} matrix, not {tuple(t.shape)} {t.dtype}")
 
 
 def _same_tokens(tokens: int, **matrices):
@@ -593,43 +594,47 @@ def _same_tokens(tokens: int, **matrices):
             raise ValueError(f"{what} must have {tokens} rows, not {t.shape[0]}")
 
 
-def _raw_stream(stream, device) -> int:
+def _raw_stream(stream, t) -> int:
+    """The given torch stream, or the current one of t's device, as the library takes it."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _linear_call(name: str, x, width: int, weight: Weight, out_width: int, out_dtype, out, stream, what: str):
     torch = _torch()
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    bf = torch.bfloat16
+    ld_x = _matrix(x, width, bf, what)
+    tokens = x.shape[0]
+    if out is None:
+        if out_dtype is None or out_dtype is bf:
+            out, code = x.new_empty((tokens, out_width)), QZ_BF16
+        else:
+            code = _dtype_code(out_dtype)
+            out = x.new_empty((tokens, out_width), dtype=out_dtype)
+        ld_y = out_width
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out has another dtype than out_dtype")
+        code = _dtype_code(out.dtype)
+        ld_y = _matrix(out, out_width, out.dtype, "out")
+        _same_tokens(tokens, out=out)
+    rc = getattr(_lib or lib(), name)(weight.desc, x.data_ptr(), ld_x, tokens, out.data_ptr(), ld_y, code,
+                                      _raw_stream(stream, x))
+    if rc:
+        raise QzError(rc, name)
+    return out
 
 
 def linear(x, weight: Weight, out_dtype=None, out=None, stream=None):
     """y = x W^T (qz_linear): x bf16 [tokens, cols] -> [tokens, rows] in out_dtype (bf16 by
     default, or fp32)."""
-    torch = _torch()
-    ld_x = _matrix(x, weight.cols, torch.bfloat16, "x")
-    tokens = x.shape[0]
-    if out is None:
-        out = torch.empty((tokens, weight.rows), dtype=out_dtype or torch.bfloat16, device=x.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError("out has another dtype than out_dtype")
-    ld_y = _matrix(out, weight.rows, out.dtype, "out")
-    _same_tokens(tokens, out=out)
-    _check(lib().qz_linear(weight.desc, x.data_ptr(), ld_x, tokens, out.data_ptr(), ld_y,
-                           _dtype_code(out.dtype), _raw_stream(stream, x.device)), "qz_linear")
-    return out
+    return _linear_call("qz_linear", x, weight.cols, weight, weight.rows, out_dtype, out, stream, "x")
 
 
 def linear_backward(dy, weight: Weight, out_dtype=None, out=None, stream=None):
     """dx = dy W (qz_linear_backward): dy bf16 [tokens, rows] -> [tokens, cols]."""
-    torch = _torch()
-    ld_dy = _matrix(dy, weight.rows, torch.bfloat16, "dy")
-    tokens = dy.shape[0]
-    if out is None:
-        out = torch.empty((tokens, weight.cols), dtype=out_dtype or torch.bfloat16, device=dy.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError("out has another dtype than out_dtype")
-    ld_dx = _matrix(out, weight.cols, out.dtype, "out")
-    _same_tokens(tokens, out=out)
-    _check(lib().qz_linear_backward(weight.desc, dy.data_ptr(), ld_dy, tokens, out.data_ptr(),
-                                    ld_dx, _dtype_code(out.dtype), _raw_stream(stream, dy.device)),
-           "qz_linear_backward")
-    return out
+    return _linear_call("qz_linear_backward", dy, weight.rows, weight, weight.cols, out_dtype, out, stream, "dy")
 
 
 def _activation(a) -> int:
@@ -641,47 +646,54 @@ def gated_ffn(x, gate: Weight, up: Weight, activation="silu", save: bool = False
     """h = act(x gate^T) * (x up^T) (qz_gated_ffn): x bf16 [tokens, cols] -> h bf16 [tokens,
     rows]; with ``save`` also the bf16 pre-activations, (h, g, u).  out: h, or (h, g, u) with
     ``save``."""
-    torch = _torch()
-    ld_x = _matrix(x, gate.cols, torch.bfloat16, "x")
+    bf = _torch().bfloat16
+    ld_x = _matrix(x, gate.cols, bf, "x")
     tokens, rows = x.shape[0], gate.rows
+    g = u = None
+    ld_gu = rows
     if out is None:
-        out = [torch.empty((tokens, rows), dtype=torch.bfloat16, device=x.device)
-               for _ in range(3 if save else 1)]
+        h, ld_h = x.new_empty((tokens, rows)), rows
+        if save:
+            g, u = x.new_empty((tokens, rows)), x.new_empty((tokens, rows))
     else:
-        out = list(out) if save else [out]
-    lds = [_matrix(t, rows, torch.bfloat16, "out") for t in out]
-    for t in out:
-        _same_tokens(tokens, out=t)
-    if save and lds[1] != lds[2]:
-        raise ValueError("g and u must have the same leading dimension")
-    g, u = (out[1].data_ptr(), out[2].data_ptr()) if save else (None, None)
-    _check(lib().qz_gated_ffn(gate.desc, up.desc, _activation(activation), x.data_ptr(), ld_x,
-                              tokens, out[0].data_ptr(), lds[0], g, u, lds[-1],
-                              _raw_stream(stream, x.device)), "qz_gated_ffn")
-    return tuple(out) if save else out[0]
+        h, g, u = out if save else (out, None, None)
+        ld_h = _matrix(h, rows, bf, "out")
+        _same_tokens(tokens, out=h)
+        if save:
+            ld_gu, ld_u = _matrix(g, rows, bf, "g"), _matrix(u, rows, bf, "u")
+            _same_tokens(tokens, g=g, u=u)
+            if ld_gu != ld_u and tokens > 1:
+                raise ValueError("g and u must have the same leading dimension")
+    rc = (_lib or lib()).qz_gated_ffn(gate.desc, up.desc, _activation(activation), x.data_ptr(), ld_x,
+                                      tokens, h.data_ptr(), ld_h, _ptr(g), _ptr(u), ld_gu,
+                                      _raw_stream(stream, x))
+    if rc:
+        raise QzError(rc, "qz_gated_ffn")
+    return (h, g, u) if save else h
 
 
 def gated_ffn_backward(dh, g, u, gate: Weight, up: Weight, activation="silu", out=None,
                        stream=None):
     """The gradients of gated_ffn from its kept pre-activations (qz_gated_ffn_backward):
     (dx [tokens, cols], dg, du [tokens, rows]), all bf16.  out: the three, in that order."""
-    torch = _torch()
-    bf = torch.bfloat16
+    bf = _torch().bfloat16
     rows, cols, tokens = gate.rows, gate.cols, dh.shape[0]
-    ld_dh, ld_g, ld_u = (_matrix(t, rows, bf, w) for t, w in ((dh, "dh"), (g, "g"), (u, "u")))
+    ld_dh, ld_g, ld_u = _matrix(dh, rows, bf, "dh"), _matrix(g, rows, bf, "g"), _matrix(u, rows, bf, "u")
     if out is None:
-        out = (torch.empty((tokens, cols), dtype=bf, device=dh.device),
-               torch.empty((tokens, rows), dtype=bf, device=dh.device),
-               torch.empty((tokens, rows), dtype=bf, device=dh.device))
-    dx, dg, du = out
-    ld_dx, ld_dg, ld_du = _matrix(dx, cols, bf, "dx"), _matrix(dg, rows, bf, "dg"), _matrix(du, rows, bf, "du")
-    _same_tokens(tokens, g=g, u=u, dx=dx, dg=dg, du=du)
-    if ld_g != ld_u or ld_dg != ld_du:
+        dx, dg, du = dh.new_empty((tokens, cols)), dh.new_empty((tokens, rows)), dh.new_empty((tokens, rows))
+        ld_dx, ld_dg, ld_du = cols, rows, rows
+        _same_tokens(tokens, g=g, u=u)
+    else:
+        dx, dg, du = out
+        ld_dx, ld_dg, ld_du = _matrix(dx, cols, bf, "dx"), _matrix(dg, rows, bf, "dg"), _matrix(du, rows, bf, "du")
+        _same_tokens(tokens, g=g, u=u, dx=dx, dg=dg, du=du)
+    if tokens > 1 and (ld_g != ld_u or ld_dg != ld_du):
         raise ValueError("g and u, and dg and du, must have the same leading dimension")
-    _check(lib().qz_gated_ffn_backward(gate.desc, up.desc, _activation(activation), dh.data_ptr(),
-                                       ld_dh, g.data_ptr(), u.data_ptr(), ld_g, tokens,
-                                       dg.data_ptr(), du.data_ptr(), ld_dg, dx.data_ptr(), ld_dx,
-                                       _raw_stream(stream, dh.device)), "qz_gated_ffn_backward")
+    rc = (_lib or lib()).qz_gated_ffn_backward(gate.desc, up.desc, _activation(activation), dh.data_ptr(), ld_dh,
+                                               g.data_ptr(), u.data_ptr(), ld_g, tokens, dg.data_ptr(),
+                                               du.data_ptr(), ld_dg, dx.data_ptr(), ld_dx, _raw_stream(stream, dh))
+    if rc:
+        raise QzError(rc, "qz_gated_ffn_backward")
     return dx, dg, du
 
 
@@ -698,22 +710,25 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
     """Layer norm over the rows of a 2-D bf16 / fp32 CUDA tensor (qz_layer_norm).  weight, bias:
     fp32 [cols] or None.  Returns (y, mean, rstd); mean and rstd, fp32 [rows], are what
     layer_norm_backward takes.  out: the three, in that order."""
-    torch = _torch()
     dt = _dtype_code(x.dtype)
     if x.dim() != 2:
         raise ValueError("2-D tensors only")
     rows, cols = x.shape
     ld_x = _matrix(x, cols, x.dtype, "x")
     if out is None:
-        stats = torch.empty((2, rows), dtype=torch.float32, device=x.device)
-        out = (torch.empty((rows, cols), dtype=x.dtype, device=x.device), stats[0], stats[1])
-    y, mean, rstd = out
-    ld_y = _matrix(y, cols, x.dtype, "y")
-    _same_tokens(rows, y=y)
-    _check(lib().qz_layer_norm(dt, x.data_ptr(), ld_x, rows, cols, _vector(weight, cols, "weight"),
-                               _vector(bias, cols, "bias"), eps, y.data_ptr(), ld_y,
-                               _vector(mean, rows, "mean"), _vector(rstd, rows, "rstd"),
-                               _raw_stream(stream, x.device)), "qz_layer_norm")
+        f32 = _torch().float32
+        y, mean, rstd = x.new_empty((rows, cols)), x.new_empty((rows,), dtype=f32), x.new_empty((rows,), dtype=f32)
+        ld_y, pm, pr = cols, mean.data_ptr(), rstd.data_ptr()
+    else:
+        y, mean, rstd = out
+        ld_y = _matrix(y, cols, x.dtype, "y")
+        _same_tokens(rows, y=y)
+        pm, pr = _vector(mean, rows, "mean"), _vector(rstd, rows, "rstd")
+    rc = (_lib or lib()).qz_layer_norm(dt, x.data_ptr(), ld_x, rows, cols, _vector(weight, cols, "weight"),
+                                       _vector(bias, cols, "bias"), eps, y.data_ptr(), ld_y, pm, pr,
+                                       _raw_stream(stream, x))
+    if rc:
+        raise QzError(rc, "qz_layer_norm")
     return y, mean, rstd
 
 
@@ -722,30 +737,33 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, params: bool = True, out
     """The gradients of layer_norm (qz_layer_norm_backward): (dx, dweight, dbias), the last two
     fp32 [cols], or None without ``params``.  out: the three, in that order.  workspace: a uint8
     CUDA tensor of qz_layer_norm_backward_workspace(rows, cols) bytes."""
-    torch = _torch()
     dt = _dtype_code(x.dtype)
     if x.dim() != 2:
         raise ValueError("2-D tensors only")
     rows, cols = x.shape
     ld_x, ld_dy = _matrix(x, cols, x.dtype, "x"), _matrix(dy, cols, x.dtype, "dy")
+    L = _lib or lib()
+    f32 = _torch().float32
+    dw = db = None
     if out is None:
-        dx = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-        dw, db = torch.empty((2, cols), dtype=torch.float32, device=x.device) if params else (None, None)
+        dx, ld_dx = x.new_empty((rows, cols)), cols
+        if params:
+            dw, db = x.new_empty((cols,), dtype=f32), x.new_empty((cols,), dtype=f32)
+        _same_tokens(rows, dy=dy)
     else:
-        dx, dw, db = out
-    ld_dx = _matrix(dx, cols, x.dtype, "dx")
-    _same_tokens(rows, dy=dy, dx=dx)
-    need = 0
+        dx, dw, db = out if params else (out[0], None, None)
+        ld_dx = _matrix(dx, cols, x.dtype, "dx")
+        _same_tokens(rows, dy=dy, dx=dx)
+    ws = None
     if params:
-        need = lib().qz_layer_norm_backward_workspace(rows, cols)
         if workspace is None:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=x.device)
-        need = workspace.numel() * workspace.element_size()
-    _check(lib().qz_layer_norm_backward(
+            workspace = x.new_empty((L.qz_layer_norm_backward_workspace(rows, cols),), dtype=_torch().uint8)
+        ws = workspace.data_ptr()
+    rc = L.qz_layer_norm_backward(
         dt, dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, rows, cols, _vector(mean, rows, "mean"),
         _vector(rstd, rows, "rstd"), _vector(weight, cols, "weight"), dx.data_ptr(), ld_dx,
-        _vector(dw, cols, "dweight") if params else None,
-        _vector(db, cols, "dbias") if params else None,
-        workspace.data_ptr() if params else None, need, _raw_stream(stream, x.device)),
-        "qz_layer_norm_backward")
+        _vector(dw, cols, "dweight"), _vector(db, cols, "dbias"), ws,
+        workspace.numel() * workspace.element_size() if params else 0, _raw_stream(stream, x))
+    if rc:
+        raise QzError(rc, "qz_layer_norm_backward")
     return dx, dw, db

@@ -92,6 +92,30 @@ struct RowRegs {
   }
 };
 
+// The parameters of this thread's columns (`dflt` where there are none, and past the row's end), in
+// 16-byte loads where the row's chunks allow them.
+template <int E, int TPR>
+__device__ __forceinline__ void load_params(float (&w)[kPer], const float* base, float dflt, int l, int cols) {
+  if constexpr (E == 1) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int c = j * TPR + l;
+      w[j] = base && c < cols ? __ldg(base + c) : dflt;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPer; j += 4) {
+      const int c = E * ((j / E) * TPR + l) + j % E;
+      float4 v = make_float4(dflt, dflt, dflt, dflt);
+      if (base && c < cols) v = __ldg(reinterpret_cast<const float4*>(base + c));
+      w[j] = v.x;
+      w[j + 1] = v.y;
+      w[j + 2] = v.z;
+      w[j + 3] = v.w;
+    }
+  }
+}
+
 // Sums of (a, b) over the TPR threads of a row: shuffles, then the warps' sums through shared
 // memory behind a barrier of the row's threads alone (number 1 + group).  `buf` alternates, so
 // the next row's sums need no second barrier.
@@ -146,14 +170,11 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_forward_kernel(con
     if (a.mean) a.mean[row] = mean;
     if (a.rstd) a.rstd[row] = rstd;
   }
-  float y[kPer];
+  float y[kPer], w[kPer], b[kPer];
+  load_params<E, TPR>(w, a.weight, 1.0f, l, cols);
+  load_params<E, TPR>(b, a.bias, 0.0f, l, cols);
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int c = R::template column<TPR>(j, l);
-    const bool in = c < cols;
-    const float w = in && a.weight ? __ldg(a.weight + c) : 1.0f, b = in && a.bias ? __ldg(a.bias + c) : 0.0f;
-    y[j] = __fmaf_rn((x.get(j) - mean) * rstd, w, b);
-  }
+  for (int j = 0; j < kPer; ++j) y[j] = __fmaf_rn((x.get(j) - mean) * rstd, w[j], b[j]);
   R::template store<TPR>(a.y, row * a.ld_y, l, cols, y);
 }
 
@@ -167,13 +188,8 @@ __global__ void __launch_bounds__(TPR < 512 ? 512 : TPR) norm_backward_kernel(co
   __shared__ float2 sums[G][2][TPR > 32 ? TPR / 32 : 1];
   const int group = threadIdx.x / TPR, l = threadIdx.x % TPR, cols = static_cast<int>(a.cols);
   const float inv = 1.0f / static_cast<float>(cols);
-  float w[kPer], dw[kPer], db[kPer];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int c = R::template column<TPR>(j, l);
-    w[j] = c < cols && a.weight ? __ldg(a.weight + c) : 1.0f;
-    dw[j] = db[j] = 0.0f;
-  }
+  float w[kPer], dw[kPer] = {}, db[kPer] = {};
+  load_params<E, TPR>(w, a.weight, 1.0f, l, cols);
   const int64_t step = static_cast<int64_t>(gridDim.x) * G;
   int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
   R x, dy;
@@ -369,7 +385,7 @@ template <int DT>
 qz_status run_norm(const NormArgs& a, bool backward, int parts, cudaStream_t s) {
   constexpr int E = DT == QZ_BF16 ? 8 : 4;
   if (a.cols <= kMaxHeld) {
-    const bool vec = a.cols % E == 0 && a.ld_x % E == 0 && a.ld_y % E == 0 && a.ld_dy % E == 0 && aligned(a.x, 16) &&
+    const bool vec = aligned(a.weight, 16) && aligned(a.bias, 16) && a.cols % E == 0 && a.ld_x % E == 0 && a.ld_y % E == 0 && a.ld_dy % E == 0 && aligned(a.x, 16) &&
                      aligned(a.y, 16) && aligned(a.dy, 16);
     return vec ? run_held<DT, E>(a, backward, parts, s) : run_held<DT, 1>(a, backward, parts, s);
   }
