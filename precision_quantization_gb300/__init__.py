@@ -608,10 +608,10 @@ def _linear_call(name: str, x, width: int, weight: Weight, out_width: int, out_d
     tokens = x.shape[0]
     if out is None:
         if out_dtype is None or out_dtype is bf:
-            out, code = x.new_empty((tokens, out_width)), QZ_BF16
+            out, code = torch.empty((tokens, out_width), dtype=bf, device=x.device), QZ_BF16
         else:
             code = _dtype_code(out_dtype)
-            out = x.new_empty((tokens, out_width), dtype=out_dtype)
+            out = torch.empty((tokens, out_width), dtype=out_dtype, device=x.device)
         ld_y = out_width
     else:
         if out_dtype is not None and out.dtype != out_dtype:
@@ -646,15 +646,16 @@ def gated_ffn(x, gate: Weight, up: Weight, activation="silu", save: bool = False
     """h = act(x gate^T) * (x up^T) (qz_gated_ffn): x bf16 [tokens, cols] -> h bf16 [tokens,
     rows]; with ``save`` also the bf16 pre-activations, (h, g, u).  out: h, or (h, g, u) with
     ``save``."""
-    bf = _torch().bfloat16
+    torch = _torch()
+    bf, empty = torch.bfloat16, torch.empty
     ld_x = _matrix(x, gate.cols, bf, "x")
     tokens, rows = x.shape[0], gate.rows
     g = u = None
     ld_gu = rows
     if out is None:
-        h, ld_h = x.new_empty((tokens, rows)), rows
+        h, ld_h = empty((tokens, rows), dtype=bf, device=x.device), rows
         if save:
-            g, u = x.new_empty((tokens, rows)), x.new_empty((tokens, rows))
+            g, u = (empty((tokens, rows), dtype=bf, device=x.device) for _ in range(2))
     else:
         h, g, u = out if save else (out, None, None)
         ld_h = _matrix(h, rows, bf, "out")
@@ -676,11 +677,12 @@ def gated_ffn_backward(dh, g, u, gate: Weight, up: Weight, activation="silu", ou
                        stream=None):
     """The gradients of gated_ffn from its kept pre-activations (qz_gated_ffn_backward):
     (dx [tokens, cols], dg, du [tokens, rows]), all bf16.  out: the three, in that order."""
-    bf = _torch().bfloat16
+    torch = _torch()
+    bf, empty = torch.bfloat16, torch.empty
     rows, cols, tokens = gate.rows, gate.cols, dh.shape[0]
     ld_dh, ld_g, ld_u = _matrix(dh, rows, bf, "dh"), _matrix(g, rows, bf, "g"), _matrix(u, rows, bf, "u")
     if out is None:
-        dx, dg, du = dh.new_empty((tokens, cols)), dh.new_empty((tokens, rows)), dh.new_empty((tokens, rows))
+        dx, dg, du = (empty((tokens, n), dtype=bf, device=dh.device) for n in (cols, rows, rows))
         ld_dx, ld_dg, ld_du = cols, rows, rows
         _same_tokens(tokens, g=g, u=u)
     else:
@@ -716,8 +718,10 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
     rows, cols = x.shape
     ld_x = _matrix(x, cols, x.dtype, "x")
     if out is None:
-        f32 = _torch().float32
-        y, mean, rstd = x.new_empty((rows, cols)), x.new_empty((rows,), dtype=f32), x.new_empty((rows,), dtype=f32)
+        torch = _torch()
+        f32, empty, dev = torch.float32, torch.empty, x.device
+        y = empty((rows, cols), dtype=x.dtype, device=dev)
+        mean, rstd = empty((rows,), dtype=f32, device=dev), empty((rows,), dtype=f32, device=dev)
         ld_y, pm, pr = cols, mean.data_ptr(), rstd.data_ptr()
     else:
         y, mean, rstd = out
@@ -743,12 +747,13 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, params: bool = True, out
     rows, cols = x.shape
     ld_x, ld_dy = _matrix(x, cols, x.dtype, "x"), _matrix(dy, cols, x.dtype, "dy")
     L = _lib or lib()
-    f32 = _torch().float32
+    torch = _torch()
+    f32, empty, dev = torch.float32, torch.empty, x.device
     dw = db = None
     if out is None:
-        dx, ld_dx = x.new_empty((rows, cols)), cols
+        dx, ld_dx = empty((rows, cols), dtype=x.dtype, device=dev), cols
         if params:
-            dw, db = x.new_empty((cols,), dtype=f32), x.new_empty((cols,), dtype=f32)
+            dw, db = empty((cols,), dtype=f32, device=dev), empty((cols,), dtype=f32, device=dev)
         _same_tokens(rows, dy=dy)
     else:
         dx, dw, db = out if params else (out[0], None, None)
@@ -757,7 +762,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, params: bool = True, out
     ws = None
     if params:
         if workspace is None:
-            workspace = x.new_empty((L.qz_layer_norm_backward_workspace(rows, cols),), dtype=_torch().uint8)
+            workspace = empty((L.qz_layer_norm_backward_workspace(rows, cols),), dtype=torch.uint8, device=dev)
         ws = workspace.data_ptr()
     rc = L.qz_layer_norm_backward(
         dt, dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, rows, cols, _vector(mean, rows, "mean"),

@@ -68,18 +68,8 @@ __device__ __forceinline__ bool few_elect() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
   return e != 0;
 }
-__device__ __forceinline__ uint4 lds4(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds1(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -89,18 +79,14 @@ __device__ __forceinline__ uint32_t mulh(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// a word's 8 weights as f16 pairs (2 q, 2 q + 1): E2M1 values, or INT4 integers
+// a word's 8 weights as four f16 pairs: E2M1 values (2 q, 2 q + 1), or INT4 integers (q, q + 4)
 template <int FMT>
 __device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&v)[4]) {
   if constexpr (FMT == QZ_INT4) {
-    const uint32_t t0 = w & 0x0F0F0F0Fu, t1 = (w >> 4) & 0x0F0F0F0Fu;
+    // pairs (q, q + 4): f16 1024 + (n ^ 8), less 1032, is the two's complement value, exactly
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t d;  // byte q's nibbles at bits 0 and 16 (selector 8: the sign of byte 0, which is 0)
-      asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(t0), "r"(t1), "r"(0x8080u | q | ((4u + q) << 8)));
-      // f16 1024 + (n ^ 8), less 1032: the two's complement value, exactly
-      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[q]) : "r"(d ^ 0x64086408u), "r"(0x64086408u));
-    }
+    for (int q = 0; q < 4; ++q)
+      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[q]) : "r"(((w >> (4 * q)) & 0x000F000Fu) ^ 0x64086408u), "r"(0x64086408u));
   } else {
     asm("{\n\t.reg .b8 b<4>;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
         "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
@@ -156,7 +142,8 @@ __global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_con
   const ProductArgs& p = a.p;
   const int depth = a.depth;
   uint8_t* few_smem = few_raw + ((1024u - (smem_addr(few_raw) & 1023u)) & 1023u);  // swizzled boxes: 1 KiB
-  const uint32_t ring = smem_addr(few_smem) + warp * (depth * kSlot);
+  const uint8_t* mine_ring = few_smem + warp * (depth * kSlot);
+  const uint32_t ring = smem_addr(mine_ring);
   float* join = reinterpret_cast<float*>(few_smem + W * depth * kSlot);
   uint8_t* xs = few_smem + W * (depth * kSlot + kJoin * 4);
   // ks warps share a tile; gated: ks more have the same outputs of the second weight
@@ -253,6 +240,13 @@ __global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_con
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[q]) : "f"(__uint_as_float(w[q] & 0xffff0000u) * f), "f"(__uint_as_float(w[q] << 16) * f));
+        if constexpr (FMT == QZ_INT4) {  // values 0 .. 7 in the order of the weights' pairs
+          const uint32_t e[4] = {o[0], o[1], o[2], o[3]};
+          o[0] = __byte_perm(e[0], e[2], 0x5410);
+          o[1] = __byte_perm(e[0], e[2], 0x7632);
+          o[2] = __byte_perm(e[1], e[3], 0x5410);
+          o[3] = __byte_perm(e[1], e[3], 0x7632);
+        }
         if (c < per_token)
           *reinterpret_cast<uint4*>(xs + ((c >> 2) * tokens + tok) * 64 + (c & 3) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
       }
@@ -261,9 +255,9 @@ __global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_con
   __syncthreads();
   if (!busy) return;  // (fewer tiles than warps to share them; no barrier of the whole CTA follows)
   // this lane's B operand: token 8 nt + g (the last again past the end: its columns are not stored)
-  uint32_t xa[NT];
+  const uint8_t* xa[NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) xa[nt] = smem_addr(xs) + min(8 * nt + g, tokens - 1) * 64 + 16 * t;
+  for (int nt = 0; nt < NT; ++nt) xa[nt] = xs + min(8 * nt + g, tokens - 1) * 64 + 16 * t;
   const uint32_t x_chunk = 64u * tokens;
 
   // scales of rows g and g + 8, one step ahead
@@ -300,7 +294,7 @@ __global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_con
       few_wait(full + 8u * ci, cph, &s_abort);
       __syncwarp();  // the slot before is read by every lane
       issue();
-      const uint32_t slot = ring + ci * kSlot + word;
+      const uint8_t* slot = mine_ring + ci * kSlot + word;
       if (++ci == depth) {
         ci = 0;
         cph ^= 1u;
@@ -350,12 +344,12 @@ __global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_con
       for (int c = 0; c < 8; ++c) {  // chunk c: 32 columns, lane t its word t
         uint4 xv[NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) xv[nt] = lds4(xa[nt] + x0 + c * x_chunk);
+        for (int nt = 0; nt < NT; ++nt) xv[nt] = *reinterpret_cast<const uint4*>(xa[nt] + x0 + c * x_chunk);
         uint32_t v[2][4];
         float f[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          decode_word<FMT>(lds1(slot + 1024 * h + ((c ^ g) << 4)), v[h]);
+          decode_word<FMT>(*reinterpret_cast<const uint32_t*>(slot + 1024 * h + ((c ^ g) << 4)), v[h]);
           if constexpr (FMT == QZ_NVFP4) {
             const uint32_t both = __byte_perm(now[h].v[c >> 1], 0, (c & 1) ? 0x3232 : 0x1010);
 #pragma unroll
@@ -465,11 +459,20 @@ qz_status run_few_nt(FewArgs& a, cudaStream_t s) {
   const ProductArgs& p = a.p;
   const int nt = static_cast<int>((p.tokens + 7) / 8), sms = sm_count();
   constexpr int kWeights = GATED ? 2 : 1;
-  // a tile takes all of a CTA's warps while the SMs have a tile each at most, else half of them at
-  // most (a shorter join); every warp has a step
-  a.ks = (a.tiles <= sms ? W : W / 2) / kWeights;
-  while (a.ks > a.steps) a.ks /= 2;
-  a.groups = std::max(1, std::min({W / (a.ks * kWeights), (a.tiles + sms - 1) / sms, 15}));  // 15 named barriers
+  // Warps per tile: the fewest steps one after the other, a join and its barriers counted as half
+  // a step; every warp has a step, and a CTA's teams have 15 named barriers.
+  double best = 1e30;
+  for (int ks = W / kWeights; ks >= 1; ks /= 2) {
+    if (ks > a.steps) continue;
+    const int groups = std::max(1, std::min({W / (ks * kWeights), (a.tiles + sms - 1) / sms, 15}));
+    const int64_t rounds = (a.tiles + static_cast<int64_t>(groups) * sms - 1) / (static_cast<int64_t>(groups) * sms);
+    const double cost = static_cast<double>(rounds) * ((a.steps + ks - 1) / ks + 0.5 * nt);
+    if (cost < best) {
+      best = cost;
+      a.ks = ks;
+      a.groups = groups;
+    }
+  }
   a.depth = few_depth(p);
   switch (nt) {
     case 1: return run_few<FMT, 1, GATED>(a, s);
