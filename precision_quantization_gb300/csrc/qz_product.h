@@ -26,10 +26,26 @@ struct ProductArgs {
   int64_t ld_gu;
 };
 
-// The streaming kernels for up to kFewTokens tokens (qz_product_few.cu).
+// The streaming kernels for up to kFewTokens tokens (qz_product_few.cuh): their shared memory is a ring
+// of code boxes and a buffer of partial sums per warp, and the activations.
 constexpr int kFewTokens = 32;
+constexpr int kFewWarps = 16;
+constexpr int kTokenStride = 20;                  // floats of a token's 16 sums (banks 8 t + g)
+constexpr uint32_t kSlot = 2048;                  // a step: 16 rows x 128 bytes of codes
+constexpr uint32_t kJoin = 8 * kTokenStride;      // floats of a warp's sums for 8 tokens
+constexpr int kMaxDepth = 6;
+constexpr uint32_t kFewSmem = 225 * 1024;         // dynamic; the barriers are static
+constexpr uint32_t few_fixed(int depth) { return kFewWarps * (depth * kSlot + kJoin * 4) + 1024; }
+// the deepest ring that leaves room for the activations, 0: none does
+inline int few_depth(const ProductArgs& p) {
+  for (int d = kMaxDepth; d >= 2; --d)
+    if (few_fixed(d) + p.tokens * p.cols * 2 <= kFewSmem) return d;
+  return 0;
+}
 bool product_few_applicable(const ProductArgs& p);
-qz_status launch_product_few(const ProductArgs& p, cudaStream_t s);
+qz_status launch_product_few_mxfp4(const ProductArgs& p, cudaStream_t s);
+qz_status launch_product_few_nvfp4(const ProductArgs& p, cudaStream_t s);
+qz_status launch_product_few_int4(const ProductArgs& p, cudaStream_t s);
 
 // The tcgen05 kernels (qz_product_tc.cuh): applicable when cols % 32 == 0 and codes, activations
 // and their rows are 16-byte aligned.

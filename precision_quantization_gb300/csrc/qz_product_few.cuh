@@ -1,5 +1,6 @@
-// qz_product_few.cu -- products of a few tokens (decoding, small batches) with 4-bit weights:
-//   y[t][r] = sum_c W[r][c] x[t][c]        (one weight, or gate and up with the activation)
+// qz_product_few.cuh -- products of a few tokens (decoding, small batches) with 4-bit weights
+// (included once per weight format):
+//   y[t][r] = sum_c kFewWarps[r][c] x[t][c]        (one weight, or gate and up with the activation)
 //
 // Every weight is used once per token, so the weights' 4 bits (and scales) are the traffic and HBM
 // the bound; what has to fit beside the traffic is the decoding: at HBM speed an SM has about 22
@@ -18,6 +19,8 @@
 // (one per SM) are persistent over the tiles.  A warp streams 256 columns of its 16 rows a step
 // (whole 128-byte lines) through a ring of its own by TMA and runs on into the next tile, so the
 // copies never pause; a step's scales are loaded into registers one step ahead.
+#pragma once
+
 #include <cuda.h>  // CUtensorMap and its enumerators (types only; the encoder is looked up)
 #include <cudaTypedefs.h>
 
@@ -33,9 +36,6 @@
 namespace qz {
 namespace {
 
-constexpr int W = 16;                   // warps per CTA
-constexpr int kTokenStride = 20;        // floats of a token's 16 sums in the join (banks 8 t + g)
-constexpr uint32_t kFewSmem = 227 * 1024;
 constexpr float kShift = 0x1p-64f;      // the sums' unit once a scale above 2^64 (INT4 2^73) has been met
 
 struct FewArgs {
@@ -100,42 +100,37 @@ __device__ __forceinline__ float pow2(int e) {  // 2^e as fp32, e in [-149, 127]
 }
 
 // The scales of a weight row's 256 columns of a step, in the words they are stored in: eight E8M0
-// bytes, sixteen E4M3 bytes, or eight fp32 (one per 32 columns, groups of 64 and 128 repeated).
-template <int FMT>
+// bytes, sixteen E4M3 bytes, or eight, four or two fp32 (groups of 32, 64, 128: LOG = 5, 6, 7).
+template <int FMT, int LOG>
 struct StepScales {
-  static constexpr int kWords = FMT == QZ_MXFP4 ? 2 : FMT == QZ_NVFP4 ? 4 : 8;
+  static constexpr int kWords = FMT == QZ_MXFP4 ? 2 : FMT == QZ_NVFP4 ? 4 : 256 >> LOG;
   uint32_t v[kWords];
 };
-// p: the row's scales.  Straight loads without a branch: where two paths meet, the loaded registers
-// would be copied and so waited for at once.
-template <int FMT>
-__device__ __forceinline__ void load_step_scales(StepScales<FMT>& s, const uint8_t* p, int step, int log2_block) {
-  if constexpr (FMT == QZ_MXFP4) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + 8 * step));
+// p: the row's scales
+template <int FMT, int LOG>
+__device__ __forceinline__ void load_step_scales(StepScales<FMT, LOG>& s, const uint8_t* p, int step) {
+  constexpr int kWords = StepScales<FMT, LOG>::kWords;
+  p += 4 * kWords * step;
+  if constexpr (kWords == 2) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
     s.v[0] = v.x;
     s.v[1] = v.y;
-  } else if constexpr (FMT == QZ_NVFP4) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + 16 * step));
-    s.v[0] = v.x;
-    s.v[1] = v.y;
-    s.v[2] = v.z;
-    s.v[3] = v.w;
   } else {
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(p) + ((256 * step) >> log2_block);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) s.v[c] = __ldg(q + ((32 * c) >> log2_block));
+    for (int i = 0; i < kWords; i += 4) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i / 4);
+      s.v[i] = v.x;
+      s.v[i + 1] = v.y;
+      s.v[i + 2] = v.z;
+      s.v[i + 3] = v.w;
+    }
   }
 }
 
-constexpr uint32_t kSlot = 2048;                    // a step: 16 rows x 128 bytes of codes
-constexpr uint32_t kJoin = 8 * kTokenStride;        // floats of a warp's sums for 8 tokens
-constexpr uint32_t few_fixed(int depth) { return W * (depth * kSlot + kJoin * 4) + 1024; }
-constexpr int kMaxDepth = 6;
-
-template <int FMT, int NT, bool GATED>
-__global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_constant__ FewArgs a) {
+template <int FMT, int LOG, int NT, bool GATED>
+__global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __grid_constant__ FewArgs a) {
   extern __shared__ uint8_t few_raw[];
-  __shared__ __align__(8) uint64_t s_full[W][kMaxDepth];
+  __shared__ __align__(8) uint64_t s_full[kFewWarps][kMaxDepth];
   __shared__ uint32_t s_amax[8 * NT];
   __shared__ volatile int s_abort;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -144,8 +139,8 @@ __global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_con
   uint8_t* few_smem = few_raw + ((1024u - (smem_addr(few_raw) & 1023u)) & 1023u);  // swizzled boxes: 1 KiB
   const uint8_t* mine_ring = few_smem + warp * (depth * kSlot);
   const uint32_t ring = smem_addr(mine_ring);
-  float* join = reinterpret_cast<float*>(few_smem + W * depth * kSlot);
-  uint8_t* xs = few_smem + W * (depth * kSlot + kJoin * 4);
+  float* join = reinterpret_cast<float*>(few_smem + kFewWarps * depth * kSlot);
+  uint8_t* xs = few_smem + kFewWarps * (depth * kSlot + kJoin * 4);
   // ks warps share a tile; gated: ks more have the same outputs of the second weight
   constexpr int kWeights = GATED ? 2 : 1;
   const int ks = a.ks, team = ks * kWeights, group = warp / team, member = warp % team, part = member % ks;
@@ -153,7 +148,7 @@ __global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_con
   const bool busy = group < a.groups;
   const int tile0 = busy ? blockIdx.x * a.groups + group : a.tiles, tile_step = gridDim.x * a.groups;
   const int s_begin = part * a.steps / ks, s_end = (part + 1) * a.steps / ks;
-  const int rows = static_cast<int>(p.rows), cols = static_cast<int>(p.cols), tokens = static_cast<int>(p.tokens);
+  const int rows = static_cast<int>(p.rows), tokens = static_cast<int>(p.tokens);
   const uint32_t full = smem_addr(&s_full[warp][0]);
 
   if (lane == 0) {
@@ -185,71 +180,73 @@ __global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_con
 
   // ---- the activations, times 2^p, as f16: [32-wide chunk][token][32], zero past the columns ----
   {
-    constexpr int kHeld = 8, kAll = 32 * W;
+    constexpr int kHeld = 8, kAll = 32 * kFewWarps;
     // a round holds up to eight pieces of 8 values a thread, each of them kAll consecutive pieces of one token
     const int per_token = a.x_chunks * 4, blocks = (per_token + kAll - 1) / kAll, n = blocks * tokens;
     uint4 v[kHeld];
-    const auto piece = [&](int j, int& tok, int& c) {  // block j (uniform): its token, this thread's piece
-      tok = j / blocks;
-      c = (j - tok * blocks) * kAll + static_cast<int>(threadIdx.x);
-    };
-    const auto load = [&](int base) {
+    // the round's blocks one after the other: (tok, blk), uniform over the CTA
+    const auto each = [&](int base_tok, int base_blk, auto&& f) {
+      int tok = base_tok, blk = base_blk;
 #pragma unroll
       for (int i = 0; i < kHeld; ++i) {
-        int tok, c;
-        piece(base + i, tok, c);
-        v[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (base + i < n && 8 * c < cols) v[i] = __ldg(reinterpret_cast<const uint4*>(p.x0 + tok * p.ld_x) + c);
-      }
-    };
-    for (int base = 0; base < n; base += kHeld) {
-      load(base);
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        if (base + i >= n) break;
-        int tok, c;
-        piece(base + i, tok, c);
-        const uint32_t w[4] = {v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu, v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu};
-        const uint32_t m2 = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
-        uint32_t m = max(m2 & 0xffffu, m2 >> 16);
-        if (m >= 0x7f80u) {  // the largest finite magnitude
-          m = 0u;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t lo = w[q] & 0xffffu, hi = w[q] >> 16;
-            m = max(m, max(hi < 0x7f80u ? hi : 0u, lo < 0x7f80u ? lo : 0u));
-          }
+        if (tok >= tokens) break;
+        f(i, tok, blk * kAll + static_cast<int>(threadIdx.x));
+        if (++blk == blocks) {
+          blk = 0;
+          ++tok;
         }
-        m = __reduce_max_sync(kFull, m);
-        if (lane == 0) atomicMax(&s_amax[tok], m << 16);
       }
+    };
+    const auto load = [&](int i, int tok, int c) {
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (c < per_token) v[i] = __ldg(reinterpret_cast<const uint4*>(p.x0 + tok * p.ld_x) + c);
+    };
+    const auto magnitude = [&](int i, int tok, int) {
+      const uint32_t w[4] = {v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu, v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu};
+      const uint32_t m2 = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+      uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+      if (m >= 0x7f80u) {  // the largest finite magnitude
+        m = 0u;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t lo = w[q] & 0xffffu, hi = w[q] >> 16;
+          m = max(m, max(hi < 0x7f80u ? hi : 0u, lo < 0x7f80u ? lo : 0u));
+        }
+      }
+      m = __reduce_max_sync(kFull, m);
+      if (lane == 0) atomicMax(&s_amax[tok], m << 16);
+    };
+    const auto convert = [&](int i, int tok, int c) {
+      const uint32_t m = s_amax[tok];
+      // 2^p: 14 less the exponent of the largest magnitude, 120 at most
+      const float f = pow2(m == 0u ? 0 : min(120, 14 + 127 - static_cast<int>(m >> 23)));
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[q]) : "f"(__uint_as_float(w[q] & 0xffff0000u) * f), "f"(__uint_as_float(w[q] << 16) * f));
+      if constexpr (FMT == QZ_INT4) {  // values 0 .. 7 in the order of the weights' pairs
+        const uint32_t e[4] = {o[0], o[1], o[2], o[3]};
+        o[0] = __byte_perm(e[0], e[2], 0x5410);
+        o[1] = __byte_perm(e[0], e[2], 0x7632);
+        o[2] = __byte_perm(e[1], e[3], 0x5410);
+        o[3] = __byte_perm(e[1], e[3], 0x7632);
+      }
+      if (c < per_token)
+        *reinterpret_cast<uint4*>(xs + ((c >> 2) * tokens + tok) * 64 + (c & 3) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+    };
+    for (int base = 0, tok = 0, blk = 0; base < n; base += kHeld) {
+      each(tok, blk, load);
+      each(tok, blk, magnitude);
+      tok = (base + kHeld) / blocks;
+      blk = (base + kHeld) - tok * blocks;
     }
     __syncthreads();
-    for (int base = 0; base < n; base += kHeld) {
-      if (n > kHeld) load(base);  // else still in registers
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        if (base + i >= n) break;
-        int tok, c;
-        piece(base + i, tok, c);
-        const uint32_t m = s_amax[tok];
-        // 2^p: 14 less the exponent of the largest magnitude, 120 at most
-        const float f = pow2(m == 0u ? 0 : min(120, 14 + 127 - static_cast<int>(m >> 23)));
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-        uint32_t o[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[q]) : "f"(__uint_as_float(w[q] & 0xffff0000u) * f), "f"(__uint_as_float(w[q] << 16) * f));
-        if constexpr (FMT == QZ_INT4) {  // values 0 .. 7 in the order of the weights' pairs
-          const uint32_t e[4] = {o[0], o[1], o[2], o[3]};
-          o[0] = __byte_perm(e[0], e[2], 0x5410);
-          o[1] = __byte_perm(e[0], e[2], 0x7632);
-          o[2] = __byte_perm(e[1], e[3], 0x5410);
-          o[3] = __byte_perm(e[1], e[3], 0x7632);
-        }
-        if (c < per_token)
-          *reinterpret_cast<uint4*>(xs + ((c >> 2) * tokens + tok) * 64 + (c & 3) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-      }
+    for (int base = 0, tok = 0, blk = 0; base < n; base += kHeld) {
+      if (n > kHeld) each(tok, blk, load);  // else still in registers
+      each(tok, blk, convert);
+      tok = (base + kHeld) / blocks;
+      blk = (base + kHeld) - tok * blocks;
     }
   }
   __syncthreads();
@@ -261,7 +258,7 @@ __global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_con
   const uint32_t x_chunk = 64u * tokens;
 
   // scales of rows g and g + 8, one step ahead
-  StepScales<FMT> next[2];
+  StepScales<FMT, LOG> next[2];
   int ntile = tile0, ns = s_begin;
   const uint8_t* pr[2];
   const auto point = [&]() {
@@ -271,7 +268,7 @@ __global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_con
   };
   const auto load_next = [&]() {  // (past the last tile: its last row's again)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) load_step_scales<FMT>(next[h], pr[h], ns, p.log2_block);
+    for (int h = 0; h < 2; ++h) load_step_scales<FMT, LOG>(next[h], pr[h], ns);
     if (++ns == s_end) {
       ns = s_begin;
       ntile += tile_step;
@@ -289,7 +286,7 @@ __global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_con
     bool shifted = false;  // z is in units of 2^64 (see kShift)
 #pragma unroll 1
     for (int s = s_begin; s < s_end; ++s) {
-      StepScales<FMT> now[2] = {next[0], next[1]};
+      StepScales<FMT, LOG> now[2] = {next[0], next[1]};
       load_next();
       few_wait(full + 8u * ci, cph, &s_abort);
       __syncwarp();  // the slot before is read by every lane
@@ -321,7 +318,7 @@ __global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_con
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int i = 0; i < StepScales<FMT>::kWords; ++i) {
+          for (int i = 0; i < StepScales<FMT, LOG>::kWords; ++i) {
             if constexpr (FMT == QZ_MXFP4) {
               const uint32_t e = now[h].v[i];
               odd |= ((e - 0x01010101u) & ~e & 0x80808080u) != 0u;  // a byte 0 (and some bytes 1 above one)
@@ -340,6 +337,8 @@ __global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_con
         odd = __any_sync(kFull, odd | shifted);
       }
       const uint32_t x0 = static_cast<uint32_t>(s) * 8u * x_chunk;
+      float acc[FMT == QZ_NVFP4 ? 1 : NT][4];  // the sum of a block or group, before its scale
+      constexpr int kPer = FMT == QZ_INT4 ? 1 << (LOG - 5) : 1;  // chunks of it
 #pragma unroll
       for (int c = 0; c < 8; ++c) {  // chunk c: 32 columns, lane t its word t
         uint4 xv[NT];
@@ -362,7 +361,8 @@ __global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_con
               f[h] = b == 255u ? __uint_as_float(0x7fc00000u) : pow2(static_cast<int>(b) - 127) * (shifted ? kShift : 1.0f);
             }
           } else {
-            f[h] = __uint_as_float(now[h].v[c]) * (odd ? kShift : 1.0f);
+            f[h] = __uint_as_float(now[h].v[c / kPer]);
+            if (odd) f[h] *= kShift;
           }
         }
 #pragma unroll
@@ -371,11 +371,13 @@ __global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_con
             mma(z[nt], v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
             mma(z[nt], v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
           } else {  // the block's scale takes its sum
-            float acc[4] = {};
-            mma(acc, v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
-            mma(acc, v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
+            if (c % kPer == 0) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+            mma(acc[nt], v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
+            mma(acc[nt], v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
+            if (c % kPer == kPer - 1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) z[nt][i] = __fmaf_rn(f[i >> 1], acc[i], z[nt][i]);
+              for (int i = 0; i < 4; ++i) z[nt][i] = __fmaf_rn(f[i >> 1], acc[nt][i], z[nt][i]);
+            }
           }
         }
       }
@@ -437,24 +439,16 @@ __global__ void __launch_bounds__(32 * W, 1) product_few_kernel(const __grid_con
     }
 }
 
-int64_t x_bytes(const ProductArgs& p) { return p.tokens * p.cols * 2; }
-// the deepest ring that leaves room for the activations, 0: none does
-int few_depth(const ProductArgs& p) {
-  for (int d = kMaxDepth; d >= 2; --d)
-    if (few_fixed(d) + x_bytes(p) <= kFewSmem - 2048) return d;
-  return 0;
-}
-
-template <int FMT, int NT, bool GATED>
+template <int FMT, int LOG, int NT, bool GATED>
 qz_status run_few(const FewArgs& a, cudaStream_t s) {
-  const void* k = reinterpret_cast<const void*>(&product_few_kernel<FMT, NT, GATED>);
-  if (!set_dyn_smem(k, static_cast<int>(kFewSmem - 2048))) return QZ_ERR_CUDA;
+  const void* k = reinterpret_cast<const void*>(&product_few_kernel<FMT, LOG, NT, GATED>);
+  if (!set_dyn_smem(k, static_cast<int>(kFewSmem))) return QZ_ERR_CUDA;
   const int grid = std::min((a.tiles + a.groups - 1) / a.groups, sm_count());
-  const size_t smem = few_fixed(a.depth) + static_cast<size_t>(x_bytes(a.p));
-  product_few_kernel<FMT, NT, GATED><<<grid, 32 * W, smem, s>>>(a);
+  const size_t smem = few_fixed(a.depth) + static_cast<size_t>(a.p.tokens * a.p.cols * 2);
+  product_few_kernel<FMT, LOG, NT, GATED><<<grid, 32 * kFewWarps, smem, s>>>(a);
   return launch_status();
 }
-template <int FMT, bool GATED>
+template <int FMT, int LOG, bool GATED>
 qz_status run_few_nt(FewArgs& a, cudaStream_t s) {
   const ProductArgs& p = a.p;
   const int nt = static_cast<int>((p.tokens + 7) / 8), sms = sm_count();
@@ -462,9 +456,9 @@ qz_status run_few_nt(FewArgs& a, cudaStream_t s) {
   // Warps per tile: the fewest steps one after the other, a join and its barriers counted as half
   // a step; every warp has a step, and a CTA's teams have 15 named barriers.
   double best = 1e30;
-  for (int ks = W / kWeights; ks >= 1; ks /= 2) {
+  for (int ks = kFewWarps / kWeights; ks >= 1; ks /= 2) {
     if (ks > a.steps) continue;
-    const int groups = std::max(1, std::min({W / (ks * kWeights), (a.tiles + sms - 1) / sms, 15}));
+    const int groups = std::max(1, std::min({kFewWarps / (ks * kWeights), (a.tiles + sms - 1) / sms, 15}));
     const int64_t rounds = (a.tiles + static_cast<int64_t>(groups) * sms - 1) / (static_cast<int64_t>(groups) * sms);
     const double cost = static_cast<double>(rounds) * ((a.steps + ks - 1) / ks + 0.5 * nt);
     if (cost < best) {
@@ -475,10 +469,10 @@ qz_status run_few_nt(FewArgs& a, cudaStream_t s) {
   }
   a.depth = few_depth(p);
   switch (nt) {
-    case 1: return run_few<FMT, 1, GATED>(a, s);
-    case 2: return run_few<FMT, 2, GATED>(a, s);
-    case 3: return run_few<FMT, 3, GATED>(a, s);
-    default: return run_few<FMT, 4, GATED>(a, s);
+    case 1: return run_few<FMT, LOG, 1, GATED>(a, s);
+    case 2: return run_few<FMT, LOG, 2, GATED>(a, s);
+    case 3: return run_few<FMT, LOG, 3, GATED>(a, s);
+    default: return run_few<FMT, LOG, 4, GATED>(a, s);
   }
 }
 bool encode_codes(CUtensorMap* m, const ProductArgs& p, const WeightView& w) {
@@ -492,31 +486,24 @@ bool encode_codes(CUtensorMap* m, const ProductArgs& p, const WeightView& w) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-}  // namespace
-
-bool product_few_applicable(const ProductArgs& p) {
-  if (p.mode == kModeBackward || p.tokens > kFewTokens || p.cols == 0 || p.cols % 256 != 0) return false;
-  if (p.format == QZ_INT4 && p.log2_block < 5) return false;  // groups of 16 change inside a chunk's sum
-  if (p.rows >= (int64_t{1} << 30) || p.cols >= (int64_t{1} << 30) || few_depth(p) == 0) return false;
-  // whole steps; a step's scales are one aligned load
-  const uintptr_t n = p.format == QZ_MXFP4 ? 8 : p.format == QZ_NVFP4 ? 16 : 4;
-  const auto ok = [&](const void* q, uintptr_t a) { return reinterpret_cast<uintptr_t>(q) % a == 0; };
-  return p.ld_x % 8 == 0 && ok(p.x0, 16) && ok(p.w0.codes, 16) && ok(p.w0.scales, n) &&
-         (p.n_weights == 1 || (ok(p.w1.codes, 16) && ok(p.w1.scales, n)));
-}
-
-qz_status launch_product_few(const ProductArgs& p, cudaStream_t s) {
+template <int FMT>
+qz_status launch_few(const ProductArgs& p, cudaStream_t s) {
   FewArgs a{};
   a.p = p;
   if (!encode_codes(&a.map_w0, p, p.w0) || (p.n_weights == 2 && !encode_codes(&a.map_w1, p, p.w1))) return QZ_ERR_CUDA;
   a.tiles = static_cast<int>((p.rows + 15) / 16);
   a.steps = static_cast<int>(p.cols / 256);
   a.x_chunks = 8 * a.steps;
-  a.scale_pitch = (p.cols >> p.log2_block) * (p.format == QZ_INT4 ? 4 : 1);
+  a.scale_pitch = (p.cols >> p.log2_block) * (FMT == QZ_INT4 ? 4 : 1);
   const bool two = p.mode == kModeGated;
-  if (p.format == QZ_MXFP4) return two ? run_few_nt<QZ_MXFP4, true>(a, s) : run_few_nt<QZ_MXFP4, false>(a, s);
-  if (p.format == QZ_NVFP4) return two ? run_few_nt<QZ_NVFP4, true>(a, s) : run_few_nt<QZ_NVFP4, false>(a, s);
-  return two ? run_few_nt<QZ_INT4, true>(a, s) : run_few_nt<QZ_INT4, false>(a, s);
+  if constexpr (FMT == QZ_INT4) {
+    if (p.log2_block == 5) return two ? run_few_nt<FMT, 5, true>(a, s) : run_few_nt<FMT, 5, false>(a, s);
+    if (p.log2_block == 6) return two ? run_few_nt<FMT, 6, true>(a, s) : run_few_nt<FMT, 6, false>(a, s);
+    return two ? run_few_nt<FMT, 7, true>(a, s) : run_few_nt<FMT, 7, false>(a, s);
+  } else {
+    return two ? run_few_nt<FMT, 0, true>(a, s) : run_few_nt<FMT, 0, false>(a, s);
+  }
 }
 
+}  // namespace
 }  // namespace qz
