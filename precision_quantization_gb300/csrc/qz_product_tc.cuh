@@ -15,7 +15,7 @@
 //   decoders     three groups of four warps that take the boxes in turn: a thread turns a line's
 //                codes into bf16 and stores them in the layout the MMA reads
 //   warp 1       issues the MMAs, eight 16-wide ones a box (one thread)
-//   last four    read finished accumulators from tensor memory, apply the activation and store
+//   the rest     read finished accumulators from tensor memory, apply the activation and store
 // A box is the unit of every hand-over: a wait or a commit of the issuing thread takes some 60 to
 // 140 cycles even when nothing is to be waited for, which 64-wide steps paid twice as often.
 // Two forms.  PAIR: two CTAs on neighbouring SMs share one 256 x 256 tile (cta_group::2: each
@@ -43,7 +43,7 @@ namespace {
 
 constexpr int kBM = 128;            // outputs per CTA (MMA rows, tensor-memory lanes)
 constexpr int kBK = 64;             // summands per step: 128 bytes of bf16, one swizzle row
-constexpr int kDecWarp0 = 4, kEpiWarps = 4;
+constexpr int kDecWarp0 = 4;
 constexpr uint32_t kABytes = kBM * kBK * 2;        // 16 KiB of decoded weights
 constexpr uint32_t kTmemCols = 512;                // two accumulators of 256 columns
 constexpr uint64_t kTcWaitNs = 1000000000ull;      // 1 s: far beyond any step's latency
@@ -61,6 +61,9 @@ struct TcFormat {
   // another on it (a parity wait could not tell the laps apart).
   static constexpr uint32_t kStageBytes = kSteps * kTerms * kABytes;  // 32 KiB
   static constexpr int kEpiWarp0 = kDecWarp0 + 4 * kGroups;
+  // Eight epilogue warps (a tile's columns in two halves) where a box is 128 summands; INT4's MMAs
+  // take twice as long per tile.
+  static constexpr int kEpiWarps = FMT == QZ_INT4 ? 4 : 8;
   static constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 };
 constexpr uint32_t kSmemMax = 227 * 1024 - 2048;   // dynamic; the barriers are static
@@ -145,25 +148,25 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
         : "memory");
 }
-// 8 consecutive fp32 columns of this thread's tensor-memory lane
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
-  uint32_t r[8];
+// 8 consecutive fp32 columns of this thread's tensor-memory lane: the load, and the wait for every
+// load before it, which hands the registers on (so nothing reads them earlier)
+__device__ __forceinline__ void tmem_load8(uint32_t taddr, float (&v)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                : "r"(taddr)
                : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait8(float (&v)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])::"memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
+  tmem_load8(taddr, v);
+  tmem_wait8(v);
 }
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void sts16(uint32_t addr, const uint32_t (&v)[4]) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
-}
-__device__ __forceinline__ uint4 lds16(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
 }
 __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -337,77 +340,210 @@ __device__ __forceinline__ void decode32(const uint4 codes, const Scales<FMT>& s
 }
 
 // ---- epilogue ---------------------------------------------------------------------------------
-__device__ __forceinline__ void store_rows2(uint16_t* y, int64_t ld, int64_t t, int row, int rows, bool vec, float a, float b) {
-  uint16_t* q = y + t * ld + row;
+// Neighbouring lanes hold neighbouring outputs r of two tokens t and t' (a and b), as a bf16 pair:
+// after the exchange the even lane has both outputs of t, the odd lane both of t'.
+__device__ __forceinline__ uint32_t exchange_pair(float a, float b, bool odd) {
+  const uint32_t own = bf16x2_bits(a, b), other = __shfl_xor_sync(kFull, own, 1);
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(own), "r"(other), "r"(odd ? 0x3276u : 0x5410u));
+  return r;
+}
+__device__ __forceinline__ void store_pair(uint16_t* q, uint32_t v, int row, int rows, bool vec) {
   if (vec && row + 1 < rows) {
-    *reinterpret_cast<uint32_t*>(q) = bf16x2_bits(a, b);
+    *reinterpret_cast<uint32_t*>(q) = v;
   } else {
-    if (row < rows) q[0] = bf16_bits(a);
-    if (row + 1 < rows) q[1] = bf16_bits(b);
+    if (row < rows) q[0] = static_cast<uint16_t>(v);
+    if (row + 1 < rows) q[1] = static_cast<uint16_t>(v >> 16);
   }
 }
-// Neighbouring lanes hold neighbouring outputs of the tokens t and t + 1 (a and b): after the
-// exchange the even lane stores both outputs of t, the odd lane both of t + 1.
-__device__ __forceinline__ void store_pair(uint16_t* y, int64_t ld, int64_t t, int64_t tokens, int row, int rows, bool vec,
-                                           float a, float b, int lane) {
-  const bool odd = lane & 1;
-  const float got = __shfl_xor_sync(kFull, odd ? a : b, 1);
-  const int64_t tt = t + (odd ? 1 : 0);
-  if (tt < tokens) store_rows2(y, ld, tt, row & ~1, rows, vec, odd ? got : a, odd ? b : got);
+
+// A tile's stores: where this lane's values go, and whether every one of them is an aligned pair
+// inside the matrices (then no store is tested).
+struct StorePlan {
+  bool whole;                // of the CTA's tile and this call's columns
+  bool y_vec, gu_vec;
+  int row;                   // this lane's first output (even), or its one output (fp32)
+  uint32_t token_off;        // its token within a group of eight
+};
+template <int MODE>
+__device__ __forceinline__ StorePlan store_plan(const TcArgs& a, int m0, int quarter, int lane, int64_t t_begin, int64_t t_end) {
+  const ProductArgs& p = a.p;
+  StorePlan f;
+  f.y_vec = (reinterpret_cast<uintptr_t>(p.y) & 3u) == 0 && (p.ld_y & 1) == 0;
+  f.gu_vec = (reinterpret_cast<uintptr_t>(p.g_out) & 3u) == 0 && (reinterpret_cast<uintptr_t>(p.u_out) & 3u) == 0 && (p.ld_gu & 1) == 0;
+  const int first = MODE == kModeGated ? m0 + 16 * quarter : m0 + 32 * quarter;
+  f.whole = t_end <= p.tokens && first + (MODE == kModeGated ? 16 : 32) <= a.nout && f.y_vec && (f.gu_vec || !p.g_out);
+  if (MODE == kModeGated) {
+    f.row = first + (lane & 14);
+    f.token_off = (lane >> 4) + 2 * (lane & 1);
+  } else if (p.out_f32) {
+    f.row = first + lane;
+    f.token_off = 0;
+  } else {
+    f.row = first + (lane & 30);
+    f.token_off = lane & 1;
+  }
+  return f;
 }
 
-struct StoreFlags {
-  bool y_vec, gu_vec;
-};
-// 8 finished sums of this thread's lane, tokens t0 .. t0 + 7.  m0: first output of the CTA's tile.
-template <int FMT, int MODE>
-__device__ __forceinline__ void store8(const TcArgs& a, StoreFlags f, const float (&v)[8], float f0, float f1, int m0, int quarter,
-                                       int lane, int64_t t0) {
+// 8 finished sums of this thread's lane, tokens t0 .. t0 + 7.
+template <int MODE>
+__device__ __forceinline__ void store8(const TcArgs& a, const StorePlan& f, const float (&v)[8], float f0, float f1, int lane, int64_t t0) {
   const ProductArgs& p = a.p;
   const int64_t tokens = p.tokens;
-  if (t0 >= tokens) return;
+  const bool odd = lane & 1;
   if constexpr (MODE == kModeGated) {
     // lanes 0-15 hold gate sums, 16-31 the same outputs' up sums: each half takes one token of
-    // a pair from the other
+    // a pair from the other, so lane l ends with tokens 2 i (+ 1 in the upper half)
     const bool upper = lane >= 16;
-    const int row = m0 + 16 * quarter + (lane & 15);
-    uint16_t* y = static_cast<uint16_t*>(p.y);
     float g[4], u[4], h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float got = __shfl_xor_sync(kFull, upper ? v[2 * i] : v[2 * i + 1], 16);
       g[i] = (upper ? got : v[2 * i]) * f0;
       u[i] = (upper ? v[2 * i + 1] : got) * f1;
-      h[i] = (p.act == QZ_ACT_SILU ? act_value<QZ_ACT_SILU>(g[i]) : act_value<QZ_ACT_GELU_TANH>(g[i])) * u[i];
     }
-    // this lane now has tokens t0 + 2 i (+ 1 in the upper half); pairs of them two tokens apart
-    const bool odd = lane & 1;
+    if (p.act == QZ_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      const int64_t t = t0 + 2 * i + (upper ? 1 : 0) + (odd ? 2 : 0);
-      const auto put = [&](uint16_t* dst, int64_t ld, bool vec, const float (&w)[4]) {
-        const float got = __shfl_xor_sync(kFull, odd ? w[i] : w[i + 1], 1);
-        if (t < tokens) store_rows2(dst, ld, t, row & ~1, a.nout, vec, odd ? got : w[i], odd ? w[i + 1] : got);
-      };
-      put(y, p.ld_y, f.y_vec, h);
-      if (p.g_out) {
-        put(p.g_out, p.ld_gu, f.gu_vec, g);
-        put(p.u_out, p.ld_gu, f.gu_vec, u);
-      }
-    }
-  } else {
-    const int row = m0 + 32 * quarter + lane;
-    if (p.out_f32) {
-      float* y = static_cast<float*>(p.y) + t0 * p.ld_y + row;
-      if (row < a.nout) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (t0 + i < tokens) y[i * p.ld_y] = v[i];
-      }
+      for (int i = 0; i < 4; ++i) h[i] = act_value<QZ_ACT_SILU>(g[i]) * u[i];
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; i += 2)
-        store_pair(static_cast<uint16_t*>(p.y), p.ld_y, t0 + i, tokens, row, a.nout, f.y_vec, v[i], v[i + 1], lane);
+      for (int i = 0; i < 4; ++i) h[i] = act_value<QZ_ACT_GELU_TANH>(g[i]) * u[i];
+    }
+    const int64_t t = t0 + f.token_off;
+    const auto put = [&](uint16_t* dst, int64_t ld, bool vec, const float (&w)[4]) {
+      const uint32_t e0 = exchange_pair(w[0], w[1], odd), e1 = exchange_pair(w[2], w[3], odd);
+      uint16_t* q = dst + t * ld + f.row;
+      if (f.whole) {
+        *reinterpret_cast<uint32_t*>(q) = e0;
+        *reinterpret_cast<uint32_t*>(q + 4 * ld) = e1;
+      } else {
+        if (t < tokens) store_pair(q, e0, f.row, a.nout, vec);
+        if (t + 4 < tokens) store_pair(q + 4 * ld, e1, f.row, a.nout, vec);
+      }
+    };
+    put(static_cast<uint16_t*>(p.y), p.ld_y, f.y_vec, h);
+    if (p.g_out) {
+      put(p.g_out, p.ld_gu, f.gu_vec, g);
+      put(p.u_out, p.ld_gu, f.gu_vec, u);
+    }
+  } else if (p.out_f32) {
+    float* y = static_cast<float*>(p.y) + t0 * p.ld_y + f.row;
+    if (f.row < a.nout) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (t0 + i < tokens) y[i * p.ld_y] = v[i];
+    }
+  } else {
+    uint16_t* q = static_cast<uint16_t*>(p.y) + (t0 + f.token_off) * p.ld_y + f.row;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t e = exchange_pair(v[2 * i], v[2 * i + 1], odd);
+      if (f.whole) *reinterpret_cast<uint32_t*>(q + 2 * i * p.ld_y) = e;
+      else if (t0 + f.token_off + 2 * i < tokens) store_pair(q + 2 * i * p.ld_y, e, f.row, a.nout, f.y_vec);
+    }
+  }
+}
+
+// ---- the decoder warps -------------------------------------------------------------------------
+struct DecodeLoop {
+  int group, line, lane, first, tile_end, tile_step, bx_begin, bx_end, m_rank;
+  uint32_t a_stage, c_full, c_empty, a_empty, a_full;
+  const uint8_t* codes;
+  volatile int* abort;
+};
+// Group g of four warps takes every kGroups-th box; thread i of it line i of each: an output
+// (backward: weight row i % 64 of a step, outputs 64 (i / 64) .. + 63).  VEC: the scales of a box
+// (INT4, backward: of 64 columns) are one aligned load.  It is a parameter of the whole loop: where
+// two ways of loading met, the loaded registers would be copied and so be waited for at once.
+template <int FMT, int MODE, bool PAIR, bool VEC>
+__device__ __forceinline__ void decode_boxes(const TcArgs& a, const DecodeLoop& d) {
+  constexpr int kSteps = TcFormat<FMT>::kSteps, kBoxK = TcFormat<FMT>::kBoxK, kGroups = TcFormat<FMT>::kGroups;
+  constexpr int kTerms = TcFormat<FMT>::kTerms, kOut = MODE == kModeGated ? kBM / 2 : kBM, CG = PAIR ? 2 : 1;
+  constexpr uint32_t kBoxBytes = TcFormat<FMT>::kBoxBytes;
+  const int line = d.line, x = line & 7, cols = static_cast<int>(a.p.cols);
+  // the code box has 64-byte lines with a 64-byte swizzle, 16-byte chunk c of line l at
+  // c ^ (l / 2 % 4), or 32-byte ones (c ^ (l / 4 % 2)); a thread's chunks are 2 k and 2 k + 1 of
+  // step k (backward: of its slab), so eight lanes' 16-byte loads take different banks
+  constexpr uint32_t kLine = MODE == kModeBackward ? 64u : kBoxK / 2;
+  const int cl = MODE == kModeBackward ? line & 63 : line, cx = kLine == 64 ? (cl >> 1) & 3 : (cl >> 2) & 1;
+  const int per_tile = d.bx_end - d.bx_begin;
+  int t = d.first, bx = d.bx_begin + d.group;  // this group's box
+  int cs = d.group;
+  uint32_t aph = 0, cph = 0;
+  constexpr int kScaleBytes = FMT == QZ_INT4 ? 4 : 1;
+  const int64_t pitch = static_cast<int64_t>(a.blocks_row) * kScaleBytes;
+  const uint8_t* row_scales = nullptr;  // forward: of this thread's line in tile `row_tile` (null: outside)
+  int row_tile = -1;
+  Scales<FMT> next[kSteps] = {};
+  const auto settle = [&]() {  // a box past the tile's end: the next tiles'
+    while (t < d.tile_end && bx >= d.bx_end) {
+      bx -= per_tile;
+      t += d.tile_step;
+    }
+  };
+  const auto load_next = [&]() {  // the scales of box bx in tile t
+    const int m0 = (t / a.tiles_n) * (kOut * CG) + d.m_rank;
+    if constexpr (MODE == kModeBackward) {
+      const bool second = bx >= a.boxes_w;
+      const int row = (second ? bx - a.boxes_w : bx) * kBoxK + (line & 63), col = m0 + 64 * (line >> 6);
+      const uint8_t* base = static_cast<const uint8_t*>(second ? a.scales1 : a.scales0) + row * pitch;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+        next[k] = load_scales<FMT>(t < d.tile_end && row + 64 * k < a.nsum ? base + 64 * k * pitch : nullptr, col, cols, a.p.log2_block, VEC);
+    } else {
+      if (row_tile != t) {
+        row_tile = t;
+        const int row = MODE == kModeGated ? m0 + 16 * (line >> 5) + (line & 15) : m0 + line;
+        const void* base = MODE == kModeGated && (line & 16) ? a.scales1 : a.scales0;
+        row_scales = t < d.tile_end && row < a.nout ? static_cast<const uint8_t*>(base) + row * pitch : nullptr;
+      }
+      const int col = bx * kBoxK;
+      if constexpr (kSteps == 2 && VEC) {
+        load_scales_box<FMT>(row_scales, col, next);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) next[k] = load_scales<FMT>(row_scales, col + 64 * k, cols, a.p.log2_block, VEC);
+      }
+    }
+  };
+  settle();
+  load_next();
+  while (t < d.tile_end) {
+    Scales<FMT> now[kSteps];
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) now[k] = next[k];
+    bx += kGroups;
+    settle();
+    load_next();  // of this group's next box, in flight during this one
+    if (!__all_sync(kFull, tc_wait(d.c_full + 8u * cs, cph, d.abort) && tc_wait(d.a_empty, aph ^ 1u, d.abort))) break;
+    const uint8_t* box = d.codes + cs * kBoxBytes + kLine * cl;
+    uint4 codes[kSteps][2];
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const int c = 2 * (MODE == kModeBackward ? line >> 6 : k);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        codes[k][i] = *reinterpret_cast<const uint4*>(box + (MODE == kModeBackward ? 4096 * k : 0) + (((c + i) ^ cx) << 4));
+    }
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      const uint32_t dst = d.a_stage + k * (kTerms * kABytes) + 128u * line;
+      decode32<FMT>(codes[k][0], now[k], dst, x, 0);
+      decode32<FMT>(codes[k][1], now[k], dst, x, 1);
+    }
+    fence_proxy_async();  // the stores, before the tensor cores read them
+    __syncwarp();
+    if (d.lane == 0) {
+      if constexpr (PAIR) arrive_remote(d.a_full);
+      else arrive_local(d.a_full);
+      arrive_local(d.c_empty + 8u * cs);
+    }
+    aph ^= 1u;
+    cs += kGroups;
+    if (cs >= a.code_slots) {
+      cs -= a.code_slots;
+      cph ^= 1u;
     }
   }
 }
@@ -431,6 +567,7 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
   const uint32_t rank = cluster_rank();
   const bool leader = !PAIR || rank == 0;
   const uint32_t base = (smem_addr(tc_raw) + 1023u) & ~1023u;
+  const uint8_t* smem = tc_raw + (base - smem_addr(tc_raw));
   constexpr uint32_t kStageBytes = TcFormat<FMT>::kStageBytes;
   const int code_slots = a.code_slots, b_stages = a.b_stages;
   const uint32_t a_base = base, c_base = base + kGroups * kStageBytes, b_base = c_base + code_slots * kBoxBytes;
@@ -452,7 +589,7 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(smem_addr(&d_full[s]), 1);
-      mbar_init(smem_addr(&d_empty[s]), kEpiWarps * CG);
+      mbar_init(smem_addr(&d_empty[s]), TcFormat<FMT>::kEpiWarps * CG);
     }
     mbar_init(smem_addr(&drain), 1);
     mbar_init_fence();
@@ -598,106 +735,34 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
     }
     __syncwarp();
   } else if (warp >= kDecWarp0 && warp < kEpiWarp0) {
-    // Group g of four warps takes every kGroups-th box; thread i of it line i of each:
-    // an output (backward: weight row i % 64 of the step, outputs 64 (i / 64) .. + 63).
-    const int group = (warp - kDecWarp0) >> 2, line = (tid - kDecWarp0 * 32) & 127, x = line & 7;
-    const uint32_t line_addr = 128u * line;
-    // the code box has 64-byte lines with a 64-byte swizzle, 16-byte chunk c of line l at
-    // c ^ (l / 2 % 4), or 32-byte ones (c ^ (l / 4 % 2)); a thread's chunks are 2 k and 2 k + 1 of
-    // step k (backward: of its slab), so eight lanes' 16-byte loads take different banks
-    constexpr uint32_t kLine = MODE == kModeBackward ? 64u : kBoxK / 2;
-    const int cl = MODE == kModeBackward ? line & 63 : line, cx = kLine == 64 ? (cl >> 1) & 3 : (cl >> 2) & 1;
-    const int per_tile = bx_end - bx_begin;
-    int t = first, bx = bx_begin + group;              // this group's box
-    const uint32_t empty = smem_addr(&a_empty[group]);
-    const uint32_t full = PAIR ? map_to_rank(smem_addr(&a_full[group]), 0) : smem_addr(&a_full[group]);
-    int cs = group;
-    uint32_t aph = 0, cph = 0;
-    const auto settle = [&]() {  // a box past the tile's end: the next tiles'
-      while (t < tile_end && bx >= bx_end) {
-        bx -= per_tile;
-        t += tile_step;
-      }
-    };
-    constexpr int kScaleBytes = FMT == QZ_INT4 ? 4 : 1;
-    const int64_t pitch = static_cast<int64_t>(a.blocks_row) * kScaleBytes;
-    const uint8_t* row_scales = nullptr;  // forward: of this thread's line in tile `row_tile` (null: outside)
-    int row_tile = -1;
-    const auto load_next = [&](Scales<FMT> (&s)[kSteps]) {  // of box bx in tile t
-      const int cols = static_cast<int>(a.p.cols);
-      if (t >= tile_end) return;
-      if constexpr (MODE == kModeBackward) {
-        const bool second = bx >= a.boxes_w;
-        const int row = (second ? bx - a.boxes_w : bx) * kBoxK + (line & 63), col = tile_m0(t) + 64 * (line >> 6);
-        const uint8_t* base = static_cast<const uint8_t*>(second ? a.scales1 : a.scales0) + row * pitch;
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k)
-          s[k] = load_scales<FMT>(row + 64 * k < a.nsum ? base + 64 * k * pitch : nullptr, col, cols, a.p.log2_block, a.scales_vec >= 1);
-      } else {
-        if (row_tile != t) {
-          row_tile = t;
-          const int m0 = tile_m0(t);
-          const int row = MODE == kModeGated ? m0 + 16 * (line >> 5) + (line & 15) : m0 + line;
-          const void* base = MODE == kModeGated && (line & 16) ? a.scales1 : a.scales0;
-          row_scales = row < a.nout ? static_cast<const uint8_t*>(base) + row * pitch : nullptr;
-        }
-        const int col = bx * kBoxK;
-        if constexpr (kSteps == 2) {
-          if (a.scales_vec == 2) {
-            load_scales_box<FMT>(row_scales, col, s);
-            return;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < kSteps; ++k) s[k] = load_scales<FMT>(row_scales, col + 64 * k, cols, a.p.log2_block, a.scales_vec >= 1);
-      }
-    };
-    settle();
-    Scales<FMT> next[kSteps] = {};
-    load_next(next);
-    while (t < tile_end) {
-      Scales<FMT> now[kSteps];
-#pragma unroll
-      for (int k = 0; k < kSteps; ++k) now[k] = next[k];
-      bx += kGroups;
-      settle();
-      load_next(next);  // of this group's next box, in flight during this one
-      if (!__all_sync(kFull, tc_wait(smem_addr(&c_full[cs]), cph, &s_abort) && tc_wait(empty, aph ^ 1u, &s_abort))) break;
-      const uint32_t box = c_base + cs * kBoxBytes;
-#pragma unroll
-      for (int k = 0; k < kSteps; ++k) {
-        const uint32_t from = box + kLine * cl + (MODE == kModeBackward ? 4096u * k : 0u);
-        const int c = 2 * (MODE == kModeBackward ? line >> 6 : k);
-        const uint4 c0 = lds16(from + static_cast<uint32_t>((c ^ cx) << 4)), c1 = lds16(from + static_cast<uint32_t>(((c + 1) ^ cx) << 4));
-        const uint32_t dst = a_base + group * kStageBytes + k * (kTerms * kABytes) + line_addr;
-        if (kSteps == 1) {  // the codes are in registers
-          __syncwarp();
-          if (lane == 0) arrive_local(smem_addr(&c_empty[cs]));
-        }
-        decode32<FMT>(c0, now[k], dst, x, 0);
-        decode32<FMT>(c1, now[k], dst, x, 1);
-      }
-      fence_proxy_async();  // the stores, before the tensor cores read them
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (PAIR) arrive_remote(full);
-        else arrive_local(full);
-        if (kSteps == 2) arrive_local(smem_addr(&c_empty[cs]));
-      }
-      aph ^= 1u;
-      cs += kGroups;
-      if (cs >= code_slots) {
-        cs -= code_slots;
-        cph ^= 1u;
-      }
-    }
+    DecodeLoop d;
+    d.group = (warp - kDecWarp0) >> 2;
+    d.line = (tid - kDecWarp0 * 32) & 127;
+    d.lane = lane;
+    d.first = first;
+    d.tile_end = tile_end;
+    d.tile_step = tile_step;
+    d.bx_begin = bx_begin;
+    d.bx_end = bx_end;
+    d.m_rank = PAIR ? static_cast<int>(rank) * kOut : 0;
+    d.a_stage = a_base + d.group * kStageBytes;
+    d.codes = smem + (c_base - base);
+    d.c_full = smem_addr(&c_full[0]);
+    d.c_empty = smem_addr(&c_empty[0]);
+    d.a_empty = smem_addr(&a_empty[d.group]);
+    d.a_full = PAIR ? map_to_rank(smem_addr(&a_full[d.group]), 0) : smem_addr(&a_full[d.group]);
+    d.abort = &s_abort;
+    if (a.scales_vec >= (MODE == kModeBackward || kSteps == 1 ? 1 : 2)) decode_boxes<FMT, MODE, PAIR, true>(a, d);
+    else decode_boxes<FMT, MODE, PAIR, false>(a, d);
   } else if (PAIR && warp >= kEpiWarp0) {
     const int quarter = warp & 3;
-    const StoreFlags fl{(reinterpret_cast<uintptr_t>(a.p.y) & 3u) == 0 && (a.p.ld_y & 1) == 0,
-                        (reinterpret_cast<uintptr_t>(a.p.g_out) & 3u) == 0 && (reinterpret_cast<uintptr_t>(a.p.u_out) & 3u) == 0 && (a.p.ld_gu & 1) == 0};
+    constexpr int kHalves = TcFormat<FMT>::kEpiWarps / 4;
+    const int part = (warp - kEpiWarp0) >> 2;
     constexpr float kUnit = FMT == QZ_NVFP4 ? 256.0f : 1.0f;  // decoded NVFP4 weights are 2^-8 of their value
     const float f0 = sum_factor<FMT>(a.tscale0) * kUnit, f1 = a.p.n_weights == 2 ? sum_factor<FMT>(a.tscale1) * kUnit : 0.0f;
     const bool two = MODE == kModeBackward && a.p.n_weights == 2;
+    const int c_begin = part * a.n / kHalves / 8 * 8, c_end = (part + 1) * a.n / kHalves / 8 * 8;
+    const uint32_t ta = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     int buf = 0;
     uint32_t fph = 0;  // parity bit per accumulator
     bool ok = true;
@@ -709,25 +774,33 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
         fph ^= 1u << b;
       }
       tc_fence_after();
-      const uint32_t ta = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-      for (int c = 0; c < a.n && n0 + c < a.p.tokens; c += 8) {
-        float v[8];
+      const int end = min(c_end, static_cast<int>(min(a.p.tokens - n0, static_cast<int64_t>(a.n))));
+      const StorePlan plan = store_plan<MODE>(a, m0, quarter, lane, n0 + c_begin, n0 + c_end);
+      // the next eight columns are on their way while these are worked on
+      float v[8], w[8];
+      const auto fetch = [&](int c, float (&x)[8], float (&y)[8]) {
+        tmem_load8(ta + 256u * buf + c, x);
+        if (two) tmem_load8(ta + 256u * (buf ^ 1) + c, y);
+      };
+      if (ok && c_begin < end) fetch(c_begin, v, w);
+      for (int c = c_begin; c < end; c += 8) {
+        float r[8];
         if (ok) {
-          tmem_ld8(ta + 256u * buf + c, v);
+          tmem_wait8(v);
           if (two) {
-            float w[8];
-            tmem_ld8(ta + 256u * (buf ^ 1) + c, w);
+            tmem_wait8(w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fmaf_rn(w[i], f1, v[i] * f0);
-          } else if (MODE != kModeGated) {
+            for (int i = 0; i < 8; ++i) r[i] = __fmaf_rn(w[i], f1, v[i] * f0);
+          } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= f0;
+            for (int i = 0; i < 8; ++i) r[i] = MODE == kModeGated ? v[i] : v[i] * f0;
           }
+          if (c + 8 < end) fetch(c + 8, v, w);
         } else {  // a wait gave up: NaN instead of a wrong result
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(0x7fc00000u);
+          for (int i = 0; i < 8; ++i) r[i] = __uint_as_float(0x7fc00000u);
         }
-        store8<FMT, MODE>(a, fl, v, f0, f1, m0, quarter, lane, n0 + c);
+        store8<MODE>(a, plan, r, f0, f1, lane, n0 + c);
       }
       tc_fence_before();
       __syncwarp();
@@ -790,9 +863,8 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
       }
       cluster_sync();
     }
-    const StoreFlags fl{(reinterpret_cast<uintptr_t>(a.p.y) & 3u) == 0 && (a.p.ld_y & 1) == 0,
-                        (reinterpret_cast<uintptr_t>(a.p.g_out) & 3u) == 0 && (reinterpret_cast<uintptr_t>(a.p.u_out) & 3u) == 0 && (a.p.ld_gu & 1) == 0};
     const int c_begin = static_cast<int>(rank) * cols;
+    const StorePlan plan = store_plan<MODE>(a, m0, quarter, lane, n0 + c_begin, n0 + c_begin + cols);
     for (int c = 8 * part; c < cols && n0 + c_begin + c < a.p.tokens; c += kStride) {
       float mine[8], v[8];
       own(c_begin + c, mine);
@@ -811,7 +883,7 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= f0;
       }
-      store8<FMT, MODE>(a, fl, v, f0, f1, m0, quarter, lane, n0 + c_begin + c);
+      store8<MODE>(a, plan, v, f0, f1, lane, n0 + c_begin + c);
     }
   }
   tc_fence_before();
