@@ -949,12 +949,12 @@ inline Plan plan_of(int64_t nout, int out_per_cta, int64_t tokens, int boxes) {
   double best_cost = 1e30;
   int n;
   int64_t tiles_n;
-  {
-    tokens_per_tile(tokens, 256, 32, &n, &tiles_n);
+  for (int most = 256; most >= 64; most -= 32) {  // narrower tiles where they fill the last round better
+    tokens_per_tile(tokens, most, 32, &n, &tiles_n);
     const int64_t tiles = (nout + 2 * out_per_cta - 1) / (2 * out_per_cta) * tiles_n;
     const int64_t pairs = std::max(1, sms / 2);
-    const double cost = static_cast<double>((tiles + pairs - 1) / pairs) * boxes * std::max(4.0 * n, 700.0) + 6000;
-    if (tiles < (int64_t{1} << 30)) {
+    const double cost = static_cast<double>((tiles + pairs - 1) / pairs) * boxes * std::max(4.0 * n + 40, 850.0) + 6000;
+    if (tiles < (int64_t{1} << 30) && cost < best_cost) {
       best = Plan{true, n, static_cast<int>(tiles_n), static_cast<int>(tiles), 1, boxes, static_cast<int>(2 * std::min(tiles, pairs))};
       best_cost = cost;
     }
