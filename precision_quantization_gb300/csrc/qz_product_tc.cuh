@@ -83,7 +83,7 @@ struct TcArgs {
   int n;                  // tokens per tile (a multiple of 32)
   int code_slots, b_stages;  // slots of the code ring (a multiple of the groups), of the tokens' ring
   int scales_vec;         // 1: the scales of 64 columns are one aligned load; 2: those of 128 are
-  int tiles_n, tiles;
+  int tiles_n, tiles, m_base;  // tiles of tokens, in all; the first output of the first
   int slices, slice_boxes;  // Alone: slices of the sum (the cluster), boxes per slice
 };
 
@@ -483,7 +483,7 @@ __device__ __forceinline__ void decode_boxes(const TcArgs& a, const DecodeLoop& 
     }
   };
   const auto load_next = [&]() {  // the scales of box bx in tile t
-    const int m0 = (t / a.tiles_n) * (kOut * CG) + d.m_rank;
+    const int m0 = a.m_base + (t / a.tiles_n) * (kOut * CG) + d.m_rank;
     if constexpr (MODE == kModeBackward) {
       const bool second = bx >= a.boxes_w;
       const int row = (second ? bx - a.boxes_w : bx) * kBoxK + (line & 63), col = m0 + 64 * (line >> 6);
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
   const int tile_step = PAIR ? static_cast<int>(gridDim.x) / 2 : 1;
   const int bx_begin = PAIR ? 0 : static_cast<int>(rank) * a.slice_boxes;
   const int bx_end = PAIR ? a.boxes : min(a.boxes, bx_begin + a.slice_boxes);
-  const auto tile_m0 = [&](int t) { return (t / a.tiles_n) * (kOut * CG) + (PAIR ? static_cast<int>(rank) * kOut : 0); };
+  const auto tile_m0 = [&](int t) { return a.m_base + (t / a.tiles_n) * (kOut * CG) + (PAIR ? static_cast<int>(rank) * kOut : 0); };
   const auto tile_n0 = [&](int t) { return (t % a.tiles_n) * a.n; };
 
   if (warp == 0) {
@@ -931,46 +931,105 @@ qz_status run_tc(const TcArgs& a, int grid, cudaStream_t s) {
   return launch_status();
 }
 
-// The form and its tiles.  Estimated in SM cycles: a box's eight MMAs take 4 cycles a token column
-// (128 x n x 16 each at 8192 FLOP a cycle), its hand-over at least 700 cycles; a tile of the second
-// form starts with an empty pipeline and ends with the exchange.
+// The form and its tiles for outputs [m_base, m_base + nout).  Estimated in SM cycles: a box's eight
+// MMAs take 4 cycles a token column (128 x n x 16 each at 8192 FLOP a cycle); its hand-over takes
+// some 750 cycles in a pair, whose decoders share the tokens' copies, and 950 alone; a tile of the
+// second form starts with an empty pipeline and ends with the exchange.
 struct Plan {
   bool pair;
   int n, tiles_n, tiles, slices, slice_boxes, grid;
+  int64_t m_base;
+  double cost;
 };
 inline void tokens_per_tile(int64_t tokens, int most, int unit, int* n, int64_t* tiles_n) {
   const int64_t t = (tokens + most - 1) / most;
   *n = static_cast<int>(((tokens + t - 1) / t + unit - 1) / unit * unit);
   *tiles_n = (tokens + *n - 1) / *n;
 }
-inline Plan plan_of(int64_t nout, int out_per_cta, int64_t tokens, int boxes) {
-  const int sms = sm_count();
+inline Plan plan_pairs(int64_t m_base, int64_t nout, int out_per_cta, int64_t tokens, int boxes, double least) {
   Plan best{};
-  double best_cost = 1e30;
-  int n;
-  int64_t tiles_n;
+  best.cost = 1e30;
+  const int64_t pairs = std::max(1, sm_count() / 2);
   for (int most = 256; most >= 64; most -= 32) {  // narrower tiles where they fill the last round better
+    int n;
+    int64_t tiles_n;
     tokens_per_tile(tokens, most, 32, &n, &tiles_n);
     const int64_t tiles = (nout + 2 * out_per_cta - 1) / (2 * out_per_cta) * tiles_n;
-    const int64_t pairs = std::max(1, sms / 2);
-    const double cost = static_cast<double>((tiles + pairs - 1) / pairs) * boxes * std::max(4.0 * n + 40, 850.0) + 6000;
-    if (tiles < (int64_t{1} << 30) && cost < best_cost) {
-      best = Plan{true, n, static_cast<int>(tiles_n), static_cast<int>(tiles), 1, boxes, static_cast<int>(2 * std::min(tiles, pairs))};
-      best_cost = cost;
-    }
-  }
-  for (int s = 1; s <= 8; s *= 2) {
-    tokens_per_tile(tokens, 128, std::max(32, 8 * s), &n, &tiles_n);  // the columns divide into eights per slice
-    const int64_t tiles = (nout + out_per_cta - 1) / out_per_cta * tiles_n;
-    const int per = (boxes + s - 1) / s;
-    const int64_t clusters = std::max(1, s == 1 ? sms : (s == 2 ? sms * 9 / 10 : sms * 5 / 6) / s);
-    const double cost = static_cast<double>((tiles + clusters - 1) / clusters) * (per * std::max(4.0 * n, 700.0) + 5000 + (s > 1 ? 2000 + 16.0 * n : 0));
-    if (tiles * s < (int64_t{1} << 30) && cost < best_cost) {
-      best = Plan{false, n, static_cast<int>(tiles_n), static_cast<int>(tiles), s, per, static_cast<int>(tiles * s)};
-      best_cost = cost;
-    }
+    const double cost = static_cast<double>((tiles + pairs - 1) / pairs) * boxes * std::max(4.0 * n + 40, least) + 6000;
+    if (tiles < (int64_t{1} << 30) && cost < best.cost)
+      best = Plan{true, n, static_cast<int>(tiles_n), static_cast<int>(tiles), 1, boxes, static_cast<int>(2 * std::min(tiles, pairs)), m_base, cost};
   }
   return best;
+}
+inline Plan plan_alone(int64_t m_base, int64_t nout, int out_per_cta, int64_t tokens, int boxes) {
+  Plan best{};
+  best.cost = 1e30;
+  const int sms = sm_count();
+  for (int s = 1; s <= 8; s *= 2)
+    for (int most : {192, 128}) {
+      int n;
+      int64_t tiles_n;
+      tokens_per_tile(tokens, most, std::max(32, 8 * s), &n, &tiles_n);  // the columns divide into eights per slice
+      const int64_t tiles = (nout + out_per_cta - 1) / out_per_cta * tiles_n;
+      const int per = (boxes + s - 1) / s;
+      const int64_t clusters = std::max(1, s == 1 ? sms : (s == 2 ? sms * 9 / 10 : sms * 5 / 6) / s);
+      // above 128 tokens the copies have two stages only
+      const double box = std::max(4.0 * n, n > 128 ? 1200.0 : 950.0);
+      const double cost = static_cast<double>((tiles + clusters - 1) / clusters) * (per * box + 6000 + (s > 1 ? 2000 + 16.0 * n : 0));
+      if (tiles * s < (int64_t{1} << 30) && cost < best.cost)
+        best = Plan{false, n, static_cast<int>(tiles_n), static_cast<int>(tiles), s, per, static_cast<int>(tiles * s), m_base, cost};
+    }
+  return best;
+}
+// One launch, or two: where a few tiles of the pairs would make a round of their own, the last
+// outputs' tiles go to a second launch that splits their sums over the whole GPU.
+inline int plan_of(int64_t nout, int out_per_cta, int64_t tokens, int boxes, double least, Plan (&plan)[2]) {
+  const Plan pairs = plan_pairs(0, nout, out_per_cta, tokens, boxes, least), alone = plan_alone(0, nout, out_per_cta, tokens, boxes);
+  plan[0] = alone.cost < pairs.cost ? alone : pairs;
+  if (plan[0].cost > 1e29) return 0;
+  const int64_t per_round = std::max(1, sm_count() / 2) / pairs.tiles_n;  // rows of pairs' tiles a round takes
+  const int64_t rows_m = (nout + 2 * out_per_cta - 1) / (2 * out_per_cta);
+  if (per_round < 1 || rows_m <= per_round || rows_m % per_round == 0) return 1;
+  const int64_t first = rows_m / per_round * per_round * 2 * out_per_cta;
+  const Plan a = plan_pairs(0, first, out_per_cta, tokens, boxes, least), b = plan_alone(first, nout - first, out_per_cta, tokens, boxes);
+  if (a.cost + b.cost + 4000 >= plan[0].cost) return 1;
+  plan[0] = a;
+  plan[1] = b;
+  return 2;
+}
+
+template <int FMT>
+qz_status launch_plan(TcArgs& a, const Plan& plan, cudaStream_t s) {
+  const ProductArgs& p = a.p;
+  const bool back = p.mode == kModeBackward;
+  a.n = plan.n;
+  a.tiles_n = plan.tiles_n;
+  a.tiles = plan.tiles;
+  a.m_base = static_cast<int>(plan.m_base);
+  a.slices = plan.slices;
+  a.slice_boxes = plan.slice_boxes;
+  constexpr int kBoxK = TcFormat<FMT>::kBoxK, kGroups = TcFormat<FMT>::kGroups;
+  constexpr uint32_t kBoxBytes = TcFormat<FMT>::kBoxBytes;
+  const int b_rows = plan.pair ? plan.n / 2 : plan.n;
+  // two rounds of code boxes, or one where that leaves the tokens fewer than three stages
+  const uint32_t stage_b = static_cast<uint32_t>(b_rows) * kBoxK * 2;
+  a.code_slots = kRingRoom<FMT> < 2 * kGroups * kBoxBytes + 3 * stage_b ? kGroups : 2 * kGroups;
+  a.b_stages = static_cast<int>(std::min<uint32_t>(kMaxBStages, (kRingRoom<FMT> - a.code_slots * kBoxBytes) / stage_b));
+  const int code_line = back ? 64 : kBoxK / 2;  // bytes, and the swizzle
+  const int code_rows = back ? kBoxK : p.mode == kModeGated ? 16 : 128;
+  bool ok = encode(&a.map_x0, 128, p.x0, a.nsum, p.tokens, p.ld_x * 2, kBK, b_rows) &&
+            encode(&a.map_w0, code_line, p.w0.codes, p.cols / 2, p.rows, p.cols / 2, code_line, code_rows);
+  if (p.n_weights == 2) ok = ok && encode(&a.map_w1, code_line, p.w1.codes, p.cols / 2, p.rows, p.cols / 2, code_line, code_rows);
+  if (p.n_weights == 2 && back) ok = ok && encode(&a.map_x1, 128, p.x1, a.nsum, p.tokens, p.ld_x * 2, kBK, b_rows);
+  if (!ok) return QZ_ERR_CUDA;
+  if (plan.pair) {
+    if (p.mode == kModeLinear) return run_tc<FMT, kModeLinear, true>(a, plan.grid, s);
+    if (p.mode == kModeGated) return run_tc<FMT, kModeGated, true>(a, plan.grid, s);
+    return run_tc<FMT, kModeBackward, true>(a, plan.grid, s);
+  }
+  if (p.mode == kModeLinear) return run_tc<FMT, kModeLinear, false>(a, plan.grid, s);
+  if (p.mode == kModeGated) return run_tc<FMT, kModeGated, false>(a, plan.grid, s);
+  return run_tc<FMT, kModeBackward, false>(a, plan.grid, s);
 }
 
 template <int FMT>
@@ -988,38 +1047,17 @@ qz_status launch_tc(const ProductArgs& p, cudaStream_t s) {
   constexpr int kBoxK = TcFormat<FMT>::kBoxK;
   a.boxes_w = (a.nsum + kBoxK - 1) / kBoxK;
   a.boxes = back ? a.boxes_w * p.n_weights : a.boxes_w;
-  const Plan plan = plan_of(a.nout, p.mode == kModeGated ? kBM / 2 : kBM, p.tokens, a.boxes);
-  if (plan.grid == 0) return QZ_ERR_UNSUPPORTED;
-  a.n = plan.n;
-  a.tiles_n = plan.tiles_n;
-  a.tiles = plan.tiles;
-  a.slices = plan.slices;
-  a.slice_boxes = plan.slice_boxes;
-  const int b_rows = plan.pair ? plan.n / 2 : plan.n;
-  // two rounds of code boxes, or one where that leaves the tokens fewer than three stages
-  const uint32_t stage_b = static_cast<uint32_t>(b_rows) * kBoxK * 2;
-  constexpr int kGroups = TcFormat<FMT>::kGroups;
-  constexpr uint32_t kBoxBytes = TcFormat<FMT>::kBoxBytes;
-  a.code_slots = kRingRoom<FMT> < 2 * kGroups * kBoxBytes + 3 * stage_b ? kGroups : 2 * kGroups;
-  a.b_stages = static_cast<int>(std::min<uint32_t>(kMaxBStages, (kRingRoom<FMT> - a.code_slots * kBoxBytes) / stage_b));
   const auto aligned_scales = [&](uintptr_t n) { return reinterpret_cast<uintptr_t>(a.scales0) % n == 0 && reinterpret_cast<uintptr_t>(a.scales1) % n == 0; };
   const int unit = p.format == QZ_MXFP4 ? 2 : 4;  // bytes of scales per 64 columns
   a.scales_vec = p.cols % 128 == 0 && aligned_scales(2 * unit) ? 2 : p.cols % 64 == 0 && aligned_scales(unit) ? 1 : 0;
-  const int code_line = back ? 64 : kBoxK / 2;  // bytes, and the swizzle
-  const int code_rows = back ? kBoxK : p.mode == kModeGated ? 16 : 128;
-  bool ok = encode(&a.map_x0, 128, p.x0, a.nsum, p.tokens, p.ld_x * 2, kBK, b_rows) &&
-            encode(&a.map_w0, code_line, p.w0.codes, p.cols / 2, p.rows, p.cols / 2, code_line, code_rows);
-  if (p.n_weights == 2) ok = ok && encode(&a.map_w1, code_line, p.w1.codes, p.cols / 2, p.rows, p.cols / 2, code_line, code_rows);
-  if (p.n_weights == 2 && back) ok = ok && encode(&a.map_x1, 128, p.x1, a.nsum, p.tokens, p.ld_x * 2, kBK, b_rows);
-  if (!ok) return QZ_ERR_CUDA;
-  if (plan.pair) {
-    if (p.mode == kModeLinear) return run_tc<FMT, kModeLinear, true>(a, plan.grid, s);
-    if (p.mode == kModeGated) return run_tc<FMT, kModeGated, true>(a, plan.grid, s);
-    return run_tc<FMT, kModeBackward, true>(a, plan.grid, s);
+  Plan plans[2];
+  const int launches = plan_of(a.nout, p.mode == kModeGated ? kBM / 2 : kBM, p.tokens, a.boxes, FMT == QZ_INT4 ? 1060.0 : 750.0, plans);
+  if (launches == 0) return QZ_ERR_UNSUPPORTED;
+  for (int i = 0; i < launches; ++i) {
+    const qz_status st = launch_plan<FMT>(a, plans[i], s);
+    if (st != QZ_OK) return st;
   }
-  if (p.mode == kModeLinear) return run_tc<FMT, kModeLinear, false>(a, plan.grid, s);
-  if (p.mode == kModeGated) return run_tc<FMT, kModeGated, false>(a, plan.grid, s);
-  return run_tc<FMT, kModeBackward, false>(a, plan.grid, s);
+  return QZ_OK;
 }
 
 }  // namespace
