@@ -8,19 +8,22 @@
 // writes dx; everything else is per row or per column.  So a row is read once and held in
 // registers, 16 values a thread (kPer), by 32 to 1024 threads (TPR, the smallest power of two
 // that covers the row): the squares are taken about the mean from the registers, a second pass
-// over the chip, not over memory.  Rows longer than 16384 are read again from L2 instead.
+// over the chip, not over memory.  The backward pass is persistent, for the column sums, and each
+// thread copies its own pieces of the next rows into shared memory (cp.async, kAhead rows ahead).
+// Rows longer than 16384 are read again from L2 instead.
 #include <climits>
 #include <cstdint>
 
 #include "qz_device.cuh"
 #include "qz_internal.h"
+#include "qz_pipe.cuh"
 #include "qz_weight.cuh"
 
 namespace qz {
 namespace {
 
 constexpr int kPer = 16;           // values of a row per thread
-constexpr int kMaxParts = 304;     // partial column sums in the workspace: two per SM
+constexpr int kMaxParts = 152;     // partial column sums in the workspace: one per SM
 constexpr int kMaxHeld = 1024 * kPer;
 
 struct NormArgs {
@@ -41,6 +44,30 @@ struct RowRegs {
   static constexpr int kWords = DT == QZ_BF16 && E > 1 ? kPer / 2 : kPer;
   uint32_t raw[kWords];
 
+  // The ring: piece i of thread x of the block in slot d at ((d kChunks + i) threads + x) 16 bytes.
+  template <int TPR>
+  static __device__ __forceinline__ void copy(uint32_t slot, int threads, const void* base, int64_t off, int l, int cols) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const int c = E * (i * TPR + l);
+      if (c < cols)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + (i * threads + threadIdx.x) * 16u),
+                     "l"(static_cast<const char*>(base) + (off + c) * (16 / E))
+                     : "memory");
+    }
+  }
+  template <int TPR>
+  __device__ __forceinline__ void take(const unsigned char* slot, int threads, int l, int cols) {
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (E * (i * TPR + l) < cols) v = *reinterpret_cast<const uint4*>(slot + (i * threads + threadIdx.x) * 16);
+      raw[4 * i] = v.x;
+      raw[4 * i + 1] = v.y;
+      raw[4 * i + 2] = v.z;
+      raw[4 * i + 3] = v.w;
+    }
+  }
   template <int TPR>
   __device__ __forceinline__ void load(const void* base, int64_t off, int l, int cols) {
 #pragma unroll
@@ -67,11 +94,24 @@ struct RowRegs {
       return __uint_as_float(raw[j]);
     }
   }
+  // values 2 i and 2 i + 1
+  __device__ __forceinline__ uint64_t pair(int i) const { return pk(get(2 * i), get(2 * i + 1)); }
+  // whether they lie in the row; the chunks of E > 1 do wholly or not at all
+  template <int TPR>
+  static __device__ __forceinline__ uint64_t inside(int i, int l, int cols, uint64_t v) {
+    if constexpr (E > 1) return column<TPR>(2 * i, l) < cols ? v : 0ull;
+    float a, b;
+    upk(v, a, b);
+    return pk(column<TPR>(2 * i, l) < cols ? a : 0.0f, column<TPR>(2 * i + 1, l) < cols ? b : 0.0f);
+  }
   template <int TPR>
   static __device__ __forceinline__ int column(int j, int l) { return E * ((j / E) * TPR + l) + j % E; }
 
   template <int TPR>
-  static __device__ __forceinline__ void store(void* base, int64_t off, int l, int cols, const float (&v)[kPer]) {
+  static __device__ __forceinline__ void store(void* base, int64_t off, int l, int cols, const uint64_t (&y)[kPer / 2]) {
+    float v[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) upk(y[i], v[2 * i], v[2 * i + 1]);
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
       const int c = E * (i * TPR + l);
@@ -95,7 +135,8 @@ struct RowRegs {
 // The parameters of this thread's columns (`dflt` where there are none, and past the row's end), in
 // 16-byte loads where the row's chunks allow them.
 template <int E, int TPR>
-__device__ __forceinline__ void load_params(float (&w)[kPer], const float* base, float dflt, int l, int cols) {
+__device__ __forceinline__ void load_params(uint64_t (&p)[kPer / 2], const float* base, float dflt, int l, int cols) {
+  float w[kPer];
   if constexpr (E == 1) {
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
@@ -114,129 +155,258 @@ __device__ __forceinline__ void load_params(float (&w)[kPer], const float* base,
       w[j + 3] = v.w;
     }
   }
+#pragma unroll
+  for (int i = 0; i < kPer / 2; ++i) p[i] = pk(w[2 * i], w[2 * i + 1]);
 }
 
-// Sums of (a, b) over the TPR threads of a row: shuffles, then the warps' sums through shared
-// memory behind a barrier of the row's threads alone (number 1 + group).  `buf` alternates, so
-// the next row's sums need no second barrier.
-template <int TPR>
-__device__ __forceinline__ void row_sums(float& a, float& b, float2* buf, int group) {
+// Sums over the TPR threads of a row: shuffles, then the warps' sums through shared memory behind a
+// barrier of the row's threads alone (number 1 + group).  `buf` alternates between the sums of a
+// row, or of two rows, so no second barrier is needed.
+template <int TPR, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*buf)[N], int group) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    a += __shfl_xor_sync(kFull, a, o);
-    b += __shfl_xor_sync(kFull, b, o);
-  }
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kFull, v[i], o);
   if constexpr (TPR > 32) {
     constexpr int W = TPR / 32;
     const int w = (threadIdx.x % TPR) / 32;
-    if ((threadIdx.x & 31) == 0) buf[w] = make_float2(a, b);
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(TPR) : "memory");
-    float2 s = (threadIdx.x & 31) < W ? buf[threadIdx.x & 31] : make_float2(0.0f, 0.0f);
+    if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      s.x += __shfl_xor_sync(kFull, s.x, o);
-      s.y += __shfl_xor_sync(kFull, s.y, o);
+      for (int i = 0; i < N; ++i) buf[w][i] = v[i];
     }
-    a = s.x;
-    b = s.y;
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(TPR) : "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = buf[threadIdx.x % W][i];
+#pragma unroll
+    for (int o = W / 2; o; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kFull, v[i], o);
   }
 }
+// 1 / sqrt(v): the approximation (2 ulp) and one Newton step
+__device__ __forceinline__ float rsqrt_of(float v) {
+  const float r = rsqrtf(v);
+  const float e = __fmaf_rn(-v * r, r, 1.0f);
+  // (an infinite r, from v = 0, stays: its correction would be NaN)
+  return fabsf(e) <= 1.0f ? __fmaf_rn(0.5f * r, e, r) : r;
+}
 
+constexpr int kAhead = 5;  // rows a thread copies ahead at most
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int TPR>
+constexpr int kNormBlock = TPR < 512 ? 512 : TPR;
+// The backward pass's ring: a slot is one row of x and dy for every group of the block, and there are
+// as many (kAhead + 1 at most) as fit 192 KiB.
+template <int DT, int TPR>
+constexpr int kNormSlot = 2 * kNormBlock<TPR> * kPer * (DT == QZ_BF16 ? 2 : 4);
+template <int DT, int TPR>
+constexpr int kNormRoom = 192 * 1024 / kNormSlot<DT, TPR>;
+template <int DT, int TPR>
+constexpr int kNormSlots = kNormRoom<DT, TPR> > kAhead + 1 ? kAhead + 1 : kNormRoom<DT, TPR>;
+
+// One row per group of threads and launch: the forward pass keeps nothing from row to row but the
+// parameters, which come from L1.  (A persistent form with the rows copied ahead, as the backward pass
+// has it, was slower: 43 us against 37 at 8192 x 4096 bf16; it is instructions that bound it.)
 template <int DT, int E, int TPR>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_forward_kernel(const NormArgs a) {
-  constexpr int kBlock = TPR < 256 ? 256 : TPR, G = kBlock / TPR;
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 6 : TPR == 512 ? 3 : 1) norm_forward_kernel(const NormArgs a) {
+  constexpr int kBlock = TPR < 256 ? 256 : TPR, G = kBlock / TPR, kChunks = kPer / E;
   using R = RowRegs<DT, E>;
-  __shared__ float2 sums[G][2][TPR > 32 ? TPR / 32 : 1];
+  __shared__ float sums[G][2][TPR > 32 ? TPR / 32 : 1][1];
   const int group = threadIdx.x / TPR, l = threadIdx.x % TPR, cols = static_cast<int>(a.cols);
   const int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
   if (row >= a.rows) return;
   R x;
   x.template load<TPR>(a.x, row * a.ld_x, l, cols);
-  float s = 0.0f, none = 0.0f;
+  float s[1] = {0.0f}, d[kPer];
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) s += x.get(j);
-  row_sums<TPR>(s, none, sums[group][0], group);
-  const float inv = 1.0f / static_cast<float>(cols), mean = s * inv;
-  float q = 0.0f;
+  for (int j = 0; j < kPer; ++j) s[0] += x.get(j);
+  row_sums<TPR>(s, sums[group][0], group);
+  const float inv = 1.0f / static_cast<float>(cols), mean = s[0] * inv;
+  s[0] = 0.0f;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j)
-    if (R::template column<TPR>(j, l) < cols) {
-      const float d = x.get(j) - mean;
-      q = __fmaf_rn(d, d, q);
+  for (int i = 0; i < kChunks; ++i) {
+    if (E * (i * TPR + l) < cols) {  // a chunk lies wholly in the row or not at all
+#pragma unroll
+      for (int j = E * i; j < E * i + E; ++j) {
+        d[j] = x.get(j) - mean;
+        s[0] = __fmaf_rn(d[j], d[j], s[0]);
+      }
     }
-  row_sums<TPR>(q, none, sums[group][1], group);
-  const float rstd = 1.0f / sqrtf(q * inv + a.eps);
+  }
+  row_sums<TPR>(s, sums[group][1], group);
+  const float rstd = rsqrt_of(s[0] * inv + a.eps);
   if (l == 0) {
     if (a.mean) a.mean[row] = mean;
     if (a.rstd) a.rstd[row] = rstd;
   }
-  float y[kPer], w[kPer], b[kPer];
-  load_params<E, TPR>(w, a.weight, 1.0f, l, cols);
-  load_params<E, TPR>(b, a.bias, 0.0f, l, cols);
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) y[j] = __fmaf_rn((x.get(j) - mean) * rstd, w[j], b[j]);
-  R::template store<TPR>(a.y, row * a.ld_y, l, cols, y);
+  for (int i = 0; i < kChunks; ++i) {
+    const int c = E * (i * TPR + l);
+    if (c >= cols) continue;
+    float y[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) y[j] = d[E * i + j] * rstd;
+    if constexpr (E == 1) {
+      if (a.weight) y[0] *= __ldg(a.weight + c);
+      if (a.bias) y[0] += __ldg(a.bias + c);
+      store_elem<DT>(a.y, row * a.ld_y + c, y[0]);
+    } else {
+      float w[E], b[E];
+#pragma unroll
+      for (int j = 0; j < E; j += 4) {
+        float4 v = make_float4(1.0f, 1.0f, 1.0f, 1.0f), u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (a.weight) v = __ldg(reinterpret_cast<const float4*>(a.weight + c + j));
+        if (a.bias) u = __ldg(reinterpret_cast<const float4*>(a.bias + c + j));
+        w[j] = v.x; w[j + 1] = v.y; w[j + 2] = v.z; w[j + 3] = v.w;
+        b[j] = u.x; b[j + 1] = u.y; b[j + 2] = u.z; b[j + 3] = u.w;
+      }
+#pragma unroll
+      for (int j = 0; j < E; ++j) y[j] = __fmaf_rn(y[j], w[j], b[j]);
+      uint4 o;
+      if constexpr (DT == QZ_BF16) o = make_uint4(bf16x2_bits(y[0], y[1]), bf16x2_bits(y[2], y[3]), bf16x2_bits(y[E - 4], y[E - 3]), bf16x2_bits(y[E - 2], y[E - 1]));
+      else o = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
+      *reinterpret_cast<uint4*>(static_cast<char*>(a.y) + (row * a.ld_y + c) * (16 / E)) = o;
+    }
+  }
 }
+
+// Rows a group works on at once: a row's sums are a chain of shuffles and a barrier, some 1000 cycles
+// whatever the row's length, which two rows share where the ring has room for them (backward pass
+// of 8192 x 4096 bf16: 52 -> 40 us).
+template <int SLOTS>
+constexpr int kNormRows = SLOTS >= 4 ? 2 : 1;
 
 // A thread keeps its 16 columns from row to row, so the column sums of dy n and dy stay in its
 // registers; at the end a block adds its groups' sums in group order and writes one partial.
 template <int DT, int E, int TPR, bool PARAMS>
-__global__ void __launch_bounds__(TPR < 512 ? 512 : TPR) norm_backward_kernel(const NormArgs a) {
-  constexpr int kBlock = TPR < 512 ? 512 : TPR, G = kBlock / TPR;
+__global__ void __launch_bounds__(kNormBlock<TPR>) norm_backward_kernel(const NormArgs a) {
+  constexpr int kBlock = kNormBlock<TPR>, G = kBlock / TPR, kSlots = kNormSlots<DT, TPR>, kSlotBytes = kNormSlot<DT, TPR> / 2;  // of one tensor
+  constexpr int kRows = kNormRows<kSlots>;
   using R = RowRegs<DT, E>;
-  extern __shared__ float columns[];  // [2][cols] where G > 1
-  __shared__ float2 sums[G][2][TPR > 32 ? TPR / 32 : 1];
+  extern __shared__ __align__(16) unsigned char norm_ring_smem[];
+  __shared__ float sums[G][2][TPR > 32 ? TPR / 32 : 1][2 * kRows];
   const int group = threadIdx.x / TPR, l = threadIdx.x % TPR, cols = static_cast<int>(a.cols);
-  const float inv = 1.0f / static_cast<float>(cols);
-  float w[kPer], dw[kPer] = {}, db[kPer] = {};
-  load_params<E, TPR>(w, a.weight, 1.0f, l, cols);
   const int64_t step = static_cast<int64_t>(gridDim.x) * G;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
-  R x, dy;
-  float mean = 0.0f, rstd = 0.0f;
-  const auto fetch = [&](int64_t r) {
-    x.template load<TPR>(a.x, r * a.ld_x, l, cols);
-    dy.template load<TPR>(a.dy, r * a.ld_dy, l, cols);
-    mean = __ldg(a.mean_in + r);
-    rstd = __ldg(a.rstd_in + r);
+  int64_t row = static_cast<int64_t>(blockIdx.x) * G + group, ahead = row;
+  int slot = 0, to = 0;
+  const auto copy_next = [&]() {
+    if constexpr (E > 1) {
+      if (ahead < a.rows) {
+        const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(norm_ring_smem)) + to * (2 * kSlotBytes);
+        R::template copy<TPR>(at, kBlock, a.x, ahead * a.ld_x, l, cols);
+        R::template copy<TPR>(at + kSlotBytes, kBlock, a.dy, ahead * a.ld_dy, l, cols);
+      }
+      copies_commit();
+      ahead += step;
+      to = to == kSlots - 1 ? 0 : to + 1;
+    }
   };
-  if (row < a.rows) fetch(row);
-  for (int flip = 0; row < a.rows; row += step, flip ^= 1) {
-    float t[kPer], n[kPer], s1 = 0.0f, s2 = 0.0f;
-    const float rs = rstd;
+  // row k of this round: this thread's own pieces, which no other thread reads
+  const auto take = [&](int k, R& x, R& dy) {
+    if constexpr (E > 1) {
+      const int d = slot + k;
+      const unsigned char* at = norm_ring_smem + (d >= kSlots ? d - kSlots : d) * (2 * kSlotBytes);
+      x.template take<TPR>(at, kBlock, l, cols);
+      dy.template take<TPR>(at + kSlotBytes, kBlock, l, cols);
+    } else {
+      const int64_t r = row + k * step;
+      x.template load<TPR>(a.x, r * a.ld_x, l, cols);
+      dy.template load<TPR>(a.dy, r * a.ld_dy, l, cols);
+    }
+  };
+  for (int i = 0; i < kSlots - kRows; ++i) copy_next();
+  const float inv = 1.0f / static_cast<float>(cols);
+  uint64_t w[kPer / 2], dw[kPer / 2] = {}, db[kPer / 2] = {};
+  load_params<E, TPR>(w, a.weight, 1.0f, l, cols);
+  // mean and rstd one round ahead
+  float mean[kRows], rstd[kRows], mean1[kRows], rstd1[kRows];
+  const auto stats = [&](int64_t r, float (&m)[kRows], float (&v)[kRows]) {
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const float d = dy.get(j);  // 0 past the row's end
-      n[j] = (x.get(j) - mean) * rstd;
-      t[j] = d * w[j];
-      if (R::template column<TPR>(j, l) < cols) {
-        s1 += t[j];
-        s2 = __fmaf_rn(t[j], n[j], s2);
+    for (int k = 0; k < kRows; ++k) {
+      const int64_t i = r + k * step < a.rows ? r + k * step : a.rows - 1;
+      m[k] = __ldg(a.mean_in + i);
+      v[k] = __ldg(a.rstd_in + i);
+    }
+  };
+  if (row < a.rows) stats(row, mean1, rstd1);
+  for (int flip = 0; row < a.rows; row += kRows * step, flip ^= 1) {
+    if constexpr (E > 1) {
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) copy_next();
+      copies_wait<kSlots - kRows>();
+    }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      mean[k] = mean1[k];
+      rstd[k] = rstd1[k];
+    }
+    stats(row + kRows * step, mean1, rstd1);
+    float s[2 * kRows], lo, hi;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      s[2 * k] = s[2 * k + 1] = 0.0f;
+      if (row + k * step >= a.rows) continue;
+      R x, dy;
+      take(k, x, dy);
+      uint64_t a1 = 0ull, a2 = 0ull;
+#pragma unroll
+      for (int i = 0; i < kPer / 2; ++i) {
+        const uint64_t d = dy.pair(i);  // 0 past the row's end, and so t and what it is summed into
+        const uint64_t n = R::template inside<TPR>(i, l, cols, mul2(add2(x.pair(i), pk(-mean[k], -mean[k])), pk(rstd[k], rstd[k])));
+        const uint64_t t = mul2(d, w[i]);
+        a1 = add2(a1, t);
+        a2 = fma2(t, n, a2);
         if constexpr (PARAMS) {
-          dw[j] = __fmaf_rn(d, n[j], dw[j]);
-          db[j] += d;
+          dw[i] = fma2(d, n, dw[i]);
+          db[i] = add2(db[i], d);
         }
       }
+      upk(a1, lo, hi);
+      s[2 * k] = lo + hi;
+      upk(a2, lo, hi);
+      s[2 * k + 1] = lo + hi;
     }
-    if (row + step < a.rows) fetch(row + step);  // in flight during the sums
-    row_sums<TPR>(s1, s2, sums[group][flip], group);
-    s1 *= inv;
-    s2 *= inv;
+    row_sums<TPR>(s, sums[group][flip], group);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) t[j] = rs * (t[j] - s1 - n[j] * s2);
-    R::template store<TPR>(a.y, row * a.ld_y, l, cols, t);
+    for (int k = 0; k < kRows; ++k) {
+      const int64_t r = row + k * step;
+      if (r >= a.rows) break;
+      R x, dy;
+      take(k, x, dy);
+      // rstd (t - m1 - n m2) with n = (x - mean) rstd
+      const float m1 = -s[2 * k] * inv, m2 = -s[2 * k + 1] * inv * rstd[k];
+      uint64_t o[kPer / 2];
+#pragma unroll
+      for (int i = 0; i < kPer / 2; ++i)
+        o[i] = mul2(pk(rstd[k], rstd[k]), add2(fma2(add2(x.pair(i), pk(-mean[k], -mean[k])), pk(m2, m2), mul2(dy.pair(i), w[i])), pk(m1, m1)));
+      R::template store<TPR>(a.y, r * a.ld_y, l, cols, o);
+    }
+    slot += kRows;
+    if (slot >= kSlots) slot -= kSlots;
   }
+  if constexpr (E > 1) copies_wait<0>();
   if constexpr (PARAMS) {
+    float fw[kPer], fb[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer / 2; ++i) {
+      upk(dw[i], fw[2 * i], fw[2 * i + 1]);
+      upk(db[i], fb[2 * i], fb[2 * i + 1]);
+    }
     float* out = a.parts + static_cast<int64_t>(blockIdx.x) * 2 * cols;
     if constexpr (G > 1) {
+      float* columns = reinterpret_cast<float*>(norm_ring_smem);  // [2][cols]; the ring is idle
+      __syncthreads();
       for (int g = 0; g < G; ++g) {
         if (group == g) {
 #pragma unroll
           for (int j = 0; j < kPer; ++j) {
             const int c = R::template column<TPR>(j, l);
             if (c < cols) {
-              columns[c] = g ? columns[c] + dw[j] : dw[j];
-              columns[cols + c] = g ? columns[cols + c] + db[j] : db[j];
+              columns[c] = g ? columns[c] + fw[j] : fw[j];
+              columns[cols + c] = g ? columns[cols + c] + fb[j] : fb[j];
             }
           }
         }
@@ -248,29 +418,33 @@ __global__ void __launch_bounds__(TPR < 512 ? 512 : TPR) norm_backward_kernel(co
       for (int j = 0; j < kPer; ++j) {
         const int c = R::template column<TPR>(j, l);
         if (c < cols) {
-          out[c] = dw[j];
-          out[cols + c] = db[j];
+          out[c] = fw[j];
+          out[cols + c] = fb[j];
         }
       }
     }
   }
 }
 
-// Sum of the blocks' partials: 32 columns a block, eight threads a column over every eighth part.
-__global__ void __launch_bounds__(256) norm_parts_kernel(const float* parts, int n_parts, int64_t cols, float* dw, float* db) {
-  __shared__ float s[8][33];
+// Sum of the blocks' partials: 32 columns a block, 32 threads a column over every 32nd part.
+__global__ void __launch_bounds__(1024) norm_parts_kernel(const float* parts, int n_parts, int64_t cols, float* dw, float* db) {
+  __shared__ float s[32][33];
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x % 32;
   const int k = threadIdx.x / 32;
   float v = 0.0f;
-  if (i < 2 * cols)
-    for (int p = k; p < n_parts; p += 8) v += parts[p * 2 * cols + i];
+  if (i < 2 * cols) {
+#pragma unroll 4
+    for (int p = k; p < n_parts; p += 32) v += parts[p * 2 * cols + i];
+  }
   s[k][threadIdx.x % 32] = v;
   __syncthreads();
-  if (k == 0 && i < 2 * cols) {
+  v = s[threadIdx.x % 32][k];  // column k of the block, summed over a warp
 #pragma unroll
-    for (int j = 1; j < 8; ++j) v += s[j][threadIdx.x];
-    if (i < cols) dw[i] = v;
-    else db[i - cols] = v;
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + k;
+  if (threadIdx.x % 32 == 0 && c < 2 * cols) {
+    if (c < cols) dw[c] = v;
+    else db[c - cols] = v;
   }
 }
 
@@ -279,20 +453,21 @@ constexpr int kLong = 1024;
 
 template <int DT>
 __global__ void __launch_bounds__(kLong) norm_forward_long_kernel(const NormArgs a) {
-  __shared__ float2 sums[2][kLong / 32];
+  __shared__ float sums[2][kLong / 32][1];
   const float inv = 1.0f / static_cast<float>(a.cols);
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const int64_t off = row * a.ld_x;
-    float s = 0.0f, none = 0.0f, q = 0.0f;
-    for (int64_t c = threadIdx.x; c < a.cols; c += kLong) s += load_elem<DT>(a.x, off + c);
-    row_sums<kLong>(s, none, sums[0], 0);
-    const float mean = s * inv;
+    float s[1] = {0.0f};
+    for (int64_t c = threadIdx.x; c < a.cols; c += kLong) s[0] += load_elem<DT>(a.x, off + c);
+    row_sums<kLong>(s, sums[0], 0);
+    const float mean = s[0] * inv;
+    s[0] = 0.0f;
     for (int64_t c = threadIdx.x; c < a.cols; c += kLong) {
       const float d = load_elem<DT>(a.x, off + c) - mean;
-      q = __fmaf_rn(d, d, q);
+      s[0] = __fmaf_rn(d, d, s[0]);
     }
-    row_sums<kLong>(q, none, sums[1], 0);
-    const float rstd = 1.0f / sqrtf(q * inv + a.eps);
+    row_sums<kLong>(s, sums[1], 0);
+    const float rstd = rsqrt_of(s[0] * inv + a.eps);
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -306,20 +481,19 @@ __global__ void __launch_bounds__(kLong) norm_forward_long_kernel(const NormArgs
 
 template <int DT>
 __global__ void __launch_bounds__(kLong) norm_backward_long_kernel(const NormArgs a) {
-  __shared__ float2 sums[2][kLong / 32];
+  __shared__ float sums[2][kLong / 32][2];
   const float inv = 1.0f / static_cast<float>(a.cols);
   int flip = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, flip ^= 1) {
     const float mean = __ldg(a.mean_in + row), rstd = __ldg(a.rstd_in + row);
-    float s1 = 0.0f, s2 = 0.0f;
+    float s[2] = {0.0f, 0.0f};
     for (int64_t c = threadIdx.x; c < a.cols; c += kLong) {
       const float t = load_elem<DT>(a.dy, row * a.ld_dy + c) * (a.weight ? __ldg(a.weight + c) : 1.0f);
-      s1 += t;
-      s2 = __fmaf_rn(t, (load_elem<DT>(a.x, row * a.ld_x + c) - mean) * rstd, s2);
+      s[0] += t;
+      s[1] = __fmaf_rn(t, (load_elem<DT>(a.x, row * a.ld_x + c) - mean) * rstd, s[1]);
     }
-    row_sums<kLong>(s1, s2, sums[flip], 0);
-    s1 *= inv;
-    s2 *= inv;
+    row_sums<kLong>(s, sums[flip], 0);
+    const float s1 = s[0] * inv, s2 = s[1] * inv;
     for (int64_t c = threadIdx.x; c < a.cols; c += kLong) {
       const float t = load_elem<DT>(a.dy, row * a.ld_dy + c) * (a.weight ? __ldg(a.weight + c) : 1.0f);
       const float n = (load_elem<DT>(a.x, row * a.ld_x + c) - mean) * rstd;
@@ -353,17 +527,20 @@ bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % 
 template <int DT, int E, int TPR>
 qz_status run_forward(const NormArgs& a, cudaStream_t s) {
   constexpr int kBlock = TPR < 256 ? 256 : TPR, G = kBlock / TPR;
-  const int64_t grid = (a.rows + G - 1) / G;
-  norm_forward_kernel<DT, E, TPR><<<static_cast<unsigned>(grid), kBlock, 0, s>>>(a);
+  norm_forward_kernel<DT, E, TPR><<<static_cast<unsigned>((a.rows + G - 1) / G), kBlock, 0, s>>>(a);
   return launch_status();
 }
 
 template <int DT, int E, int TPR>
 qz_status run_backward(const NormArgs& a, int parts, cudaStream_t s) {
-  constexpr int kBlock = TPR < 512 ? 512 : TPR, G = kBlock / TPR;
-  const int smem = a.parts && G > 1 ? static_cast<int>(a.cols) * 8 : 0;
-  if (a.parts) norm_backward_kernel<DT, E, TPR, true><<<parts, kBlock, smem, s>>>(a);
-  else norm_backward_kernel<DT, E, TPR, false><<<parts, kBlock, smem, s>>>(a);
+  constexpr int kBlock = kNormBlock<TPR>, G = kBlock / TPR;
+  constexpr int kColumns = G > 1 ? 2 * TPR * kPer * 4 : 0, kRing = E > 1 ? kNormSlots<DT, TPR> * kNormSlot<DT, TPR> : 0;
+  constexpr int kSmem = kRing > kColumns ? kRing : kColumns;
+  const void* k = a.parts ? reinterpret_cast<const void*>(&norm_backward_kernel<DT, E, TPR, true>)
+                          : reinterpret_cast<const void*>(&norm_backward_kernel<DT, E, TPR, false>);
+  if (kSmem && !set_dyn_smem(k, kSmem)) return QZ_ERR_CUDA;
+  if (a.parts) norm_backward_kernel<DT, E, TPR, true><<<parts, kBlock, kSmem, s>>>(a);
+  else norm_backward_kernel<DT, E, TPR, false><<<parts, kBlock, kSmem, s>>>(a);
   return launch_status();
 }
 
@@ -503,6 +680,6 @@ extern "C" qz_status qz_layer_norm_backward(int32_t dtype, const void* dy, int64
   const int parts = parts_for(rows, cols);
   st = dtype == QZ_BF16 ? run_norm<QZ_BF16>(a, true, parts, s) : run_norm<QZ_F32>(a, true, parts, s);
   if (st != QZ_OK || !dweight) return st;
-  norm_parts_kernel<<<static_cast<unsigned>((2 * cols + 31) / 32), 256, 0, s>>>(a.parts, parts, cols, dweight, dbias);
+  norm_parts_kernel<<<static_cast<unsigned>((2 * cols + 31) / 32), 1024, 0, s>>>(a.parts, parts, cols, dweight, dbias);
   return launch_status();
 }
