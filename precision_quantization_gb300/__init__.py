@@ -721,7 +721,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
         torch = _torch()
         f32, empty, dev = torch.float32, torch.empty, x.device
         y = empty((rows, cols), dtype=x.dtype, device=dev)
-        mean, rstd = empty((rows,), dtype=f32, device=dev), empty((rows,), dtype=f32, device=dev)
+        mean, rstd = empty((2, rows), dtype=f32, device=dev).unbind(0)
         ld_y, pm, pr = cols, mean.data_ptr(), rstd.data_ptr()
     else:
         y, mean, rstd = out
@@ -753,7 +753,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, params: bool = True, out
     if out is None:
         dx, ld_dx = empty((rows, cols), dtype=x.dtype, device=dev), cols
         if params:
-            dw, db = empty((cols,), dtype=f32, device=dev), empty((cols,), dtype=f32, device=dev)
+            dw, db = empty((2, cols), dtype=f32, device=dev).unbind(0)
         _same_tokens(rows, dy=dy)
     else:
         dx, dw, db = out if params else (out[0], None, None)

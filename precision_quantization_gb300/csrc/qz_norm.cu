@@ -397,22 +397,29 @@ __global__ void __launch_bounds__(kNormBlock<TPR>) norm_backward_kernel(const No
     }
     float* out = a.parts + static_cast<int64_t>(blockIdx.x) * 2 * cols;
     if constexpr (G > 1) {
-      float* columns = reinterpret_cast<float*>(norm_ring_smem);  // [2][cols]; the ring is idle
+      // every group's sums side by side, then each column's in group order; the ring is idle
+      constexpr int kWide = TPR * kPer;
+      float* columns = reinterpret_cast<float*>(norm_ring_smem);  // [G][2][kWide]
       __syncthreads();
-      for (int g = 0; g < G; ++g) {
-        if (group == g) {
 #pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            const int c = R::template column<TPR>(j, l);
-            if (c < cols) {
-              columns[c] = g ? columns[c] + fw[j] : fw[j];
-              columns[cols + c] = g ? columns[cols + c] + fb[j] : fb[j];
-            }
-          }
+      for (int j = 0; j < kPer; j += E > 1 ? 4 : 1) {
+        float* at = columns + group * 2 * kWide + R::template column<TPR>(j, l);
+        if constexpr (E > 1) {
+          *reinterpret_cast<float4*>(at) = make_float4(fw[j], fw[j + 1], fw[j + 2], fw[j + 3]);
+          *reinterpret_cast<float4*>(at + kWide) = make_float4(fb[j], fb[j + 1], fb[j + 2], fb[j + 3]);
+        } else {
+          at[0] = fw[j];
+          at[kWide] = fb[j];
         }
-        __syncthreads();
       }
-      for (int i = threadIdx.x; i < 2 * cols; i += kBlock) out[i] = columns[i];
+      __syncthreads();
+      for (int i = threadIdx.x; i < 2 * cols; i += kBlock) {
+        const float* at = columns + (i < cols ? i : i - cols + kWide);
+        float v = at[0];
+#pragma unroll
+        for (int g = 1; g < G; ++g) v += at[g * 2 * kWide];
+        out[i] = v;
+      }
     } else {
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
@@ -534,7 +541,7 @@ qz_status run_forward(const NormArgs& a, cudaStream_t s) {
 template <int DT, int E, int TPR>
 qz_status run_backward(const NormArgs& a, int parts, cudaStream_t s) {
   constexpr int kBlock = kNormBlock<TPR>, G = kBlock / TPR;
-  constexpr int kColumns = G > 1 ? 2 * TPR * kPer * 4 : 0, kRing = E > 1 ? kNormSlots<DT, TPR> * kNormSlot<DT, TPR> : 0;
+  constexpr int kColumns = G > 1 ? 2 * kBlock * kPer * 4 : 0, kRing = E > 1 ? kNormSlots<DT, TPR> * kNormSlot<DT, TPR> : 0;
   constexpr int kSmem = kRing > kColumns ? kRing : kColumns;
   const void* k = a.parts ? reinterpret_cast<const void*>(&norm_backward_kernel<DT, E, TPR, true>)
                           : reinterpret_cast<const void*>(&norm_backward_kernel<DT, E, TPR, false>);
