@@ -85,8 +85,12 @@ __device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&v)[4]) {
   if constexpr (FMT == QZ_INT4) {
     // pairs (q, q + 4): f16 1024 + (n ^ 8), less 1032, is the two's complement value, exactly
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[q]) : "r"(((w >> (4 * q)) & 0x000F000Fu) ^ 0x64086408u), "r"(0x64086408u));
+    for (int q = 0; q < 4; q += 2) {
+      const uint32_t h = q == 0 ? w : w >> 8;
+      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(v[q]) : "r"((h & 0x000F000Fu) ^ 0x64086408u), "r"(0x64086408u));
+      // four bits further up: 1024 + 16 (n ^ 8), times 1 / 16, less 72
+      asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(v[q + 1]) : "r"((h & 0x00F000F0u) ^ 0x64806480u), "r"(0x2C002C00u), "r"(0xD480D480u));
+    }
   } else {
     asm("{\n\t.reg .b8 b<4>;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
         "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
@@ -339,8 +343,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
       const uint32_t x0 = static_cast<uint32_t>(s) * 8u * x_chunk;
       float acc[FMT == QZ_NVFP4 ? 1 : NT][4];  // the sum of a block or group, before its scale
       constexpr int kPer = FMT == QZ_INT4 ? 1 << (LOG - 5) : 1;  // chunks of it
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {  // chunk c: 32 columns, lane t its word t
+      const auto chunk = [&](int c, bool rare) {  // chunk c: 32 columns, lane t its word t
         uint4 xv[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) xv[nt] = *reinterpret_cast<const uint4*>(xa[nt] + x0 + c * x_chunk);
@@ -356,13 +359,13 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
           } else if constexpr (FMT == QZ_MXFP4) {
             const uint32_t E = now[h].v[c >> 2];
             f[h] = __uint_as_float(((c & 3) == 3 ? E >> 1 : E << (23 - 8 * (c & 3))) & 0x7f800000u);
-            if (odd) {
+            if (rare) {
               const uint32_t b = (E >> (8 * (c & 3))) & 255u;
               f[h] = b == 255u ? __uint_as_float(0x7fc00000u) : pow2(static_cast<int>(b) - 127) * (shifted ? kShift : 1.0f);
             }
           } else {
             f[h] = __uint_as_float(now[h].v[c / kPer]);
-            if (odd) f[h] *= kShift;
+            if (rare) f[h] *= kShift;
           }
         }
 #pragma unroll
@@ -380,6 +383,14 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
             }
           }
         }
+      };
+      // (two loops: tests inside one cost its chunks their overlap)
+      if (FMT == QZ_NVFP4 || !odd) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) chunk(c, false);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) chunk(c, true);
       }
     }
     // ---- join the parts, eight tokens at a time, and store ----
