@@ -1,6 +1,6 @@
 // qz_product_few.cuh -- products of a few tokens (decoding, small batches) with 4-bit weights
 // (included once per weight format):
-//   y[t][r] = sum_c kFewWarps[r][c] x[t][c]        (one weight, or gate and up with the activation)
+//   y[t][r] = sum_c W[r][c] x[t][c]        (one weight, or gate and up with the activation)
 //
 // Every weight is used once per token, so the weights' 4 bits (and scales) are the traffic and HBM
 // the bound; what has to fit beside the traffic is the decoding: at HBM speed an SM has about 22
