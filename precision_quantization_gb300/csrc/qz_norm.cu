@@ -11,6 +11,10 @@
 // over the chip, not over memory.  The backward pass is persistent, for the column sums, and each
 // thread copies its own pieces of the next rows into shared memory (cp.async, kAhead rows ahead).
 // Rows longer than 16384 are read again from L2 instead.
+//
+// Measured, 8192 x 4096 bf16: forward 33 us, 4.1 TB/s, bound by its instructions (19 M, issued in
+// 0.53 of the cycles) and the two sums one after the other; backward 41 us, 4.9 TB/s, 4 of them the
+// join of the blocks' column sums.
 #include <climits>
 #include <cstdint>
 
@@ -209,7 +213,7 @@ constexpr int kNormSlots = kNormRoom<DT, TPR> > kAhead + 1 ? kAhead + 1 : kNormR
 
 // One row per group of threads and launch: the forward pass keeps nothing from row to row but the
 // parameters, which come from L1.  (A persistent form with the rows copied ahead, as the backward pass
-// has it, was slower: 43 us against 37 at 8192 x 4096 bf16; it is instructions that bound it.)
+// has it, was slower: 43 us against 33 at 8192 x 4096 bf16; it is instructions that bound it.)
 template <int DT, int E, int TPR>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 6 : TPR == 512 ? 3 : 1) norm_forward_kernel(const NormArgs a) {
   constexpr int kBlock = TPR < 256 ? 256 : TPR, G = kBlock / TPR, kChunks = kPer / E;

@@ -17,8 +17,9 @@ namespace {
 
 // ---- the plain tile kernel ------------------------------------------------------------------
 // A CTA computes 64 tokens x 64 outputs in fp32 FMAs, 32 summands at a time through shared
-// memory, weights decoded as they are loaded.  It is bound by the FMA pipe and serves the calls
-// whose strides or alignment the other kernels do not take.
+// memory, weights decoded as they are loaded.  It is bound by the FMA pipe and the decoding and
+// serves the calls whose strides or alignment the other kernels do not take (gated 4096 tokens of
+// 2 x 16384 x 4096 here: 45 ms, 24 TFLOP/s, against 0.58 ms on the tensor cores).
 constexpr int kTileT = 64, kTileN = 64, kTileK = 32;
 
 template <int FMT>
@@ -136,7 +137,8 @@ qz_status launch_product(const ProductArgs& p, cudaStream_t s) {
 
 // ---- dg = dh u act'(g), du = dh act(g) --------------------------------------------------------
 // Elementwise: three reads and two writes of 2 bytes per element, bound by HBM.  Eight elements
-// a thread when rows and leading dimensions allow 16-byte access, one otherwise.
+// a thread when rows and leading dimensions allow 16-byte access, one otherwise.  4096 x 16384:
+// 99 us, 6.8 TB/s.
 struct GateGradArgs {
   const uint16_t *dh, *g, *u;
   uint16_t *dg, *du;
