@@ -121,9 +121,10 @@ qz_status run_tile(const ProductArgs& p, cudaStream_t s) {
 
 qz_status launch_product(const ProductArgs& p, cudaStream_t s) {
   if (product_few_applicable(p)) {
-    if (p.format == QZ_MXFP4) return launch_product_few_mxfp4(p, s);
-    if (p.format == QZ_NVFP4) return launch_product_few_nvfp4(p, s);
-    return launch_product_few_int4(p, s);
+    const bool whole = few_whole(p);
+    if (p.format == QZ_MXFP4) return whole ? launch_product_few_mxfp4(p, s) : launch_product_few_mxfp4_ragged(p, s);
+    if (p.format == QZ_NVFP4) return whole ? launch_product_few_nvfp4(p, s) : launch_product_few_nvfp4_ragged(p, s);
+    return whole ? launch_product_few_int4(p, s) : launch_product_few_int4_ragged(p, s);
   }
   if (product_tc_applicable(p)) {
     if (p.format == QZ_MXFP4) return launch_product_tc_mxfp4(p, s);
@@ -206,14 +207,19 @@ qz_status launch_gate_grad(const GateGradArgs& a, int act, cudaStream_t s) {
 }  // namespace
 
 bool product_few_applicable(const ProductArgs& p) {
-  // whole steps of 256 columns; an INT4 group of 16 would change inside a 32-wide chunk's sum
-  if (p.mode == kModeBackward || p.tokens > kFewTokens || p.cols == 0 || p.cols % 256 != 0) return false;
+  // whole chunks of 32 columns (16 bytes of codes); an INT4 group of 16 would change inside one's sum
+  if (p.mode == kModeBackward || p.tokens > kFewTokens || p.cols == 0 || p.cols % 32 != 0) return false;
   if (p.format == QZ_INT4 && p.log2_block < 5) return false;
   if (p.rows >= (int64_t{1} << 30) || p.cols >= (int64_t{1} << 30) || few_depth(p) == 0) return false;
-  // a step's scales are aligned vector loads
-  const size_t n = p.format == QZ_MXFP4 || (p.format == QZ_INT4 && p.log2_block == 7) ? 8 : 16;
+  // (NVFP4: the scales of 32 columns are loaded together)
+  const size_t n = p.format == QZ_NVFP4 ? 2 : 1;
   return p.ld_x % 8 == 0 && aligned(p.x0, 16) && aligned(p.w0.codes, 16) && aligned(p.w0.scales, n) &&
          (p.n_weights == 1 || (aligned(p.w1.codes, 16) && aligned(p.w1.scales, n)));
+}
+
+bool few_whole(const ProductArgs& p) {
+  const size_t n = p.format == QZ_MXFP4 || (p.format == QZ_INT4 && p.log2_block == 7) ? 8 : 16;
+  return p.cols % 256 == 0 && aligned(p.w0.scales, n) && (p.n_weights == 1 || aligned(p.w1.scales, n));
 }
 
 bool product_tc_applicable(const ProductArgs& p) {

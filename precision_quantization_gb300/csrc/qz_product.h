@@ -36,16 +36,22 @@ constexpr uint32_t kJoin = 8 * kTokenStride;      // floats of a warp's sums for
 constexpr int kMaxDepth = 6;
 constexpr uint32_t kFewSmem = 225 * 1024;         // dynamic; the barriers are static
 constexpr uint32_t few_fixed(int depth) { return kFewWarps * (depth * kSlot + kJoin * 4) + 1024; }
+inline int64_t few_steps(const ProductArgs& p) { return (p.cols + 255) / 256; }
+// whole steps, whose scales are aligned vectors; else the steps' tails and scales take narrow loads
+bool few_whole(const ProductArgs& p);
 // the deepest ring that leaves room for the activations, 0: none does
 inline int few_depth(const ProductArgs& p) {
   for (int d = kMaxDepth; d >= 2; --d)
-    if (few_fixed(d) + p.tokens * p.cols * 2 <= kFewSmem) return d;
+    if (few_fixed(d) + p.tokens * few_steps(p) * 512 <= kFewSmem) return d;
   return 0;
 }
 bool product_few_applicable(const ProductArgs& p);
 qz_status launch_product_few_mxfp4(const ProductArgs& p, cudaStream_t s);
 qz_status launch_product_few_nvfp4(const ProductArgs& p, cudaStream_t s);
 qz_status launch_product_few_int4(const ProductArgs& p, cudaStream_t s);
+qz_status launch_product_few_mxfp4_ragged(const ProductArgs& p, cudaStream_t s);
+qz_status launch_product_few_nvfp4_ragged(const ProductArgs& p, cudaStream_t s);
+qz_status launch_product_few_int4_ragged(const ProductArgs& p, cudaStream_t s);
 
 // The tcgen05 kernels (qz_product_tc.cuh): applicable when cols % 32 == 0 and codes, activations
 // and their rows are 16-byte aligned.

@@ -136,7 +136,68 @@ __device__ __forceinline__ void load_step_scales(StepScales<FMT, LOG>& s, const 
   }
 }
 
-template <int FMT, int LOG, int NT, bool GATED>
+// One step's scales of weight rows g and g + 8 as this lane loads them ahead.  RAGGED: rows that are
+// not whole steps have their scales at any alignment, so the quad's lanes share the narrow loads (past
+// the row's end: a scale of 1 or 0, the codes there are 0) and exchange the words when they are used.
+template <int FMT, int LOG, bool RAGGED>
+struct AheadScales {
+  StepScales<FMT, LOG> row[2];
+  __device__ __forceinline__ void load(const uint8_t* const (&p)[2], int step, int, int) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) load_step_scales<FMT, LOG>(row[h], p[h], step);
+  }
+  __device__ __forceinline__ void words(StepScales<FMT, LOG> (&s)[2], int) const {
+    s[0] = row[0];
+    s[1] = row[1];
+  }
+};
+template <int FMT, int LOG>
+struct AheadScales<FMT, LOG, true> {
+  static constexpr int kWords = StepScales<FMT, LOG>::kWords;
+  uint32_t raw[FMT == QZ_INT4 ? 2 * kWords : 4];
+  // blocks: scales of a row
+  __device__ __forceinline__ void load(const uint8_t* const (&p)[2], int step, int t, int blocks) {
+    if constexpr (FMT == QZ_MXFP4) {  // lane t: word t % 2 of row t / 2
+      const uint8_t* q = t < 2 ? p[0] : p[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = 8 * step + 4 * (t & 1) + i;
+        raw[i] = b < blocks ? __ldg(q + b) : 127u;
+      }
+    } else if constexpr (FMT == QZ_NVFP4) {  // lane t: word t of both rows; an even number of blocks
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int b = 16 * step + 4 * t + 2 * (i & 1);
+        raw[i] = b < blocks ? __ldg(reinterpret_cast<const uint16_t*>(p[i >> 1] + b)) : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * kWords; ++i) {
+        const int b = kWords * step + i % kWords;
+        raw[i] = b < blocks ? __ldg(reinterpret_cast<const uint32_t*>(p[i / kWords]) + b) : 0u;
+      }
+    }
+  }
+  __device__ __forceinline__ void words(StepScales<FMT, LOG> (&s)[2], int lane) const {
+    if constexpr (FMT == QZ_MXFP4) {
+      const uint32_t w = __byte_perm(__byte_perm(raw[0], raw[1], 0x0040), __byte_perm(raw[2], raw[3], 0x0040), 0x5410);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i >> 1].v[i & 1] = __shfl_sync(kFull, w, (lane & 28) | i);
+    } else if constexpr (FMT == QZ_NVFP4) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w = raw[2 * h] | raw[2 * h + 1] << 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[h].v[i] = __shfl_sync(kFull, w, (lane & 28) | i);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * kWords; ++i) s[i / kWords].v[i % kWords] = raw[i];
+    }
+  }
+};
+
+template <int FMT, int LOG, int NT, bool GATED, bool RAGGED>
 __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __grid_constant__ FewArgs a) {
   extern __shared__ uint8_t few_raw[];
   __shared__ __align__(8) uint64_t s_full[kFewWarps][kMaxDepth];
@@ -191,7 +252,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
   {
     constexpr int kHeld = 8, kAll = 32 * kFewWarps;
     // a round holds up to eight pieces of 8 values a thread, each of them kAll consecutive pieces of one token
-    const int per_token = a.x_chunks * 4, blocks = (per_token + kAll - 1) / kAll, n = blocks * tokens;
+    const int per_token = a.x_chunks * 4, per_row = static_cast<int>(p.cols / 8), blocks = (per_token + kAll - 1) / kAll, n = blocks * tokens;
     uint4 v[kHeld];
     // the round's blocks one after the other: (tok, blk), uniform over the CTA
     const auto each = [&](int base_tok, int base_blk, auto&& f) {
@@ -208,7 +269,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
     };
     const auto load = [&](int i, int tok, int c) {
       v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (c < per_token) v[i] = __ldg(reinterpret_cast<const uint4*>(p.x0 + tok * p.ld_x) + c);
+      if (c < per_row) v[i] = __ldg(reinterpret_cast<const uint4*>(p.x0 + tok * p.ld_x) + c);
     };
     const auto magnitude = [&](int i, int tok, int) {
       const uint32_t w[4] = {v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu, v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu};
@@ -267,7 +328,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
   const uint32_t x_chunk = 64u * tokens;
 
   // scales of rows g and g + 8, one step ahead
-  StepScales<FMT, LOG> next[2];
+  AheadScales<FMT, LOG, RAGGED> next;
+  const int row_blocks = static_cast<int>(p.cols >> p.log2_block);
   int ntile = tile0, ns = s_begin;
   const uint8_t* pr[2];
   const auto point = [&]() {
@@ -276,8 +338,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
       pr[h] = static_cast<const uint8_t*>(second ? p.w1.scales : p.w0.scales) + min(ntile * 16 + g + 8 * h, rows - 1) * a.scale_pitch;
   };
   const auto load_next = [&]() {  // (past the last tile: its last row's again)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) load_step_scales<FMT, LOG>(next[h], pr[h], ns);
+    next.load(pr, ns, t, row_blocks);
     if (++ns == s_end) {
       ns = s_begin;
       ntile += tile_step;
@@ -295,7 +356,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
     bool shifted = false;  // z is in units of 2^64 (see kShift)
 #pragma unroll 1
     for (int s = s_begin; s < s_end; ++s) {
-      StepScales<FMT, LOG> now[2] = {next[0], next[1]};
+      StepScales<FMT, LOG> now[2];
+      next.words(now, lane);
       load_next();
       few_wait(full + 8u * ci, cph, &s_abort);
       __syncwarp();  // the slot before is read by every lane
@@ -455,16 +517,16 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
     }
 }
 
-template <int FMT, int LOG, int NT, bool GATED>
+template <int FMT, int LOG, int NT, bool GATED, bool RAGGED>
 qz_status run_few(const FewArgs& a, cudaStream_t s) {
-  const void* k = reinterpret_cast<const void*>(&product_few_kernel<FMT, LOG, NT, GATED>);
+  const void* k = reinterpret_cast<const void*>(&product_few_kernel<FMT, LOG, NT, GATED, RAGGED>);
   if (!set_dyn_smem(k, static_cast<int>(kFewSmem))) return QZ_ERR_CUDA;
   const int grid = std::min((a.tiles + a.groups - 1) / a.groups, sm_count());
-  const size_t smem = few_fixed(a.depth) + static_cast<size_t>(a.p.tokens * a.p.cols * 2);
-  product_few_kernel<FMT, LOG, NT, GATED><<<grid, 32 * kFewWarps, smem, s>>>(a);
+  const size_t smem = few_fixed(a.depth) + static_cast<size_t>(a.p.tokens * few_steps(a.p) * 512);
+  product_few_kernel<FMT, LOG, NT, GATED, RAGGED><<<grid, 32 * kFewWarps, smem, s>>>(a);
   return launch_status();
 }
-template <int FMT, int LOG, bool GATED>
+template <int FMT, int LOG, bool GATED, bool RAGGED>
 qz_status run_few_nt(FewArgs& a, cudaStream_t s) {
   const ProductArgs& p = a.p;
   const int nt = static_cast<int>((p.tokens + 7) / 8), sms = sm_count();
@@ -485,10 +547,10 @@ qz_status run_few_nt(FewArgs& a, cudaStream_t s) {
   }
   a.depth = few_depth(p);
   switch (nt) {
-    case 1: return run_few<FMT, LOG, 1, GATED>(a, s);
-    case 2: return run_few<FMT, LOG, 2, GATED>(a, s);
-    case 3: return run_few<FMT, LOG, 3, GATED>(a, s);
-    default: return run_few<FMT, LOG, 4, GATED>(a, s);
+    case 1: return run_few<FMT, LOG, 1, GATED, RAGGED>(a, s);
+    case 2: return run_few<FMT, LOG, 2, GATED, RAGGED>(a, s);
+    case 3: return run_few<FMT, LOG, 3, GATED, RAGGED>(a, s);
+    default: return run_few<FMT, LOG, 4, GATED, RAGGED>(a, s);
   }
 }
 bool encode_codes(CUtensorMap* m, const ProductArgs& p, const WeightView& w) {
@@ -502,22 +564,22 @@ bool encode_codes(CUtensorMap* m, const ProductArgs& p, const WeightView& w) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int FMT>
+template <int FMT, bool RAGGED = false>
 qz_status launch_few(const ProductArgs& p, cudaStream_t s) {
   FewArgs a{};
   a.p = p;
   if (!encode_codes(&a.map_w0, p, p.w0) || (p.n_weights == 2 && !encode_codes(&a.map_w1, p, p.w1))) return QZ_ERR_CUDA;
   a.tiles = static_cast<int>((p.rows + 15) / 16);
-  a.steps = static_cast<int>(p.cols / 256);
+  a.steps = static_cast<int>(few_steps(p));
   a.x_chunks = 8 * a.steps;
   a.scale_pitch = (p.cols >> p.log2_block) * (FMT == QZ_INT4 ? 4 : 1);
   const bool two = p.mode == kModeGated;
   if constexpr (FMT == QZ_INT4) {
-    if (p.log2_block == 5) return two ? run_few_nt<FMT, 5, true>(a, s) : run_few_nt<FMT, 5, false>(a, s);
-    if (p.log2_block == 6) return two ? run_few_nt<FMT, 6, true>(a, s) : run_few_nt<FMT, 6, false>(a, s);
-    return two ? run_few_nt<FMT, 7, true>(a, s) : run_few_nt<FMT, 7, false>(a, s);
+    if (p.log2_block == 5) return two ? run_few_nt<FMT, 5, true, RAGGED>(a, s) : run_few_nt<FMT, 5, false, RAGGED>(a, s);
+    if (p.log2_block == 6) return two ? run_few_nt<FMT, 6, true, RAGGED>(a, s) : run_few_nt<FMT, 6, false, RAGGED>(a, s);
+    return two ? run_few_nt<FMT, 7, true, RAGGED>(a, s) : run_few_nt<FMT, 7, false, RAGGED>(a, s);
   } else {
-    return two ? run_few_nt<FMT, 0, true>(a, s) : run_few_nt<FMT, 0, false>(a, s);
+    return two ? run_few_nt<FMT, 0, true, RAGGED>(a, s) : run_few_nt<FMT, 0, false, RAGGED>(a, s);
   }
 }
 

@@ -82,6 +82,34 @@ def test_linear_strides(qz, tokens, view, cols):
     check_linear(qz, w, F.activations(rng, tokens, cols), **view)
 
 
+@pytest.mark.parametrize("offset", [0, 1, 2])
+@pytest.mark.parametrize("fmt,group", [("mxfp4", 32), ("nvfp4", 16), ("int4", 32), ("int4", 64), ("int4", 128)])
+@pytest.mark.parametrize("shape", [(1, 33, 32), (1, 50, 224), (4, 1003, 288), (6, 16, 992), (11, 40, 1376), (20, 70, 544),
+                                   (32, 31, 96), (27, 300, 4064)])
+def test_linear_narrow_rows(qz, fmt, group, shape, offset):
+    """Up to 32 tokens with rows that are not whole 256-column steps, and scales at odd places."""
+    import torch
+    tokens, rows, cols = shape[0], shape[1], -(-shape[2] // group) * group
+    rng = np.random.default_rng(hash(shape) % 1000 + group)
+    w = F.make_weight(rng, fmt, rows, cols, group, exact=True)
+    x = F.activations(rng, tokens, cols, exact=True)
+    h = F.handle(w)
+    if offset:
+        s = h.q.scales.reshape(-1)
+        buf = torch.zeros(s.numel() + offset, dtype=s.dtype, device="cuda")
+        buf[offset:] = s
+        h.q.scales = buf[offset:].reshape(h.q.scales.shape)
+        h = qz.Weight(h.q)
+    got = F.host(qz.linear(F.bf16_cuda(x), h, out_dtype=torch.float32))
+    assert np.array_equal(got, x @ w["values"].T)
+    if not offset:
+        check_linear(qz, F.make_weight(rng, fmt, rows, cols, group), F.activations(rng, tokens, cols), "f32")
+        up = F.handle(w)
+        hid, g, u = qz.gated_ffn(F.bf16_cuda(x), h, up, save=True)
+        assert np.array_equal(F.host(g), F.host(u))
+        assert np.all(np.abs(F.host(g) - x @ w["values"].T) <= F.bf16_bound(x @ w["values"].T))
+
+
 @pytest.mark.parametrize("tokens", [1, 5, 70])
 def test_linear_codes_offset(qz, tokens):
     """Codes that start at an odd byte, and an output view inside a larger tensor."""
