@@ -424,7 +424,7 @@ typedef enum {
  *   tokens == 0 or an empty output enqueues nothing; an empty sum is 0.
  *   Alignment: any pointer and leading dimension of the element type's own alignment is right;
  *   16-byte aligned codes and activations, leading dimensions that are multiples of 8 and cols a
- *   multiple of 32 get the fast kernels (up to 32 tokens: cols a multiple of 256 the fastest).
+ *   multiple of 32 get the fast kernels.
  *   Waits inside the kernels are bounded (1 s); should one give up, the outputs it stands for are NaN.
  *   Asynchronous on `stream`; no workspace. */
 

@@ -26,9 +26,12 @@ struct ProductArgs {
   int64_t ld_gu;
 };
 
-// The streaming kernels for up to kFewTokens tokens (qz_product_few.cuh): their shared memory is a ring
+// The streaming kernels for a few tokens (qz_product_few.cuh): their shared memory is a ring
 // of code boxes and a buffer of partial sums per warp, and the activations.
-constexpr int kFewTokens = 32;
+// Tokens they take at most.  E2M1 weights: 16 (4096 x 4096: 16 tokens 14.5 us against 16.5 on the
+// tensor-core tiles, 17 tokens 16.5 both; 8192 x 4096: 18 and 21 against 16.5).  INT4, whose tiles take
+// two products a weight: 32 (4096 x 4096: 17 tokens 16.5 us against 27).
+constexpr int few_tokens(int format) { return format == QZ_INT4 ? 32 : 16; }
 constexpr int kFewWarps = 16;
 constexpr int kTokenStride = 20;                  // floats of a token's 16 sums (banks 8 t + g)
 constexpr uint32_t kSlot = 2048;                  // a step: 16 rows x 128 bytes of codes
@@ -38,6 +41,8 @@ constexpr uint32_t kFewSmem = 225 * 1024;         // dynamic; the barriers are s
 constexpr uint32_t few_fixed(int depth) { return kFewWarps * (depth * kSlot + kJoin * 4) + 1024; }
 inline int64_t few_steps(const ProductArgs& p) { return (p.cols + 255) / 256; }
 // whole steps, whose scales are aligned vectors; else the steps' tails and scales take narrow loads
+// (4 tokens, 32768 outputs, MXFP4: 8192 columns 39 us; 8160 columns 41 us, on the tensor-core tiles 70;
+// INT4 groups of 32: 54, 56 and 134)
 bool few_whole(const ProductArgs& p);
 // the deepest ring that leaves room for the activations, 0: none does
 inline int few_depth(const ProductArgs& p) {

@@ -546,12 +546,12 @@ qz_status run_few_nt(FewArgs& a, cudaStream_t s) {
     }
   }
   a.depth = few_depth(p);
-  switch (nt) {
-    case 1: return run_few<FMT, LOG, 1, GATED, RAGGED>(a, s);
-    case 2: return run_few<FMT, LOG, 2, GATED, RAGGED>(a, s);
-    case 3: return run_few<FMT, LOG, 3, GATED, RAGGED>(a, s);
-    default: return run_few<FMT, LOG, 4, GATED, RAGGED>(a, s);
+  if (nt == 1) return run_few<FMT, LOG, 1, GATED, RAGGED>(a, s);
+  if constexpr (few_tokens(FMT) > 16) {
+    if (nt == 3) return run_few<FMT, LOG, 3, GATED, RAGGED>(a, s);
+    if (nt == 4) return run_few<FMT, LOG, 4, GATED, RAGGED>(a, s);
   }
+  return run_few<FMT, LOG, 2, GATED, RAGGED>(a, s);
 }
 bool encode_codes(CUtensorMap* m, const ProductArgs& p, const WeightView& w) {
   const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());

@@ -82,6 +82,24 @@ def test_linear_strides(qz, tokens, view, cols):
     check_linear(qz, w, F.activations(rng, tokens, cols), **view)
 
 
+@pytest.mark.parametrize("tokens", [8, 9, 10, 15, 16, 17])
+@pytest.mark.parametrize("cols", [8192, 9088])
+def test_int4_tokens_in_two_halves(qz, tokens, cols):
+    """Activations too large for one CTA's shared memory, next to ones that still fit."""
+    import torch
+    rng = np.random.default_rng(tokens + cols)
+    w = F.make_weight(rng, "int4", 45, cols, 64, exact=True)
+    x = F.activations(rng, tokens, cols, exact=True)
+    h, want = F.handle(w), x @ w["values"].T
+    for dt, pad in ((torch.float32, 0), (torch.bfloat16, 3)):
+        buf = torch.full((tokens, 45 + pad), 7.0, dtype=dt, device="cuda")
+        qz.linear(F.bf16_cuda(x, pad=8), h, out=buf[:, :45])
+        assert np.all(np.abs(F.host(buf[:, :45]) - want) <= (F.bf16_bound(want) if dt == torch.bfloat16 else 0))
+        assert bool((buf[:, 45:] == 7).all())
+    _, g, u = qz.gated_ffn(F.bf16_cuda(x), h, h, save=True)
+    assert np.array_equal(F.host(g), F.host(u)) and np.all(np.abs(F.host(g) - want) <= F.bf16_bound(want))
+
+
 @pytest.mark.parametrize("offset", [0, 1, 2])
 @pytest.mark.parametrize("fmt,group", [("mxfp4", 32), ("nvfp4", 16), ("int4", 32), ("int4", 64), ("int4", 128)])
 @pytest.mark.parametrize("shape", [(1, 33, 32), (1, 50, 224), (4, 1003, 288), (6, 16, 992), (11, 40, 1376), (20, 70, 544),

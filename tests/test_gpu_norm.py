@@ -109,6 +109,47 @@ def test_backward(qz, dtype, affine, shape):
     assert all(np.array_equal(F.host(p), F.host(q)) for p, q in zip(again, (dx, dw, db)))
 
 
+def placed(a, dtype, lead, ld, fill):
+    """The matrix as a view: `lead` values into a buffer of `fill`, rows `ld` apart."""
+    import torch
+    rows, cols = a.shape
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    buf = torch.full((lead + rows * ld + 8,), fill, dtype=dt, device="cuda")
+    view = buf.as_strided((rows, cols), (ld, 1), lead)
+    view.copy_(torch.from_numpy(np.ascontiguousarray(a)).to(dt).cuda())
+    return buf, view
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lead,pad", [(0, 0), (1, 0), (3, 2), (6, 5), (7, 8)])
+@pytest.mark.parametrize("shape", [(1, 1), (1, 7), (2, 15), (17, 63), (1300, 37), (310, 505), (300, 1021), (160, 2047), (170, 4095),
+                                   (30, 8185), (18, 16377), (9, 16383)])
+def test_backward_rows_at_any_place(qz, dtype, lead, pad, shape):
+    """Rows that start anywhere between two 16-byte boundaries: the values around them (NaN) stay
+    out of the results and what surrounds dx stays as it was."""
+    rows, cols = shape
+    rng = np.random.default_rng(rows + 3 * cols + lead)
+    x, dy, w, _ = inputs(rng, rows, cols, dtype)
+    _, m, r = forward(x, w, 0, 1e-5)
+    m, r = (v.astype(np.float32).astype(np.float64) for v in (m, r))
+    _, vx = placed(x, dtype, lead, cols + pad, float("nan"))
+    _, vdy = placed(dy, dtype, lead + 8, cols + pad + 8, float("nan"))
+    buf, vdx = placed(np.zeros_like(x), dtype, lead, cols + pad, 5.0)
+    dw, db = f32(np.zeros(cols)), f32(np.zeros(cols))
+    qz.layer_norm_backward(vdy, vx, f32(m[:, 0]), f32(r[:, 0]), f32(w), out=(vdx, dw, db))
+    n = (x - m) * r
+    t = dy * w
+    want = r * (t - t.mean(-1, keepdims=True) - n * (t * n).mean(-1, keepdims=True))
+    mag = np.abs(t) + np.abs(t).mean(-1, keepdims=True) + np.abs(n) * np.abs(t * n).mean(-1, keepdims=True)
+    bound = (u_of(cols) + 2.0 ** -20) * r * mag * (1 + np.abs(m) * r)
+    F.assert_within(F.host(vdx), want, bound + (F.bf16_bound(want) if dtype == "bf16" else 0), "dx")
+    cu = (rows + 64) * 2.0 ** -24
+    F.assert_within(F.host(dw), (dy * n).sum(0), cu * (np.abs(dy) * (np.abs(n) + np.abs(m) * r)).sum(0) + 1e-30, "dweight")
+    F.assert_within(F.host(db), dy.sum(0), cu * np.abs(dy).sum(0) + 1e-30, "dbias")
+    vdx.fill_(5.0)
+    assert bool((buf == 5).all())
+
+
 def test_gradient_is_the_difference(qz):
     """sum(dy * y) moved by +-h along a direction, through the fp32 kernel itself."""
     rng = np.random.default_rng(4)
