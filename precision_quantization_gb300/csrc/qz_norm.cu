@@ -12,8 +12,8 @@
 // thread copies its own pieces of the next rows into shared memory (cp.async, kAhead rows ahead).
 // Rows longer than 16384 are read again from L2 instead.
 //
-// Measured, 8192 x 4096 bf16: forward 33 us, 4.1 TB/s, bound by its instructions (19 M, issued in
-// 0.53 of the cycles) and the two sums one after the other; backward 41 us, 4.9 TB/s, 4 of them the
+// Measured, 8192 x 4096 bf16: forward 28.7 us, 4.7 TB/s, bound by L1 (the parameters, 8 bytes a column
+// against 4 of x and y) and the two sums one after the other; backward 41 us, 4.9 TB/s, 4 of them the
 // join of the blocks' column sums.
 #include <climits>
 #include <cstdint>
@@ -211,54 +211,64 @@ constexpr int kNormRoom = 192 * 1024 / kNormSlot<DT, TPR>;
 template <int DT, int TPR>
 constexpr int kNormSlots = kNormRoom<DT, TPR> > kAhead + 1 ? kAhead + 1 : kNormRoom<DT, TPR>;
 
-// One row per group of threads and launch: the forward pass keeps nothing from row to row but the
-// parameters, which come from L1.  (A persistent form with the rows copied ahead, as the backward pass
-// has it, was slower: 43 us against 33 at 8192 x 4096 bf16; it is instructions that bound it.)
-template <int DT, int E, int TPR>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 6 : TPR == 512 ? 3 : 1) norm_forward_kernel(const NormArgs a) {
+// ROWS rows per group of threads and launch: the forward pass keeps nothing from row to row but the
+// parameters, which come from L1 and there take more of the wavefronts than the rows themselves; two
+// rows share them and the chains of their sums (8192 x 4096 bf16: 33 -> 28.7 us).  (A persistent form with
+// the rows copied ahead, as the backward pass has it, was slower: 43 us.)
+template <int DT, int E, int TPR, int ROWS>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR == 1024 ? 1 : (ROWS == 2 ? 1024 : 1536) / (TPR < 256 ? 256 : TPR))
+norm_forward_kernel(const NormArgs a) {
   constexpr int kBlock = TPR < 256 ? 256 : TPR, G = kBlock / TPR, kChunks = kPer / E;
   using R = RowRegs<DT, E>;
-  __shared__ float sums[G][2][TPR > 32 ? TPR / 32 : 1][1];
+  __shared__ float sums[G][2][TPR > 32 ? TPR / 32 : 1][ROWS];
   const int group = threadIdx.x / TPR, l = threadIdx.x % TPR, cols = static_cast<int>(a.cols);
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * G + group) * ROWS;
   if (row >= a.rows) return;
-  R x;
-  x.template load<TPR>(a.x, row * a.ld_x, l, cols);
-  float s[1] = {0.0f}, d[kPer];
+  R x[ROWS];
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) s[0] += x.get(j);
+  for (int k = 0; k < ROWS; ++k) x[k].template load<TPR>(a.x, (row + k < a.rows ? row + k : row) * a.ld_x, l, cols);
+  float s[ROWS], mean[ROWS], rstd[ROWS];
+  const float inv = 1.0f / static_cast<float>(cols);
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    s[k] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) s[k] += x[k].get(j);
+  }
   row_sums<TPR>(s, sums[group][0], group);
-  const float inv = 1.0f / static_cast<float>(cols), mean = s[0] * inv;
-  s[0] = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kChunks; ++i) {
-    if (E * (i * TPR + l) < cols) {  // a chunk lies wholly in the row or not at all
+  for (int k = 0; k < ROWS; ++k) {
+    mean[k] = s[k] * inv;
+    s[k] = 0.0f;
 #pragma unroll
-      for (int j = E * i; j < E * i + E; ++j) {
-        d[j] = x.get(j) - mean;
-        s[0] = __fmaf_rn(d[j], d[j], s[0]);
+    for (int i = 0; i < kChunks; ++i) {
+      if (E * (i * TPR + l) < cols) {  // a chunk lies wholly in the row or not at all
+#pragma unroll
+        for (int j = E * i; j < E * i + E; ++j) {
+          const float d = x[k].get(j) - mean[k];
+          s[k] = __fmaf_rn(d, d, s[k]);
+        }
       }
     }
   }
   row_sums<TPR>(s, sums[group][1], group);
-  const float rstd = rsqrt_of(s[0] * inv + a.eps);
-  if (l == 0) {
-    if (a.mean) a.mean[row] = mean;
-    if (a.rstd) a.rstd[row] = rstd;
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    rstd[k] = rsqrt_of(s[k] * inv + a.eps);
+    if (l == 0 && row + k < a.rows) {
+      if (a.mean) a.mean[row + k] = mean[k];
+      if (a.rstd) a.rstd[row + k] = rstd[k];
+    }
   }
 #pragma unroll
   for (int i = 0; i < kChunks; ++i) {
     const int c = E * (i * TPR + l);
     if (c >= cols) continue;
-    float y[E];
-#pragma unroll
-    for (int j = 0; j < E; ++j) y[j] = d[E * i + j] * rstd;
+    float w[E], b[E];
     if constexpr (E == 1) {
-      if (a.weight) y[0] *= __ldg(a.weight + c);
-      if (a.bias) y[0] += __ldg(a.bias + c);
-      store_elem<DT>(a.y, row * a.ld_y + c, y[0]);
+      w[0] = a.weight ? __ldg(a.weight + c) : 1.0f;
+      b[0] = a.bias ? __ldg(a.bias + c) : 0.0f;
     } else {
-      float w[E], b[E];
 #pragma unroll
       for (int j = 0; j < E; j += 4) {
         float4 v = make_float4(1.0f, 1.0f, 1.0f, 1.0f), u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -267,12 +277,22 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR <= 256 ? 6 : TPR ==
         w[j] = v.x; w[j + 1] = v.y; w[j + 2] = v.z; w[j + 3] = v.w;
         b[j] = u.x; b[j + 1] = u.y; b[j + 2] = u.z; b[j + 3] = u.w;
       }
+    }
 #pragma unroll
-      for (int j = 0; j < E; ++j) y[j] = __fmaf_rn(y[j], w[j], b[j]);
-      uint4 o;
-      if constexpr (DT == QZ_BF16) o = make_uint4(bf16x2_bits(y[0], y[1]), bf16x2_bits(y[2], y[3]), bf16x2_bits(y[E - 4], y[E - 3]), bf16x2_bits(y[E - 2], y[E - 1]));
-      else o = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
-      *reinterpret_cast<uint4*>(static_cast<char*>(a.y) + (row * a.ld_y + c) * (16 / E)) = o;
+    for (int k = 0; k < ROWS; ++k) {
+      if (row + k >= a.rows) break;
+      const int64_t at = (row + k) * a.ld_y + c;
+      float y[E];
+#pragma unroll
+      for (int j = 0; j < E; ++j) y[j] = __fmaf_rn((x[k].get(E * i + j) - mean[k]) * rstd[k], w[j], b[j]);
+      if constexpr (E == 1) {
+        store_elem<DT>(a.y, at, y[0]);
+      } else {
+        uint4 o;
+        if constexpr (DT == QZ_BF16) o = make_uint4(bf16x2_bits(y[0], y[1]), bf16x2_bits(y[2], y[3]), bf16x2_bits(y[E - 4], y[E - 3]), bf16x2_bits(y[E - 2], y[E - 1]));
+        else o = make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
+        *reinterpret_cast<uint4*>(static_cast<char*>(a.y) + at * (16 / E)) = o;
+      }
     }
   }
 }
@@ -538,7 +558,13 @@ bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % 
 template <int DT, int E, int TPR>
 qz_status run_forward(const NormArgs& a, cudaStream_t s) {
   constexpr int kBlock = TPR < 256 ? 256 : TPR, G = kBlock / TPR;
-  norm_forward_kernel<DT, E, TPR><<<static_cast<unsigned>((a.rows + G - 1) / G), kBlock, 0, s>>>(a);
+  // two rows a group where the GPU stays full with them
+  if (TPR < 1024 && a.rows >= static_cast<int64_t>(2 * sm_count()) * (2048 / kBlock) * G) {
+    constexpr int kRows = TPR < 1024 ? 2 : 1;
+    norm_forward_kernel<DT, E, TPR, kRows><<<static_cast<unsigned>((a.rows + kRows * G - 1) / (kRows * G)), kBlock, 0, s>>>(a);
+  } else {
+    norm_forward_kernel<DT, E, TPR, 1><<<static_cast<unsigned>((a.rows + G - 1) / G), kBlock, 0, s>>>(a);
+  }
   return launch_status();
 }
 
