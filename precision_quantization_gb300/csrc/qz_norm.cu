@@ -6,8 +6,7 @@
 //
 // Bound by HBM: the forward pass reads x and writes y, the backward pass reads dy and x and
 // writes dx; everything else is per row or per column.  So a row is read once and held in
-// registers, 16 values a thread (kPer), by 32 to 1024 threads (TPR, the smallest power of two
-// that covers the row): the squares are taken about the mean from the registers, a second pass
+// registers, 16 values a thread (kPer), by 32 to 1024 threads (TPR, see threads_per_row): the squares are taken about the mean from the registers, a second pass
 // over the chip, not over memory.  The backward pass is persistent, for the column sums, and each
 // thread copies its own pieces of the next rows into shared memory (cp.async, kAhead rows ahead).
 // Rows longer than 16384 are read again from L2 instead.
@@ -181,9 +180,9 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*buf)[N], int gro
     }
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(TPR) : "memory");
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = buf[threadIdx.x % W][i];
+    for (int i = 0; i < N; ++i) v[i] = (W & (W - 1)) == 0 ? buf[threadIdx.x % W][i] : (threadIdx.x & 31) < W ? buf[threadIdx.x & 31][i] : 0.0f;
 #pragma unroll
-    for (int o = W / 2; o; o >>= 1)
+    for (int o = (W & (W - 1)) == 0 ? W / 2 : 16; o; o >>= 1)
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kFull, v[i], o);
   }
@@ -200,8 +199,20 @@ constexpr int kAhead = 5;  // rows a thread copies ahead at most
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Threads a row takes: the smallest of these that hold it.  (Powers of two alone left half of them idle
+// just above one: 4092 x 8200 bf16, forward 72 -> 43 us, backward 152 -> 72 us with 640 for 1024.)
+int threads_per_row(int64_t cols) {
+  for (int t : {32, 64, 128, 192, 256, 384, 512, 640, 768})
+    if (t * kPer >= cols) return t;
+  return 1024;
+}
+// threads of a block of the backward pass
+constexpr int norm_block(int tpr) { return tpr == 192 || tpr == 384 ? 384 : tpr < 512 ? 512 : tpr; }
 template <int TPR>
-constexpr int kNormBlock = TPR < 512 ? 512 : TPR;
+constexpr int kNormBlock = norm_block(TPR);
+// threads of a block of the forward pass
+template <int TPR>
+constexpr int kForwardBlock = TPR < 192 ? 256 : TPR;
 // The backward pass's ring: a slot is one row of x and dy for every group of the block, and there are
 // as many (kAhead + 1 at most) as fit 192 KiB.
 template <int DT, int TPR>
@@ -216,9 +227,9 @@ constexpr int kNormSlots = kNormRoom<DT, TPR> > kAhead + 1 ? kAhead + 1 : kNormR
 // rows share them and the chains of their sums (8192 x 4096 bf16: 33 -> 28.7 us).  (A persistent form with
 // the rows copied ahead, as the backward pass has it, was slower: 43 us.)
 template <int DT, int E, int TPR, int ROWS>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR == 1024 ? 1 : (ROWS == 2 ? 1024 : 1536) / (TPR < 256 ? 256 : TPR))
+__global__ void __launch_bounds__(kForwardBlock<TPR>, (ROWS == 2 ? 1024 : 1536) / kForwardBlock<TPR>)
 norm_forward_kernel(const NormArgs a) {
-  constexpr int kBlock = TPR < 256 ? 256 : TPR, G = kBlock / TPR, kChunks = kPer / E;
+  constexpr int kBlock = kForwardBlock<TPR>, G = kBlock / TPR, kChunks = kPer / E;
   using R = RowRegs<DT, E>;
   __shared__ float sums[G][2][TPR > 32 ? TPR / 32 : 1][ROWS];
   const int group = threadIdx.x / TPR, l = threadIdx.x % TPR, cols = static_cast<int>(a.cols);
@@ -557,10 +568,10 @@ bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % 
 
 template <int DT, int E, int TPR>
 qz_status run_forward(const NormArgs& a, cudaStream_t s) {
-  constexpr int kBlock = TPR < 256 ? 256 : TPR, G = kBlock / TPR;
+  constexpr int kBlock = kForwardBlock<TPR>, G = kBlock / TPR;
   // two rows a group where the GPU stays full with them
-  if (TPR < 1024 && a.rows >= static_cast<int64_t>(2 * sm_count()) * (2048 / kBlock) * G) {
-    constexpr int kRows = TPR < 1024 ? 2 : 1;
+  if (TPR <= 512 && a.rows >= static_cast<int64_t>(2 * sm_count()) * (2048 / kBlock) * G) {
+    constexpr int kRows = TPR <= 512 ? 2 : 1;
     norm_forward_kernel<DT, E, TPR, kRows><<<static_cast<unsigned>((a.rows + kRows * G - 1) / (kRows * G)), kBlock, 0, s>>>(a);
   } else {
     norm_forward_kernel<DT, E, TPR, 1><<<static_cast<unsigned>((a.rows + G - 1) / G), kBlock, 0, s>>>(a);
@@ -583,15 +594,38 @@ qz_status run_backward(const NormArgs& a, int parts, cudaStream_t s) {
 
 template <int DT, int E>
 qz_status run_held(const NormArgs& a, bool backward, int parts, cudaStream_t s) {
-  int tpr = 32;
-  while (tpr * kPer < a.cols) tpr *= 2;
+  const int tpr = threads_per_row(a.cols);
+  if (!backward) {
+    switch (tpr) {
+      case 32: return run_forward<DT, E, 32>(a, s);
+      case 64: return run_forward<DT, E, 64>(a, s);
+      case 128: return run_forward<DT, E, 128>(a, s);
+      case 192: return run_forward<DT, E, 192>(a, s);
+      case 256: return run_forward<DT, E, 256>(a, s);
+      case 384: return run_forward<DT, E, 384>(a, s);
+      case 512: return run_forward<DT, E, 512>(a, s);
+      case 640: return run_forward<DT, E, 640>(a, s);
+      case 768: return run_forward<DT, E, 768>(a, s);
+      default: return run_forward<DT, E, 1024>(a, s);
+    }
+  }
+  // 192 and 384 threads make blocks of 384: fp32 rows gain (16320 x 2056: 88 -> 70 us; 8176 x 4104: 92 ->
+  // 70), bf16 rows have more instructions a byte and want the warps (68 -> 86 us; 84 -> 92)
+  if constexpr (DT == QZ_F32) {
+    if (tpr == 192) return run_backward<DT, E, 192>(a, parts, s);
+    if (tpr == 384) return run_backward<DT, E, 384>(a, parts, s);
+  }
   switch (tpr) {
-    case 32: return backward ? run_backward<DT, E, 32>(a, parts, s) : run_forward<DT, E, 32>(a, s);
-    case 64: return backward ? run_backward<DT, E, 64>(a, parts, s) : run_forward<DT, E, 64>(a, s);
-    case 128: return backward ? run_backward<DT, E, 128>(a, parts, s) : run_forward<DT, E, 128>(a, s);
-    case 256: return backward ? run_backward<DT, E, 256>(a, parts, s) : run_forward<DT, E, 256>(a, s);
-    case 512: return backward ? run_backward<DT, E, 512>(a, parts, s) : run_forward<DT, E, 512>(a, s);
-    default: return backward ? run_backward<DT, E, 1024>(a, parts, s) : run_forward<DT, E, 1024>(a, s);
+    case 32: return run_backward<DT, E, 32>(a, parts, s);
+    case 64: return run_backward<DT, E, 64>(a, parts, s);
+    case 128: return run_backward<DT, E, 128>(a, parts, s);
+    case 192:
+    case 256: return run_backward<DT, E, 256>(a, parts, s);
+    case 384:
+    case 512: return run_backward<DT, E, 512>(a, parts, s);
+    case 640: return run_backward<DT, E, 640>(a, parts, s);
+    case 768: return run_backward<DT, E, 768>(a, parts, s);
+    default: return run_backward<DT, E, 1024>(a, parts, s);
   }
 }
 
@@ -617,9 +651,8 @@ qz_status run_norm(const NormArgs& a, bool backward, int parts, cudaStream_t s) 
 int parts_for(int64_t rows, int64_t cols) {
   int64_t per = 1;  // rows a block works on at once
   if (cols <= kMaxHeld) {
-    int tpr = 32;
-    while (tpr * kPer < cols) tpr *= 2;
-    per = tpr < 512 ? 512 / tpr : 1;
+    const int tpr = threads_per_row(cols);
+    per = norm_block(tpr) / tpr;  // the same with 192 threads as with 256, with 384 as with 512
   }
   const int64_t want = (rows + per - 1) / per;
   return static_cast<int>(want < kMaxParts ? want : kMaxParts);

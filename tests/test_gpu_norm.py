@@ -150,6 +150,13 @@ def test_backward_rows_at_any_place(qz, dtype, lead, pad, shape):
     assert bool((buf == 5).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(900, 2056), (901, 3071), (640, 4104), (641, 6143), (800, 8200), (330, 10239), (320, 12288), (310, 12296)])
+def test_threads_between_powers_of_two(qz, dtype, shape):
+    test_forward(qz, dtype, True, shape)
+    test_backward(qz, dtype, True, shape)
+
+
 def test_gradient_is_the_difference(qz):
     """sum(dy * y) moved by +-h along a direction, through the fp32 kernel itself."""
     rng = np.random.default_rng(4)
