@@ -10,9 +10,11 @@
 //     NVFP4 weights are scaled before the product; E8M0 and fp32 scales take the fp32 sum of their
 //     block or group (one FMA per output).
 //   - The activations are f16 too: token t's values times a power of two 2^p that brings its
-//     largest finite magnitude into [2^14, 2^15).  bf16's 8 bits fit f16's 11 as long as a value is
-//     at least 2^-28 of that magnitude; below it keeps an absolute error of 2^-39 of it, against
-//     the 2^-24 of the largest product that an fp32 sum rounds to.  The sum is multiplied by 2^-p.
+//     largest finite magnitude into [2^14, 2^15), and the sum is multiplied by 2^-p.  f16 holds the 8
+//     bits of every value down to 2^-31 of that magnitude (2^-17, in units of 2^-24).  Where a token
+//     spans more, or p is negative (sums times the smallest scales would leave fp32), all activations
+//     of the call stay bf16 and the weights are turned into bf16, exactly: see `wide`.  (Logits below:
+//     38 us, such activations 59.)
 //
 // A tile is 16 outputs (gated: 16 of gate and of up).  ks of a CTA's warps share a tile, each with a
 // contiguous part of the sum, and join their partial sums in shared memory in warp order; CTAs
@@ -31,6 +33,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "qz_device.cuh"
 #include "qz_internal.h"
@@ -79,6 +82,12 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ uint32_t mulh(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -103,6 +112,17 @@ __device__ __forceinline__ void decode_word(uint32_t w, uint32_t (&v)[4]) {
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
         : "r"(w));
   }
+}
+__device__ __forceinline__ uint32_t min_abs_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 x, y;\n\tabs.f16x2 x, %1;\n\tabs.f16x2 y, %2;\n\tmin.f16x2 %0, x, y;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// an f16 pair of values of at most 8 significant bits as bf16, exactly
+__device__ __forceinline__ uint32_t to_bf16(uint32_t h) {
+  float lo, hi;
+  f16x2_to_f32(h, lo, hi);
+  return bf16x2_bits(lo, hi);
 }
 __device__ __forceinline__ float pow2(int e) {  // 2^e as fp32, e in [-149, 127]
   return e >= -126 ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23) : __uint_as_float(1u << (e + 149));
@@ -248,7 +268,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
   };
   for (int i = 0; i < depth - 1; ++i) issue();
 
-  // ---- the activations, times 2^p, as f16: [32-wide chunk][token][32], zero past the columns ----
+  // ---- the activations, times 2^p, as f16 (wide: as they are): [32-wide chunk][token][32], zero past the columns ----
+  // wide: f16 does not hold them.  Every CTA sees the same activations and so decides the same.
+  bool wide;
   {
     constexpr int kHeld = 8, kAll = 32 * kFewWarps;
     // a round holds up to eight pieces of 8 values a thread, each of them kAll consecutive pieces of one token
@@ -286,15 +308,31 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
       m = __reduce_max_sync(kFull, m);
       if (lane == 0) atomicMax(&s_amax[tok], m << 16);
     };
-    const auto convert = [&](int i, int tok, int c) {
+    bool beyond = false;  // this thread has met a value that f16 does not hold
+    const auto convert = [&](int i, int tok, int c, bool raw) {
       const uint32_t m = s_amax[tok];
       // 2^p: 14 less the exponent of the largest magnitude, 120 at most
       const float f = pow2(m == 0u ? 0 : min(120, 14 + 127 - static_cast<int>(m >> 23)));
       const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      uint32_t o[4];
+      uint32_t o[4] = {w[0], w[1], w[2], w[3]};
+      if (!raw) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[q]) : "f"(__uint_as_float(w[q] & 0xffff0000u) * f), "f"(__uint_as_float(w[q] << 16) * f));
+        for (int q = 0; q < 4; ++q)
+          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[q]) : "f"(__uint_as_float(w[q] & 0xffff0000u) * f), "f"(__uint_as_float(w[q] << 16) * f));
+        // The largest has exponent field E, p = 141 - E (120 at most: then f16 holds every bf16 value).
+        // Values but 0 with a field below E - 31 are too small (subnormals have the spacing of field 1);
+        // they are among those that came out below 2^-16.
+        const uint32_t small = min_abs_f16x2(min_abs_f16x2(o[0], o[1]), min_abs_f16x2(o[2], o[3]));
+        if ((small & 0xff00u) == 0u || (small & 0xff000000u) == 0u) {
+          const int E = static_cast<int>(m >> 23), least = E > 32 ? (E - 31) << 7 : 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int lo = w[q] & 0x7fffu, hi = (w[q] >> 16) & 0x7fffu;
+            beyond |= (lo != 0 && lo < least) || (hi != 0 && hi < least);
+          }
+        }
+        if constexpr (FMT != QZ_NVFP4) beyond |= m >= 142u << 23;
+      }
       if constexpr (FMT == QZ_INT4) {  // values 0 .. 7 in the order of the weights' pairs
         const uint32_t e[4] = {o[0], o[1], o[2], o[3]};
         o[0] = __byte_perm(e[0], e[2], 0x5410);
@@ -312,201 +350,255 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
       blk = (base + kHeld) - tok * blocks;
     }
     __syncthreads();
-    for (int base = 0, tok = 0, blk = 0; base < n; base += kHeld) {
-      if (n > kHeld) each(tok, blk, load);  // else still in registers
-      each(tok, blk, convert);
-      tok = (base + kHeld) / blocks;
-      blk = (base + kHeld) - tok * blocks;
+    const auto stage = [&](bool raw) {
+      for (int base = 0, tok = 0, blk = 0; base < n; base += kHeld) {
+        if (n > kHeld) each(tok, blk, load);  // else still in registers
+        each(tok, blk, [&](int i, int t, int c) { convert(i, t, c, raw); });
+        tok = (base + kHeld) / blocks;
+        blk = (base + kHeld) - tok * blocks;
+      }
+    };
+    stage(false);
+    wide = __syncthreads_or(beyond);
+    if (wide) {
+      stage(true);
+      __syncthreads();
     }
   }
-  __syncthreads();
   if (!busy) return;  // (fewer tiles than warps to share them; no barrier of the whole CTA follows)
-  // this lane's B operand: token 8 nt + g (the last again past the end: its columns are not stored)
-  const uint8_t* xa[NT];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) xa[nt] = xs + min(8 * nt + g, tokens - 1) * 64 + 16 * t;
-  const uint32_t x_chunk = 64u * tokens;
-
-  // scales of rows g and g + 8, one step ahead
-  AheadScales<FMT, LOG, RAGGED> next;
-  const int row_blocks = static_cast<int>(p.cols >> p.log2_block);
-  int ntile = tile0, ns = s_begin;
-  const uint8_t* pr[2];
-  const auto point = [&]() {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      pr[h] = static_cast<const uint8_t*>(second ? p.w1.scales : p.w0.scales) + min(ntile * 16 + g + 8 * h, rows - 1) * a.scale_pitch;
-  };
-  const auto load_next = [&]() {  // (past the last tile: its last row's again)
-    next.load(pr, ns, t, row_blocks);
-    if (++ns == s_end) {
-      ns = s_begin;
-      ntile += tile_step;
-      point();
-    }
-  };
-  point();
-  load_next();
-
   int ci = 0;
   uint32_t cph = 0;
-  const uint32_t word = 128u * g + 4u * t;  // word t of chunk c of row g: 16 (c ^ g) further (128-byte swizzle)
-  for (int tile = tile0; tile < a.tiles; tile += tile_step) {
-    float z[NT][4] = {};
-    bool shifted = false;  // z is in units of 2^64 (see kShift)
+  // The tiles, in code of its own for wide activations (tests inside one loop cost the other 1.5 us of 37).
+  const auto run = [&](auto kind) {
+    constexpr bool kWide = decltype(kind)::value;
+    // this lane's B operand: token 8 nt + g (the last again past the end: its columns are not stored)
+    const uint8_t* xa[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) xa[nt] = xs + min(8 * nt + g, tokens - 1) * 64 + 16 * t;
+    const uint32_t x_chunk = 64u * tokens;
+
+    // scales of rows g and g + 8, one step ahead
+    AheadScales<FMT, LOG, RAGGED> next;
+    const int row_blocks = static_cast<int>(p.cols >> p.log2_block);
+    int ntile = tile0, ns = s_begin;
+    const uint8_t* pr[2];
+    const auto point = [&]() {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        pr[h] = static_cast<const uint8_t*>(second ? p.w1.scales : p.w0.scales) + min(ntile * 16 + g + 8 * h, rows - 1) * a.scale_pitch;
+    };
+    const auto load_next = [&]() {  // (past the last tile: its last row's again)
+      next.load(pr, ns, t, row_blocks);
+      if (++ns == s_end) {
+        ns = s_begin;
+        ntile += tile_step;
+        point();
+      }
+    };
+    point();
+    load_next();
+
+    const uint32_t word = 128u * g + 4u * t;  // word t of chunk c of row g: 16 (c ^ g) further (128-byte swizzle)
+    for (int tile = tile0; tile < a.tiles; tile += tile_step) {
+      float z[NT][4] = {};
+      bool shifted = false;  // z is in units of 2^64 (see kShift)
 #pragma unroll 1
-    for (int s = s_begin; s < s_end; ++s) {
-      StepScales<FMT, LOG> now[2];
-      next.words(now, lane);
-      load_next();
-      few_wait(full + 8u * ci, cph, &s_abort);
-      __syncwarp();  // the slot before is read by every lane
-      issue();
-      const uint8_t* slot = mine_ring + ci * kSlot + word;
-      if (++ci == depth) {
-        ci = 0;
-        cph ^= 1u;
-      }
-      bool odd = false;
-      if constexpr (FMT == QZ_NVFP4) {
-        // this lane's block of chunk c is 2 c + t / 2: eight E4M3 bytes, then f16 (chunks 2 i, 2 i + 1)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t sel = t < 2 ? 0x6420u : 0x7531u;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t b;
-            asm("prmt.b32 %0, %1, %2, %3;" : "=r"(b) : "r"(now[h].v[2 * i]), "r"(now[h].v[2 * i + 1]), "r"(sel));
-            asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-                : "=r"(now[h].v[2 * i]), "=r"(now[h].v[2 * i + 1])
-                : "r"(b));
-          }
+      for (int s = s_begin; s < s_end; ++s) {
+        StepScales<FMT, LOG> now[2];
+        next.words(now, lane);
+        load_next();
+        few_wait(full + 8u * ci, cph, &s_abort);
+        __syncwarp();  // the slot before is read by every lane
+        issue();
+        const uint8_t* slot = mine_ring + ci * kSlot + word;
+        if (++ci == depth) {
+          ci = 0;
+          cph ^= 1u;
         }
-      } else {
-        // Scales that fp32 does not hold as normal numbers or that could take a sum out of range:
-        // E8M0 bytes 0 and above 191, fp32 above 2^73.
-        bool high = false;
+        bool odd = false;
+        if constexpr (FMT == QZ_NVFP4) {
+          // this lane's block of chunk c is 2 c + t / 2: eight E4M3 bytes, then f16 (chunks 2 i, 2 i + 1)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t sel = t < 2 ? 0x6420u : 0x7531u;
 #pragma unroll
-          for (int i = 0; i < StepScales<FMT, LOG>::kWords; ++i) {
-            if constexpr (FMT == QZ_MXFP4) {
-              const uint32_t e = now[h].v[i];
-              odd |= ((e - 0x01010101u) & ~e & 0x80808080u) != 0u;  // a byte 0 (and some bytes 1 above one)
-              high |= ((e & 0x80808080u) & ((e << 1) & 0x80808080u)) != 0u;  // a byte above 191
+            for (int i = 0; i < 2; ++i) {
+              uint32_t b;
+              asm("prmt.b32 %0, %1, %2, %3;" : "=r"(b) : "r"(now[h].v[2 * i]), "r"(now[h].v[2 * i + 1]), "r"(sel));
+              asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+                  : "=r"(now[h].v[2 * i]), "=r"(now[h].v[2 * i + 1])
+                  : "r"(b));
+            }
+          }
+        } else if (!kWide) {
+          // Scales that fp32 does not hold as normal numbers or that could take a sum out of range:
+          // E8M0 bytes 0 and above 191, fp32 above 2^73.
+          bool high = false;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < StepScales<FMT, LOG>::kWords; ++i) {
+              if constexpr (FMT == QZ_MXFP4) {
+                const uint32_t e = now[h].v[i];
+                odd |= ((e - 0x01010101u) & ~e & 0x80808080u) != 0u;  // a byte 0 (and some bytes 1 above one)
+                high |= ((e & 0x80808080u) & ((e << 1) & 0x80808080u)) != 0u;  // a byte above 191
+              } else {
+                high |= fabsf(__uint_as_float(now[h].v[i])) > 0x1p73f;
+              }
+            }
+          if (!shifted && __any_sync(kFull, high)) {
+            shifted = true;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) z[nt][i] *= kShift;
+          }
+          odd = __any_sync(kFull, odd | shifted);
+        }
+        const uint32_t x0 = static_cast<uint32_t>(s) * 8u * x_chunk;
+        [[maybe_unused]] float acc[FMT == QZ_NVFP4 ? 1 : NT][4];  // the sum of a block or group, before its scale
+        [[maybe_unused]] constexpr int kPer = FMT == QZ_INT4 ? 1 << (LOG - 5) : 1;  // chunks of it
+        const auto chunk = [&](int c, bool rare) {  // chunk c: 32 columns, lane t its word t
+          uint4 xv[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) xv[nt] = *reinterpret_cast<const uint4*>(xa[nt] + x0 + c * x_chunk);
+          uint32_t v[2][4];
+          [[maybe_unused]] float f[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            decode_word<FMT>(*reinterpret_cast<const uint32_t*>(slot + 1024 * h + ((c ^ g) << 4)), v[h]);
+            if constexpr (FMT == QZ_NVFP4) {
+              const uint32_t both = __byte_perm(now[h].v[c >> 1], 0, (c & 1) ? 0x3232 : 0x1010);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) v[h][q] = mulh(v[h][q], both);
+            } else if constexpr (FMT == QZ_MXFP4) {
+              const uint32_t E = now[h].v[c >> 2];
+              f[h] = __uint_as_float(((c & 3) == 3 ? E >> 1 : E << (23 - 8 * (c & 3))) & 0x7f800000u);
+              if (rare) {
+                const uint32_t b = (E >> (8 * (c & 3))) & 255u;
+                f[h] = b == 255u ? __uint_as_float(0x7fc00000u) : pow2(static_cast<int>(b) - 127) * (shifted ? kShift : 1.0f);
+              }
             } else {
-              high |= fabsf(__uint_as_float(now[h].v[i])) > 0x1p73f;
+              f[h] = __uint_as_float(now[h].v[c / kPer]);
+              if (rare) f[h] *= kShift;
             }
           }
-        if (!shifted && __any_sync(kFull, high)) {
-          shifted = true;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (FMT == QZ_NVFP4) {
+              mma(z[nt], v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
+              mma(z[nt], v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
+            } else {  // the block's scale takes its sum
+              if (c % kPer == 0) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+              mma(acc[nt], v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
+              mma(acc[nt], v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
+              if (c % kPer == kPer - 1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) z[nt][i] *= kShift;
-        }
-        odd = __any_sync(kFull, odd | shifted);
-      }
-      const uint32_t x0 = static_cast<uint32_t>(s) * 8u * x_chunk;
-      float acc[FMT == QZ_NVFP4 ? 1 : NT][4];  // the sum of a block or group, before its scale
-      constexpr int kPer = FMT == QZ_INT4 ? 1 << (LOG - 5) : 1;  // chunks of it
-      const auto chunk = [&](int c, bool rare) {  // chunk c: 32 columns, lane t its word t
-        uint4 xv[NT];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) xv[nt] = *reinterpret_cast<const uint4*>(xa[nt] + x0 + c * x_chunk);
-        uint32_t v[2][4];
-        float f[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          decode_word<FMT>(*reinterpret_cast<const uint32_t*>(slot + 1024 * h + ((c ^ g) << 4)), v[h]);
-          if constexpr (FMT == QZ_NVFP4) {
-            const uint32_t both = __byte_perm(now[h].v[c >> 1], 0, (c & 1) ? 0x3232 : 0x1010);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[h][q] = mulh(v[h][q], both);
-          } else if constexpr (FMT == QZ_MXFP4) {
-            const uint32_t E = now[h].v[c >> 2];
-            f[h] = __uint_as_float(((c & 3) == 3 ? E >> 1 : E << (23 - 8 * (c & 3))) & 0x7f800000u);
-            if (rare) {
-              const uint32_t b = (E >> (8 * (c & 3))) & 255u;
-              f[h] = b == 255u ? __uint_as_float(0x7fc00000u) : pow2(static_cast<int>(b) - 127) * (shifted ? kShift : 1.0f);
-            }
-          } else {
-            f[h] = __uint_as_float(now[h].v[c / kPer]);
-            if (rare) f[h] *= kShift;
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if constexpr (FMT == QZ_NVFP4) {
-            mma(z[nt], v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
-            mma(z[nt], v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
-          } else {  // the block's scale takes its sum
-            if (c % kPer == 0) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
-            mma(acc[nt], v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
-            mma(acc[nt], v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
-            if (c % kPer == kPer - 1) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) z[nt][i] = __fmaf_rn(f[i >> 1], acc[nt][i], z[nt][i]);
+                for (int i = 0; i < 4; ++i) z[nt][i] = __fmaf_rn(f[i >> 1], acc[nt][i], z[nt][i]);
+              }
             }
           }
-        }
-      };
-      // (two loops: tests inside one cost its chunks their overlap)
-      if (FMT == QZ_NVFP4 || !odd) {
+        };
+        // The same on bf16 operands, for any activations and scales.  MXFP4 and NVFP4 weights take their
+        // scales before the product (6 significant bits); NVFP4 weights are 2^-12 and INT4 integers 2^-11
+        // of their value, so that no product leaves fp32 before the tensor scale or the group's scale.
+        const auto wide_chunk = [&](int c) {
+          uint4 xv[NT];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) chunk(c, false);
-      } else {
+          for (int nt = 0; nt < NT; ++nt) xv[nt] = *reinterpret_cast<const uint4*>(xa[nt] + x0 + c * x_chunk);
+          uint32_t v[2][4];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) chunk(c, true);
-      }
-    }
-    // ---- join the parts, eight tokens at a time, and store ----
-    const float f0 = sum_factor<FMT>(p.w0.tscale), f1 = GATED ? sum_factor<FMT>(p.w1.tscale) : 0.0f;
+          for (int h = 0; h < 2; ++h) {
+            decode_word<FMT>(*reinterpret_cast<const uint32_t*>(slot + 1024 * h + ((c ^ g) << 4)), v[h]);
+            uint32_t k = 0x10001000u;  // 2^-11
+            if constexpr (FMT == QZ_NVFP4) {
+              k = mulh(__byte_perm(now[h].v[c >> 1], 0, (c & 1) ? 0x3232 : 0x1010), 0x0C000C00u);
+            } else if constexpr (FMT == QZ_MXFP4) {
+              const uint32_t b = (now[h].v[c >> 2] >> (8 * (c & 3))) & 255u;
+              k = (b == 255u ? 0x7FC0u : b == 0u ? 0x0040u : b << 7) * 0x00010001u;
+            }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float* mine = join + warp * kJoin;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {  // tokens 8 nt + 2 t and + 1: 2^-p of each
-        const uint32_t m = s_amax[min(8 * nt + 2 * t + i, tokens - 1)];
-        const float down = pow2(m == 0u ? 0 : -min(120, 14 + 127 - static_cast<int>(m >> 23)));
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float v = z[nt][2 * h + i] * down;
-          mine[(2 * t + i) * kTokenStride + g + 8 * h] = shifted ? v * 0x1p64f : v;
-        }
-      }
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * team) : "memory");
-      const float* from = join + group * team * kJoin;
-      const int count = 16 * min(8, tokens - 8 * nt);
-      for (int e = member * 32 + lane; e < count; e += 32 * team) {
-        const int row = tile * 16 + (e & 15), tok = 8 * nt + (e >> 4);
-        float sum[kWeights];
-#pragma unroll
-        for (int m = 0; m < kWeights; ++m) {
-          const float* q = from + m * ks * kJoin + (e >> 4) * kTokenStride + (e & 15);
-          sum[m] = q[0];
-          for (int w = 1; w < ks; ++w) sum[m] += q[w * kJoin];
-        }
-        if (row >= rows) continue;
-        const int64_t o = static_cast<int64_t>(tok) * p.ld_y + row;
-        const float v = s_abort ? __uint_as_float(0x7fc00000u) : sum[0] * f0;
-        if constexpr (GATED) {
-          const float u = sum[kWeights - 1] * f1;
-          static_cast<uint16_t*>(p.y)[o] = bf16_bits((p.act == QZ_ACT_SILU ? act_value<QZ_ACT_SILU>(v) : act_value<QZ_ACT_GELU_TANH>(v)) * u);
-          if (p.g_out) {
-            const int64_t q = static_cast<int64_t>(tok) * p.ld_gu + row;
-            p.g_out[q] = bf16_bits(v);
-            p.u_out[q] = bf16_bits(u);
+            for (int q = 0; q < 4; ++q) v[h][q] = FMT == QZ_MXFP4 ? mul_bf16x2(to_bf16(v[h][q]), k) : to_bf16(mulh(v[h][q], k));
           }
-        } else if (p.out_f32) {
-          static_cast<float*>(p.y)[o] = v;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (FMT == QZ_INT4) {
+              if (c % kPer == 0) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.0f;
+              mma_bf16(acc[nt], v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
+              mma_bf16(acc[nt], v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
+              if (c % kPer == kPer - 1) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[nt][i] = __fmaf_rn(__uint_as_float(now[i >> 1].v[c / kPer]), acc[nt][i], z[nt][i]);
+              }
+            } else {
+              mma_bf16(z[nt], v[0][0], v[1][0], v[0][1], v[1][1], xv[nt].x, xv[nt].y);
+              mma_bf16(z[nt], v[0][2], v[1][2], v[0][3], v[1][3], xv[nt].z, xv[nt].w);
+            }
+          }
+        };
+        // (loops of their own: tests inside one cost its chunks their overlap)
+        if constexpr (kWide) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) wide_chunk(c);
+        } else if (FMT == QZ_NVFP4 || !odd) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) chunk(c, false);
         } else {
-          static_cast<uint16_t*>(p.y)[o] = bf16_bits(v);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) chunk(c, true);
         }
       }
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * team) : "memory");
+      // ---- join the parts, eight tokens at a time, and store ----
+      [[maybe_unused]] const float f0 = sum_factor<FMT>(p.w0.tscale), f1 = GATED ? sum_factor<FMT>(p.w1.tscale) : 0.0f;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float* mine = join + warp * kJoin;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // tokens 8 nt + 2 t and + 1: 2^-p of each
+          const uint32_t m = s_amax[min(8 * nt + 2 * t + i, tokens - 1)];
+          constexpr float kWideUnit = FMT == QZ_NVFP4 ? 0x1p12f : FMT == QZ_INT4 ? 0x1p11f : 1.0f;
+          const float down = kWide ? kWideUnit : pow2(m == 0u ? 0 : -min(120, 14 + 127 - static_cast<int>(m >> 23)));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float v = z[nt][2 * h + i] * down;
+            mine[(2 * t + i) * kTokenStride + g + 8 * h] = shifted ? v * 0x1p64f : v;
+          }
+        }
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * team) : "memory");
+        const float* from = join + group * team * kJoin;
+        const int count = 16 * min(8, tokens - 8 * nt);
+        for (int e = member * 32 + lane; e < count; e += 32 * team) {
+          const int row = tile * 16 + (e & 15), tok = 8 * nt + (e >> 4);
+          float sum[kWeights];
+#pragma unroll
+          for (int m = 0; m < kWeights; ++m) {
+            const float* q = from + m * ks * kJoin + (e >> 4) * kTokenStride + (e & 15);
+            sum[m] = q[0];
+            for (int w = 1; w < ks; ++w) sum[m] += q[w * kJoin];
+          }
+          if (row >= rows) continue;
+          const int64_t o = static_cast<int64_t>(tok) * p.ld_y + row;
+          const float v = s_abort ? __uint_as_float(0x7fc00000u) : sum[0] * f0;
+          if constexpr (GATED) {
+            const float u = sum[kWeights - 1] * f1;
+            static_cast<uint16_t*>(p.y)[o] = bf16_bits((p.act == QZ_ACT_SILU ? act_value<QZ_ACT_SILU>(v) : act_value<QZ_ACT_GELU_TANH>(v)) * u);
+            if (p.g_out) {
+              const int64_t q = static_cast<int64_t>(tok) * p.ld_gu + row;
+              p.g_out[q] = bf16_bits(v);
+              p.u_out[q] = bf16_bits(u);
+            }
+          } else if (p.out_f32) {
+            static_cast<float*>(p.y)[o] = v;
+          } else {
+            static_cast<uint16_t*>(p.y)[o] = bf16_bits(v);
+          }
+        }
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * team) : "memory");
+      }
     }
-  }
+  };
+  if (wide) run(std::true_type{});
+  else run(std::false_type{});
   // (every copy issued has been waited for by its step; after a wait that gave up they get a second more)
   if (s_abort)
     for (int i = 0; i < depth; ++i) {

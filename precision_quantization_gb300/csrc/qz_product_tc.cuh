@@ -224,11 +224,6 @@ __device__ __forceinline__ void let_land(uint64_t* full, int s, uint32_t ph, int
 }
 
 // ---- decoding -------------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 // Byte q of a word as two 4-bit fields at bits 0 and 16 (even and odd nibble); t0 = word &
 // 0x0F0F0F0F, t1 = (word >> 4) & 0x0F0F0F0F.  Selectors 8 give the sign of byte 0, which is 0.
 template <int Q>
