@@ -44,8 +44,6 @@
 namespace qz {
 namespace {
 
-constexpr float kShift = 0x1p-64f;      // the sums' unit once a scale above 2^64 (INT4 2^73) has been met
-
 struct FewArgs {
   CUtensorMap map_w0, map_w1;  // codes [rows][cols / 2] bytes, box 128 x 16
   ProductArgs p;
@@ -377,6 +375,13 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
     for (int nt = 0; nt < NT; ++nt) xa[nt] = xs + min(8 * nt + g, tokens - 1) * 64 + 16 * t;
     const uint32_t x_chunk = 64u * tokens;
 
+    // 2^-p of a token, and the unit of the sums on bf16 operands
+    const auto token_down = [&](int tok) {
+      const uint32_t m = s_amax[min(tok, tokens - 1)];
+      return pow2(m == 0u ? 0 : -min(120, 14 + 127 - static_cast<int>(m >> 23)));
+    };
+    constexpr float kWideUnit = FMT == QZ_NVFP4 ? 0x1p12f : FMT == QZ_INT4 ? 0x1p11f : 1.0f;
+
     // scales of rows g and g + 8, one step ahead
     AheadScales<FMT, LOG, RAGGED> next;
     const int row_blocks = static_cast<int>(p.cols >> p.log2_block);
@@ -401,7 +406,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
     const uint32_t word = 128u * g + 4u * t;  // word t of chunk c of row g: 16 (c ^ g) further (128-byte swizzle)
     for (int tile = tile0; tile < a.tiles; tile += tile_step) {
       float z[NT][4] = {};
-      bool shifted = false;  // z is in units of 2^64 (see kShift)
+      bool exact = false;  // not wide: this tile's sums have gone over to bf16 operands
 #pragma unroll 1
       for (int s = s_begin; s < s_end; ++s) {
         StepScales<FMT, LOG> now[2];
@@ -431,8 +436,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
             }
           }
         } else if (!kWide) {
-          // Scales that fp32 does not hold as normal numbers or that could take a sum out of range:
-          // E8M0 bytes 0 and above 191, fp32 above 2^73.
+          // E8M0 bytes of 0 are not what an exponent field of 0 means.  Bytes above 191 and fp32 scales above
+          // 2^73 could take the sum of a block times 2^p out of fp32: from there on this warp's part of the
+          // tile is summed as in `wide` (a unit of its own for the large sums would lose the small ones).
           bool high = false;
 #pragma unroll
           for (int h = 0; h < 2; ++h)
@@ -446,14 +452,14 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
                 high |= fabsf(__uint_as_float(now[h].v[i])) > 0x1p73f;
               }
             }
-          if (!shifted && __any_sync(kFull, high)) {
-            shifted = true;
+          if (!exact && __any_sync(kFull, high)) {
+            exact = true;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) z[nt][i] *= kShift;
+              for (int i = 0; i < 4; ++i) z[nt][i] *= token_down(8 * nt + 2 * t + (i & 1)) * (1.0f / kWideUnit);
           }
-          odd = __any_sync(kFull, odd | shifted);
+          odd = __any_sync(kFull, odd);
         }
         const uint32_t x0 = static_cast<uint32_t>(s) * 8u * x_chunk;
         [[maybe_unused]] float acc[FMT == QZ_NVFP4 ? 1 : NT][4];  // the sum of a block or group, before its scale
@@ -474,13 +480,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
             } else if constexpr (FMT == QZ_MXFP4) {
               const uint32_t E = now[h].v[c >> 2];
               f[h] = __uint_as_float(((c & 3) == 3 ? E >> 1 : E << (23 - 8 * (c & 3))) & 0x7f800000u);
-              if (rare) {
-                const uint32_t b = (E >> (8 * (c & 3))) & 255u;
-                f[h] = b == 255u ? __uint_as_float(0x7fc00000u) : pow2(static_cast<int>(b) - 127) * (shifted ? kShift : 1.0f);
-              }
+              if (rare) f[h] = pow2(static_cast<int>((E >> (8 * (c & 3))) & 255u) - 127);
             } else {
               f[h] = __uint_as_float(now[h].v[c / kPer]);
-              if (rare) f[h] *= kShift;
             }
           }
 #pragma unroll
@@ -505,7 +507,17 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
         const auto wide_chunk = [&](int c) {
           uint4 xv[NT];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) xv[nt] = *reinterpret_cast<const uint4*>(xa[nt] + x0 + c * x_chunk);
+          for (int nt = 0; nt < NT; ++nt) {
+            xv[nt] = *reinterpret_cast<const uint4*>(xa[nt] + x0 + c * x_chunk);
+            if constexpr (!kWide) {  // back from f16: the activations as they were
+              const float d = token_down(8 * nt + g);
+              for (uint32_t* q : {&xv[nt].x, &xv[nt].y, &xv[nt].z, &xv[nt].w}) {
+                float lo, hi;
+                f16x2_to_f32(*q, lo, hi);
+                *q = bf16x2_bits(lo * d, hi * d);
+              }
+            }
+          }
           uint32_t v[2][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -537,10 +549,10 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
           }
         };
         // (loops of their own: tests inside one cost its chunks their overlap)
-        if constexpr (kWide) {
+        if (kWide || (FMT != QZ_NVFP4 && exact)) {
 #pragma unroll
           for (int c = 0; c < 8; ++c) wide_chunk(c);
-        } else if (FMT == QZ_NVFP4 || !odd) {
+        } else if (FMT != QZ_MXFP4 || !odd) {
 #pragma unroll
           for (int c = 0; c < 8; ++c) chunk(c, false);
         } else {
@@ -555,14 +567,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
         float* mine = join + warp * kJoin;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {  // tokens 8 nt + 2 t and + 1: 2^-p of each
-          const uint32_t m = s_amax[min(8 * nt + 2 * t + i, tokens - 1)];
-          constexpr float kWideUnit = FMT == QZ_NVFP4 ? 0x1p12f : FMT == QZ_INT4 ? 0x1p11f : 1.0f;
-          const float down = kWide ? kWideUnit : pow2(m == 0u ? 0 : -min(120, 14 + 127 - static_cast<int>(m >> 23)));
+          const float down = kWide || exact ? kWideUnit : token_down(8 * nt + 2 * t + i);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const float v = z[nt][2 * h + i] * down;
-            mine[(2 * t + i) * kTokenStride + g + 8 * h] = shifted ? v * 0x1p64f : v;
-          }
+          for (int h = 0; h < 2; ++h) mine[(2 * t + i) * kTokenStride + g + 8 * h] = z[nt][2 * h + i] * down;
         }
         asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "r"(32 * team) : "memory");
         const float* from = join + group * team * kJoin;

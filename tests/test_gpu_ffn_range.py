@@ -116,3 +116,30 @@ def test_nonfinite_beside_a_wide_token(qz, fmt):
     assert np.isnan(got[0]).all() and not np.isfinite(got[4]).any()
     keep = [1, 2, 3, 5]
     assert np.array_equal(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("where", ["rows", "blocks"])
+@pytest.mark.parametrize("tokens", TOKENS)
+@pytest.mark.parametrize("fmt", ["mxfp4", "int4"])
+def test_scales_far_apart(qz, fmt, tokens, where):
+    """Scales near 2^100 in every fourth output (or on blocks of zeros in every fourth, and on real
+    weights in one), 2^-100 in the others: each output has the accuracy of its own products."""
+    rng = np.random.default_rng(tokens)
+    cols = 1024
+    w = F.make_weight(rng, fmt, 83, cols)
+    blocks = cols // w["group"]
+    k = rng.integers(-104, -96, (83, blocks))
+    if where == "rows":
+        k[1::4] = rng.integers(96, 104, (len(k[1::4]), blocks))
+    else:
+        high = rng.integers(0, blocks, 83)
+        k[np.arange(83), high] = 110
+        for r in range(83):
+            if r != 40:
+                part = slice(high[r] * w["group"] // 2, (high[r] + 1) * w["group"] // 2)
+                w["codes"][r, part] = 0
+                w["elements"][r, 2 * part.start:2 * part.stop] = 0
+    w["scales"] = np.ldexp(1.0, k).astype(np.float32) if fmt == "int4" else (k + 127).astype(np.uint8)
+    w["values"] = w["elements"] * np.repeat(np.ldexp(1.0, k), w["group"], axis=1)
+    x = F.activations(rng, tokens, cols)
+    F.assert_within(linear(qz, x, w), x @ w["values"].T, bound(w, tokens, cols, np.abs(x) @ np.abs(w["values"]).T))
