@@ -36,6 +36,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "qz_device.cuh"
 #include "qz_internal.h"
@@ -285,8 +286,8 @@ __device__ __forceinline__ void load_scales_box(const uint8_t* p, int col, Scale
 }
 
 // 32 weights (16 bytes of codes; half h of a line's 64) to bf16, stored as chunks 4 h .. 4 h + 3
-// of the line at `dst`, each at its swizzled place (x: line % 8).
-template <int FMT>
+// of the line at `dst`, each at its swizzled place (x: line % 8).  ANY: E4M3 scales may be NaN (0x7F) or negative.
+template <int FMT, bool ANY>
 __device__ __forceinline__ void decode32(const uint4 codes, const Scales<FMT>& s, uint32_t dst, int x, int h) {
   const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
   uint32_t f0, f1;  // bf16 pairs: the factor of the first and the second 16 weights
@@ -303,10 +304,16 @@ __device__ __forceinline__ void decode32(const uint4 codes, const Scales<FMT>& s
     // an E4M3 byte at bits 4-10 is its value times 2^-120 as bf16; 2^127 and 2^111 bring it to
     // 2^118 times its value (below 2^127), so a weight comes out as 2^-8 of its own
     const uint32_t b = s.v[0] >> (16 * h);
-    uint32_t c = ((b & 255u) << 4) | ((b & 0xff00u) << 12);
-    c = mul_bf16x2(mul_bf16x2(c, 0x7F007F00u), 0x77007700u);
-    f0 = (c & 0xffffu) * 0x00010001u;
-    f1 = (c >> 16) * 0x00010001u;
+    if constexpr (ANY) {
+      const float v0 = dec_e4m3(b & 255u) * 0x1p118f, v1 = dec_e4m3((b >> 8) & 255u) * 0x1p118f;
+      f0 = bf16x2_bits(v0, v0);
+      f1 = bf16x2_bits(v1, v1);
+    } else {
+      uint32_t c = ((b & 255u) << 4) | ((b & 0xff00u) << 12);
+      c = mul_bf16x2(mul_bf16x2(c, 0x7F007F00u), 0x77007700u);
+      f0 = (c & 0xffffu) * 0x00010001u;
+      f1 = (c >> 16) * 0x00010001u;
+    }
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -516,7 +523,14 @@ __device__ __forceinline__ void decode_boxes(const TcArgs& a, const DecodeLoop& 
     bx += kGroups;
     settle();
     load_next();  // of this group's next box, in flight during this one
-    if (!__all_sync(kFull, tc_wait(d.c_full + 8u * cs, cph, d.abort) && tc_wait(d.a_empty, aph ^ 1u, d.abort))) break;
+    bool any = false;  // an E4M3 byte from 0x7F on
+    if constexpr (FMT == QZ_NVFP4) {
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k) any |= (((now[k].v[0] + 0x01010101u) | now[k].v[0]) & 0x80808080u) != 0u;
+    }
+    const bool ok = tc_wait(d.c_full + 8u * cs, cph, d.abort) && tc_wait(d.a_empty, aph ^ 1u, d.abort);
+    const bool plain = __all_sync(kFull, ok && !any);  // (one vote a box, 1.5 per cent; a branch at each scale took 4)
+    if (!plain && !__all_sync(kFull, ok)) break;
     const uint8_t* box = d.codes + cs * kBoxBytes + kLine * cl;
     uint4 codes[kSteps][2];
 #pragma unroll
@@ -526,12 +540,16 @@ __device__ __forceinline__ void decode_boxes(const TcArgs& a, const DecodeLoop& 
       for (int i = 0; i < 2; ++i)
         codes[k][i] = *reinterpret_cast<const uint4*>(box + (MODE == kModeBackward ? 4096 * k : 0) + (((c + i) ^ cx) << 4));
     }
+    const auto decode = [&](auto any) {
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      const uint32_t dst = d.a_stage + k * (kTerms * kABytes) + 128u * line;
-      decode32<FMT>(codes[k][0], now[k], dst, x, 0);
-      decode32<FMT>(codes[k][1], now[k], dst, x, 1);
-    }
+      for (int k = 0; k < kSteps; ++k) {
+        const uint32_t dst = d.a_stage + k * (kTerms * kABytes) + 128u * line;
+        decode32<FMT, decltype(any)::value>(codes[k][0], now[k], dst, x, 0);
+        decode32<FMT, decltype(any)::value>(codes[k][1], now[k], dst, x, 1);
+      }
+    };
+    if (FMT != QZ_NVFP4 || plain) decode(std::false_type{});
+    else decode(std::true_type{});
     fence_proxy_async();  // the stores, before the tensor cores read them
     __syncwarp();
     if (d.lane == 0) {

@@ -143,3 +143,45 @@ def test_scales_far_apart(qz, fmt, tokens, where):
     w["values"] = w["elements"] * np.repeat(np.ldexp(1.0, k), w["group"], axis=1)
     x = F.activations(rng, tokens, cols)
     F.assert_within(linear(qz, x, w), x @ w["values"].T, bound(w, tokens, cols, np.abs(x) @ np.abs(w["values"]).T))
+
+
+@pytest.mark.parametrize("cols", [512, 544])  # scales loaded together, or one at a time
+@pytest.mark.parametrize("tokens", [1, 17, 40, 300])
+@pytest.mark.parametrize("fmt", list(F.FORMATS))
+def test_scale_is_nan(qz, fmt, tokens, cols):
+    """A NaN scale makes its output NaN (backward: the gradients of its columns) and nothing else."""
+    import torch
+    group = 32 if fmt == "int4" else F.FORMATS[fmt]
+    rng = np.random.default_rng(cols)
+    w = F.make_weight(rng, fmt, 70, cols, group)
+    x, dy = F.activations(rng, tokens, cols), F.activations(rng, tokens, 70)
+    clean = linear(qz, x, w)
+    clean_dx = F.host(qz.linear_backward(F.bf16_cuda(dy), F.handle(w), out_dtype=torch.float32))
+    w["scales"][5, 3] = w["scales"][64, 0] = {"mxfp4": 255, "nvfp4": 0x7F, "int4": np.nan}[fmt]
+    got = linear(qz, x, w)
+    assert np.isnan(got[:, [5, 64]]).all()
+    rest = np.setdiff1d(np.arange(70), [5, 64])
+    F.assert_within(got[:, rest], clean[:, rest], 2 * bound(w, tokens, cols, np.abs(x) @ np.abs(w["values"][rest]).T))
+    dx = F.host(qz.linear_backward(F.bf16_cuda(dy), F.handle(w), out_dtype=torch.float32))
+    hit = np.zeros(cols, bool)
+    hit[:group] = hit[3 * group:4 * group] = True
+    assert np.isnan(dx[:, hit]).all() and np.array_equal(dx[:, ~hit], clean_dx[:, ~hit])
+    _, g, u = qz.gated_ffn(F.bf16_cuda(x), F.handle(w), F.handle(w), save=True)
+    assert np.isnan(F.host(g)[:, [5, 64]]).all() and np.isfinite(F.host(u)[:, rest]).all()
+
+
+@pytest.mark.parametrize("tokens", [1, 17, 300])
+def test_every_e4m3_scale(qz, tokens):
+    """All 254 finite E4M3 bytes, the negative ones too, have the value that dequantize gives them."""
+    import torch
+    rng = np.random.default_rng(tokens)
+    w = F.make_weight(rng, "nvfp4", 64, 256)
+    b = rng.permutation(np.concatenate([np.arange(0x7F), np.arange(0x80, 0xFF)]).repeat(5)[:1024]).reshape(64, 16)
+    w["scales"] = b.astype(np.uint8)
+    k = F.e4m3_value(b & 127) * np.where(b > 127, -1, 1) * np.float64(w["ts"])
+    w["values"] = w["elements"] * np.repeat(k, 16, axis=1)
+    x, dy = F.activations(rng, tokens, 256), F.activations(rng, tokens, 64)
+    a = np.abs(w["values"])
+    F.assert_within(linear(qz, x, w), x @ w["values"].T, bound(w, tokens, 256, np.abs(x) @ a.T))
+    dx = F.host(qz.linear_backward(F.bf16_cuda(dy), F.handle(w), out_dtype=torch.float32))
+    F.assert_within(dx, dy @ w["values"], bound(w, tokens, 64, np.abs(dy) @ a))
