@@ -594,14 +594,23 @@ def _same_tokens(tokens: int, **matrices):
             raise ValueError(f"{what} must have {tokens} rows, not {t.shape[0]}")
 
 
-def _raw_stream(stream, t) -> int:
-    """The given torch stream, or the current one of t's device, as the library takes it."""
-    if stream is not None:
-        return stream.cuda_stream
+def _on(stream, t):
+    """The context of a call on `stream`: outputs and scratch memory come from that stream's pool (a
+    block of the current stream's may still be in use there, and would go back to it too early)."""
+    if stream.device != t.device:
+        raise ValueError(f"the stream belongs to {stream.device}, the inputs to {t.device}")
+    return _torch().cuda.stream(stream)
+
+
+def _raw_stream(t) -> int:
+    """The current stream of t's device, as the library takes it."""
     return _torch()._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _linear_call(name: str, x, width: int, weight: Weight, out_width: int, out_dtype, out, stream, what: str):
+    if stream is not None:
+        with _on(stream, x):
+            return _linear_call(name, x, width, weight, out_width, out_dtype, out, None, what)
     torch = _torch()
     bf = torch.bfloat16
     ld_x = _matrix(x, width, bf, what)
@@ -620,7 +629,7 @@ def _linear_call(name: str, x, width: int, weight: Weight, out_width: int, out_d
         ld_y = _matrix(out, out_width, out.dtype, "out")
         _same_tokens(tokens, out=out)
     rc = getattr(_lib or lib(), name)(weight.desc, x.data_ptr(), ld_x, tokens, out.data_ptr(), ld_y, code,
-                                      _raw_stream(stream, x))
+                                      _raw_stream(x))
     if rc:
         raise QzError(rc, name)
     return out
@@ -646,6 +655,9 @@ def gated_ffn(x, gate: Weight, up: Weight, activation="silu", save: bool = False
     """h = act(x gate^T) * (x up^T) (qz_gated_ffn): x bf16 [tokens, cols] -> h bf16 [tokens,
     rows]; with ``save`` also the bf16 pre-activations, (h, g, u).  out: h, or (h, g, u) with
     ``save``."""
+    if stream is not None:
+        with _on(stream, x):
+            return gated_ffn(x, gate, up, activation, save, out)
     torch = _torch()
     bf, empty = torch.bfloat16, torch.empty
     ld_x = _matrix(x, gate.cols, bf, "x")
@@ -667,7 +679,7 @@ def gated_ffn(x, gate: Weight, up: Weight, activation="silu", save: bool = False
                 raise ValueError("g and u must have the same leading dimension")
     rc = (_lib or lib()).qz_gated_ffn(gate.desc, up.desc, _activation(activation), x.data_ptr(), ld_x,
                                       tokens, h.data_ptr(), ld_h, _ptr(g), _ptr(u), ld_gu,
-                                      _raw_stream(stream, x))
+                                      _raw_stream(x))
     if rc:
         raise QzError(rc, "qz_gated_ffn")
     return (h, g, u) if save else h
@@ -677,6 +689,9 @@ def gated_ffn_backward(dh, g, u, gate: Weight, up: Weight, activation="silu", ou
                        stream=None):
     """The gradients of gated_ffn from its kept pre-activations (qz_gated_ffn_backward):
     (dx [tokens, cols], dg, du [tokens, rows]), all bf16.  out: the three, in that order."""
+    if stream is not None:
+        with _on(stream, dh):
+            return gated_ffn_backward(dh, g, u, gate, up, activation, out)
     torch = _torch()
     bf, empty = torch.bfloat16, torch.empty
     rows, cols, tokens = gate.rows, gate.cols, dh.shape[0]
@@ -693,7 +708,7 @@ def gated_ffn_backward(dh, g, u, gate: Weight, up: Weight, activation="silu", ou
         raise ValueError("g and u, and dg and du, must have the same leading dimension")
     rc = (_lib or lib()).qz_gated_ffn_backward(gate.desc, up.desc, _activation(activation), dh.data_ptr(), ld_dh,
                                                g.data_ptr(), u.data_ptr(), ld_g, tokens, dg.data_ptr(),
-                                               du.data_ptr(), ld_dg, dx.data_ptr(), ld_dx, _raw_stream(stream, dh))
+                                               du.data_ptr(), ld_dg, dx.data_ptr(), ld_dx, _raw_stream(dh))
     if rc:
         raise QzError(rc, "qz_gated_ffn_backward")
     return dx, dg, du
@@ -712,6 +727,9 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
     """Layer norm over the rows of a 2-D bf16 / fp32 CUDA tensor (qz_layer_norm).  weight, bias:
     fp32 [cols] or None.  Returns (y, mean, rstd); mean and rstd, fp32 [rows], are what
     layer_norm_backward takes.  out: the three, in that order."""
+    if stream is not None:
+        with _on(stream, x):
+            return layer_norm(x, weight, bias, eps, out)
     dt = _dtype_code(x.dtype)
     if x.dim() != 2:
         raise ValueError("2-D tensors only")
@@ -730,7 +748,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
         pm, pr = _vector(mean, rows, "mean"), _vector(rstd, rows, "rstd")
     rc = (_lib or lib()).qz_layer_norm(dt, x.data_ptr(), ld_x, rows, cols, _vector(weight, cols, "weight"),
                                        _vector(bias, cols, "bias"), eps, y.data_ptr(), ld_y, pm, pr,
-                                       _raw_stream(stream, x))
+                                       _raw_stream(x))
     if rc:
         raise QzError(rc, "qz_layer_norm")
     return y, mean, rstd
@@ -741,6 +759,9 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, params: bool = True, out
     """The gradients of layer_norm (qz_layer_norm_backward): (dx, dweight, dbias), the last two
     fp32 [cols], or None without ``params``.  out: the three, in that order.  workspace: a uint8
     CUDA tensor of qz_layer_norm_backward_workspace(rows, cols) bytes."""
+    if stream is not None:
+        with _on(stream, x):
+            return layer_norm_backward(dy, x, mean, rstd, weight, params, out, workspace)
     dt = _dtype_code(x.dtype)
     if x.dim() != 2:
         raise ValueError("2-D tensors only")
@@ -768,7 +789,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, params: bool = True, out
         dt, dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, rows, cols, _vector(mean, rows, "mean"),
         _vector(rstd, rows, "rstd"), _vector(weight, cols, "weight"), dx.data_ptr(), ld_dx,
         _vector(dw, cols, "dweight"), _vector(db, cols, "dbias"), ws,
-        workspace.numel() * workspace.element_size() if params else 0, _raw_stream(stream, x))
+        workspace.numel() * workspace.element_size() if params else 0, _raw_stream(x))
     if rc:
         raise QzError(rc, "qz_layer_norm_backward")
     return dx, dw, db
