@@ -566,14 +566,22 @@ class Weight:
         if (q.codes.dtype != torch.uint8 or q.codes.numel() * 2 != q.rows * q.cols
                 or q.scales.dtype != sdt or q.scales.numel() * bs != q.rows * q.cols):
             raise ValueError("codes / scales do not match the weight's shape and format")
+        self.device = q.codes.get_device()
+        used = [q.scales]
+        if q.fmt == QZ_NVFP4:
+            if q.tensor_scale.dtype != torch.float32 or q.tensor_scale.numel() != 1:
+                raise ValueError("the tensor scale must be one fp32 value")
+            used.append(q.tensor_scale)
+        if any(t.get_device() != self.device for t in used):
+            raise ValueError("codes and scales must be on one device")
         self.desc = QzWeight(q.fmt, bs, q.rows, q.cols, q.codes.data_ptr(), q.scales.data_ptr(),
                              _ptr(q.tensor_scale) if q.fmt == QZ_NVFP4 else None)
 
 
-def _matrix(t, width: int, dtype, what: str) -> int:
-    """Leading dimension of a [tokens, width] CUDA matrix with unit inner stride.  (A product of one
-    token takes a few microseconds on the GPU, so the common case is one test of each property.)"""
-    if t.dim() == 2 and t.dtype is dtype and t.is_cuda:
+def _matrix(t, width: int, dtype, what: str, device: int) -> int:
+    """Leading dimension of a [tokens, width] matrix on GPU `device` with unit inner stride.  (A product
+    of one token takes a few microseconds on the GPU, so the common case is one test of each property.)"""
+    if t.dim() == 2 and t.dtype is dtype and t.get_device() == device >= 0:
         (n, w), (s0, s1) = t.shape, t.stride()
         if w == width and (s1 == 1 or w <= 1 or n == 0):
             if n <= 1:
@@ -585,6 +593,8 @@ def _matrix(t, width: int, dtype, what: str) -> int:
             raise ValueError(f"{what}: the inner dimension must be contiguous")
     if not t.is_cuda:
         raise ValueError(f"{what} must be on the GPU")
+    if t.get_device() != device:
+        raise ValueError(f"{what} must be on cuda:{device}, not {t.device}")
     raise ValueError(f"{what} must be a [tokens, {width}] {dtype} matrix, not {tuple(t.shape)} {t.dtype}")
 
 
@@ -595,25 +605,25 @@ def _same_tokens(tokens: int, **matrices):
 
 
 def _on(stream, t):
-    """The context of a call on `stream`: outputs and scratch memory come from that stream's pool (a
-    block of the current stream's may still be in use there, and would go back to it too early)."""
+    """The context of a call on `stream`, or on t's device where that is not the current one.
+    Outputs and scratch memory come from that stream's pool (a block of the current stream's may
+    still be in use there, and would go back to it too early)."""
+    if stream is None:
+        return _torch().cuda.device(t.device)
     if stream.device != t.device:
         raise ValueError(f"the stream belongs to {stream.device}, the inputs to {t.device}")
     return _torch().cuda.stream(stream)
 
 
-def _raw_stream(t) -> int:
-    """The current stream of t's device, as the library takes it."""
-    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
-
-
 def _linear_call(name: str, x, width: int, weight: Weight, out_width: int, out_dtype, out, stream, what: str):
-    if stream is not None:
+    torch, device = _torch(), x.get_device()
+    if stream is not None or (device >= 0 and device != torch._C._cuda_getDevice()):
         with _on(stream, x):
             return _linear_call(name, x, width, weight, out_width, out_dtype, out, None, what)
-    torch = _torch()
     bf = torch.bfloat16
-    ld_x = _matrix(x, width, bf, what)
+    ld_x = _matrix(x, width, bf, what, device)
+    if weight.device != device:
+        raise ValueError(f"the weight must be on cuda:{device}")
     tokens = x.shape[0]
     if out is None:
         if out_dtype is None or out_dtype is bf:
@@ -626,10 +636,10 @@ def _linear_call(name: str, x, width: int, weight: Weight, out_width: int, out_d
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError("out has another dtype than out_dtype")
         code = _dtype_code(out.dtype)
-        ld_y = _matrix(out, out_width, out.dtype, "out")
+        ld_y = _matrix(out, out_width, out.dtype, "out", device)
         _same_tokens(tokens, out=out)
     rc = getattr(_lib or lib(), name)(weight.desc, x.data_ptr(), ld_x, tokens, out.data_ptr(), ld_y, code,
-                                      _raw_stream(x))
+                                      torch._C._cuda_getCurrentRawStream(device))
     if rc:
         raise QzError(rc, name)
     return out
@@ -655,12 +665,14 @@ def gated_ffn(x, gate: Weight, up: Weight, activation="silu", save: bool = False
     """h = act(x gate^T) * (x up^T) (qz_gated_ffn): x bf16 [tokens, cols] -> h bf16 [tokens,
     rows]; with ``save`` also the bf16 pre-activations, (h, g, u).  out: h, or (h, g, u) with
     ``save``."""
-    if stream is not None:
+    torch, device = _torch(), x.get_device()
+    if stream is not None or (device >= 0 and device != torch._C._cuda_getDevice()):
         with _on(stream, x):
             return gated_ffn(x, gate, up, activation, save, out)
-    torch = _torch()
     bf, empty = torch.bfloat16, torch.empty
-    ld_x = _matrix(x, gate.cols, bf, "x")
+    ld_x = _matrix(x, gate.cols, bf, "x", device)
+    if gate.device != device or up.device != device:
+        raise ValueError(f"the weights must be on cuda:{device}")
     tokens, rows = x.shape[0], gate.rows
     g = u = None
     ld_gu = rows
@@ -670,16 +682,16 @@ def gated_ffn(x, gate: Weight, up: Weight, activation="silu", save: bool = False
             g, u = (empty((tokens, rows), dtype=bf, device=x.device) for _ in range(2))
     else:
         h, g, u = out if save else (out, None, None)
-        ld_h = _matrix(h, rows, bf, "out")
+        ld_h = _matrix(h, rows, bf, "out", device)
         _same_tokens(tokens, out=h)
         if save:
-            ld_gu, ld_u = _matrix(g, rows, bf, "g"), _matrix(u, rows, bf, "u")
+            ld_gu, ld_u = _matrix(g, rows, bf, "g", device), _matrix(u, rows, bf, "u", device)
             _same_tokens(tokens, g=g, u=u)
             if ld_gu != ld_u and tokens > 1:
                 raise ValueError("g and u must have the same leading dimension")
     rc = (_lib or lib()).qz_gated_ffn(gate.desc, up.desc, _activation(activation), x.data_ptr(), ld_x,
                                       tokens, h.data_ptr(), ld_h, _ptr(g), _ptr(u), ld_gu,
-                                      _raw_stream(x))
+                                      torch._C._cuda_getCurrentRawStream(device))
     if rc:
         raise QzError(rc, "qz_gated_ffn")
     return (h, g, u) if save else h
@@ -689,37 +701,41 @@ def gated_ffn_backward(dh, g, u, gate: Weight, up: Weight, activation="silu", ou
                        stream=None):
     """The gradients of gated_ffn from its kept pre-activations (qz_gated_ffn_backward):
     (dx [tokens, cols], dg, du [tokens, rows]), all bf16.  out: the three, in that order."""
-    if stream is not None:
+    torch, device = _torch(), dh.get_device()
+    if stream is not None or (device >= 0 and device != torch._C._cuda_getDevice()):
         with _on(stream, dh):
             return gated_ffn_backward(dh, g, u, gate, up, activation, out)
-    torch = _torch()
     bf, empty = torch.bfloat16, torch.empty
     rows, cols, tokens = gate.rows, gate.cols, dh.shape[0]
-    ld_dh, ld_g, ld_u = _matrix(dh, rows, bf, "dh"), _matrix(g, rows, bf, "g"), _matrix(u, rows, bf, "u")
+    ld_dh, ld_g, ld_u = (_matrix(t, rows, bf, what, device) for t, what in ((dh, "dh"), (g, "g"), (u, "u")))
+    if gate.device != device or up.device != device:
+        raise ValueError(f"the weights must be on cuda:{device}")
     if out is None:
         dx, dg, du = (empty((tokens, n), dtype=bf, device=dh.device) for n in (cols, rows, rows))
         ld_dx, ld_dg, ld_du = cols, rows, rows
         _same_tokens(tokens, g=g, u=u)
     else:
         dx, dg, du = out
-        ld_dx, ld_dg, ld_du = _matrix(dx, cols, bf, "dx"), _matrix(dg, rows, bf, "dg"), _matrix(du, rows, bf, "du")
+        ld_dx, ld_dg, ld_du = (_matrix(t, n, bf, what, device)
+                               for t, n, what in ((dx, cols, "dx"), (dg, rows, "dg"), (du, rows, "du")))
         _same_tokens(tokens, g=g, u=u, dx=dx, dg=dg, du=du)
     if tokens > 1 and (ld_g != ld_u or ld_dg != ld_du):
         raise ValueError("g and u, and dg and du, must have the same leading dimension")
     rc = (_lib or lib()).qz_gated_ffn_backward(gate.desc, up.desc, _activation(activation), dh.data_ptr(), ld_dh,
                                                g.data_ptr(), u.data_ptr(), ld_g, tokens, dg.data_ptr(),
-                                               du.data_ptr(), ld_dg, dx.data_ptr(), ld_dx, _raw_stream(dh))
+                                               du.data_ptr(), ld_dg, dx.data_ptr(), ld_dx,
+                                               torch._C._cuda_getCurrentRawStream(device))
     if rc:
         raise QzError(rc, "qz_gated_ffn_backward")
     return dx, dg, du
 
 
-def _vector(t, n: int, what: str):
+def _vector(t, n: int, what: str, device: int):
     if t is None:
         return None
     torch = _torch()
-    if t.dtype != torch.float32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{what} must be a contiguous fp32 CUDA vector of {n} values")
+    if t.dtype != torch.float32 or t.dim() != 1 or t.numel() != n or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{what} must be a contiguous fp32 vector of {n} values on cuda:{device}")
     return t.data_ptr()
 
 
@@ -727,28 +743,28 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, stream=No
     """Layer norm over the rows of a 2-D bf16 / fp32 CUDA tensor (qz_layer_norm).  weight, bias:
     fp32 [cols] or None.  Returns (y, mean, rstd); mean and rstd, fp32 [rows], are what
     layer_norm_backward takes.  out: the three, in that order."""
-    if stream is not None:
+    torch, device = _torch(), x.get_device()
+    if stream is not None or (device >= 0 and device != torch._C._cuda_getDevice()):
         with _on(stream, x):
             return layer_norm(x, weight, bias, eps, out)
     dt = _dtype_code(x.dtype)
     if x.dim() != 2:
         raise ValueError("2-D tensors only")
     rows, cols = x.shape
-    ld_x = _matrix(x, cols, x.dtype, "x")
+    ld_x = _matrix(x, cols, x.dtype, "x", device)
     if out is None:
-        torch = _torch()
         f32, empty, dev = torch.float32, torch.empty, x.device
         y = empty((rows, cols), dtype=x.dtype, device=dev)
         mean, rstd = empty((2, rows), dtype=f32, device=dev).unbind(0)
         ld_y, pm, pr = cols, mean.data_ptr(), rstd.data_ptr()
     else:
         y, mean, rstd = out
-        ld_y = _matrix(y, cols, x.dtype, "y")
+        ld_y = _matrix(y, cols, x.dtype, "y", device)
         _same_tokens(rows, y=y)
-        pm, pr = _vector(mean, rows, "mean"), _vector(rstd, rows, "rstd")
-    rc = (_lib or lib()).qz_layer_norm(dt, x.data_ptr(), ld_x, rows, cols, _vector(weight, cols, "weight"),
-                                       _vector(bias, cols, "bias"), eps, y.data_ptr(), ld_y, pm, pr,
-                                       _raw_stream(x))
+        pm, pr = _vector(mean, rows, "mean", device), _vector(rstd, rows, "rstd", device)
+    rc = (_lib or lib()).qz_layer_norm(dt, x.data_ptr(), ld_x, rows, cols, _vector(weight, cols, "weight", device),
+                                       _vector(bias, cols, "bias", device), eps, y.data_ptr(), ld_y, pm, pr,
+                                       torch._C._cuda_getCurrentRawStream(device))
     if rc:
         raise QzError(rc, "qz_layer_norm")
     return y, mean, rstd
@@ -759,16 +775,16 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, params: bool = True, out
     """The gradients of layer_norm (qz_layer_norm_backward): (dx, dweight, dbias), the last two
     fp32 [cols], or None without ``params``.  out: the three, in that order.  workspace: a uint8
     CUDA tensor of qz_layer_norm_backward_workspace(rows, cols) bytes."""
-    if stream is not None:
+    torch, device = _torch(), x.get_device()
+    if stream is not None or (device >= 0 and device != torch._C._cuda_getDevice()):
         with _on(stream, x):
             return layer_norm_backward(dy, x, mean, rstd, weight, params, out, workspace)
     dt = _dtype_code(x.dtype)
     if x.dim() != 2:
         raise ValueError("2-D tensors only")
     rows, cols = x.shape
-    ld_x, ld_dy = _matrix(x, cols, x.dtype, "x"), _matrix(dy, cols, x.dtype, "dy")
+    ld_x, ld_dy = _matrix(x, cols, x.dtype, "x", device), _matrix(dy, cols, x.dtype, "dy", device)
     L = _lib or lib()
-    torch = _torch()
     f32, empty, dev = torch.float32, torch.empty, x.device
     dw = db = None
     if out is None:
@@ -778,18 +794,20 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, params: bool = True, out
         _same_tokens(rows, dy=dy)
     else:
         dx, dw, db = out if params else (out[0], None, None)
-        ld_dx = _matrix(dx, cols, x.dtype, "dx")
+        ld_dx = _matrix(dx, cols, x.dtype, "dx", device)
         _same_tokens(rows, dy=dy, dx=dx)
     ws = None
     if params:
         if workspace is None:
             workspace = empty((L.qz_layer_norm_backward_workspace(rows, cols),), dtype=torch.uint8, device=dev)
+        elif workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError(f"the workspace must be contiguous on cuda:{device}")
         ws = workspace.data_ptr()
     rc = L.qz_layer_norm_backward(
-        dt, dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, rows, cols, _vector(mean, rows, "mean"),
-        _vector(rstd, rows, "rstd"), _vector(weight, cols, "weight"), dx.data_ptr(), ld_dx,
-        _vector(dw, cols, "dweight"), _vector(db, cols, "dbias"), ws,
-        workspace.numel() * workspace.element_size() if params else 0, _raw_stream(x))
+        dt, dy.data_ptr(), ld_dy, x.data_ptr(), ld_x, rows, cols, _vector(mean, rows, "mean", device),
+        _vector(rstd, rows, "rstd", device), _vector(weight, cols, "weight", device), dx.data_ptr(), ld_dx,
+        _vector(dw, cols, "dweight", device), _vector(db, cols, "dbias", device), ws,
+        workspace.numel() * workspace.element_size() if params else 0, torch._C._cuda_getCurrentRawStream(device))
     if rc:
         raise QzError(rc, "qz_layer_norm_backward")
     return dx, dw, db

@@ -127,3 +127,44 @@ def test_stream_of_another_device(world):
     with pytest.raises(ValueError):
         calls(world)["linear"](stream=Stream(SIDE, "cuda:1"))
     assert not world.ran
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_launches_on_the_device_of_the_inputs(world, name):
+    """Inputs on a device that is not the current one: the call runs there, on its current stream."""
+    calls(world, "cuda:1")[name]()
+    assert [(s, d) for _, s, d in world.ran] == [(MAIN + 100, 1)] and world.device == 0
+
+
+def test_other_devices_are_refused(world):
+    qz, here, cpu, far = world.qz, world.weight(), world.weight("cpu"), world.weight("cuda:1")
+    m = lambda rows, cols, device="cuda:0": Tensor((rows, cols), "bf16", device)  # noqa: E731
+    v = lambda n, device="cuda:0": Tensor((n,), "f32", device)  # noqa: E731
+    x, y = m(4, 128), m(4, 64)
+    refused = [lambda w=w: qz.linear(x, w) for w in (cpu, far)]
+    refused += [lambda w=w: qz.linear_backward(y, w) for w in (cpu, far)]
+    refused += [lambda w=w: qz.gated_ffn(x, *w) for w in ((cpu, here), (here, cpu), (far, here), (here, far))]
+    refused += [lambda w=w: qz.gated_ffn_backward(y, y, y, *w) for w in ((here, far), (cpu, here))]
+    for d in ("cpu", "cuda:1"):
+        mixed = qz.Quantized(Tensor((64, 64), "u8"), Tensor((64, 8), "u8", d), v(1), qz.QZ_NVFP4, qz.QZ_GRAN_BLOCK, 0, 64, 128, 16)
+        scale = qz.Quantized(Tensor((64, 64), "u8"), Tensor((64, 8), "u8"), v(1, d), qz.QZ_NVFP4, qz.QZ_GRAN_BLOCK, 0, 64, 128, 16)
+        refused += [lambda q=mixed: qz.Weight(q), lambda q=scale: qz.Weight(q),
+                    lambda d=d: qz.linear(x, here, out=m(4, 64, d)), lambda d=d: qz.linear_backward(y, here, out=m(4, 128, d)),
+                    lambda d=d: qz.gated_ffn(x, here, here, out=m(4, 64, d)),
+                    lambda d=d: qz.gated_ffn(x, here, here, save=True, out=(y, y, m(4, 64, d))),
+                    lambda d=d: qz.gated_ffn_backward(y, m(4, 64, d), y, here, here),
+                    lambda d=d: qz.gated_ffn_backward(y, y, y, here, here, out=(x, y, m(4, 64, d))),
+                    lambda d=d: qz.layer_norm(x, v(128, d)), lambda d=d: qz.layer_norm(x, out=(x, v(4, d), v(4))),
+                    lambda d=d: qz.layer_norm_backward(m(4, 128, d), x, v(4), v(4)),
+                    lambda d=d: qz.layer_norm_backward(x, x, v(4, d), v(4)),
+                    lambda d=d: qz.layer_norm_backward(x, x, v(4), v(4), out=(x, v(128), v(128, d))),
+                    lambda d=d: qz.layer_norm_backward(x, x, v(4), v(4), workspace=Tensor((1024,), "u8", d))]
+    two_bytes = qz.Quantized(Tensor((64, 64), "u8"), Tensor((64, 8), "u8"), Tensor((1,), "bf16"), qz.QZ_NVFP4, qz.QZ_GRAN_BLOCK, 0, 64, 128, 16)
+    gaps = Tensor((1024,), "u8")
+    gaps.is_contiguous = lambda: False
+    refused += [lambda: qz.Weight(two_bytes), lambda: qz.layer_norm_backward(x, x, v(4), v(4), workspace=gaps)]
+    for i, call in enumerate(refused):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    assert not world.ran
