@@ -550,7 +550,7 @@ def amax(x, workspace: Workspace | None = None, stream=None):
 class Weight:
     """A 4-bit weight for ``linear`` and ``gated_ffn``: the handle of a ``Quantized`` [rows, cols]
     tensor of MXFP4, NVFP4 or INT4 codes (rows = output channels).  It refers to the codes and
-    scales where they are; they must stay there, and may change in place."""
+    scales that q has when it is made, and keeps them; they may change in place."""
 
     def __init__(self, q: Quantized):
         if q.fmt not in (QZ_MXFP4, QZ_NVFP4, QZ_INT4):
@@ -574,6 +574,8 @@ class Weight:
             used.append(q.tensor_scale)
         if any(t.get_device() != self.device for t in used):
             raise ValueError("codes and scales must be on one device")
+        # the pointers' owners: q may come to refer to other tensors
+        self.buffers = (q.codes, q.scales, q.tensor_scale)
         self.desc = QzWeight(q.fmt, bs, q.rows, q.cols, q.codes.data_ptr(), q.scales.data_ptr(),
                              _ptr(q.tensor_scale) if q.fmt == QZ_NVFP4 else None)
 

@@ -168,3 +168,20 @@ def test_other_devices_are_refused(world):
             call()
             pytest.fail(f"call {i} was not refused")
     assert not world.ran
+
+
+def test_a_weight_keeps_its_buffers(world):
+    """Codes, scales and tensor scale live as long as the handle that points to them, whatever the
+    Quantized they came from refers to by then."""
+    import gc
+    import weakref
+    q = world.qz.Quantized(Tensor((64, 64), "u8"), Tensor((64, 8), "u8"), Tensor((1,), "f32"), world.qz.QZ_NVFP4,
+                           world.qz.QZ_GRAN_BLOCK, 0, 64, 128, 16)
+    refs = [weakref.ref(t) for t in (q.codes, q.scales, q.tensor_scale)]
+    w = world.qz.Weight(q)
+    q.codes, q.scales, q.tensor_scale = Tensor((64, 64), "u8"), Tensor((64, 8), "u8"), Tensor((1,), "f32")
+    gc.collect()
+    assert [r() is not None and r().data_ptr() for r in refs] == [w.desc.codes, w.desc.scales, w.desc.tensor_scale_dev]
+    del w
+    gc.collect()
+    assert all(r() is None for r in refs)
