@@ -748,8 +748,9 @@ __global__ void __launch_bounds__(TcFormat<FMT>::kThreads, 1) product_tc_kernel(
           buf ^= 1;
         }
       }
-      // every MMA issued has completed before tensor memory and shared memory are released
-      tc_commit<CG>(smem_addr(&drain));
+      // every MMA issued has completed before tensor memory and shared memory are released (a slice without
+      // boxes waits for nothing, so nothing may arrive there)
+      if (bx_begin < bx_end) tc_commit<CG>(smem_addr(&drain));
     }
     __syncwarp();
   } else if (warp >= kDecWarp0 && warp < kEpiWarp0) {
