@@ -283,6 +283,8 @@ qz_status check_matrix(int64_t tokens, int64_t width, int64_t ld) {
   if (tokens > 0 && ld > (INT64_MAX / 8) / tokens) return QZ_ERR_SHAPE;
   return QZ_OK;
 }
+// The leading dimension of one row means nothing: it may be odd, or beyond the strides that TMA takes (2^40 bytes).
+int64_t pitch_of(int64_t tokens, int64_t width, int64_t ld) { return tokens == 1 ? (width + 7) / 8 * 8 : ld; }
 qz_status check_pointer(const void* p, size_t a) {
   if (!p) return QZ_ERR_NULL;
   return aligned(p, a) ? QZ_OK : QZ_ERR_ALIGN;
@@ -331,7 +333,7 @@ extern "C" qz_status qz_linear(const qz_weight* w, const void* x, int64_t ld_x, 
   QZ_TRY(check_pointer(y, out_dtype == QZ_BF16 ? 2 : 4));
   ProductArgs p = args_of(*w, kModeLinear, tokens);
   p.x0 = static_cast<const uint16_t*>(x);
-  p.ld_x = ld_x;
+  p.ld_x = pitch_of(tokens, w->cols, ld_x);
   p.y = y;
   p.ld_y = ld_y;
   p.out_f32 = out_dtype == QZ_F32;
@@ -350,7 +352,7 @@ extern "C" qz_status qz_linear_backward(const qz_weight* w, const void* dy, int6
   QZ_TRY(check_pointer(dx, out_dtype == QZ_BF16 ? 2 : 4));
   ProductArgs p = args_of(*w, kModeBackward, tokens);
   p.x0 = static_cast<const uint16_t*>(dy);
-  p.ld_x = ld_dy;
+  p.ld_x = pitch_of(tokens, w->rows, ld_dy);
   p.y = dx;
   p.ld_y = ld_dx;
   p.out_f32 = out_dtype == QZ_F32;
@@ -381,7 +383,7 @@ extern "C" qz_status qz_gated_ffn(const qz_weight* gate, const qz_weight* up, in
   p.w1 = view_of(*up);
   p.act = act;
   p.x0 = static_cast<const uint16_t*>(x);
-  p.ld_x = ld_x;
+  p.ld_x = pitch_of(tokens, gate->cols, ld_x);
   p.y = h;
   p.ld_y = ld_h;
   p.g_out = static_cast<uint16_t*>(g_out);
@@ -420,7 +422,7 @@ extern "C" qz_status qz_gated_ffn_backward(const qz_weight* gate, const qz_weigh
   p.w1 = view_of(*up);
   p.x0 = static_cast<const uint16_t*>(dg);
   p.x1 = static_cast<const uint16_t*>(du);
-  p.ld_x = ld_dgu;
+  p.ld_x = pitch_of(tokens, gate->rows, ld_dgu);
   p.y = dx;
   p.ld_y = ld_dx;
   return launch_product(p, s);
