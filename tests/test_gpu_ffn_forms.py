@@ -43,3 +43,140 @@ def test_one_token_has_any_leading_dimension(qz, fmt, ld):
                                     ld, 1, p[0], p[1], ld, gdx.data_ptr(), ld) == qz.QZ_OK
     torch.cuda.synchronize()
     assert torch.equal(gdx, wdx[0]) and torch.equal(got[0], wdg[0]) and torch.equal(got[1], wdu[0])
+
+
+# The forms below are those that the launch plan takes on 152 SMs.  (mode, tokens, outputs, summands):
+# pairs of CTAs with three tiles and more each (both accumulators come round again, decoders run on
+# into the next tile), tiles of 64, 192 and 256 tokens, one and several of them a row
+PAIRS = [(33, 60000, 128), (250, 60000, 160), (513, 20000, 128), (700, 20000, 96)]
+# a second launch for the outputs that would start a nearly empty round: linear, gated, backward, both weights'
+TWO_E2M1 = [("linear", 131, 20008, 4096), ("gated", 250, 10024, 2048), ("backward", 131, 20000, 4096), ("both", 33, 20000, 2048)]
+TWO_INT4 = [("linear", 77, 20008, 1152), ("gated", 33, 10024, 1152), ("backward", 77, 20000, 1152), ("both", 33, 20000, 640)]
+# the streaming kernel: several tiles at once in a CTA (over 2432 outputs), and several rounds of them
+FEW = [(1, 5003, 128), (5, 41003, 128), (16, 41003, 288), (9, 5003, 4352)]
+
+
+def double(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda().double()
+
+
+def pair(fmt, rows, cols, seed, **k):
+    rng = np.random.default_rng(seed)
+    w = F.make_weight(rng, fmt, rows, cols, **k)
+    return rng, w, double(w["values"])
+
+
+def linear_exactly(qz, fmt, tokens, rows, cols, group=None):
+    import torch
+    rng, w, v = pair(fmt, rows, cols, tokens + cols, exact=True, group=group)
+    x = F.activations(rng, tokens, cols, exact=True)
+    xt, h, want = F.bf16_cuda(x), F.handle(w), double(x) @ v.T
+    assert torch.equal(qz.linear(xt, h, out_dtype=torch.float32).double(), want)
+    assert torch.equal(qz.linear(xt, h), want.to(torch.float32).to(torch.bfloat16))  # one rounding
+
+
+def backward_exactly(qz, fmt, tokens, cols, rows):
+    import torch
+    rng, w, v = pair(fmt, rows, cols, tokens + rows, exact=True)
+    dy = F.activations(rng, tokens, rows, exact=True)
+    got = qz.linear_backward(F.bf16_cuda(dy), F.handle(w), out_dtype=torch.float32)
+    assert torch.equal(got.double(), double(dy) @ v)
+
+
+def gated_exactly(qz, fmt, tokens, rows, cols):
+    import torch
+    rng, wg, vg = pair(fmt, rows, cols, tokens + cols, exact=True)
+    _, wu, vu = pair(fmt, rows, cols, tokens + cols + 1, exact=True)
+    x = F.activations(rng, tokens, cols, exact=True)
+    h, g, u = qz.gated_ffn(F.bf16_cuda(x), F.handle(wg), F.handle(wu), save=True)
+    gw, uw = double(x) @ vg.T, double(x) @ vu.T
+    bf = lambda t: t.to(torch.float32).to(torch.bfloat16)  # noqa: E731
+    assert torch.equal(g, bf(gw)) and torch.equal(u, bf(uw))
+    # the activation in fp32 (2^-18 of |g| + 1, as for exact sums elsewhere), and one rounding to bf16
+    want = gw * torch.sigmoid(gw) * uw
+    assert bool(((h.double() - want).abs() <= 2.0 ** -18 * (gw.abs() + 1) * uw.abs() + 2.0 ** -8 * 1.01 * want.abs()).all())
+
+
+def both_backward(qz, fmt, tokens, cols, rows):
+    """dx of the gated block: integers for dg and du would need g and u that give them, so the sum's bound."""
+    rng, wg, vg = pair(fmt, rows, cols, tokens + rows)
+    _, wu, vu = pair(fmt, rows, cols, tokens + rows + 1)
+    dh, g, u = (F.bf16_cuda(F.activations(rng, tokens, rows)) for _ in range(3))
+    dx, dg, du = qz.gated_ffn_backward(dh, g, u, F.handle(wg), F.handle(wu))
+    want = dg.double() @ vg + du.double() @ vu
+    terms = dg.double().abs() @ vg.abs() + du.double().abs() @ vu.abs()
+    assert bool(((dx.double() - want).abs() <= F.sum_bound(2 * rows, terms) + 2.0 ** -8 * 1.01 * want.abs()).all())
+
+
+@pytest.mark.parametrize("fmt", list(F.FORMATS))
+@pytest.mark.parametrize("shape", PAIRS)
+def test_pairs_of_many_tiles(qz, fmt, shape):
+    tokens, nout, nsum = shape
+    nsum = -(-nsum // F.FORMATS[fmt]) * F.FORMATS[fmt]
+    linear_exactly(qz, fmt, tokens, nout + 8, nsum)
+    backward_exactly(qz, fmt, tokens, -(-nout // 128) * 128, nsum + 8)
+
+
+@pytest.mark.parametrize("fmt", list(F.FORMATS))
+@pytest.mark.parametrize("shape", [(33, 40008, 128), (250, 20008, 128), (700, 10024, 128)])
+def test_gated_pairs_of_many_tiles(qz, fmt, shape):
+    gated_exactly(qz, fmt, *shape)
+    both_backward(qz, fmt, shape[0], -(-shape[1] // 128) * 128, 200)
+
+
+@pytest.mark.parametrize("fmt,case", [(f, c) for f in ("mxfp4", "nvfp4") for c in TWO_E2M1] + [("int4", c) for c in TWO_INT4])
+def test_two_launches(qz, fmt, case):
+    mode, tokens, nout, nsum = case
+    if mode == "linear":
+        linear_exactly(qz, fmt, tokens, nout, nsum)
+    elif mode == "gated":
+        gated_exactly(qz, fmt, tokens, nout, nsum)
+    else:
+        (backward_exactly if mode == "backward" else both_backward)(qz, fmt, tokens, -(-nout // 128) * 128, nsum)
+
+
+@pytest.mark.parametrize("fmt,group", [("mxfp4", 32), ("nvfp4", 16), ("int4", 32), ("int4", 64), ("int4", 128)])
+@pytest.mark.parametrize("shape", FEW)
+def test_few_tokens_many_outputs(qz, fmt, group, shape):
+    tokens, rows, cols = shape
+    cols = -(-cols // group) * group
+    linear_exactly(qz, fmt, tokens, rows, cols, group)
+    if fmt == "int4":
+        linear_exactly(qz, fmt, tokens + 16, rows, cols, group)
+    gated_exactly(qz, fmt, tokens, rows, -(-cols // 128) * 128)
+
+
+@pytest.mark.parametrize("tokens", [1, 8, 17, 40, 300])
+@pytest.mark.parametrize("ends", [(-127, -126, -125, -100), (100, 120, 124, 125)])
+def test_e8m0_scales_at_both_ends(qz, ends, tokens):
+    """2^-127 (weights below bf16's normal range) and 2^125 (6 * 2^125 is the largest in fp32) by every kernel,
+    forward and backward."""
+    import torch
+    rng = np.random.default_rng(tokens)
+    w = F.make_weight(rng, "mxfp4", 96, 256)
+    k = np.array(ends)[rng.integers(0, 4, (96, 8))]
+    w["scales"] = (k + 127).astype(np.uint8)
+    w["values"] = w["elements"] * np.repeat(np.ldexp(1.0, k), 32, axis=1)
+    scale = 2.0 ** 100 if ends[0] < 0 else 2.0 ** -60
+    x, dy = (F.activations(rng, tokens, n) * scale for n in (256, 96))
+    h, a = F.handle(w), np.abs(w["values"])
+    # (the weights are held exactly: no 2^-17)
+    bound = lambda n, terms: F.sum_bound(n, terms) - 2.0 ** -17 * terms  # noqa: E731
+    F.assert_within(F.host(qz.linear(F.bf16_cuda(x), h, out_dtype=torch.float32)), x @ w["values"].T, bound(256, np.abs(x) @ a.T))
+    F.assert_within(F.host(qz.linear_backward(F.bf16_cuda(dy), h, out_dtype=torch.float32)), dy @ w["values"], bound(96, np.abs(dy) @ a))
+
+
+@pytest.mark.parametrize("shape", [(1, 70, 512), (7, 300, 640), (16, 96, 2048), (40, 200, 512), (300, 264, 1152)])
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_e2m1_weights_are_held_exactly(qz, fmt, shape):
+    """Random values against the bound of an fp32 sum alone."""
+    import torch
+    tokens, rows, cols = shape
+    rng = np.random.default_rng(rows)
+    w = F.make_weight(rng, fmt, rows, cols)
+    x, dy = F.activations(rng, tokens, cols), F.activations(rng, tokens, rows)
+    h, a = F.handle(w), np.abs(w["values"])
+    for got, want, n, terms in ((qz.linear(F.bf16_cuda(x), h, out_dtype=torch.float32), x @ w["values"].T, cols, np.abs(x) @ a.T),
+                                (qz.linear_backward(F.bf16_cuda(dy), h, out_dtype=torch.float32), dy @ w["values"], rows, np.abs(dy) @ a)):
+        F.assert_within(F.host(got), want, F.sum_bound(n, terms) - 2.0 ** -17 * terms)
