@@ -10,6 +10,7 @@
 #include "qz_device.cuh"
 #include "qz_internal.h"
 #include "qz_product.h"
+#include "qz_product_plan.h"
 #include "qz_weight.cuh"
 
 namespace qz {
@@ -138,14 +139,22 @@ ProductArgs some_tokens(ProductArgs p, int64_t first, int64_t count) {
   return p;
 }
 
+// The streaming kernel or the tiles, by what they are estimated to take.  Where the activations' staging costs
+// little against the start of a tile (3 tokens of 4096 columns 5.6 us, on the tiles 9.0 and more) nothing is estimated.
+bool few_pays(const ProductArgs& p) {
+  return p.tokens * ((p.cols + 4095) / 4096) <= 4 || few_us(p) <= tiles_us(p);
+}
+
 qz_status launch_product(const ProductArgs& p, cudaStream_t s) {
-  if (product_few_applicable(p)) return launch_few(p, s);
-  // INT4, at most 16 tokens that do not fit shared memory together: two halves of 8 read the weights
-  // twice and still beat the tiles (12 tokens, 32768 x 8192, groups of 128: 91 us against 168)
-  if (p.format == QZ_INT4 && p.mode != kModeBackward && p.tokens > 1 && p.tokens <= 16) {
+  if (product_few_applicable(p)) {
+    if (few_pays(p)) return launch_few(p, s);
+  } else if (p.format == QZ_INT4 && p.mode != kModeBackward && p.tokens > 1 && p.tokens <= 16) {
+    // INT4, at most 16 tokens that do not fit shared memory together: two halves of 8 read the weights
+    // twice and may still beat the tiles (16 tokens, groups of 128, 32768 x 8192: 93 us against 166;
+    // 512 x 8192: 26 against 18)
     const int64_t half = (p.tokens + 1) / 2;
     const ProductArgs a = some_tokens(p, 0, half), b = some_tokens(p, half, p.tokens - half);
-    if (product_few_applicable(a)) {
+    if (product_few_applicable(a) && 2 * few_us(a) <= tiles_us(p)) {
       const qz_status st = launch_few(a, s);
       return st == QZ_OK ? launch_few(b, s) : st;
     }

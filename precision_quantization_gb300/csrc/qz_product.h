@@ -28,9 +28,8 @@ struct ProductArgs {
 
 // The streaming kernels for a few tokens (qz_product_few.cuh): their shared memory is a ring
 // of code boxes and a buffer of partial sums per warp, and the activations.
-// Tokens they take at most.  E2M1 weights: 16 (4096 x 4096: 16 tokens 14.5 us against 16.5 on the
-// tensor-core tiles, 17 tokens 16.5 both; 8192 x 4096: 18 and 21 against 16.5).  INT4, whose tiles take
-// two products a weight: 32 (4096 x 4096: 17 tokens 16.5 us against 27).
+// Tokens they take at most (above, the tiles are faster at every size): E2M1 weights 16, INT4, whose tiles
+// take two products a weight, 32.  Up to there the estimates of qz_product_plan.h decide.
 constexpr int few_tokens(int format) { return format == QZ_INT4 ? 32 : 16; }
 constexpr int kFewWarps = 16;
 constexpr int kTokenStride = 20;                  // floats of a token's 16 sums (banks 8 t + g)

@@ -42,12 +42,12 @@
 #include "qz_internal.h"
 #include "qz_pipe.cuh"
 #include "qz_product.h"
+#include "qz_product_plan.h"
 #include "qz_weight.cuh"
 
 namespace qz {
 namespace {
 
-constexpr int kBM = 128;            // outputs per CTA (MMA rows, tensor-memory lanes)
 constexpr int kBK = 64;             // summands per step: 128 bytes of bf16, one swizzle row
 constexpr int kDecWarp0 = 4;
 constexpr uint32_t kABytes = kBM * kBK * 2;        // 16 KiB of decoded weights
@@ -60,6 +60,7 @@ struct TcFormat {
   static constexpr int kTerms = FMT == QZ_INT4 ? 2 : 1;      // bf16 terms per weight
   static constexpr int kSteps = FMT == QZ_INT4 ? 1 : 2;      // 64-wide steps of a box: eight MMAs
   static constexpr int kBoxK = kSteps * kBK;
+  static_assert(kBoxK == box_of(FMT));
   static constexpr uint32_t kBoxBytes = kBM * kBoxK / 2;     // of codes
   static constexpr int kGroups = 3;                          // decoder groups of four warps
   // Stages of decoded weights: one box per group.  Both this ring and the code ring hold a whole
@@ -950,73 +951,6 @@ qz_status run_tc(const TcArgs& a, int grid, cudaStream_t s) {
   return launch_status();
 }
 
-// The form and its tiles for outputs [m_base, m_base + nout).  Estimated in SM cycles: a box's eight
-// MMAs take 4 cycles a token column (128 x n x 16 each at 8192 FLOP a cycle); its hand-over takes
-// some 750 cycles in a pair, whose decoders share the tokens' copies, and 950 alone; a tile of the
-// second form starts with an empty pipeline and ends with the exchange.
-struct Plan {
-  bool pair;
-  int n, tiles_n, tiles, slices, slice_boxes, grid;
-  int64_t m_base;
-  double cost;
-};
-inline void tokens_per_tile(int64_t tokens, int most, int unit, int* n, int64_t* tiles_n) {
-  const int64_t t = (tokens + most - 1) / most;
-  *n = static_cast<int>(((tokens + t - 1) / t + unit - 1) / unit * unit);
-  *tiles_n = (tokens + *n - 1) / *n;
-}
-inline Plan plan_pairs(int64_t m_base, int64_t nout, int out_per_cta, int64_t tokens, int boxes, double least) {
-  Plan best{};
-  best.cost = 1e30;
-  const int64_t pairs = std::max(1, sm_count() / 2);
-  for (int most = 256; most >= 64; most -= 32) {  // narrower tiles where they fill the last round better
-    int n;
-    int64_t tiles_n;
-    tokens_per_tile(tokens, most, 32, &n, &tiles_n);
-    const int64_t tiles = (nout + 2 * out_per_cta - 1) / (2 * out_per_cta) * tiles_n;
-    const double cost = static_cast<double>((tiles + pairs - 1) / pairs) * boxes * std::max(4.0 * n + 40, least) + 6000;
-    if (tiles < (int64_t{1} << 30) && cost < best.cost)
-      best = Plan{true, n, static_cast<int>(tiles_n), static_cast<int>(tiles), 1, boxes, static_cast<int>(2 * std::min(tiles, pairs)), m_base, cost};
-  }
-  return best;
-}
-inline Plan plan_alone(int64_t m_base, int64_t nout, int out_per_cta, int64_t tokens, int boxes) {
-  Plan best{};
-  best.cost = 1e30;
-  const int sms = sm_count();
-  for (int s = 1; s <= 8; s *= 2)
-    for (int most : {192, 128}) {
-      int n;
-      int64_t tiles_n;
-      tokens_per_tile(tokens, most, std::max(32, 8 * s), &n, &tiles_n);  // the columns divide into eights per slice
-      const int64_t tiles = (nout + out_per_cta - 1) / out_per_cta * tiles_n;
-      const int per = (boxes + s - 1) / s;
-      const int64_t clusters = std::max(1, s == 1 ? sms : (s == 2 ? sms * 9 / 10 : sms * 5 / 6) / s);
-      // above 128 tokens the copies have two stages only
-      const double box = std::max(4.0 * n, n > 128 ? 1200.0 : 950.0);
-      const double cost = static_cast<double>((tiles + clusters - 1) / clusters) * (per * box + 6000 + (s > 1 ? 2000 + 16.0 * n : 0));
-      if (tiles * s < (int64_t{1} << 30) && cost < best.cost)
-        best = Plan{false, n, static_cast<int>(tiles_n), static_cast<int>(tiles), s, per, static_cast<int>(tiles * s), m_base, cost};
-    }
-  return best;
-}
-// One launch, or two: where a few tiles of the pairs would make a round of their own, the last
-// outputs' tiles go to a second launch that splits their sums over the whole GPU.
-inline int plan_of(int64_t nout, int out_per_cta, int64_t tokens, int boxes, double least, Plan (&plan)[2]) {
-  const Plan pairs = plan_pairs(0, nout, out_per_cta, tokens, boxes, least), alone = plan_alone(0, nout, out_per_cta, tokens, boxes);
-  plan[0] = alone.cost < pairs.cost ? alone : pairs;
-  if (plan[0].cost > 1e29) return 0;
-  const int64_t per_round = std::max(1, sm_count() / 2) / pairs.tiles_n;  // rows of pairs' tiles a round takes
-  const int64_t rows_m = (nout + 2 * out_per_cta - 1) / (2 * out_per_cta);
-  if (per_round < 1 || rows_m <= per_round || rows_m % per_round == 0) return 1;
-  const int64_t first = rows_m / per_round * per_round * 2 * out_per_cta;
-  const Plan a = plan_pairs(0, first, out_per_cta, tokens, boxes, least), b = plan_alone(first, nout - first, out_per_cta, tokens, boxes);
-  if (a.cost + b.cost + 4000 >= plan[0].cost) return 1;
-  plan[0] = a;
-  plan[1] = b;
-  return 2;
-}
-
 template <int FMT>
 qz_status launch_plan(TcArgs& a, const Plan& plan, cudaStream_t s) {
   const ProductArgs& p = a.p;
@@ -1063,14 +997,13 @@ qz_status launch_tc(const ProductArgs& p, cudaStream_t s) {
   a.nout = static_cast<int>(back ? p.cols : p.rows);
   a.nsum = static_cast<int>(back ? p.rows : p.cols);
   a.blocks_row = static_cast<int>(p.cols >> p.log2_block);
-  constexpr int kBoxK = TcFormat<FMT>::kBoxK;
-  a.boxes_w = (a.nsum + kBoxK - 1) / kBoxK;
+  a.boxes_w = boxes_of(p.format, a.nsum);
   a.boxes = back ? a.boxes_w * p.n_weights : a.boxes_w;
   const auto aligned_scales = [&](uintptr_t n) { return reinterpret_cast<uintptr_t>(a.scales0) % n == 0 && reinterpret_cast<uintptr_t>(a.scales1) % n == 0; };
   const int unit = p.format == QZ_MXFP4 ? 2 : 4;  // bytes of scales per 64 columns
   a.scales_vec = p.cols % 128 == 0 && aligned_scales(2 * unit) ? 2 : p.cols % 64 == 0 && aligned_scales(unit) ? 1 : 0;
   Plan plans[2];
-  const int launches = plan_of(a.nout, p.mode == kModeGated ? kBM / 2 : kBM, p.tokens, a.boxes, FMT == QZ_INT4 ? 1060.0 : 750.0, plans);
+  const int launches = plan_of(p, plans);
   if (launches == 0) return QZ_ERR_UNSUPPORTED;
   for (int i = 0; i < launches; ++i) {
     const qz_status st = launch_plan<FMT>(a, plans[i], s);

@@ -180,3 +180,65 @@ def test_e2m1_weights_are_held_exactly(qz, fmt, shape):
     for got, want, n, terms in ((qz.linear(F.bf16_cuda(x), h, out_dtype=torch.float32), x @ w["values"].T, cols, np.abs(x) @ a.T),
                                 (qz.linear_backward(F.bf16_cuda(dy), h, out_dtype=torch.float32), dy @ w["values"], rows, np.abs(dy) @ a)):
         F.assert_within(F.host(got), want, F.sum_bound(n, terms) - 2.0 ** -17 * terms)
+
+
+# Calls large enough for the streaming kernel by its estimate: every n-tile count, rows of whole steps of 256
+# columns and not, one weight and two, INT4 in two halves.  (mode, format, group, tokens, outputs, columns)
+STREAMED = [("linear", "nvfp4", 16, 8, 8192, 4096), ("linear", "mxfp4", 32, 8, 8200, 4064), ("linear", "nvfp4", 16, 9, 32768, 4096),
+            ("linear", "mxfp4", 32, 16, 40000, 4064), ("linear", "nvfp4", 16, 16, 40003, 4096), ("gated", "mxfp4", 32, 7, 8192, 4096),
+            ("gated", "nvfp4", 16, 8, 8192, 4064), ("gated", "mxfp4", 32, 12, 16384, 4096), ("gated", "nvfp4", 16, 13, 16400, 3872),
+            ("linear", "int4", 32, 8, 8192, 1056), ("linear", "int4", 128, 8, 8192, 4096), ("linear", "int4", 32, 16, 8192, 4096),
+            ("linear", "int4", 64, 24, 32770, 2048), ("linear", "int4", 128, 31, 32768, 1920), ("linear", "int4", 32, 32, 32768, 2016),
+            ("gated", "int4", 128, 9, 8192, 2048), ("gated", "int4", 64, 20, 16384, 1984), ("gated", "int4", 32, 32, 20000, 2048),
+            ("linear", "int4", 128, 16, 16384, 8192), ("gated", "int4", 64, 13, 9000, 9088)]
+
+
+def large(qz, gen, fmt, group, rows, cols):
+    """A weight of any codes with scales that are powers of two near 1: the handle's Quantized and the values."""
+    import torch
+    codes = torch.randint(0, 256, (rows, cols // 2), dtype=torch.uint8, device="cuda", generator=gen)
+    k = torch.randint(-2, 2, (rows, cols // group), device="cuda", generator=gen)
+    one = torch.ones(1, device="cuda")
+    scales = torch.ldexp(one, k) if fmt == "int4" else (k + 127 if fmt == "mxfp4" else (k + 7) << 3).to(torch.uint8)
+    q = qz.Quantized(codes, scales, one, qz.FORMATS[fmt], qz.QZ_GRAN_BLOCK, qz.QZ_SCALE_UP, rows, cols, group)
+    table = torch.tensor([c - 16 * (c > 7) for c in range(16)] if fmt == "int4" else [*F.E2M1, *-F.E2M1], dtype=torch.float64, device="cuda")
+    values = torch.stack((table[(codes & 15).int()], table[(codes >> 4).int()]), -1).reshape(rows, cols // group, group)
+    return q, (values * torch.ldexp(one, k).double()[..., None]).reshape(rows, cols)
+
+
+@pytest.mark.parametrize("case", STREAMED)
+def test_streamed(qz, case):
+    """Exact sums of ordinary activations, of a token that f16 does not hold (its large value meets codes of 0),
+    and beside an output whose scales are 2^100."""
+    import torch
+    mode, fmt, group, tokens, rows, cols = case
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(tokens + cols)
+    ws = [large(qz, gen, fmt, group, rows, cols) for _ in range(2 if mode == "gated" else 1)]
+    for q, v in ws:
+        q.codes[:, 0] &= 0xF0
+        v[:, 0] = 0
+    x = torch.randint(-4, 5, (tokens, cols), device="cuda", generator=gen).double()
+    x[:, 0] = 4
+
+    def check(skip=None):
+        outs = qz.linear(x.bfloat16(), qz.Weight(ws[0][0]), out_dtype=torch.float32), None
+        if mode == "gated":
+            outs = qz.gated_ffn(x.bfloat16(), *(qz.Weight(q) for q, _ in ws), save=True)[1:]
+        for got, (_, v) in zip(outs, ws):
+            want = x @ v.T
+            if mode == "gated":
+                want = want.float().bfloat16().double()
+            same = got.double() == want
+            if skip is not None:
+                same[:, skip] = True
+            assert bool(same.all())
+
+    check()
+    x[tokens // 2, 0] = 2.0 ** 45
+    check()
+    x[tokens // 2, 0] = 4
+    if fmt != "nvfp4":  # one output of a tile, most of the way through its sum
+        at = (cols // group) * 3 // 4
+        ws[0][0].scales[rows - 3, at] = 2.0 ** 100 if fmt == "int4" else 227
+        check(skip=rows - 3)
