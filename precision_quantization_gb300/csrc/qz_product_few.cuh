@@ -14,7 +14,7 @@
 //     bits of every value down to 2^-31 of that magnitude (2^-17, in units of 2^-24).  Where a token
 //     spans more, or p is negative (sums times the smallest scales would leave fp32), all activations
 //     of the call stay bf16 and the weights are turned into bf16, exactly: see `wide`.  (Logits below:
-//     38 us, such activations 59.)
+//     38 us, such activations 60.)
 //
 // A tile is 16 outputs (gated: 16 of gate and of up).  ks of a CTA's warps share a tile, each with a
 // contiguous part of the sum, and join their partial sums in shared memory in warp order; CTAs
@@ -306,31 +306,7 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
       m = __reduce_max_sync(kFull, m);
       if (lane == 0) atomicMax(&s_amax[tok], m << 16);
     };
-    bool beyond = false;  // this thread has met a value that f16 does not hold
-    const auto convert = [&](int i, int tok, int c, bool raw) {
-      const uint32_t m = s_amax[tok];
-      // 2^p: 14 less the exponent of the largest magnitude, 120 at most
-      const float f = pow2(m == 0u ? 0 : min(120, 14 + 127 - static_cast<int>(m >> 23)));
-      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      uint32_t o[4] = {w[0], w[1], w[2], w[3]};
-      if (!raw) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[q]) : "f"(__uint_as_float(w[q] & 0xffff0000u) * f), "f"(__uint_as_float(w[q] << 16) * f));
-        // The largest has exponent field E, p = 141 - E (120 at most: then f16 holds every bf16 value).
-        // Values but 0 with a field below E - 31 are too small (subnormals have the spacing of field 1);
-        // they are among those that came out below 2^-16.
-        const uint32_t small = min_abs_f16x2(min_abs_f16x2(o[0], o[1]), min_abs_f16x2(o[2], o[3]));
-        if ((small & 0xff00u) == 0u || (small & 0xff000000u) == 0u) {
-          const int E = static_cast<int>(m >> 23), least = E > 32 ? (E - 31) << 7 : 0;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int lo = w[q] & 0x7fffu, hi = (w[q] >> 16) & 0x7fffu;
-            beyond |= (lo != 0 && lo < least) || (hi != 0 && hi < least);
-          }
-        }
-        if constexpr (FMT != QZ_NVFP4) beyond |= m >= 142u << 23;
-      }
+    const auto put = [&](int tok, int c, uint32_t (&o)[4]) {
       if constexpr (FMT == QZ_INT4) {  // values 0 .. 7 in the order of the weights' pairs
         const uint32_t e[4] = {o[0], o[1], o[2], o[3]};
         o[0] = __byte_perm(e[0], e[2], 0x5410);
@@ -341,6 +317,31 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
       if (c < per_token)
         *reinterpret_cast<uint4*>(xs + ((c >> 2) * tokens + tok) * 64 + (c & 3) * 16) = make_uint4(o[0], o[1], o[2], o[3]);
     };
+    bool beyond = false;  // this thread has met a value that f16 does not hold
+    const auto convert = [&](int i, int tok, int c) {
+      const uint32_t m = s_amax[tok];
+      // 2^p: 14 less the exponent of the largest magnitude, 120 at most
+      const float f = pow2(m == 0u ? 0 : min(120, 14 + 127 - static_cast<int>(m >> 23)));
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[q]) : "f"(__uint_as_float(w[q] & 0xffff0000u) * f), "f"(__uint_as_float(w[q] << 16) * f));
+      // The largest has exponent field E, p = 141 - E (120 at most: then f16 holds every bf16 value).
+      // Values but 0 with a field below E - 31 are too small (subnormals have the spacing of field 1);
+      // they are among those that came out below 2^-16.
+      const uint32_t small = min_abs_f16x2(min_abs_f16x2(o[0], o[1]), min_abs_f16x2(o[2], o[3]));
+      if ((small & 0xff00u) == 0u || (small & 0xff000000u) == 0u) {
+        const int E = static_cast<int>(m >> 23), least = E > 32 ? (E - 31) << 7 : 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int lo = w[q] & 0x7fffu, hi = (w[q] >> 16) & 0x7fffu;
+          beyond |= (lo != 0 && lo < least) || (hi != 0 && hi < least);
+        }
+      }
+      if constexpr (FMT != QZ_NVFP4) beyond |= m >= 142u << 23;
+      put(tok, c, o);
+    };
     for (int base = 0, tok = 0, blk = 0; base < n; base += kHeld) {
       each(tok, blk, load);
       each(tok, blk, magnitude);
@@ -348,18 +349,21 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
       blk = (base + kHeld) - tok * blocks;
     }
     __syncthreads();
-    const auto stage = [&](bool raw) {
-      for (int base = 0, tok = 0, blk = 0; base < n; base += kHeld) {
-        if (n > kHeld) each(tok, blk, load);  // else still in registers
-        each(tok, blk, [&](int i, int t, int c) { convert(i, t, c, raw); });
-        tok = (base + kHeld) / blocks;
-        blk = (base + kHeld) - tok * blocks;
-      }
-    };
-    stage(false);
+    for (int base = 0, tok = 0, blk = 0; base < n; base += kHeld) {
+      if (n > kHeld) each(tok, blk, load);  // else still in registers
+      each(tok, blk, convert);
+      tok = (base + kHeld) / blocks;
+      blk = (base + kHeld) - tok * blocks;
+    }
     wide = __syncthreads_or(beyond);
-    if (wide) {
-      stage(true);
+    if (wide) {  // again, in little code
+#pragma unroll 1
+      for (int i = threadIdx.x; i < per_token * tokens; i += kAll) {
+        const int tok = i / per_token, c = i - tok * per_token;
+        const uint4 w = c < per_row ? __ldg(reinterpret_cast<const uint4*>(p.x0 + tok * p.ld_x) + c) : make_uint4(0u, 0u, 0u, 0u);
+        uint32_t o[4] = {w.x, w.y, w.z, w.w};
+        put(tok, c, o);
+      }
       __syncthreads();
     }
   }
@@ -604,8 +608,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 1) product_few_kernel(const __
       }
     }
   };
-  if (wide) run(std::true_type{});
-  else run(std::false_type{});
+  if (!wide) run(std::false_type{});
+  else run(std::true_type{});
   // (every copy issued has been waited for by its step; after a wait that gave up they get a second more)
   if (s_abort)
     for (int i = 0; i < depth; ++i) {
