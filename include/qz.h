@@ -413,18 +413,24 @@ typedef enum {
  *   Activations and gradients are bf16, [tokens, ld] row-major with unit inner stride; each
  *   matrix has its own leading dimension, at least its width.  Outputs must not overlap inputs
  *   or each other.
- *   Arithmetic: products of bf16 activations with the exact weight values, summed in fp32 in an
- *   unspecified but fixed order (equal inputs give equal results); outputs are rounded once,
- *   to nearest even.  A non-finite activation makes the outputs of its own token non-finite
- *   and no others, as IEEE arithmetic has it (INT4: an Inf may become NaN, because a weight may
- *   be held as the sum of two bf16 values).
+ *   Arithmetic: products of bf16 activations with the weight values, summed in fp32 in an
+ *   unspecified but fixed order (equal inputs give equal results; the order may change with the
+ *   sizes and, up to 32 tokens, where one token's magnitudes lie more than 2^31 apart); outputs
+ *   are rounded once, to nearest even.  MXFP4 and NVFP4 weights are exact in every product.  An
+ *   INT4 weight q s is exact up to fp32 rounding in products of a few tokens; on the tensor-core
+ *   tiles (always above 32 tokens, in backward passes, and with groups of 16 columns) it is held as
+ *   the sum of two bf16 values, 2^-17 of it at most away, because a third would cost half as many
+ *   products again: bf16 outputs do not show it, fp32 outputs may (2.4e-6 of a weight at rms).
+ *   A non-finite activation makes the outputs of its own token non-finite and no others, as IEEE
+ *   arithmetic has it (INT4: an Inf may become NaN, because of the two values); a NaN scale does
+ *   the same for its output (backward: for the gradients of its block's columns).
  *   Errors: QZ_ERR_NULL, QZ_ERR_ENUM (format, out_dtype, act), QZ_ERR_UNSUPPORTED (block_size;
  *   2^31 and more tokens, rows or cols), QZ_ERR_SHAPE (negative sizes, cols not a multiple of
  *   block_size, a leading dimension too small, gate and up of different shapes), QZ_ERR_ALIGN.
  *   tokens == 0 or an empty output enqueues nothing; an empty sum is 0.
  *   Alignment: any pointer and leading dimension of the element type's own alignment is right;
- *   16-byte aligned codes and activations, leading dimensions that are multiples of 8 and cols a
- *   multiple of 32 get the fast kernels.
+ *   16-byte aligned codes and activations, leading dimensions that are multiples of 8 (any, for one
+ *   token) and cols a multiple of 32 get the fast kernels; the others run some 80 times slower.
  *   Waits inside the kernels are bounded (1 s); should one give up, the outputs it stands for are NaN.
  *   Asynchronous on `stream`; no workspace. */
 
@@ -449,7 +455,9 @@ QZ_API qz_status qz_gated_ffn(const qz_weight* gate, const qz_weight* up, int32_
 /* Its backward pass from the kept pre-activations:
  *   dg = dh * u * act'(g), du = dh * act(g), dx = dg gate + du up.
  *   dh, g, u, dg, du  [tokens, rows] (g and u share ld_gu, dg and du ld_dgu);  dx [tokens, cols].
- * dg and du are rounded to bf16 once, as outputs and as the tensor cores' operands of dx. */
+ * dg and du are rounded to bf16 once, as outputs and as the tensor cores' operands of dx: dx is the
+ * gradient of what is returned as dg and du, at 1.4 times the rounding error of a bf16 dx from
+ * unrounded ones.  (Two bf16 terms of each would double the products.) */
 QZ_API qz_status qz_gated_ffn_backward(const qz_weight* gate, const qz_weight* up, int32_t act,
                                        const void* dh, int64_t ld_dh, const void* g, const void* u,
                                        int64_t ld_gu, int64_t tokens, void* dg, void* du, int64_t ld_dgu,

@@ -28,8 +28,8 @@ struct ProductArgs {
 
 // The streaming kernels for a few tokens (qz_product_few.cuh): their shared memory is a ring
 // of code boxes and a buffer of partial sums per warp, and the activations.
-// Tokens they take at most (above, the tiles are faster at every size): E2M1 weights 16, INT4, whose tiles
-// take two products a weight, 32.  Up to there the estimates of qz_product_plan.h decide.
+// Tokens they are built for: E2M1 weights 16, INT4, whose tiles take two products a weight, 32.  Up to there
+// the estimates of qz_product_plan.h decide.
 constexpr int few_tokens(int format) { return format == QZ_INT4 ? 32 : 16; }
 constexpr int kFewWarps = 16;
 constexpr int kTokenStride = 20;                  // floats of a token's 16 sums (banks 8 t + g)
@@ -40,8 +40,8 @@ constexpr uint32_t kFewSmem = 225 * 1024;         // dynamic; the barriers are s
 constexpr uint32_t few_fixed(int depth) { return kFewWarps * (depth * kSlot + kJoin * 4) + 1024; }
 inline int64_t few_steps(const ProductArgs& p) { return (p.cols + 255) / 256; }
 // whole steps, whose scales are aligned vectors; else the steps' tails and scales take narrow loads
-// (4 tokens, 32768 outputs, MXFP4: 8192 columns 39 us; 8160 columns 41 us, on the tensor-core tiles 70;
-// INT4 groups of 32: 54, 56 and 134)
+// (4 tokens, 32768 outputs, MXFP4: 8192 columns 38 us; 8160 columns 39 us, on the tensor-core tiles 70;
+// INT4 groups of 32: 51, 56 and 134)
 bool few_whole(const ProductArgs& p);
 // the deepest ring that leaves room for the activations, 0: none does
 inline int few_depth(const ProductArgs& p) {

@@ -22,10 +22,12 @@
 // (whole 128-byte lines) through a ring of its own by TMA and runs on into the next tile, so the
 // copies never pause; a step's scales are loaded into registers one step ahead.
 //
-// Measured: 32768 x 8192 MXFP4, 4 tokens: 39 us, 3.7 TB/s (floor 21); 16384 x 4096 NVFP4 gate and
-// up, 1 token: 22.5 us, 3.4 TB/s (floor 11).  Bound by the latency of the decoding and the products:
-// some 20 instructions per mma.sync, issued in 0.6 of the cycles by four warps a scheduler; more
-// warps leave each too few registers (31 -> 36 us for the gated token).
+// Measured, on the GPU alone: 32768 x 8192 MXFP4, 4 tokens: 38 us, 3.8 TB/s (floor 21); 16384 x 4096
+// NVFP4 gate and up, 1 token: 21 us, 3.6 TB/s (floor 11); 4096 x 4096 NVFP4, 1 token: 5.7 us (floor 1.4).
+// No pipe is full: some 20 instructions per mma.sync, issued in 0.5 of the cycles by four warps a
+// scheduler, wait for one another, and the start stages all activations in every CTA (0.48 us a token
+// and 4096 columns) before the first product.  More warps leave each too few registers (31 -> 36 us
+// for the gated token).
 #pragma once
 
 #include <cuda.h>  // CUtensorMap and its enumerators (types only; the encoder is looked up)

@@ -5,9 +5,10 @@
 //
 // The weights are the MMA's A operand (M: 128 outputs a CTA, one tensor-memory lane each), the
 // activations its B operand (N: up to 256 tokens, one fp32 tensor-memory column each).  E2M1
-// times its block scale has at most 6 significant bits and so is exact in bf16; an INT4 weight
-// q s is held as the sum of two bf16 values (16 bits of it) and takes two MMAs.  So kind::f16
-// with fp32 accumulation gives the sums of include/qz.h without a rounding of the weights.
+// times its block scale has at most 6 significant bits and so is exact in bf16: kind::f16 with fp32
+// accumulation gives the sums of include/qz.h without a rounding of the weights.  An INT4 weight q s
+// is held as the sum of two bf16 values (2^-17 of it at most away) and takes two MMAs; three would
+// hold it and take half as long again.
 //
 // Roles of a CTA's warps (every wait is bounded):
 //   warp 0       streams the tokens' boxes (128 summands, INT4 64) into a ring by TMA
@@ -26,10 +27,12 @@
 // distributed shared memory and add them in slice order, so few tokens still fill the GPU and
 // equal inputs give equal results.
 //
-// Measured, NVFP4: gated 4096 tokens, 2 x 16384 x 4096: 575 us, 1.91 PFLOP/s, bound by the tensor
-// cores (the library's product of that size on bf16 weights takes 560); 2048 tokens backward,
-// 8192 x 4096: 91 us, 1.51 PFLOP/s, the last round of tiles.  MXFP4, gated 77 tokens, 2 x 10240 x
-// 4096: 38 us, bound by the decoders (842 cycles a box against 384 of MMAs) and the start.
+// Measured, NVFP4, passes one after the other for seconds: gated 4096 tokens, 2 x 16384 x 4096: 659 us,
+// 1.67 PFLOP/s, at 1552 MHz under the power cap, bound by the tensor cores (the library's product of
+// that size on bf16 weights, measured likewise: 610 us at 1507 MHz); 2048 tokens backward, 8192 x 4096:
+// 94 us, 1.46 PFLOP/s at 1972 MHz, the last round of tiles (the library 86).  MXFP4, gated 77 tokens,
+// 2 x 10240 x 4096: 33 us on the GPU in two launches, bound by the decoders (842 cycles a box against
+// 384 of MMAs) and the starts.
 #pragma once
 
 #include <cuda.h>  // CUtensorMap and its enumerators (types only; the encoder is looked up)

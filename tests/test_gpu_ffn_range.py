@@ -19,8 +19,9 @@ def qz():
 
 def bound(w, tokens, k, terms):
     """F.sum_bound for weights that are held exactly; its 2^-17 belongs to INT4 weights on the
-    tensor-core tiles alone (more than 32 tokens, or a group of 16), as the sum of two bf16 values."""
-    two_terms = w["fmt"] == "int4" and tokens > 32
+    tensor-core tiles alone (up to 4 tokens of up to 4096 columns never take them), as the sum of two
+    bf16 values."""
+    two_terms = w["fmt"] == "int4" and tokens > 4
     return F.sum_bound(k, terms) - (0 if two_terms else 2.0 ** -17) * terms + 2.0 ** -140
 
 
@@ -29,7 +30,7 @@ def linear(qz, x, w):
     return F.host(qz.linear(F.bf16_cuda(x), F.handle(w), out_dtype=torch.float32))
 
 
-# one n-tile of the streaming kernel, two, the tiles after it (INT4: from 33 on)
+# one token, one n-tile of eight, two and more, whichever kernel they take at these sizes
 TOKENS = [1, 7, 16, 17, 32, 33]
 
 
