@@ -244,7 +244,8 @@ def _append(s):
         x = torch.where(is_new[..., None, None], x[row], 0.0)            # [seqs, blocks, block, heads, dim]
         old = scales[to[..., 0], :, part]                                # [seqs, blocks, heads]
         was = torch.where(is_held.any(-1)[..., None], old, 0.0)
-        scale = torch.maximum(was, x.abs().amax((2, 4)) / QMAX[fmt])
+        # (a division by a number would be a product with its rounded reciprocal)
+        scale = torch.maximum(was, x.abs().amax((2, 4)) / torch.full((), QMAX[fmt], device="cuda"))
         safe = torch.where(scale > 0, scale, 1.0)
         c = codes[to, :, slot]                                           # [seqs, blocks, block, heads, dim]
         again = _round_codes(c.view(VIEW[fmt]).float() * (was / safe)[:, :, None, :, None], fmt)
