@@ -493,6 +493,137 @@ QZ_API qz_status qz_layer_norm_backward(int32_t dtype, const void* dy, int64_t l
                                         float* dweight, float* dbias, void* ws, size_t ws_bytes,
                                         qz_stream_t stream);
 
+/* ---- Keys and values held in 8 bits --------------------------------------------------------
+ * What the attention half of a transformer layer does with a key-value cache: the rotation of
+ * queries and keys by their positions, with its gradient, appending keys and values to a paged
+ * cache of INT8 or FP8 codes, and the attention that reads it.  The blog post has no counterpart;
+ * element and scale rules are those of the formats above.
+ *
+ * Vectors of a head lie in [tokens, heads, dim] tensors with unit inner stride and strides of their
+ * own for tokens (ld_*) and heads (hd_*), in elements: slices of a fused projection need no copy.
+ * Outputs must not overlap inputs, except where noted. */
+
+/* Rotation by positions: cos and sin, device fp32 [positions, pairs], of each position's angles
+ * (qz_rotary_fill makes them; any table of one position or more will do).  Pair i of a head's vector is elements i and
+ * i + pairs, or, interleaved != 0, 2 i and 2 i + 1; elements from 2 pairs on pass unchanged. */
+typedef struct {
+  const float* cos;
+  const float* sin;
+  int64_t positions;
+  int32_t pairs;
+  int32_t interleaved;
+} qz_rotary_table;
+
+/* cos[p][i] = fl32(amplitude cos(p turns[i])), sin alike, for positions 0 .. positions - 1:
+ *   turns   device fp64 [pairs], the angle per position, in radians
+ *   cos, sin  device fp32 [positions, pairs]
+ * The angle and its functions are computed in 64 bits. */
+QZ_API qz_status qz_rotary_fill(const double* turns, int64_t positions, int64_t pairs, double amplitude,
+                                float* cos, float* sin, qz_stream_t stream);
+
+/* y = x rotated: with (a, b) a pair and c, s the cos and sin of its token's position,
+ *   a' = fl32(fl32(a c) - fl32(b s)),  b' = fl32(fl32(b c) + fl32(a s)),
+ * rounded once to dtype (QZ_BF16 or QZ_F32, of x and y): every bit is defined.
+ *   positions  device int32 [tokens]; NULL: 0, 1, ...  A token whose position lies outside the table
+ *              gets NaN in place of its pairs.
+ *   y          may be x itself (same strides)
+ * Errors: QZ_ERR_NULL, QZ_ERR_ENUM (dtype), QZ_ERR_SHAPE (negative sizes, 2 pairs > dim, vectors that
+ * overlap), QZ_ERR_UNSUPPORTED (2^31 and more tokens, heads or dim; heads * dim of 2^31 and more), QZ_ERR_ALIGN. */
+QZ_API qz_status qz_rotary(const qz_rotary_table* table, int32_t dtype, const void* x, int64_t ld_x, int64_t hd_x,
+                           int64_t tokens, int64_t heads, int64_t dim, const int32_t* positions, void* y,
+                           int64_t ld_y, int64_t hd_y, qz_stream_t stream);
+
+/* Its gradient, dx = dy rotated back (the same with -s for s).  The table takes no gradient. */
+QZ_API qz_status qz_rotary_backward(const qz_rotary_table* table, int32_t dtype, const void* dy, int64_t ld_dy,
+                                    int64_t hd_dy, int64_t tokens, int64_t heads, int64_t dim,
+                                    const int32_t* positions, void* dx, int64_t ld_dx, int64_t hd_dx,
+                                    qz_stream_t stream);
+
+/* A cache: pages of `page` tokens, each holding the keys and the values of every kv head.
+ *   format            QZ_INT8, QZ_FP8_E4M3 or QZ_FP8_E5M2
+ *   block             tokens that share a scale: 16, 32, 64 or 128
+ *   page              tokens of a page: a multiple of block, up to 1024
+ *   dim               elements of a vector: a multiple of 16, up to 256
+ *   k_codes, v_codes  device, [pages, kv_heads, page, dim] bytes, 16-byte aligned
+ *   k_scales, v_scales  device fp32 [pages, kv_heads, page / block]
+ * A value is decode(code) * scale of its block.  A block of zeros may have scale 0. */
+typedef struct {
+  int32_t format;
+  int32_t block;
+  int32_t page;
+  int32_t kv_heads;
+  int32_t dim;
+  int32_t reserved; /* 0 */
+  int64_t pages;
+  void* k_codes;
+  float* k_scales;
+  void* v_codes;
+  float* v_scales;
+} qz_cache;
+
+/* The sequences of a call, all device int32.
+ *   table    [sequences, ld_table]: the page of each `page` tokens of a sequence; table_pages of
+ *            a row's entries are read, so a sequence holds up to table_pages * page tokens.  An entry
+ *            outside [0, pages) means no page.
+ *   lengths  [sequences]: the tokens of each sequence, those of this call (the last ones) included
+ *   starts   [sequences + 1]: the first row of each sequence's tokens in the call's tensors, not
+ *            decreasing; rows from starts[sequences] on belong to no sequence.  NULL: one token each
+ *            (tokens == sequences).
+ * The new token i of n of a sequence has position length - n + i.  None of the three is copied to the
+ * host, so the same call can be captured once and replayed as they change. */
+typedef struct {
+  int64_t sequences;
+  const int32_t* table;
+  int64_t ld_table;
+  int64_t table_pages;
+  const int32_t* lengths;
+  const int32_t* starts;
+} qz_batch;
+
+/* Appends the keys and values of new tokens, k, v [tokens, kv_heads, dim] of dtype (QZ_BF16 or QZ_F32),
+ * the keys rotated by their positions on the way; with q != NULL also rotates the queries of the same
+ * tokens, q -> q_out [tokens, heads, dim] of dtype, as qz_rotary does (q_out may be q itself).
+ *   table  NULL: no rotation (then q must be NULL)
+ * For each block that gets new tokens, of keys and of values alike, with `old` its scale where it
+ * already holds tokens (their positions lie below the first new one) and 0 where it holds none:
+ *   s = max(old, fl32(A / qmax)), A the largest magnitude of the new values (rotated keys unrounded),
+ *   new codes  RNE(fl32(x / s)), saturating;   held codes, where s > old,  RNE(fl32(decode(q) fl32(old / s)));
+ *   s == 0: codes 0.  Every code and scale is defined to the bit.  A NaN or Inf among the new values makes
+ *   its block's scale NaN or Inf and the block's codes 0, so that attention to the block gives NaN.
+ * A token with no page, or at a position below 0, past the table's end or outside the rotation table,
+ * is not written; its q_out is rotated all the same (NaN in place of the pairs, outside the table).  A block
+ * gets new tokens from one sequence per call: two that share a page must not append to it.
+ * Errors: as above, QZ_ERR_UNSUPPORTED also for block, page, dim outside the ranges above, QZ_ERR_SHAPE for
+ * heads not a multiple of kv_heads, tokens != sequences without starts. */
+QZ_API qz_status qz_cache_append(const qz_cache* cache, const qz_batch* batch, int32_t dtype, const void* k,
+                                 int64_t ld_k, int64_t hd_k, const void* v, int64_t ld_v, int64_t hd_v,
+                                 int64_t tokens, const qz_rotary_table* table, const void* q, int64_t ld_q,
+                                 int64_t hd_q, int64_t heads, void* q_out, int64_t ld_qo, int64_t hd_qo,
+                                 qz_stream_t stream);
+
+/* Attention of new tokens to the cache that holds their sequence (their own keys included):
+ *   out[t][h] = sum_j p_j V[j],  p = softmax over the visible positions j of (scale Q[t][h] . K[j]),
+ * kv head h / (heads / kv_heads), visible: max(0, i - window + 1) <= j <= i for a token at position i
+ * (window 0: all j <= i).  Positions without a page are not visible.  A token that sees nothing gets 0.
+ *   q        bf16 [tokens, heads, dim], heads a multiple of kv_heads;  out  bf16 alike
+ *   lse      fp32 [tokens, heads] (leading dimension ld_lse) or NULL: log sum exp of the visible scores,
+ *            -inf where there are none
+ *   scale    a finite number > 0
+ *   ws, ws_bytes  qz_cache_attention_workspace bytes of device memory, uninitialised, 16-byte aligned;
+ *            calls that may overlap need one each
+ * Rows that belong to no sequence are left as they are.
+ * Arithmetic: scores are sums of exact products of q and decoded codes in fp32, the keys' scale applied to
+ * the sum; weights p times the values' scale are rounded to 11 bits (f16, relative to the largest in the
+ * sequence; below 2^-29 of it gradually fewer) for the product with the decoded codes; sums in fp32, in an
+ * unspecified but fixed order: equal inputs give equal results.  A non-finite query makes its own outputs
+ * non-finite and no others.  Codes and scales of positions past a sequence's length are not looked at.
+ * Errors: as above; QZ_ERR_WORKSPACE. */
+QZ_API size_t qz_cache_attention_workspace(const qz_cache* cache, int64_t sequences, int64_t tokens, int64_t heads);
+QZ_API qz_status qz_cache_attention(const qz_cache* cache, const qz_batch* batch, const void* q, int64_t ld_q,
+                                    int64_t hd_q, int64_t tokens, int64_t heads, float scale, int64_t window,
+                                    void* out, int64_t ld_out, int64_t hd_out, float* lse, int64_t ld_lse,
+                                    void* ws, size_t ws_bytes, qz_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

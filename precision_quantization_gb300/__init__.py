@@ -1,7 +1,8 @@
 """Python binding of libqz: quantize tensors on a GB300 to INT8 / FP8 E4M3 / FP8 E5M2 /
 MXFP4 / NVFP4, dequantize them, measure the quantization error, and run the feed-forward half
 of a transformer layer on the 4-bit weights (``Weight``, ``linear``, ``gated_ffn``,
-``layer_norm`` and their gradients).
+``layer_norm`` and their gradients) and its attention half on a paged INT8 / FP8 key-value cache
+(``KVCache``, ``RotaryTable``, ``rotary``, ``cache_append``, ``cache_attention``).
 
 The functions ``qz_*`` mirror the C ABI of ``include/qz.h`` one to one (same names, same
 arguments, device pointers as integers).  ``quantize`` / ``dequantize`` / ``error_stats`` /
@@ -47,7 +48,9 @@ ABI_SYMBOLS = ("qz_status_string", "qz_workspace_size", "qz_workspace_init", "qz
                "qz_selftest_pipeline_timeout", "qz_get_device_status", "qz_host_plan_create",
                "qz_host_run", "qz_host_plan_status", "qz_host_plan_destroy", "qz_linear",
                "qz_linear_backward", "qz_gated_ffn", "qz_gated_ffn_backward", "qz_layer_norm",
-               "qz_layer_norm_backward_workspace", "qz_layer_norm_backward")
+               "qz_layer_norm_backward_workspace", "qz_layer_norm_backward", "qz_rotary_fill",
+               "qz_rotary", "qz_rotary_backward", "qz_cache_append", "qz_cache_attention_workspace",
+               "qz_cache_attention")
 QZ_HOST_MAX_RUNS = 16
 
 
@@ -81,6 +84,26 @@ class QzWeight(C.Structure):
                 ("tensor_scale_dev", C.c_void_p)]
 
 
+class QzRotaryTable(C.Structure):
+    """qz_rotary_table: cos and sin of each position's angles."""
+    _fields_ = [("cos", C.c_void_p), ("sin", C.c_void_p), ("positions", C.c_int64),
+                ("pairs", C.c_int32), ("interleaved", C.c_int32)]
+
+
+class QzCache(C.Structure):
+    """qz_cache: a paged 8-bit key-value cache."""
+    _fields_ = [("format", C.c_int32), ("block", C.c_int32), ("page", C.c_int32),
+                ("kv_heads", C.c_int32), ("dim", C.c_int32), ("reserved", C.c_int32),
+                ("pages", C.c_int64), ("k_codes", C.c_void_p), ("k_scales", C.c_void_p),
+                ("v_codes", C.c_void_p), ("v_scales", C.c_void_p)]
+
+
+class QzBatch(C.Structure):
+    """qz_batch: the sequences of a call."""
+    _fields_ = [("sequences", C.c_int64), ("table", C.c_void_p), ("ld_table", C.c_int64),
+                ("table_pages", C.c_int64), ("lengths", C.c_void_p), ("starts", C.c_void_p)]
+
+
 class QzError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {qz_status_string(status)} (status {status})")
@@ -99,6 +122,7 @@ def lib():
         L = C.CDLL(LIB_PATH)
         vp, dp, i32, i64 = C.c_void_p, C.POINTER(QzDesc), C.c_int32, C.c_int64
         wp = C.POINTER(QzWeight)
+        rp, cp, bp = C.POINTER(QzRotaryTable), C.POINTER(QzCache), C.POINTER(QzBatch)
         sig = {
             "qz_status_string": (C.c_char_p, [i32]),
             "qz_workspace_size": (C.c_size_t, [dp]),
@@ -131,6 +155,14 @@ def lib():
             "qz_layer_norm_backward_workspace": (C.c_size_t, [i64, i64]),
             "qz_layer_norm_backward": (i32, [i32, vp, i64, vp, i64, i64, i64, vp, vp, vp, vp, i64,
                                              vp, vp, vp, C.c_size_t, vp]),
+            "qz_rotary_fill": (i32, [vp, i64, i64, C.c_double, vp, vp, vp]),
+            "qz_rotary": (i32, [rp, i32, vp, i64, i64, i64, i64, i64, vp, vp, i64, i64, vp]),
+            "qz_rotary_backward": (i32, [rp, i32, vp, i64, i64, i64, i64, i64, vp, vp, i64, i64, vp]),
+            "qz_cache_append": (i32, [cp, bp, i32, vp, i64, i64, vp, i64, i64, i64, rp, vp, i64, i64,
+                                      i64, vp, i64, i64, vp]),
+            "qz_cache_attention_workspace": (C.c_size_t, [cp, i64, i64, i64]),
+            "qz_cache_attention": (i32, [cp, bp, vp, i64, i64, i64, i64, C.c_float, i64, vp, i64, i64,
+                                         vp, i64, vp, C.c_size_t, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -306,6 +338,42 @@ def qz_layer_norm_backward(dtype: int, dy: int, ld_dy: int, x: int, ld_x: int, r
                            stream: int = 0) -> int:
     return lib().qz_layer_norm_backward(dtype, dy, ld_dy, x, ld_x, rows, cols, mean, rstd, weight,
                                         dx, ld_dx, dweight, dbias, ws, ws_bytes, stream)
+
+
+def qz_rotary_fill(turns: int, positions: int, pairs: int, amplitude: float, cos: int, sin: int,
+                   stream: int = 0) -> int:
+    return lib().qz_rotary_fill(turns, positions, pairs, amplitude, cos, sin, stream)
+
+
+def qz_rotary(table: QzRotaryTable, dtype: int, x: int, ld_x: int, hd_x: int, tokens: int, heads: int,
+              dim: int, positions: int | None, y: int, ld_y: int, hd_y: int, stream: int = 0) -> int:
+    return lib().qz_rotary(table, dtype, x, ld_x, hd_x, tokens, heads, dim, positions, y, ld_y, hd_y, stream)
+
+
+def qz_rotary_backward(table: QzRotaryTable, dtype: int, dy: int, ld_dy: int, hd_dy: int, tokens: int,
+                       heads: int, dim: int, positions: int | None, dx: int, ld_dx: int, hd_dx: int,
+                       stream: int = 0) -> int:
+    return lib().qz_rotary_backward(table, dtype, dy, ld_dy, hd_dy, tokens, heads, dim, positions, dx,
+                                    ld_dx, hd_dx, stream)
+
+
+def qz_cache_append(cache: QzCache, batch: QzBatch, dtype: int, k: int, ld_k: int, hd_k: int, v: int,
+                    ld_v: int, hd_v: int, tokens: int, table: QzRotaryTable | None, q: int | None,
+                    ld_q: int, hd_q: int, heads: int, q_out: int | None, ld_qo: int, hd_qo: int,
+                    stream: int = 0) -> int:
+    return lib().qz_cache_append(cache, batch, dtype, k, ld_k, hd_k, v, ld_v, hd_v, tokens, table, q, ld_q,
+                                 hd_q, heads, q_out, ld_qo, hd_qo, stream)
+
+
+def qz_cache_attention_workspace(cache: QzCache, sequences: int, tokens: int, heads: int) -> int:
+    return lib().qz_cache_attention_workspace(cache, sequences, tokens, heads)
+
+
+def qz_cache_attention(cache: QzCache, batch: QzBatch, q: int, ld_q: int, hd_q: int, tokens: int,
+                       heads: int, scale: float, window: int, out: int, ld_out: int, hd_out: int,
+                       lse: int | None, ld_lse: int, ws: int | None, ws_bytes: int, stream: int = 0) -> int:
+    return lib().qz_cache_attention(cache, batch, q, ld_q, hd_q, tokens, heads, scale, window, out, ld_out,
+                                    hd_out, lse, ld_lse, ws, ws_bytes, stream)
 
 
 # ---------------------------------------------------------------- torch marshalling
@@ -813,3 +881,302 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, params: bool = True, out
     if rc:
         raise QzError(rc, "qz_layer_norm_backward")
     return dx, dw, db
+
+
+# ---------------------------------------------------------------- keys and values held in 8 bits
+def rotary_turns(pairs: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                 original: int = 0, fast: float = 32.0, slow: float = 1.0):
+    """The angle per position of each pair, base ** (-i / pairs) as fp64 [pairs] on the CPU, scaled for
+    contexts ``factor`` times as long as the model was trained on:
+
+    "linear"  every angle divided by factor (position interpolation);
+    "ntk"     the base raised so that the slowest pair's angle is divided by factor and the fastest's
+              kept (NTK-aware interpolation);
+    "parts"   pairs that turn more than ``fast`` times over the ``original`` positions are kept, those
+              that turn less than ``slow`` times divided by factor, those between blended linearly in
+              their index (the interpolation by parts of YaRN, whose amplitude is
+              0.1 log(factor) + 1)."""
+    import math
+    torch = _torch()
+    if pairs < 0 or not base > 0 or not factor > 0:
+        raise ValueError("pairs, base and factor must be positive")
+    i = torch.arange(pairs, dtype=torch.float64)
+    if scaling == "ntk":
+        base = base * factor ** (pairs / max(pairs - 1, 1))
+    turns = base ** (-i / max(pairs, 1))
+    if scaling in (None, "ntk"):
+        return turns
+    if scaling == "linear":
+        return turns / factor
+    if scaling != "parts":
+        raise ValueError(f"unknown scaling {scaling!r}: linear, ntk or parts")
+    if original <= 0 or not fast > slow > 0 or base == 1:
+        raise ValueError("parts: original positions, and fast > slow > 0")
+    # the index of the pair that turns n times over the original positions
+    at = lambda n: pairs * math.log(original / (n * 2 * math.pi)) / math.log(base)  # noqa: E731
+    low, high = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), pairs - 1)
+    kept = 1 - ((i - low) / max(high - low, 1e-3)).clamp(0, 1)
+    return turns / factor * (1 - kept) + turns * kept
+
+
+class RotaryTable:
+    """The rotation by positions for ``rotary`` and ``cache_append``: cos and sin, fp32 CUDA tensors
+    [positions, pairs], contiguous.  It refers to the tensors and keeps them.  ``RotaryTable.make``
+    fills them."""
+
+    def __init__(self, cos, sin, interleaved: bool = False):
+        f32 = _torch().float32
+        if cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != f32 or sin.dtype != f32:
+            raise ValueError("cos and sin must be fp32 [positions, pairs] tensors of one shape")
+        if not (cos.is_contiguous() and sin.is_contiguous()):
+            raise ValueError("cos and sin must be contiguous")
+        if cos.get_device() != sin.get_device():
+            raise ValueError("cos and sin must be on one device")
+        self.positions, self.pairs = cos.shape
+        if self.positions < 1:
+            raise ValueError("a table needs one position or more")
+        self.interleaved, self.device = bool(interleaved), cos.get_device()
+        self.buffers = (cos, sin)  # the pointers' owners
+        self.desc = QzRotaryTable(cos.data_ptr(), sin.data_ptr(), self.positions, self.pairs, int(self.interleaved))
+
+    @classmethod
+    def make(cls, positions: int, turns, interleaved: bool = False, amplitude: float = 1.0, device="cuda"):
+        """cos and sin of p * turns[i] for positions 0 .. positions - 1, times amplitude, computed in 64
+        bits on the GPU (qz_rotary_fill).  turns: fp64 [pairs], as of rotary_turns."""
+        torch = _torch()
+        device = torch.device(device)
+        with torch.cuda.device(device):
+            turns = torch.as_tensor(turns, dtype=torch.float64).to(device).contiguous()
+            if turns.dim() != 1:
+                raise ValueError("turns must be a vector")
+            cos, sin = (torch.empty((positions, turns.numel()), dtype=torch.float32, device=device) for _ in range(2))
+            _check(qz_rotary_fill(turns.data_ptr(), positions, turns.numel(), amplitude, cos.data_ptr(), sin.data_ptr(),
+                                  _stream(None)), "qz_rotary_fill")
+        return cls(cos, sin, interleaved)
+
+
+def _vectors(t, heads: int | None, dim: int | None, dtype, what: str, device: int):
+    """Strides (of tokens, of heads) of a [tokens, heads, dim] tensor on GPU `device` with unit inner
+    stride; heads, dim, dtype None: any."""
+    if t.dim() == 3 and t.get_device() == device >= 0 and (dtype is None or t.dtype is dtype):
+        (n, h, d), (ld, hd, s) = t.shape, t.stride()
+        if (heads is None or h == heads) and (dim is None or d == dim):
+            if s == 1 or d <= 1 or n == 0 or h == 0:
+                return ld, hd
+            raise ValueError(f"{what}: the inner dimension must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on the GPU")
+    if t.get_device() != device:
+        raise ValueError(f"{what} must be on cuda:{device}, not {t.device}")
+    raise ValueError(f"{what} must be a [tokens, {heads or 'heads'}, {dim or 'dim'}] {dtype or ''} tensor, not {tuple(t.shape)} {t.dtype}")
+
+
+def _ints(t, shape: tuple, what: str, device: int):
+    """The address of a contiguous int32 tensor of `shape` on GPU `device`."""
+    if t.dtype is not _torch().int32 or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on cuda:{device}")
+    return t.data_ptr()
+
+
+def _rotary_call(name: str, x, table: RotaryTable, positions, out, stream, what: str):
+    torch, device = _torch(), x.get_device()
+    if stream is not None or (device >= 0 and device != torch._C._cuda_getDevice()):
+        with _on(stream, x):
+            return _rotary_call(name, x, table, positions, out, None, what)
+    code = _dtype_code(x.dtype)
+    ld_x, hd_x = _vectors(x, None, None, None, what, device)
+    tokens, heads, dim = x.shape
+    if table.device != device:
+        raise ValueError(f"the table must be on cuda:{device}")
+    if out is None:
+        out = torch.empty((tokens, heads, dim), dtype=x.dtype, device=x.device)
+        ld_y, hd_y = heads * dim, dim
+    else:
+        ld_y, hd_y = _vectors(out, heads, dim, x.dtype, "out", device)
+        _same_tokens(tokens, out=out)
+    rc = getattr(_lib or lib(), name)(table.desc, code, x.data_ptr(), ld_x, hd_x, tokens, heads, dim,
+                                      None if positions is None else _ints(positions, (tokens,), "positions", device),
+                                      out.data_ptr(), ld_y, hd_y, torch._C._cuda_getCurrentRawStream(device))
+    if rc:
+        raise QzError(rc, name)
+    return out
+
+
+def rotary(x, table: RotaryTable, positions=None, out=None, stream=None):
+    """x, a bf16 / fp32 CUDA tensor [tokens, heads, dim], rotated by the tokens' positions (qz_rotary).
+    positions: int32 [tokens], by default 0, 1, ...  out may be x."""
+    return _rotary_call("qz_rotary", x, table, positions, out, stream, "x")
+
+
+def rotary_backward(dy, table: RotaryTable, positions=None, out=None, stream=None):
+    """The gradient of rotary: dy rotated back (qz_rotary_backward).  out may be dy."""
+    return _rotary_call("qz_rotary_backward", dy, table, positions, out, stream, "dy")
+
+
+class KVCache:
+    """A paged INT8 / FP8 key-value cache for ``cache_append`` and ``cache_attention``: the handle of
+    k_codes, v_codes (uint8 CUDA tensors [pages, kv_heads, page, dim]) and k_scales, v_scales (fp32
+    [pages, kv_heads, page / block]), all contiguous.  It refers to the tensors, which the calls
+    change in place, and keeps them.  ``KVCache.alloc`` makes them."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, fmt):
+        torch, self.fmt = _torch(), _fmt(fmt)
+        if self.fmt not in (QZ_INT8, QZ_FP8_E4M3, QZ_FP8_E5M2):
+            raise ValueError("a cache holds INT8, E4M3 or E5M2 codes")
+        if k_codes.dim() != 4 or k_scales.dim() != 3:
+            raise ValueError("codes are [pages, kv_heads, page, dim], scales [pages, kv_heads, page / block]")
+        self.pages, self.kv_heads, self.page, self.dim = k_codes.shape
+        blocks = k_scales.shape[2]
+        if blocks < 1 or self.page % blocks or k_scales.shape[:2] != k_codes.shape[:2]:
+            raise ValueError("the scales do not match the codes")
+        self.block = self.page // blocks
+        if self.block not in (16, 32, 64, 128) or self.page > 1024 or self.dim % 16 or not 0 < self.dim <= 256 or self.kv_heads < 1:
+            raise ValueError("block: 16, 32, 64 or 128 tokens; page: up to 1024; dim: a multiple of 16 up to 256")
+        if v_codes.shape != k_codes.shape or v_scales.shape != k_scales.shape:
+            raise ValueError("keys and values must have one shape")
+        self.device = k_codes.get_device()
+        self.buffers = (k_codes, k_scales, v_codes, v_scales)  # the pointers' owners
+        for t, dt in zip(self.buffers, (torch.uint8, torch.float32) * 2):
+            if t.dtype != dt or not t.is_contiguous() or t.get_device() != self.device:
+                raise ValueError("codes must be uint8, scales fp32, all contiguous and on one device")
+        self.desc = QzCache(self.fmt, self.block, self.page, self.kv_heads, self.dim, 0, self.pages,
+                            *(t.data_ptr() for t in self.buffers))
+
+    @property
+    def k_codes(self):
+        return self.buffers[0]
+
+    @property
+    def k_scales(self):
+        return self.buffers[1]
+
+    @property
+    def v_codes(self):
+        return self.buffers[2]
+
+    @property
+    def v_scales(self):
+        return self.buffers[3]
+
+    @classmethod
+    def alloc(cls, fmt, pages: int, kv_heads: int, page: int, dim: int, block: int | None = None, device="cuda"):
+        """An empty cache: ``pages`` pages of ``page`` tokens, one scale for each ``block`` tokens
+        (default: a page, 128 at most) and head."""
+        torch = _torch()
+        block = min(page, 128) if block is None else block
+        if block < 1 or page % block:
+            raise ValueError("page must be a multiple of block")
+        codes = [torch.zeros((pages, kv_heads, page, dim), dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.zeros((pages, kv_heads, page // block), dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(codes[0], scales[0], codes[1], scales[1], fmt)
+
+
+def _batch(table, lengths, starts, tokens: int, device: int) -> QzBatch:
+    """The sequences of a call: table int32 [sequences, pages], rows at any stride."""
+    if lengths.dim() != 1:
+        raise ValueError("lengths must be a vector")
+    n = lengths.shape[0]
+    if (table.dim() != 2 or table.dtype is not _torch().int32 or table.shape[0] != n or table.get_device() != device
+            or (table.shape[1] > 1 and n > 0 and table.stride(1) != 1)):
+        raise ValueError(f"table must be an int32 [{n}, pages] tensor on cuda:{device} with contiguous rows")
+    width = table.shape[1]
+    ld = table.stride(0) if n > 1 else width
+    if ld < width:
+        raise ValueError("table: rows overlap")
+    if starts is None and tokens != n:
+        raise ValueError(f"without starts each of the {n} sequences has one token, not {tokens} in all")
+    return QzBatch(n, table.data_ptr(), ld, width, _ints(lengths, (n,), "lengths", device),
+                   None if starts is None else _ints(starts, (n + 1,), "starts", device))
+
+
+def cache_append(cache: KVCache, k, v, table, lengths, starts=None, rotary: RotaryTable | None = None,
+                 q=None, out=None, stream=None):
+    """Append keys and values, bf16 / fp32 [tokens, kv_heads, dim], to the cache (qz_cache_append), the
+    keys rotated by their positions with ``rotary``.  With q [tokens, heads, dim] also rotates the
+    queries of the same tokens and returns them (out: where to; may be q); else returns None.
+
+    table: int32 [sequences, pages], the pages of each sequence; lengths: int32 [sequences], its tokens
+    with the new ones; starts: int32 [sequences + 1], its first row in k, v and q, None: one token each."""
+    torch, device = _torch(), k.get_device()
+    if stream is not None or (device >= 0 and device != torch._C._cuda_getDevice()):
+        with _on(stream, k):
+            return cache_append(cache, k, v, table, lengths, starts, rotary, q, out)
+    dt, code = k.dtype, _dtype_code(k.dtype)
+    ld_k, hd_k = _vectors(k, cache.kv_heads, cache.dim, dt, "k", device)
+    ld_v, hd_v = _vectors(v, cache.kv_heads, cache.dim, dt, "v", device)
+    tokens = k.shape[0]
+    _same_tokens(tokens, v=v)
+    if cache.device != device or (rotary is not None and rotary.device != device):
+        raise ValueError(f"the cache and the rotary table must be on cuda:{device}")
+    batch = _batch(table, lengths, starts, tokens, device)
+    heads = ld_q = hd_q = ld_o = hd_o = 0
+    if q is not None:
+        if rotary is None:
+            raise ValueError("q takes a rotary table")
+        heads = q.shape[1] if q.dim() == 3 else None
+        ld_q, hd_q = _vectors(q, heads, cache.dim, dt, "q", device)
+        if heads % cache.kv_heads:
+            raise ValueError(f"q must have a multiple of {cache.kv_heads} heads, not {heads}")
+        if out is None:
+            out = torch.empty((tokens, heads, cache.dim), dtype=dt, device=q.device)
+            ld_o, hd_o = heads * cache.dim, cache.dim
+        else:
+            ld_o, hd_o = _vectors(out, heads, cache.dim, dt, "out", device)
+        _same_tokens(tokens, q=q, out=out)
+    elif out is not None:
+        raise ValueError("out is for the rotated queries")
+    rc = (_lib or lib()).qz_cache_append(cache.desc, batch, code, k.data_ptr(), ld_k, hd_k, v.data_ptr(), ld_v, hd_v, tokens,
+                                         None if rotary is None else rotary.desc, _ptr(q), ld_q, hd_q, heads, _ptr(out),
+                                         ld_o, hd_o, torch._C._cuda_getCurrentRawStream(device))
+    if rc:
+        raise QzError(rc, "qz_cache_append")
+    return out
+
+
+def cache_attention(q, cache: KVCache, table, lengths, starts=None, scale: float | None = None,
+                    window: int | None = None, lse: bool = False, out=None, workspace=None, stream=None):
+    """Attention of the new tokens' queries, bf16 [tokens, heads, dim], to the cache that holds their
+    sequences, their own keys and values included (qz_cache_attention); causal, over the last
+    ``window`` positions only where that is given.  Returns out [tokens, heads, dim], or (out, lse
+    [tokens, heads]) with ``lse``; out: the one or the two.  scale: 1 / sqrt(dim) by default.
+    table, lengths, starts as for cache_append.  workspace: a uint8 CUDA tensor of
+    qz_cache_attention_workspace bytes."""
+    torch, device = _torch(), q.get_device()
+    if stream is not None or (device >= 0 and device != torch._C._cuda_getDevice()):
+        with _on(stream, q):
+            return cache_attention(q, cache, table, lengths, starts, scale, window, lse, out, workspace)
+    bf, dim = torch.bfloat16, cache.dim
+    ld_q, hd_q = _vectors(q, None, dim, bf, "q", device)
+    tokens, heads = q.shape[:2]
+    if heads % cache.kv_heads:
+        raise ValueError(f"q must have a multiple of {cache.kv_heads} heads, not {heads}")
+    if cache.device != device:
+        raise ValueError(f"the cache must be on cuda:{device}")
+    if window is not None and window < 1:
+        raise ValueError("window must be one position or more")
+    batch = _batch(table, lengths, starts, tokens, device)
+    logs, ld_lse = None, heads
+    if out is None:
+        y, ld_o, hd_o = torch.empty((tokens, heads, dim), dtype=bf, device=q.device), heads * dim, dim
+        if lse:
+            logs = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
+    else:
+        y, logs = out if lse else (out, None)
+        ld_o, hd_o = _vectors(y, heads, dim, bf, "out", device)
+        _same_tokens(tokens, out=y)
+        if lse:
+            ld_lse = _matrix(logs, heads, torch.float32, "lse", device)
+            _same_tokens(tokens, lse=logs)
+    L = _lib or lib()
+    need = L.qz_cache_attention_workspace(cache.desc, batch.sequences, tokens, heads)
+    if workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous on cuda:{device}")
+    rc = L.qz_cache_attention(cache.desc, batch, q.data_ptr(), ld_q, hd_q, tokens, heads,
+                              dim ** -0.5 if scale is None else scale, window or 0, y.data_ptr(), ld_o, hd_o, _ptr(logs), ld_lse,
+                              _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0,
+                              torch._C._cuda_getCurrentRawStream(device))
+    if rc:
+        raise QzError(rc, "qz_cache_attention")
+    return (y, logs) if lse else y
