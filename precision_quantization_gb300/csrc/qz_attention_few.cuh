@@ -1,0 +1,661 @@
+// qz_attention_few.cuh -- attention of a few rows to the 8-bit cache (decoding), included once per format.
+//
+//   x_j = (scale log2 e) ks_j (q . k_j),  m = max x_j,  p_j = 2^(x_j - m),  l = sum p_j,
+//   out = sum p_j vs_j v_j / l        (k_j, v_j the codes, ks_j, vs_j their block's scales)
+//
+// Bound by HBM: every code is read once and meets up to 32 rows.  So the codes stream and everything else
+// has to fit beside them.  A warp takes steps of 16 tokens.  Each lane copies (cp.async) exactly the
+// bytes that it will feed to the tensor cores itself, a ring of kStages steps ahead, so no lane waits for
+// another: the summation index of q . k and the columns of p v are free to be permuted, and with lane
+// (g, c) = (lane / 4, lane % 4)
+//   keys    row g and g + 8 of the step, bytes 64 h + 16 c .. + 15: four 16-wide products' B operand,
+//   values  rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9, bytes w g .. w g + w - 1 (w = dim / 8): the B operand of
+//           w products, one output column a byte,
+// are whole 16-byte pieces.  8-bit codes are exact in f16, q is made f16 by a power of two of its row.
+// The weights p vs are made f16 times 2^15 / unit, unit a power of two >= every vs so far, so that a scale
+// far below the largest keeps its 11 bits (down to 2^-29 of it).
+//
+// The work is cut in equal shares of steps over a persistent grid, whatever the lengths are (they lie on
+// the GPU): item after item (sequence, kv head, row tile), a CTA's share begins and ends anywhere.  A share
+// that holds part of an item leaves its sums in the workspace, and the CTAs of the second kernel join them.
+#pragma once
+
+#include "qz_attention.h"
+#include "qz_device.cuh"
+#include "qz_internal.h"
+#include "qz_pipe.cuh"
+#include "qz_weight.cuh"
+
+namespace qz {
+namespace {
+
+constexpr float kNone = -__builtin_inff();
+
+// ---- one 8-bit pair to f16 ----------------------------------------------------------------------
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// INT8 words have their sign bits flipped first (bias 128): 0x6400 | n is 1024 + n.
+template <int FMT>
+__device__ __forceinline__ uint32_t prepare_word(uint32_t w) {
+  return FMT == QZ_INT8 ? w ^ 0x80808080u : w;
+}
+// bytes 2 i and 2 i + 1 of a prepared word
+template <int FMT, int I>
+__device__ __forceinline__ uint32_t pair_in_word(uint32_t w) {
+  if constexpr (FMT == QZ_INT8) return sub_f16x2(prmt(w, 0x64646464u, I ? 0x4342u : 0x4140u), 0x64806480u);
+  else if constexpr (FMT == QZ_FP8_E5M2) return prmt(w, 0u, I ? 0x3424u : 0x1404u);
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(I ? w >> 16 : w)));
+  return h;
+}
+// byte J of two prepared words
+template <int FMT, int J>
+__device__ __forceinline__ uint32_t pair_of_words(uint32_t a, uint32_t b) {
+  if constexpr (FMT == QZ_INT8) {
+    const uint32_t t = prmt(a, b, J | ((4 + J) << 8) | (J << 4) | ((4 + J) << 12));  // (a, a, b, b)
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(t), "r"(0x00FF00FFu), "r"(0x64006400u));  // (t & m) | c
+    return sub_f16x2(d, 0x64806480u);
+  } else if constexpr (FMT == QZ_FP8_E5M2) {
+    return prmt(a, b, J | (J << 4) | ((4 + J) << 8) | ((4 + J) << 12)) & 0xFF00FF00u;
+  }
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(prmt(a, b, J | ((4 + J) << 4)))));
+  return h;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// copies of `bytes` (16 or 8); n = 0: zeros instead, nothing is read
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, uint32_t n) {
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else if constexpr (BYTES == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void lds16(uint32_t (&w)[4], uint32_t addr) {
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t pair_of_words_at(uint32_t a, uint32_t b, int j) {
+  return j == 0 ? pair_of_words<FMT, 0>(a, b) : j == 1 ? pair_of_words<FMT, 1>(a, b) : j == 2 ? pair_of_words<FMT, 2>(a, b) : pair_of_words<FMT, 3>(a, b);
+}
+
+// 4 elements of q at element offset `at` (zeros where !in)
+__device__ __forceinline__ void load_q4(const AttentionArgs& a, bool in, int64_t at, float (&x)[4]) {
+  x[0] = x[1] = x[2] = x[3] = 0.0f;
+  if (!in) return;
+  if (a.q_vec) {
+    const uint2 b = __ldg(reinterpret_cast<const uint2*>(a.q + at));
+    x[0] = __uint_as_float(b.x << 16), x[1] = __uint_as_float(b.x & 0xffff0000u);
+    x[2] = __uint_as_float(b.y << 16), x[3] = __uint_as_float(b.y & 0xffff0000u);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = bf16_float(__ldg(a.q + at + e));
+  }
+}
+// The power of two that brings a row whose largest magnitude is `top` into [2^14, 2^15), and its inverse;
+// elements 2^-38 of the largest and less lose bits, 2^-40 of it at most.  NaN for a row that is not finite.
+__device__ __forceinline__ float q_unit(float top, float& down) {
+  const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
+  down = __uint_as_float(static_cast<uint32_t>(127 - 14 + min(e, 127)) << 23);
+  return is_finite_f(top) ? __uint_as_float(static_cast<uint32_t>(127 + 14 - min(e, 127)) << 23) : __uint_as_float(0x7fc00000u);
+}
+// 4 finished sums of a row, elements d .. d + 3: l and the sums relative to 2^top
+__device__ __forceinline__ void store_row(const AttentionArgs& a, int64_t token, int head, int d, const float (&v)[4], float top, float l) {
+  if (a.lse && d == 0) a.lse[token * a.ld_lse + head] = l == 0.0f ? kNone : (top + log2f(l)) * 0.69314718055994531f;
+  if (d >= a.c.dim) return;
+  const float r = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+  uint16_t* p = a.out + token * a.ld_out + head * a.hd_out + d;
+  const uint32_t lo = bf16x2_bits(v[0] * r, v[1] * r), hi = bf16x2_bits(v[2] * r, v[3] * r);
+  if (a.out_vec) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+  } else {
+    p[0] = static_cast<uint16_t>(lo), p[1] = static_cast<uint16_t>(lo >> 16);
+    p[2] = static_cast<uint16_t>(hi), p[3] = static_cast<uint16_t>(hi >> 16);
+  }
+}
+
+// ---- sizes --------------------------------------------------------------------------------------
+template <int DP, int MT>
+struct FewSizes {
+  static constexpr int kRows = 16 * MT;
+  static constexpr uint32_t kStage = 2 * kTile * DP;                // bytes: keys, then values
+  static constexpr int kStages = DP == 64 ? 8 : DP == 128 ? 4 : 3;
+  static constexpr uint32_t kRing = kFewAttWarps * kStages * kStage;
+  static constexpr uint32_t kQ = MT * (DP / 16) * 512;              // q as A operands
+  static constexpr int kJoinCols = 32;                              // columns joined at a time
+  static constexpr uint32_t kJoin = kFewAttWarps * kRows * kJoinCols * 4;
+  static constexpr uint32_t kSmem = kRing + kQ + kJoin;
+  static constexpr int kSlot = kRows * (DP + 2);                    // floats of a partial result: sums, m, l
+};
+struct FewMeta {     // an item that begins in a CTA's share and does not end there
+  int32_t seq, head, row0, last;   // last: the CTA whose share holds its end; seq < 0: none
+};
+
+// ---- the work -----------------------------------------------------------------------------------
+struct SeqWork {
+  Span sp;
+  int32_t tiles;       // row tiles
+  int32_t step0, steps;  // the steps that any of its rows may see (whole items: 1 unit an item)
+};
+__device__ __forceinline__ SeqWork seq_work(const AttentionArgs& a, int32_t s, int rows) {
+  SeqWork w;
+  w.sp = span_of(a.b, s, a.c.page);
+  w.tiles = static_cast<int32_t>((static_cast<int64_t>(w.sp.n) * a.group + rows - 1) / rows);
+  const int64_t lo = w.sp.p0 + 1 - a.window;
+  w.step0 = lo > 0 ? static_cast<int32_t>(lo / kTile) : 0;
+  w.steps = max((w.sp.len + kTile - 1) / kTile - w.step0, 1);
+  return w;
+}
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(kFull, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+template <int FMT, int DP, int MT, bool WHOLE>
+__global__ void __launch_bounds__(kFewAttThreads, 1) attention_few_kernel(const AttentionArgs a, int grid, int min_chunk) {
+  using Z = FewSizes<DP, MT>;
+  constexpr int kRows = Z::kRows, kStages = Z::kStages, kSteps16 = DP / 16, kCols = DP / 8;
+  constexpr int kPieces = DP == 256 ? 2 : 1;    // 16-byte pieces of a lane's columns; 4-element ones of its part of a row of q
+  constexpr int kVBytes = DP == 64 ? 8 : 16;
+  constexpr bool kHeld = MT * DP <= 128;        // q in registers, else read from shared memory for each step
+  extern __shared__ __align__(128) uint8_t few_smem[];
+  __shared__ int64_t s_scan[kFewAttWarps + 1], s_found[2];
+  __shared__ float s_fq[kRows], s_m[kFewAttWarps][kRows], s_l[kFewAttWarps][kRows], s_unit[kFewAttWarps];
+  __shared__ int32_t s_end[kRows], s_begin[kRows];
+  __shared__ __align__(16) float s_scale[kFewAttWarps][kStages][4];  // ks, vs, whether the step has a page
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const uint32_t ring = smem_addr(few_smem) + warp * (kStages * Z::kStage);
+  const uint32_t q_smem = smem_addr(few_smem) + Z::kRing;
+  float* join = reinterpret_cast<float*>(few_smem + Z::kRing + Z::kQ);
+
+  // ---- this CTA's share: units [u0, u1) of the sequences' work one after the other ---------------
+  const auto units_of = [&](int32_t s) -> int64_t {
+    if (s >= a.b.seqs) return 0;
+    const SeqWork w = seq_work(a, s, kRows);
+    return static_cast<int64_t>(w.tiles) * a.c.heads * (WHOLE ? 1 : w.steps);
+  };
+  int64_t u0, u1, chunk = 1, before = 0;
+  int32_t seq = 0;
+  {
+    if (!WHOLE) {
+      int64_t mine = 0;
+      for (int32_t s = tid; s < a.b.seqs; s += kFewAttThreads) mine += units_of(s);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(kFull, mine, o);
+      if (lane == 0) s_scan[warp] = mine;
+      __syncthreads();
+      int64_t total = 0;
+#pragma unroll
+      for (int w = 0; w < kFewAttWarps; ++w) total += s_scan[w];
+      __syncthreads();
+      chunk = max((total + grid - 1) / grid, static_cast<int64_t>(min_chunk));
+      u0 = blockIdx.x * chunk;
+      u1 = min(u0 + chunk, total);
+    } else {
+      u0 = blockIdx.x;
+      u1 = u0 + 1;
+    }
+    if (u0 >= u1) {
+      if (!WHOLE && tid == 0) static_cast<FewMeta*>(a.ws)[blockIdx.x].seq = -1;
+      return;
+    }
+    // the sequence that holds unit u0
+    if (tid == 0) s_found[0] = -1;
+    bool found = false;
+    for (int32_t s0 = 0; s0 < a.b.seqs && !found; s0 += kFewAttThreads) {
+      const int64_t mine = units_of(s0 + tid), in_warp = warp_scan(mine, lane);
+      if (lane == 31) s_scan[warp] = in_warp;
+      __syncthreads();
+      int64_t at = before + in_warp, all = before;
+#pragma unroll
+      for (int w = 0; w < kFewAttWarps; ++w) {
+        if (w < warp) at += s_scan[w];
+        all += s_scan[w];
+      }
+      if (u0 < at && u0 >= at - mine) {
+        s_found[0] = s0 + tid;
+        s_found[1] = at - mine;
+      }
+      found = u0 < all;
+      before = all;
+      __syncthreads();
+    }
+    if (!found) return;  // (whole items: the grid covers the most that there can be)
+    seq = static_cast<int32_t>(s_found[0]);
+    before = s_found[1];
+  }
+  if (!WHOLE && tid == 0) static_cast<FewMeta*>(a.ws)[blockIdx.x].seq = -1;
+  float* slots = reinterpret_cast<float*>(static_cast<char*>(a.ws) + static_cast<size_t>(grid) * sizeof(FewMeta));
+
+  int64_t u = u0;
+  SeqWork w = seq_work(a, seq, kRows);
+  while (u < u1) {
+    while (u >= before + static_cast<int64_t>(w.tiles) * a.c.heads * (WHOLE ? 1 : w.steps)) {
+      before += static_cast<int64_t>(w.tiles) * a.c.heads * (WHOLE ? 1 : w.steps);
+      if (++seq >= a.b.seqs) return;  // (not reached while the lengths stay as they are)
+      w = seq_work(a, seq, kRows);
+    }
+    // ---- the item and the part of it in this share --------------------------------------------
+    const int64_t in_seq = u - before;
+    const int64_t item = WHOLE ? in_seq : in_seq / w.steps;
+    const int32_t t0 = WHOLE ? 0 : static_cast<int32_t>(in_seq - item * w.steps);
+    const int32_t t1 = WHOLE ? w.steps : static_cast<int32_t>(min(static_cast<int64_t>(w.steps), t0 + (u1 - u)));
+    const int kvh = static_cast<int>(item / w.tiles), row0 = static_cast<int>(item % w.tiles) * kRows;
+    const bool first = t0 == 0, last = t1 == w.steps;
+    const int64_t item_u0 = u - t0;
+    u += WHOLE ? 1 : t1 - t0;
+
+    // ---- q as f16 A operands, row by row; what each row sees ------------------------------------
+    __syncthreads();  // the previous item's q and row data have been used
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(w.sp.n) * a.group - row0));
+    for (int r = warp; r < kRows; r += kFewAttWarps) {
+      const int i = (row0 + r) / a.group, head = kvh * a.group + (row0 + r) % a.group;
+      float x[kPieces][4];
+      float top = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const int d = 4 * (lane + 32 * k);
+        load_q4(a, r < rows && d < a.c.dim, (w.sp.row + i) * a.ld_q + head * a.hd_q + d, x[k]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = absmax_nan(top, x[k][e]);
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = absmax_nan(top, __shfl_xor_sync(kFull, top, o));
+      float down;
+      const float up = q_unit(top, down);
+      if (lane == 0) {
+        const int64_t pos = w.sp.p0 + i;
+        s_fq[r] = down * a.scale;
+        s_end[r] = r < rows ? static_cast<int32_t>(max(min(pos + 1, static_cast<int64_t>(w.sp.len)), static_cast<int64_t>(0))) : 0;
+        s_begin[r] = static_cast<int32_t>(max(pos + 1 - a.window, static_cast<int64_t>(0)));
+      }
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const int d = 4 * (lane + 32 * k);
+        if (d < DP) {
+          const uint32_t at = q_smem + (((r >> 4) * kSteps16 + d / 16 / 4 * 4 + (d >> 2) % 4) * 32 + (r & 7) * 4 + (d >> 4) % 4) * 16 + ((r >> 3) & 1) * 4;
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(f16x2_bits(x[k][0] * up, x[k][1] * up)) : "memory");
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 8), "r"(f16x2_bits(x[k][2] * up, x[k][3] * up)) : "memory");
+        }
+      }
+    }
+    __syncthreads();
+    uint32_t qf[kHeld ? MT * kSteps16 : 1][4];
+    if constexpr (kHeld) {
+#pragma unroll
+      for (int k = 0; k < MT * kSteps16; ++k) lds16(qf[k], q_smem + (k * 32 + lane) * 16);
+    }
+    float fq[MT][2];
+    int32_t end[MT][2], begin[MT][2];
+    int32_t all_end = INT32_MAX, all_begin = 0;  // what every row sees
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 16 * m + 8 * e + g;
+        fq[m][e] = s_fq[r];
+        end[m][e] = s_end[r];
+        begin[m][e] = s_begin[r];
+      }
+    all_end = s_end[0];             // rows' positions do not decrease
+    all_begin = s_begin[rows - 1];
+
+    // ---- the steps of this warp -----------------------------------------------------------------
+    const int32_t len = w.sp.len;
+    const auto entry = [&](int32_t t) -> int32_t {  // the page of step t, -1 where there is none
+      const int64_t p = static_cast<int64_t>(w.step0 + t) * kTile;
+      return t < t1 && p < len ? __ldg(a.b.table + seq * a.b.ld_table + static_cast<int32_t>(p) / a.c.page) : -1;
+    };
+    const auto copy = [&](int32_t t, int stage, int32_t page) {
+      const int32_t p = (w.step0 + t) * kTile;
+      const bool has = page >= 0 && page < a.c.pages;
+      const int in_page = has ? p % a.c.page : 0;
+      const int64_t head = static_cast<int64_t>(has ? page : 0) * a.c.heads + kvh;
+      const int64_t base = (head * a.c.page + in_page) * a.c.dim;
+      const uint32_t to = ring + stage * Z::kStage;
+#pragma unroll
+      for (int h = 0; h < DP / 64; ++h)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = g + 8 * e, d = 64 * h + 16 * c;
+          const bool in = has && p + r < len && d < a.c.dim;
+          copy_async<16>(to + ((2 * h + e) * 32 + lane) * 16, a.c.k + (in ? base + r * a.c.dim + d : 0), in ? 16u : 0u);
+        }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int h = 0; h < kPieces; ++h) {
+          const int r = 2 * c + (i & 1) + 8 * (i >> 1), d = kCols * g + 16 * h;
+          const bool in = has && p + r < len && d < a.c.dim;
+          copy_async<kVBytes>(to + kTile * DP + ((i * kPieces + h) * 32 + lane) * kVBytes, a.c.v + (in ? base + r * a.c.dim + d : 0),
+                              in ? static_cast<uint32_t>(kVBytes) : 0u);
+        }
+      if (lane < 2) {
+        const int64_t block = head * (a.c.page >> a.c.log2_block) + (in_page >> a.c.log2_block);
+        copy_async<4>(smem_addr(&s_scale[warp][stage][lane]), (lane ? a.c.vs : a.c.ks) + block, has ? 4u : 0u);
+      } else if (lane == 2) {
+        s_scale[warp][stage][2] = has ? 1.0f : 0.0f;
+      }
+    };
+
+    float o[MT][kCols][4], mx[MT][2], sum[MT][2];
+    float unit = 0x1p-100f;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      mx[m][0] = mx[m][1] = kNone;
+      sum[m][0] = sum[m][1] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kCols; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[m][j][e] = 0.0f;
+    }
+    const int32_t tw = t0 + warp;
+    int32_t pages[kStages];
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) pages[i] = entry(tw + i * kFewAttWarps);
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+      if (tw + i * kFewAttWarps < t1) copy(tw + i * kFewAttWarps, i, pages[i]);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    int32_t page_next = pages[kStages - 1];
+    int stage = 0;
+    for (int32_t t = tw; t < t1; t += kFewAttWarps) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+      __syncwarp();  // the scales are other lanes' copies; every lane has done with the step before
+      {
+        const int32_t ahead = t + (kStages - 1) * kFewAttWarps;
+        if (ahead < t1) copy(ahead, stage == 0 ? kStages - 1 : stage - 1, page_next);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        page_next = entry(ahead + kFewAttWarps);
+      }
+      const uint32_t from = ring + stage * Z::kStage;
+      const float ks = s_scale[warp][stage][0], vs = s_scale[warp][stage][1];
+      const bool has = s_scale[warp][stage][2] != 0.0f;
+      const int32_t p = (w.step0 + t) * kTile;
+      if (++stage == kStages) stage = 0;
+      if (!has) continue;
+
+      float x[MT][2][4] = {};
+#pragma unroll
+      for (int h = 0; h < DP / 64; ++h) {
+        uint32_t k0[4], k1[4];
+        lds16(k0, from + ((2 * h) * 32 + lane) * 16);
+        lds16(k1, from + ((2 * h + 1) * 32 + lane) * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w0 = prepare_word<FMT>(k0[i]), w1 = prepare_word<FMT>(k1[i]);
+          const uint32_t b00 = pair_in_word<FMT, 0>(w0), b01 = pair_in_word<FMT, 1>(w0);
+          const uint32_t b10 = pair_in_word<FMT, 0>(w1), b11 = pair_in_word<FMT, 1>(w1);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            uint32_t qa[4];
+            if constexpr (!kHeld) lds16(qa, q_smem + ((m * kSteps16 + 4 * h + i) * 32 + lane) * 16);
+            const uint32_t(&qq)[4] = kHeld ? qf[kHeld ? m * kSteps16 + 4 * h + i : 0] : qa;
+            mma16816(x[m][0], qq, b00, b01);
+            mma16816(x[m][1], qq, b10, b11);
+          }
+        }
+      }
+      const bool whole = p + kTile <= all_end && p >= all_begin;
+      bool moved = false;
+      float was[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {  // row 16 m + 8 e + g, tokens 8 n + 2 c + i
+          const float f = fq[m][e] * ks;
+          float top = kNone;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float& v = x[m][n][2 * e + i];
+              v *= f;
+              const int32_t j = p + 8 * n + 2 * c + i;
+              if (!whole && (j >= end[m][e] || j < begin[m][e])) v = kNone;
+              top = fmaxf(top, v);
+            }
+          top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+          was[m][e] = mx[m][e];
+          if (top > mx[m][e]) {
+            mx[m][e] = top;
+            moved = true;
+          }
+        }
+      const float vmag = fabsf(vs), unit_was = unit;
+      if (vmag > unit && is_finite_f(vmag)) {  // the next power of two (vs is a power of two itself: twice that)
+        unit = __uint_as_float((__float_as_uint(fminf(vmag, 0x1p125f)) & 0x7f800000u) + 0x00800000u);
+        moved = true;
+      }
+      if (__any_sync(kFull, moved)) {
+        const float shrink = unit_was / unit;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float f = mx[m][e] == kNone ? 1.0f : ex2(was[m][e] - mx[m][e]), fo = f * shrink;
+            sum[m][e] *= f;
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) {
+              o[m][j][2 * e] *= fo;
+              o[m][j][2 * e + 1] *= fo;
+            }
+          }
+      }
+      const float fv = vs * (0x1p15f / unit);
+      uint32_t pa[MT][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float top = mx[m][e] == kNone ? 0.0f : mx[m][e];
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            float y[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float v = x[m][n][2 * e + i], q = ex2(v - top);
+              sum[m][e] += q;
+              y[i] = v == kNone ? 0.0f : q * fv;  // (the scale of what is not seen may be anything)
+            }
+            pa[m][2 * n + e] = f16x2_bits(y[0], y[1]);
+          }
+        }
+#pragma unroll
+      for (int h = 0; h < kPieces; ++h) {
+        constexpr int kWords = kVBytes / 4;
+        uint32_t vw[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t at = from + kTile * DP + ((i * kPieces + h) * 32 + lane) * kVBytes;
+          if constexpr (kVBytes == 16) lds16(vw[i], at);
+          else asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(vw[i][0]), "=r"(vw[i][1]) : "r"(at));
+        }
+#pragma unroll
+        for (int q = 0; q < kWords; ++q) {
+          uint32_t y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = prepare_word<FMT>(vw[i][q]);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const uint32_t b0 = pair_of_words_at<FMT>(y[0], y[1], b), b1 = pair_of_words_at<FMT>(y[2], y[3], b);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) mma16816(o[m][16 * h + 4 * q + b], pa[m], b0, b1);
+          }
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+
+    // ---- the warps' sums, four columns of each of the eight column groups at a time ----------------
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sum[m][e] += __shfl_xor_sync(kFull, sum[m][e], 1);
+        sum[m][e] += __shfl_xor_sync(kFull, sum[m][e], 2);
+        if (c == 0) {
+          s_m[warp][16 * m + 8 * e + g] = mx[m][e];
+          s_l[warp][16 * m + 8 * e + g] = sum[m][e];
+        }
+      }
+    if (lane == 0) s_unit[warp] = unit;
+    const bool whole_item = first && last;
+    float* slot = WHOLE || whole_item ? nullptr : slots + (2 * static_cast<size_t>(blockIdx.x) + (first ? 1 : 0)) * Z::kSlot;
+#pragma unroll
+    for (int q = 0; q < kCols / 4; ++q) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 16 * m + 8 * (e >> 1) + g, n = 2 * c + (e & 1);
+          *reinterpret_cast<float4*>(join + ((warp * kRows + r) * 8 + n) * 4) =
+              make_float4(o[m][4 * q][e], o[m][4 * q + 1][e], o[m][4 * q + 2][e], o[m][4 * q + 3][e]);
+        }
+      __syncthreads();
+      for (int i = tid; i < kRows * 8; i += kFewAttThreads) {
+        const int r = i >> 3, d = kCols * (i & 7) + 4 * q;
+        if (r >= rows) break;
+        float top = kNone, l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kFewAttWarps; ++k) top = fmaxf(top, s_m[k][r]);
+        const float from = top == kNone ? 0.0f : top;
+        float v[4] = {};
+#pragma unroll
+        for (int k = 0; k < kFewAttWarps; ++k) {
+          const float f = ex2(s_m[k][r] - from), fo = f * s_unit[k] * 0x1p-15f;
+          const float4 y = *reinterpret_cast<const float4*>(join + ((k * kRows + r) * 8 + (i & 7)) * 4);
+          l = __fmaf_rn(s_l[k][r], f, l);
+          v[0] = __fmaf_rn(y.x, fo, v[0]), v[1] = __fmaf_rn(y.y, fo, v[1]);
+          v[2] = __fmaf_rn(y.z, fo, v[2]), v[3] = __fmaf_rn(y.w, fo, v[3]);
+        }
+        if (slot) {
+          *reinterpret_cast<float4*>(slot + r * DP + d) = make_float4(v[0], v[1], v[2], v[3]);
+          if (q == 0 && (i & 7) == 0) {
+            slot[kRows * DP + r] = top;
+            slot[kRows * (DP + 1) + r] = l;
+          }
+        } else {
+          store_row(a, w.sp.row + (row0 + r) / a.group, kvh * a.group + (row0 + r) % a.group, d, v, top, l);
+        }
+      }
+      __syncthreads();
+    }
+    if (!WHOLE && first && !last && tid == 0) {
+      FewMeta meta;
+      meta.seq = seq;
+      meta.head = kvh;
+      meta.row0 = row0;
+      meta.last = static_cast<int32_t>((item_u0 + w.steps - 1) / chunk);
+      static_cast<FewMeta*>(a.ws)[blockIdx.x] = meta;
+    }
+  }
+}
+
+// Joins the partial results of the items that more than one share holds: CTA (i, y) the y-th part of the
+// rows of the item that begins in share i.
+template <int DP, int MT>
+__global__ void __launch_bounds__(128) attention_join_kernel(const AttentionArgs a, int grid) {
+  using Z = FewSizes<DP, MT>;
+  constexpr int kRows = Z::kRows;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const FewMeta meta = static_cast<const FewMeta*>(a.ws)[blockIdx.x];
+  if (meta.seq < 0) return;
+  const float* slots = reinterpret_cast<const float*>(static_cast<const char*>(a.ws) + static_cast<size_t>(grid) * sizeof(FewMeta));
+  const Span sp = span_of(a.b, meta.seq, a.c.page);
+  const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(sp.n) * a.group - meta.row0));
+  const int parts = meta.last - static_cast<int>(blockIdx.x) + 1;
+  const auto part = [&](int k) { return slots + (2 * (static_cast<size_t>(blockIdx.x) + k) + (k == 0 ? 1 : 0)) * Z::kSlot; };
+  for (int i = static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x); i < rows * (DP / 4); i += static_cast<int>(gridDim.y * blockDim.x)) {
+    const int r = i / (DP / 4), d = 4 * (i % (DP / 4));
+    if (d >= a.c.dim) continue;
+    float top = kNone;
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) top = fmaxf(top, part(k)[kRows * DP + r]);
+    const float from = top == kNone ? 0.0f : top;
+    float v[4] = {}, l = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const float* p = part(k);
+      const float f = ex2(p[kRows * DP + r] - from);
+      const float4 y = *reinterpret_cast<const float4*>(p + r * DP + d);
+      l = __fmaf_rn(p[kRows * (DP + 1) + r], f, l);
+      v[0] = __fmaf_rn(y.x, f, v[0]), v[1] = __fmaf_rn(y.y, f, v[1]);
+      v[2] = __fmaf_rn(y.z, f, v[2]), v[3] = __fmaf_rn(y.w, f, v[3]);
+    }
+    store_row(a, sp.row + (meta.row0 + r) / a.group, meta.head * a.group + (meta.row0 + r) % a.group, d, v, top, l);
+  }
+}
+
+// ---- host side ----------------------------------------------------------------------------------
+template <int FMT, int DP, int MT>
+qz_status run_few(const AttentionArgs& a, const FewPlan& p, cudaStream_t s) {
+  using Z = FewSizes<DP, MT>;
+  if (p.whole) {
+    const auto k = &attention_few_kernel<FMT, DP, MT, true>;
+    if (!set_dyn_smem(reinterpret_cast<const void*>(k), Z::kSmem)) return QZ_ERR_CUDA;
+    k<<<static_cast<unsigned>(p.grid), kFewAttThreads, Z::kSmem, s>>>(a, p.grid, p.min_chunk);
+    return launch_status();
+  }
+  const auto k = &attention_few_kernel<FMT, DP, MT, false>;
+  if (!set_dyn_smem(reinterpret_cast<const void*>(k), Z::kSmem)) return QZ_ERR_CUDA;
+  k<<<static_cast<unsigned>(p.grid), kFewAttThreads, Z::kSmem, s>>>(a, p.grid, p.min_chunk);
+  if (launch_status() != QZ_OK) return QZ_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(p.grid), 4);
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attention_join_kernel<DP, MT>, a, p.grid) != cudaSuccess) {
+    cudaGetLastError();
+    return QZ_ERR_CUDA;
+  }
+  return launch_status();
+}
+template <int FMT>
+qz_status launch_few(const AttentionArgs& a, const FewPlan& p, cudaStream_t s) {
+  switch (few_att_dim(a.c.dim)) {
+    case 64: return p.row_tiles == 2 ? run_few<FMT, 64, 2>(a, p, s) : run_few<FMT, 64, 1>(a, p, s);
+    case 128: return p.row_tiles == 2 ? run_few<FMT, 128, 2>(a, p, s) : run_few<FMT, 128, 1>(a, p, s);
+    default: return run_few<FMT, 256, 1>(a, p, s);
+  }
+}
+
+}  // namespace
+}  // namespace qz

@@ -235,6 +235,12 @@ ATTEND = [  # lengths, new tokens, page, block, heads, kv, dim, window
     ([400], [260], 128, 64, 2, 2, 112, 300),
     ([290, 300], [70, 45], 128, 128, 16, 1, 128, 0),
     ([140], [77], 16, 16, 6, 2, 240, 60),
+    # too long for one CTA: cut and joined
+    ([3000, 17, 1111, 0], [1, 1, 1, 1], 64, 32, 16, 2, 128, 0),
+    ([2500, 0, 1800], [3, 0, 2], 32, 16, 12, 2, 64, 700),
+    ([5000], [1], 128, 64, 4, 1, 256, 0),
+    ([1300, 2100], [9, 4], 16, 16, 8, 2, 128, 0),
+    ([1100, 40], [150, 40], 32, 32, 4, 2, 96, 0),
 ]
 
 
