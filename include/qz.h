@@ -542,7 +542,7 @@ QZ_API qz_status qz_rotary_backward(const qz_rotary_table* table, int32_t dtype,
 /* A cache: pages of `page` tokens, each holding the keys and the values of every kv head.
  *   format            QZ_INT8, QZ_FP8_E4M3 or QZ_FP8_E5M2
  *   block             tokens that share a scale: 16, 32, 64 or 128
- *   page              tokens of a page: a multiple of block, up to 1024
+ *   page              tokens of a page: a multiple of block, up to 1024 (pages * kv_heads below 2^31)
  *   dim               elements of a vector: a multiple of 16, up to 256
  *   k_codes, v_codes  device, [pages, kv_heads, page, dim] bytes, 16-byte aligned
  *   k_scales, v_scales  device fp32 [pages, kv_heads, page / block]

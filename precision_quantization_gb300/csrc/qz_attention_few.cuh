@@ -4,21 +4,23 @@
 //   out = sum p_j vs_j v_j / l        (k_j, v_j the codes, ks_j, vs_j their block's scales)
 //
 // Bound by HBM: every code is read once and meets up to 32 rows.  So the codes stream and everything else
-// has to fit beside them.  A warp takes steps of 16 tokens.  Each lane copies (cp.async) exactly the
-// bytes that it will feed to the tensor cores itself, a ring of kStages steps ahead, so no lane waits for
-// another: the summation index of q . k and the columns of p v are free to be permuted, and with lane
-// (g, c) = (lane / 4, lane % 4)
+// has to fit beside them: a warp has a ring of kStages steps of 16 tokens of its own that TMA fills, keys and
+// values each a box of 16 rows in the hardware's swizzle.  The summation index of q . k and the columns of
+// p v are free to be permuted, and with lane (g, c) = (lane / 4, lane % 4)
 //   keys    row g and g + 8 of the step, bytes 64 h + 16 c .. + 15: four 16-wide products' B operand,
 //   values  rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9, bytes w g .. w g + w - 1 (w = dim / 8): the B operand of
 //           w products, one output column a byte,
-// are whole 16-byte pieces.  8-bit codes are exact in f16, q is made f16 by a power of two of its row.
-// The weights p vs are made f16 times 2^15 / unit, unit a power of two >= every vs so far, so that a scale
-// far below the largest keeps its 11 bits (down to 2^-29 of it).
+// are whole 16-byte pieces, read from different banks.  8-bit codes are exact in f16, q is made f16 by a
+// power of two of its row.  The weights p vs are made f16 times 2^15 / unit, unit a power of two >= every vs
+// so far, so that a scale far below the largest keeps its 11 bits (down to 2^-29 of it).
 //
 // The work is cut in equal shares of steps over a persistent grid, whatever the lengths are (they lie on
 // the GPU): item after item (sequence, kv head, row tile), a CTA's share begins and ends anywhere.  A share
 // that holds part of an item leaves its sums in the workspace, and the CTAs of the second kernel join them.
 #pragma once
+
+#include <cuda.h>  // CUtensorMap and its enumerators (types only; the encoder is looked up)
+#include <cudaTypedefs.h>
 
 #include "qz_attention.h"
 #include "qz_device.cuh"
@@ -30,6 +32,11 @@ namespace qz {
 namespace {
 
 constexpr float kNone = -__builtin_inff();
+constexpr uint64_t kFewWaitNs = 1000000000ull;  // 1 s: far beyond any copy's latency
+
+struct CacheMaps {
+  CUtensorMap k, v;   // codes as [pages * kv heads][page][dim], boxes of 16 rows
+};
 
 // ---- one 8-bit pair to f16 ----------------------------------------------------------------------
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -56,13 +63,13 @@ __device__ __forceinline__ uint32_t pair_in_word(uint32_t w) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(I ? w >> 16 : w)));
   return h;
 }
-// byte J of two prepared words
+// byte J of two words
 template <int FMT, int J>
 __device__ __forceinline__ uint32_t pair_of_words(uint32_t a, uint32_t b) {
   if constexpr (FMT == QZ_INT8) {
     const uint32_t t = prmt(a, b, J | ((4 + J) << 8) | (J << 4) | ((4 + J) << 12));  // (a, a, b, b)
     uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(t), "r"(0x00FF00FFu), "r"(0x64006400u));  // (t & m) | c
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(t), "r"(0x00FF00FFu), "r"(0x64806480u));  // (t & m) ^ c
     return sub_f16x2(d, 0x64806480u);
   } else if constexpr (FMT == QZ_FP8_E5M2) {
     return prmt(a, b, J | (J << 4) | ((4 + J) << 8) | ((4 + J) << 12)) & 0xFF00FF00u;
@@ -88,12 +95,19 @@ __device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// copies of `bytes` (16 or 8); n = 0: zeros instead, nothing is read
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, uint32_t n) {
-  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else if constexpr (BYTES == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+// one 4-byte value, announced on the barrier like the lane's own arrival
+__device__ __forceinline__ void copy_scale(uint32_t dst, const float* src, uint32_t bar) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_on(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void lds16(uint32_t (&w)[4], uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
@@ -144,12 +158,12 @@ template <int DP, int MT>
 struct FewSizes {
   static constexpr int kRows = 16 * MT;
   static constexpr uint32_t kStage = 2 * kTile * DP;                // bytes: keys, then values
-  static constexpr int kStages = DP == 64 ? 8 : DP == 128 ? 4 : 3;
+  static constexpr int kStages = DP == 64 ? 8 : DP == 128 ? 5 : 3;
   static constexpr uint32_t kRing = kFewAttWarps * kStages * kStage;
   static constexpr uint32_t kQ = MT * (DP / 16) * 512;              // q as A operands
   static constexpr int kJoinCols = 32;                              // columns joined at a time
   static constexpr uint32_t kJoin = kFewAttWarps * kRows * kJoinCols * 4;
-  static constexpr uint32_t kSmem = kRing + kQ + kJoin;
+  static constexpr uint32_t kSmem = kRing + kQ + kJoin + 1024;      // (the ring starts on a 1024-byte boundary)
   static constexpr int kSlot = kRows * (DP + 2);                    // floats of a partial result: sums, m, l
 };
 struct FewMeta {     // an item that begins in a CTA's share and does not end there
@@ -180,112 +194,186 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
   return v;
 }
 
+// A segment: the part of an item that lies in this CTA's share.
+struct Segment {
+  SeqWork w;
+  int32_t seq, kvh, row0, rows;
+  int32_t t0, t1;        // its steps
+  int64_t item_u0;       // the item's first unit
+};
+
 template <int FMT, int DP, int MT, bool WHOLE>
-__global__ void __launch_bounds__(kFewAttThreads, 1) attention_few_kernel(const AttentionArgs a, int grid, int min_chunk) {
+__global__ void __launch_bounds__(kFewAttThreads, 1)
+    attention_few_kernel(const AttentionArgs a, const __grid_constant__ CacheMaps maps, int grid, int min_chunk) {
   using Z = FewSizes<DP, MT>;
   constexpr int kRows = Z::kRows, kStages = Z::kStages, kSteps16 = DP / 16, kCols = DP / 8;
   constexpr int kPieces = DP == 256 ? 2 : 1;    // 16-byte pieces of a lane's columns; 4-element ones of its part of a row of q
   constexpr int kVBytes = DP == 64 ? 8 : 16;
   constexpr bool kHeld = MT * DP <= 128;        // q in registers, else read from shared memory for each step
-  extern __shared__ __align__(128) uint8_t few_smem[];
+  constexpr uint32_t kSlab = kTile * (DP < 128 ? DP : 128);  // bytes of a box: rows of 64 or 128 bytes
+  extern __shared__ uint8_t few_raw[];
   __shared__ int64_t s_scan[kFewAttWarps + 1], s_found[2];
   __shared__ float s_fq[kRows], s_m[kFewAttWarps][kRows], s_l[kFewAttWarps][kRows], s_unit[kFewAttWarps];
   __shared__ int32_t s_end[kRows], s_begin[kRows];
   __shared__ __align__(16) float s_scale[kFewAttWarps][kStages][4];  // ks, vs, whether the step has a page
+  __shared__ __align__(8) uint64_t s_full[kFewAttWarps][kStages];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  const uint32_t ring = smem_addr(few_smem) + warp * (kStages * Z::kStage);
-  const uint32_t q_smem = smem_addr(few_smem) + Z::kRing;
-  float* join = reinterpret_cast<float*>(few_smem + Z::kRing + Z::kQ);
+  const uint32_t base = (smem_addr(few_raw) + 1023u) & ~1023u;
+  uint8_t* smem = few_raw + (base - smem_addr(few_raw));
+  const uint32_t ring = base + warp * (kStages * Z::kStage);
+  const uint32_t q_smem = base + Z::kRing;
+  float* join = reinterpret_cast<float*>(smem + Z::kRing + Z::kQ);
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(smem_addr(&s_full[warp][i]), 3);  // the codes, ks, vs
+    mbar_init_fence();
+  }
 
   // ---- this CTA's share: units [u0, u1) of the sequences' work one after the other ---------------
-  const auto units_of = [&](int32_t s) -> int64_t {
-    if (s >= a.b.seqs) return 0;
-    const SeqWork w = seq_work(a, s, kRows);
-    return static_cast<int64_t>(w.tiles) * a.c.heads * (WHOLE ? 1 : w.steps);
-  };
+  const auto work_of = [&](const SeqWork& w) { return static_cast<int64_t>(w.tiles) * a.c.heads * (WHOLE ? 1 : w.steps); };
+  const auto units_of = [&](int32_t s) { return s < a.b.seqs ? work_of(seq_work(a, s, kRows)) : 0; };
   int64_t u0, u1, chunk = 1, before = 0;
-  int32_t seq = 0;
-  {
-    if (!WHOLE) {
-      int64_t mine = 0;
-      for (int32_t s = tid; s < a.b.seqs; s += kFewAttThreads) mine += units_of(s);
+  if (!WHOLE) {
+    int64_t mine = 0;
+    for (int32_t s = tid; s < a.b.seqs; s += kFewAttThreads) mine += units_of(s);
 #pragma unroll
-      for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(kFull, mine, o);
-      if (lane == 0) s_scan[warp] = mine;
-      __syncthreads();
-      int64_t total = 0;
+    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(kFull, mine, o);
+    if (lane == 0) s_scan[warp] = mine;
+    __syncthreads();
+    int64_t total = 0;
 #pragma unroll
-      for (int w = 0; w < kFewAttWarps; ++w) total += s_scan[w];
-      __syncthreads();
-      chunk = max((total + grid - 1) / grid, static_cast<int64_t>(min_chunk));
-      u0 = blockIdx.x * chunk;
-      u1 = min(u0 + chunk, total);
-    } else {
-      u0 = blockIdx.x;
-      u1 = u0 + 1;
-    }
-    if (u0 >= u1) {
-      if (!WHOLE && tid == 0) static_cast<FewMeta*>(a.ws)[blockIdx.x].seq = -1;
-      return;
-    }
-    // the sequence that holds unit u0
-    if (tid == 0) s_found[0] = -1;
-    bool found = false;
-    for (int32_t s0 = 0; s0 < a.b.seqs && !found; s0 += kFewAttThreads) {
-      const int64_t mine = units_of(s0 + tid), in_warp = warp_scan(mine, lane);
-      if (lane == 31) s_scan[warp] = in_warp;
-      __syncthreads();
-      int64_t at = before + in_warp, all = before;
-#pragma unroll
-      for (int w = 0; w < kFewAttWarps; ++w) {
-        if (w < warp) at += s_scan[w];
-        all += s_scan[w];
-      }
-      if (u0 < at && u0 >= at - mine) {
-        s_found[0] = s0 + tid;
-        s_found[1] = at - mine;
-      }
-      found = u0 < all;
-      before = all;
-      __syncthreads();
-    }
-    if (!found) return;  // (whole items: the grid covers the most that there can be)
-    seq = static_cast<int32_t>(s_found[0]);
-    before = s_found[1];
+    for (int w = 0; w < kFewAttWarps; ++w) total += s_scan[w];
+    __syncthreads();
+    chunk = max((total + grid - 1) / grid, static_cast<int64_t>(min_chunk));
+    u0 = blockIdx.x * chunk;
+    u1 = min(u0 + chunk, total);
+    if (tid == 0) static_cast<FewMeta*>(a.ws)[blockIdx.x].seq = -1;
+  } else {
+    u0 = blockIdx.x;
+    u1 = u0 + 1;
   }
-  if (!WHOLE && tid == 0) static_cast<FewMeta*>(a.ws)[blockIdx.x].seq = -1;
+  if (u0 >= u1) return;
+  bool found = false;  // the sequence that holds unit u0
+  for (int32_t s0 = 0; s0 < a.b.seqs && !found; s0 += kFewAttThreads) {
+    const int64_t mine = units_of(s0 + tid), in_warp = warp_scan(mine, lane);
+    if (lane == 31) s_scan[warp] = in_warp;
+    __syncthreads();
+    int64_t at = before + in_warp, all = before;
+#pragma unroll
+    for (int w = 0; w < kFewAttWarps; ++w) {
+      if (w < warp) at += s_scan[w];
+      all += s_scan[w];
+    }
+    if (u0 < at && u0 >= at - mine) {
+      s_found[0] = s0 + tid;
+      s_found[1] = at - mine;
+    }
+    found = u0 < all;
+    before = all;
+    __syncthreads();
+  }
+  if (!found) return;  // (whole items: the grid covers the most that there can be)
+  before = s_found[1];
   float* slots = reinterpret_cast<float*>(static_cast<char*>(a.ws) + static_cast<size_t>(grid) * sizeof(FewMeta));
 
   int64_t u = u0;
-  SeqWork w = seq_work(a, seq, kRows);
-  while (u < u1) {
-    while (u >= before + static_cast<int64_t>(w.tiles) * a.c.heads * (WHOLE ? 1 : w.steps)) {
-      before += static_cast<int64_t>(w.tiles) * a.c.heads * (WHOLE ? 1 : w.steps);
-      if (++seq >= a.b.seqs) return;  // (not reached while the lengths stay as they are)
-      w = seq_work(a, seq, kRows);
+  Segment n;  // the next segment
+  n.seq = static_cast<int32_t>(s_found[0]);
+  n.w = seq_work(a, n.seq, kRows);
+  const auto advance = [&]() -> bool {
+    if (u >= u1) return false;
+    while (u >= before + work_of(n.w)) {
+      before += work_of(n.w);
+      if (++n.seq >= a.b.seqs) return false;  // (not reached while the lengths stay as they are)
+      n.w = seq_work(a, n.seq, kRows);
     }
-    // ---- the item and the part of it in this share --------------------------------------------
-    const int64_t in_seq = u - before;
-    const int64_t item = WHOLE ? in_seq : in_seq / w.steps;
-    const int32_t t0 = WHOLE ? 0 : static_cast<int32_t>(in_seq - item * w.steps);
-    const int32_t t1 = WHOLE ? w.steps : static_cast<int32_t>(min(static_cast<int64_t>(w.steps), t0 + (u1 - u)));
-    const int kvh = static_cast<int>(item / w.tiles), row0 = static_cast<int>(item % w.tiles) * kRows;
-    const bool first = t0 == 0, last = t1 == w.steps;
-    const int64_t item_u0 = u - t0;
-    u += WHOLE ? 1 : t1 - t0;
+    const int64_t in_seq = u - before, item = WHOLE ? in_seq : in_seq / n.w.steps;
+    n.t0 = WHOLE ? 0 : static_cast<int32_t>(in_seq - item * n.w.steps);
+    n.t1 = WHOLE ? n.w.steps : static_cast<int32_t>(min(static_cast<int64_t>(n.w.steps), n.t0 + (u1 - u)));
+    n.kvh = static_cast<int32_t>(item / n.w.tiles);
+    n.row0 = static_cast<int32_t>(item % n.w.tiles) * kRows;
+    n.rows = static_cast<int32_t>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(n.w.sp.n) * a.group - n.row0));
+    n.item_u0 = u - n.t0;
+    u += WHOLE ? 1 : n.t1 - n.t0;
+    return true;
+  };
 
+  // ---- the copies of this warp's steps, a ring ahead ---------------------------------------------
+  int32_t ct = 0, c_end = 0, c_index = 0, c_in = 0;   // the next step, the end; its page's place in the table, its first row there
+  int32_t c_page = -1, c_stage = 0;
+  const int32_t* c_row = nullptr;
+  int32_t c_len = 0, c_kvh = 0;
+  const auto entry = [&]() { return ct < c_end && static_cast<int64_t>(c_index) * a.c.page + c_in < c_len ? __ldg(c_row + c_index) : -1; };
+  const auto aim = [&](const Segment& s) {  // at a segment's steps: a run of them for each warp
+    const int32_t count = s.t1 - s.t0;
+    ct = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * warp / kFewAttWarps);
+    c_end = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * (warp + 1) / kFewAttWarps);
+    const int32_t p = (s.w.step0 + ct) * kTile;
+    c_index = p / a.c.page;
+    c_in = p - c_index * a.c.page;
+    c_row = a.b.table + s.seq * a.b.ld_table;
+    c_len = s.w.sp.len;
+    c_kvh = s.kvh;
+    c_page = entry();
+  };
+  const auto copy = [&]() {  // one step, into c_stage
+    if (ct >= c_end) return;
+    const int32_t page = c_page, in = c_in;
+    ++ct;
+    c_in += kTile;
+    if (c_in >= a.c.page) {
+      c_in = 0;
+      ++c_index;
+      c_page = entry();
+    }
+    const bool has = page >= 0 && page < a.c.pages;
+    const int32_t head = (has ? page : 0) * a.c.heads + c_kvh;
+    const uint32_t bar = smem_addr(&s_full[warp][c_stage]), to = ring + c_stage * Z::kStage;
+    if (lane < 2) {
+      if (has) {
+        const int64_t block = static_cast<int64_t>(head) * (a.c.page >> a.c.log2_block) + (in >> a.c.log2_block);
+        copy_scale(smem_addr(&s_scale[warp][c_stage][lane]), (lane ? a.c.vs : a.c.ks) + block, bar);
+      } else {
+        arrive_on(bar);
+      }
+    }
+    if (lane == 0) {
+      s_scale[warp][c_stage][2] = has ? 1.0f : 0.0f;
+      if (has) {
+        mbar_expect_tx(bar, Z::kStage);
+#pragma unroll
+        for (int h = 0; h < kPieces; ++h) {
+          box_load(to + h * kSlab, &maps.k, 128 * h, in, head, bar);
+          box_load(to + kTile * DP + h * kSlab, &maps.v, 128 * h, in, head, bar);
+        }
+      } else {
+        arrive_on(bar);
+      }
+    }
+    c_stage = c_stage + 1 == kStages ? 0 : c_stage + 1;
+  };
+  int stage = 0;
+  uint32_t phase = 0;
+  bool failed = false;   // a wait has given up: this CTA's results are NaN
+  __syncwarp();
+  bool more = advance();
+  if (more) {
+    aim(n);
+#pragma unroll 1
+    for (int i = 0; i < kStages; ++i) copy();
+  }
+
+  while (more) {
+    const Segment s = n;
     // ---- q as f16 A operands, row by row; what each row sees ------------------------------------
-    __syncthreads();  // the previous item's q and row data have been used
-    const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), static_cast<int64_t>(w.sp.n) * a.group - row0));
     for (int r = warp; r < kRows; r += kFewAttWarps) {
-      const int i = (row0 + r) / a.group, head = kvh * a.group + (row0 + r) % a.group;
+      const int i = (s.row0 + r) / a.group, head = s.kvh * a.group + (s.row0 + r) % a.group;
       float x[kPieces][4];
       float top = 0.0f;
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {
         const int d = 4 * (lane + 32 * k);
-        load_q4(a, r < rows && d < a.c.dim, (w.sp.row + i) * a.ld_q + head * a.hd_q + d, x[k]);
+        load_q4(a, r < s.rows && d < a.c.dim, (s.w.sp.row + i) * a.ld_q + head * a.hd_q + d, x[k]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = absmax_nan(top, x[k][e]);
       }
@@ -294,16 +382,16 @@ __global__ void __launch_bounds__(kFewAttThreads, 1) attention_few_kernel(const 
       float down;
       const float up = q_unit(top, down);
       if (lane == 0) {
-        const int64_t pos = w.sp.p0 + i;
+        const int64_t pos = s.w.sp.p0 + i;
         s_fq[r] = down * a.scale;
-        s_end[r] = r < rows ? static_cast<int32_t>(max(min(pos + 1, static_cast<int64_t>(w.sp.len)), static_cast<int64_t>(0))) : 0;
+        s_end[r] = r < s.rows ? static_cast<int32_t>(max(min(pos + 1, static_cast<int64_t>(s.w.sp.len)), static_cast<int64_t>(0))) : 0;
         s_begin[r] = static_cast<int32_t>(max(pos + 1 - a.window, static_cast<int64_t>(0)));
       }
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {
         const int d = 4 * (lane + 32 * k);
         if (d < DP) {
-          const uint32_t at = q_smem + (((r >> 4) * kSteps16 + d / 16 / 4 * 4 + (d >> 2) % 4) * 32 + (r & 7) * 4 + (d >> 4) % 4) * 16 + ((r >> 3) & 1) * 4;
+          const uint32_t at = q_smem + (((r >> 4) * kSteps16 + d / 64 * 4 + (d >> 2) % 4) * 32 + (r & 7) * 4 + (d >> 4) % 4) * 16 + ((r >> 3) & 1) * 4;
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(f16x2_bits(x[k][0] * up, x[k][1] * up)) : "memory");
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 8), "r"(f16x2_bits(x[k][2] * up, x[k][3] * up)) : "memory");
         }
@@ -317,7 +405,6 @@ __global__ void __launch_bounds__(kFewAttThreads, 1) attention_few_kernel(const 
     }
     float fq[MT][2];
     int32_t end[MT][2], begin[MT][2];
-    int32_t all_end = INT32_MAX, all_begin = 0;  // what every row sees
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -327,46 +414,8 @@ __global__ void __launch_bounds__(kFewAttThreads, 1) attention_few_kernel(const 
         end[m][e] = s_end[r];
         begin[m][e] = s_begin[r];
       }
-    all_end = s_end[0];             // rows' positions do not decrease
-    all_begin = s_begin[rows - 1];
-
-    // ---- the steps of this warp -----------------------------------------------------------------
-    const int32_t len = w.sp.len;
-    const auto entry = [&](int32_t t) -> int32_t {  // the page of step t, -1 where there is none
-      const int64_t p = static_cast<int64_t>(w.step0 + t) * kTile;
-      return t < t1 && p < len ? __ldg(a.b.table + seq * a.b.ld_table + static_cast<int32_t>(p) / a.c.page) : -1;
-    };
-    const auto copy = [&](int32_t t, int stage, int32_t page) {
-      const int32_t p = (w.step0 + t) * kTile;
-      const bool has = page >= 0 && page < a.c.pages;
-      const int in_page = has ? p % a.c.page : 0;
-      const int64_t head = static_cast<int64_t>(has ? page : 0) * a.c.heads + kvh;
-      const int64_t base = (head * a.c.page + in_page) * a.c.dim;
-      const uint32_t to = ring + stage * Z::kStage;
-#pragma unroll
-      for (int h = 0; h < DP / 64; ++h)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = g + 8 * e, d = 64 * h + 16 * c;
-          const bool in = has && p + r < len && d < a.c.dim;
-          copy_async<16>(to + ((2 * h + e) * 32 + lane) * 16, a.c.k + (in ? base + r * a.c.dim + d : 0), in ? 16u : 0u);
-        }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int h = 0; h < kPieces; ++h) {
-          const int r = 2 * c + (i & 1) + 8 * (i >> 1), d = kCols * g + 16 * h;
-          const bool in = has && p + r < len && d < a.c.dim;
-          copy_async<kVBytes>(to + kTile * DP + ((i * kPieces + h) * 32 + lane) * kVBytes, a.c.v + (in ? base + r * a.c.dim + d : 0),
-                              in ? static_cast<uint32_t>(kVBytes) : 0u);
-        }
-      if (lane < 2) {
-        const int64_t block = head * (a.c.page >> a.c.log2_block) + (in_page >> a.c.log2_block);
-        copy_async<4>(smem_addr(&s_scale[warp][stage][lane]), (lane ? a.c.vs : a.c.ks) + block, has ? 4u : 0u);
-      } else if (lane == 2) {
-        s_scale[warp][stage][2] = has ? 1.0f : 0.0f;
-      }
-    };
+    // what every row sees (their positions do not decrease)
+    const int32_t all_end = s_end[0], all_begin = s_begin[s.rows - 1], len = s.w.sp.len;
 
     float o[MT][kCols][4], mx[MT][2], sum[MT][2];
     float unit = 0x1p-100f;
@@ -379,145 +428,156 @@ __global__ void __launch_bounds__(kFewAttThreads, 1) attention_few_kernel(const 
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[m][j][e] = 0.0f;
     }
-    const int32_t tw = t0 + warp;
-    int32_t pages[kStages];
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) pages[i] = entry(tw + i * kFewAttWarps);
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (tw + i * kFewAttWarps < t1) copy(tw + i * kFewAttWarps, i, pages[i]);
-      asm volatile("cp.async.commit_group;" ::: "memory");
-    }
-    int32_t page_next = pages[kStages - 1];
-    int stage = 0;
-    for (int32_t t = tw; t < t1; t += kFewAttWarps) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-      __syncwarp();  // the scales are other lanes' copies; every lane has done with the step before
-      {
-        const int32_t ahead = t + (kStages - 1) * kFewAttWarps;
-        if (ahead < t1) copy(ahead, stage == 0 ? kStages - 1 : stage - 1, page_next);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        page_next = entry(ahead + kFewAttWarps);
-      }
+    const int32_t count = s.t1 - s.t0;
+    const int32_t w0 = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * warp / kFewAttWarps);
+    const int32_t w1 = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * (warp + 1) / kFewAttWarps);
+    for (int32_t t = w0; t < w1; ++t) {
+      if (!failed) failed = !__all_sync(kFull, mbar_wait(smem_addr(&s_full[warp][stage]), phase, kFewWaitNs));
+      if (failed) break;
       const uint32_t from = ring + stage * Z::kStage;
       const float ks = s_scale[warp][stage][0], vs = s_scale[warp][stage][1];
       const bool has = s_scale[warp][stage][2] != 0.0f;
-      const int32_t p = (w.step0 + t) * kTile;
-      if (++stage == kStages) stage = 0;
-      if (!has) continue;
-
-      float x[MT][2][4] = {};
+      const int32_t p = (s.w.step0 + t) * kTile;
+      if (has) {
+        float x[MT][2][4] = {};
 #pragma unroll
-      for (int h = 0; h < DP / 64; ++h) {
-        uint32_t k0[4], k1[4];
-        lds16(k0, from + ((2 * h) * 32 + lane) * 16);
-        lds16(k1, from + ((2 * h + 1) * 32 + lane) * 16);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w0 = prepare_word<FMT>(k0[i]), w1 = prepare_word<FMT>(k1[i]);
-          const uint32_t b00 = pair_in_word<FMT, 0>(w0), b01 = pair_in_word<FMT, 1>(w0);
-          const uint32_t b10 = pair_in_word<FMT, 0>(w1), b11 = pair_in_word<FMT, 1>(w1);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            uint32_t qa[4];
-            if constexpr (!kHeld) lds16(qa, q_smem + ((m * kSteps16 + 4 * h + i) * 32 + lane) * 16);
-            const uint32_t(&qq)[4] = kHeld ? qf[kHeld ? m * kSteps16 + 4 * h + i : 0] : qa;
-            mma16816(x[m][0], qq, b00, b01);
-            mma16816(x[m][1], qq, b10, b11);
+        for (int h = 0; h < DP / 64; ++h) {
+          uint32_t k0[4], k1[4];
+          if constexpr (DP == 64) {  // 64-byte rows: 16-byte piece i of row r lies at i ^ (r / 2 % 4)
+            lds16(k0, from + g * 64 + ((c ^ ((g >> 1) & 3)) << 4));
+            lds16(k1, from + (g + 8) * 64 + ((c ^ ((g >> 1) & 3)) << 4));
+          } else {                   // 128-byte rows: at i ^ (r % 8)
+            const uint32_t at = from + (h >> 1) * kSlab + g * 128 + (((4 * (h & 1) + c) ^ g) << 4);
+            lds16(k0, at);
+            lds16(k1, at + 8 * 128);
           }
-        }
-      }
-      const bool whole = p + kTile <= all_end && p >= all_begin;
-      bool moved = false;
-      float was[MT][2];
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t y0 = prepare_word<FMT>(k0[i]), y1 = prepare_word<FMT>(k1[i]);
+            const uint32_t b00 = pair_in_word<FMT, 0>(y0), b01 = pair_in_word<FMT, 1>(y0);
+            const uint32_t b10 = pair_in_word<FMT, 0>(y1), b11 = pair_in_word<FMT, 1>(y1);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {  // row 16 m + 8 e + g, tokens 8 n + 2 c + i
-          const float f = fq[m][e] * ks;
-          float top = kNone;
-#pragma unroll
-          for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float& v = x[m][n][2 * e + i];
-              v *= f;
-              const int32_t j = p + 8 * n + 2 * c + i;
-              if (!whole && (j >= end[m][e] || j < begin[m][e])) v = kNone;
-              top = fmaxf(top, v);
+            for (int m = 0; m < MT; ++m) {
+              uint32_t qa[4];
+              if constexpr (!kHeld) lds16(qa, q_smem + ((m * kSteps16 + 4 * h + i) * 32 + lane) * 16);
+              const uint32_t(&qq)[4] = kHeld ? qf[kHeld ? m * kSteps16 + 4 * h + i : 0] : qa;
+              mma16816(x[m][0], qq, b00, b01);
+              mma16816(x[m][1], qq, b10, b11);
             }
-          top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-          was[m][e] = mx[m][e];
-          if (top > mx[m][e]) {
-            mx[m][e] = top;
-            moved = true;
           }
         }
-      const float vmag = fabsf(vs), unit_was = unit;
-      if (vmag > unit && is_finite_f(vmag)) {  // the next power of two (vs is a power of two itself: twice that)
-        unit = __uint_as_float((__float_as_uint(fminf(vmag, 0x1p125f)) & 0x7f800000u) + 0x00800000u);
-        moved = true;
-      }
-      if (__any_sync(kFull, moved)) {
-        const float shrink = unit_was / unit;
+        const bool whole = p + kTile <= all_end && p >= all_begin;
+        bool moved = false;
+        float was[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // row 16 m + 8 e + g, tokens 8 n + 2 c + i
+            const float f = fq[m][e] * ks;
+            float top = kNone;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) x[m][q >> 1][2 * e + (q & 1)] *= f;
+            if (!whole) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int32_t j = p + 8 * (q >> 1) + 2 * c + (q & 1);
+                if (j >= end[m][e] || j < begin[m][e]) x[m][q >> 1][2 * e + (q & 1)] = kNone;
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) top = fmaxf(top, x[m][q >> 1][2 * e + (q & 1)]);
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+            was[m][e] = mx[m][e];
+            if (top > mx[m][e]) {
+              mx[m][e] = top;
+              moved = true;
+            }
+          }
+        const float vmag = fabsf(vs), unit_was = unit;
+        if (vmag > unit && is_finite_f(vmag)) {  // the next power of two above it
+          unit = __uint_as_float((__float_as_uint(fminf(vmag, 0x1p125f)) & 0x7f800000u) + 0x00800000u);
+          moved = true;
+        }
+        if (__any_sync(kFull, moved)) {
+          const float shrink = unit_was / unit;
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float f = mx[m][e] == kNone ? 1.0f : ex2(was[m][e] - mx[m][e]), fo = f * shrink;
+              sum[m][e] *= f;
+#pragma unroll
+              for (int j = 0; j < kCols; ++j) {
+                o[m][j][2 * e] *= fo;
+                o[m][j][2 * e + 1] *= fo;
+              }
+            }
+        }
+        const float fv = vs * (0x1p15f / unit);
+        uint32_t pa[MT][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float f = mx[m][e] == kNone ? 1.0f : ex2(was[m][e] - mx[m][e]), fo = f * shrink;
-            sum[m][e] *= f;
+            const float top = mx[m][e] == kNone ? 0.0f : mx[m][e];
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) {
-              o[m][j][2 * e] *= fo;
-              o[m][j][2 * e + 1] *= fo;
+            for (int q = 0; q < 2; ++q) {
+              float y[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float v = x[m][q][2 * e + i], w = ex2(v - top);
+                sum[m][e] += w;
+                y[i] = w * fv;
+                if (!whole && v == kNone) y[i] = 0.0f;  // (the scale of what is not seen may be anything)
+              }
+              pa[m][2 * q + e] = f16x2_bits(y[0], y[1]);
             }
           }
+#pragma unroll
+        for (int h = 0; h < kPieces; ++h) {
+          constexpr int kWords = kVBytes / 4;
+          uint32_t vw[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 2 * c + (i & 1) + 8 * (i >> 1);
+            if constexpr (DP == 64) {
+              const uint32_t at = from + kTile * DP + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8;
+              asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(vw[i][0]), "=r"(vw[i][1]) : "r"(at));
+            } else {  // DP = 256: pieces 2 g and 2 g + 1 of 16, eight a box
+              const int piece = DP == 128 ? g : 2 * g + h;
+              lds16(vw[i], from + kTile * DP + (piece >> 3) * kSlab + r * 128 + (((piece & 7) ^ (r & 7)) << 4));
+            }
+            if (!whole && p + r >= len) vw[i][0] = vw[i][1] = vw[i][2] = vw[i][3] = 0u;  // memory past the end may hold anything
+          }
+#pragma unroll
+          for (int q = 0; q < kWords; ++q) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const uint32_t b0 = pair_of_words_at<FMT>(vw[0][q], vw[1][q], b), b1 = pair_of_words_at<FMT>(vw[2][q], vw[3][q], b);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) mma16816(o[m][16 * h + 4 * q + b], pa[m], b0, b1);
+            }
+          }
+        }
       }
-      const float fv = vs * (0x1p15f / unit);
-      uint32_t pa[MT][4];
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float top = mx[m][e] == kNone ? 0.0f : mx[m][e];
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            float y[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float v = x[m][n][2 * e + i], q = ex2(v - top);
-              sum[m][e] += q;
-              y[i] = v == kNone ? 0.0f : q * fv;  // (the scale of what is not seen may be anything)
-            }
-            pa[m][2 * n + e] = f16x2_bits(y[0], y[1]);
-          }
-        }
-#pragma unroll
-      for (int h = 0; h < kPieces; ++h) {
-        constexpr int kWords = kVBytes / 4;
-        uint32_t vw[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t at = from + kTile * DP + ((i * kPieces + h) * 32 + lane) * kVBytes;
-          if constexpr (kVBytes == 16) lds16(vw[i], at);
-          else asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(vw[i][0]), "=r"(vw[i][1]) : "r"(at));
-        }
-#pragma unroll
-        for (int q = 0; q < kWords; ++q) {
-          uint32_t y[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = prepare_word<FMT>(vw[i][q]);
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const uint32_t b0 = pair_of_words_at<FMT>(y[0], y[1], b), b1 = pair_of_words_at<FMT>(y[2], y[3], b);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) mma16816(o[m][16 * h + 4 * q + b], pa[m], b0, b1);
-          }
-        }
+      __syncwarp();  // every lane has read the stage
+      copy();
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (failed) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) sum[m][0] = sum[m][1] = __uint_as_float(0x7fc00000u);
+    }
+    more = advance();
+    if (more && !failed) {  // the next segment's first steps are on their way while the sums are joined
+      aim(n);
+#pragma unroll 1
+      for (int i = 0; i < kStages; ++i) copy();
+    }
 
     // ---- the warps' sums, four columns of each of the eight column groups at a time ----------------
 #pragma unroll
@@ -532,22 +592,22 @@ __global__ void __launch_bounds__(kFewAttThreads, 1) attention_few_kernel(const 
         }
       }
     if (lane == 0) s_unit[warp] = unit;
-    const bool whole_item = first && last;
-    float* slot = WHOLE || whole_item ? nullptr : slots + (2 * static_cast<size_t>(blockIdx.x) + (first ? 1 : 0)) * Z::kSlot;
+    const bool first = s.t0 == 0, last = s.t1 == s.w.steps;
+    float* slot = WHOLE || (first && last) ? nullptr : slots + (2 * static_cast<size_t>(blockIdx.x) + (first ? 1 : 0)) * Z::kSlot;
 #pragma unroll
     for (int q = 0; q < kCols / 4; ++q) {
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int r = 16 * m + 8 * (e >> 1) + g, n = 2 * c + (e & 1);
-          *reinterpret_cast<float4*>(join + ((warp * kRows + r) * 8 + n) * 4) =
+          const int r = 16 * m + 8 * (e >> 1) + g, col = 2 * c + (e & 1);
+          *reinterpret_cast<float4*>(join + ((warp * kRows + r) * 8 + col) * 4) =
               make_float4(o[m][4 * q][e], o[m][4 * q + 1][e], o[m][4 * q + 2][e], o[m][4 * q + 3][e]);
         }
       __syncthreads();
       for (int i = tid; i < kRows * 8; i += kFewAttThreads) {
         const int r = i >> 3, d = kCols * (i & 7) + 4 * q;
-        if (r >= rows) break;
+        if (r >= s.rows) break;
         float top = kNone, l = 0.0f;
 #pragma unroll
         for (int k = 0; k < kFewAttWarps; ++k) top = fmaxf(top, s_m[k][r]);
@@ -563,23 +623,32 @@ __global__ void __launch_bounds__(kFewAttThreads, 1) attention_few_kernel(const 
         }
         if (slot) {
           *reinterpret_cast<float4*>(slot + r * DP + d) = make_float4(v[0], v[1], v[2], v[3]);
-          if (q == 0 && (i & 7) == 0) {
+          if (d == 0) {
             slot[kRows * DP + r] = top;
             slot[kRows * (DP + 1) + r] = l;
           }
         } else {
-          store_row(a, w.sp.row + (row0 + r) / a.group, kvh * a.group + (row0 + r) % a.group, d, v, top, l);
+          store_row(a, s.w.sp.row + (s.row0 + r) / a.group, s.kvh * a.group + (s.row0 + r) % a.group, d, v, top, l);
         }
       }
       __syncthreads();
     }
     if (!WHOLE && first && !last && tid == 0) {
       FewMeta meta;
-      meta.seq = seq;
-      meta.head = kvh;
-      meta.row0 = row0;
-      meta.last = static_cast<int32_t>((item_u0 + w.steps - 1) / chunk);
+      meta.seq = s.seq;
+      meta.head = s.kvh;
+      meta.row0 = s.row0;
+      meta.last = static_cast<int32_t>((s.item_u0 + s.w.steps - 1) / chunk);
       static_cast<FewMeta*>(a.ws)[blockIdx.x] = meta;
+    }
+  }
+  if (failed) {  // copies still in flight land before the memory is released
+    for (int i = 0; i < kStages; ++i) {
+      mbar_wait(smem_addr(&s_full[warp][stage]), phase, kFewWaitNs);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
   }
 }
@@ -620,18 +689,31 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttentionArgs
 }
 
 // ---- host side ----------------------------------------------------------------------------------
+inline bool encode_codes(CUtensorMap* m, const AttentionArgs& a, const void* codes) {
+  const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!enc) return false;
+  const bool narrow = a.c.dim <= 64;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.c.dim), static_cast<cuuint64_t>(a.c.page), static_cast<cuuint64_t>(a.c.pages * a.c.heads)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.c.dim), static_cast<cuuint64_t>(a.c.page) * a.c.dim};
+  const cuuint32_t box[3] = {narrow ? 64u : 128u, kTile, 1}, es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 template <int FMT, int DP, int MT>
 qz_status run_few(const AttentionArgs& a, const FewPlan& p, cudaStream_t s) {
   using Z = FewSizes<DP, MT>;
+  CacheMaps maps{};
+  if (a.c.pages > 0 && (!encode_codes(&maps.k, a, a.c.k) || !encode_codes(&maps.v, a, a.c.v))) return QZ_ERR_CUDA;
   if (p.whole) {
     const auto k = &attention_few_kernel<FMT, DP, MT, true>;
     if (!set_dyn_smem(reinterpret_cast<const void*>(k), Z::kSmem)) return QZ_ERR_CUDA;
-    k<<<static_cast<unsigned>(p.grid), kFewAttThreads, Z::kSmem, s>>>(a, p.grid, p.min_chunk);
+    k<<<static_cast<unsigned>(p.grid), kFewAttThreads, Z::kSmem, s>>>(a, maps, p.grid, p.min_chunk);
     return launch_status();
   }
   const auto k = &attention_few_kernel<FMT, DP, MT, false>;
   if (!set_dyn_smem(reinterpret_cast<const void*>(k), Z::kSmem)) return QZ_ERR_CUDA;
-  k<<<static_cast<unsigned>(p.grid), kFewAttThreads, Z::kSmem, s>>>(a, p.grid, p.min_chunk);
+  k<<<static_cast<unsigned>(p.grid), kFewAttThreads, Z::kSmem, s>>>(a, maps, p.grid, p.min_chunk);
   if (launch_status() != QZ_OK) return QZ_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];

@@ -229,7 +229,7 @@ qz_status check_cache(const qz_cache* c) {
   if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128) return QZ_ERR_UNSUPPORTED;
   if (c->page > 1024 || c->dim > 256 || c->dim % 16) return QZ_ERR_UNSUPPORTED;
   if (c->page % c->block) return QZ_ERR_SHAPE;
-  if (c->pages > INT32_MAX || c->kv_heads > 65535) return QZ_ERR_UNSUPPORTED;
+  if (c->kv_heads > 65535 || c->pages > INT32_MAX / c->kv_heads) return QZ_ERR_UNSUPPORTED;
   if (c->pages > 0 && (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales)) return QZ_ERR_NULL;
   if (!is_aligned(c->k_codes, 16) || !is_aligned(c->v_codes, 16) || !is_aligned(c->k_scales, 4) || !is_aligned(c->v_scales, 4))
     return QZ_ERR_ALIGN;
