@@ -11,21 +11,21 @@
 namespace qz {
 
 // A CTA takes whole items where no sequence can be long enough to be worth cutting (its pages hold at most
-// kWhole steps); else the steps are shared out evenly, kMinChunk at least to a CTA.
-constexpr int64_t kWhole = 64, kMinChunk = 32;
+// kWhole tokens); else the steps are shared out evenly, kMinChunk tokens at least to a CTA.
+constexpr int64_t kWhole = 1024, kMinChunk = 512;
 
 FewPlan few_att_plan(const qz_cache& c, int64_t seqs, int64_t tokens, int64_t heads, int64_t table_pages, int sms) {
   FewPlan p{};
   const int64_t group = heads / c.kv_heads, rows = (tokens * group + seqs - 1) / seqs;
   p.row_tiles = few_att_tiles(c.dim, rows);
-  const int64_t items = c.kv_heads * ((tokens * group) / (16 * p.row_tiles) + seqs);
-  p.whole = table_pages * c.page <= kWhole * kTile && items < INT32_MAX;
+  const int64_t items = c.kv_heads * ((tokens * group) / (8 * p.row_tiles) + seqs);
+  p.whole = table_pages * c.page <= kWhole && items < INT32_MAX;
   p.grid = p.whole ? static_cast<int>(items) : sms;
-  p.min_chunk = static_cast<int>(kMinChunk);
+  p.min_chunk = static_cast<int>(kMinChunk / few_att_step(c.dim));
   return p;
 }
 size_t few_att_workspace(const FewPlan& p, int dim) {
-  const size_t slot = static_cast<size_t>(16 * p.row_tiles) * (few_att_dim(dim) + 2) * sizeof(float);
+  const size_t slot = static_cast<size_t>(8 * p.row_tiles) * (few_att_dim(dim) + 2) * sizeof(float);
   return p.whole ? 0 : static_cast<size_t>(p.grid) * (16 + 2 * slot);
 }
 

@@ -26,18 +26,17 @@ struct AttentionArgs {
 };
 
 // The rows of an item are the (token, head of the group) pairs of one sequence and kv head, heads fastest:
-// row r is new token r / group.  The few-row kernel takes 16 or 32 of them at a time.
-constexpr int kTile = 16;   // tokens of a step: every scale block and page is whole steps
+// row r is new token r / group.
 
 // ---- a few rows (qz_attention_few.cuh) ---------------------------------------------------------
-constexpr int kFewAttWarps = 8;
-constexpr int kFewAttThreads = 32 * kFewAttWarps;
 constexpr int few_att_dim(int dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
-// row tiles of 16 that a CTA holds: two where more than 16 rows are to be expected and registers allow it
-inline int few_att_tiles(int dim, int64_t rows) { return rows > 16 && dim <= 128 ? 2 : 1; }
+// tiles of 8 rows that a CTA holds, as many as the rows to be expected fill and registers allow
+inline int few_att_tiles(int dim, int64_t rows) { return rows <= 8 ? 1 : rows <= 16 || dim > 128 ? 2 : 4; }
+// tokens of a step of one warp: 4 or 8 KiB of keys and values
+constexpr int few_att_step(int dim) { return dim > 128 ? 16 : 32; }
 
 struct FewPlan {
-  int row_tiles;      // MT
+  int row_tiles;      // of 8 rows
   bool whole;         // a CTA takes whole items, no partial results
   int grid;
   int min_chunk;      // steps of a CTA at least

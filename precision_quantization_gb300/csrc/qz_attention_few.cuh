@@ -4,15 +4,18 @@
 //   out = sum p_j vs_j v_j / l        (k_j, v_j the codes, ks_j, vs_j their block's scales)
 //
 // Bound by HBM: every code is read once and meets up to 32 rows.  So the codes stream and everything else
-// has to fit beside them: a warp has a ring of kStages steps of 16 tokens of its own that TMA fills, keys and
-// values each a box of 16 rows in the hardware's swizzle.  The summation index of q . k and the columns of
-// p v are free to be permuted, and with lane (g, c) = (lane / 4, lane % 4)
-//   keys    row g and g + 8 of the step, bytes 64 h + 16 c .. + 15: four 16-wide products' B operand,
-//   values  rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9, bytes w g .. w g + w - 1 (w = dim / 8): the B operand of
-//           w products, one output column a byte,
+// has to fit beside them: a warp has a ring of its own that TMA fills, a step of 32 tokens (of more than 128
+// elements: 16) a stage, in the hardware's swizzle.  Keys and values are the products' A operands,
+//   x^T [tokens][rows] = K q^T,   out^T [elements][rows] += V^T p^T,
+// so that eight rows, what a kv head's group often has, fill the operand of eight columns, and what was
+// decoded for one column tile serves them all.  The summation index of K q^T and the rows of V^T may be
+// permuted; with lane (g, c) = (lane / 4, lane % 4)
+//   keys    rows g and g + 8 of 16, bytes 64 h + 16 c .. + 15: four 16-wide products,
+//   values  rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9, bytes w g .. w g + w - 1 (w = dim / 8): w / 2 products
 // are whole 16-byte pieces, read from different banks.  8-bit codes are exact in f16, q is made f16 by a
 // power of two of its row.  The weights p vs are made f16 times 2^15 / unit, unit a power of two >= every vs
-// so far, so that a scale far below the largest keeps its 11 bits (down to 2^-29 of it).
+// so far, so that a scale far below the largest keeps its 11 bits (down to 2^-29 of it); a transpose of
+// 8 x 8 (movmatrix) makes them operands.
 //
 // The work is cut in equal shares of steps over a persistent grid, whatever the lengths are (they lie on
 // the GPU): item after item (sequence, kv head, row tile), a CTA's share begins and ends anywhere.  A share
@@ -85,6 +88,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// the transpose of an 8 x 8 matrix of 16-bit values, row g's columns 2 c and 2 c + 1 in lane (g, c)
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -154,17 +163,24 @@ __device__ __forceinline__ void store_row(const AttentionArgs& a, int64_t token,
 }
 
 // ---- sizes --------------------------------------------------------------------------------------
-template <int DP, int MT>
+// DP: dim rounded up to 64, 128 or 256; NT: tiles of 8 rows.
+template <int DP, int NT>
 struct FewSizes {
-  static constexpr int kRows = 16 * MT;
-  static constexpr uint32_t kStage = 2 * kTile * DP;                // bytes: keys, then values
-  static constexpr int kStages = DP == 64 ? 8 : DP == 128 ? 5 : 3;
-  static constexpr uint32_t kRing = kFewAttWarps * kStages * kStage;
-  static constexpr uint32_t kQ = MT * (DP / 16) * 512;              // q as A operands
-  static constexpr int kJoinCols = 32;                              // columns joined at a time
-  static constexpr uint32_t kJoin = kFewAttWarps * kRows * kJoinCols * 4;
-  static constexpr uint32_t kSmem = kRing + kQ + kJoin + 1024;      // (the ring starts on a 1024-byte boundary)
-  static constexpr int kSlot = kRows * (DP + 2);                    // floats of a partial result: sums, m, l
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kStep = few_att_step(DP), kHalves = kStep / 16;   // tokens of a step, in 16s
+  // the sums take NT DP / 4 registers a thread: twelve warps where they leave room for the rest
+  static constexpr int kWarps = NT == 1 || NT * DP == 128 ? 12 : 8, kThreads = 32 * kWarps;
+  static constexpr uint32_t kHalf = 16 * DP;                             // bytes of 16 tokens' keys or values
+  static constexpr uint32_t kStage = 2 * kHalves * kHalf;                // keys, then values
+  static constexpr uint32_t kQ = NT * (DP / 16) * 256;                   // q as B operands
+  static constexpr int kJoinCols = 32;                                   // columns joined at a time
+  static constexpr uint32_t kJoin = kWarps * kRows * kJoinCols * 4;
+  static constexpr int kRoom = 226 * 1024 - 1024 - 4096 - static_cast<int>(kQ + kJoin);  // 4 KiB: static
+  static constexpr int kStages = kRoom / static_cast<int>(kWarps * kStage) < 4 ? kRoom / static_cast<int>(kWarps * kStage) : 4;
+  static_assert(kStages >= 2);
+  static constexpr uint32_t kRing = kWarps * kStages * kStage;
+  static constexpr uint32_t kSmem = kRing + kQ + kJoin + 1024;           // (the ring starts on a 1024-byte boundary)
+  static constexpr int kSlot = kRows * (DP + 2);                         // floats of a partial result: sums, m, l
 };
 struct FewMeta {     // an item that begins in a CTA's share and does not end there
   int32_t seq, head, row0, last;   // last: the CTA whose share holds its end; seq < 0: none
@@ -176,13 +192,13 @@ struct SeqWork {
   int32_t tiles;       // row tiles
   int32_t step0, steps;  // the steps that any of its rows may see (whole items: 1 unit an item)
 };
-__device__ __forceinline__ SeqWork seq_work(const AttentionArgs& a, int32_t s, int rows) {
+__device__ __forceinline__ SeqWork seq_work(const AttentionArgs& a, int32_t s, int rows, int step) {
   SeqWork w;
   w.sp = span_of(a.b, s, a.c.page);
   w.tiles = static_cast<int32_t>((static_cast<int64_t>(w.sp.n) * a.group + rows - 1) / rows);
   const int64_t lo = w.sp.p0 + 1 - a.window;
-  w.step0 = lo > 0 ? static_cast<int32_t>(lo / kTile) : 0;
-  w.steps = max((w.sp.len + kTile - 1) / kTile - w.step0, 1);
+  w.step0 = lo > 0 ? static_cast<int32_t>(lo / step) : 0;
+  w.steps = max(static_cast<int32_t>((static_cast<int64_t>(w.sp.len) + step - 1) / step) - w.step0, 1);
   return w;
 }
 __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
@@ -202,21 +218,22 @@ struct Segment {
   int64_t item_u0;       // the item's first unit
 };
 
-template <int FMT, int DP, int MT, bool WHOLE>
-__global__ void __launch_bounds__(kFewAttThreads, 1)
+template <int FMT, int DP, int NT, bool WHOLE>
+__global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
     attention_few_kernel(const AttentionArgs a, const __grid_constant__ CacheMaps maps, int grid, int min_chunk) {
-  using Z = FewSizes<DP, MT>;
-  constexpr int kRows = Z::kRows, kStages = Z::kStages, kSteps16 = DP / 16, kCols = DP / 8;
+  using Z = FewSizes<DP, NT>;
+  constexpr int kRows = Z::kRows, kStages = Z::kStages, kStep = Z::kStep, kHalves = Z::kHalves, kWarps = Z::kWarps;
+  constexpr int kSteps16 = DP / 16, kCols = DP / 8, kTiles = DP / 16;  // products of a sum, columns of a lane, tiles of 16 elements
   constexpr int kPieces = DP == 256 ? 2 : 1;    // 16-byte pieces of a lane's columns; 4-element ones of its part of a row of q
-  constexpr int kVBytes = DP == 64 ? 8 : 16;
-  constexpr bool kHeld = MT * DP <= 128;        // q in registers, else read from shared memory for each step
-  constexpr uint32_t kSlab = kTile * (DP < 128 ? DP : 128);  // bytes of a box: rows of 64 or 128 bytes
+  constexpr bool kHeld = NT * DP <= 128;        // q in registers, else read from shared memory for each step
+  constexpr uint32_t kRowBytes = DP < 128 ? 64 : 128, kSlab = kStep * kRowBytes;  // a box's row, and a step's boxes of one x
   extern __shared__ uint8_t few_raw[];
-  __shared__ int64_t s_scan[kFewAttWarps + 1], s_found[2];
-  __shared__ float s_fq[kRows], s_m[kFewAttWarps][kRows], s_l[kFewAttWarps][kRows], s_unit[kFewAttWarps];
+  __shared__ int64_t s_scan[kWarps + 1], s_found[2];
+  __shared__ float s_fq[kRows], s_m[kWarps][kRows], s_l[kWarps][kRows], s_unit[kWarps];
   __shared__ int32_t s_end[kRows], s_begin[kRows];
-  __shared__ __align__(16) float s_scale[kFewAttWarps][kStages][4];  // ks, vs, whether the step has a page
-  __shared__ __align__(8) uint64_t s_full[kFewAttWarps][kStages];
+  __shared__ __align__(16) float s_scale[kWarps][kStages][4];  // ks, vs of the first 16 tokens, of the second
+  __shared__ int32_t s_has[kWarps][kStages];                   // bit i: the i-th 16 tokens have a page
+  __shared__ __align__(8) uint64_t s_full[kWarps][kStages];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const uint32_t base = (smem_addr(few_raw) + 1023u) & ~1023u;
@@ -225,24 +242,24 @@ __global__ void __launch_bounds__(kFewAttThreads, 1)
   const uint32_t q_smem = base + Z::kRing;
   float* join = reinterpret_cast<float*>(smem + Z::kRing + Z::kQ);
   if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(smem_addr(&s_full[warp][i]), 3);  // the codes, ks, vs
+    for (int i = 0; i < kStages; ++i) mbar_init(smem_addr(&s_full[warp][i]), 1 + 2 * kHalves);  // the codes, the scales
     mbar_init_fence();
   }
 
   // ---- this CTA's share: units [u0, u1) of the sequences' work one after the other ---------------
   const auto work_of = [&](const SeqWork& w) { return static_cast<int64_t>(w.tiles) * a.c.heads * (WHOLE ? 1 : w.steps); };
-  const auto units_of = [&](int32_t s) { return s < a.b.seqs ? work_of(seq_work(a, s, kRows)) : 0; };
+  const auto units_of = [&](int32_t s) { return s < a.b.seqs ? work_of(seq_work(a, s, kRows, kStep)) : 0; };
   int64_t u0, u1, chunk = 1, before = 0;
   if (!WHOLE) {
     int64_t mine = 0;
-    for (int32_t s = tid; s < a.b.seqs; s += kFewAttThreads) mine += units_of(s);
+    for (int32_t s = tid; s < a.b.seqs; s += Z::kThreads) mine += units_of(s);
 #pragma unroll
     for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(kFull, mine, o);
     if (lane == 0) s_scan[warp] = mine;
     __syncthreads();
     int64_t total = 0;
 #pragma unroll
-    for (int w = 0; w < kFewAttWarps; ++w) total += s_scan[w];
+    for (int w = 0; w < kWarps; ++w) total += s_scan[w];
     __syncthreads();
     chunk = max((total + grid - 1) / grid, static_cast<int64_t>(min_chunk));
     u0 = blockIdx.x * chunk;
@@ -254,13 +271,13 @@ __global__ void __launch_bounds__(kFewAttThreads, 1)
   }
   if (u0 >= u1) return;
   bool found = false;  // the sequence that holds unit u0
-  for (int32_t s0 = 0; s0 < a.b.seqs && !found; s0 += kFewAttThreads) {
+  for (int32_t s0 = 0; s0 < a.b.seqs && !found; s0 += Z::kThreads) {
     const int64_t mine = units_of(s0 + tid), in_warp = warp_scan(mine, lane);
     if (lane == 31) s_scan[warp] = in_warp;
     __syncthreads();
     int64_t at = before + in_warp, all = before;
 #pragma unroll
-    for (int w = 0; w < kFewAttWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       if (w < warp) at += s_scan[w];
       all += s_scan[w];
     }
@@ -279,13 +296,13 @@ __global__ void __launch_bounds__(kFewAttThreads, 1)
   int64_t u = u0;
   Segment n;  // the next segment
   n.seq = static_cast<int32_t>(s_found[0]);
-  n.w = seq_work(a, n.seq, kRows);
+  n.w = seq_work(a, n.seq, kRows, kStep);
   const auto advance = [&]() -> bool {
     if (u >= u1) return false;
     while (u >= before + work_of(n.w)) {
       before += work_of(n.w);
       if (++n.seq >= a.b.seqs) return false;  // (not reached while the lengths stay as they are)
-      n.w = seq_work(a, n.seq, kRows);
+      n.w = seq_work(a, n.seq, kRows, kStep);
     }
     const int64_t in_seq = u - before, item = WHOLE ? in_seq : in_seq / n.w.steps;
     n.t0 = WHOLE ? 0 : static_cast<int32_t>(in_seq - item * n.w.steps);
@@ -299,52 +316,67 @@ __global__ void __launch_bounds__(kFewAttThreads, 1)
   };
 
   // ---- the copies of this warp's steps, a ring ahead ---------------------------------------------
-  int32_t ct = 0, c_end = 0, c_index = 0, c_in = 0;   // the next step, the end; its page's place in the table, its first row there
-  int32_t c_page = -1, c_stage = 0;
+  // the next step and the end; the next 16 tokens' position, their page's place in the table and first row there
+  int32_t ct = 0, c_end = 0, c_index = 0, c_in = 0, c_page = -1, c_stage = 0, c_len = 0, c_kvh = 0;
+  int64_t c_pos = 0;
   const int32_t* c_row = nullptr;
-  int32_t c_len = 0, c_kvh = 0;
-  const auto entry = [&]() { return ct < c_end && static_cast<int64_t>(c_index) * a.c.page + c_in < c_len ? __ldg(c_row + c_index) : -1; };
+  const auto entry = [&]() { return c_pos < c_len ? __ldg(c_row + c_index) : -1; };
   const auto aim = [&](const Segment& s) {  // at a segment's steps: a run of them for each warp
     const int32_t count = s.t1 - s.t0;
-    ct = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * warp / kFewAttWarps);
-    c_end = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * (warp + 1) / kFewAttWarps);
-    const int32_t p = (s.w.step0 + ct) * kTile;
-    c_index = p / a.c.page;
-    c_in = p - c_index * a.c.page;
+    ct = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * warp / kWarps);
+    c_end = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * (warp + 1) / kWarps);
+    c_pos = (static_cast<int64_t>(s.w.step0) + ct) * kStep;
+    c_index = static_cast<int32_t>(c_pos / a.c.page);
+    c_in = static_cast<int32_t>(c_pos - static_cast<int64_t>(c_index) * a.c.page);
     c_row = a.b.table + s.seq * a.b.ld_table;
     c_len = s.w.sp.len;
     c_kvh = s.kvh;
-    c_page = entry();
+    c_page = ct < c_end ? entry() : -1;
   };
   const auto copy = [&]() {  // one step, into c_stage
     if (ct >= c_end) return;
-    const int32_t page = c_page, in = c_in;
     ++ct;
-    c_in += kTile;
-    if (c_in >= a.c.page) {
-      c_in = 0;
-      ++c_index;
-      c_page = entry();
-    }
-    const bool has = page >= 0 && page < a.c.pages;
-    const int32_t head = (has ? page : 0) * a.c.heads + c_kvh;
     const uint32_t bar = smem_addr(&s_full[warp][c_stage]), to = ring + c_stage * Z::kStage;
-    if (lane < 2) {
-      if (has) {
-        const int64_t block = static_cast<int64_t>(head) * (a.c.page >> a.c.log2_block) + (in >> a.c.log2_block);
-        copy_scale(smem_addr(&s_scale[warp][c_stage][lane]), (lane ? a.c.vs : a.c.ks) + block, bar);
+    int32_t page[kHalves], in[kHalves];
+#pragma unroll
+    for (int i = 0; i < kHalves; ++i) {
+      page[i] = static_cast<uint32_t>(c_page) < static_cast<uint32_t>(a.c.pages) ? c_page : -1;
+      if (c_pos >= c_len) page[i] = -1;
+      in[i] = c_in;
+      c_pos += 16;
+      c_in += 16;
+      if (c_in == a.c.page) {
+        c_in = 0;
+        ++c_index;
+        c_page = entry();
+      }
+    }
+    if (lane < 2 * kHalves) {
+      const int i = kHalves == 2 ? lane >> 1 : 0;
+      const int32_t pg = kHalves == 2 && i ? page[kHalves - 1] : page[0], at = kHalves == 2 && i ? in[kHalves - 1] : in[0];
+      if (pg >= 0) {
+        const int64_t block = (static_cast<int64_t>(pg) * a.c.heads + c_kvh) * (a.c.page >> a.c.log2_block) + (at >> a.c.log2_block);
+        copy_scale(smem_addr(&s_scale[warp][c_stage][lane]), ((lane & 1) ? a.c.vs : a.c.ks) + block, bar);
       } else {
         arrive_on(bar);
       }
     }
     if (lane == 0) {
-      s_scale[warp][c_stage][2] = has ? 1.0f : 0.0f;
-      if (has) {
-        mbar_expect_tx(bar, Z::kStage);
+      int32_t has = 0;
 #pragma unroll
-        for (int h = 0; h < kPieces; ++h) {
-          box_load(to + h * kSlab, &maps.k, 128 * h, in, head, bar);
-          box_load(to + kTile * DP + h * kSlab, &maps.v, 128 * h, in, head, bar);
+      for (int i = 0; i < kHalves; ++i) has |= (page[i] >= 0 ? 1 : 0) << i;
+      s_has[warp][c_stage] = has;
+      if (has) {
+        mbar_expect_tx(bar, (kHalves == 2 && has == 3 ? 2u : 1u) * 2u * Z::kHalf);
+#pragma unroll
+        for (int i = 0; i < kHalves; ++i) {
+          if (page[i] < 0) continue;
+          const int32_t head = page[i] * a.c.heads + c_kvh;
+#pragma unroll
+          for (int h = 0; h < kPieces; ++h) {
+            box_load(to + h * kSlab + i * (16 * kRowBytes), &maps.k, 128 * h, in[i], head, bar);
+            box_load(to + kHalves * Z::kHalf + h * kSlab + i * (16 * kRowBytes), &maps.v, 128 * h, in[i], head, bar);
+          }
         }
       } else {
         arrive_on(bar);
@@ -365,8 +397,8 @@ __global__ void __launch_bounds__(kFewAttThreads, 1)
 
   while (more) {
     const Segment s = n;
-    // ---- q as f16 A operands, row by row; what each row sees ------------------------------------
-    for (int r = warp; r < kRows; r += kFewAttWarps) {
+    // ---- q as f16 B operands, row by row; what each row sees ------------------------------------
+    for (int r = warp; r < kRows; r += kWarps) {
       const int i = (s.row0 + r) / a.group, head = s.kvh * a.group + (s.row0 + r) % a.group;
       float x[kPieces][4];
       float top = 0.0f;
@@ -391,175 +423,203 @@ __global__ void __launch_bounds__(kFewAttThreads, 1)
       for (int k = 0; k < kPieces; ++k) {
         const int d = 4 * (lane + 32 * k);
         if (d < DP) {
-          const uint32_t at = q_smem + (((r >> 4) * kSteps16 + d / 64 * 4 + (d >> 2) % 4) * 32 + (r & 7) * 4 + (d >> 4) % 4) * 16 + ((r >> 3) & 1) * 4;
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(f16x2_bits(x[k][0] * up, x[k][1] * up)) : "memory");
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 8), "r"(f16x2_bits(x[k][2] * up, x[k][3] * up)) : "memory");
+          const uint32_t at = q_smem + (((r >> 3) * kSteps16 + d / 64 * 4 + (d >> 2) % 4) * 32 + (r & 7) * 4 + (d >> 4) % 4) * 8;
+          asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(f16x2_bits(x[k][0] * up, x[k][1] * up)),
+                       "r"(f16x2_bits(x[k][2] * up, x[k][3] * up))
+                       : "memory");
         }
       }
     }
     __syncthreads();
-    uint32_t qf[kHeld ? MT * kSteps16 : 1][4];
+    const auto load_q = [&](int t, int k, uint32_t (&b)[2]) {
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(b[0]), "=r"(b[1]) : "r"(q_smem + ((t * kSteps16 + k) * 32 + lane) * 8));
+    };
+    uint32_t qf[kHeld ? NT * kSteps16 : 1][2];
     if constexpr (kHeld) {
 #pragma unroll
-      for (int k = 0; k < MT * kSteps16; ++k) lds16(qf[k], q_smem + (k * 32 + lane) * 16);
+      for (int k = 0; k < NT * kSteps16; ++k) load_q(k / kSteps16, k % kSteps16, qf[k]);
     }
-    float fq[MT][2];
-    int32_t end[MT][2], begin[MT][2];
+    // this lane's rows: 8 t + 2 c + e
+    float fq[NT][2];
+    int32_t end[NT][2], begin[NT][2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = 16 * m + 8 * e + g;
-        fq[m][e] = s_fq[r];
-        end[m][e] = s_end[r];
-        begin[m][e] = s_begin[r];
+        const int r = 8 * t + 2 * c + e;
+        fq[t][e] = s_fq[r];
+        end[t][e] = s_end[r];
+        begin[t][e] = s_begin[r];
       }
     // what every row sees (their positions do not decrease)
     const int32_t all_end = s_end[0], all_begin = s_begin[s.rows - 1], len = s.w.sp.len;
 
-    float o[MT][kCols][4], mx[MT][2], sum[MT][2];
+    float o[NT][kTiles][4], mx[NT][2], sum[NT][2];
     float unit = 0x1p-100f;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      mx[m][0] = mx[m][1] = kNone;
-      sum[m][0] = sum[m][1] = 0.0f;
+    for (int t = 0; t < NT; ++t) {
+      mx[t][0] = mx[t][1] = kNone;
+      sum[t][0] = sum[t][1] = 0.0f;
 #pragma unroll
-      for (int j = 0; j < kCols; ++j)
+      for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[m][j][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) o[t][j][e] = 0.0f;
     }
     const int32_t count = s.t1 - s.t0;
-    const int32_t w0 = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * warp / kFewAttWarps);
-    const int32_t w1 = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * (warp + 1) / kFewAttWarps);
-    for (int32_t t = w0; t < w1; ++t) {
-      if (!failed) failed = !__all_sync(kFull, mbar_wait(smem_addr(&s_full[warp][stage]), phase, kFewWaitNs));
+    const int32_t w0 = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * warp / kWarps);
+    const int32_t w1 = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * (warp + 1) / kWarps);
+    for (int32_t st = w0; st < w1; ++st) {
+      failed = !__all_sync(kFull, mbar_wait(smem_addr(&s_full[warp][stage]), phase, kFewWaitNs)) || failed;
       if (failed) break;
       const uint32_t from = ring + stage * Z::kStage;
-      const float ks = s_scale[warp][stage][0], vs = s_scale[warp][stage][1];
-      const bool has = s_scale[warp][stage][2] != 0.0f;
-      const int32_t p = (s.w.step0 + t) * kTile;
+      const int32_t has = s_has[warp][stage];
+      const float4 scales = *reinterpret_cast<const float4*>(s_scale[warp][stage]);
+      const float ks[2] = {scales.x, scales.z}, vs[2] = {scales.y, scales.w};
+      const int64_t p64 = (static_cast<int64_t>(s.w.step0) + st) * kStep;
+      const int32_t p = static_cast<int32_t>(p64);
       if (has) {
-        float x[MT][2][4] = {};
+        // ---- x^T = K q^T ------------------------------------------------------------------------
+        float x[NT][kHalves][4] = {};
 #pragma unroll
         for (int h = 0; h < DP / 64; ++h) {
-          uint32_t k0[4], k1[4];
-          if constexpr (DP == 64) {  // 64-byte rows: 16-byte piece i of row r lies at i ^ (r / 2 % 4)
-            lds16(k0, from + g * 64 + ((c ^ ((g >> 1) & 3)) << 4));
-            lds16(k1, from + (g + 8) * 64 + ((c ^ ((g >> 1) & 3)) << 4));
-          } else {                   // 128-byte rows: at i ^ (r % 8)
-            const uint32_t at = from + (h >> 1) * kSlab + g * 128 + (((4 * (h & 1) + c) ^ g) << 4);
-            lds16(k0, at);
-            lds16(k1, at + 8 * 128);
+          uint32_t k0[kHalves][4], k1[kHalves][4];
+#pragma unroll
+          for (int i = 0; i < kHalves; ++i) {
+            if constexpr (DP == 64) {  // 64-byte rows: 16-byte piece i of row r lies at i ^ (r / 2 % 4)
+              const uint32_t at = from + i * 1024 + g * 64 + ((c ^ ((g >> 1) & 3)) << 4);
+              lds16(k0[i], at);
+              lds16(k1[i], at + 8 * 64);
+            } else {                   // 128-byte rows: at i ^ (r % 8)
+              const uint32_t at = from + (h >> 1) * kSlab + i * 2048 + g * 128 + (((4 * (h & 1) + c) ^ g) << 4);
+              lds16(k0[i], at);
+              lds16(k1[i], at + 8 * 128);
+            }
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t y0 = prepare_word<FMT>(k0[i]), y1 = prepare_word<FMT>(k1[i]);
-            const uint32_t b00 = pair_in_word<FMT, 0>(y0), b01 = pair_in_word<FMT, 1>(y0);
-            const uint32_t b10 = pair_in_word<FMT, 0>(y1), b11 = pair_in_word<FMT, 1>(y1);
+          for (int k = 0; k < 4; ++k) {
+            uint32_t qb[NT][2];
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              uint32_t qa[4];
-              if constexpr (!kHeld) lds16(qa, q_smem + ((m * kSteps16 + 4 * h + i) * 32 + lane) * 16);
-              const uint32_t(&qq)[4] = kHeld ? qf[kHeld ? m * kSteps16 + 4 * h + i : 0] : qa;
-              mma16816(x[m][0], qq, b00, b01);
-              mma16816(x[m][1], qq, b10, b11);
+            for (int t = 0; t < NT; ++t) {
+              if constexpr (kHeld) qb[t][0] = qf[t * kSteps16 + 4 * h + k][0], qb[t][1] = qf[t * kSteps16 + 4 * h + k][1];
+              else load_q(t, 4 * h + k, qb[t]);
+            }
+#pragma unroll
+            for (int i = 0; i < kHalves; ++i) {
+              const uint32_t y0 = prepare_word<FMT>(k0[i][k]), y1 = prepare_word<FMT>(k1[i][k]);
+              const uint32_t ka[4] = {pair_in_word<FMT, 0>(y0), pair_in_word<FMT, 0>(y1), pair_in_word<FMT, 1>(y0), pair_in_word<FMT, 1>(y1)};
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma16816(x[t][i], ka, qb[t][0], qb[t][1]);
             }
           }
         }
-        const bool whole = p + kTile <= all_end && p >= all_begin;
+        // ---- softmax: value 2 z + e of half i is token 16 i + 8 z + g, row 8 t + 2 c + e ------------
+        const bool whole = p64 + kStep <= all_end && p >= all_begin && has == (1 << kHalves) - 1;
         bool moved = false;
-        float was[MT][2];
+        float was[NT][2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {  // row 16 m + 8 e + g, tokens 8 n + 2 c + i
-            const float f = fq[m][e] * ks;
+          for (int e = 0; e < 2; ++e) {
             float top = kNone;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[m][q >> 1][2 * e + (q & 1)] *= f;
-            if (!whole) {
+            for (int i = 0; i < kHalves; ++i) {
+              const float f = fq[t][e] * ks[i];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int32_t j = p + 8 * (q >> 1) + 2 * c + (q & 1);
-                if (j >= end[m][e] || j < begin[m][e]) x[m][q >> 1][2 * e + (q & 1)] = kNone;
+              for (int z = 0; z < 2; ++z) {
+                float& v = x[t][i][2 * z + e];
+                v *= f;
+                if (!whole) {
+                  const int64_t j = p64 + 16 * i + 8 * z + g;
+                  if (j >= end[t][e] || j < begin[t][e] || !((has >> i) & 1)) v = kNone;
+                }
+                top = fmaxf(top, v);
               }
             }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) top = fmaxf(top, x[m][q >> 1][2 * e + (q & 1)]);
-            top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
-            was[m][e] = mx[m][e];
-            if (top > mx[m][e]) {
-              mx[m][e] = top;
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 16));
+            was[t][e] = mx[t][e];
+            if (top > mx[t][e]) {
+              mx[t][e] = top;
               moved = true;
             }
           }
-        const float vmag = fabsf(vs), unit_was = unit;
-        if (vmag > unit && is_finite_f(vmag)) {  // the next power of two above it
-          unit = __uint_as_float((__float_as_uint(fminf(vmag, 0x1p125f)) & 0x7f800000u) + 0x00800000u);
-          moved = true;
+        const float unit_was = unit;
+#pragma unroll
+        for (int i = 0; i < kHalves; ++i) {
+          const float vmag = fabsf(vs[i]);
+          if (((has >> i) & 1) && vmag > unit && is_finite_f(vmag)) {  // the next power of two above it
+            unit = __uint_as_float((__float_as_uint(fminf(vmag, 0x1p125f)) & 0x7f800000u) + 0x00800000u);
+            moved = true;
+          }
         }
         if (__any_sync(kFull, moved)) {
           const float shrink = unit_was / unit;
 #pragma unroll
-          for (int m = 0; m < MT; ++m)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float f = mx[m][e] == kNone ? 1.0f : ex2(was[m][e] - mx[m][e]), fo = f * shrink;
-              sum[m][e] *= f;
+              const float f = mx[t][e] == kNone ? 1.0f : ex2(was[t][e] - mx[t][e]), fo = f * shrink;
+              sum[t][e] *= f;
 #pragma unroll
-              for (int j = 0; j < kCols; ++j) {
-                o[m][j][2 * e] *= fo;
-                o[m][j][2 * e + 1] *= fo;
+              for (int j = 0; j < kTiles; ++j) {
+                o[t][j][e] *= fo;
+                o[t][j][2 + e] *= fo;
               }
             }
         }
-        const float fv = vs * (0x1p15f / unit);
-        uint32_t pa[MT][4];
+        const float inverse = 0x1p15f / unit;
+        uint32_t pb[NT][kHalves][2];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int t = 0; t < NT; ++t) {
+          float y[kHalves][4];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float top = mx[m][e] == kNone ? 0.0f : mx[m][e];
+            const float top = mx[t][e] == kNone ? 0.0f : mx[t][e];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              float y[2];
+            for (int i = 0; i < kHalves; ++i)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const float v = x[m][q][2 * e + i], w = ex2(v - top);
-                sum[m][e] += w;
-                y[i] = w * fv;
-                if (!whole && v == kNone) y[i] = 0.0f;  // (the scale of what is not seen may be anything)
+              for (int z = 0; z < 2; ++z) {
+                const float v = x[t][i][2 * z + e], w = ex2(v - top);
+                sum[t][e] += w;
+                y[i][2 * z + e] = w * (vs[i] * inverse);
+                if (!whole && v == kNone) y[i][2 * z + e] = 0.0f;  // (the scale of what is not seen may be anything)
               }
-              pa[m][2 * q + e] = f16x2_bits(y[0], y[1]);
-            }
           }
 #pragma unroll
-        for (int h = 0; h < kPieces; ++h) {
-          constexpr int kWords = kVBytes / 4;
-          uint32_t vw[4][4];
+          for (int i = 0; i < kHalves; ++i)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 2 * c + (i & 1) + 8 * (i >> 1);
-            if constexpr (DP == 64) {
-              const uint32_t at = from + kTile * DP + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8;
-              asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(vw[i][0]), "=r"(vw[i][1]) : "r"(at));
-            } else {  // DP = 256: pieces 2 g and 2 g + 1 of 16, eight a box
-              const int piece = DP == 128 ? g : 2 * g + h;
-              lds16(vw[i], from + kTile * DP + (piece >> 3) * kSlab + r * 128 + (((piece & 7) ^ (r & 7)) << 4));
-            }
-            if (!whole && p + r >= len) vw[i][0] = vw[i][1] = vw[i][2] = vw[i][3] = 0u;  // memory past the end may hold anything
-          }
-#pragma unroll
-          for (int q = 0; q < kWords; ++q) {
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const uint32_t b0 = pair_of_words_at<FMT>(vw[0][q], vw[1][q], b), b1 = pair_of_words_at<FMT>(vw[2][q], vw[3][q], b);
-#pragma unroll
-              for (int m = 0; m < MT; ++m) mma16816(o[m][16 * h + 4 * q + b], pa[m], b0, b1);
-            }
-          }
+            for (int z = 0; z < 2; ++z) pb[t][i][z] = transposed(f16x2_bits(y[i][2 * z], y[i][2 * z + 1]));
         }
+        // ---- out^T += V^T p^T ---------------------------------------------------------------------
+#pragma unroll
+        for (int i = 0; i < kHalves; ++i)
+#pragma unroll
+          for (int h = 0; h < kPieces; ++h) {
+            uint32_t vw[4][4];
+            const uint32_t vfrom = from + kHalves * Z::kHalf + i * (16 * kRowBytes);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int r = 2 * c + (k & 1) + 8 * (k >> 1);
+              if constexpr (DP == 64) {
+                const uint32_t at = vfrom + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8;
+                asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(vw[k][0]), "=r"(vw[k][1]) : "r"(at));
+              } else {  // DP = 256: pieces 2 g and 2 g + 1 of 16, eight a box
+                const int piece = DP == 128 ? g : 2 * g + h;
+                lds16(vw[k], vfrom + (piece >> 3) * kSlab + r * 128 + (((piece & 7) ^ (r & 7)) << 4));
+              }
+              // memory past the end, or of a page that is not there, may hold anything
+              if (!whole && (p64 + 16 * i + r >= len || !((has >> i) & 1))) vw[k][0] = vw[k][1] = vw[k][2] = vw[k][3] = 0u;
+            }
+#pragma unroll
+            for (int j = 0; j < kTiles / kPieces; ++j) {
+              const int q = j >> 1, b = 2 * (j & 1);
+              const uint32_t va[4] = {pair_of_words_at<FMT>(vw[0][q], vw[1][q], b), pair_of_words_at<FMT>(vw[0][q], vw[1][q], b + 1),
+                                      pair_of_words_at<FMT>(vw[2][q], vw[3][q], b), pair_of_words_at<FMT>(vw[2][q], vw[3][q], b + 1)};
+#pragma unroll
+              for (int t = 0; t < NT; ++t) mma16816(o[t][8 * h + j], va, pb[t][i][0], pb[t][i][1]);
+            }
+          }
       }
       __syncwarp();  // every lane has read the stage
       copy();
@@ -570,7 +630,7 @@ __global__ void __launch_bounds__(kFewAttThreads, 1)
     }
     if (failed) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) sum[m][0] = sum[m][1] = __uint_as_float(0x7fc00000u);
+      for (int t = 0; t < NT; ++t) sum[t][0] = sum[t][1] = __uint_as_float(0x7fc00000u);
     }
     more = advance();
     if (more && !failed) {  // the next segment's first steps are on their way while the sums are joined
@@ -581,14 +641,14 @@ __global__ void __launch_bounds__(kFewAttThreads, 1)
 
     // ---- the warps' sums, four columns of each of the eight column groups at a time ----------------
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        sum[m][e] += __shfl_xor_sync(kFull, sum[m][e], 1);
-        sum[m][e] += __shfl_xor_sync(kFull, sum[m][e], 2);
-        if (c == 0) {
-          s_m[warp][16 * m + 8 * e + g] = mx[m][e];
-          s_l[warp][16 * m + 8 * e + g] = sum[m][e];
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) sum[t][e] += __shfl_xor_sync(kFull, sum[t][e], w);
+        if (g == 0) {
+          s_m[warp][8 * t + 2 * c + e] = mx[t][e];
+          s_l[warp][8 * t + 2 * c + e] = sum[t][e];
         }
       }
     if (lane == 0) s_unit[warp] = unit;
@@ -597,24 +657,22 @@ __global__ void __launch_bounds__(kFewAttThreads, 1)
 #pragma unroll
     for (int q = 0; q < kCols / 4; ++q) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 16 * m + 8 * (e >> 1) + g, col = 2 * c + (e & 1);
-          *reinterpret_cast<float4*>(join + ((warp * kRows + r) * 8 + col) * 4) =
-              make_float4(o[m][4 * q][e], o[m][4 * q + 1][e], o[m][4 * q + 2][e], o[m][4 * q + 3][e]);
-        }
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float4*>(join + ((warp * kRows + 8 * t + 2 * c + e) * 8 + g) * 4) =
+              make_float4(o[t][2 * q][e], o[t][2 * q][2 + e], o[t][2 * q + 1][e], o[t][2 * q + 1][2 + e]);
       __syncthreads();
-      for (int i = tid; i < kRows * 8; i += kFewAttThreads) {
+      for (int i = tid; i < kRows * 8; i += Z::kThreads) {
         const int r = i >> 3, d = kCols * (i & 7) + 4 * q;
         if (r >= s.rows) break;
         float top = kNone, l = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kFewAttWarps; ++k) top = fmaxf(top, s_m[k][r]);
+        for (int k = 0; k < kWarps; ++k) top = fmaxf(top, s_m[k][r]);
         const float from = top == kNone ? 0.0f : top;
         float v[4] = {};
 #pragma unroll
-        for (int k = 0; k < kFewAttWarps; ++k) {
+        for (int k = 0; k < kWarps; ++k) {
           const float f = ex2(s_m[k][r] - from), fo = f * s_unit[k] * 0x1p-15f;
           const float4 y = *reinterpret_cast<const float4*>(join + ((k * kRows + r) * 8 + (i & 7)) * 4);
           l = __fmaf_rn(s_l[k][r], f, l);
@@ -655,9 +713,9 @@ __global__ void __launch_bounds__(kFewAttThreads, 1)
 
 // Joins the partial results of the items that more than one share holds: CTA (i, y) the y-th part of the
 // rows of the item that begins in share i.
-template <int DP, int MT>
+template <int DP, int NT>
 __global__ void __launch_bounds__(128) attention_join_kernel(const AttentionArgs a, int grid) {
-  using Z = FewSizes<DP, MT>;
+  using Z = FewSizes<DP, NT>;
   constexpr int kRows = Z::kRows;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const FewMeta meta = static_cast<const FewMeta*>(a.ws)[blockIdx.x];
@@ -695,25 +753,25 @@ inline bool encode_codes(CUtensorMap* m, const AttentionArgs& a, const void* cod
   const bool narrow = a.c.dim <= 64;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.c.dim), static_cast<cuuint64_t>(a.c.page), static_cast<cuuint64_t>(a.c.pages * a.c.heads)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.c.dim), static_cast<cuuint64_t>(a.c.page) * a.c.dim};
-  const cuuint32_t box[3] = {narrow ? 64u : 128u, kTile, 1}, es[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {narrow ? 64u : 128u, 16, 1}, es[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
              narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-template <int FMT, int DP, int MT>
+template <int FMT, int DP, int NT>
 qz_status run_few(const AttentionArgs& a, const FewPlan& p, cudaStream_t s) {
-  using Z = FewSizes<DP, MT>;
+  using Z = FewSizes<DP, NT>;
   CacheMaps maps{};
   if (a.c.pages > 0 && (!encode_codes(&maps.k, a, a.c.k) || !encode_codes(&maps.v, a, a.c.v))) return QZ_ERR_CUDA;
   if (p.whole) {
-    const auto k = &attention_few_kernel<FMT, DP, MT, true>;
+    const auto k = &attention_few_kernel<FMT, DP, NT, true>;
     if (!set_dyn_smem(reinterpret_cast<const void*>(k), Z::kSmem)) return QZ_ERR_CUDA;
-    k<<<static_cast<unsigned>(p.grid), kFewAttThreads, Z::kSmem, s>>>(a, maps, p.grid, p.min_chunk);
+    k<<<static_cast<unsigned>(p.grid), Z::kThreads, Z::kSmem, s>>>(a, maps, p.grid, p.min_chunk);
     return launch_status();
   }
-  const auto k = &attention_few_kernel<FMT, DP, MT, false>;
+  const auto k = &attention_few_kernel<FMT, DP, NT, false>;
   if (!set_dyn_smem(reinterpret_cast<const void*>(k), Z::kSmem)) return QZ_ERR_CUDA;
-  k<<<static_cast<unsigned>(p.grid), kFewAttThreads, Z::kSmem, s>>>(a, maps, p.grid, p.min_chunk);
+  k<<<static_cast<unsigned>(p.grid), Z::kThreads, Z::kSmem, s>>>(a, maps, p.grid, p.min_chunk);
   if (launch_status() != QZ_OK) return QZ_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute at[1];
@@ -724,7 +782,7 @@ qz_status run_few(const AttentionArgs& a, const FewPlan& p, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attention_join_kernel<DP, MT>, a, p.grid) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, attention_join_kernel<DP, NT>, a, p.grid) != cudaSuccess) {
     cudaGetLastError();
     return QZ_ERR_CUDA;
   }
@@ -733,9 +791,9 @@ qz_status run_few(const AttentionArgs& a, const FewPlan& p, cudaStream_t s) {
 template <int FMT>
 qz_status launch_few(const AttentionArgs& a, const FewPlan& p, cudaStream_t s) {
   switch (few_att_dim(a.c.dim)) {
-    case 64: return p.row_tiles == 2 ? run_few<FMT, 64, 2>(a, p, s) : run_few<FMT, 64, 1>(a, p, s);
-    case 128: return p.row_tiles == 2 ? run_few<FMT, 128, 2>(a, p, s) : run_few<FMT, 128, 1>(a, p, s);
-    default: return run_few<FMT, 256, 1>(a, p, s);
+    case 64: return p.row_tiles == 1 ? run_few<FMT, 64, 1>(a, p, s) : p.row_tiles == 2 ? run_few<FMT, 64, 2>(a, p, s) : run_few<FMT, 64, 4>(a, p, s);
+    case 128: return p.row_tiles == 1 ? run_few<FMT, 128, 1>(a, p, s) : p.row_tiles == 2 ? run_few<FMT, 128, 2>(a, p, s) : run_few<FMT, 128, 4>(a, p, s);
+    default: return p.row_tiles == 1 ? run_few<FMT, 256, 1>(a, p, s) : run_few<FMT, 256, 2>(a, p, s);
   }
 }
 
