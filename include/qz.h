@@ -613,10 +613,11 @@ QZ_API qz_status qz_cache_append(const qz_cache* cache, const qz_batch* batch, i
  *            calls that may overlap need one each
  * Rows that belong to no sequence are left as they are.
  * Arithmetic: scores are sums of exact products of q and decoded codes in fp32, the keys' scale applied to
- * the sum; weights p times the values' scale are rounded to 11 bits (f16, relative to the largest in the
- * sequence; below 2^-29 of it gradually fewer) for the product with the decoded codes; sums in fp32, in an
- * unspecified but fixed order: equal inputs give equal results.  A non-finite query makes its own outputs
- * non-finite and no others.  Codes and scales of positions past a sequence's length are not looked at.
+ * the sum; weights p times the values' scale are rounded to 11 bits (f16; from 2^-22 of the sequence's largest
+ * such product on gradually fewer) for the product with the decoded codes; sums in fp32, in an unspecified but
+ * fixed order: equal inputs give equal results.  A non-finite query makes its own outputs non-finite and no
+ * others.  Scales are not negative.  Codes and scales of positions past a sequence's length are not looked at.
+ * Waits inside the kernels are bounded (1 s); should one give up, the outputs it stands for are NaN.
  * Errors: as above; QZ_ERR_WORKSPACE. */
 QZ_API size_t qz_cache_attention_workspace(const qz_cache* cache, int64_t sequences, int64_t tokens, int64_t heads);
 QZ_API qz_status qz_cache_attention(const qz_cache* cache, const qz_batch* batch, const void* q, int64_t ld_q,

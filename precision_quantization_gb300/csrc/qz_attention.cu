@@ -29,13 +29,35 @@ size_t few_att_workspace(const FewPlan& p, int dim) {
   return p.whole ? 0 : static_cast<size_t>(p.grid) * (16 + 2 * slot);
 }
 
+// More than kTcRows rows a sequence and kv head go to the tensor-core tiles.  Tiles that do not fill the GPU are cut
+// along the keys, a part no shorter than kTcPart tokens.
+constexpr int64_t kTcRows = 32, kTcPart = 512;
+
+TcAttPlan tc_att_plan(const qz_cache& c, int64_t seqs, int64_t tokens, int64_t heads, int64_t table_pages, int sms) {
+  TcAttPlan p{};
+  const int64_t group = heads / c.kv_heads, rows = (tokens * group + seqs - 1) / seqs;
+  if (c.dim > 128 || rows <= kTcRows) return p;
+  p.nq = rows > 128 ? 2 : 1;
+  const int64_t slots = tokens * group / (128 * p.nq) + seqs, tiles = c.kv_heads * ((tokens * group + 128 * p.nq - 1) / (128 * p.nq));
+  const int64_t most = std::max<int64_t>(table_pages * c.page / kTcPart, 1);
+  const int64_t splits = std::max<int64_t>(std::min<int64_t>(sms / std::max<int64_t>(tiles, 1), most), 1);
+  const int64_t grid = slots * c.kv_heads * splits;
+  if (grid > INT32_MAX || tokens * heads > INT32_MAX) return p;
+  p.splits = static_cast<int>(splits), p.slots = static_cast<int>(slots), p.grid = static_cast<int>(grid);
+  return p;
+}
+
 }  // namespace qz
 
 using namespace qz;
 
 extern "C" size_t qz_cache_attention_workspace(const qz_cache* cache, int64_t sequences, int64_t tokens, int64_t heads) {
   if (check_cache(cache) != QZ_OK || sequences <= 0 || tokens <= 0 || heads <= 0) return 0;
-  return few_att_workspace(few_att_plan(*cache, sequences, tokens, heads, INT32_MAX, sm_count()), cache->dim);
+  if (heads % cache->kv_heads || tokens > (1 << 30) || heads > INT32_MAX / cache->dim || sequences > (1 << 24)) return 0;
+  const int sms = sm_count();
+  const TcAttPlan tc = tc_att_plan(*cache, sequences, tokens, heads, INT32_MAX, sms);
+  if (tc.grid) return std::max<size_t>(tc_att_workspace(tc, tokens, heads, cache->dim), 16);
+  return few_att_workspace(few_att_plan(*cache, sequences, tokens, heads, INT32_MAX, sms), cache->dim);
 }
 
 extern "C" qz_status qz_cache_attention(const qz_cache* cache, const qz_batch* batch, const void* q, int64_t ld_q, int64_t hd_q,
@@ -52,7 +74,6 @@ extern "C" qz_status qz_cache_attention(const qz_cache* cache, const qz_batch* b
   if (tokens == 0 || heads == 0 || batch->sequences == 0) return QZ_OK;
   if (!q || !out) return QZ_ERR_NULL;
   if (!is_aligned(q, 2) || !is_aligned(out, 2) || !is_aligned(lse, 4)) return QZ_ERR_ALIGN;
-  const FewPlan plan = few_att_plan(*cache, batch->sequences, tokens, heads, batch->table_pages, sm_count());
   if (!ws || ws_bytes < qz_cache_attention_workspace(cache, batch->sequences, tokens, heads)) return QZ_ERR_WORKSPACE;
   if (!is_aligned(ws, 16)) return QZ_ERR_ALIGN;
   AttentionArgs a{};
@@ -69,6 +90,14 @@ extern "C" qz_status qz_cache_attention(const qz_cache* cache, const qz_batch* b
   a.q_vec = pieces(q, ld_q, hd_q), a.out_vec = pieces(out, ld_out, hd_out);
   a.ws = ws;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int sms = sm_count();
+  const TcAttPlan tc = tc_att_plan(*cache, batch->sequences, tokens, heads, batch->table_pages, sms);
+  if (tc.grid) {
+    if (cache->format == QZ_INT8) return launch_attention_tc_int8(a, tc, s);
+    if (cache->format == QZ_FP8_E4M3) return launch_attention_tc_e4m3(a, tc, s);
+    return launch_attention_tc_e5m2(a, tc, s);
+  }
+  const FewPlan plan = few_att_plan(*cache, batch->sequences, tokens, heads, batch->table_pages, sms);
   if (cache->format == QZ_INT8) return launch_attention_few_int8(a, plan, s);
   if (cache->format == QZ_FP8_E4M3) return launch_attention_few_e4m3(a, plan, s);
   return launch_attention_few_e5m2(a, plan, s);

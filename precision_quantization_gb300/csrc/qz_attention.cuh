@@ -1,0 +1,106 @@
+// qz_attention.cuh -- what the attention kernels share on the device: 8-bit codes to f16 pairs, a row of q
+// made f16, and the store of a finished row.
+#pragma once
+
+#include "qz_attention.h"
+#include "qz_device.cuh"
+#include "qz_pipe.cuh"
+#include "qz_weight.cuh"
+
+namespace qz {
+namespace {
+
+constexpr float kNone = -__builtin_inff();
+// ---- one 8-bit pair to f16 ----------------------------------------------------------------------
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t d;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
+  return d;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// INT8 words have their sign bits flipped first (bias 128): 0x6400 | n is 1024 + n.
+template <int FMT>
+__device__ __forceinline__ uint32_t prepare_word(uint32_t w) {
+  return FMT == QZ_INT8 ? w ^ 0x80808080u : w;
+}
+// bytes 2 i and 2 i + 1 of a prepared word
+template <int FMT, int I>
+__device__ __forceinline__ uint32_t pair_in_word(uint32_t w) {
+  if constexpr (FMT == QZ_INT8) return sub_f16x2(prmt(w, 0x64646464u, I ? 0x4342u : 0x4140u), 0x64806480u);
+  else if constexpr (FMT == QZ_FP8_E5M2) return prmt(w, 0u, I ? 0x3424u : 0x1404u);
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(I ? w >> 16 : w)));
+  return h;
+}
+// byte J of two words
+template <int FMT, int J>
+__device__ __forceinline__ uint32_t pair_of_words(uint32_t a, uint32_t b) {
+  if constexpr (FMT == QZ_INT8) {
+    const uint32_t t = prmt(a, b, J | ((4 + J) << 8) | (J << 4) | ((4 + J) << 12));  // (a, a, b, b)
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(t), "r"(0x00FF00FFu), "r"(0x64806480u));  // (t & m) ^ c
+    return sub_f16x2(d, 0x64806480u);
+  } else if constexpr (FMT == QZ_FP8_E5M2) {
+    return prmt(a, b, J | (J << 4) | ((4 + J) << 8) | ((4 + J) << 12)) & 0xFF00FF00u;
+  }
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(prmt(a, b, J | ((4 + J) << 4)))));
+  return h;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t pair_of_words_at(uint32_t a, uint32_t b, int j) {
+  return j == 0 ? pair_of_words<FMT, 0>(a, b) : j == 1 ? pair_of_words<FMT, 1>(a, b) : j == 2 ? pair_of_words<FMT, 2>(a, b) : pair_of_words<FMT, 3>(a, b);
+}
+
+// 4 elements of q at element offset `at` (zeros where !in)
+__device__ __forceinline__ void load_q4(const AttentionArgs& a, bool in, int64_t at, float (&x)[4]) {
+  x[0] = x[1] = x[2] = x[3] = 0.0f;
+  if (!in) return;
+  if (a.q_vec) {
+    const uint2 b = __ldg(reinterpret_cast<const uint2*>(a.q + at));
+    x[0] = __uint_as_float(b.x << 16), x[1] = __uint_as_float(b.x & 0xffff0000u);
+    x[2] = __uint_as_float(b.y << 16), x[3] = __uint_as_float(b.y & 0xffff0000u);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = bf16_float(__ldg(a.q + at + e));
+  }
+}
+// The power of two that brings a row whose largest magnitude is `top` into [2^14, 2^15), and its inverse;
+// elements 2^-38 of the largest and less lose bits, 2^-40 of it at most.  NaN for a row that is not finite.
+__device__ __forceinline__ float q_unit(float top, float& down) {
+  const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
+  down = __uint_as_float(static_cast<uint32_t>(127 - 14 + min(e, 127)) << 23);
+  return is_finite_f(top) ? __uint_as_float(static_cast<uint32_t>(127 + 14 - min(e, 127)) << 23) : __uint_as_float(0x7fc00000u);
+}
+// 4 finished sums of a row, elements d .. d + 3: l and the sums relative to 2^top
+__device__ __forceinline__ void store_row(const AttentionArgs& a, int64_t token, int head, int d, const float (&v)[4], float top, float l) {
+  if (a.lse && d == 0) a.lse[token * a.ld_lse + head] = l == 0.0f ? kNone : (top + log2f(l)) * 0.69314718055994531f;
+  if (d >= a.c.dim) return;
+  const float r = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+  uint16_t* p = a.out + token * a.ld_out + head * a.hd_out + d;
+  const uint32_t lo = bf16x2_bits(v[0] * r, v[1] * r), hi = bf16x2_bits(v[2] * r, v[3] * r);
+  if (a.out_vec) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+  } else {
+    p[0] = static_cast<uint16_t>(lo), p[1] = static_cast<uint16_t>(lo >> 16);
+    p[2] = static_cast<uint16_t>(hi), p[3] = static_cast<uint16_t>(hi >> 16);
+  }
+}
+
+}  // namespace
+}  // namespace qz

@@ -48,4 +48,20 @@ qz_status launch_attention_few_int8(const AttentionArgs& a, const FewPlan& p, cu
 qz_status launch_attention_few_e4m3(const AttentionArgs& a, const FewPlan& p, cudaStream_t s);
 qz_status launch_attention_few_e5m2(const AttentionArgs& a, const FewPlan& p, cudaStream_t s);
 
+// ---- many rows (qz_attention_tc.cuh) -------------------------------------------------------------
+struct TcAttPlan {
+  int nq;       // row tiles of 128 of a CTA
+  int splits;   // parts of the keys
+  int slots;    // places for a kv head's CTAs
+  int grid;     // 0: not applicable
+};
+TcAttPlan tc_att_plan(const qz_cache& c, int64_t seqs, int64_t tokens, int64_t heads, int64_t table_pages, int sms);
+inline size_t tc_att_workspace(const TcAttPlan& p, int64_t tokens, int64_t heads, int dim) {
+  return p.splits > 1 ? static_cast<size_t>(p.splits) * tokens * heads * (dim + 2) * sizeof(float) : 0;
+}
+
+qz_status launch_attention_tc_int8(const AttentionArgs& a, const TcAttPlan& p, cudaStream_t s);
+qz_status launch_attention_tc_e4m3(const AttentionArgs& a, const TcAttPlan& p, cudaStream_t s);
+qz_status launch_attention_tc_e5m2(const AttentionArgs& a, const TcAttPlan& p, cudaStream_t s);
+
 }  // namespace qz

@@ -1,0 +1,569 @@
+// qz_attention_tc.cuh -- attention of many rows to the 8-bit cache (prompts) on the tcgen05 tensor cores,
+// included once per format.  Heads of up to 128 elements.
+//
+//   x_j = (scale log2 e) ks_j (q . k_j),  p_j = 2^(x_j - m),  l = sum p_j,  out = sum p_j vs_j v_j / l
+//
+// A CTA holds two tiles of 128 rows (one where the sequences have fewer) of one sequence and kv head and
+// walks the keys in tiles of 128 tokens.  Bound by the tensor cores and the exponentials together, so that
+// each warp has one thing to do and two row tiles take turns on both:
+//   warps 0-7    softmax, one row of a tile a thread: x from tensor memory, p back into its place as f16
+//   warps 8-15   decode: 16-byte pieces of codes, loaded a tile ahead into registers, become f16 in shared
+//                memory in the layout that the MMA reads (keys K-major, values MN-major: the same bytes)
+//   warp 16      issues the MMAs: x = Q K^T into 128 columns of tensor memory, out += P V with P as the
+//                A operand from there
+// in the order P0 V(j - 1), Q0 K(j), P1 V(j - 1), Q1 K(j): while one tile's softmax runs, the tensor cores work
+// for the other.
+// 8-bit codes are exact in f16, q is made f16 by a power of two of its row.  The maximum m is moved only
+// when it is exceeded by more than 2^4, and the unit of the weights p vs (a power of two >= vs) by factors
+// of four, so that the sums in tensor memory are rarely rescaled; p vs 2^11 / unit stays within f16, and keeps its
+// 11 bits down to 2^-22 of the largest scale.
+// Where the row tiles do not fill the GPU the keys are cut in `splits` parts, whose sums a second kernel joins.
+#pragma once
+
+#include "qz_attention.cuh"
+#include "qz_internal.h"
+#include "qz_tcgen05.cuh"
+
+namespace qz {
+namespace {
+
+constexpr int kAttRows = 128, kAttKeys = 128;
+constexpr int kAttSoftWarps = 8, kAttDecWarps = 8, kAttThreads = 32 * (kAttSoftWarps + kAttDecWarps + 1);
+constexpr uint32_t kAttPanel = 128 * 128;            // 128 rows of 64 f16 values
+constexpr uint32_t kAttTile = 2 * kAttPanel;
+constexpr int kAttStages = 2, kAttScales = 4;
+constexpr uint32_t kAttSmem = (2 + 2 * kAttStages) * kAttTile + 1024;  // q, keys, values
+constexpr float kLazy = 4.0f, kPUnit = 0x1p11f;
+
+struct AttTcArgs {
+  AttentionArgs a;
+  int32_t nq, splits, slots;   // row tiles of a CTA; parts of the keys; places for a kv head's CTAs
+};
+
+// x (f16 pairs, tensor memory) as the A operand
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,"
+      "%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]),
+        "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]),
+        "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]),
+        "=f"(v[31])
+      : "r"(at)
+      : "memory");
+}
+// every load before it has landed; the registers are handed on, so that nothing reads them earlier
+__device__ __forceinline__ void tmem_wait32(float (&v)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]),
+                 "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]),
+                 "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]),
+                 "+f"(v[31])::"memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
+               "r"(v[14]), "r"(v[15])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint64_t add_pairs(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// fp32 accumulator, f16 operands; b_mn: B with its N index contiguous
+__device__ __forceinline__ uint32_t idesc_f16(int n, bool b_mn) {
+  return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kAttRows >> 4) << 24);
+}
+
+struct AttBarriers {
+  uint64_t k_full[kAttStages], k_empty[kAttStages], v_full[kAttStages], v_empty[kAttStages];
+  uint64_t s_full[2], p_full[2], scales[kAttScales], q_full, done;
+};
+struct AttScales {   // of a tile's 16-token groups
+  float ks[8], vs[8];
+  uint32_t has;      // bit i: group i has a page
+};
+
+// The CTA's rows and keys.
+struct AttWork {
+  Span sp;
+  int32_t seq, kvh, row0, rows;  // rows from row0 on, of `rows` in all
+  int32_t t0, t1;                // tiles of keys
+};
+
+// ---- softmax ------------------------------------------------------------------------------------
+// One row of tile q; a warp's 32 lanes of tensor memory.
+__device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& w, AttBarriers& bar, const AttScales* scales, uint32_t smem_q,
+                                             uint32_t tmem, int q, volatile int* abort) {
+  const AttentionArgs& a = p.a;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, r = 32 * warp + lane;
+  const int row = w.row0 + q * kAttRows + r, dim = a.c.dim;
+  const bool mine = row < w.rows;
+  const int i = row / a.group, head = w.kvh * a.group + row % a.group;
+  const int64_t token = w.sp.row + i, pos = w.sp.p0 + i;
+  // q as f16, K-major panels of 64 elements, 128-byte swizzle
+  float fq;
+  {
+    const int64_t at = token * a.ld_q + head * a.hd_q;
+    float top = 0.0f, x[4];
+    for (int d = 0; d < dim; d += 4) {
+      load_q4(a, mine, at + d, x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = absmax_nan(top, x[e]);
+    }
+    float down;
+    const float up = q_unit(top, down);
+    fq = down * a.scale;
+    const uint32_t line = smem_q + q * kAttTile + r * 128;
+    for (int d = 0; d < dim; d += 8) {
+      float y[4];
+      load_q4(a, mine, at + d, x);
+      load_q4(a, mine, at + d + 4, y);
+      const uint32_t v[4] = {f16x2_bits(x[0] * up, x[1] * up), f16x2_bits(x[2] * up, x[3] * up), f16x2_bits(y[0] * up, y[1] * up),
+                             f16x2_bits(y[2] * up, y[3] * up)};
+      sts16(line + (d >> 6) * kAttPanel + ((((d >> 3) & 7) ^ (r & 7)) << 4), v);
+    }
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) arrive_local(smem_addr(&bar.q_full));
+  }
+  const int64_t end = mine ? min(pos + 1, static_cast<int64_t>(w.sp.len)) : static_cast<int64_t>(INT32_MAX);
+  const int64_t begin = mine ? pos + 1 - a.window : 0;
+  int64_t all_end = end, all_begin = begin;  // what every row of the warp sees
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    all_end = min(all_end, __shfl_xor_sync(kFull, all_end, o));
+    all_begin = max(all_begin, __shfl_xor_sync(kFull, all_begin, o));
+  }
+  const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+  const uint32_t ts = tmem + q * kAttKeys + lanes, to = tmem + 2 * kAttKeys + q * kAttRows + lanes;
+  float m = kNone, l = 0.0f, unit = 0x1p-100f;
+  bool ok = true;
+  for (int32_t t = w.t0; t < w.t1; ++t) {
+    const int n = t - w.t0;
+    const AttScales& sc = scales[n % kAttScales];
+    ok = tc_wait(smem_addr(&bar.scales[n % kAttScales]), (n / kAttScales) & 1, abort) && tc_wait(smem_addr(&bar.s_full[q]), n & 1, abort);
+    ok = __all_sync(kFull, ok);
+    if (!ok) break;
+    tc_fence_after();
+    const int64_t j0 = static_cast<int64_t>(t) * kAttKeys;
+    const uint32_t has = sc.has;
+    const bool whole = j0 + kAttKeys <= all_end && j0 >= all_begin && has == 255u;
+    // ---- the maximum ----
+    float top = kNone, v[32];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      tmem_load32(ts + 32 * c, v);
+      tmem_wait32(v);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const float f = fq * sc.ks[2 * c + g];
+        if (whole) {  // (a scale is not negative)
+          float x = v[16 * g];
+#pragma unroll
+          for (int e = 1; e < 15; e += 2) x = max3(x, v[16 * g + e], v[16 * g + e + 1]);
+          top = fmaxf(top, fmaxf(x, v[16 * g + 15]) * f);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int64_t j = j0 + 32 * c + 16 * g + e;
+            if (j < end && j >= begin && ((has >> (2 * c + g)) & 1u)) top = fmaxf(top, v[16 * g + e] * f);
+          }
+        }
+      }
+    }
+    const float was = m, unit_was = unit;
+    if (top > m + kLazy || (m == kNone && top > m)) m = top;
+    float vmax = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      const float x = fabsf(sc.vs[g]);
+      if (((has >> g) & 1u) && is_finite_f(x)) vmax = fmaxf(vmax, x);
+    }
+    if (vmax > unit)  // four times the next power of two
+      unit = __uint_as_float((__float_as_uint(fminf(vmax, 0x1p120f)) & 0x7f800000u) + 3u * 0x00800000u);
+    const bool moved = m != was || unit != unit_was;
+    if (__any_sync(kFull, moved)) {
+      const float f = was == kNone ? 1.0f : ex2(was - m), fo = f * (unit_was / unit);
+      l *= f;
+      if (n > 0) {
+        for (int c = 0; c < dim; c += 16) {
+          float o8[8], o9[8];
+          tmem_load8(to + c, o8);
+          tmem_load8(to + c + 8, o9);
+          tmem_wait8(o8);
+          tmem_wait8(o9);
+          uint32_t y[16];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(o8[e] * fo), y[8 + e] = __float_as_uint(o9[e] * fo);
+          tmem_store16(to + c, y);
+        }
+      }
+    }
+    // ---- the weights ----
+    const float from = m == kNone ? 0.0f : m, inverse = kPUnit / unit;
+    const uint64_t minus = pk(-from, -from);
+    uint64_t sum = pk(0.0f, 0.0f);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      tmem_load32(ts + 32 * c, v);
+      tmem_wait32(v);
+      uint32_t y[16];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const float f = fq * sc.ks[2 * c + g], fv = sc.vs[2 * c + g] * inverse;
+        const uint64_t ff = pk(f, f), ffv = pk(fv, fv);
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float x0, x1;
+            upk(fma2(pk(v[16 * g + 2 * e], v[16 * g + 2 * e + 1]), ff, minus), x0, x1);
+            const uint64_t w2 = pk(ex2(x0), ex2(x1));
+            sum = add_pairs(sum, w2);
+            upk(mul2(w2, ffv), x0, x1);
+            y[8 * g + e] = f16x2_bits(x0, x1);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float x[2];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const int64_t j = j0 + 32 * c + 16 * g + 2 * e + z;
+              const bool seen = j < end && j >= begin && ((has >> (2 * c + g)) & 1u);
+              const float w1 = seen ? ex2(__fmaf_rn(v[16 * g + 2 * e + z], f, -from)) : 0.0f;
+              l += w1;
+              x[z] = seen ? w1 * fv : 0.0f;  // (the scale of what is not seen may be anything)
+            }
+            y[8 * g + e] = f16x2_bits(x[0], x[1]);
+          }
+        }
+      }
+      tmem_store16(ts + 16 * c, y);
+    }
+    float s0, s1;
+    upk(sum, s0, s1);
+    l += s0 + s1;
+    tmem_stored();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) arrive_local(smem_addr(&bar.p_full[q]));
+  }
+  // ---- the result ----
+  if (w.t0 < w.t1) ok = __all_sync(kFull, tc_wait(smem_addr(&bar.done), 0, abort)) && ok && !*abort;
+  tc_fence_after();
+  if (!ok) l = __uint_as_float(0x7fc00000u);
+  const float back = unit * (1.0f / kPUnit);
+  float *part = nullptr, *stat = nullptr;
+  if (p.splits > 1) {
+    const int64_t all = static_cast<int64_t>(a.b.tokens) * a.heads, split = blockIdx.x % p.splits, at = split * all + token * a.heads + head;
+    part = static_cast<float*>(a.ws) + at * dim;
+    stat = static_cast<float*>(a.ws) + p.splits * all * dim + at * 2;
+    if (mine) stat[0] = m, stat[1] = l;
+  }
+  for (int c = 0; c < dim; c += 8) {
+    float o8[8] = {};
+    if (w.t0 < w.t1) tmem_ld8(to + c, o8);
+    if (mine) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float y[4] = {o8[4 * h] * back, o8[4 * h + 1] * back, o8[4 * h + 2] * back, o8[4 * h + 3] * back};
+        if (part) *reinterpret_cast<float4*>(part + c + 4 * h) = make_float4(y[0], y[1], y[2], y[3]);
+        else store_row(a, token, head, c + 4 * h, y, m, l);
+      }
+    }
+  }
+  tc_fence_before();
+}
+
+// ---- decoding -----------------------------------------------------------------------------------
+// 16 codes to f16, at their places in a line of a 64-wide panel (128-byte swizzle)
+template <int FMT>
+__device__ __forceinline__ void decode16(const uint4& codes, uint32_t tile, int row, int ch) {
+  const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint32_t h[8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t y = prepare_word<FMT>(cw[k]);
+    h[2 * k] = pair_in_word<FMT, 0>(y);
+    h[2 * k + 1] = pair_in_word<FMT, 1>(y);
+  }
+  // eight lanes hold one row's pieces, four of either panel: the second panel's store their halves the other way round,
+  // so that they take other banks
+  const bool odd = ch & 4;
+  uint32_t x[4], y[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) x[k] = odd ? h[4 + k] : h[k], y[k] = odd ? h[k] : h[4 + k];
+  const uint32_t line = tile + (ch >> 2) * kAttPanel + row * 128, at = 2 * (ch & 3);
+  sts16(line + (((at + (odd ? 1 : 0)) ^ (row & 7)) << 4), x);
+  sts16(line + (((at + (odd ? 0 : 1)) ^ (row & 7)) << 4), y);
+}
+
+template <int FMT>
+__device__ __forceinline__ void decode_role(const AttTcArgs& p, const AttWork& w, AttBarriers& bar, AttScales* scales, uint32_t smem_k, uint32_t smem_v,
+                                            volatile int* abort) {
+  const AttentionArgs& a = p.a;
+  const int lane = threadIdx.x & 31, id = static_cast<int>(threadIdx.x) - 32 * kAttSoftWarps, dim = a.c.dim, pieces = dim / 16;
+  constexpr int kEach = 4;  // pieces of a thread: 128 rows of up to 8 over 256 threads
+  int row[kEach], ch[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int k = id + 32 * kAttDecWarps * i;
+    row[i] = k / pieces;
+    ch[i] = k - row[i] * pieces;
+  }
+  // lanes 0-7: the 16-token groups of the next tile: byte offset of their codes, -1 where they have no page
+  int64_t group = -1, block = 0;
+  const auto look = [&](int32_t t) {
+    const int64_t j = static_cast<int64_t>(t) * kAttKeys + 16 * (lane & 7);
+    group = -1;
+    if (t < w.t1 && j < w.sp.len) {
+      const int32_t at = static_cast<int32_t>(j) / a.c.page, in = static_cast<int32_t>(j) - at * a.c.page;
+      const int32_t page = __ldg(a.b.table + w.seq * a.b.ld_table + at);
+      if (page >= 0 && page < a.c.pages) {
+        const int64_t head = static_cast<int64_t>(page) * a.c.heads + w.kvh;
+        group = (head * a.c.page + in) * dim;
+        block = head * (a.c.page >> a.c.log2_block) + (in >> a.c.log2_block);
+      }
+    }
+  };
+  uint4 kr[kEach], vr[kEach];
+  float ks = 0.0f, vs = 0.0f;
+  uint32_t has = 0;
+  const auto load = [&](const uint8_t* codes, int64_t from, int32_t t, uint4 (&r)[kEach]) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int64_t at = __shfl_sync(kFull, from, (row[i] >> 4) & 7);
+      r[i] = make_uint4(0u, 0u, 0u, 0u);  // what is past the end, or not there, is 0: it may be anything in memory
+      if (row[i] < kAttKeys && at >= 0 && static_cast<int64_t>(t) * kAttKeys + row[i] < w.sp.len)
+        r[i] = __ldg(reinterpret_cast<const uint4*>(codes + at + (row[i] & 15) * dim + 16 * ch[i]));
+    }
+  };
+  look(w.t0);
+  int64_t now = group;
+  load(a.c.k, now, w.t0, kr);
+  load(a.c.v, now, w.t0, vr);
+  if (group >= 0) ks = __ldg(a.c.ks + block), vs = __ldg(a.c.vs + block);
+  has = __ballot_sync(kFull, group >= 0) & 255u;
+  look(w.t0 + 1);
+  for (int32_t t = w.t0; t < w.t1; ++t) {
+    const int n = t - w.t0, s = n % kAttStages;
+    const uint32_t ph = (n / kAttStages) & 1;
+    if (!__all_sync(kFull, tc_wait(smem_addr(&bar.k_empty[s]), ph ^ 1u, abort))) break;
+    if (id < 32) {  // (tile n - 4's scales are no longer read: the tile before last would not have been finished)
+      AttScales& sc = scales[n % kAttScales];
+      if (lane < 8) sc.ks[lane] = ks, sc.vs[lane] = vs;
+      if (lane == 0) sc.has = has;
+      __syncwarp();
+      if (lane == 0) arrive_local(smem_addr(&bar.scales[n % kAttScales]));
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (row[i] < kAttKeys) decode16<FMT>(kr[i], smem_k + s * kAttTile, row[i], ch[i]);
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) arrive_local(smem_addr(&bar.k_full[s]));
+    now = group;
+    load(a.c.k, now, t + 1, kr);  // (past the last tile: no groups)
+    ks = vs = 0.0f;
+    if (now >= 0) ks = __ldg(a.c.ks + block), vs = __ldg(a.c.vs + block);
+    has = __ballot_sync(kFull, now >= 0) & 255u;
+    if (!__all_sync(kFull, tc_wait(smem_addr(&bar.v_empty[s]), ph ^ 1u, abort))) break;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (row[i] < kAttKeys) decode16<FMT>(vr[i], smem_v + s * kAttTile, row[i], ch[i]);
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) arrive_local(smem_addr(&bar.v_full[s]));
+    load(a.c.v, now, t + 1, vr);
+    look(t + 2);
+  }
+}
+
+// ---- the tensor cores ----------------------------------------------------------------------------
+__device__ __forceinline__ void mma_role(const AttTcArgs& p, const AttWork& w, AttBarriers& bar, uint32_t smem_q, uint32_t smem_k, uint32_t smem_v,
+                                         uint32_t tmem, volatile int* abort) {
+  const int steps = p.a.c.dim / 16;
+  const uint32_t id_s = idesc_f16(kAttKeys, false), id_o = idesc_f16(p.a.c.dim, true);
+  bool ok = tc_wait(smem_addr(&bar.q_full), 0, abort);
+  const auto scores = [&](int q, int s) {
+    const uint64_t qd = desc_sw128(smem_q + q * kAttTile, 16u, 1024u), kd = desc_sw128(smem_k + s * kAttTile, 16u, 1024u);
+    for (int k = 0; k < steps; ++k) {
+      const uint32_t at = (k >> 2) * (kAttPanel >> 4) + 2u * (k & 3);
+      tc_mma<1>(tmem + q * kAttKeys, qd + at, kd + at, id_s, k > 0);
+    }
+    tc_commit<1>(smem_addr(&bar.s_full[q]));
+  };
+  const auto sums = [&](int q, int s, bool first) {
+    const uint64_t vd = desc_sw128(smem_v + s * kAttTile, kAttPanel, 1024u);
+#pragma unroll
+    for (int k = 0; k < kAttKeys / 16; ++k)
+      mma_ts(tmem + 2 * kAttKeys + q * kAttRows, tmem + q * kAttKeys + 8 * k, vd + 128u * k, id_o, !(first && k == 0));
+  };
+  for (int32_t t = w.t0; t <= w.t1 && ok; ++t) {   // scores of tile t, sums of the one before
+    const int n = t - w.t0, s = n % kAttStages, before = (n + kAttStages - 1) % kAttStages;
+    if (t < w.t1 && !(ok = tc_wait(smem_addr(&bar.k_full[s]), (n / kAttStages) & 1, abort))) break;
+    if (n > 0 && !(ok = tc_wait(smem_addr(&bar.v_full[before]), ((n - 1) / kAttStages) & 1, abort))) break;
+    for (int q = 0; q < p.nq && ok; ++q) {
+      if (n > 0) {
+        if (!(ok = tc_wait(smem_addr(&bar.p_full[q]), (n - 1) & 1, abort))) break;
+        tc_fence_after();
+        sums(q, before, n == 1);
+        if (q == p.nq - 1) tc_commit<1>(smem_addr(&bar.v_empty[before]));
+      }
+      tc_fence_after();
+      if (t < w.t1) scores(q, s);
+    }
+    if (ok && t < w.t1) tc_commit<1>(smem_addr(&bar.k_empty[s]));
+  }
+  tc_commit<1>(smem_addr(&bar.done));  // every MMA issued has completed before tensor and shared memory are released
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(kAttThreads, 1) attention_tc_kernel(const __grid_constant__ AttTcArgs p) {
+  extern __shared__ uint8_t att_raw[];
+  __shared__ __align__(8) AttBarriers bar;
+  __shared__ AttScales scales[kAttScales];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int s_abort;
+  const AttentionArgs& a = p.a;
+  const int warp = static_cast<int>(threadIdx.x) >> 5;
+  const uint32_t base = (smem_addr(att_raw) + 1023u) & ~1023u;
+  const uint32_t smem_q = base, smem_k = base + 2 * kAttTile, smem_v = smem_k + kAttStages * kAttTile;
+
+  // the longest work first: the last rows of the last sequences see the most
+  const int64_t at = blockIdx.x / p.splits;
+  const int split = static_cast<int>(blockIdx.x % p.splits);
+  const int64_t slot = p.slots - 1 - at / a.c.heads;
+  AttWork w;
+  w.kvh = static_cast<int32_t>(at % a.c.heads);
+  const int tile_rows = p.nq * kAttRows;
+  // sequence s begins at slot floor(start group / rows) + s: its tiles end before the next one's begin
+  const auto first_slot = [&](int32_t s) { return static_cast<int64_t>(start_of(a.b, s)) * a.group / tile_rows + s; };
+  w.seq = count_upto(a.b.seqs, first_slot, slot) - 1;
+  if (w.seq < 0) return;
+  w.sp = span_of(a.b, w.seq, a.c.page);
+  const int64_t all_rows = static_cast<int64_t>(w.sp.n) * a.group, row0 = (slot - first_slot(w.seq)) * tile_rows;
+  if (row0 >= all_rows) return;
+  w.row0 = static_cast<int32_t>(row0);
+  w.rows = static_cast<int32_t>(all_rows);
+  {
+    const int64_t last = min(row0 + tile_rows, all_rows) - 1;
+    const int64_t lo = max(w.sp.p0 + row0 / a.group + 1 - a.window, static_cast<int64_t>(0));
+    const int64_t hi = min(w.sp.p0 + last / a.group + 1, static_cast<int64_t>(w.sp.len));
+    const int64_t t0 = lo / kAttKeys, count = max((hi + kAttKeys - 1) / kAttKeys - t0, static_cast<int64_t>(0));
+    w.t0 = static_cast<int32_t>(t0 + count * split / p.splits);
+    w.t1 = static_cast<int32_t>(t0 + count * (split + 1) / p.splits);
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kAttStages; ++s) {
+      mbar_init(smem_addr(&bar.k_full[s]), kAttDecWarps);
+      mbar_init(smem_addr(&bar.v_full[s]), kAttDecWarps);
+      mbar_init(smem_addr(&bar.k_empty[s]), 1);
+      mbar_init(smem_addr(&bar.v_empty[s]), 1);
+    }
+    for (int q = 0; q < 2; ++q) {
+      mbar_init(smem_addr(&bar.s_full[q]), 1);
+      mbar_init(smem_addr(&bar.p_full[q]), 4);
+    }
+    for (int s = 0; s < kAttScales; ++s) mbar_init(smem_addr(&bar.scales[s]), 1);
+    mbar_init(smem_addr(&bar.q_full), 4 * p.nq);
+    mbar_init(smem_addr(&bar.done), 1);
+    mbar_init_fence();
+    s_abort = 0;
+  }
+  if (warp == kAttSoftWarps + kAttDecWarps) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)), "r"(512u) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  if (warp < kAttSoftWarps) {
+    if (warp / 4 < p.nq) softmax_role(p, w, bar, scales, smem_q, tmem, warp / 4, &s_abort);
+  } else if (warp < kAttSoftWarps + kAttDecWarps) {
+    decode_role<FMT>(p, w, bar, scales, smem_k, smem_v, &s_abort);
+  } else {
+    if (w.t0 < w.t1 && elect_one()) mma_role(p, w, bar, smem_q, smem_k, smem_v, tmem, &s_abort);
+    __syncwarp();
+    // (after a wait has given up the others may come here before the last MMA has completed)
+    if (w.t0 < w.t1) tc_wait(smem_addr(&bar.done), 0, &s_abort);
+    if (s_abort) mbar_wait(smem_addr(&bar.done), 0, kTcWaitNs);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kAttSoftWarps + kAttDecWarps) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  }
+}
+
+// The parts' sums, four elements a thread.
+__global__ void __launch_bounds__(256) attention_tc_join_kernel(const __grid_constant__ AttTcArgs p) {
+  const AttentionArgs& a = p.a;
+  const int dim = a.c.dim, quads = dim / 4;
+  const int64_t all = static_cast<int64_t>(a.b.tokens) * a.heads;
+  const int64_t first = static_cast<int64_t>(start_of(a.b, 0)) * a.heads, end = static_cast<int64_t>(start_of(a.b, a.b.seqs)) * a.heads;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float* parts = static_cast<const float*>(a.ws);
+  const float2* stats = reinterpret_cast<const float2*>(parts + p.splits * all * dim);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < all * quads; i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t row = i / quads;
+    const int d = 4 * static_cast<int>(i - row * quads);
+    if (row < first || row >= end) continue;  // no sequence's
+    float top = kNone;
+#pragma unroll 4
+    for (int k = 0; k < p.splits; ++k) top = fmaxf(top, stats[k * all + row].x);
+    const float from = top == kNone ? 0.0f : top;
+    float v[4] = {}, l = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < p.splits; ++k) {
+      const float2 st = stats[k * all + row];
+      const float f = ex2(st.x - from);
+      const float4 y = *reinterpret_cast<const float4*>(parts + (k * all + row) * dim + d);
+      l = __fmaf_rn(st.y, f, l);
+      v[0] = __fmaf_rn(y.x, f, v[0]), v[1] = __fmaf_rn(y.y, f, v[1]);
+      v[2] = __fmaf_rn(y.z, f, v[2]), v[3] = __fmaf_rn(y.w, f, v[3]);
+    }
+    store_row(a, row / a.heads, static_cast<int>(row % a.heads), d, v, top, l);
+  }
+}
+
+template <int FMT>
+qz_status launch_tc(const AttentionArgs& a, const TcAttPlan& plan, cudaStream_t s) {
+  AttTcArgs p{};
+  p.a = a;
+  p.nq = plan.nq, p.splits = plan.splits, p.slots = plan.slots;
+  const auto k = &attention_tc_kernel<FMT>;
+  if (!set_dyn_smem(reinterpret_cast<const void*>(k), kAttSmem)) return QZ_ERR_CUDA;
+  k<<<static_cast<unsigned>(plan.grid), kAttThreads, kAttSmem, s>>>(p);
+  if (launch_status() != QZ_OK) return QZ_ERR_CUDA;
+  if (plan.splits == 1) return QZ_OK;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  const int64_t blocks = (static_cast<int64_t>(a.b.tokens) * a.heads * (a.c.dim / 4) + 255) / 256;
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attention_tc_join_kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return QZ_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+}  // namespace
+}  // namespace qz

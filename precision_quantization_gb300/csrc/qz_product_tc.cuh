@@ -46,6 +46,7 @@
 #include "qz_pipe.cuh"
 #include "qz_product.h"
 #include "qz_product_plan.h"
+#include "qz_tcgen05.cuh"
 #include "qz_weight.cuh"
 
 namespace qz {
@@ -55,7 +56,6 @@ constexpr int kBK = 64;             // summands per step: 128 bytes of bf16, one
 constexpr int kDecWarp0 = 4;
 constexpr uint32_t kABytes = kBM * kBK * 2;        // 16 KiB of decoded weights
 constexpr uint32_t kTmemCols = 512;                // two accumulators of 256 columns
-constexpr uint64_t kTcWaitNs = 1000000000ull;      // 1 s: far beyond any step's latency
 constexpr int kMaxBStages = 8, kMaxGroups = 3, kMaxBoxes = 6;
 
 template <int FMT>
@@ -96,137 +96,6 @@ struct TcArgs {
   int tiles_n, tiles, m_base;  // tiles of tokens, in all; the first output of the first
   int slices, slice_boxes;  // Alone: slices of the sum (the cluster), boxes per slice
 };
-
-// ---- PTX ------------------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t map_to_rank(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void arrive_local(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// Arrive on a barrier of another CTA of the cluster (a shared::cluster address).  What it announces
-// is read by the tensor core of this SM, behind a proxy fence, and by no thread of the other CTA,
-// so the default scope does; release.cluster waits for every load in flight (1100 cycles a step).
-__device__ __forceinline__ void arrive_remote(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  if constexpr (CG == 2)
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// completion of every MMA issued so far arrives on `bar`, in both CTAs of a pair
-template <int CG>
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  if constexpr (CG == 2)
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-                 "h"(static_cast<uint16_t>(3))
-                 : "memory");
-  else
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-template <int CG>
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-  if constexpr (CG == 2)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
-        : "memory");
-}
-// 8 consecutive fp32 columns of this thread's tensor-memory lane: the load, and the wait for every
-// load before it, which hands the registers on (so nothing reads them earlier)
-__device__ __forceinline__ void tmem_load8(uint32_t taddr, float (&v)[8]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
-               : "r"(taddr)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_wait8(float (&v)[8]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7])::"memory");
-}
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
-  tmem_load8(taddr, v);
-  tmem_wait8(v);
-}
-__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void sts16(uint32_t addr, const uint32_t (&v)[4]) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
-}
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-
-// Shared-memory matrix descriptor, 128-byte swizzle (byte offsets in 16-byte units, version 1).
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-         (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-// Instruction descriptor: fp32 accumulator, bf16 operands, B K-major, A K-major or MN-major.
-__device__ __forceinline__ uint32_t idesc_of(int m, int n, bool a_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
-         (static_cast<uint32_t>(m >> 4) << 24);
-}
-
-// Bounded wait on phase `parity`.
-__device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (*abort) return false;
-    if (globaltimer_ns() - t0 > kTcWaitNs) {
-      *abort = 1;
-      return false;
-    }
-  }
-  return true;
-}
-// One lane of a converged warp.  The compiler knows that at most one thread passes, and so feeds
-// the uniform operands of tcgen05 and TMA instructions without a loop over the lanes.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
-
-// After a wait has given up: let the copies already issued land before their memory is released.
-// The last one went to the stage before `s`; `ph` is the parity of stage s's next use.
-__device__ __forceinline__ void let_land(uint64_t* full, int s, uint32_t ph, int stages, uint32_t issued) {
-  const uint64_t t0 = globaltimer_ns();
-  for (uint32_t k = 0; k < min(issued, static_cast<uint32_t>(stages)); ++k) {
-    if (--s < 0) {
-      s = stages - 1;
-      ph ^= 1u;
-    }
-    while (!mbar_try_wait(smem_addr(&full[s]), ph) && globaltimer_ns() - t0 < kTcWaitNs) {
-    }
-  }
-}
 
 // ---- decoding -------------------------------------------------------------------------------
 // Byte q of a word as two 4-bit fields at bits 0 and 16 (even and odd nibble); t0 = word &

@@ -129,10 +129,11 @@ def attention(q, cache: Cache, table, lengths, starts, scale, window=0):
     """(out, lse, magnitude, exponent error, floor) in float64: q [tokens, heads, dim] (the values the
     library gets), magnitude = sum p |v|, the bound on the error of a score in units of log (fp32
     tensor-core sums, 34 x 2^-24 of the terms' magnitudes for each 16: one step c + 16 exact products cut
-    to 24 bits and normalised), and what is lost where a weight p x scale is small: as f16 times 2^-15 it
-    is off by 2^-25 2^-15 of the unit, a power of two up to twice the sequence's largest scale of values,
-    so each code of a visible position contributes up to 2^-39 of that scale (and no less than fp32's
-    smallest normal number, 2^-126)."""
+    to 24 bits and normalised), and what is lost where a weight p x scale is small: as f16 times 2^-11 of
+    the unit it is off by 2^-25 2^-11 of the unit, a power of two up to eight times the sequence's largest
+    scale of values, against a p of the largest score of 2^-4 at least (the maximum is followed that far
+    behind), so each code of a visible position contributes up to 2^-29 of that scale (and no less than
+    fp32's smallest normal number, 2^-126)."""
     tokens, heads, dim = q.shape
     group = heads // cache.heads
     out, lse = np.full((tokens, heads, dim), np.nan), np.full((tokens, heads), np.nan)
@@ -164,7 +165,7 @@ def attention(q, cache: Cache, table, lengths, starts, scale, window=0):
                     p = np.exp(x - top)
                     out[row + i, h], lse[row + i, h] = p @ vv / p.sum(), top + np.log(p.sum())
                     mag[row + i, h] = p @ np.abs(vv) / p.sum()
-                    floor[row + i, h] = 2.0 ** -39 * unit[h // group] * QMAX[cache.fmt] * len(vv) / p.sum() + 2.0 ** -126
+                    floor[row + i, h] = 2.0 ** -29 * unit[h // group] * QMAX[cache.fmt] * len(vv) / p.sum() + 2.0 ** -126
                     err[row + i, h] = 34 * -(-dim // 16) * 2.0 ** -24 * scale * (np.abs(kk) @ np.abs(q[row + i, h])).max()
     return out, lse, mag, err, floor
 

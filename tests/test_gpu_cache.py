@@ -241,6 +241,10 @@ ATTEND = [  # lengths, new tokens, page, block, heads, kv, dim, window
     ([5000], [1], 128, 64, 4, 1, 256, 0),
     ([1300, 2100], [9, 4], 16, 16, 8, 2, 128, 0),
     ([1100, 40], [150, 40], 32, 32, 4, 2, 96, 0),
+    ([2600, 0, 900], [300, 0, 257], 64, 64, 8, 1, 128, 0),
+    ([2000], [130], 32, 16, 4, 4, 64, 200),
+    ([700, 1300], [100, 90], 48, 16, 6, 2, 80, 0),
+    ([600], [1000], 64, 64, 2, 2, 16, 0),
 ]
 
 
