@@ -2,8 +2,12 @@
 // made f16, and the store of a finished row.
 #pragma once
 
+#include <cuda.h>  // CUtensorMap and its enumerators (types only; the encoder is looked up)
+#include <cudaTypedefs.h>
+
 #include "qz_attention.h"
 #include "qz_device.cuh"
+#include "qz_internal.h"
 #include "qz_pipe.cuh"
 #include "qz_weight.cuh"
 
@@ -11,6 +15,17 @@ namespace qz {
 namespace {
 
 constexpr float kNone = -__builtin_inff();
+
+struct CacheMaps {
+  CUtensorMap k, v;   // codes as [pages * kv heads][page][dim], boxes of 16 rows or more
+};
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
 // ---- one 8-bit pair to f16 ----------------------------------------------------------------------
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t d;
@@ -100,6 +115,22 @@ __device__ __forceinline__ void store_row(const AttentionArgs& a, int64_t token,
     p[0] = static_cast<uint16_t>(lo), p[1] = static_cast<uint16_t>(lo >> 16);
     p[2] = static_cast<uint16_t>(hi), p[3] = static_cast<uint16_t>(hi >> 16);
   }
+}
+
+// rows of 64 bytes (up to 64 elements) or 128 in the swizzle of that width; past the vector's end zeros
+inline bool encode_codes(CUtensorMap* m, const AttentionArgs& a, const void* codes, int rows) {
+  const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!enc) return false;
+  const bool narrow = a.c.dim <= 64;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.c.dim), static_cast<cuuint64_t>(a.c.page), static_cast<cuuint64_t>(a.c.pages * a.c.heads)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.c.dim), static_cast<cuuint64_t>(a.c.page) * a.c.dim};
+  const cuuint32_t box[3] = {narrow ? 64u : 128u, static_cast<cuuint32_t>(rows), 1}, es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+inline bool encode_maps(CacheMaps* m, const AttentionArgs& a, int rows) {
+  return encode_codes(&m->k, a, a.c.k, rows) && encode_codes(&m->v, a, a.c.v, rows);
 }
 
 }  // namespace

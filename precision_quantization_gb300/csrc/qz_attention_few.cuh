@@ -22,9 +22,6 @@
 // that holds part of an item leaves its sums in the workspace, and the CTAs of the second kernel join them.
 #pragma once
 
-#include <cuda.h>  // CUtensorMap and its enumerators (types only; the encoder is looked up)
-#include <cudaTypedefs.h>
-
 #include "qz_attention.cuh"
 #include "qz_internal.h"
 
@@ -32,10 +29,6 @@ namespace qz {
 namespace {
 
 constexpr uint64_t kFewWaitNs = 1000000000ull;  // 1 s: far beyond any copy's latency
-
-struct CacheMaps {
-  CUtensorMap k, v;   // codes as [pages * kv heads][page][dim], boxes of 16 rows
-};
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -53,12 +46,6 @@ __device__ __forceinline__ uint32_t transposed(uint32_t v) {
 __device__ __forceinline__ void copy_scale(uint32_t dst, const float* src, uint32_t bar) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
 }
 __device__ __forceinline__ void arrive_on(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -652,22 +639,11 @@ __global__ void __launch_bounds__(128) attention_join_kernel(const AttentionArgs
 }
 
 // ---- host side ----------------------------------------------------------------------------------
-inline bool encode_codes(CUtensorMap* m, const AttentionArgs& a, const void* codes) {
-  const auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
-  if (!enc) return false;
-  const bool narrow = a.c.dim <= 64;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.c.dim), static_cast<cuuint64_t>(a.c.page), static_cast<cuuint64_t>(a.c.pages * a.c.heads)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.c.dim), static_cast<cuuint64_t>(a.c.page) * a.c.dim};
-  const cuuint32_t box[3] = {narrow ? 64u : 128u, 16, 1}, es[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 template <int FMT, int DP, int NT>
 qz_status run_few(const AttentionArgs& a, const FewPlan& p, cudaStream_t s) {
   using Z = FewSizes<DP, NT>;
   CacheMaps maps{};
-  if (a.c.pages > 0 && (!encode_codes(&maps.k, a, a.c.k) || !encode_codes(&maps.v, a, a.c.v))) return QZ_ERR_CUDA;
+  if (a.c.pages > 0 && !encode_maps(&maps, a, 16)) return QZ_ERR_CUDA;
   if (p.whole) {
     const auto k = &attention_few_kernel<FMT, DP, NT, true>;
     if (!set_dyn_smem(reinterpret_cast<const void*>(k), Z::kSmem)) return QZ_ERR_CUDA;

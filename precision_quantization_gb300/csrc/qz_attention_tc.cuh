@@ -6,11 +6,13 @@
 // A CTA holds two tiles of 128 rows (one where the sequences have fewer) of one sequence and kv head and
 // walks the keys in tiles of 128 tokens.  Bound by the tensor cores and the exponentials together, so that
 // each warp has one thing to do and two row tiles take turns on both:
-//   warps 0-7    softmax, one row of a tile a thread: x from tensor memory, p back into its place as f16
-//   warps 8-15   decode: 16-byte pieces of codes, loaded a tile ahead into registers, become f16 in shared
-//                memory in the layout that the MMA reads (keys K-major, values MN-major: the same bytes)
+//   warps 0-7    softmax, one row of a tile a thread: x from tensor memory into registers, p back into its
+//                place as f16
+//   warps 8-15   decode: 16-byte pieces of codes become f16 in shared memory in the layout that the MMA
+//                reads (keys K-major, values MN-major: the same bytes)
 //   warp 16      issues the MMAs: x = Q K^T into 128 columns of tensor memory, out += P V with P as the
 //                A operand from there
+//   warp 17      looks up the pages and copies the next tile's codes by TMA
 // in the order P0 V(j - 1), Q0 K(j), P1 V(j - 1), Q1 K(j): while one tile's softmax runs, the tensor cores work
 // for the other.
 // 8-bit codes are exact in f16, q is made f16 by a power of two of its row.  The maximum m is moved only
@@ -28,16 +30,21 @@ namespace qz {
 namespace {
 
 constexpr int kAttRows = 128, kAttKeys = 128;
-constexpr int kAttSoftWarps = 8, kAttDecWarps = 8, kAttThreads = 32 * (kAttSoftWarps + kAttDecWarps + 1);
+constexpr int kAttSoftWarps = 8, kAttDecWarps = 8, kAttThreads = 32 * (kAttSoftWarps + kAttDecWarps + 4);
+// registers a thread: launched with 96, 61440 in all = 256 x 176 + 256 x 40 + 128 x 48
+constexpr int kAttSoftRegs = 176, kAttDecRegs = 40, kAttRestRegs = 48;
 constexpr uint32_t kAttPanel = 128 * 128;            // 128 rows of 64 f16 values
 constexpr uint32_t kAttTile = 2 * kAttPanel;
 constexpr int kAttStages = 2, kAttScales = 4;
-constexpr uint32_t kAttSmem = (2 + 2 * kAttStages) * kAttTile + 1024;  // q, keys, values
+constexpr uint32_t kAttRaw = 128 * 128;              // a tile's codes
+constexpr uint32_t kAttSmem = (2 + 2 * kAttStages) * kAttTile + 2 * kAttRaw + 1024;  // q, keys, values, codes of each
 constexpr float kLazy = 4.0f, kPUnit = 0x1p11f;
 
 struct AttTcArgs {
   AttentionArgs a;
   int32_t nq, splits, slots;   // row tiles of a CTA; parts of the keys; places for a kv head's CTAs
+  int32_t box;                 // tokens of a copy: the largest of 16, 32, 64, 128 that divides a page
+  CacheMaps maps;
 };
 
 // x (f16 pairs, tensor memory) as the A operand
@@ -85,11 +92,13 @@ __device__ __forceinline__ uint32_t idesc_f16(int n, bool b_mn) {
 
 struct AttBarriers {
   uint64_t k_full[kAttStages], k_empty[kAttStages], v_full[kAttStages], v_empty[kAttStages];
+  uint64_t rk_full, rk_empty, rv_full, rv_empty;
   uint64_t s_full[2], p_full[2], scales[kAttScales], q_full, done;
 };
-struct AttScales {   // of a tile's 16-token groups
+struct AttScales {   // of a tile's 16-token groups; 0 for those past the end or without a page
   float ks[8], vs[8];
-  uint32_t has;      // bit i: group i has a page
+  float most;        // the largest finite |vs|
+  uint32_t has;      // bit i: group i is there
 };
 
 // The CTA's rows and keys.
@@ -135,9 +144,9 @@ __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& 
     __syncwarp();
     if (lane == 0) arrive_local(smem_addr(&bar.q_full));
   }
-  const int64_t end = mine ? min(pos + 1, static_cast<int64_t>(w.sp.len)) : static_cast<int64_t>(INT32_MAX);
-  const int64_t begin = mine ? pos + 1 - a.window : 0;
-  int64_t all_end = end, all_begin = begin;  // what every row of the warp sees
+  const int32_t end = mine ? static_cast<int32_t>(max(min(pos + 1, static_cast<int64_t>(w.sp.len)), static_cast<int64_t>(0))) : INT32_MAX;
+  const int32_t begin = mine ? static_cast<int32_t>(max(pos + 1 - a.window, static_cast<int64_t>(0))) : 0;
+  int32_t all_end = end, all_begin = begin;  // what every row of the warp sees
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     all_end = min(all_end, __shfl_xor_sync(kFull, all_end, o));
@@ -154,47 +163,51 @@ __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& 
     ok = __all_sync(kFull, ok);
     if (!ok) break;
     tc_fence_after();
-    const int64_t j0 = static_cast<int64_t>(t) * kAttKeys;
-    const uint32_t has = sc.has;
-    const bool whole = j0 + kAttKeys <= all_end && j0 >= all_begin && has == 255u;
-    // ---- the maximum ----
-    float top = kNone, v[32];
+    float v[4][32];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      tmem_load32(ts + 32 * c, v);
-      tmem_wait32(v);
+    for (int c = 0; c < 4; ++c) tmem_load32(ts + 32 * c, v[c]);
+    const int32_t j0 = t * kAttKeys;   // (keys lie below 2^31: so does the tile's last place but for the very last tile)
+    const bool whole = all_end - j0 >= kAttKeys && j0 >= all_begin && sc.has == 255u;
+    uint32_t off = 0;  // groups that the row sees nothing of: their scales may be anything
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const float f = fq * sc.ks[2 * c + g];
-        if (whole) {  // (a scale is not negative)
-          float x = v[16 * g];
+    for (int c = 0; c < 4; ++c) tmem_wait32(v[c]);
+    if (!whole) {
+      const int hi = max(min(end - j0, kAttKeys), 0), lo = max(min(begin - j0, kAttKeys), 0);
 #pragma unroll
-          for (int e = 1; e < 15; e += 2) x = max3(x, v[16 * g + e], v[16 * g + e + 1]);
-          top = fmaxf(top, fmaxf(x, v[16 * g + 15]) * f);
-        } else {
+      for (int g = 0; g < 8; ++g) {
+        const bool none = 16 * g >= hi || 16 * g + 16 <= lo || !((sc.has >> g) & 1u);
+        off |= (none ? 1u : 0u) << g;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int64_t j = j0 + 32 * c + 16 * g + e;
-            if (j < end && j >= begin && ((has >> (2 * c + g)) & 1u)) top = fmaxf(top, v[16 * g + e] * f);
-          }
+        for (int e = 0; e < 16; ++e) {
+          float& x = v[g >> 1][16 * (g & 1) + e];
+          if (none || 16 * g + e >= hi || 16 * g + e < lo) x = kNone;
         }
       }
     }
-    const float was = m, unit_was = unit;
-    if (top > m + kLazy || (m == kNone && top > m)) m = top;
-    float vmax = 0.0f;
+    const auto key_scale = [&](int g) {  // not 0, so that -inf stays -inf
+      const float f = fq * sc.ks[g];
+      return f == 0.0f || ((off >> g) & 1u) ? 0x1p-126f : f;
+    };
+    // ---- the maximum ----
+    float top = kNone;
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
-      const float x = fabsf(sc.vs[g]);
-      if (((has >> g) & 1u) && is_finite_f(x)) vmax = fmaxf(vmax, x);
+      const float* x = &v[g >> 1][16 * (g & 1)];
+      float y = x[0];
+#pragma unroll
+      for (int e = 1; e < 15; e += 2) y = max3(y, x[e], x[e + 1]);
+      top = fmaxf(top, fmaxf(y, x[15]) * key_scale(g));  // (a scale is not negative)
     }
-    if (vmax > unit)  // four times the next power of two
-      unit = __uint_as_float((__float_as_uint(fminf(vmax, 0x1p120f)) & 0x7f800000u) + 3u * 0x00800000u);
+    const float was = m, unit_was = unit;
+    if (top > m + kLazy || (m == kNone && top > m)) m = top;
+    if (sc.most > unit)  // four times the next power of two
+      unit = __uint_as_float((__float_as_uint(fminf(sc.most, 0x1p120f)) & 0x7f800000u) + 3u * 0x00800000u);
     const bool moved = m != was || unit != unit_was;
     if (__any_sync(kFull, moved)) {
       const float f = was == kNone ? 1.0f : ex2(was - m), fo = f * (unit_was / unit);
       l *= f;
       if (n > 0) {
+#pragma unroll 1
         for (int c = 0; c < dim; c += 16) {
           float o8[8], o9[8];
           tmem_load8(to + c, o8);
@@ -214,37 +227,19 @@ __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& 
     uint64_t sum = pk(0.0f, 0.0f);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      tmem_load32(ts + 32 * c, v);
-      tmem_wait32(v);
       uint32_t y[16];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const float f = fq * sc.ks[2 * c + g], fv = sc.vs[2 * c + g] * inverse;
+        const float f = key_scale(2 * c + g), fv = (off >> (2 * c + g)) & 1u ? 0.0f : sc.vs[2 * c + g] * inverse;
         const uint64_t ff = pk(f, f), ffv = pk(fv, fv);
-        if (whole) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float x0, x1;
-            upk(fma2(pk(v[16 * g + 2 * e], v[16 * g + 2 * e + 1]), ff, minus), x0, x1);
-            const uint64_t w2 = pk(ex2(x0), ex2(x1));
-            sum = add_pairs(sum, w2);
-            upk(mul2(w2, ffv), x0, x1);
-            y[8 * g + e] = f16x2_bits(x0, x1);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float x[2];
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const int64_t j = j0 + 32 * c + 16 * g + 2 * e + z;
-              const bool seen = j < end && j >= begin && ((has >> (2 * c + g)) & 1u);
-              const float w1 = seen ? ex2(__fmaf_rn(v[16 * g + 2 * e + z], f, -from)) : 0.0f;
-              l += w1;
-              x[z] = seen ? w1 * fv : 0.0f;  // (the scale of what is not seen may be anything)
-            }
-            y[8 * g + e] = f16x2_bits(x[0], x[1]);
-          }
+        for (int e = 0; e < 8; ++e) {
+          float x0, x1;
+          upk(fma2(pk(v[c][16 * g + 2 * e], v[c][16 * g + 2 * e + 1]), ff, minus), x0, x1);
+          const uint64_t w2 = pk(ex2(x0), ex2(x1));
+          sum = add_pairs(sum, w2);
+          upk(mul2(w2, ffv), x0, x1);
+          y[8 * g + e] = f16x2_bits(x0, x1);
         }
       }
       tmem_store16(ts + 16 * c, y);
@@ -284,107 +279,123 @@ __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& 
   tc_fence_before();
 }
 
-// ---- decoding -----------------------------------------------------------------------------------
-// 16 codes to f16, at their places in a line of a 64-wide panel (128-byte swizzle)
-template <int FMT>
-__device__ __forceinline__ void decode16(const uint4& codes, uint32_t tile, int row, int ch) {
-  const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
-  uint32_t h[8];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t y = prepare_word<FMT>(cw[k]);
-    h[2 * k] = pair_in_word<FMT, 0>(y);
-    h[2 * k + 1] = pair_in_word<FMT, 1>(y);
-  }
-  // eight lanes hold one row's pieces, four of either panel: the second panel's store their halves the other way round,
-  // so that they take other banks
-  const bool odd = ch & 4;
-  uint32_t x[4], y[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) x[k] = odd ? h[4 + k] : h[k], y[k] = odd ? h[k] : h[4 + k];
-  const uint32_t line = tile + (ch >> 2) * kAttPanel + row * 128, at = 2 * (ch & 3);
-  sts16(line + (((at + (odd ? 1 : 0)) ^ (row & 7)) << 4), x);
-  sts16(line + (((at + (odd ? 0 : 1)) ^ (row & 7)) << 4), y);
-}
-
-template <int FMT>
-__device__ __forceinline__ void decode_role(const AttTcArgs& p, const AttWork& w, AttBarriers& bar, AttScales* scales, uint32_t smem_k, uint32_t smem_v,
-                                            volatile int* abort) {
+// ---- copies --------------------------------------------------------------------------------------
+__device__ __forceinline__ void copy_role(const AttTcArgs& p, const AttWork& w, AttBarriers& bar, AttScales* scales, uint32_t raw_k, uint32_t raw_v,
+                                          volatile int* abort) {
   const AttentionArgs& a = p.a;
-  const int lane = threadIdx.x & 31, id = static_cast<int>(threadIdx.x) - 32 * kAttSoftWarps, dim = a.c.dim, pieces = dim / 16;
-  constexpr int kEach = 4;  // pieces of a thread: 128 rows of up to 8 over 256 threads
-  int row[kEach], ch[kEach];
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int k = id + 32 * kAttDecWarps * i;
-    row[i] = k / pieces;
-    ch[i] = k - row[i] * pieces;
-  }
-  // lanes 0-7: the 16-token groups of the next tile: byte offset of their codes, -1 where they have no page
-  int64_t group = -1, block = 0;
+  const int lane = threadIdx.x & 31;
+  const uint32_t row = a.c.dim <= 64 ? 64u : 128u, bytes = static_cast<uint32_t>(p.box) * row;
+  // lane i < 8: the i-th 16 tokens of a tile
+  int32_t page = -1, in = 0;
   const auto look = [&](int32_t t) {
-    const int64_t j = static_cast<int64_t>(t) * kAttKeys + 16 * (lane & 7);
-    group = -1;
-    if (t < w.t1 && j < w.sp.len) {
-      const int32_t at = static_cast<int32_t>(j) / a.c.page, in = static_cast<int32_t>(j) - at * a.c.page;
-      const int32_t page = __ldg(a.b.table + w.seq * a.b.ld_table + at);
-      if (page >= 0 && page < a.c.pages) {
-        const int64_t head = static_cast<int64_t>(page) * a.c.heads + w.kvh;
-        group = (head * a.c.page + in) * dim;
-        block = head * (a.c.page >> a.c.log2_block) + (in >> a.c.log2_block);
-      }
-    }
-  };
-  uint4 kr[kEach], vr[kEach];
-  float ks = 0.0f, vs = 0.0f;
-  uint32_t has = 0;
-  const auto load = [&](const uint8_t* codes, int64_t from, int32_t t, uint4 (&r)[kEach]) {
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int64_t at = __shfl_sync(kFull, from, (row[i] >> 4) & 7);
-      r[i] = make_uint4(0u, 0u, 0u, 0u);  // what is past the end, or not there, is 0: it may be anything in memory
-      if (row[i] < kAttKeys && at >= 0 && static_cast<int64_t>(t) * kAttKeys + row[i] < w.sp.len)
-        r[i] = __ldg(reinterpret_cast<const uint4*>(codes + at + (row[i] & 15) * dim + 16 * ch[i]));
+    const int64_t j = static_cast<int64_t>(t) * kAttKeys + 16 * lane;
+    page = -1;
+    if (lane < 8 && t < w.t1 && j < w.sp.len) {
+      const int32_t at = static_cast<int32_t>(j) / a.c.page;
+      in = static_cast<int32_t>(j) - at * a.c.page;
+      page = __ldg(a.b.table + w.seq * a.b.ld_table + at);
+      if (page >= a.c.pages) page = -1;
     }
   };
   look(w.t0);
-  int64_t now = group;
-  load(a.c.k, now, w.t0, kr);
-  load(a.c.v, now, w.t0, vr);
-  if (group >= 0) ks = __ldg(a.c.ks + block), vs = __ldg(a.c.vs + block);
-  has = __ballot_sync(kFull, group >= 0) & 255u;
-  look(w.t0 + 1);
+  uint32_t parity = 0;
+  int32_t t = w.t0;
+  for (; t < w.t1; ++t, parity ^= 1u) {
+    const int n = t - w.t0;
+    const bool there = page >= 0;
+    const int32_t head = (there ? page : 0) * a.c.heads + w.kvh, y = in;
+    float ks = 0.0f, vs = 0.0f;
+    if (there) {
+      const int64_t block = static_cast<int64_t>(head) * (a.c.page >> a.c.log2_block) + (y >> a.c.log2_block);
+      ks = __ldg(a.c.ks + block), vs = __ldg(a.c.vs + block);
+    }
+    look(t + 1);
+    float most = is_finite_f(vs) ? fabsf(vs) : 0.0f;
+#pragma unroll
+    for (int o = 4; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
+    const uint32_t has = __ballot_sync(kFull, there);
+    const bool starts = there && lane % (p.box / 16) == 0;
+    const uint32_t total = __popc(__ballot_sync(kFull, starts)) * bytes;
+    const uint32_t at = static_cast<uint32_t>(16 * lane) * row;
+    if (!__all_sync(kFull, tc_wait(smem_addr(&bar.rk_empty), parity ^ 1u, abort))) break;
+    // (slot n % 4 is free: the keys of tile n - 1 are decoded, so the scores of n - 3 are in, so the weights of n - 4 were)
+    AttScales& sc = scales[n % kAttScales];
+    if (lane < 8) sc.ks[lane] = ks, sc.vs[lane] = vs;
+    if (lane == 0) sc.has = has, sc.most = most;
+    __syncwarp();
+    if (lane == 0) {
+      arrive_local(smem_addr(&bar.scales[n % kAttScales]));
+      mbar_expect_tx(smem_addr(&bar.rk_full), total);
+    }
+    __syncwarp();
+    if (starts) box_load(raw_k + at, &p.maps.k, 0, y, head, smem_addr(&bar.rk_full));
+    if (!__all_sync(kFull, tc_wait(smem_addr(&bar.rv_empty), parity ^ 1u, abort))) break;
+    if (lane == 0) mbar_expect_tx(smem_addr(&bar.rv_full), total);
+    __syncwarp();
+    if (starts) box_load(raw_v + at, &p.maps.v, 0, y, head, smem_addr(&bar.rv_full));
+  }
+  if (*abort && t > w.t0) {  // copies in flight land before the memory is released
+    mbar_wait(smem_addr(&bar.rk_full), 0, kTcWaitNs / 4), mbar_wait(smem_addr(&bar.rk_full), 1, kTcWaitNs / 4);
+    mbar_wait(smem_addr(&bar.rv_full), 0, kTcWaitNs / 4), mbar_wait(smem_addr(&bar.rv_full), 1, kTcWaitNs / 4);
+  }
+}
+
+// ---- decoding -----------------------------------------------------------------------------------
+// A thread's pieces of a tile: eight lanes take eight rows, so that both the reads (TMA's swizzle) and the
+// writes (the MMA's) touch every bank once.
+template <int FMT>
+__device__ __forceinline__ void decode_role(const AttTcArgs& p, const AttWork& w, AttBarriers& bar, const AttScales* scales, uint32_t raw_k,
+                                            uint32_t raw_v, uint32_t smem_k, uint32_t smem_v, volatile int* abort) {
+  const int lane = threadIdx.x & 31, dw = static_cast<int>(threadIdx.x >> 5) - kAttSoftWarps, dim = p.a.c.dim, pieces = dim / 16;
+  constexpr int kEach = 4;  // pieces of a thread, at most
+  uint32_t from[kEach], to[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int k = (lane >> 3) + 4 * i, row = 8 * (2 * dw + k / pieces) + (lane & 7), ch = k % pieces;
+    from[i] = dim <= 64 ? row * 64 + ((ch ^ ((row >> 1) & 3)) << 4) : row * 128 + ((ch ^ (row & 7)) << 4);
+    to[i] = (ch >> 2) * kAttPanel + row * 128 + (((2 * (ch & 3)) ^ (row & 7)) << 4);
+    if (k >= 2 * pieces) from[i] = ~0u;
+  }
+  const auto decode = [&](uint32_t raw, uint32_t tile, uint32_t has, int32_t rows) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      if (from[i] == ~0u) break;
+      uint32_t cw[4], h[8];
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(cw[0]), "=r"(cw[1]), "=r"(cw[2]), "=r"(cw[3]) : "r"(raw + from[i]));
+      if (rows < kAttKeys || has != 255u) {  // what is past the end, or not there, may be anything
+        const int row = 8 * (2 * dw + ((lane >> 3) + 4 * i) / pieces) + (lane & 7);
+        if (row >= rows || !((has >> (row >> 4)) & 1u)) cw[0] = cw[1] = cw[2] = cw[3] = 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t y = prepare_word<FMT>(cw[k]);
+        h[2 * k] = pair_in_word<FMT, 0>(y);
+        h[2 * k + 1] = pair_in_word<FMT, 1>(y);
+      }
+      const uint32_t x0[4] = {h[0], h[1], h[2], h[3]}, x1[4] = {h[4], h[5], h[6], h[7]};
+      sts16(tile + to[i], x0);
+      sts16((tile + to[i]) ^ 16u, x1);
+    }
+    fence_proxy_async();
+    __syncwarp();
+  };
   for (int32_t t = w.t0; t < w.t1; ++t) {
     const int n = t - w.t0, s = n % kAttStages;
-    const uint32_t ph = (n / kAttStages) & 1;
-    if (!__all_sync(kFull, tc_wait(smem_addr(&bar.k_empty[s]), ph ^ 1u, abort))) break;
-    if (id < 32) {  // (tile n - 4's scales are no longer read: the tile before last would not have been finished)
-      AttScales& sc = scales[n % kAttScales];
-      if (lane < 8) sc.ks[lane] = ks, sc.vs[lane] = vs;
-      if (lane == 0) sc.has = has;
-      __syncwarp();
-      if (lane == 0) arrive_local(smem_addr(&bar.scales[n % kAttScales]));
+    const uint32_t ph = (n / kAttStages) & 1, raw = n & 1;
+    const int32_t rows = static_cast<int32_t>(min(w.sp.len - static_cast<int64_t>(t) * kAttKeys, static_cast<int64_t>(kAttKeys)));
+    if (!__all_sync(kFull, tc_wait(smem_addr(&bar.rk_full), raw, abort) && tc_wait(smem_addr(&bar.k_empty[s]), ph ^ 1u, abort))) break;
+    const uint32_t has = scales[n % kAttScales].has;
+    decode(raw_k, smem_k + s * kAttTile, has, rows);
+    if (lane == 0) {
+      arrive_local(smem_addr(&bar.k_full[s]));
+      arrive_local(smem_addr(&bar.rk_empty));
     }
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (row[i] < kAttKeys) decode16<FMT>(kr[i], smem_k + s * kAttTile, row[i], ch[i]);
-    fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) arrive_local(smem_addr(&bar.k_full[s]));
-    now = group;
-    load(a.c.k, now, t + 1, kr);  // (past the last tile: no groups)
-    ks = vs = 0.0f;
-    if (now >= 0) ks = __ldg(a.c.ks + block), vs = __ldg(a.c.vs + block);
-    has = __ballot_sync(kFull, now >= 0) & 255u;
-    if (!__all_sync(kFull, tc_wait(smem_addr(&bar.v_empty[s]), ph ^ 1u, abort))) break;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i)
-      if (row[i] < kAttKeys) decode16<FMT>(vr[i], smem_v + s * kAttTile, row[i], ch[i]);
-    fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) arrive_local(smem_addr(&bar.v_full[s]));
-    load(a.c.v, now, t + 1, vr);
-    look(t + 2);
+    if (!__all_sync(kFull, tc_wait(smem_addr(&bar.rv_full), raw, abort) && tc_wait(smem_addr(&bar.v_empty[s]), ph ^ 1u, abort))) break;
+    decode(raw_v, smem_v + s * kAttTile, has, rows);
+    if (lane == 0) {
+      arrive_local(smem_addr(&bar.v_full[s]));
+      arrive_local(smem_addr(&bar.rv_empty));
+    }
   }
 }
 
@@ -437,7 +448,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attention_tc_kernel(const __gr
   const AttentionArgs& a = p.a;
   const int warp = static_cast<int>(threadIdx.x) >> 5;
   const uint32_t base = (smem_addr(att_raw) + 1023u) & ~1023u;
-  const uint32_t smem_q = base, smem_k = base + 2 * kAttTile, smem_v = smem_k + kAttStages * kAttTile;
+  const uint32_t smem_q = base, smem_k = base + 2 * kAttTile, smem_v = smem_k + kAttStages * kAttTile, raw_k = smem_v + kAttStages * kAttTile, raw_v = raw_k + kAttRaw;
 
   // the longest work first: the last rows of the last sequences see the most
   const int64_t at = blockIdx.x / p.splits;
@@ -475,6 +486,10 @@ __global__ void __launch_bounds__(kAttThreads, 1) attention_tc_kernel(const __gr
       mbar_init(smem_addr(&bar.p_full[q]), 4);
     }
     for (int s = 0; s < kAttScales; ++s) mbar_init(smem_addr(&bar.scales[s]), 1);
+    mbar_init(smem_addr(&bar.rk_full), 1);
+    mbar_init(smem_addr(&bar.rv_full), 1);
+    mbar_init(smem_addr(&bar.rk_empty), kAttDecWarps);
+    mbar_init(smem_addr(&bar.rv_empty), kAttDecWarps);
     mbar_init(smem_addr(&bar.q_full), 4 * p.nq);
     mbar_init(smem_addr(&bar.done), 1);
     mbar_init_fence();
@@ -489,15 +504,22 @@ __global__ void __launch_bounds__(kAttThreads, 1) attention_tc_kernel(const __gr
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   if (warp < kAttSoftWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kAttSoftRegs));
     if (warp / 4 < p.nq) softmax_role(p, w, bar, scales, smem_q, tmem, warp / 4, &s_abort);
   } else if (warp < kAttSoftWarps + kAttDecWarps) {
-    decode_role<FMT>(p, w, bar, scales, smem_k, smem_v, &s_abort);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAttDecRegs));
+    decode_role<FMT>(p, w, bar, scales, raw_k, raw_v, smem_k, smem_v, &s_abort);
   } else {
-    if (w.t0 < w.t1 && elect_one()) mma_role(p, w, bar, smem_q, smem_k, smem_v, tmem, &s_abort);
-    __syncwarp();
-    // (after a wait has given up the others may come here before the last MMA has completed)
-    if (w.t0 < w.t1) tc_wait(smem_addr(&bar.done), 0, &s_abort);
-    if (s_abort) mbar_wait(smem_addr(&bar.done), 0, kTcWaitNs);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kAttRestRegs));
+    if (warp == kAttSoftWarps + kAttDecWarps) {
+      if (w.t0 < w.t1 && elect_one()) mma_role(p, w, bar, smem_q, smem_k, smem_v, tmem, &s_abort);
+      __syncwarp();
+      // (after a wait has given up the others may come here before the last MMA has completed)
+      if (w.t0 < w.t1) tc_wait(smem_addr(&bar.done), 0, &s_abort);
+      if (s_abort) mbar_wait(smem_addr(&bar.done), 0, kTcWaitNs);
+    } else if (warp == kAttSoftWarps + kAttDecWarps + 1) {
+      copy_role(p, w, bar, scales, raw_k, raw_v, &s_abort);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -543,6 +565,8 @@ qz_status launch_tc(const AttentionArgs& a, const TcAttPlan& plan, cudaStream_t 
   AttTcArgs p{};
   p.a = a;
   p.nq = plan.nq, p.splits = plan.splits, p.slots = plan.slots;
+  p.box = a.c.page % 128 == 0 ? 128 : a.c.page % 64 == 0 ? 64 : a.c.page % 32 == 0 ? 32 : 16;
+  if (a.c.pages > 0 && !encode_maps(&p.maps, a, p.box)) return QZ_ERR_CUDA;
   const auto k = &attention_tc_kernel<FMT>;
   if (!set_dyn_smem(reinterpret_cast<const void*>(k), kAttSmem)) return QZ_ERR_CUDA;
   k<<<static_cast<unsigned>(plan.grid), kAttThreads, kAttSmem, s>>>(p);
