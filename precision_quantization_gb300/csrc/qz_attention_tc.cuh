@@ -99,6 +99,7 @@ struct AttScales {   // of a tile's 16-token groups; 0 for those past the end or
   float ks[8], vs[8];
   float most;        // the largest finite |vs|
   uint32_t has;      // bit i: group i is there
+  uint32_t odd;      // a scale is not finite
 };
 
 // The CTA's rows and keys.
@@ -167,7 +168,7 @@ __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& 
 #pragma unroll
     for (int c = 0; c < 4; ++c) tmem_load32(ts + 32 * c, v[c]);
     const int32_t j0 = t * kAttKeys;   // (keys lie below 2^31: so does the tile's last place but for the very last tile)
-    const bool whole = all_end - j0 >= kAttKeys && j0 >= all_begin && sc.has == 255u;
+    const bool whole = all_end - j0 >= kAttKeys && j0 >= all_begin && sc.has == 255u, odd = sc.odd != 0;
     uint32_t off = 0;  // groups that the row sees nothing of: their scales may be anything
 #pragma unroll
     for (int c = 0; c < 4; ++c) tmem_wait32(v[c]);
@@ -177,26 +178,31 @@ __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& 
       for (int g = 0; g < 8; ++g) {
         const bool none = 16 * g >= hi || 16 * g + 16 <= lo || !((sc.has >> g) & 1u);
         off |= (none ? 1u : 0u) << g;
+        const int first = none ? 16 : lo - 16 * g, last = none ? 0 : hi - 16 * g;
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float& x = v[g >> 1][16 * (g & 1) + e];
-          if (none || 16 * g + e >= hi || 16 * g + e < lo) x = kNone;
+          if (e >= last || e < first) x = kNone;
         }
       }
     }
-    const auto key_scale = [&](int g) {  // not 0, so that -inf stays -inf
-      const float f = fq * sc.ks[g];
-      return f == 0.0f || ((off >> g) & 1u) ? 0x1p-126f : f;
+    const auto key_scale = [&](int g) {  // not 0, so that -inf stays -inf; NaN stays NaN
+      float f;
+      asm("max.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(fq * sc.ks[g]), "f"(0x1p-126f));
+      if (odd && ((off >> g) & 1u)) f = 0x1p-126f;
+      return f;
     };
+    const auto value_scale = [&](int g, float inverse) { return odd && ((off >> g) & 1u) ? 0.0f : sc.vs[g] * inverse; };
     // ---- the maximum ----
     float top = kNone;
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
       const float* x = &v[g >> 1][16 * (g & 1)];
-      float y = x[0];
+      float y = x[0], z = x[1];
 #pragma unroll
-      for (int e = 1; e < 15; e += 2) y = max3(y, x[e], x[e + 1]);
-      top = fmaxf(top, fmaxf(y, x[15]) * key_scale(g));  // (a scale is not negative)
+      for (int e = 2; e < 14; e += 4) y = max3(y, x[e], x[e + 1]), z = max3(z, x[e + 2], x[e + 3]);
+      y = max3(y, x[14], x[15]);
+      top = fmaxf(top, fmaxf(y, z) * key_scale(g));  // (a scale is not negative)
     }
     const float was = m, unit_was = unit;
     if (top > m + kLazy || (m == kNone && top > m)) m = top;
@@ -224,28 +230,36 @@ __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& 
     // ---- the weights ----
     const float from = m == kNone ? 0.0f : m, inverse = kPUnit / unit;
     const uint64_t minus = pk(-from, -from);
-    uint64_t sum = pk(0.0f, 0.0f);
+    uint64_t sum0 = pk(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       uint32_t y[16];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const float f = key_scale(2 * c + g), fv = (off >> (2 * c + g)) & 1u ? 0.0f : sc.vs[2 * c + g] * inverse;
+        const float f = key_scale(2 * c + g), fv = value_scale(2 * c + g, inverse);
         const uint64_t ff = pk(f, f), ffv = pk(fv, fv);
+        uint64_t x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = fma2(pk(v[c][16 * g + 2 * e], v[c][16 * g + 2 * e + 1]), ff, minus);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float x0, x1;
-          upk(fma2(pk(v[c][16 * g + 2 * e], v[c][16 * g + 2 * e + 1]), ff, minus), x0, x1);
-          const uint64_t w2 = pk(ex2(x0), ex2(x1));
-          sum = add_pairs(sum, w2);
-          upk(mul2(w2, ffv), x0, x1);
+          upk(x[e], x0, x1);
+          x[e] = pk(ex2(x0), ex2(x1));
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) sum0 = add_pairs(sum0, x[e]), sum1 = add_pairs(sum1, x[e + 1]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float x0, x1;
+          upk(mul2(x[e], ffv), x0, x1);
           y[8 * g + e] = f16x2_bits(x0, x1);
         }
       }
       tmem_store16(ts + 16 * c, y);
     }
     float s0, s1;
-    upk(sum, s0, s1);
+    upk(add_pairs(sum0, sum1), s0, s1);
     l += s0 + s1;
     tmem_stored();
     tc_fence_before();
@@ -314,6 +328,7 @@ __device__ __forceinline__ void copy_role(const AttTcArgs& p, const AttWork& w, 
 #pragma unroll
     for (int o = 4; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
     const uint32_t has = __ballot_sync(kFull, there);
+    const uint32_t odd = __any_sync(kFull, !is_finite_f(ks) || !is_finite_f(vs)) ? 1u : 0u;
     const bool starts = there && lane % (p.box / 16) == 0;
     const uint32_t total = __popc(__ballot_sync(kFull, starts)) * bytes;
     const uint32_t at = static_cast<uint32_t>(16 * lane) * row;
@@ -321,7 +336,7 @@ __device__ __forceinline__ void copy_role(const AttTcArgs& p, const AttWork& w, 
     // (slot n % 4 is free: the keys of tile n - 1 are decoded, so the scores of n - 3 are in, so the weights of n - 4 were)
     AttScales& sc = scales[n % kAttScales];
     if (lane < 8) sc.ks[lane] = ks, sc.vs[lane] = vs;
-    if (lane == 0) sc.has = has, sc.most = most;
+    if (lane == 0) sc.has = has, sc.most = most, sc.odd = odd;
     __syncwarp();
     if (lane == 0) {
       arrive_local(smem_addr(&bar.scales[n % kAttScales]));
