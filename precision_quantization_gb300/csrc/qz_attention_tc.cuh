@@ -12,7 +12,7 @@
 //                reads (keys K-major, values MN-major: the same bytes)
 //   warp 16      issues the MMAs: x = Q K^T into 128 columns of tensor memory, out += P V with P as the
 //                A operand from there
-//   warp 17      looks up the pages and copies the next tile's codes by TMA
+//   warps 17, 18 look up the pages and copy codes by TMA, keys and values, half a tile at a time
 // in the order P0 V(j - 1), Q0 K(j), P1 V(j - 1), Q1 K(j): while one tile's softmax runs, the tensor cores work
 // for the other.
 // 8-bit codes are exact in f16, q is made f16 by a power of two of its row.  The maximum m is moved only
@@ -43,10 +43,29 @@ constexpr float kLazy = 4.0f, kPUnit = 0x1p11f;
 struct AttTcArgs {
   AttentionArgs a;
   int32_t nq, splits, slots;   // row tiles of a CTA; parts of the keys; places for a kv head's CTAs
-  int32_t box;                 // tokens of a copy: the largest of 16, 32, 64, 128 that divides a page
+  int32_t box;                 // tokens of a copy: the largest of 16, 32, 64 that divides a page
+  bool out_wide;               // 16-byte pieces of out are aligned
   CacheMaps maps;
 };
 
+// Bounded wait on phase `parity`; the clock is looked at now and then only.
+__device__ __forceinline__ bool att_wait(uint64_t& bar, uint32_t parity, volatile int* abort) {
+  const uint32_t at = smem_addr(&bar);
+  if (mbar_try_wait(at, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !mbar_try_wait(at, parity); ++i) {
+    if (i % 64 == 0) {
+      if (*abort) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kTcWaitNs) {
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+  return true;
+}
 // x (f16 pairs, tensor memory) as the A operand
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
@@ -92,7 +111,7 @@ __device__ __forceinline__ uint32_t idesc_f16(int n, bool b_mn) {
 
 struct AttBarriers {
   uint64_t k_full[kAttStages], k_empty[kAttStages], v_full[kAttStages], v_empty[kAttStages];
-  uint64_t rk_full, rk_empty, rv_full, rv_empty;
+  uint64_t rk_full[2], rk_empty[2], rv_full[2], rv_empty[2];   // codes, by halves of a tile
   uint64_t s_full[2], p_full[2], scales[kAttScales], q_full, done;
 };
 struct AttScales {   // of a tile's 16-token groups; 0 for those past the end or without a page
@@ -109,6 +128,18 @@ struct AttWork {
   int32_t t0, t1;                // tiles of keys
 };
 
+// load_q4 of an address that is there whether or not the values are wanted, without a branch for aligned ones
+__device__ __forceinline__ void load_q4_masked(const AttentionArgs& a, bool in, int64_t at, float (&x)[4]) {
+  if (a.q_vec) {
+    const uint2 b = __ldg(reinterpret_cast<const uint2*>(a.q + at));
+    const uint32_t lo = in ? b.x : 0u, hi = in ? b.y : 0u;
+    x[0] = __uint_as_float(lo << 16), x[1] = __uint_as_float(lo & 0xffff0000u);
+    x[2] = __uint_as_float(hi << 16), x[3] = __uint_as_float(hi & 0xffff0000u);
+  } else {
+    load_q4(a, in, at, x);
+  }
+}
+
 // ---- softmax ------------------------------------------------------------------------------------
 // One row of tile q; a warp's 32 lanes of tensor memory.
 __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& w, AttBarriers& bar, const AttScales* scales, uint32_t smem_q,
@@ -119,32 +150,39 @@ __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& 
   const bool mine = row < w.rows;
   const int i = row / a.group, head = w.kvh * a.group + row % a.group;
   const int64_t token = w.sp.row + i, pos = w.sp.p0 + i;
-  // q as f16, K-major panels of 64 elements, 128-byte swizzle
-  float fq;
-  {
-    const int64_t at = token * a.ld_q + head * a.hd_q;
-    float top = 0.0f, x[4];
-    for (int d = 0; d < dim; d += 4) {
-      load_q4(a, mine, at + d, x);
+  // The warp's 32 rows of q as f16, K-major panels of 64 elements, 128-byte swizzle: a row at a time, four elements a
+  // lane, eight rows' loads in flight.  Lane r keeps row r's factor.
+  float fq = 0.0f;
+  const int32_t left = min(w.rows - (w.row0 + q * kAttRows + 32 * warp), 32);  // of the warp's rows
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += 8) {
+    float x[8][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top = absmax_nan(top, x[e]);
+    for (int k = 0; k < 8; ++k) {
+      const bool in = r0 + k < left && 4 * lane < dim;
+      const int rr = in ? w.row0 + q * kAttRows + 32 * warp + r0 + k : w.row0, ri = rr / a.group;
+      load_q4_masked(a, in, (w.sp.row + ri) * a.ld_q + (w.kvh * a.group + rr - ri * a.group) * a.hd_q + (in ? 4 * lane : 0), x[k]);
     }
-    float down;
-    const float up = q_unit(top, down);
-    fq = down * a.scale;
-    const uint32_t line = smem_q + q * kAttTile + r * 128;
-    for (int d = 0; d < dim; d += 8) {
-      float y[4];
-      load_q4(a, mine, at + d, x);
-      load_q4(a, mine, at + d + 4, y);
-      const uint32_t v[4] = {f16x2_bits(x[0] * up, x[1] * up), f16x2_bits(x[2] * up, x[3] * up), f16x2_bits(y[0] * up, y[1] * up),
-                             f16x2_bits(y[2] * up, y[3] * up)};
-      sts16(line + (d >> 6) * kAttPanel + ((((d >> 3) & 7) ^ (r & 7)) << 4), v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float top = absmax_nan(absmax_nan(absmax_nan(fabsf(x[k][0]), x[k][1]), x[k][2]), x[k][3]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = absmax_nan(top, __shfl_xor_sync(kFull, top, o));
+      float down;
+      const float up = q_unit(top, down);
+      if (lane == r0 + k) fq = down * a.scale;
+      if (4 * lane < dim) {
+        const int line = 32 * warp + r0 + k;
+        const uint32_t at = smem_q + q * kAttTile + (lane >> 4) * kAttPanel + line * 128 + ((((lane >> 1) & 7) ^ (line & 7)) << 4) + (lane & 1) * 8;
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(f16x2_bits(x[k][0] * up, x[k][1] * up)),
+                     "r"(f16x2_bits(x[k][2] * up, x[k][3] * up))
+                     : "memory");
+      }
     }
-    fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) arrive_local(smem_addr(&bar.q_full));
   }
+  fence_proxy_async();
+  __syncwarp();
+  if (lane == 0) arrive_local(smem_addr(&bar.q_full));
   const int32_t end = mine ? static_cast<int32_t>(max(min(pos + 1, static_cast<int64_t>(w.sp.len)), static_cast<int64_t>(0))) : INT32_MAX;
   const int32_t begin = mine ? static_cast<int32_t>(max(pos + 1 - a.window, static_cast<int64_t>(0))) : 0;
   int32_t all_end = end, all_begin = begin;  // what every row of the warp sees
@@ -160,114 +198,146 @@ __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& 
   for (int32_t t = w.t0; t < w.t1; ++t) {
     const int n = t - w.t0;
     const AttScales& sc = scales[n % kAttScales];
-    ok = tc_wait(smem_addr(&bar.scales[n % kAttScales]), (n / kAttScales) & 1, abort) && tc_wait(smem_addr(&bar.s_full[q]), n & 1, abort);
+    ok = att_wait(bar.scales[n % kAttScales], (n / kAttScales) & 1, abort) && att_wait(bar.s_full[q], n & 1, abort);
     ok = __all_sync(kFull, ok);
     if (!ok) break;
     tc_fence_after();
     float v[4][32];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_load32(ts + 32 * c, v[c]);
+    tmem_load32(ts, v[0]);
+    tmem_load32(ts + 32, v[1]);
     const int32_t j0 = t * kAttKeys;   // (keys lie below 2^31: so does the tile's last place but for the very last tile)
     const bool whole = all_end - j0 >= kAttKeys && j0 >= all_begin && sc.has == 255u, odd = sc.odd != 0;
-    uint32_t off = 0;  // groups that the row sees nothing of: their scales may be anything
+    // 16 weights of group g from their scores: p = 2^(f x - from), their sum, and p fv as f16
+    const auto weigh = [&](int g, float f, float fv, uint64_t minus, uint64_t (&sum)[2], uint32_t* y) {
+      const float* s16 = &v[g >> 1][16 * (g & 1)];
+      const uint64_t ff = pk(f, f), ffv = pk(fv, fv);
+      uint64_t x[8];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) tmem_wait32(v[c]);
-    if (!whole) {
-      const int hi = max(min(end - j0, kAttKeys), 0), lo = max(min(begin - j0, kAttKeys), 0);
+      for (int e = 0; e < 8; ++e) x[e] = fma2(pk(s16[2 * e], s16[2 * e + 1]), ff, minus);
 #pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        const bool none = 16 * g >= hi || 16 * g + 16 <= lo || !((sc.has >> g) & 1u);
-        off |= (none ? 1u : 0u) << g;
-        const int first = none ? 16 : lo - 16 * g, last = none ? 0 : hi - 16 * g;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          float& x = v[g >> 1][16 * (g & 1) + e];
-          if (e >= last || e < first) x = kNone;
-        }
+      for (int e = 0; e < 8; ++e) {
+        float x0, x1;
+        upk(x[e], x0, x1);
+        x[e] = pk(ex2(x0), ex2(x1));
       }
-    }
-    const auto key_scale = [&](int g) {  // not 0, so that -inf stays -inf; NaN stays NaN
-      float f;
-      asm("max.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(fq * sc.ks[g]), "f"(0x1p-126f));
-      if (odd && ((off >> g) & 1u)) f = 0x1p-126f;
-      return f;
-    };
-    const auto value_scale = [&](int g, float inverse) { return odd && ((off >> g) & 1u) ? 0.0f : sc.vs[g] * inverse; };
-    // ---- the maximum ----
-    float top = kNone;
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
+      for (int e = 0; e < 8; ++e) sum[e & 1] = add_pairs(sum[e & 1], x[e]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float x0, x1;
+        upk(mul2(x[e], ffv), x0, x1);
+        y[e] = f16x2_bits(x0, x1);
+      }
+    };
+    const auto largest = [&](int g) {
       const float* x = &v[g >> 1][16 * (g & 1)];
       float y = x[0], z = x[1];
 #pragma unroll
       for (int e = 2; e < 14; e += 4) y = max3(y, x[e], x[e + 1]), z = max3(z, x[e + 2], x[e + 3]);
-      y = max3(y, x[14], x[15]);
-      top = fmaxf(top, fmaxf(y, z) * key_scale(g));  // (a scale is not negative)
+      return fmaxf(max3(y, x[14], x[15]), z);
+    };
+    tmem_wait32(v[0]);
+    tmem_wait32(v[1]);
+    tmem_load32(ts + 64, v[2]);
+    tmem_load32(ts + 96, v[3]);
+    bool done = false;
+    if (__all_sync(kFull, whole && !odd && m != kNone && sc.most <= unit)) {
+      // the usual tile: the weights against the maximum so far while this tile's is still being found; taken back in the
+      // rare case that it is exceeded
+      const float inverse = kPUnit / unit;
+      const uint64_t minus = pk(-m, -m);
+      uint64_t sum[2] = {pk(0.0f, 0.0f), pk(0.0f, 0.0f)};
+      float top = kNone;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (c == 2) tmem_wait32(v[2]), tmem_wait32(v[3]);
+        uint32_t y[16];
+#pragma unroll
+        for (int g = 2 * c; g < 2 * c + 2; ++g) {
+          const float f = fq * sc.ks[g];
+          weigh(g, f, sc.vs[g] * inverse, minus, sum, y + 8 * (g & 1));
+          top = fmaxf(top, largest(g) * f);  // (a scale is not negative)
+        }
+        tmem_store16(ts + 16 * c, y);
+      }
+      if (!__any_sync(kFull, top > m + kLazy)) {
+        float s0, s1;
+        upk(add_pairs(sum[0], sum[1]), s0, s1);
+        l += s0 + s1;
+        done = true;
+      }
+    } else {
+      tmem_wait32(v[2]);
+      tmem_wait32(v[3]);
     }
-    const float was = m, unit_was = unit;
-    if (top > m + kLazy || (m == kNone && top > m)) m = top;
-    if (sc.most > unit)  // four times the next power of two
-      unit = __uint_as_float((__float_as_uint(fminf(sc.most, 0x1p120f)) & 0x7f800000u) + 3u * 0x00800000u);
-    const bool moved = m != was || unit != unit_was;
-    if (__any_sync(kFull, moved)) {
-      const float f = was == kNone ? 1.0f : ex2(was - m), fo = f * (unit_was / unit);
-      l *= f;
-      if (n > 0) {
+    if (!done) {
+      uint32_t off = 0;  // groups that the row sees nothing of: their scales may be anything
+      if (!whole) {
+        const int hi = max(min(end - j0, kAttKeys), 0), lo = max(min(begin - j0, kAttKeys), 0);
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          const bool none = 16 * g >= hi || 16 * g + 16 <= lo || !((sc.has >> g) & 1u);
+          off |= (none ? 1u : 0u) << g;
+          const int first = none ? 16 : lo - 16 * g, last = none ? 0 : hi - 16 * g;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float& x = v[g >> 1][16 * (g & 1) + e];
+            if (e >= last || e < first) x = kNone;
+          }
+        }
+      }
+      const auto key_scale = [&](int g) {  // not 0, so that -inf stays -inf; NaN stays NaN
+        float f;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(f) : "f"(fq * sc.ks[g]), "f"(0x1p-126f));
+        return odd && ((off >> g) & 1u) ? 0x1p-126f : f;
+      };
+      float top = kNone;
+#pragma unroll
+      for (int g = 0; g < 8; ++g) top = fmaxf(top, largest(g) * key_scale(g));
+      const float was = m, unit_was = unit;
+      if (top > m + kLazy || (m == kNone && top > m)) m = top;
+      if (sc.most > unit)  // four times the next power of two
+        unit = __uint_as_float((__float_as_uint(fminf(sc.most, 0x1p120f)) & 0x7f800000u) + 3u * 0x00800000u);
+      if (__any_sync(kFull, m != was || unit != unit_was)) {
+        const float f = was == kNone ? 1.0f : ex2(was - m), fo = f * (unit_was / unit);
+        l *= f;
+        if (n > 0) {
 #pragma unroll 1
-        for (int c = 0; c < dim; c += 16) {
-          float o8[8], o9[8];
-          tmem_load8(to + c, o8);
-          tmem_load8(to + c + 8, o9);
-          tmem_wait8(o8);
-          tmem_wait8(o9);
-          uint32_t y[16];
+          for (int c = 0; c < dim; c += 16) {
+            float o8[8], o9[8];
+            tmem_load8(to + c, o8);
+            tmem_load8(to + c + 8, o9);
+            tmem_wait8(o8);
+            tmem_wait8(o9);
+            uint32_t y[16];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(o8[e] * fo), y[8 + e] = __float_as_uint(o9[e] * fo);
-          tmem_store16(to + c, y);
+            for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(o8[e] * fo), y[8 + e] = __float_as_uint(o9[e] * fo);
+            tmem_store16(to + c, y);
+          }
         }
       }
-    }
-    // ---- the weights ----
-    const float from = m == kNone ? 0.0f : m, inverse = kPUnit / unit;
-    const uint64_t minus = pk(-from, -from);
-    uint64_t sum0 = pk(0.0f, 0.0f), sum1 = sum0;
+      const float from = m == kNone ? 0.0f : m, inverse = kPUnit / unit;
+      const uint64_t minus = pk(-from, -from);
+      uint64_t sum[2] = {pk(0.0f, 0.0f), pk(0.0f, 0.0f)};
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      uint32_t y[16];
+      for (int c = 0; c < 4; ++c) {
+        uint32_t y[16];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const float f = key_scale(2 * c + g), fv = value_scale(2 * c + g, inverse);
-        const uint64_t ff = pk(f, f), ffv = pk(fv, fv);
-        uint64_t x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = fma2(pk(v[c][16 * g + 2 * e], v[c][16 * g + 2 * e + 1]), ff, minus);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float x0, x1;
-          upk(x[e], x0, x1);
-          x[e] = pk(ex2(x0), ex2(x1));
-        }
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) sum0 = add_pairs(sum0, x[e]), sum1 = add_pairs(sum1, x[e + 1]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          float x0, x1;
-          upk(mul2(x[e], ffv), x0, x1);
-          y[8 * g + e] = f16x2_bits(x0, x1);
-        }
+        for (int g = 2 * c; g < 2 * c + 2; ++g)
+          weigh(g, key_scale(g), odd && ((off >> g) & 1u) ? 0.0f : sc.vs[g] * inverse, minus, sum, y + 8 * (g & 1));
+        tmem_store16(ts + 16 * c, y);
       }
-      tmem_store16(ts + 16 * c, y);
+      float s0, s1;
+      upk(add_pairs(sum[0], sum[1]), s0, s1);
+      l += s0 + s1;
     }
-    float s0, s1;
-    upk(add_pairs(sum0, sum1), s0, s1);
-    l += s0 + s1;
     tmem_stored();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) arrive_local(smem_addr(&bar.p_full[q]));
   }
   // ---- the result ----
-  if (w.t0 < w.t1) ok = __all_sync(kFull, tc_wait(smem_addr(&bar.done), 0, abort)) && ok && !*abort;
+  if (w.t0 < w.t1) ok = __all_sync(kFull, att_wait(bar.done, 0, abort)) && ok && !*abort;
   tc_fence_after();
   if (!ok) l = __uint_as_float(0x7fc00000u);
   const float back = unit * (1.0f / kPUnit);
@@ -278,15 +348,35 @@ __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& 
     stat = static_cast<float*>(a.ws) + p.splits * all * dim + at * 2;
     if (mine) stat[0] = m, stat[1] = l;
   }
-  for (int c = 0; c < dim; c += 8) {
-    float o8[8] = {};
-    if (w.t0 < w.t1) tmem_ld8(to + c, o8);
-    if (mine) {
+  const bool wide = p.splits == 1 && p.out_wide;  // 16-byte stores
+  const float scale = l == 0.0f ? 0.0f : __fdiv_rn(back, l);
+  if (wide && mine && a.lse) a.lse[token * a.ld_lse + head] = l == 0.0f ? kNone : (m + log2f(l)) * 0.69314718055994531f;
+#pragma unroll 1
+  for (int c = 0; c < dim; c += 32) {  // (the accumulator has 128 columns whatever dim is)
+    float o[32];
+    __syncwarp();
+    if (w.t0 < w.t1) {
+      tmem_load32(to + c, o);
+      tmem_wait32(o);
+    } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float y[4] = {o8[4 * h] * back, o8[4 * h + 1] * back, o8[4 * h + 2] * back, o8[4 * h + 3] * back};
-        if (part) *reinterpret_cast<float4*>(part + c + 4 * h) = make_float4(y[0], y[1], y[2], y[3]);
-        else store_row(a, token, head, c + 4 * h, y, m, l);
+      for (int e = 0; e < 32; ++e) o[e] = 0.0f;
+    }
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      const int d = c + 8 * h;
+      if (!mine || d >= dim) break;
+      if (wide) {
+        *reinterpret_cast<uint4*>(a.out + token * a.ld_out + head * a.hd_out + d) =
+            make_uint4(bf16x2_bits(o[8 * h] * scale, o[8 * h + 1] * scale), bf16x2_bits(o[8 * h + 2] * scale, o[8 * h + 3] * scale),
+                       bf16x2_bits(o[8 * h + 4] * scale, o[8 * h + 5] * scale), bf16x2_bits(o[8 * h + 6] * scale, o[8 * h + 7] * scale));
+        continue;
+      }
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const float y[4] = {o[8 * h + 4 * z] * back, o[8 * h + 4 * z + 1] * back, o[8 * h + 4 * z + 2] * back, o[8 * h + 4 * z + 3] * back};
+        if (part) *reinterpret_cast<float4*>(part + d + 4 * z) = make_float4(y[0], y[1], y[2], y[3]);
+        else store_row(a, token, head, d + 4 * z, y, m, l);
       }
     }
   }
@@ -294,93 +384,102 @@ __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& 
 }
 
 // ---- copies --------------------------------------------------------------------------------------
-__device__ __forceinline__ void copy_role(const AttTcArgs& p, const AttWork& w, AttBarriers& bar, AttScales* scales, uint32_t raw_k, uint32_t raw_v,
-                                          volatile int* abort) {
+// KEYS: the keys' codes, and the scales of both; else the values' codes.  Lane i < 8 stands for the i-th 16
+// tokens of a tile.  Pages are looked up two tiles ahead, scales one.
+template <bool KEYS>
+__device__ __forceinline__ void copy_role(const AttTcArgs& p, const AttWork& w, AttBarriers& bar, AttScales* scales, uint32_t raw, volatile int* abort) {
   const AttentionArgs& a = p.a;
   const int lane = threadIdx.x & 31;
-  const uint32_t row = a.c.dim <= 64 ? 64u : 128u, bytes = static_cast<uint32_t>(p.box) * row;
-  // lane i < 8: the i-th 16 tokens of a tile
-  int32_t page = -1, in = 0;
+  const uint32_t row = a.c.dim <= 64 ? 64u : 128u, bytes = static_cast<uint32_t>(p.box) * row, at = static_cast<uint32_t>(16 * lane) * row;
+  uint64_t* full = KEYS ? bar.rk_full : bar.rv_full;
+  uint64_t* empty = KEYS ? bar.rk_empty : bar.rv_empty;
+  struct Place {
+    int32_t page, in;
+  };
   const auto look = [&](int32_t t) {
     const int64_t j = static_cast<int64_t>(t) * kAttKeys + 16 * lane;
-    page = -1;
+    Place r{-1, 0};
     if (lane < 8 && t < w.t1 && j < w.sp.len) {
-      const int32_t at = static_cast<int32_t>(j) / a.c.page;
-      in = static_cast<int32_t>(j) - at * a.c.page;
-      page = __ldg(a.b.table + w.seq * a.b.ld_table + at);
-      if (page >= a.c.pages) page = -1;
+      const int32_t i = static_cast<int32_t>(j) / a.c.page;
+      r.in = static_cast<int32_t>(j) - i * a.c.page;
+      r.page = __ldg(a.b.table + w.seq * a.b.ld_table + i);
+      if (r.page >= a.c.pages) r.page = -1;
     }
+    return r;
   };
-  look(w.t0);
-  uint32_t parity = 0;
-  int32_t t = w.t0;
-  for (; t < w.t1; ++t, parity ^= 1u) {
-    const int n = t - w.t0;
-    const bool there = page >= 0;
-    const int32_t head = (there ? page : 0) * a.c.heads + w.kvh, y = in;
-    float ks = 0.0f, vs = 0.0f;
-    if (there) {
-      const int64_t block = static_cast<int64_t>(head) * (a.c.page >> a.c.log2_block) + (y >> a.c.log2_block);
+  const auto head_of = [&](const Place& r) { return max(r.page, 0) * a.c.heads + w.kvh; };
+  float ks = 0.0f, vs = 0.0f;
+  const auto fetch = [&](const Place& r) {
+    ks = vs = 0.0f;
+    if (KEYS && r.page >= 0) {
+      const int64_t block = static_cast<int64_t>(head_of(r)) * (a.c.page >> a.c.log2_block) + (r.in >> a.c.log2_block);
       ks = __ldg(a.c.ks + block), vs = __ldg(a.c.vs + block);
     }
-    look(t + 1);
-    float most = is_finite_f(vs) ? fabsf(vs) : 0.0f;
+  };
+  Place now = look(w.t0), next = look(w.t0 + 1);
+  fetch(now);
+  uint32_t parity = 0;
+  bool ok = true;
+  int32_t t = w.t0;
+  for (; t < w.t1 && ok; ++t, parity ^= 1u) {
+    const int n = t - w.t0;
+    const bool starts = now.page >= 0 && lane % (p.box / 16) == 0;
+    const uint32_t mask = __ballot_sync(kFull, starts);
+    const int32_t head = head_of(now);
 #pragma unroll
-    for (int o = 4; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
-    const uint32_t has = __ballot_sync(kFull, there);
-    const uint32_t odd = __any_sync(kFull, !is_finite_f(ks) || !is_finite_f(vs)) ? 1u : 0u;
-    const bool starts = there && lane % (p.box / 16) == 0;
-    const uint32_t total = __popc(__ballot_sync(kFull, starts)) * bytes;
-    const uint32_t at = static_cast<uint32_t>(16 * lane) * row;
-    if (!__all_sync(kFull, tc_wait(smem_addr(&bar.rk_empty), parity ^ 1u, abort))) break;
-    // (slot n % 4 is free: the keys of tile n - 1 are decoded, so the scores of n - 3 are in, so the weights of n - 4 were)
-    AttScales& sc = scales[n % kAttScales];
-    if (lane < 8) sc.ks[lane] = ks, sc.vs[lane] = vs;
-    if (lane == 0) sc.has = has, sc.most = most, sc.odd = odd;
-    __syncwarp();
-    if (lane == 0) {
-      arrive_local(smem_addr(&bar.scales[n % kAttScales]));
-      mbar_expect_tx(smem_addr(&bar.rk_full), total);
+    for (int h = 0; h < 2; ++h) {
+      if (!(ok = __all_sync(kFull, att_wait(empty[h], parity ^ 1u, abort)))) break;
+      if (KEYS && h == 0) {
+        // (slot n % 4 is free: the keys of tile n - 1 are being decoded, so the scores of n - 3 are in, so the weights
+        // of n - 4 were)
+        float most = is_finite_f(vs) ? fabsf(vs) : 0.0f;
+#pragma unroll
+        for (int o = 4; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(kFull, most, o));
+        const uint32_t has = __ballot_sync(kFull, now.page >= 0);
+        const uint32_t odd = __any_sync(kFull, !is_finite_f(ks) || !is_finite_f(vs)) ? 1u : 0u;
+        AttScales& sc = scales[n % kAttScales];
+        if (lane < 8) sc.ks[lane] = ks, sc.vs[lane] = vs;
+        if (lane == 0) sc.has = has, sc.most = most, sc.odd = odd;
+        __syncwarp();
+        if (lane == 0) arrive_local(smem_addr(&bar.scales[n % kAttScales]));
+      }
+      if (lane == 0) mbar_expect_tx(smem_addr(&full[h]), __popc(mask & (h ? 0xf0u : 0x0fu)) * bytes);
+      __syncwarp();
+      if (starts && lane >> 2 == h) box_load(raw + at, KEYS ? &p.maps.k : &p.maps.v, 0, now.in, head, smem_addr(&full[h]));
     }
-    __syncwarp();
-    if (starts) box_load(raw_k + at, &p.maps.k, 0, y, head, smem_addr(&bar.rk_full));
-    if (!__all_sync(kFull, tc_wait(smem_addr(&bar.rv_empty), parity ^ 1u, abort))) break;
-    if (lane == 0) mbar_expect_tx(smem_addr(&bar.rv_full), total);
-    __syncwarp();
-    if (starts) box_load(raw_v + at, &p.maps.v, 0, y, head, smem_addr(&bar.rv_full));
+    now = next;
+    next = look(t + 2);
+    fetch(now);
   }
-  if (*abort && t > w.t0) {  // copies in flight land before the memory is released
-    mbar_wait(smem_addr(&bar.rk_full), 0, kTcWaitNs / 4), mbar_wait(smem_addr(&bar.rk_full), 1, kTcWaitNs / 4);
-    mbar_wait(smem_addr(&bar.rv_full), 0, kTcWaitNs / 4), mbar_wait(smem_addr(&bar.rv_full), 1, kTcWaitNs / 4);
+  if (*abort) {  // copies in flight land before the memory is released
+    for (int i = 0; i < 4; ++i) mbar_wait(smem_addr(&full[i >> 1]), i & 1, kTcWaitNs / 4);
   }
 }
 
 // ---- decoding -----------------------------------------------------------------------------------
-// A thread's pieces of a tile: eight lanes take eight rows, so that both the reads (TMA's swizzle) and the
-// writes (the MMA's) touch every bank once.
+// A thread's pieces of half a tile: eight lanes take eight rows, so that both the reads (TMA's swizzle) and
+// the writes (the MMA's) touch every bank once.
 template <int FMT>
 __device__ __forceinline__ void decode_role(const AttTcArgs& p, const AttWork& w, AttBarriers& bar, const AttScales* scales, uint32_t raw_k,
                                             uint32_t raw_v, uint32_t smem_k, uint32_t smem_v, volatile int* abort) {
   const int lane = threadIdx.x & 31, dw = static_cast<int>(threadIdx.x >> 5) - kAttSoftWarps, dim = p.a.c.dim, pieces = dim / 16;
-  constexpr int kEach = 4;  // pieces of a thread, at most
-  uint32_t from[kEach], to[kEach];
+  const int line = 8 * dw + (lane & 7);   // of 64
+  const uint32_t row_bytes = dim <= 64 ? 64u : 128u;
+  uint32_t from[2], to[2];                // pieces lane / 8 and lane / 8 + 4
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int k = (lane >> 3) + 4 * i, row = 8 * (2 * dw + k / pieces) + (lane & 7), ch = k % pieces;
-    from[i] = dim <= 64 ? row * 64 + ((ch ^ ((row >> 1) & 3)) << 4) : row * 128 + ((ch ^ (row & 7)) << 4);
-    to[i] = (ch >> 2) * kAttPanel + row * 128 + (((2 * (ch & 3)) ^ (row & 7)) << 4);
-    if (k >= 2 * pieces) from[i] = ~0u;
+  for (int i = 0; i < 2; ++i) {
+    const int ch = (lane >> 3) + 4 * i;
+    from[i] = dim <= 64 ? line * 64 + ((ch ^ ((line >> 1) & 3)) << 4) : line * 128 + ((ch ^ (line & 7)) << 4);
+    to[i] = i * kAttPanel + line * 128 + (((2 * (ch & 3)) ^ (line & 7)) << 4);
   }
-  const auto decode = [&](uint32_t raw, uint32_t tile, uint32_t has, int32_t rows) {
+  const bool first = (lane >> 3) < pieces, second = (lane >> 3) + 4 < pieces;
+  const auto decode = [&](uint32_t raw, uint32_t tile, bool there) {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      if (from[i] == ~0u) break;
+    for (int i = 0; i < 2; ++i) {
+      if (!(i ? second : first)) continue;
       uint32_t cw[4], h[8];
       asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(cw[0]), "=r"(cw[1]), "=r"(cw[2]), "=r"(cw[3]) : "r"(raw + from[i]));
-      if (rows < kAttKeys || has != 255u) {  // what is past the end, or not there, may be anything
-        const int row = 8 * (2 * dw + ((lane >> 3) + 4 * i) / pieces) + (lane & 7);
-        if (row >= rows || !((has >> (row >> 4)) & 1u)) cw[0] = cw[1] = cw[2] = cw[3] = 0u;
-      }
+      if (!there) cw[0] = cw[1] = cw[2] = cw[3] = 0u;  // what is past the end, or not there, may be anything
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const uint32_t y = prepare_word<FMT>(cw[k]);
@@ -391,26 +490,30 @@ __device__ __forceinline__ void decode_role(const AttTcArgs& p, const AttWork& w
       sts16(tile + to[i], x0);
       sts16((tile + to[i]) ^ 16u, x1);
     }
-    fence_proxy_async();
-    __syncwarp();
   };
   for (int32_t t = w.t0; t < w.t1; ++t) {
     const int n = t - w.t0, s = n % kAttStages;
     const uint32_t ph = (n / kAttStages) & 1, raw = n & 1;
-    const int32_t rows = static_cast<int32_t>(min(w.sp.len - static_cast<int64_t>(t) * kAttKeys, static_cast<int64_t>(kAttKeys)));
-    if (!__all_sync(kFull, tc_wait(smem_addr(&bar.rk_full), raw, abort) && tc_wait(smem_addr(&bar.k_empty[s]), ph ^ 1u, abort))) break;
-    const uint32_t has = scales[n % kAttScales].has;
-    decode(raw_k, smem_k + s * kAttTile, has, rows);
-    if (lane == 0) {
-      arrive_local(smem_addr(&bar.k_full[s]));
-      arrive_local(smem_addr(&bar.rk_empty));
+    const int64_t rows = w.sp.len - static_cast<int64_t>(t) * kAttKeys;
+    bool ok = true, there[2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {  // keys, values
+      uint64_t* full = z ? bar.rv_full : bar.rk_full;
+      uint64_t* empty = z ? bar.rv_empty : bar.rk_empty;
+      ok = att_wait(z ? bar.v_empty[s] : bar.k_empty[s], ph ^ 1u, abort);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (!(ok = __all_sync(kFull, ok && att_wait(full[h], raw, abort)))) break;
+        if (z == 0) there[h] = 64 * h + line < rows && ((scales[n % kAttScales].has >> ((64 * h + line) >> 4)) & 1u);
+        decode((z ? raw_v : raw_k) + 64 * h * row_bytes, (z ? smem_v : smem_k) + s * kAttTile + 64 * h * 128, there[h]);
+        if (h == 1) fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) arrive_local(smem_addr(&empty[h]));
+      }
+      if (!ok) break;
+      if (lane == 0) arrive_local(smem_addr(z ? &bar.v_full[s] : &bar.k_full[s]));
     }
-    if (!__all_sync(kFull, tc_wait(smem_addr(&bar.rv_full), raw, abort) && tc_wait(smem_addr(&bar.v_empty[s]), ph ^ 1u, abort))) break;
-    decode(raw_v, smem_v + s * kAttTile, has, rows);
-    if (lane == 0) {
-      arrive_local(smem_addr(&bar.v_full[s]));
-      arrive_local(smem_addr(&bar.rv_empty));
-    }
+    if (!ok) break;
   }
 }
 
@@ -419,7 +522,7 @@ __device__ __forceinline__ void mma_role(const AttTcArgs& p, const AttWork& w, A
                                          uint32_t tmem, volatile int* abort) {
   const int steps = p.a.c.dim / 16;
   const uint32_t id_s = idesc_f16(kAttKeys, false), id_o = idesc_f16(p.a.c.dim, true);
-  bool ok = tc_wait(smem_addr(&bar.q_full), 0, abort);
+  bool ok = att_wait(bar.q_full, 0, abort);
   const auto scores = [&](int q, int s) {
     const uint64_t qd = desc_sw128(smem_q + q * kAttTile, 16u, 1024u), kd = desc_sw128(smem_k + s * kAttTile, 16u, 1024u);
     for (int k = 0; k < steps; ++k) {
@@ -436,11 +539,11 @@ __device__ __forceinline__ void mma_role(const AttTcArgs& p, const AttWork& w, A
   };
   for (int32_t t = w.t0; t <= w.t1 && ok; ++t) {   // scores of tile t, sums of the one before
     const int n = t - w.t0, s = n % kAttStages, before = (n + kAttStages - 1) % kAttStages;
-    if (t < w.t1 && !(ok = tc_wait(smem_addr(&bar.k_full[s]), (n / kAttStages) & 1, abort))) break;
-    if (n > 0 && !(ok = tc_wait(smem_addr(&bar.v_full[before]), ((n - 1) / kAttStages) & 1, abort))) break;
+    if (t < w.t1 && !(ok = att_wait(bar.k_full[s], (n / kAttStages) & 1, abort))) break;
+    if (n > 0 && !(ok = att_wait(bar.v_full[before], ((n - 1) / kAttStages) & 1, abort))) break;
     for (int q = 0; q < p.nq && ok; ++q) {
       if (n > 0) {
-        if (!(ok = tc_wait(smem_addr(&bar.p_full[q]), (n - 1) & 1, abort))) break;
+        if (!(ok = att_wait(bar.p_full[q], (n - 1) & 1, abort))) break;
         tc_fence_after();
         sums(q, before, n == 1);
         if (q == p.nq - 1) tc_commit<1>(smem_addr(&bar.v_empty[before]));
@@ -501,10 +604,12 @@ __global__ void __launch_bounds__(kAttThreads, 1) attention_tc_kernel(const __gr
       mbar_init(smem_addr(&bar.p_full[q]), 4);
     }
     for (int s = 0; s < kAttScales; ++s) mbar_init(smem_addr(&bar.scales[s]), 1);
-    mbar_init(smem_addr(&bar.rk_full), 1);
-    mbar_init(smem_addr(&bar.rv_full), 1);
-    mbar_init(smem_addr(&bar.rk_empty), kAttDecWarps);
-    mbar_init(smem_addr(&bar.rv_empty), kAttDecWarps);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(smem_addr(&bar.rk_full[h]), 1);
+      mbar_init(smem_addr(&bar.rv_full[h]), 1);
+      mbar_init(smem_addr(&bar.rk_empty[h]), kAttDecWarps);
+      mbar_init(smem_addr(&bar.rv_empty[h]), kAttDecWarps);
+    }
     mbar_init(smem_addr(&bar.q_full), 4 * p.nq);
     mbar_init(smem_addr(&bar.done), 1);
     mbar_init_fence();
@@ -530,10 +635,12 @@ __global__ void __launch_bounds__(kAttThreads, 1) attention_tc_kernel(const __gr
       if (w.t0 < w.t1 && elect_one()) mma_role(p, w, bar, smem_q, smem_k, smem_v, tmem, &s_abort);
       __syncwarp();
       // (after a wait has given up the others may come here before the last MMA has completed)
-      if (w.t0 < w.t1) tc_wait(smem_addr(&bar.done), 0, &s_abort);
+      if (w.t0 < w.t1) att_wait(bar.done, 0, &s_abort);
       if (s_abort) mbar_wait(smem_addr(&bar.done), 0, kTcWaitNs);
     } else if (warp == kAttSoftWarps + kAttDecWarps + 1) {
-      copy_role(p, w, bar, scales, raw_k, raw_v, &s_abort);
+      copy_role<true>(p, w, bar, scales, raw_k, &s_abort);
+    } else if (warp == kAttSoftWarps + kAttDecWarps + 2) {
+      copy_role<false>(p, w, bar, scales, raw_v, &s_abort);
     }
   }
   tc_fence_before();
@@ -580,7 +687,8 @@ qz_status launch_tc(const AttentionArgs& a, const TcAttPlan& plan, cudaStream_t 
   AttTcArgs p{};
   p.a = a;
   p.nq = plan.nq, p.splits = plan.splits, p.slots = plan.slots;
-  p.box = a.c.page % 128 == 0 ? 128 : a.c.page % 64 == 0 ? 64 : a.c.page % 32 == 0 ? 32 : 16;
+  p.out_wide = is_aligned(a.out, 16) && (a.b.tokens <= 1 || a.ld_out % 8 == 0) && (a.heads <= 1 || a.hd_out % 8 == 0);
+  p.box = a.c.page % 64 == 0 ? 64 : a.c.page % 32 == 0 ? 32 : 16;
   if (a.c.pages > 0 && !encode_maps(&p.maps, a, p.box)) return QZ_ERR_CUDA;
   const auto k = &attention_tc_kernel<FMT>;
   if (!set_dyn_smem(reinterpret_cast<const void*>(k), kAttSmem)) return QZ_ERR_CUDA;
