@@ -26,6 +26,27 @@ __device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
+// Bounded wait on phase `parity`.  The hint lets the hardware hold the warp until the phase completes: without it
+// try_wait comes back early, and the polls of a CTA's waiting warps took two fifths of the instructions issued.
+constexpr uint32_t kWaitHintNs = 1000000;
+__device__ __forceinline__ bool held_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(kWaitHintNs)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool held_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  if (held_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!held_try_wait(bar, parity))
+    if (globaltimer_ns() - t0 > limit_ns) return false;
+  return true;
+}
+
 // ---- one 8-bit pair to f16 ----------------------------------------------------------------------
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t d;

@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
     const int32_t w0 = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * warp / kWarps);
     const int32_t w1 = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * (warp + 1) / kWarps);
     for (int32_t st = w0; st < w1; ++st) {
-      failed = !__all_sync(kFull, mbar_wait(smem_addr(&s_full[warp][stage]), phase, kFewWaitNs)) || failed;
+      failed = !__all_sync(kFull, held_wait(smem_addr(&s_full[warp][stage]), phase, kFewWaitNs)) || failed;
       if (failed) break;
       const uint32_t from = ring + stage * Z::kStage;
       const int32_t has = s_has[warp][stage];
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
   }
   if (failed) {  // copies still in flight land before the memory is released
     for (int i = 0; i < kStages; ++i) {
-      mbar_wait(smem_addr(&s_full[warp][stage]), phase, kFewWaitNs);
+      held_wait(smem_addr(&s_full[warp][stage]), phase, kFewWaitNs);
       if (++stage == kStages) {
         stage = 0;
         phase ^= 1u;

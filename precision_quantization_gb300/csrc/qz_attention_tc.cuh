@@ -48,20 +48,16 @@ struct AttTcArgs {
   CacheMaps maps;
 };
 
-// Bounded wait on phase `parity`; the clock is looked at now and then only.
+// Bounded wait on phase `parity`.
 __device__ __forceinline__ bool att_wait(uint64_t& bar, uint32_t parity, volatile int* abort) {
   const uint32_t at = smem_addr(&bar);
-  if (mbar_try_wait(at, parity)) return true;
-  uint64_t t0 = 0;
-  for (uint32_t i = 1; !mbar_try_wait(at, parity); ++i) {
-    if (i % 64 == 0) {
-      if (*abort) return false;
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > kTcWaitNs) {
-        *abort = 1;
-        return false;
-      }
+  if (held_try_wait(at, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!held_try_wait(at, parity)) {
+    if (*abort) return false;
+    if (globaltimer_ns() - t0 > kTcWaitNs) {
+      *abort = 1;
+      return false;
     }
   }
   return true;
