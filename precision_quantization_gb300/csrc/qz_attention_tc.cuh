@@ -77,8 +77,7 @@ __device__ __forceinline__ void tmem_load32(uint32_t at, float (&v)[32]) {
         "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]),
         "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]),
         "=f"(v[31])
-      : "r"(at)
-      : "memory");
+      : "r"(at));
 }
 // every load before it has landed; the registers are handed on, so that nothing reads them earlier
 __device__ __forceinline__ void tmem_wait32(float (&v)[32]) {
@@ -86,13 +85,13 @@ __device__ __forceinline__ void tmem_wait32(float (&v)[32]) {
                : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]),
                  "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]),
                  "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]),
-                 "+f"(v[31])::"memory");
+                 "+f"(v[31]));
 }
 __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at), "r"(v[0]), "r"(v[1]),
                "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]),
                "r"(v[14]), "r"(v[15])
-               : "memory");
+               );
 }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint64_t add_pairs(uint64_t a, uint64_t b) {
@@ -147,28 +146,31 @@ __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& 
   const int i = row / a.group, head = w.kvh * a.group + row % a.group;
   const int64_t token = w.sp.row + i, pos = w.sp.p0 + i;
   // The warp's 32 rows of q as f16, K-major panels of 64 elements, 128-byte swizzle: a row at a time, four elements a
-  // lane, eight rows' loads in flight.  Lane r keeps row r's factor.
+  // lane, eight rows' loads and shuffles side by side.  Lane r keeps row r's factor.
   float fq = 0.0f;
-  const int32_t left = min(w.rows - (w.row0 + q * kAttRows + 32 * warp), 32);  // of the warp's rows
+  const int32_t left = w.rows - (w.row0 + q * kAttRows);  // of the tile's rows
 #pragma unroll 1
-  for (int r0 = 0; r0 < 32; r0 += 8) {
-    float x[8][4];
+  for (int r0 = 32 * warp; r0 < 32 * warp + 32; r0 += 8) {
+    float x[8][4], top[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const bool in = r0 + k < left && 4 * lane < dim;
-      const int rr = in ? w.row0 + q * kAttRows + 32 * warp + r0 + k : w.row0, ri = rr / a.group;
+      const int rr = in ? w.row0 + q * kAttRows + r0 + k : w.row0, ri = rr / a.group;
       load_q4_masked(a, in, (w.sp.row + ri) * a.ld_q + (w.kvh * a.group + rr - ri * a.group) * a.hd_q + (in ? 4 * lane : 0), x[k]);
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float top = absmax_nan(absmax_nan(absmax_nan(fabsf(x[k][0]), x[k][1]), x[k][2]), x[k][3]);
+    for (int k = 0; k < 8; ++k) top[k] = absmax_nan(absmax_nan(absmax_nan(fabsf(x[k][0]), x[k][1]), x[k][2]), x[k][3]);
 #pragma unroll
-      for (int o = 16; o; o >>= 1) top = absmax_nan(top, __shfl_xor_sync(kFull, top, o));
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top[k] = absmax_nan(top[k], __shfl_xor_sync(kFull, top[k], o));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
       float down;
-      const float up = q_unit(top, down);
-      if (lane == r0 + k) fq = down * a.scale;
+      const float up = q_unit(top[k], down);
+      if (32 * warp + lane == r0 + k) fq = down * a.scale;
       if (4 * lane < dim) {
-        const int line = 32 * warp + r0 + k;
+        const int line = r0 + k;
         const uint32_t at = smem_q + q * kAttTile + (lane >> 4) * kAttPanel + line * 128 + ((((lane >> 1) & 7) ^ (line & 7)) << 4) + (lane & 1) * 8;
         asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(f16x2_bits(x[k][0] * up, x[k][1] * up)),
                      "r"(f16x2_bits(x[k][2] * up, x[k][3] * up))
