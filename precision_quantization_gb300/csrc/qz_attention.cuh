@@ -116,6 +116,15 @@ __device__ __forceinline__ void load_q4(const AttentionArgs& a, bool in, int64_t
     for (int e = 0; e < 4; ++e) x[e] = bf16_float(__ldg(a.q + at + e));
   }
 }
+// the same as bf16 pairs
+__device__ __forceinline__ uint2 load_q4_raw(const AttentionArgs& a, bool in, int64_t at) {
+  if (!in) return make_uint2(0u, 0u);
+  if (a.q_vec) return __ldg(reinterpret_cast<const uint2*>(a.q + at));
+  uint32_t x[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = __ldg(a.q + at + e);
+  return make_uint2(x[0] | (x[1] << 16), x[2] | (x[3] << 16));
+}
 // The power of two that brings a row whose largest magnitude is `top` into [2^14, 2^15), and its inverse;
 // elements 2^-38 of the largest and less lose bits, 2^-40 of it at most.  NaN for a row that is not finite.
 __device__ __forceinline__ float q_unit(float top, float& down) {

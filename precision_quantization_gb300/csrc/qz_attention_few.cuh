@@ -65,7 +65,7 @@ struct FewSizes {
   static constexpr uint32_t kHalf = 16 * DP;                             // bytes of 16 tokens' keys or values
   static constexpr uint32_t kStage = 2 * kHalves * kHalf;                // keys, then values
   static constexpr uint32_t kQ = NT * (DP / 16) * 256;                   // q as B operands
-  static constexpr int kJoinCols = 32;                                   // columns joined at a time
+  static constexpr int kJoinCols = NT == 1 ? 64 : 32;                    // columns joined at a time
   static constexpr uint32_t kJoin = kWarps * kRows * kJoinCols * 4;
   static constexpr int kRoom = 226 * 1024 - 1024 - 4096 - static_cast<int>(kQ + kJoin);  // 4 KiB: static
   static constexpr int kStages = kRoom / static_cast<int>(kWarps * kStage) < 4 ? kRoom / static_cast<int>(kWarps * kStage) : 4;
@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
   __shared__ int64_t s_scan[kWarps + 1], s_found[2];
   __shared__ float s_fq[kRows], s_m[kWarps][kRows], s_l[kWarps][kRows], s_unit[kWarps];
   __shared__ int32_t s_end[kRows], s_begin[kRows];
+  __shared__ float s_top[kRows], s_sum[kRows];
   __shared__ __align__(16) float s_scale[kWarps][kStages][4];  // ks, vs of the first 16 tokens, of the second
   __shared__ int32_t s_has[kWarps][kStages];                   // bit i: the i-th 16 tokens have a page
   __shared__ __align__(8) uint64_t s_full[kWarps][kStages];
@@ -142,12 +143,14 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
   const auto work_of = [&](const SeqWork& w) { return static_cast<int64_t>(w.tiles) * a.c.heads * (WHOLE ? 1 : w.steps); };
   const auto units_of = [&](int32_t s) { return s < a.b.seqs ? work_of(seq_work(a, s, kRows, kStep)) : 0; };
   int64_t u0, u1, chunk = 1, before = 0;
+  const bool few = a.b.seqs <= Z::kThreads;  // one look at the lengths does
+  int64_t mine = few || !WHOLE ? units_of(tid) : 0;
   if (!WHOLE) {
-    int64_t mine = 0;
-    for (int32_t s = tid; s < a.b.seqs; s += Z::kThreads) mine += units_of(s);
+    int64_t sum = mine;
+    for (int32_t s = tid + Z::kThreads; s < a.b.seqs; s += Z::kThreads) sum += units_of(s);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(kFull, mine, o);
-    if (lane == 0) s_scan[warp] = mine;
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    if (lane == 0) s_scan[warp] = sum;
     __syncthreads();
     int64_t total = 0;
 #pragma unroll
@@ -164,7 +167,8 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
   if (u0 >= u1) return;
   bool found = false;  // the sequence that holds unit u0
   for (int32_t s0 = 0; s0 < a.b.seqs && !found; s0 += Z::kThreads) {
-    const int64_t mine = units_of(s0 + tid), in_warp = warp_scan(mine, lane);
+    if (!few) mine = units_of(s0 + tid);
+    const int64_t in_warp = warp_scan(mine, lane);
     if (lane == 31) s_scan[warp] = in_warp;
     __syncthreads();
     int64_t at = before + in_warp, all = before;
@@ -276,12 +280,28 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
     }
     c_stage = c_stage + 1 == kStages ? 0 : c_stage + 1;
   };
+  // this warp's rows of the next segment's q, on their way before its codes are asked for (behind those they take
+  // four times as long)
+  constexpr int kQRows = (kRows + kWarps - 1) / kWarps;
+  uint2 q_next[kQRows][kPieces];
+  const auto ask_q = [&](const Segment& s) {
+#pragma unroll
+    for (int j = 0; j < kQRows; ++j) {
+      const int r = warp + j * kWarps, i = (s.row0 + r) / a.group, head = s.kvh * a.group + (s.row0 + r) - i * a.group;
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        const int d = 4 * (lane + 32 * k);
+        q_next[j][k] = load_q4_raw(a, r < s.rows && d < a.c.dim, (s.w.sp.row + i) * a.ld_q + head * a.hd_q + d);
+      }
+    }
+  };
   int stage = 0;
   uint32_t phase = 0;
   bool failed = false;   // a wait has given up: this CTA's results are NaN
   __syncwarp();
   bool more = advance();
   if (more) {
+    ask_q(n);
     aim(n);
 #pragma unroll 1
     for (int i = 0; i < kStages; ++i) copy();
@@ -290,14 +310,17 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
   while (more) {
     const Segment s = n;
     // ---- q as f16 B operands, row by row; what each row sees ------------------------------------
-    for (int r = warp; r < kRows; r += kWarps) {
-      const int i = (s.row0 + r) / a.group, head = s.kvh * a.group + (s.row0 + r) % a.group;
+#pragma unroll
+    for (int j = 0; j < kQRows; ++j) {
+      const int r = warp + j * kWarps, i = (s.row0 + r) / a.group;
+      if (r >= kRows) break;
       float x[kPieces][4];
       float top = 0.0f;
 #pragma unroll
       for (int k = 0; k < kPieces; ++k) {
-        const int d = 4 * (lane + 32 * k);
-        load_q4(a, r < s.rows && d < a.c.dim, (s.w.sp.row + i) * a.ld_q + head * a.hd_q + d, x[k]);
+        const uint2 b = q_next[j][k];
+        x[k][0] = __uint_as_float(b.x << 16), x[k][1] = __uint_as_float(b.x & 0xffff0000u);
+        x[k][2] = __uint_as_float(b.y << 16), x[k][3] = __uint_as_float(b.y & 0xffff0000u);
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = absmax_nan(top, x[k][e]);
       }
@@ -526,12 +549,13 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
     }
     more = advance();
     if (more && !failed) {  // the next segment's first steps are on their way while the sums are joined
+      ask_q(n);
       aim(n);
 #pragma unroll 1
       for (int i = 0; i < kStages; ++i) copy();
     }
 
-    // ---- the warps' sums, four columns of each of the eight column groups at a time ----------------
+    // ---- the warps' sums, joined some columns at a time ------------------------------------------
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -546,39 +570,54 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
     if (lane == 0) s_unit[warp] = unit;
     const bool first = s.t0 == 0, last = s.t1 == s.w.steps;
     float* slot = WHOLE || (first && last) ? nullptr : slots + (2 * static_cast<size_t>(blockIdx.x) + (first ? 1 : 0)) * Z::kSlot;
+    constexpr int kQuads = Z::kJoinCols / 32;    // float4s of each of the eight column groups at a time
 #pragma unroll
-    for (int q = 0; q < kCols / 4; ++q) {
+    for (int q = 0; q < kCols / 4; q += kQuads) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int z = 0; z < kQuads; ++z)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<float4*>(join + ((warp * kRows + 8 * t + 2 * c + e) * 8 + g) * 4) =
-              make_float4(o[t][2 * q][e], o[t][2 * q][2 + e], o[t][2 * q + 1][e], o[t][2 * q + 1][2 + e]);
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)  // [warp][row][z][column group]
+            *reinterpret_cast<float4*>(join + (((warp * kRows + 8 * t + 2 * c + e) * kQuads + z) * 8 + g) * 4) =
+                make_float4(o[t][2 * (q + z)][e], o[t][2 * (q + z)][2 + e], o[t][2 * (q + z) + 1][e], o[t][2 * (q + z) + 1][2 + e]);
       __syncthreads();
-      for (int i = tid; i < kRows * 8; i += Z::kThreads) {
-        const int r = i >> 3, d = kCols * (i & 7) + 4 * q;
-        if (r >= s.rows) break;
-        float top = kNone, l = 0.0f;
+      if (q == 0) {  // each warp's factor for the row's sums, in place of its maximum; the row's own m and l
+        for (int r = tid; r < kRows; r += Z::kThreads) {
+          float top = kNone, l = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) top = fmaxf(top, s_m[k][r]);
-        const float from = top == kNone ? 0.0f : top;
+          for (int k = 0; k < kWarps; ++k) top = fmaxf(top, s_m[k][r]);
+          const float from = top == kNone ? 0.0f : top;
+#pragma unroll
+          for (int k = 0; k < kWarps; ++k) {
+            const float f = ex2(s_m[k][r] - from);
+            l = __fmaf_rn(s_l[k][r], f, l);
+            s_m[k][r] = f * s_unit[k] * 0x1p-15f;
+          }
+          s_top[r] = top, s_sum[r] = l;
+        }
+        __syncthreads();
+      }
+      for (int i = tid; i < kRows * 8 * kQuads; i += Z::kThreads) {
+        const int r = i / (8 * kQuads), d = kCols * (i & 7) + 4 * (q + (i >> 3) % kQuads);
+        if (r >= s.rows) break;
         float v[4] = {};
 #pragma unroll
         for (int k = 0; k < kWarps; ++k) {
-          const float f = ex2(s_m[k][r] - from), fo = f * s_unit[k] * 0x1p-15f;
-          const float4 y = *reinterpret_cast<const float4*>(join + ((k * kRows + r) * 8 + (i & 7)) * 4);
-          l = __fmaf_rn(s_l[k][r], f, l);
-          v[0] = __fmaf_rn(y.x, fo, v[0]), v[1] = __fmaf_rn(y.y, fo, v[1]);
-          v[2] = __fmaf_rn(y.z, fo, v[2]), v[3] = __fmaf_rn(y.w, fo, v[3]);
+          const float f = s_m[k][r];
+          const float4 y = *reinterpret_cast<const float4*>(join + (k * kRows * kQuads * 8 + i) * 4);
+          v[0] = __fmaf_rn(y.x, f, v[0]), v[1] = __fmaf_rn(y.y, f, v[1]);
+          v[2] = __fmaf_rn(y.z, f, v[2]), v[3] = __fmaf_rn(y.w, f, v[3]);
         }
         if (slot) {
           *reinterpret_cast<float4*>(slot + r * DP + d) = make_float4(v[0], v[1], v[2], v[3]);
           if (d == 0) {
-            slot[kRows * DP + r] = top;
-            slot[kRows * (DP + 1) + r] = l;
+            slot[kRows * DP + r] = s_top[r];
+            slot[kRows * (DP + 1) + r] = s_sum[r];
           }
         } else {
-          store_row(a, s.w.sp.row + (s.row0 + r) / a.group, s.kvh * a.group + (s.row0 + r) % a.group, d, v, top, l);
+          const int i0 = (s.row0 + r) / a.group;
+          store_row(a, s.w.sp.row + i0, s.kvh * a.group + (s.row0 + r) - i0 * a.group, d, v, s_top[r], s_sum[r]);
         }
       }
       __syncthreads();
