@@ -583,18 +583,17 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
                 make_float4(o[t][2 * (q + z)][e], o[t][2 * (q + z)][2 + e], o[t][2 * (q + z) + 1][e], o[t][2 * (q + z) + 1][2 + e]);
       __syncthreads();
       if (q == 0) {  // each warp's factor for the row's sums, in place of its maximum; the row's own m and l
-        for (int r = tid; r < kRows; r += Z::kThreads) {
-          float top = kNone, l = 0.0f;
+        for (int r = warp; r < kRows; r += kWarps) {  // lane k: warp k's
+          const float m = lane < kWarps ? s_m[lane < kWarps ? lane : 0][r] : kNone;
+          float top = m;
 #pragma unroll
-          for (int k = 0; k < kWarps; ++k) top = fmaxf(top, s_m[k][r]);
-          const float from = top == kNone ? 0.0f : top;
+          for (int w = 8; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, w));
+          const float f = ex2(m - (top == kNone ? 0.0f : top));
+          float l = lane < kWarps ? f * s_l[lane < kWarps ? lane : 0][r] : 0.0f;
 #pragma unroll
-          for (int k = 0; k < kWarps; ++k) {
-            const float f = ex2(s_m[k][r] - from);
-            l = __fmaf_rn(s_l[k][r], f, l);
-            s_m[k][r] = f * s_unit[k] * 0x1p-15f;
-          }
-          s_top[r] = top, s_sum[r] = l;
+          for (int w = 8; w; w >>= 1) l += __shfl_xor_sync(kFull, l, w);
+          if (lane < kWarps) s_m[lane][r] = f * s_unit[lane] * 0x1p-15f;
+          if (lane == 0) s_top[r] = top, s_sum[r] = l;
         }
         __syncthreads();
       }
