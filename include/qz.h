@@ -609,8 +609,8 @@ QZ_API qz_status qz_cache_append(const qz_cache* cache, const qz_batch* batch, i
  *   lse      fp32 [tokens, heads] (leading dimension ld_lse) or NULL: log sum exp of the visible scores,
  *            -inf where there are none
  *   scale    a finite number > 0
- *   ws, ws_bytes  qz_cache_attention_workspace bytes of device memory, uninitialised, 16-byte aligned;
- *            calls that may overlap need one each
+ *   ws, ws_bytes  qz_cache_attention_workspace bytes of device memory (of these sizes; 0: ws may be NULL), uninitialised,
+ *            16-byte aligned; calls that may overlap need one each
  * Rows that belong to no sequence are left as they are.
  * Arithmetic: scores are sums of exact products of q and decoded codes in fp32, the keys' scale applied to
  * the sum; weights p times the values' scale are rounded to 11 bits (f16; from 2^-22 of the sequence's largest
@@ -619,7 +619,8 @@ QZ_API qz_status qz_cache_append(const qz_cache* cache, const qz_batch* batch, i
  * others.  Scales are not negative.  Codes and scales of positions past a sequence's length are not looked at.
  * Waits inside the kernels are bounded (1 s); should one give up, the outputs it stands for are NaN.
  * Errors: as above; QZ_ERR_WORKSPACE. */
-QZ_API size_t qz_cache_attention_workspace(const qz_cache* cache, int64_t sequences, int64_t tokens, int64_t heads);
+QZ_API size_t qz_cache_attention_workspace(const qz_cache* cache, int64_t sequences, int64_t tokens, int64_t heads,
+                                           int64_t table_pages);
 QZ_API qz_status qz_cache_attention(const qz_cache* cache, const qz_batch* batch, const void* q, int64_t ld_q,
                                     int64_t hd_q, int64_t tokens, int64_t heads, float scale, int64_t window,
                                     void* out, int64_t ld_out, int64_t hd_out, float* lse, int64_t ld_lse,

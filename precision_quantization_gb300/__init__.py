@@ -160,7 +160,7 @@ def lib():
             "qz_rotary_backward": (i32, [rp, i32, vp, i64, i64, i64, i64, i64, vp, vp, i64, i64, vp]),
             "qz_cache_append": (i32, [cp, bp, i32, vp, i64, i64, vp, i64, i64, i64, rp, vp, i64, i64,
                                       i64, vp, i64, i64, vp]),
-            "qz_cache_attention_workspace": (C.c_size_t, [cp, i64, i64, i64]),
+            "qz_cache_attention_workspace": (C.c_size_t, [cp, i64, i64, i64, i64]),
             "qz_cache_attention": (i32, [cp, bp, vp, i64, i64, i64, i64, C.c_float, i64, vp, i64, i64,
                                          vp, i64, vp, C.c_size_t, vp]),
         }
@@ -365,8 +365,8 @@ def qz_cache_append(cache: QzCache, batch: QzBatch, dtype: int, k: int, ld_k: in
                                  hd_q, heads, q_out, ld_qo, hd_qo, stream)
 
 
-def qz_cache_attention_workspace(cache: QzCache, sequences: int, tokens: int, heads: int) -> int:
-    return lib().qz_cache_attention_workspace(cache, sequences, tokens, heads)
+def qz_cache_attention_workspace(cache: QzCache, sequences: int, tokens: int, heads: int, table_pages: int) -> int:
+    return lib().qz_cache_attention_workspace(cache, sequences, tokens, heads, table_pages)
 
 
 def qz_cache_attention(cache: QzCache, batch: QzBatch, q: int, ld_q: int, hd_q: int, tokens: int,
@@ -971,10 +971,10 @@ def _vectors(t, heads: int | None, dim: int | None, dtype, what: str, device: in
     raise ValueError(f"{what} must be a [tokens, {heads or 'heads'}, {dim or 'dim'}] {dtype or ''} tensor, not {tuple(t.shape)} {t.dtype}")
 
 
-def _ints(t, shape: tuple, what: str, device: int):
-    """The address of a contiguous int32 tensor of `shape` on GPU `device`."""
-    if t.dtype is not _torch().int32 or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
-        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {tuple(shape)} on cuda:{device}")
+def _ints(t, n: int, what: str, device: int):
+    """The address of a contiguous int32 vector of n values on GPU `device`."""
+    if t.dtype is not _torch().int32 or t.shape != (n,) or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{what} must be a contiguous int32 vector of {n} values on cuda:{device}")
     return t.data_ptr()
 
 
@@ -983,19 +983,20 @@ def _rotary_call(name: str, x, table: RotaryTable, positions, out, stream, what:
     if stream is not None or (device >= 0 and device != torch._C._cuda_getDevice()):
         with _on(stream, x):
             return _rotary_call(name, x, table, positions, out, None, what)
-    code = _dtype_code(x.dtype)
+    dt = x.dtype
+    code = QZ_BF16 if dt is torch.bfloat16 else _dtype_code(dt)
     ld_x, hd_x = _vectors(x, None, None, None, what, device)
     tokens, heads, dim = x.shape
     if table.device != device:
         raise ValueError(f"the table must be on cuda:{device}")
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x) if ld_x == heads * dim and hd_x == dim else torch.empty((tokens, heads, dim), dtype=dt, device=x.device)
         ld_y, hd_y = heads * dim, dim
     else:
-        ld_y, hd_y = _vectors(out, heads, dim, x.dtype, "out", device)
+        ld_y, hd_y = _vectors(out, heads, dim, dt, "out", device)
         _same_tokens(tokens, out=out)
     rc = getattr(_lib or lib(), name)(table.desc, code, x.data_ptr(), ld_x, hd_x, tokens, heads, dim,
-                                      None if positions is None else _ints(positions, (tokens,), "positions", device),
+                                      None if positions is None else _ints(positions, tokens, "positions", device),
                                       out.data_ptr(), ld_y, hd_y, torch._C._cuda_getCurrentRawStream(device))
     if rc:
         raise QzError(rc, name)
@@ -1071,22 +1072,26 @@ class KVCache:
         return cls(codes[0], scales[0], codes[1], scales[1], fmt)
 
 
-def _batch(table, lengths, starts, tokens: int, device: int) -> QzBatch:
+def _batch(table, lengths, starts, tokens: int, device: int, i32) -> QzBatch:
     """The sequences of a call: table int32 [sequences, pages], rows at any stride."""
-    if lengths.dim() != 1:
-        raise ValueError("lengths must be a vector")
-    n = lengths.shape[0]
-    if (table.dim() != 2 or table.dtype is not _torch().int32 or table.shape[0] != n or table.get_device() != device
-            or (table.shape[1] > 1 and n > 0 and table.stride(1) != 1)):
+    shape, stride = table.shape, table.stride()
+    n = lengths.shape[0] if lengths.dim() == 1 else -1
+    if (len(shape) != 2 or shape[0] != n or table.dtype is not i32 or table.get_device() != device
+            or (stride[1] != 1 and shape[1] > 1 and n > 0)):
+        if n < 0:
+            raise ValueError("lengths must be a vector")
         raise ValueError(f"table must be an int32 [{n}, pages] tensor on cuda:{device} with contiguous rows")
-    width = table.shape[1]
-    ld = table.stride(0) if n > 1 else width
+    width = shape[1]
+    ld = stride[0] if n > 1 else width
     if ld < width:
         raise ValueError("table: rows overlap")
-    if starts is None and tokens != n:
-        raise ValueError(f"without starts each of the {n} sequences has one token, not {tokens} in all")
-    return QzBatch(n, table.data_ptr(), ld, width, _ints(lengths, (n,), "lengths", device),
-                   None if starts is None else _ints(starts, (n + 1,), "starts", device))
+    if lengths.dtype is not i32 or lengths.get_device() != device or not lengths.is_contiguous():
+        raise ValueError(f"lengths must be a contiguous int32 vector on cuda:{device}")
+    if starts is None:
+        if tokens != n:
+            raise ValueError(f"without starts each of the {n} sequences has one token, not {tokens} in all")
+        return QzBatch(n, table.data_ptr(), ld, width, lengths.data_ptr(), None)
+    return QzBatch(n, table.data_ptr(), ld, width, lengths.data_ptr(), _ints(starts, n + 1, "starts", device))
 
 
 def cache_append(cache: KVCache, k, v, table, lengths, starts=None, rotary: RotaryTable | None = None,
@@ -1101,28 +1106,33 @@ def cache_append(cache: KVCache, k, v, table, lengths, starts=None, rotary: Rota
     if stream is not None or (device >= 0 and device != torch._C._cuda_getDevice()):
         with _on(stream, k):
             return cache_append(cache, k, v, table, lengths, starts, rotary, q, out)
-    dt, code = k.dtype, _dtype_code(k.dtype)
+    dt = k.dtype
+    code = QZ_BF16 if dt is torch.bfloat16 else _dtype_code(dt)
     ld_k, hd_k = _vectors(k, cache.kv_heads, cache.dim, dt, "k", device)
     ld_v, hd_v = _vectors(v, cache.kv_heads, cache.dim, dt, "v", device)
     tokens = k.shape[0]
-    _same_tokens(tokens, v=v)
+    if v.shape[0] != tokens:
+        _same_tokens(tokens, v=v)
     if cache.device != device or (rotary is not None and rotary.device != device):
         raise ValueError(f"the cache and the rotary table must be on cuda:{device}")
-    batch = _batch(table, lengths, starts, tokens, device)
+    batch = _batch(table, lengths, starts, tokens, device, torch.int32)
     heads = ld_q = hd_q = ld_o = hd_o = 0
     if q is not None:
         if rotary is None:
             raise ValueError("q takes a rotary table")
-        heads = q.shape[1] if q.dim() == 3 else None
-        ld_q, hd_q = _vectors(q, heads, cache.dim, dt, "q", device)
+        dim = cache.dim
+        ld_q, hd_q = _vectors(q, None, dim, dt, "q", device)
+        n, heads, _ = q.shape
         if heads % cache.kv_heads:
             raise ValueError(f"q must have a multiple of {cache.kv_heads} heads, not {heads}")
+        if n != tokens:
+            _same_tokens(tokens, q=q)
         if out is None:
-            out = torch.empty((tokens, heads, cache.dim), dtype=dt, device=q.device)
-            ld_o, hd_o = heads * cache.dim, cache.dim
+            out = torch.empty_like(q) if ld_q == heads * dim and hd_q == dim else torch.empty((tokens, heads, dim), dtype=dt, device=q.device)
+            ld_o, hd_o = heads * dim, dim
         else:
-            ld_o, hd_o = _vectors(out, heads, cache.dim, dt, "out", device)
-        _same_tokens(tokens, q=q, out=out)
+            ld_o, hd_o = _vectors(out, heads, dim, dt, "out", device)
+            _same_tokens(tokens, out=out)
     elif out is not None:
         raise ValueError("out is for the rotated queries")
     rc = (_lib or lib()).qz_cache_append(cache.desc, batch, code, k.data_ptr(), ld_k, hd_k, v.data_ptr(), ld_v, hd_v, tokens,
@@ -1154,10 +1164,11 @@ def cache_attention(q, cache: KVCache, table, lengths, starts=None, scale: float
         raise ValueError(f"the cache must be on cuda:{device}")
     if window is not None and window < 1:
         raise ValueError("window must be one position or more")
-    batch = _batch(table, lengths, starts, tokens, device)
+    batch = _batch(table, lengths, starts, tokens, device, torch.int32)
     logs, ld_lse = None, heads
     if out is None:
-        y, ld_o, hd_o = torch.empty((tokens, heads, dim), dtype=bf, device=q.device), heads * dim, dim
+        y = torch.empty_like(q) if ld_q == heads * dim and hd_q == dim else torch.empty((tokens, heads, dim), dtype=bf, device=q.device)
+        ld_o, hd_o = heads * dim, dim
         if lse:
             logs = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
     else:
@@ -1168,15 +1179,17 @@ def cache_attention(q, cache: KVCache, table, lengths, starts=None, scale: float
             ld_lse = _matrix(logs, heads, torch.float32, "lse", device)
             _same_tokens(tokens, lse=logs)
     L = _lib or lib()
-    need = L.qz_cache_attention_workspace(cache.desc, batch.sequences, tokens, heads)
     if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=q.device) if need else None
+        ws_bytes = L.qz_cache_attention_workspace(cache.desc, batch.sequences, tokens, heads, batch.table_pages)
+        if ws_bytes:
+            workspace = torch.empty((ws_bytes,), dtype=torch.uint8, device=q.device)
     elif workspace.get_device() != device or not workspace.is_contiguous():
         raise ValueError(f"the workspace must be contiguous on cuda:{device}")
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
     rc = L.qz_cache_attention(cache.desc, batch, q.data_ptr(), ld_q, hd_q, tokens, heads,
                               dim ** -0.5 if scale is None else scale, window or 0, y.data_ptr(), ld_o, hd_o, _ptr(logs), ld_lse,
-                              _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0,
-                              torch._C._cuda_getCurrentRawStream(device))
+                              _ptr(workspace), ws_bytes, torch._C._cuda_getCurrentRawStream(device))
     if rc:
         raise QzError(rc, "qz_cache_attention")
     return (y, logs) if lse else y

@@ -52,13 +52,14 @@ TcAttPlan tc_att_plan(const qz_cache& c, int64_t seqs, int64_t tokens, int64_t h
 
 using namespace qz;
 
-extern "C" size_t qz_cache_attention_workspace(const qz_cache* cache, int64_t sequences, int64_t tokens, int64_t heads) {
-  if (check_cache(cache) != QZ_OK || sequences <= 0 || tokens <= 0 || heads <= 0) return 0;
-  if (heads % cache->kv_heads || tokens > (1 << 30) || heads > INT32_MAX / cache->dim || sequences > (1 << 24)) return 0;
+extern "C" size_t qz_cache_attention_workspace(const qz_cache* cache, int64_t sequences, int64_t tokens, int64_t heads,
+                                               int64_t table_pages) {
+  if (check_cache(cache) != QZ_OK || sequences <= 0 || tokens <= 0 || heads <= 0 || table_pages < 0) return 0;
+  if (heads % cache->kv_heads || tokens > (1 << 30) || heads > INT32_MAX / cache->dim || sequences > (1 << 24) || table_pages > (1 << 24)) return 0;
   const int sms = sm_count();
-  const TcAttPlan tc = tc_att_plan(*cache, sequences, tokens, heads, INT32_MAX, sms);
-  if (tc.grid) return std::max<size_t>(tc_att_workspace(tc, tokens, heads, cache->dim), 16);
-  return few_att_workspace(few_att_plan(*cache, sequences, tokens, heads, INT32_MAX, sms), cache->dim);
+  const TcAttPlan tc = tc_att_plan(*cache, sequences, tokens, heads, table_pages, sms);
+  if (tc.grid) return tc_att_workspace(tc, tokens, heads, cache->dim);
+  return few_att_workspace(few_att_plan(*cache, sequences, tokens, heads, table_pages, sms), cache->dim);
 }
 
 extern "C" qz_status qz_cache_attention(const qz_cache* cache, const qz_batch* batch, const void* q, int64_t ld_q, int64_t hd_q,
@@ -75,7 +76,11 @@ extern "C" qz_status qz_cache_attention(const qz_cache* cache, const qz_batch* b
   if (tokens == 0 || heads == 0 || batch->sequences == 0) return QZ_OK;
   if (!q || !out) return QZ_ERR_NULL;
   if (!is_aligned(q, 2) || !is_aligned(out, 2) || !is_aligned(lse, 4)) return QZ_ERR_ALIGN;
-  if (!ws || ws_bytes < qz_cache_attention_workspace(cache, batch->sequences, tokens, heads)) return QZ_ERR_WORKSPACE;
+  const int sms = sm_count();
+  const TcAttPlan tc = tc_att_plan(*cache, batch->sequences, tokens, heads, batch->table_pages, sms);
+  const FewPlan few = few_att_plan(*cache, batch->sequences, tokens, heads, batch->table_pages, sms);
+  const size_t need = tc.grid ? tc_att_workspace(tc, tokens, heads, cache->dim) : few_att_workspace(few, cache->dim);
+  if (need && (!ws || ws_bytes < need)) return QZ_ERR_WORKSPACE;
   if (!is_aligned(ws, 16)) return QZ_ERR_ALIGN;
   AttentionArgs a{};
   a.c = view_of(*cache);
@@ -91,15 +96,12 @@ extern "C" qz_status qz_cache_attention(const qz_cache* cache, const qz_batch* b
   a.q_vec = pieces(q, ld_q, hd_q), a.out_vec = pieces(out, ld_out, hd_out);
   a.ws = ws;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int sms = sm_count();
-  const TcAttPlan tc = tc_att_plan(*cache, batch->sequences, tokens, heads, batch->table_pages, sms);
   if (tc.grid) {
     if (cache->format == QZ_INT8) return launch_attention_tc_int8(a, tc, s);
     if (cache->format == QZ_FP8_E4M3) return launch_attention_tc_e4m3(a, tc, s);
     return launch_attention_tc_e5m2(a, tc, s);
   }
-  const FewPlan plan = few_att_plan(*cache, batch->sequences, tokens, heads, batch->table_pages, sms);
-  if (cache->format == QZ_INT8) return launch_attention_few_int8(a, plan, s);
-  if (cache->format == QZ_FP8_E4M3) return launch_attention_few_e4m3(a, plan, s);
-  return launch_attention_few_e5m2(a, plan, s);
+  if (cache->format == QZ_INT8) return launch_attention_few_int8(a, few, s);
+  if (cache->format == QZ_FP8_E4M3) return launch_attention_few_e4m3(a, few, s);
+  return launch_attention_few_e5m2(a, few, s);
 }

@@ -93,7 +93,7 @@ def test_append_errors(qz):
 
 
 def test_attention_errors(qz):
-    need = qz.qz_cache_attention_workspace(cache(qz), 3, 5, 4)
+    need = qz.qz_cache_attention_workspace(cache(qz), 3, 5, 4, 4)
     f = lambda c=cache(qz), b=batch(qz), q=FAKE, lq=256, hq=64, n=5, h=4, s=0.1, w=0, o=FAKE, lo=256, ho=64, l=FAKE, ll=4, ws=FAKE, wb=need: (  # noqa: E731, E741
         qz.qz_cache_attention(c, b, q, lq, hq, n, h, s, w, o, lo, ho, l, ll, ws, wb))
     for bad, err in CACHES:
@@ -106,12 +106,14 @@ def test_attention_errors(qz):
         assert f(s=s) == qz.QZ_ERR_SHAPE
     assert f(q=FAKE + 1) == f(o=FAKE + 1) == f(l=FAKE + 2) == qz.QZ_ERR_ALIGN
     assert f(n=(1 << 30) + 1) == qz.QZ_ERR_UNSUPPORTED
-    if need:
-        assert f(ws=None) == f(wb=need - 1) == qz.QZ_ERR_WORKSPACE and f(ws=FAKE + 8) == qz.QZ_ERR_ALIGN
+    assert need == 0 and f(ws=FAKE + 8) == qz.QZ_ERR_ALIGN  # such short sequences take none
+    long = batch(qz, ld=4000, width=4000)
+    need = qz.qz_cache_attention_workspace(cache(qz), 3, 5, 4, 4000)
+    assert need > 0 and f(b=long, ws=None) == f(b=long, wb=need - 1) == qz.QZ_ERR_WORKSPACE
     assert f(n=0) == f(n=0, q=None, o=None, ws=None, wb=0) == f(h=0) == f(b=batch(qz, n=0)) == qz.QZ_OK
     for bad in (dict(fmt=9), dict(block=8)):
-        assert qz.qz_cache_attention_workspace(cache(qz, **bad), 3, 5, 4) == 0
-    assert qz.qz_cache_attention_workspace(cache(qz), 0, 0, 4) == 0
+        assert qz.qz_cache_attention_workspace(cache(qz, **bad), 3, 5, 4, 4000) == 0
+    assert qz.qz_cache_attention_workspace(cache(qz), 0, 0, 4, 4000) == 0
 
 
 def test_handles_refuse(qz):
