@@ -613,12 +613,12 @@ QZ_API qz_status qz_cache_append(const qz_cache* cache, const qz_batch* batch, i
  *            16-byte aligned; calls that may overlap need one each
  * Rows that belong to no sequence are left as they are.
  * Arithmetic: scores are sums of exact products of q and decoded codes in fp32, the keys' scale applied to
- * the sum; weights p times the values' scale are rounded to 11 bits (f16; from 2^-22 of the sequence's largest
- * such product on gradually fewer) for the product with the decoded codes; sums in fp32, in an unspecified but
+ * the sum; weights p times the values' scale are rounded to 11 bits (f16; below 2^-18 of the sequence's largest
+ * such product gradually fewer) for the product with the decoded codes; sums in fp32, in an unspecified but
  * fixed order: equal inputs give equal results.  A non-finite query makes its own outputs non-finite and no
  * others.  Scales are not negative.  Codes and scales of positions past a sequence's length are not looked at.
  * Waits inside the kernels are bounded (1 s); should one give up, the outputs it stands for are NaN.
- * Errors: as above; QZ_ERR_WORKSPACE. */
+ * Errors: as above (tokens * heads of 2^31 and more are QZ_ERR_UNSUPPORTED); QZ_ERR_WORKSPACE. */
 QZ_API size_t qz_cache_attention_workspace(const qz_cache* cache, int64_t sequences, int64_t tokens, int64_t heads,
                                            int64_t table_pages);
 QZ_API qz_status qz_cache_attention(const qz_cache* cache, const qz_batch* batch, const void* q, int64_t ld_q,

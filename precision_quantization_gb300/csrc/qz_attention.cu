@@ -10,16 +10,18 @@
 
 namespace qz {
 
-// A CTA takes whole items where no sequence can be long enough to be worth cutting (its pages hold at most
-// kWhole tokens); else the steps are shared out evenly, kMinChunk tokens at least to a CTA.
-constexpr int64_t kWhole = 1024, kMinChunk = 512;
+// A CTA takes whole items where no sequence can be long enough to be worth cutting: its pages hold at most kWhole
+// tokens, or twice that where the items fill half the GPU (8 sequences of 1000 tokens, 8 kv heads: 10.9 us whole,
+// 12.4 cut; 32 of 2000: 36.0 and 40.2; one of 2000: 17.7 and 16.3).  Else the steps are shared out evenly, kMinChunk
+// tokens at least to a CTA (one sequence of 2000 tokens: 16.3 us, 17.6 with twice as many).
+constexpr int64_t kWhole = 1024, kMinChunk = 256;
 
 FewPlan few_att_plan(const qz_cache& c, int64_t seqs, int64_t tokens, int64_t heads, int64_t table_pages, int sms) {
   FewPlan p{};
   const int64_t group = heads / c.kv_heads, rows = (tokens * group + seqs - 1) / seqs;
   p.row_tiles = few_att_tiles(c.dim, rows);
   const int64_t items = c.kv_heads * ((tokens * group) / (8 * p.row_tiles) + seqs);
-  p.whole = table_pages * c.page <= kWhole && items < INT32_MAX;
+  p.whole = table_pages * c.page <= (2 * items >= sms ? 2 * kWhole : kWhole) && items < INT32_MAX;
   p.grid = p.whole ? static_cast<int>(items) : sms;
   p.min_chunk = static_cast<int>(kMinChunk / few_att_step(c.dim));
   return p;
@@ -29,9 +31,11 @@ size_t few_att_workspace(const FewPlan& p, int dim) {
   return p.whole ? 0 : static_cast<size_t>(p.grid) * (16 + 2 * slot);
 }
 
-// More than kTcRows rows a sequence and kv head go to the tensor-core tiles.  Tiles that do not fill the GPU are cut
-// along the keys, a part no shorter than kTcPart tokens.  (Cutting tiles that fill it once or more to even out the last
-// round costs more in partial sums than it gives: prompt of 4096 tokens 485 us whole, 581 in two parts.)
+// More than kTcRows rows a sequence and kv head go to the tensor-core tiles (16 sequences of 4096 tokens, 8 kv heads,
+// E4M3: 32 rows 80 us by the few-row kernel and 88 by the tiles, 48 rows 137 and 88; INT8, 64 elements, 64 x 2048:
+// 32 rows 114 and 181, 64 rows 199 and 186).  Tiles that do not fill the GPU are cut along the keys, a part no shorter
+// than kTcPart tokens (64 queries of 8192: 37 us; 42 with twice as many).  Cutting tiles that fill it, to even out the
+// last round, costs more in partial sums than it gives: prompt of 4096 tokens 485 us whole, 581 in two parts.
 constexpr int64_t kTcRows = 32, kTcPart = 512;
 
 TcAttPlan tc_att_plan(const qz_cache& c, int64_t seqs, int64_t tokens, int64_t heads, int64_t table_pages, int sms) {
@@ -39,7 +43,7 @@ TcAttPlan tc_att_plan(const qz_cache& c, int64_t seqs, int64_t tokens, int64_t h
   const int64_t group = heads / c.kv_heads, rows = (tokens * group + seqs - 1) / seqs;
   if (c.dim > 128 || rows <= kTcRows) return p;
   p.nq = rows > 128 ? 2 : 1;
-  const int64_t slots = tokens * group / (128 * p.nq) + seqs, tiles = c.kv_heads * ((tokens * group + 128 * p.nq - 1) / (128 * p.nq));
+  const int64_t slots = tokens * group / (128 * p.nq) + seqs, tiles = c.kv_heads * seqs * ((rows + 128 * p.nq - 1) / (128 * p.nq));
   const int64_t most = std::max<int64_t>(table_pages * c.page / kTcPart, 1);
   const int64_t splits = std::max<int64_t>(std::min<int64_t>(sms / std::max<int64_t>(tiles, 1), most), 1);
   const int64_t grid = slots * c.kv_heads * splits;
@@ -76,6 +80,7 @@ extern "C" qz_status qz_cache_attention(const qz_cache* cache, const qz_batch* b
   if (tokens == 0 || heads == 0 || batch->sequences == 0) return QZ_OK;
   if (!q || !out) return QZ_ERR_NULL;
   if (!is_aligned(q, 2) || !is_aligned(out, 2) || !is_aligned(lse, 4)) return QZ_ERR_ALIGN;
+  if (tokens > INT32_MAX / heads) return QZ_ERR_UNSUPPORTED;
   const int sms = sm_count();
   const TcAttPlan tc = tc_att_plan(*cache, batch->sequences, tokens, heads, batch->table_pages, sms);
   const FewPlan few = few_att_plan(*cache, batch->sequences, tokens, heads, batch->table_pages, sms);

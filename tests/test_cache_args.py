@@ -105,7 +105,7 @@ def test_attention_errors(qz):
     for s in (0.0, -1.0, math.inf, math.nan):
         assert f(s=s) == qz.QZ_ERR_SHAPE
     assert f(q=FAKE + 1) == f(o=FAKE + 1) == f(l=FAKE + 2) == qz.QZ_ERR_ALIGN
-    assert f(n=(1 << 30) + 1) == qz.QZ_ERR_UNSUPPORTED
+    assert f(n=(1 << 30) + 1) == f(n=1 << 30, lq=256) == qz.QZ_ERR_UNSUPPORTED
     assert need == 0 and f(ws=FAKE + 8) == qz.QZ_ERR_ALIGN  # such short sequences take none
     long = batch(qz, ld=4000, width=4000)
     need = qz.qz_cache_attention_workspace(cache(qz), 3, 5, 4, 4000)

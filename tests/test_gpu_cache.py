@@ -356,10 +356,11 @@ def test_attention_sees_no_later_spoiled_block(qz, fmt, new):
     assert np.isnan(got[bad]).all() and np.isfinite(got[~bad]).all()
 
 
-def test_attention_strides_and_padding(qz):
+@pytest.mark.parametrize("new", [[3, 2, 40], [1, 2, 1]])
+def test_attention_strides_and_padding(qz, new):
     """Queries and outputs as slices, heads outside tokens; rows behind the last sequence stay."""
     import torch
-    case = ([60, 33, 100], [3, 2, 40], 32, 16, 6, 2, 64, 0)
+    case = ([60, 33, 100], new, 32, 16, 6, 2, 64, 0)
     lengths, new, page, block, heads, kv, dim, window = case
     host, table, q, starts = attend(qz, "e4m3", case)
     tokens = sum(new)
@@ -394,3 +395,135 @@ def test_append_then_attend(qz):
         host.append(k, v, table, lengths, starts, cos, sin, False)
         same_cache(cache, host)
         check(out, lse, U.attention(qr.double().cpu().numpy(), host, table, list(lengths), starts, dim ** -0.5))
+
+
+# ---- streams, graphs, many calls at once --------------------------------------------------------
+def decode_state(qz, lengths, fmt="int8", new=None, page=32, block=16, heads=8, kv=2, dim=64, capacity=4096):
+    """A cache with room for `capacity` tokens a sequence, and the tensors of one step."""
+    rng = np.random.default_rng(len(lengths))
+    new = new or [1] * len(lengths)
+    each = capacity // page
+    host = U.Cache(rng, fmt, len(lengths) * each, kv, page, dim, block, junk=False)
+    table = sequences(rng, len(lengths), each, host.pages)
+    for s, n in enumerate(lengths):
+        host.fill(rng, table[s], n)
+    q = U.bf16(rng.standard_normal((sum(new), heads, dim)).astype(np.float32))
+    starts = np.concatenate(([0], np.cumsum(new))).astype(np.int32)
+    return host, on_gpu(qz, host), gpu(table), gpu(np.array(lengths, np.int32)), gpu(starts), gpu(q).bfloat16()
+
+
+@pytest.mark.parametrize("new", [None, [70, 40, 90]])
+def test_captured_once_replayed_as_the_sequences_grow(qz, new):
+    """Append and attention in one graph: lengths and tables are read on the GPU at each replay."""
+    import torch
+    lengths = [300, 1700, 33] if new is None else [300, 1700, 133]
+    host, cache, table, n, starts, q = decode_state(qz, lengths, new=new)
+    st = None if new is None else starts
+    tokens = q.shape[0]
+    table_r = qz.RotaryTable.make(4096, qz.rotary_turns(32))
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    k, v = (torch.randn(tokens, 2, 64, device="cuda", generator=gen).bfloat16() for _ in range(2))
+
+    def step():
+        qr = qz.cache_append(cache, k, v, table, n, st, rotary=table_r, q=q)
+        return qz.cache_attention(qr, cache, table, n, st, lse=True)
+
+    fresh = [b.clone() for b in cache.buffers]
+    step()
+    for b, f in zip(cache.buffers, fresh):
+        b.copy_(f)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out, lse = step()
+    got = []
+    for _ in range(3):
+        graph.replay()
+        got.append((out.clone(), lse.clone()))
+        n += 1 if new is None else 100
+    replayed = [b.clone() for b in cache.buffers]
+    for b, f in zip(cache.buffers, fresh):
+        b.copy_(f)
+    n -= 3 if new is None else 300
+    for o, s in got:
+        want, wl = step()
+        assert torch.equal(o, want) and torch.equal(s, wl)
+        n += 1 if new is None else 100
+    assert all(torch.equal(a, b) for a, b in zip(replayed, cache.buffers))
+
+
+def test_two_streams_at_once(qz):
+    """Calls that overlap have a workspace each: long sequences (partial results) on one stream, prompts on the
+    other, and both again after each other."""
+    import torch
+    a = decode_state(qz, [4000, 3000], capacity=4096)
+    b = decode_state(qz, [3500], new=[200], fmt="e4m3")
+    call = lambda s, st, **k: qz.cache_attention(s[5], s[1], s[2], s[3], st, lse=True, **k)  # noqa: E731
+    want = call(a, None), call(b, b[4])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = call(a, None, stream=side), call(b, b[4])
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
+def test_rotary_and_append_on_a_busy_side_stream(qz):
+    import torch
+    host, cache, table, n, starts, q = decode_state(qz, [100, 40])
+    rot = qz.RotaryTable.make(200, qz.rotary_turns(32))
+    k = torch.randn(2, 2, 64, device="cuda").bfloat16()
+    want_q = qz.cache_append(cache, k, k, table, n, rotary=rot, q=q)
+    want_r = qz.rotary(q, rot)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(1_000_000)
+    got_q = qz.cache_append(cache, k, k, table, n, rotary=rot, q=q, stream=side)
+    got_r = qz.rotary(q, rot, stream=side)
+    torch.full((q.numel() * 2,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert torch.equal(got_q, want_q) and torch.equal(got_r, want_r)
+
+
+def test_positions_past_the_table_and_bad_starts(qz):
+    """A length beyond what the table's pages hold, starts that decrease or pass the rows: nothing outside the
+    tensors is touched, and what is inside is as if they ended there."""
+    import torch
+    for new in ([1, 1], [40, 40]):
+        host, cache, table, n, starts, q = decode_state(qz, [64, 64], new=new, capacity=64)
+        k = torch.randn(q.shape[0], 2, 64, device="cuda").bfloat16()
+        before = [b.clone() for b in cache.buffers]
+        n[1] = 64 + new[1] + 5                       # sequence 1: every new token past its pages
+        qz.cache_append(cache, k, k, table, n, starts)
+        assert all(torch.equal(a[table[1].long()], b[table[1].long()]) for a, b in zip(cache.buffers, before))
+        out = qz.cache_attention(q, cache, table, n, starts)
+        assert torch.isfinite(out.float()).all()
+        for bad in ([0, 5, 3], [0, -7, 1 << 30], [1 << 30, 0, 2], [-5, -4, -3]):
+            st = torch.tensor(bad, dtype=torch.int32, device="cuda")
+            qz.cache_append(cache, k, k, table, n, st)
+            qz.cache_attention(q, cache, table, n, st, lse=True)
+        torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("seqs", [700])
+def test_many_sequences(qz, seqs):
+    """More sequences than a CTA has threads, most of them short, one long."""
+    rng = np.random.default_rng(0)
+    lengths = [int(x) for x in rng.integers(0, 40, seqs)]
+    lengths[555] = 1500
+    page, block, heads, kv, dim = 16, 16, 2, 1, 32
+    host = U.Cache(rng, "e5m2", seqs * 4 + 200, kv, page, dim, block, junk=False)
+    table = np.full((seqs, 200), -1, np.int32)
+    at = 0
+    for s, n in enumerate(lengths):
+        table[s, :-(-n // page)] = np.arange(at, at + -(-n // page))
+        at += -(-n // page)
+        host.fill(rng, table[s], n)
+    q = U.bf16(rng.standard_normal((seqs, heads, dim)).astype(np.float32))
+    starts = np.arange(seqs + 1)
+    want = U.attention(q.astype(np.float64), host, table, lengths, starts, dim ** -0.5)
+    for width in (200, 94):   # cut into shares; whole items (the table's first columns hold every page)
+        out, lse = qz.cache_attention(gpu(q).bfloat16(), on_gpu(qz, host), gpu(table)[:, :width], gpu(np.array(lengths, np.int32)), lse=True)
+        check(out, lse, want, width)
