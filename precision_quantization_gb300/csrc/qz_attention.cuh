@@ -63,29 +63,40 @@ template <int FMT>
 __device__ __forceinline__ uint32_t prepare_word(uint32_t w) {
   return FMT == QZ_INT8 ? w ^ 0x80808080u : w;
 }
-// bytes 2 i and 2 i + 1 of a prepared word
-template <int FMT, int I>
-__device__ __forceinline__ uint32_t pair_in_word(uint32_t w) {
-  if constexpr (FMT == QZ_INT8) return sub_f16x2(prmt(w, 0x64646464u, I ? 0x4342u : 0x4140u), 0x64806480u);
-  else if constexpr (FMT == QZ_FP8_E5M2) return prmt(w, 0u, I ? 0x3424u : 0x1404u);
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(I ? w >> 16 : w)));
-  return h;
+// the E4M3 pairs in a word's halves (as 16-bit halves of a register: a shift and a cast cost an instruction more)
+__device__ __forceinline__ void e4m3_pairs(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}" : "=r"(lo), "=r"(hi) : "r"(w));
 }
-// byte J of two words
-template <int FMT, int J>
-__device__ __forceinline__ uint32_t pair_of_words(uint32_t a, uint32_t b) {
+// the two pairs of a prepared word's bytes: 0 and 1, 2 and 3
+template <int FMT>
+__device__ __forceinline__ void pairs_in_word(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if constexpr (FMT == QZ_INT8) {
-    const uint32_t t = prmt(a, b, J | ((4 + J) << 8) | (J << 4) | ((4 + J) << 12));  // (a, a, b, b)
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(t), "r"(0x00FF00FFu), "r"(0x64806480u));  // (t & m) ^ c
-    return sub_f16x2(d, 0x64806480u);
+    lo = sub_f16x2(prmt(w, 0x64646464u, 0x4140u), 0x64806480u);
+    hi = sub_f16x2(prmt(w, 0x64646464u, 0x4342u), 0x64806480u);
   } else if constexpr (FMT == QZ_FP8_E5M2) {
-    return prmt(a, b, J | (J << 4) | ((4 + J) << 8) | ((4 + J) << 12)) & 0xFF00FF00u;
+    lo = prmt(w, 0u, 0x1404u);
+    hi = prmt(w, 0u, 0x3424u);
+  } else {
+    e4m3_pairs(w, lo, hi);
   }
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(prmt(a, b, J | ((4 + J) << 4)))));
-  return h;
+}
+// bytes J and J + 1 of two words, the pairs (a, b) of each
+template <int FMT, int J>
+__device__ __forceinline__ void pairs_of_words(uint32_t a, uint32_t b, uint32_t& p0, uint32_t& p1) {
+  if constexpr (FMT == QZ_INT8) {
+    constexpr uint32_t kSel = J | (J << 4) | ((4 + J) << 8) | ((4 + J) << 12);  // (a, a, b, b)
+    uint32_t d0, d1;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d0) : "r"(prmt(a, b, kSel)), "r"(0x00FF00FFu), "r"(0x64806480u));  // (t & m) ^ c
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d1) : "r"(prmt(a, b, kSel + 0x1111u)), "r"(0x00FF00FFu), "r"(0x64806480u));
+    p0 = sub_f16x2(d0, 0x64806480u);
+    p1 = sub_f16x2(d1, 0x64806480u);
+  } else if constexpr (FMT == QZ_FP8_E5M2) {
+    const uint32_t t = prmt(a, b, J | ((J + 1) << 4) | ((4 + J) << 8) | ((5 + J) << 12));  // (a, a', b, b')
+    p0 = prmt(t, 0u, 0x2404u);
+    p1 = t & 0xFF00FF00u;
+  } else {
+    e4m3_pairs(prmt(a, b, J | ((4 + J) << 4) | ((J + 1) << 8) | ((5 + J) << 12)), p0, p1);
+  }
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -98,11 +109,6 @@ __device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-template <int FMT>
-__device__ __forceinline__ uint32_t pair_of_words_at(uint32_t a, uint32_t b, int j) {
-  return j == 0 ? pair_of_words<FMT, 0>(a, b) : j == 1 ? pair_of_words<FMT, 1>(a, b) : j == 2 ? pair_of_words<FMT, 2>(a, b) : pair_of_words<FMT, 3>(a, b);
-}
-
 // 4 elements of q at element offset `at` (zeros where !in)
 __device__ __forceinline__ void load_q4(const AttentionArgs& a, bool in, int64_t at, float (&x)[4]) {
   x[0] = x[1] = x[2] = x[3] = 0.0f;

@@ -421,7 +421,9 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kHalves; ++i) {
               const uint32_t y0 = prepare_word<FMT>(k0[i][k]), y1 = prepare_word<FMT>(k1[i][k]);
-              const uint32_t ka[4] = {pair_in_word<FMT, 0>(y0), pair_in_word<FMT, 0>(y1), pair_in_word<FMT, 1>(y0), pair_in_word<FMT, 1>(y1)};
+              uint32_t ka[4];
+              pairs_in_word<FMT>(y0, ka[0], ka[2]);
+              pairs_in_word<FMT>(y1, ka[1], ka[3]);
 #pragma unroll
               for (int t = 0; t < NT; ++t) mma16816(x[t][i], ka, qb[t][0], qb[t][1]);
             }
@@ -528,9 +530,15 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
             }
 #pragma unroll
             for (int j = 0; j < kTiles / kPieces; ++j) {
-              const int q = j >> 1, b = 2 * (j & 1);
-              const uint32_t va[4] = {pair_of_words_at<FMT>(vw[0][q], vw[1][q], b), pair_of_words_at<FMT>(vw[0][q], vw[1][q], b + 1),
-                                      pair_of_words_at<FMT>(vw[2][q], vw[3][q], b), pair_of_words_at<FMT>(vw[2][q], vw[3][q], b + 1)};
+              const int q = j >> 1;
+              uint32_t va[4];
+              if (j & 1) {
+                pairs_of_words<FMT, 2>(vw[0][q], vw[1][q], va[0], va[1]);
+                pairs_of_words<FMT, 2>(vw[2][q], vw[3][q], va[2], va[3]);
+              } else {
+                pairs_of_words<FMT, 0>(vw[0][q], vw[1][q], va[0], va[1]);
+                pairs_of_words<FMT, 0>(vw[2][q], vw[3][q], va[2], va[3]);
+              }
 #pragma unroll
               for (int t = 0; t < NT; ++t) mma16816(o[t][8 * h + j], va, pb[t][i][0], pb[t][i][1]);
             }

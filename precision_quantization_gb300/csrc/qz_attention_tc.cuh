@@ -480,9 +480,7 @@ __device__ __forceinline__ void decode_role(const AttTcArgs& p, const AttWork& w
       if (!there) cw[0] = cw[1] = cw[2] = cw[3] = 0u;  // what is past the end, or not there, may be anything
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t y = prepare_word<FMT>(cw[k]);
-        h[2 * k] = pair_in_word<FMT, 0>(y);
-        h[2 * k + 1] = pair_in_word<FMT, 1>(y);
+        pairs_in_word<FMT>(prepare_word<FMT>(cw[k]), h[2 * k], h[2 * k + 1]);
       }
       const uint32_t x0[4] = {h[0], h[1], h[2], h[3]}, x1[4] = {h[4], h[5], h[6], h[7]};
       sts16(tile + to[i], x0);
