@@ -528,7 +528,7 @@ QZ_API qz_status qz_rotary_fill(const double* turns, int64_t positions, int64_t 
  *              gets NaN in place of its pairs.
  *   y          may be x itself (same strides)
  * Errors: QZ_ERR_NULL, QZ_ERR_ENUM (dtype), QZ_ERR_SHAPE (negative sizes, 2 pairs > dim, vectors that
- * overlap), QZ_ERR_UNSUPPORTED (2^31 and more tokens, heads or dim; heads * dim of 2^31 and more), QZ_ERR_ALIGN. */
+ * overlap, y = x with other strides), QZ_ERR_UNSUPPORTED (2^31 and more tokens, heads or dim; heads * dim of 2^31 and more), QZ_ERR_ALIGN. */
 QZ_API qz_status qz_rotary(const qz_rotary_table* table, int32_t dtype, const void* x, int64_t ld_x, int64_t hd_x,
                            int64_t tokens, int64_t heads, int64_t dim, const int32_t* positions, void* y,
                            int64_t ld_y, int64_t hd_y, qz_stream_t stream);
@@ -582,7 +582,7 @@ typedef struct {
 
 /* Appends the keys and values of new tokens, k, v [tokens, kv_heads, dim] of dtype (QZ_BF16 or QZ_F32),
  * the keys rotated by their positions on the way; with q != NULL also rotates the queries of the same
- * tokens, q -> q_out [tokens, heads, dim] of dtype, as qz_rotary does (q_out may be q itself).
+ * tokens, q -> q_out [tokens, heads, dim] of dtype, as qz_rotary does (q_out may be q itself, same strides).
  *   table  NULL: no rotation (then q must be NULL)
  * For each block that gets new tokens, of keys and of values alike, with `old` its scale where it
  * already holds tokens (their positions lie below the first new one) and 0 where it holds none:

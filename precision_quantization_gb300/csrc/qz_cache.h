@@ -79,6 +79,10 @@ inline qz_status check_vectors(int64_t tokens, int64_t heads, int64_t dim, int64
   if (heads > 1 && tokens > 1 && ld < (heads - 1) * hd + dim && hd < (tokens - 1) * ld + dim) return QZ_ERR_SHAPE;
   return QZ_OK;
 }
+// rotated in place: each vector to where it came from
+inline bool moves_in_place(const void* x, int64_t ld_x, int64_t hd_x, const void* y, int64_t ld_y, int64_t hd_y, int64_t tokens, int64_t heads) {
+  return x == y && ((tokens > 1 && ld_x != ld_y) || (heads > 1 && hd_x != hd_y));
+}
 qz_status check_cache(const qz_cache* c);
 qz_status check_batch(const qz_batch* b, int64_t tokens);
 qz_status check_rotary_table(const qz_rotary_table* t, int64_t dim);

@@ -1,5 +1,13 @@
 // qz_rotary.cu -- rotation of queries and keys by their positions and its gradient (include/qz.h,
 // qz_rotary), and the table of cosines and sines.
+//
+//   a' = a c - b s,  b' = b c + a s  per pair, c and s of the token's position; backward: -s
+//
+// One pass: x read, y written, and a table row per token that every head shares: bound by HBM in principle, by the latency of a thread's loads in practice, since it holds few of them.  So a thread takes the same
+// elements of several heads: more loads in flight for one look at the table, in 16-byte pieces.  GPU times:
+//   bf16, 8192 tokens x 32 heads x 128, adjacent pairs (139 MB)   29.2 us, 4.75 TB/s  (one head a thread, 64-bit places: 39)
+//   fp32, backward of 4093 x 40 x 80, 10 pairs (105 MB)           22.6 us, 4.65 TB/s  (rotary_quad_kernel)
+//   one token                                                     2.3 us, all of it launch
 #include "qz_rotary.cuh"
 
 #include <climits>
@@ -173,6 +181,7 @@ qz_status run_rotary(const qz_rotary_table* table, int32_t dtype, const void* x,
     return st;
   if (tokens == 0 || heads == 0 || dim == 0) return QZ_OK;
   if (!x || !y) return QZ_ERR_NULL;
+  if (moves_in_place(x, ld_x, hd_x, y, ld_y, hd_y, tokens, heads)) return QZ_ERR_SHAPE;
   const int64_t e = dtype == QZ_BF16 ? 2 : 4;
   if (!is_aligned(x, e) || !is_aligned(y, e) || !is_aligned(positions, 4)) return QZ_ERR_ALIGN;
   RotaryArgs a{};

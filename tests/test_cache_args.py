@@ -56,6 +56,7 @@ def test_rotary_errors(qz):
         assert f(n=-1) == f(d=62) == f(t=rot(qz, positions=0)) == f(t=rot(qz, positions=-1)) == f(t=rot(qz, pairs=-1)) == qz.QZ_ERR_SHAPE
         assert f(hd=63) == f(ld=127) == f(ly=127) == f(hy=-64) == f(ld=1 << 60) == qz.QZ_ERR_SHAPE  # vectors that overlap, offsets past 64 bits
         assert f(ld=0) == f(hd=0) == qz.QZ_ERR_SHAPE
+        assert f(ly=256) == f(hy=320, ly=640) == qz.QZ_ERR_SHAPE  # in place, but elsewhere
         assert f(n=1 << 31) == f(h=1 << 31) == f(h=1 << 26) == f(t=rot(qz, positions=1 << 31)) == qz.QZ_ERR_UNSUPPORTED
         assert f(x=FAKE + 1) == f(y=FAKE + 1) == f(p=FAKE + 2) == f(t=rot(qz, cos=FAKE + 2)) == f(dt=qz.QZ_F32, x=FAKE + 2) == qz.QZ_ERR_ALIGN
         assert f(n=0) == f(h=0) == qz.QZ_OK
@@ -87,6 +88,7 @@ def test_append_errors(qz):
     assert f(q=None) == f(o=None) == f(t=None) == qz.QZ_ERR_NULL  # queries need both tensors and a table
     assert f(dt=0) == qz.QZ_ERR_ENUM
     assert f(hk=63) == f(lv=127) == f(hq=63) == f(lo=255) == f(n=-1) == f(h=3) == f(t=rot(qz, pairs=33)) == qz.QZ_ERR_SHAPE
+    assert f(lo=512) == f(ho=128, lo=512) == qz.QZ_ERR_SHAPE  # in place, but elsewhere
     assert f(n=1 << 31) == f(n=(1 << 30) + 1) == qz.QZ_ERR_UNSUPPORTED
     assert f(k=FAKE + 1) == f(v=FAKE + 1) == f(q=FAKE + 1) == f(o=FAKE + 1) == qz.QZ_ERR_ALIGN
     assert f(n=0) == f(n=0, k=None, v=None) == f(b=batch(qz, n=0)) == qz.QZ_OK
