@@ -527,3 +527,57 @@ def test_many_sequences(qz, seqs):
     for width in (200, 94):   # cut into shares; whole items (the table's first columns hold every page)
         out, lse = qz.cache_attention(gpu(q).bfloat16(), on_gpu(qz, host), gpu(table)[:, :width], gpu(np.array(lengths, np.int32)), lse=True)
         check(out, lse, want, width)
+
+
+@pytest.mark.parametrize("new", [[1, 1], [40, 70]])
+def test_shared_pages(qz, new):
+    """Sequences with the same first pages see what each would see of a copy of its own."""
+    host, table, q, starts = attend(qz, "int8", ([1200, 900], new, 64, 32, 8, 2, 128, 0))
+    table[1, :12] = table[0, :12]
+    cache, n = on_gpu(qz, host), np.array([1200, 900], np.int32)
+    out, lse = qz.cache_attention(gpu(q).bfloat16(), cache, gpu(table), gpu(n), gpu(starts), lse=True)
+    check(out, lse, U.attention(q.astype(np.float64), host, table, [1200, 900], starts, 128 ** -0.5, 0))
+
+
+@pytest.mark.parametrize("fmt,new", [("e4m3", [1, 1]), ("int8", [60, 90])])
+def test_offsets_past_32_bits(qz, fmt, new):
+    """Codes, queries, keys and outputs that lie 2^32 elements and more from their tensors' start: the same results
+    as near it."""
+    import torch
+    far, near, kv, heads, page, dim, pairs = 70000, 64, 8, 16, 64, 128, 64   # 70000 pages: 4.6e9 codes an array
+    tokens, lengths = sum(new), gpu(np.array([900, 700], np.int32))
+    starts, ld = gpu(np.concatenate(([0], np.cumsum(new))).astype(np.int32)), (1 << 32) // (tokens - 1) // 64 * 64 + 64
+    torch.manual_seed(5)
+    room = torch.empty(((tokens - 1) * ld + heads * dim,), dtype=torch.bfloat16, device="cuda")
+    wide = room.as_strided((tokens, heads, dim), (ld, dim, 1))
+    table = torch.arange(30, dtype=torch.int32, device="cuda").reshape(2, 15)
+    cos, sin = table_of(1000, pairs, 4)
+    rot, got = qz.RotaryTable(gpu(cos), gpu(sin)), []
+    q, k, v = (torch.randn((tokens, n, dim), device="cuda").bfloat16() for n in (heads, kv, kv))
+    held = torch.randint(0, 120, (2, 30, kv, page, dim), dtype=torch.uint8, device="cuda")
+    for pages in (near, far):
+        cache, t = qz.KVCache.alloc(fmt, pages, kv, page, dim), table + (pages - 30)
+        cache.k_codes[-30:], cache.v_codes[-30:] = held[0], held[1]
+        cache.k_scales[-30:], cache.v_scales[-30:] = 0.01, 0.02
+        if pages == near:
+            turned = qz.cache_append(cache, k, v, t, lengths, starts, rotary=rot, q=q)
+            out, lse = qz.cache_attention(turned, cache, t, lengths, starts, lse=True)
+        else:
+            wide.copy_(q)
+            assert qz.cache_append(cache, k, v, t, lengths, starts, rotary=rot, q=wide, out=wide) is wide
+            turned = wide.clone(memory_format=torch.contiguous_format)
+            out, lse = qz.cache_attention(wide, cache, t, lengths, starts, lse=True)
+            assert torch.equal(qz.rotary(wide, rot), qz.rotary(turned, rot))
+            wide.copy_(q)
+            kk = wide[:, :kv]
+            kk.copy_(k)
+            before = cache.k_codes[-30:].clone()
+            qz.cache_append(cache, kk, v, t, lengths, starts, rotary=rot)
+            assert torch.equal(cache.k_codes[-30:], before)
+            wide.fill_(7)
+            qz.cache_attention(turned, cache, t, lengths, starts, out=wide)
+            assert torch.equal(wide.clone(memory_format=torch.contiguous_format), out)
+        got.append((turned, out, lse, *(b[-30:].clone() for b in cache.buffers)))
+        del cache
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
