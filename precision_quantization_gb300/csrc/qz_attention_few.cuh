@@ -57,6 +57,19 @@ __device__ __forceinline__ void copy_scale(uint32_t dst, const float* src, uint3
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+// Bounded wait for a step.  After one of the CTA's warps has given up no other waits long: the CTA's results are NaN.
+// (The flag is looked at where a wait is long already; a test before each wait costs registers, and 64 x 1 token 2 to 4 us.)
+__device__ __forceinline__ bool step_wait(uint32_t bar, uint32_t parity, volatile int& gave_up) {
+  if (held_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!held_try_wait(bar, parity)) {
+    if (gave_up || globaltimer_ns() - t0 > kFewWaitNs) {
+      gave_up = 1;
+      return false;
+    }
+  }
+  return true;
+}
 __device__ __forceinline__ void arrive_on(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -137,6 +150,7 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
   __shared__ __align__(16) float s_scale[kWarps][kStages][4];  // ks, vs of the first 16 tokens, of the second
   __shared__ int32_t s_has[kWarps][kStages];                   // bit i: the i-th 16 tokens have a page
   __shared__ __align__(8) uint64_t s_full[kWarps][kStages];
+  __shared__ volatile int s_gave_up;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const uint32_t base = (smem_addr(few_raw) + 1023u) & ~1023u;
@@ -144,6 +158,7 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
   const uint32_t ring = base + warp * (kStages * Z::kStage);
   const uint32_t q_smem = base + Z::kRing;
   float* join = reinterpret_cast<float*>(smem + Z::kRing + Z::kQ);
+  if (tid == 0) s_gave_up = 0;
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(smem_addr(&s_full[warp][i]), 1 + 2 * kHalves);  // the codes, the scales
     mbar_init_fence();
@@ -394,10 +409,8 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
     const int32_t w0 = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * warp / kWarps);
     const int32_t w1 = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * (warp + 1) / kWarps);
     for (int32_t st = w0; st < w1; ++st) {
-      if (failed || !__all_sync(kFull, held_wait(smem_addr(&s_full[warp][stage]), phase, kFewWaitNs))) {
-        failed = true;
-        break;
-      }
+      failed = !__all_sync(kFull, step_wait(smem_addr(&s_full[warp][stage]), phase, s_gave_up)) || failed;
+      if (failed) break;
       const uint32_t from = ring + stage * Z::kStage;
       const int32_t has = s_has[warp][stage];
       const float4 scales = *reinterpret_cast<const float4*>(s_scale[warp][stage]);
