@@ -109,20 +109,7 @@ __device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// 4 elements of q at element offset `at` (zeros where !in)
-__device__ __forceinline__ void load_q4(const AttentionArgs& a, bool in, int64_t at, float (&x)[4]) {
-  x[0] = x[1] = x[2] = x[3] = 0.0f;
-  if (!in) return;
-  if (a.q_vec) {
-    const uint2 b = __ldg(reinterpret_cast<const uint2*>(a.q + at));
-    x[0] = __uint_as_float(b.x << 16), x[1] = __uint_as_float(b.x & 0xffff0000u);
-    x[2] = __uint_as_float(b.y << 16), x[3] = __uint_as_float(b.y & 0xffff0000u);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = bf16_float(__ldg(a.q + at + e));
-  }
-}
-// the same as bf16 pairs
+// 4 elements of q at element offset `at` as bf16 pairs (zeros where !in)
 __device__ __forceinline__ uint2 load_q4_raw(const AttentionArgs& a, bool in, int64_t at) {
   if (!in) return make_uint2(0u, 0u);
   if (a.q_vec) return __ldg(reinterpret_cast<const uint2*>(a.q + at));
@@ -132,7 +119,7 @@ __device__ __forceinline__ uint2 load_q4_raw(const AttentionArgs& a, bool in, in
   return make_uint2(x[0] | (x[1] << 16), x[2] | (x[3] << 16));
 }
 // The power of two that brings a row whose largest magnitude is `top` into [2^14, 2^15), and its inverse;
-// elements 2^-38 of the largest and less lose bits, 2^-40 of it at most.  NaN for a row that is not finite.
+// elements 2^-31 of the largest and less lose bits, 2^-39 of it at most.  NaN for a row that is not finite.
 __device__ __forceinline__ float q_unit(float top, float& down) {
   const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 127, -100);
   down = __uint_as_float(static_cast<uint32_t>(127 - 14 + min(e, 127)) << 23);

@@ -129,18 +129,6 @@ struct AttWork {
   int32_t t0, t1;                // tiles of keys
 };
 
-// load_q4 of an address that is there whether or not the values are wanted, without a branch for aligned ones
-__device__ __forceinline__ void load_q4_masked(const AttentionArgs& a, bool in, int64_t at, float (&x)[4]) {
-  if (a.q_vec) {
-    const uint2 b = __ldg(reinterpret_cast<const uint2*>(a.q + at));
-    const uint32_t lo = in ? b.x : 0u, hi = in ? b.y : 0u;
-    x[0] = __uint_as_float(lo << 16), x[1] = __uint_as_float(lo & 0xffff0000u);
-    x[2] = __uint_as_float(hi << 16), x[3] = __uint_as_float(hi & 0xffff0000u);
-  } else {
-    load_q4(a, in, at, x);
-  }
-}
-
 // ---- softmax ------------------------------------------------------------------------------------
 // One row of tile q; a warp's 32 lanes of tensor memory.
 __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& w, AttBarriers& bar, const AttScales* scales, uint32_t smem_q,
@@ -152,17 +140,25 @@ __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& 
   const int i = row / a.group, head = w.kvh * a.group + row % a.group;
   const int64_t token = w.sp.row + i, pos = w.sp.p0 + i;
   // The warp's 32 rows of q as f16, K-major panels of 64 elements, 128-byte swizzle: a row at a time, four elements a
-  // lane, eight rows' loads and shuffles side by side.  Lane r keeps row r's factor.
+  // lane, all loads at once, eight rows' shuffles side by side.  Lane r keeps row r's factor.
   float fq = 0.0f;
   const int32_t left = w.rows - (w.row0 + q * kAttRows);  // of the tile's rows
-#pragma unroll 1
-  for (int r0 = 32 * warp; r0 < 32 * warp + 32; r0 += 8) {
+  uint2 raw[32];
+#pragma unroll
+  for (int k = 0; k < 32; ++k) {
+    const bool in = 32 * warp + k < left && 4 * lane < dim;
+    const int rr = w.row0 + q * kAttRows + 32 * warp + k, ri = rr / a.group;
+    raw[k] = load_q4_raw(a, in, (w.sp.row + ri) * a.ld_q + (w.kvh * a.group + rr - ri * a.group) * a.hd_q + 4 * lane);
+  }
+#pragma unroll
+  for (int rows = 0; rows < 32; rows += 8) {
+    const int r0 = 32 * warp + rows;
     float x[8][4], top[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const bool in = r0 + k < left && 4 * lane < dim;
-      const int rr = in ? w.row0 + q * kAttRows + r0 + k : w.row0, ri = rr / a.group;
-      load_q4_masked(a, in, (w.sp.row + ri) * a.ld_q + (w.kvh * a.group + rr - ri * a.group) * a.hd_q + (in ? 4 * lane : 0), x[k]);
+      const uint2 b = raw[rows + k];
+      x[k][0] = __uint_as_float(b.x << 16), x[k][1] = __uint_as_float(b.x & 0xffff0000u);
+      x[k][2] = __uint_as_float(b.y << 16), x[k][3] = __uint_as_float(b.y & 0xffff0000u);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) top[k] = absmax_nan(absmax_nan(absmax_nan(fabsf(x[k][0]), x[k][1]), x[k][2]), x[k][3]);
