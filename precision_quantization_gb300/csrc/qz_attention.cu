@@ -35,7 +35,7 @@ size_t few_att_workspace(const FewPlan& p, int dim) {
 // E4M3: 32 rows 80 us by the few-row kernel and 88 by the tiles, 48 rows 137 and 88; INT8, 64 elements, 64 x 2048:
 // 32 rows 114 and 181, 64 rows 199 and 186).  Tiles that do not fill the GPU are cut along the keys, a part no shorter
 // than kTcPart tokens (64 queries of 8192: 37 us; 42 with twice as many).  Cutting tiles that fill it, to even out the
-// last round, costs more in partial sums than it gives: prompt of 4096 tokens 485 us whole, 581 in two parts.
+// last round, costs more in partial sums than it gives: prompt of 4096 tokens, with q staged more slowly, 485 us whole, 581 in two parts.
 constexpr int64_t kTcRows = 32, kTcPart = 512;
 
 TcAttPlan tc_att_plan(const qz_cache& c, int64_t seqs, int64_t tokens, int64_t heads, int64_t table_pages, int sms) {

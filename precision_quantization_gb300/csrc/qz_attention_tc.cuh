@@ -21,8 +21,8 @@
 // 11 bits down to 2^-22 of the largest scale.
 // Where the row tiles do not fill the GPU the keys are cut in `splits` parts, whose sums a second kernel joins.
 //
-// GPU times: 4096 new tokens of 8192, 32 / 8 heads x 128, E4M3: 486 us, 848 TFLOP/s (the operations at the library
-// product's rate: 215); prompts of 5 sequences, 16 / 4 heads x 64, INT8: 110 us.  A step of 256 rows x 128 keys takes some
+// GPU times: 4096 new tokens of 8192, 32 / 8 heads x 128, E4M3: 466 us, 885 TFLOP/s (the operations at the library
+// product's rate: 215); prompts of 5 sequences, 16 / 4 heads x 64, INT8: 111 us.  A step of 256 rows x 128 keys takes some
 // 4400 cycles: 1330 of MMAs, and two softmaxes of 2900, a row tile's own chain of load, exponentials, conversion and
 // store, which overlap with one another and with the MMAs only in part.  Sixteen softmax warps, two MMA warps, exponentials
 // pipelined by hand and turns of the two tiles were slower.
