@@ -568,7 +568,8 @@ typedef struct {
  *   lengths  [sequences]: the tokens of each sequence, those of this call (the last ones) included
  *   starts   [sequences + 1]: the first row of each sequence's tokens in the call's tensors, not
  *            decreasing; rows from starts[sequences] on belong to no sequence.  NULL: one token each
- *            (tokens == sequences).
+ *            (tokens == sequences).  Where they do decrease it is unspecified which rows are computed;
+ *            still nothing outside the tensors and the sequences' pages is read or written.
  * The new token i of n of a sequence has position length - n + i.  None of the three is copied to the
  * host, so the same call can be captured once and replayed as they change. */
 typedef struct {

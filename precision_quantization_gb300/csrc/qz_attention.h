@@ -56,6 +56,16 @@ struct TcAttPlan {
   int grid;     // 0: not applicable
 };
 TcAttPlan tc_att_plan(const qz_cache& c, int64_t seqs, int64_t tokens, int64_t heads, int64_t table_pages, int sms);
+// Places: sequence s's row tiles begin at slot floor(start group / tile_rows) + s, so that they end before the next one's
+// begin.  Where starts decrease (which no caller may let them) a slot can be counted to a sequence that begins behind it.
+__host__ __device__ inline int64_t tc_first_slot(int32_t start, int32_t s, int group, int tile_rows) {
+  return static_cast<int64_t>(start) * group / tile_rows + s;
+}
+// The first row of the tile at `slot` of a sequence of `rows` rows; -1: no tile of it lies there.
+__host__ __device__ inline int64_t tc_tile_row(int64_t slot, int64_t first_slot, int64_t rows, int tile_rows) {
+  const int64_t row0 = (slot - first_slot) * tile_rows;
+  return row0 >= 0 && row0 < rows ? row0 : -1;
+}
 inline size_t tc_att_workspace(const TcAttPlan& p, int64_t tokens, int64_t heads, int dim) {
   return p.splits > 1 ? static_cast<size_t>(p.splits) * tokens * heads * (dim + 2) * sizeof(float) : 0;
 }

@@ -571,13 +571,12 @@ __global__ void __launch_bounds__(kAttThreads, 1) attention_tc_kernel(const __gr
   AttWork w;
   w.kvh = static_cast<int32_t>(at % a.c.heads);
   const int tile_rows = p.nq * kAttRows;
-  // sequence s begins at slot floor(start group / rows) + s: its tiles end before the next one's begin
-  const auto first_slot = [&](int32_t s) { return static_cast<int64_t>(start_of(a.b, s)) * a.group / tile_rows + s; };
+  const auto first_slot = [&](int32_t s) { return tc_first_slot(start_of(a.b, s), s, a.group, tile_rows); };
   w.seq = count_upto(a.b.seqs, first_slot, slot) - 1;
   if (w.seq < 0) return;
   w.sp = span_of(a.b, w.seq, a.c.page);
-  const int64_t all_rows = static_cast<int64_t>(w.sp.n) * a.group, row0 = (slot - first_slot(w.seq)) * tile_rows;
-  if (row0 >= all_rows) return;
+  const int64_t all_rows = static_cast<int64_t>(w.sp.n) * a.group, row0 = tc_tile_row(slot, first_slot(w.seq), all_rows, tile_rows);
+  if (row0 < 0) return;
   w.row0 = static_cast<int32_t>(row0);
   w.rows = static_cast<int32_t>(all_rows);
   {
