@@ -614,8 +614,9 @@ QZ_API qz_status qz_cache_append(const qz_cache* cache, const qz_batch* batch, i
  *            16-byte aligned; calls that may overlap need one each
  * Rows that belong to no sequence are left as they are.
  * Arithmetic: scores are sums of exact products of q and decoded codes in fp32, the keys' scale applied to
- * the sum; weights p times the values' scale are rounded to 11 bits (f16; below 2^-18 of the sequence's largest
- * such product gradually fewer) for the product with the decoded codes; sums in fp32, in an unspecified but
+ * the sum; weights p, the largest 1, times the values' scale are rounded to 11 bits for the product with the decoded
+ * codes (f16; gradually fewer below 2^-22 of the largest scale of values that the token sees, or of 2^-100 where that
+ * is larger: what it does not see changes nothing); sums in fp32, in an unspecified but
  * fixed order: equal inputs give equal results.  A non-finite query makes its own outputs non-finite and no
  * others.  Scales are not negative.  Codes and scales of positions past a sequence's length are not looked at.
  * Waits inside the kernels are bounded (1 s); should one give up, the outputs it stands for are NaN.

@@ -13,9 +13,9 @@
 //   keys    rows g and g + 8 of 16, bytes 64 h + 16 c .. + 15: four 16-wide products,
 //   values  rows 2 c, 2 c + 1, 2 c + 8, 2 c + 9, bytes w g .. w g + w - 1 (w = dim / 8): w / 2 products
 // are whole 16-byte pieces, read from different banks.  8-bit codes are exact in f16, q is made f16 by a
-// power of two of its row.  The weights p vs are made f16 times 2^15 / unit, unit a power of two >= every vs
-// so far, so that a scale far below the largest keeps its 11 bits (down to 2^-29 of it); a transpose of
-// 8 x 8 (movmatrix) makes them operands.
+// power of two of its row.  The weights p vs are made f16 times 2^15 / unit, unit a power of two of the row's, above
+// every vs that it has seen so far, so that a weight far below the largest scale keeps its 11 bits (down to 2^-28 of
+// it); a transpose of 8 x 8 (movmatrix) makes them operands.
 //
 // The work is cut in equal shares of steps over a persistent grid, whatever the lengths are (they lie on
 // the GPU): item after item (sequence, kv head, row tile), a CTA's share begins and ends anywhere.  A share
@@ -31,6 +31,8 @@
 // the products, and the instructions are the bound, with the joins at the ends of items.  Codes as the B operand, rows
 // as A, took 226 and 80 us; rings filled by cp.async 240 and 84.
 #pragma once
+
+#include <type_traits>
 
 #include "qz_attention.cuh"
 #include "qz_internal.h"
@@ -144,7 +146,8 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
   constexpr uint32_t kRowBytes = DP < 128 ? 64 : 128, kSlab = kStep * kRowBytes;  // a box's row, and a step's boxes of one x
   extern __shared__ uint8_t few_raw[];
   __shared__ int64_t s_scan[kWarps + 1], s_found[2];
-  __shared__ float s_fq[kRows], s_m[kWarps][kRows], s_l[kWarps][kRows], s_unit[kWarps];
+  __shared__ float s_fq[kRows], s_m[kWarps][kRows], s_l[kWarps][kRows];
+  __shared__ float s_unit[kWarps][kRows], s_shrink[kWarps][kRows];  // (in registers: spills with four row tiles)
   __shared__ int32_t s_end[kRows], s_begin[kRows];
   __shared__ float s_top[kRows], s_sum[kRows];
   __shared__ __align__(16) float s_scale[kWarps][kStages][4];  // ks, vs of the first 16 tokens, of the second
@@ -354,9 +357,9 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
       float down;
       const float up = q_unit(top, down);
       if (lane == 0) {
-        const int64_t pos = s.w.sp.p0 + i;
+        const int64_t pos = s.w.sp.p0 + (s.row0 + min(r, s.rows - 1)) / a.group;  // (rows past the item's see what its last one sees)
         s_fq[r] = down * a.scale;
-        s_end[r] = r < s.rows ? static_cast<int32_t>(max(min(pos + 1, static_cast<int64_t>(s.w.sp.len)), static_cast<int64_t>(0))) : 0;
+        s_end[r] = static_cast<int32_t>(max(min(pos + 1, static_cast<int64_t>(s.w.sp.len)), static_cast<int64_t>(0)));
         s_begin[r] = static_cast<int32_t>(max(pos + 1 - a.window, static_cast<int64_t>(0)));
       }
 #pragma unroll
@@ -395,7 +398,6 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
     const int32_t all_end = s_end[0], all_begin = s_begin[s.rows - 1], len = s.w.sp.len;
 
     float o[NT][kTiles][4], mx[NT][2], sum[NT][2];
-    float unit = 0x1p-100f;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       mx[t][0] = mx[t][1] = kNone;
@@ -405,6 +407,8 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[t][j][e] = 0.0f;
     }
+    float least = 0x1p-100f;   // the smallest of the rows' units,
+    bool mixed = false;        // and whether there are others (all in s_unit then): rows that do not see a block of large values keep theirs
     const int32_t count = s.t1 - s.t0;
     const int32_t w0 = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * warp / kWarps);
     const int32_t w1 = s.t0 + static_cast<int32_t>(static_cast<int64_t>(count) * (warp + 1) / kWarps);
@@ -486,17 +490,54 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
               moved = true;
             }
           }
-        const float unit_was = unit;
+        float unit_was = least;
+        const auto unit_for = [](float unit, float most) {  // the next power of two above `most`
+          return most > unit ? __uint_as_float((__float_as_uint(fminf(most, 0x1p125f)) & 0x7f800000u) + 0x00800000u) : unit;
+        };
+        const float most = fmaxf(has & 1 ? vs[0] : 0.0f, has & 2 ? vs[kHalves - 1] : 0.0f);
+        if (most > least) {  // (the same for every lane)
+          bool shared = !mixed;    // every row sees something of what there is
 #pragma unroll
-        for (int i = 0; i < kHalves; ++i) {
-          const float vmag = fabsf(vs[i]);
-          if (((has >> i) & 1) && vmag > unit && is_finite_f(vmag)) {  // the next power of two above it
-            unit = __uint_as_float((__float_as_uint(fminf(vmag, 0x1p125f)) & 0x7f800000u) + 0x00800000u);
+          for (int i = 0; i < kHalves; ++i) shared = shared && (!((has >> i) & 1) || (p64 + 16 * i < all_end && p64 + 16 * i + 15 >= all_begin));
+          if (shared) {
+            least = unit_for(least, most);
             moved = true;
+          } else {           // no block changes what a row that sees nothing of it keeps
+            float lowest = 0x1p127f, highest = 0.0f;
+#pragma unroll 1
+            for (int r = 2 * c; r < kRows; r += r & 1 ? 7 : 1) {  // this lane's rows
+              float seen = 0.0f;
+#pragma unroll
+              for (int i = 0; i < kHalves; ++i)
+                if (((has >> i) & 1) && p64 + 16 * i < s_end[r] && p64 + 16 * i + 15 >= s_begin[r]) seen = fmaxf(seen, vs[i]);
+              const float unit = mixed ? s_unit[warp][r] : least, to = unit_for(unit, seen);
+              lowest = fminf(lowest, to), highest = fmaxf(highest, to);
+              __syncwarp();  // every lane of the row has read it
+              if (g == 0) s_unit[warp][r] = to, s_shrink[warp][r] = unit / to;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float shrink = s_shrink[warp][8 * t + 2 * c + e];
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j) {
+                  o[t][j][e] *= shrink;
+                  o[t][j][2 + e] *= shrink;
+                }
+              }
+#pragma unroll
+            for (int d = 1; d < 4; d <<= 1) {
+              lowest = fminf(lowest, __shfl_xor_sync(kFull, lowest, d));
+              highest = fmaxf(highest, __shfl_xor_sync(kFull, highest, d));
+            }
+            least = unit_was = lowest;
+            mixed = lowest != highest;
           }
         }
         if (__any_sync(kFull, moved)) {
-          const float shrink = unit_was / unit;
+          const float shrink = unit_was / least;
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -510,29 +551,34 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
               }
             }
         }
-        const float inverse = 0x1p15f / unit;
         uint32_t pb[NT][kHalves][2];
+        const auto weigh = [&](auto each) {  // each: every row its own unit
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float y[kHalves][4];
+          for (int t = 0; t < NT; ++t) {
+            float y[kHalves][4];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float top = mx[t][e] == kNone ? 0.0f : mx[t][e];
+            for (int e = 0; e < 2; ++e) {
+              const float top = mx[t][e] == kNone ? 0.0f : mx[t][e];
+              const float unit = decltype(each)::value ? s_unit[warp][8 * t + 2 * c + e] : least;
+              const float inverse = __uint_as_float((269u << 23) - __float_as_uint(unit));  // 2^15 / unit
+#pragma unroll
+              for (int i = 0; i < kHalves; ++i)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const float v = x[t][i][2 * z + e], w = ex2(v - top);
+                  sum[t][e] += w;
+                  y[i][2 * z + e] = w * (vs[i] * inverse);
+                  if (!whole && v == kNone) y[i][2 * z + e] = 0.0f;  // (the scale of what is not seen may be anything)
+                }
+            }
 #pragma unroll
             for (int i = 0; i < kHalves; ++i)
 #pragma unroll
-              for (int z = 0; z < 2; ++z) {
-                const float v = x[t][i][2 * z + e], w = ex2(v - top);
-                sum[t][e] += w;
-                y[i][2 * z + e] = w * (vs[i] * inverse);
-                if (!whole && v == kNone) y[i][2 * z + e] = 0.0f;  // (the scale of what is not seen may be anything)
-              }
+              for (int z = 0; z < 2; ++z) pb[t][i][z] = transposed(f16x2_bits(y[i][2 * z], y[i][2 * z + 1]));
           }
-#pragma unroll
-          for (int i = 0; i < kHalves; ++i)
-#pragma unroll
-            for (int z = 0; z < 2; ++z) pb[t][i][z] = transposed(f16x2_bits(y[i][2 * z], y[i][2 * z + 1]));
-        }
+        };
+        if (mixed) weigh(std::true_type{});
+        else weigh(std::false_type{});
         // ---- out^T += V^T p^T ---------------------------------------------------------------------
 #pragma unroll
         for (int i = 0; i < kHalves; ++i)
@@ -598,9 +644,9 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
         if (g == 0) {
           s_m[warp][8 * t + 2 * c + e] = mx[t][e];
           s_l[warp][8 * t + 2 * c + e] = sum[t][e];
+          if (!mixed) s_unit[warp][8 * t + 2 * c + e] = least;
         }
       }
-    if (lane == 0) s_unit[warp] = unit;
     const bool first = s.t0 == 0, last = s.t1 == s.w.steps;
     float* slot = WHOLE || (first && last) ? nullptr : slots + (2 * static_cast<size_t>(blockIdx.x) + (first ? 1 : 0)) * Z::kSlot;
     constexpr int kQuads = Z::kJoinCols / 32;    // float4s of each of the eight column groups at a time
@@ -625,7 +671,7 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
           float l = lane < kWarps ? f * s_l[lane < kWarps ? lane : 0][r] : 0.0f;
 #pragma unroll
           for (int w = 8; w; w >>= 1) l += __shfl_xor_sync(kFull, l, w);
-          if (lane < kWarps) s_m[lane][r] = f * s_unit[lane] * 0x1p-15f;
+          if (lane < kWarps) s_m[lane][r] = f * s_unit[lane][r] * 0x1p-15f;
           if (lane == 0) s_top[r] = top, s_sum[r] = l;
         }
         __syncthreads();

@@ -16,9 +16,9 @@
 // in the order P0 V(j - 1), Q0 K(j), P1 V(j - 1), Q1 K(j): while one tile's softmax runs, the tensor cores work
 // for the other.
 // 8-bit codes are exact in f16, q is made f16 by a power of two of its row.  The maximum m is moved only
-// when it is exceeded by more than 2^4, and the unit of the weights p vs (a power of two >= vs) by factors
-// of four, so that the sums in tensor memory are rarely rescaled; p vs 2^11 / unit stays within f16, and keeps its
-// 11 bits down to 2^-22 of the largest scale.
+// when it is exceeded by more than 2^4, and the unit of the weights p vs (a power of two above every vs that the row
+// has seen) by factors of four, so that the sums in tensor memory are rarely rescaled; p vs 2^11 / unit stays within
+// f16, and keeps its 11 bits down to 2^-22 of the largest scale.
 // Where the row tiles do not fill the GPU the keys are cut in `splits` parts, whose sums a second kernel joins.
 //
 // GPU times: 4096 new tokens of 8192, 32 / 8 heads x 128, E4M3: 466 us, 885 TFLOP/s (the operations at the library
@@ -271,7 +271,7 @@ __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& 
       tmem_wait32(v[3]);
     }
     if (!done) {
-      uint32_t off = 0;  // groups that the row sees nothing of: their scales may be anything
+      uint32_t off = 0;  // groups that the row sees nothing of: their scales may be anything, and change nothing that it keeps
       if (!whole) {
         const int hi = max(min(end - j0, kAttKeys), 0), lo = max(min(begin - j0, kAttKeys), 0);
 #pragma unroll
@@ -296,8 +296,14 @@ __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& 
       for (int g = 0; g < 8; ++g) top = fmaxf(top, largest(g) * key_scale(g));
       const float was = m, unit_was = unit;
       if (top > m + kLazy || (m == kNone && top > m)) m = top;
-      if (sc.most > unit)  // four times the next power of two
-        unit = __uint_as_float((__float_as_uint(fminf(sc.most, 0x1p120f)) & 0x7f800000u) + 3u * 0x00800000u);
+      float most = sc.most;
+      if (off) {
+        most = 0.0f;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) most = fmaxf(most, (off >> g) & 1u || !is_finite_f(sc.vs[g]) ? 0.0f : fabsf(sc.vs[g]));
+      }
+      if (most > unit)  // four times the next power of two
+        unit = __uint_as_float((__float_as_uint(fminf(most, 0x1p120f)) & 0x7f800000u) + 3u * 0x00800000u);
       if (__any_sync(kFull, m != was || unit != unit_was)) {
         const float f = was == kNone ? 1.0f : ex2(was - m), fo = f * (unit_was / unit);
         l *= f;
@@ -324,7 +330,7 @@ __device__ __forceinline__ void softmax_role(const AttTcArgs& p, const AttWork& 
         uint32_t y[16];
 #pragma unroll
         for (int g = 2 * c; g < 2 * c + 2; ++g)
-          weigh(g, key_scale(g), odd && ((off >> g) & 1u) ? 0.0f : sc.vs[g] * inverse, minus, sum, y + 8 * (g & 1));
+          weigh(g, key_scale(g), (off >> g) & 1u ? 0.0f : sc.vs[g] * inverse, minus, sum, y + 8 * (g & 1));
         tmem_store16(ts + 16 * c, y);
       }
       float s0, s1;
