@@ -914,7 +914,8 @@ def rotary_turns(pairs: int, base: float = 10000.0, scaling: str | None = None, 
         raise ValueError("parts: original positions, and fast > slow > 0")
     # the index of the pair that turns n times over the original positions
     at = lambda n: pairs * math.log(original / (n * 2 * math.pi)) / math.log(base)  # noqa: E731
-    low, high = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), pairs - 1)
+    # (the upper end may lie past the last pair, which then keeps part of its angle)
+    low, high = max(math.floor(at(fast)), 0), min(math.ceil(at(slow)), 2 * pairs - 1)
     kept = 1 - ((i - low) / max(high - low, 1e-3)).clamp(0, 1)
     return turns / factor * (1 - kept) + turns * kept
 
