@@ -910,8 +910,8 @@ def rotary_turns(pairs: int, base: float = 10000.0, scaling: str | None = None, 
         return turns / factor
     if scaling != "parts":
         raise ValueError(f"unknown scaling {scaling!r}: linear, ntk or parts")
-    if original <= 0 or not fast > slow > 0 or base == 1:
-        raise ValueError("parts: original positions, and fast > slow > 0")
+    if original <= 0 or not fast > slow > 0 or not base > 1:  # (below 1 later pairs turn faster)
+        raise ValueError("parts: original positions, fast > slow > 0, and a base above 1")
     # the index of the pair that turns n times over the original positions
     at = lambda n: pairs * math.log(original / (n * 2 * math.pi)) / math.log(base)  # noqa: E731
     # (the upper end may lie past the last pair, which then keeps part of its angle)

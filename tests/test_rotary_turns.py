@@ -44,3 +44,11 @@ def test_pairs_that_turn_more_than_slow_are_not_divided_by_all_of_the_factor():
         assert turns > 1 and t > 1.3 * p / factor       # every pair turns more than twice: none is divided by all of 4
         if turns > 32 * 10000.0 ** (1 / pairs):
             assert abs(t - p) <= 1e-12 * p
+
+
+def test_parts_refuses_bases_that_order_the_pairs_the_other_way():
+    import precision_quantization_gb300 as qz
+    for base in (1.0, 0.5, 1e-4):
+        with pytest.raises(ValueError):
+            qz.rotary_turns(8, base=base, scaling="parts", factor=2.0, original=4096)
+    assert qz.rotary_turns(8, base=0.5).numel() == 8
