@@ -618,7 +618,9 @@ QZ_API qz_status qz_cache_append(const qz_cache* cache, const qz_batch* batch, i
  * codes (f16; gradually fewer below 2^-22 of the largest scale of values that the token sees, or of 2^-100 where that
  * is larger: what it does not see changes nothing); sums in fp32, in an unspecified but
  * fixed order: equal inputs give equal results.  A non-finite query makes its own outputs non-finite and no
- * others.  Scales are not negative.  Codes and scales of positions past a sequence's length are not looked at.
+ * others; a code that is NaN or Inf (qz_cache_append writes none) those of the tokens that see it, in its element or
+ * in all of them, and no others.  Scales are not negative.  Codes and scales of positions past a sequence's length
+ * are not looked at.
  * Waits inside the kernels are bounded (1 s); should one give up, the outputs it stands for are NaN.
  * Errors: as above (tokens * heads of 2^31 and more are QZ_ERR_UNSUPPORTED); QZ_ERR_WORKSPACE. */
 QZ_API size_t qz_cache_attention_workspace(const qz_cache* cache, int64_t sequences, int64_t tokens, int64_t heads,

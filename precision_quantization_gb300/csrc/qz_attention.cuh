@@ -98,6 +98,13 @@ __device__ __forceinline__ void pairs_of_words(uint32_t a, uint32_t b, uint32_t&
     e4m3_pairs(prmt(a, b, J | ((4 + J) << 4) | ((J + 1) << 8) | ((5 + J) << 12)), p0, p1);
   }
 }
+// Whether one of 16 codes stands for no finite number (E4M3: NaN; E5M2: NaN and Inf).  qz_cache_append writes none, but
+// what lies at a position may be anything where a row does not see it, and the products take values by the tile: 0 x NaN.
+template <int FMT>
+__device__ __forceinline__ bool has_nonfinite(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  constexpr uint32_t kMask = FMT == QZ_FP8_E4M3 ? 0x7f7f7f7fu : 0x7c7c7c7cu, kOne = FMT == QZ_FP8_E4M3 ? 0x01010101u : 0x04040404u;
+  return FMT != QZ_INT8 && ((((a & kMask) + kOne) | ((b & kMask) + kOne) | ((c & kMask) + kOne) | ((d & kMask) + kOne)) & 0x80808080u);
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;

@@ -36,6 +36,7 @@
 
 #include "qz_attention.cuh"
 #include "qz_internal.h"
+#include "qz_tcgen05.cuh"
 
 namespace qz {
 namespace {
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
   __shared__ __align__(16) float s_scale[kWarps][kStages][4];  // ks, vs of the first 16 tokens, of the second
   __shared__ int32_t s_has[kWarps][kStages];                   // bit i: the i-th 16 tokens have a page
   __shared__ __align__(8) uint64_t s_full[kWarps][kStages];
+  __shared__ uint32_t s_spoiled[kWarps];  // tokens of a step, seen by some rows alone, whose values are not finite numbers
   __shared__ volatile int s_gave_up;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
@@ -458,8 +460,8 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
             }
           }
         }
-        // ---- softmax: value 2 z + e of half i is token 16 i + 8 z + g, row 8 t + 2 c + e ------------
         const bool whole = p64 + kStep <= all_end && p >= all_begin && has == (1 << kHalves) - 1;
+        // ---- softmax: value 2 z + e of half i is token 16 i + 8 z + g, row 8 t + 2 c + e ------------
         bool moved = false;
         float was[NT][2];
 #pragma unroll
@@ -490,53 +492,90 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
               moved = true;
             }
           }
-        float unit_was = least;
-        const auto unit_for = [](float unit, float most) {  // the next power of two above `most`
-          return most > unit ? __uint_as_float((__float_as_uint(fminf(most, 0x1p125f)) & 0x7f800000u) + 0x00800000u) : unit;
-        };
         const float most = fmaxf(has & 1 ? vs[0] : 0.0f, has & 2 ? vs[kHalves - 1] : 0.0f);
-        if (most > least) {  // (the same for every lane)
-          bool shared = !mixed;    // every row sees something of what there is
+        // a row sees part of the step, and another more: a warp's rare work lies behind the one branch that it has anyway
+        const bool edge = FMT != QZ_INT8 && (p < all_begin || (p64 + kStep > all_end && all_end < len));
+        if (__any_sync(kFull, moved || most > least || edge)) {
+          float unit_was = least;
+          const auto unit_for = [](float unit, float most) {  // the next power of two above `most`
+            return most > unit ? __uint_as_float((__float_as_uint(fminf(most, 0x1p125f)) & 0x7f800000u) + 0x00800000u) : unit;
+          };
+          if (most > least) {  // (the same for every lane)
+            bool shared = !mixed;    // every row sees something of what there is
 #pragma unroll
-          for (int i = 0; i < kHalves; ++i) shared = shared && (!((has >> i) & 1) || (p64 + 16 * i < all_end && p64 + 16 * i + 15 >= all_begin));
-          if (shared) {
-            least = unit_for(least, most);
-            moved = true;
-          } else {           // no block changes what a row that sees nothing of it keeps
-            float lowest = 0x1p127f, highest = 0.0f;
+            for (int i = 0; i < kHalves; ++i) shared = shared && (!((has >> i) & 1) || (p64 + 16 * i < all_end && p64 + 16 * i + 15 >= all_begin));
+            if (shared) {
+              least = unit_for(least, most);
+            } else {           // no block changes what a row that sees nothing of it keeps
+              float lowest = 0x1p127f, highest = 0.0f;
 #pragma unroll 1
-            for (int r = 2 * c; r < kRows; r += r & 1 ? 7 : 1) {  // this lane's rows
-              float seen = 0.0f;
+              for (int r = 2 * c; r < kRows; r += r & 1 ? 7 : 1) {  // this lane's rows
+                float seen = 0.0f;
 #pragma unroll
-              for (int i = 0; i < kHalves; ++i)
-                if (((has >> i) & 1) && p64 + 16 * i < s_end[r] && p64 + 16 * i + 15 >= s_begin[r]) seen = fmaxf(seen, vs[i]);
-              const float unit = mixed ? s_unit[warp][r] : least, to = unit_for(unit, seen);
-              lowest = fminf(lowest, to), highest = fmaxf(highest, to);
-              __syncwarp();  // every lane of the row has read it
-              if (g == 0) s_unit[warp][r] = to, s_shrink[warp][r] = unit / to;
-            }
-            __syncwarp();
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float shrink = s_shrink[warp][8 * t + 2 * c + e];
-#pragma unroll
-                for (int j = 0; j < kTiles; ++j) {
-                  o[t][j][e] *= shrink;
-                  o[t][j][2 + e] *= shrink;
-                }
+                for (int i = 0; i < kHalves; ++i)
+                  if (((has >> i) & 1) && p64 + 16 * i < s_end[r] && p64 + 16 * i + 15 >= s_begin[r]) seen = fmaxf(seen, vs[i]);
+                const float unit = mixed ? s_unit[warp][r] : least, to = unit_for(unit, seen);
+                lowest = fminf(lowest, to), highest = fmaxf(highest, to);
+                __syncwarp();  // every lane of the row has read it
+                if (g == 0) s_unit[warp][r] = to, s_shrink[warp][r] = unit / to;
               }
+              __syncwarp();
 #pragma unroll
-            for (int d = 1; d < 4; d <<= 1) {
-              lowest = fminf(lowest, __shfl_xor_sync(kFull, lowest, d));
-              highest = fmaxf(highest, __shfl_xor_sync(kFull, highest, d));
+              for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const float shrink = s_shrink[warp][8 * t + 2 * c + e];
+#pragma unroll
+                  for (int j = 0; j < kTiles; ++j) {
+                    o[t][j][e] *= shrink;
+                    o[t][j][2 + e] *= shrink;
+                  }
+                }
+#pragma unroll
+              for (int d = 1; d < 4; d <<= 1) {
+                lowest = fminf(lowest, __shfl_xor_sync(kFull, lowest, d));
+                highest = fmaxf(highest, __shfl_xor_sync(kFull, highest, d));
+              }
+              least = unit_was = lowest;
+              mixed = lowest != highest;
             }
-            least = unit_was = lowest;
-            mixed = lowest != highest;
           }
-        }
-        if (__any_sync(kFull, moved)) {
+          if (edge) {
+            // Positions that not every row sees: values there that are not finite numbers become zeros, and NaN the sums of the
+            // rows that see them.
+            const uint32_t at = from + kHalves * Z::kHalf + 16 * lane;
+            const auto odd_at = [&](uint32_t d) {
+              uint32_t w[4];
+              lds16(w, at + d);
+              return has_nonfinite<FMT>(w[0], w[1], w[2], w[3]);
+            };
+            bool odd = false;
+#pragma unroll 4
+            for (uint32_t d = 0; d < kHalves * Z::kHalf; d += 512) odd = odd_at(d) || odd;
+            if (__any_sync(kFull, odd)) {
+              if (lane == 0) s_spoiled[warp] = 0u;
+              __syncwarp();
+#pragma unroll 1
+              for (uint32_t d = 0; d < kHalves * Z::kHalf; d += 512) {
+                if (!odd_at(d)) continue;
+                atomicOr(&s_spoiled[warp], 1u << ((16 * lane + d) / kRowBytes % kStep));
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at + d), "r"(0u) : "memory");
+                fence_proxy_async();  // (before the next copy to this stage)
+              }
+              __syncwarp();
+              const uint32_t spoiled = s_spoiled[warp];
+              const uint32_t held = (has & 1 ? 0xffffu : 0u) | (has & 2 ? 0xffff0000u : 0u);
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const int64_t lo = max(begin[t][e] - p64, static_cast<int64_t>(0)), hi = min(end[t][e] - p64, static_cast<int64_t>(kStep));
+                  const uint32_t seen = hi > lo ? (0xffffffffu >> (32 - static_cast<int>(hi - lo))) << lo : 0u;
+                  if (spoiled & held & seen) sum[t][e] = __uint_as_float(0x7fc00000u);
+                }
+              __syncwarp();  // (read by every lane)
+            }
+          }
           const float shrink = unit_was / least;
 #pragma unroll
           for (int t = 0; t < NT; ++t)

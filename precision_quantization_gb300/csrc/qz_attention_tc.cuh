@@ -127,6 +127,7 @@ struct AttWork {
   Span sp;
   int32_t seq, kvh, row0, rows;  // rows from row0 on, of `rows` in all
   int32_t t0, t1;                // tiles of keys
+  int32_t seen0, seen1;          // the positions that every row sees
 };
 
 // ---- softmax ------------------------------------------------------------------------------------
@@ -498,6 +499,35 @@ __device__ __forceinline__ void decode_role(const AttTcArgs& p, const AttWork& w
     const uint32_t ph = (n / kAttStages) & 1, raw = n & 1;
     const int64_t rows = w.sp.len - static_cast<int64_t>(t) * kAttKeys;
     bool ok = true, there[2];
+    // Where not every row sees the whole tile, a token whose values are not finite numbers gets zeros for them and NaN for
+    // its key: its scores are masked for the rows that do not see it, and spoil the others.  (A warp's own lines.)
+    if (FMT != QZ_INT8 && (t * static_cast<int64_t>(kAttKeys) < w.seen0 || t * static_cast<int64_t>(kAttKeys) + kAttKeys > w.seen1)) {
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        if (!(ok = __all_sync(kFull, att_wait(bar.rv_full[h], raw, abort) && att_wait(bar.rk_full[h], raw, abort)))) break;
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t cw[4] = {0u, 0u, 0u, 0u};
+          if (i ? second : first)
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(cw[0]), "=r"(cw[1]), "=r"(cw[2]), "=r"(cw[3]) : "r"(raw_v + 64 * h * row_bytes + from[i]));
+          odd = odd || has_nonfinite<FMT>(cw[0], cw[1], cw[2], cw[3]);
+        }
+        const uint32_t lines = __ballot_sync(kFull, odd);  // a line's pieces are those of lanes 8 apart
+        if (lines & (0x01010101u << (lane & 7))) {
+          const uint32_t zeros[4] = {0u, 0u, 0u, 0u}, nans[4] = {0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (!(i ? second : first)) continue;
+            sts16(raw_v + 64 * h * row_bytes + from[i], zeros);
+            sts16(raw_k + 64 * h * row_bytes + from[i], nans);
+          }
+          fence_proxy_async();  // (before the next copies there)
+        }
+        __syncwarp();
+      }
+    }
+    if (!ok) break;
 #pragma unroll
     for (int z = 0; z < 2; ++z) {  // keys, values
       uint64_t* full = z ? bar.rv_full : bar.rk_full;
@@ -592,6 +622,8 @@ __global__ void __launch_bounds__(kAttThreads, 1) attention_tc_kernel(const __gr
     const int64_t t0 = lo / kAttKeys, count = max((hi + kAttKeys - 1) / kAttKeys - t0, static_cast<int64_t>(0));
     w.t0 = static_cast<int32_t>(t0 + count * split / p.splits);
     w.t1 = static_cast<int32_t>(t0 + count * (split + 1) / p.splits);
+    w.seen0 = static_cast<int32_t>(max(w.sp.p0 + last / a.group + 1 - a.window, static_cast<int64_t>(0)));
+    w.seen1 = static_cast<int32_t>(max(min(w.sp.p0 + row0 / a.group + 1, static_cast<int64_t>(w.sp.len)), static_cast<int64_t>(0)));
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kAttStages; ++s) {

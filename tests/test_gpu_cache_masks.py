@@ -61,3 +61,41 @@ def test_large_values_that_a_row_does_not_see(qz, fmt, size, case):  # noqa: F81
     out, lse = qz.cache_attention(gpu(q).bfloat16(), on_gpu(qz, host), gpu(table), gpu(np.array(lengths, np.int32)), gpu(starts),
                                   scale=scale, window=window or None, lse=True)
     check(out, lse, wanted(q.astype(np.float64), host, table, lengths, starts, scale, window))
+
+
+NONFINITE = {"e4m3": [0x7F, 0xFF], "e5m2": [0x7C, 0x7F, 0xFC, 0xFD]}
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("which", ["keys", "values"])
+@pytest.mark.parametrize("case", range(len(MASKED)))
+def test_codes_that_are_no_numbers_spoil_the_rows_that_see_them(qz, fmt, which, case):  # noqa: F811
+    """NaN and Inf codes just before the first token's window, at its first position and at the last token's own."""
+    lengths, new, page, block, heads, kv, dim, window, _ = MASKED[case]
+    rng = np.random.default_rng(50 + case)
+    seqs, tokens = len(lengths), sum(new)
+    each = -(-max(lengths) // page)
+    host = U.Cache(rng, fmt, seqs * each + 1, kv, page, dim, block)
+    table = sequences(rng, seqs, each, host.pages)
+    for s in range(seqs):
+        host.fill(rng, table[s], lengths[s])
+    q = U.bf16((2 * rng.standard_normal((tokens, heads, dim))).astype(np.float32))
+    starts, scale = np.concatenate(([0], np.cumsum(new))).astype(np.int32), dim ** -0.5
+    out, lse, *rest = U.attention(q.astype(np.float64), host, table, lengths, starts, scale, window)
+    sees = np.zeros(tokens, bool)
+    for s, length in enumerate(lengths):
+        at = np.arange(length - new[s], length)
+        first = np.maximum(at - window + 1, 0) if window else np.zeros(new[s], int)
+        for p in {int(first[0]) - 1, int(first[0]) if first[-1] > first[0] else -1, length - 1 if new[s] > 1 else -1} - {-1}:
+            codes = host.codes[which == "values"][table[s, p // page], :, p % page]
+            codes[:, rng.integers(0, dim)] = 0x7F    # a NaN of either format
+            if not ((p <= at) & (p >= first)).any():
+                codes[:] = rng.choice(NONFINITE[fmt], codes.shape)
+            sees[starts[s]:starts[s + 1]] |= (p <= at) & (p >= first)
+    got, logs = qz.cache_attention(gpu(q).bfloat16(), on_gpu(qz, host), gpu(table), gpu(np.array(lengths, np.int32)), gpu(starts),
+                                   scale=scale, window=window or None, lse=True)
+    keep = ~sees
+    assert keep.any() or sees.all()
+    if keep.any():
+        check(got[gpu(keep)], logs[gpu(keep)], (out[keep], lse[keep], *(r[keep] for r in rest)))
+    assert (~np.isfinite(got[gpu(sees)].double().cpu().numpy())).any(-1).all()
