@@ -609,7 +609,7 @@ QZ_API qz_status qz_cache_append(const qz_cache* cache, const qz_batch* batch, i
  *   q        bf16 [tokens, heads, dim], heads a multiple of kv_heads;  out  bf16 alike
  *   lse      fp32 [tokens, heads] (leading dimension ld_lse) or NULL: log sum exp of the visible scores,
  *            -inf where there are none
- *   scale    a finite number > 0
+ *   scale    > 0 and at most 2^127
  *   ws, ws_bytes  qz_cache_attention_workspace bytes of device memory (of these sizes; 0: ws may be NULL), uninitialised,
  *            16-byte aligned; calls that may overlap need one each
  * Rows that belong to no sequence are left as they are.

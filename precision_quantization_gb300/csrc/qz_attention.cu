@@ -75,7 +75,7 @@ extern "C" qz_status qz_cache_attention(const qz_cache* cache, const qz_batch* b
   if ((st = check_vectors(tokens, heads, dim, ld_q, hd_q)) != QZ_OK || (st = check_vectors(tokens, heads, dim, ld_out, hd_out)) != QZ_OK ||
       (st = check_batch(batch, tokens)) != QZ_OK)
     return st;
-  if (heads % cache->kv_heads || window < 0 || !(scale > 0.0f && scale <= 3.402823466e38f) || (lse && ld_lse < heads)) return QZ_ERR_SHAPE;
+  if (heads % cache->kv_heads || window < 0 || !(scale > 0.0f && scale <= 0x1p127f) || (lse && ld_lse < heads)) return QZ_ERR_SHAPE;
   if (lse && tokens > 0 && ld_lse > INT64_MAX / 16 / tokens) return QZ_ERR_SHAPE;
   if (tokens == 0 || heads == 0 || batch->sequences == 0) return QZ_OK;
   if (!q || !out) return QZ_ERR_NULL;
