@@ -164,6 +164,8 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
   const uint32_t q_smem = base + Z::kRing;
   float* join = reinterpret_cast<float*>(smem + Z::kRing + Z::kQ);
   if (tid == 0) s_gave_up = 0;
+  // 0 at a segment's start; NaN where a row sees a value that is no finite number
+  for (int r = lane; r < kRows; r += 32) s_l[warp][r] = 0.0f;
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(smem_addr(&s_full[warp][i]), 1 + 2 * kHalves);  // the codes, the scales
     mbar_init_fence();
@@ -493,9 +495,8 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
             }
           }
         const float most = fmaxf(has & 1 ? vs[0] : 0.0f, has & 2 ? vs[kHalves - 1] : 0.0f);
-        // a row sees part of the step, and another more: a warp's rare work lies behind the one branch that it has anyway
-        const bool edge = FMT != QZ_INT8 && (p < all_begin || (p64 + kStep > all_end && all_end < len));
-        if (__any_sync(kFull, moved || most > least || edge)) {
+        // (what is rare lies behind the one branch that there is anyway)
+        if (__any_sync(kFull, moved || most > least || (FMT != QZ_INT8 && !whole))) {
           float unit_was = least;
           const auto unit_for = [](float unit, float most) {  // the next power of two above `most`
             return most > unit ? __uint_as_float((__float_as_uint(fminf(most, 0x1p125f)) & 0x7f800000u) + 0x00800000u) : unit;
@@ -504,7 +505,7 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
             bool shared = !mixed;    // every row sees something of what there is
 #pragma unroll
             for (int i = 0; i < kHalves; ++i) shared = shared && (!((has >> i) & 1) || (p64 + 16 * i < all_end && p64 + 16 * i + 15 >= all_begin));
-            if (shared) {
+            if (__builtin_expect(shared, 1)) {
               least = unit_for(least, most);
             } else {           // no block changes what a row that sees nothing of it keeps
               float lowest = 0x1p127f, highest = 0.0f;
@@ -540,7 +541,7 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
               mixed = lowest != highest;
             }
           }
-          if (edge) {
+          if (FMT != QZ_INT8 && !whole && (p < all_begin || (p64 + kStep > all_end && all_end < len))) {
             // Positions that not every row sees: values there that are not finite numbers become zeros, and NaN the sums of the
             // rows that see them.
             const uint32_t at = from + kHalves * Z::kHalf + 16 * lane;
@@ -563,17 +564,13 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
                 fence_proxy_async();  // (before the next copy to this stage)
               }
               __syncwarp();
-              const uint32_t spoiled = s_spoiled[warp];
-              const uint32_t held = (has & 1 ? 0xffffu : 0u) | (has & 2 ? 0xffff0000u : 0u);
-#pragma unroll
-              for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const int64_t lo = max(begin[t][e] - p64, static_cast<int64_t>(0)), hi = min(end[t][e] - p64, static_cast<int64_t>(kStep));
-                  const uint32_t seen = hi > lo ? (0xffffffffu >> (32 - static_cast<int>(hi - lo))) << lo : 0u;
-                  if (spoiled & held & seen) sum[t][e] = __uint_as_float(0x7fc00000u);
-                }
-              __syncwarp();  // (read by every lane)
+              const uint32_t spoiled = s_spoiled[warp] & ((has & 1 ? 0xffffu : 0u) | (has & 2 ? 0xffff0000u : 0u));
+#pragma unroll 1
+              for (int r = lane; r < kRows; r += 32) {
+                const int64_t lo = max(s_begin[r] - p64, static_cast<int64_t>(0)), hi = min(s_end[r] - p64, static_cast<int64_t>(kStep));
+                const uint32_t seen = hi > lo ? (0xffffffffu >> (32 - static_cast<int>(hi - lo))) << lo : 0u;
+                if (spoiled & seen) s_l[warp][r] = __uint_as_float(0x7fc00000u);
+              }
             }
           }
           const float shrink = unit_was / least;
@@ -616,7 +613,7 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
               for (int z = 0; z < 2; ++z) pb[t][i][z] = transposed(f16x2_bits(y[i][2 * z], y[i][2 * z + 1]));
           }
         };
-        if (mixed) weigh(std::true_type{});
+        if (__builtin_expect(mixed, 0)) weigh(std::true_type{});
         else weigh(std::false_type{});
         // ---- out^T += V^T p^T ---------------------------------------------------------------------
 #pragma unroll
@@ -682,7 +679,7 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
         for (int w = 4; w < 32; w <<= 1) sum[t][e] += __shfl_xor_sync(kFull, sum[t][e], w);
         if (g == 0) {
           s_m[warp][8 * t + 2 * c + e] = mx[t][e];
-          s_l[warp][8 * t + 2 * c + e] = sum[t][e];
+          s_l[warp][8 * t + 2 * c + e] += sum[t][e];
           if (!mixed) s_unit[warp][8 * t + 2 * c + e] = least;
         }
       }
@@ -708,6 +705,7 @@ __global__ void __launch_bounds__(FewSizes<DP, NT>::kThreads, 1)
           for (int w = 8; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, w));
           const float f = ex2(m - (top == kNone ? 0.0f : top));
           float l = lane < kWarps ? f * s_l[lane < kWarps ? lane : 0][r] : 0.0f;
+          if (lane < kWarps) s_l[lane][r] = 0.0f;  // for the next segment
 #pragma unroll
           for (int w = 8; w; w >>= 1) l += __shfl_xor_sync(kFull, l, w);
           if (lane < kWarps) s_m[lane][r] = f * s_unit[lane][r] * 0x1p-15f;
