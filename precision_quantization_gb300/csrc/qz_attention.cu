@@ -11,9 +11,9 @@
 namespace qz {
 
 // A CTA takes whole items where no sequence can be long enough to be worth cutting: its pages hold at most kWhole
-// tokens, or twice that where the items fill half the GPU (8 sequences of 1000 tokens, 8 kv heads: 10.9 us whole,
-// 12.4 cut; 32 of 2000: 36.0 and 40.2; one of 2000: 17.7 and 16.3).  Else the steps are shared out evenly, kMinChunk
-// tokens at least to a CTA (one sequence of 2000 tokens: 16.3 us, 17.6 with twice as many).
+// tokens, or twice that where the items fill half the GPU (8 sequences of 1000 tokens, 8 kv heads: 11.5 us whole,
+// 16.2 cut; 32 of 2000: 36.3 and 40.7; one of 2000: 17.9 and 16.7).  Else the steps are shared out evenly, kMinChunk
+// tokens at least to a CTA (one sequence of 2000 tokens: 16.7 us, 18.9 with twice as many).
 constexpr int64_t kWhole = 1024, kMinChunk = 256;
 
 FewPlan few_att_plan(const qz_cache& c, int64_t seqs, int64_t tokens, int64_t heads, int64_t table_pages, int sms) {
@@ -32,9 +32,9 @@ size_t few_att_workspace(const FewPlan& p, int dim) {
 }
 
 // More than kTcRows rows a sequence and kv head go to the tensor-core tiles (16 sequences of 4096 tokens, 8 kv heads,
-// E4M3: 32 rows 80 us by the few-row kernel and 88 by the tiles, 48 rows 137 and 88; INT8, 64 elements, 64 x 2048:
-// 32 rows 114 and 181, 64 rows 199 and 186).  Tiles that do not fill the GPU are cut along the keys, a part no shorter
-// than kTcPart tokens (64 queries of 8192: 37 us; 42 with twice as many).  Cutting tiles that fill it, to even out the
+// E4M3: 32 rows 85 us by the few-row kernel and 91 by the tiles, 48 rows 143 and 90; INT8, 64 elements, 64 x 2048:
+// 32 rows 117 and 170, 64 rows 205 and 174).  Tiles that do not fill the GPU are cut along the keys, a part no shorter
+// than kTcPart tokens (64 queries of 8192: 39.7 us; 41.4 with twice as many).  Cutting tiles that fill it, to even out the
 // last round, costs more in partial sums than it gives: prompt of 4096 tokens, with q staged more slowly, 485 us whole, 581 in two parts.
 constexpr int64_t kTcRows = 32, kTcPart = 512;
 

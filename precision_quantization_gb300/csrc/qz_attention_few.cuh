@@ -22,14 +22,15 @@
 // that holds part of an item leaves its sums in the workspace, and the CTAs of the second kernel join them.
 //
 // GPU times (in brackets the bytes of the visible keys and values at the copy rate, 6.7 TB/s):
-//   64 sequences x 1 token, up to 8192 long, 32 / 8 heads x 128, INT8    156 us (123), 5.3 TB/s
-//   1 token of 131072, 64 / 8 heads x 128, E4M3                          57 us (40), 4.7 TB/s
-//   24 sequences x 3 tokens, window 4096, 40 / 8 heads x 64, E5M2        52 us (15)
-//   1 token of 517                                                       9.0 us
-// Between 60 and 80 % of HBM no pipe is full (the decoding ALU 60 %, issue 0.5 to 0.6 a cycle): three warps a
+//   64 sequences x 1 token, up to 8192 long, 32 / 8 heads x 128, INT8    158 us (123), 5.2 TB/s
+//   1 token of 131072, 64 / 8 heads x 128, E4M3                          58 us (40), 4.6 TB/s
+//   24 sequences x 3 tokens, window 4096, 40 / 8 heads x 64, E5M2        57 us (15)
+//   1 token of 517                                                       9.4 us
+// Between 60 and 80 % of HBM no pipe is full (the decoding ALU 58 %, issue 0.5 to 0.6 a cycle): three warps a
 // scheduler wait for fixed latencies.  With 15 rows of 64 elements (the third) a code meets twice the softmax and half
-// the products, and the instructions are the bound, with the joins at the ends of items.  Codes as the B operand, rows
-// as A, took 226 and 80 us; rings filled by cp.async 240 and 84.
+// the products; its warps wait most of the time too (issue 0.47, HBM 24 %), with the joins at the ends of items.  Codes
+// as the B operand, rows as A, took 226 and 80 us; rings filled by cp.async 240 and 84.  Units by what a row sees, and
+// the look for codes that are no finite numbers, cost 1 % of the first two and 5 us of the third.
 #pragma once
 
 #include <type_traits>

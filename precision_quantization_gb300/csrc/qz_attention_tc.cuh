@@ -4,8 +4,9 @@
 //   x_j = (scale log2 e) ks_j (q . k_j),  p_j = 2^(x_j - m),  l = sum p_j,  out = sum p_j vs_j v_j / l
 //
 // A CTA holds two tiles of 128 rows (one where the sequences have fewer) of one sequence and kv head and
-// walks the keys in tiles of 128 tokens.  Bound by the tensor cores and the exponentials together, so that
-// each warp has one thing to do and two row tiles take turns on both:
+// walks the keys in tiles of 128 tokens.  Neither the tensor cores (41 %) nor the exponentials (21 %) are full: a row
+// tile's own chain is the bound, scores - softmax - weights - P V - the next scores, which take the weights' place.  So
+// each warp has one thing to do, and two row tiles take turns:
 //   warps 0-7    softmax, one row of a tile a thread: x from tensor memory into registers, p back into its
 //                place as f16
 //   warps 8-15   decode: 16-byte pieces of codes become f16 in shared memory in the layout that the MMA
@@ -21,8 +22,8 @@
 // f16, and keeps its 11 bits down to 2^-22 of the largest scale.
 // Where the row tiles do not fill the GPU the keys are cut in `splits` parts, whose sums a second kernel joins.
 //
-// GPU times: 4096 new tokens of 8192, 32 / 8 heads x 128, E4M3: 466 us, 885 TFLOP/s (the operations at the library
-// product's rate: 215); prompts of 5 sequences, 16 / 4 heads x 64, INT8: 111 us.  A step of 256 rows x 128 keys takes some
+// GPU times: 4096 new tokens of 8192, 32 / 8 heads x 128, E4M3: 471 us, 875 TFLOP/s (the operations at the library
+// product's rate: 215); prompts of 5 sequences, 16 / 4 heads x 64, INT8: 108 us.  A step of 256 rows x 128 keys takes some
 // 4400 cycles: 1330 of MMAs, and two softmaxes of 2900, a row tile's own chain of load, exponentials, conversion and
 // store, which overlap with one another and with the MMAs only in part.  Sixteen softmax warps, two MMA warps, exponentials
 // pipelined by hand and turns of the two tiles were slower.

@@ -3,8 +3,10 @@
 //
 //   a' = a c - b s,  b' = b c + a s  per pair, c and s of the token's position; backward: -s
 //
-// One pass: x read, y written, and a table row per token that every head shares: bound by HBM in principle, by the latency of a thread's loads in practice, since it holds few of them.  So a thread takes the same
-// elements of several heads: more loads in flight for one look at the table, in 16-byte pieces.  GPU times:
+// One pass: x read, y written, and a table row per token that every head shares: bound by HBM, of which it reaches
+// 70 %.  A thread takes the same elements of several heads, for one look at the table, in 16-byte pieces; four loads each
+// of 1024 threads are more in flight than HBM needs, so that what is missing is likely that every thread loads, waits and
+// stores once and ends (no persistent form was tried).  GPU times:
 //   bf16, 8192 tokens x 32 heads x 128, adjacent pairs (139 MB)   29.2 us, 4.75 TB/s  (one head a thread, 64-bit places: 39)
 //   fp32, backward of 4093 x 40 x 80, 10 pairs (105 MB)           22.6 us, 4.65 TB/s  (rotary_quad_kernel)
 //   one token                                                     2.3 us, all of it launch
