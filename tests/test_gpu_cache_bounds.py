@@ -59,3 +59,37 @@ def test_starts_out_of_order(qz, case, heads_outside, heads, kv, dim, held):  # 
     assert (lse[:4] == 7).all() and (lse[-4:] == 7).all() and (lse[4:-4][~owned] == 7).all()
     for b, s in zip(cache.buffers, spare):
         assert torch.equal(b[[i for i in range(host.pages) if i not in table]], s)
+
+
+@pytest.mark.parametrize("lengths,new,heads", [([300, 70, 40], [1, 2, 1], 8), ([200, 140, 90], [90, 31, 60], 8), ([2600, 0, 900], [300, 0, 257], 4),
+                                               ([3000, 17], [1, 1], 8)])
+def test_rows_around_the_sequences_are_left_alone(qz, lengths, new, heads):  # noqa: F811
+    """Rows in front of the first sequence and behind the last one; the others as if they were the whole call."""
+    import torch
+    rng = np.random.default_rng(8)
+    page, block, kv, dim, front, back, seqs = 32, 16, 2, 64, 5, 3, len(lengths)
+    each = -(-max(lengths) // page)
+    host = U.Cache(rng, "int8", seqs * each, kv, page, dim, block, junk=False)
+    table = sequences(rng, seqs, each, host.pages)
+    for s in range(seqs):
+        host.fill(rng, table[s], lengths[s])
+    tokens, starts = sum(new), np.concatenate(([0], np.cumsum(new))).astype(np.int32)
+    t, n = gpu(table), gpu(np.array(lengths, np.int32))
+    q, k = (torch.randn(front + tokens + back, h, dim, device="cuda").bfloat16() for h in (heads, kv))
+    inner = slice(front, front + tokens)
+    cos, sin = table_of(max(lengths), 32)
+    rot, got = qz.RotaryTable(gpu(cos), gpu(sin)), []
+    for all_rows in (False, True):
+        cache, rows = on_gpu(qz, host), slice(None) if all_rows else inner
+        st = gpu(starts + (front if all_rows else 0))
+        turned, out = torch.full_like(q[rows], 7.0), torch.full_like(q[rows], 7.0)
+        lse = torch.full(out.shape[:2], 7.0, device="cuda")
+        qz.cache_append(cache, k[rows], k[rows], t, n, st, rotary=rot, q=q[rows], out=turned)
+        qz.cache_attention(turned, cache, t, n, st, lse=True, out=(out, lse))
+        if all_rows:
+            for x in (turned, out, lse):
+                assert (x[:front] == 7).all() and (x[front + tokens:] == 7).all()
+            turned, out, lse = turned[inner], out[inner], lse[inner]
+        got.append((turned, out, lse, *cache.buffers))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
